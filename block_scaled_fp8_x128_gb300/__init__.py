@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -45,6 +46,15 @@ _SIGS = {
                             ctypes.c_int),
     "r9q_gate_up_swiglu_down_noalloc": ([_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, ctypes.c_int, _P],
                                         ctypes.c_int),
+    "r9q_qk_norm_rope": ([_P, _I64, _I64] * 2 + [_P] * 5 + [_P, _I64, _I64] * 2 + [_I64] * 6 +
+                         [ctypes.c_float, ctypes.c_int, _P], ctypes.c_int),
+    "r9q_qk_norm_rope_bwd": ([_P, _I64, _I64] * 4 + [_P] * 5 + [_P, _I64, _I64] * 2 + [_P] * 2 + [_I64] * 6 +
+                             [ctypes.c_float, ctypes.c_int, _P, _SZ, _P], ctypes.c_int),
+    "r9q_qk_norm_rope_kv4": ([_P, _I64, _I64] * 3 + [_P] * 5 + [_P, _I64, _I64] + [_P] * 5 + [_I64] * 8 +
+                             [ctypes.c_float, ctypes.c_int, _P], ctypes.c_int),
+    "r9q_kv4_append": ([_P, _I64, _I64] * 2 + [_P] * 5 + [_I64] * 5 + [_P], ctypes.c_int),
+    "r9q_kv4_gather": ([_P] * 5 + [_I64] * 5 + [_P] * 3, ctypes.c_int),
+    "r9q_kv4_attention": ([_P] + [_I64] * 3 + [_P] * 8 + [_I64] * 9 + [ctypes.c_float, _P, _SZ, _P], ctypes.c_int),
 }
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -61,6 +71,9 @@ R9Q_MLP_UNFUSED = 2
 R9Q_OP_GEMM_W8A8 = 1
 R9Q_OP_GEMM_W8BF16 = 2
 R9Q_OP_GATE_UP_SWIGLU_DOWN = 3
+R9Q_OP_QK_NORM_ROPE_BWD = 4
+R9Q_OP_KV4_ATTENTION = 5
+R9Q_ROPE_INTERLEAVED = 1
 
 
 class R9QError(RuntimeError):
@@ -161,7 +174,8 @@ def _stream_workspace(need: int, device: torch.device, stream=None) -> torch.Ten
     key = (device.index, s.cuda_stream)
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < need:
-        ws = torch.zeros(need, dtype=torch.uint8, device=device)
+        with torch.cuda.stream(s):                            # zeroed on the stream that uses it
+            ws = torch.zeros(need, dtype=torch.uint8, device=device)
         _WORKSPACES[key] = ws
     return ws
 
@@ -325,3 +339,206 @@ def r9q_gate_up_swiglu_down_noalloc(x: torch.Tensor, w_gu: torch.Tensor, s_gu: t
                                                 M, H, I, H_out, _ptr(hq), _ptr(hs), int(flags), _stream(stream)),
            "r9q_gate_up_swiglu_down_noalloc")
     return y
+
+
+# ---- the attention block of a decode layer ----
+
+class KV4Cache(NamedTuple):
+    """The paged 4-bit key-value cache (layout: include/r9q.h).  k uint8 [pages][Hk][page][D/2], v uint8 of the
+    same shape (its bytes in groups of 16 tokens), kp and vp bf16 [pages][Hk][page][2]; r9q_kv4_cache makes one."""
+    k: torch.Tensor
+    kp: torch.Tensor
+    v: torch.Tensor
+    vp: torch.Tensor
+
+
+def r9q_kv4_cache(pages: int, heads: int, page: int, dim: int, device=None) -> KV4Cache:
+    """An empty cache of `pages` pages of `page` tokens (a multiple of 16) for `heads` key-value heads of `dim`."""
+    if page < 16 or page % 16 or dim not in (64, 128) or pages < 1 or heads < 1:
+        raise ValueError("page must be a multiple of 16, dim 64 or 128, pages and heads positive")
+    device = device if device is not None else torch.device("cuda", torch.cuda.current_device())
+    k = torch.zeros((pages, heads, page, dim // 2), dtype=torch.uint8, device=device)
+    kp = torch.zeros((pages, heads, page, 2), dtype=torch.bfloat16, device=device)
+    return KV4Cache(k, kp, torch.zeros_like(k), torch.zeros_like(kp))
+
+
+def _heads(t, name, shape):
+    """(pointer, token stride, head stride) of a bf16 [T][H][D] tensor with contiguous vectors."""
+    _expect(t, torch.bfloat16, shape, name)
+    if not t.is_cuda:
+        raise ValueError("tensor must be on a CUDA device")
+    ts, hs, es = t.stride()
+    if es != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr(), ts, hs
+
+
+def _cache_args(cache, heads, dim):
+    """The cache's pointers, its pages and their tokens."""
+    pages, _, page, _ = cache.k.shape
+    codes, pairs = (pages, heads, page, dim // 2), (pages, heads, page, 2)
+    _expect(cache.k, torch.uint8, codes, "cache.k")
+    _expect(cache.v, torch.uint8, codes, "cache.v")
+    _expect(cache.kp, torch.bfloat16, pairs, "cache.kp")
+    _expect(cache.vp, torch.bfloat16, pairs, "cache.vp")
+    return (_ptr(cache.k), _ptr(cache.kp), _ptr(cache.v), _ptr(cache.vp)), pages, page
+
+
+def _rope_args(wq, wk, cos, sin, positions, T, D):
+    """The weights', tables' and positions' pointers, rot and the tables' rows."""
+    _expect(wq, torch.float32, (D,), "wq")
+    _expect(wk, torch.float32, (D,), "wk")
+    if cos is None:
+        return (_ptr(wq), _ptr(wk), None, None, None), 0, 0
+    npos, half = cos.shape
+    _expect(cos, torch.float32, (npos, half), "cos")
+    _expect(sin, torch.float32, (npos, half), "sin")
+    _expect(positions, torch.int64, (T,), "positions")
+    return (_ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin), _ptr(positions)), 2 * half, npos
+
+
+_WS_BYTES: dict = {}
+
+
+def _op_workspace(op, M, N, workspace, device, stream):
+    """(pointer, bytes) of the caller's workspace, or of the stream's own."""
+    if workspace is None:
+        key = (op, M, N, device.index)
+        need = _WS_BYTES.get(key)
+        if need is None:
+            need = _WS_BYTES[key] = r9q_workspace_bytes(op, M, N, 0)
+        workspace = _stream_workspace(need, device, stream)
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def r9q_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, wq: torch.Tensor, wk: torch.Tensor,
+                     cos: torch.Tensor | None = None, sin: torch.Tensor | None = None,
+                     positions: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+                     q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """RMS norm of the heads of q bf16 [T][Hq][D] and k bf16 [T][Hk][D] (any token and head strides) and the
+    rotation by cos, sin fp32 [npos][rot/2] at positions int64 [T] (None: norm only); returns (q_out, k_out)."""
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    rope, rot, npos = _rope_args(wq, wk, cos, sin, positions, T, D)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=q.device)
+    _check(_lib.r9q_qk_norm_rope(*_heads(q, "q", (T, Hq, D)), *_heads(k, "k", (T, Hk, D)), *rope,
+                                 *_heads(q_out, "q_out", (T, Hq, D)), *_heads(k_out, "k_out", (T, Hk, D)),
+                                 T, Hq, Hk, D, rot, npos, eps, int(interleaved), _stream(stream)), "r9q_qk_norm_rope")
+    return q_out, k_out
+
+
+def r9q_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                         wq: torch.Tensor, wk: torch.Tensor, cos: torch.Tensor | None = None,
+                         sin: torch.Tensor | None = None, positions: torch.Tensor | None = None, eps: float = 1e-6,
+                         interleaved: bool = False, dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+                         dwq: torch.Tensor | None = None, dwk: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, stream=None):
+    """The gradient of r9q_qk_norm_rope; returns (dq, dk, dwq, dwk).  workspace: as for r9q_gemm_fp8_block_qa
+    (zero-filled before its first use; omitted: the stream's own)."""
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    rope, rot, npos = _rope_args(wq, wk, cos, sin, positions, T, D)
+    if dq is None:
+        dq = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    if dk is None:
+        dk = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=q.device)
+    if dwq is None:
+        dwq = torch.empty(D, dtype=torch.float32, device=q.device)
+    if dwk is None:
+        dwk = torch.empty(D, dtype=torch.float32, device=q.device)
+    _expect(dwq, torch.float32, (D,), "dwq")
+    _expect(dwk, torch.float32, (D,), "dwk")
+    ws, wsb = _op_workspace(R9Q_OP_QK_NORM_ROPE_BWD, 1, D, workspace, q.device, stream)
+    _check(_lib.r9q_qk_norm_rope_bwd(*_heads(dq_out, "dq_out", (T, Hq, D)), *_heads(dk_out, "dk_out", (T, Hk, D)),
+                                     *_heads(q, "q", (T, Hq, D)), *_heads(k, "k", (T, Hk, D)), *rope,
+                                     *_heads(dq, "dq", (T, Hq, D)), *_heads(dk, "dk", (T, Hk, D)), _ptr(dwq),
+                                     _ptr(dwk), T, Hq, Hk, D, rot, npos, eps, int(interleaved), ws, wsb,
+                                     _stream(stream)), "r9q_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk
+
+
+def r9q_qk_norm_rope_kv4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, wq: torch.Tensor, wk: torch.Tensor,
+                         cos: torch.Tensor | None, sin: torch.Tensor | None, positions: torch.Tensor | None,
+                         cache: KV4Cache, slots: torch.Tensor, eps: float = 1e-6, interleaved: bool = False,
+                         q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """r9q_qk_norm_rope with the keys, and v bf16 [T][Hk][D] as it is, written to the cache at slots int64 [T]
+    (page * tokens of a page + place; negative: padding); returns q_out."""
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    rope, rot, npos = _rope_args(wq, wk, cos, sin, positions, T, D)
+    ptrs, pages, page = _cache_args(cache, Hk, D)
+    _expect(slots, torch.int64, (T,), "slots")
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    _check(_lib.r9q_qk_norm_rope_kv4(*_heads(q, "q", (T, Hq, D)), *_heads(k, "k", (T, Hk, D)),
+                                     *_heads(v, "v", (T, Hk, D)), *rope, *_heads(q_out, "q_out", (T, Hq, D)), *ptrs,
+                                     _ptr(slots), T, Hq, Hk, D, rot, npos, pages, page, eps, int(interleaved),
+                                     _stream(stream)), "r9q_qk_norm_rope_kv4")
+    return q_out
+
+
+def r9q_kv4_append(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, slots: torch.Tensor, stream=None) -> None:
+    """Writes k and v bf16 [T][Hk][D] to the cache at slots int64 [T] (negative: padding)."""
+    T, Hk, D = k.shape
+    ptrs, pages, page = _cache_args(cache, Hk, D)
+    _expect(slots, torch.int64, (T,), "slots")
+    _check(_lib.r9q_kv4_append(*_heads(k, "k", (T, Hk, D)), *_heads(v, "v", (T, Hk, D)), *ptrs, _ptr(slots), T, Hk, D,
+                               pages, page, _stream(stream)), "r9q_kv4_append")
+
+
+def r9q_kv4_gather(cache: KV4Cache, slots: torch.Tensor, k: torch.Tensor | None = None,
+                   v: torch.Tensor | None = None, stream=None):
+    """The tokens at slots int64 [T] as bf16 (k, v) [T][Hk][D]; zeros for padding."""
+    T = slots.shape[0]
+    _, Hk, _, half = cache.k.shape
+    D = 2 * half
+    ptrs, pages, page = _cache_args(cache, Hk, D)
+    _expect(slots, torch.int64, (T,), "slots")
+    if k is None:
+        k = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=slots.device)
+    if v is None:
+        v = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=slots.device)
+    _expect(k, torch.bfloat16, (T, Hk, D), "k")
+    _expect(v, torch.bfloat16, (T, Hk, D), "v")
+    _check(_lib.r9q_kv4_gather(*ptrs, _ptr(slots), T, Hk, D, pages, page, _ptr(k), _ptr(v), _stream(stream)),
+           "r9q_kv4_gather")
+    return k, v
+
+
+def r9q_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                      scale: float | None = None, window: int = 0, out: torch.Tensor | None = None,
+                      lse: torch.Tensor | None = None, return_lse: bool = False,
+                      workspace: torch.Tensor | None = None, stream=None):
+    """Attention of the last Lq tokens of each sequence, q bf16 [B][Lq][Hq][D] (any batch, token and head strides),
+    over the cache: block_table int32 [B][max_pages], seq_lens int32 [B] (new tokens included).  scale: 1/sqrt(D) by
+    default.  Returns o bf16 [B][Lq][Hq][D], or (o, lse fp32 [B][Lq][Hq]) with return_lse.  workspace: as for
+    r9q_gemm_fp8_block_qa (zero-filled before its first use; omitted: the stream's own)."""
+    B, Lq, Hq, D = q.shape
+    Hk = cache.k.shape[1]
+    ptrs, pages, page = _cache_args(cache, Hk, D)
+    _expect(q, torch.bfloat16, (B, Lq, Hq, D), "q")
+    if not q.is_cuda:
+        raise ValueError("tensor must be on a CUDA device")
+    bs, ts, hs, es = q.stride()
+    if es != 1:
+        raise ValueError("q: the last dimension must be contiguous")
+    if Hk < 1 or Hq % Hk:
+        raise ValueError("q's heads must be a multiple of the cache's")
+    max_pages = block_table.shape[1]
+    _expect(block_table, torch.int32, (B, max_pages), "block_table")
+    _expect(seq_lens, torch.int32, (B,), "seq_lens")
+    if out is None:
+        out = torch.empty((B, Lq, Hq, D), dtype=torch.bfloat16, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty((B, Lq, Hq), dtype=torch.float32, device=q.device)
+    _expect(out, torch.bfloat16, (B, Lq, Hq, D), "out")
+    _expect(lse, torch.float32, (B, Lq, Hq), "lse")
+    ws, wsb = _op_workspace(R9Q_OP_KV4_ATTENTION, max(1, Lq * Hq // Hk), D, workspace, q.device, stream)
+    _check(_lib.r9q_kv4_attention(q.data_ptr(), bs, ts, hs, *ptrs, _ptr(block_table), _ptr(seq_lens), _ptr(out),
+                                  _ptr(lse), B, Lq, Hq, Hk, D, pages, page, max_pages, window,
+                                  D ** -0.5 if scale is None else scale, ws, wsb, _stream(stream)),
+           "r9q_kv4_attention")
+    return (out, lse) if return_lse else out

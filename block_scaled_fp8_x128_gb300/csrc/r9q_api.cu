@@ -397,6 +397,15 @@ int device_error_word(int** out) {
     return R9Q_OK;
 }
 
+int device_error_word_and_sms(int** out, int* sms) {
+    DeviceInfo* d = nullptr;
+    const int rc = current_device(&d);
+    if (rc) return rc;
+    *out = d->err;
+    *sms = d->sms;
+    return R9Q_OK;
+}
+
 }  // namespace r9q
 
 using namespace r9q;
@@ -571,6 +580,13 @@ int r9q_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int64_t N2, int
             if (rc) return rc;
             *bytes = mlp_workspace(M, N, flags, false, false);
             return R9Q_OK;
+        }
+        case R9Q_OP_QK_NORM_ROPE_BWD:
+        case R9Q_OP_KV4_ATTENTION: {
+            int rc = R9Q_OK;
+            const size_t need = decode_workspace(op, M, N, &rc);
+            if (!rc) *bytes = need;
+            return rc;
         }
         default: return R9Q_ERR_ARG;
     }

@@ -17,6 +17,7 @@ constexpr int kBlock = 128;                 // scale block edge (K group and wei
 constexpr uint32_t kSpinLimit = 1u << 18;
 constexpr uint32_t kCountSpinLimit = 1u << 22;
 constexpr int kErrTimeout = -6;             // R9Q_ERR_TIMEOUT
+constexpr int kErrArg = -8;                 // R9Q_ERR_ARG
 
 // ------------------------------------------------------------------ basics --
 

@@ -124,8 +124,11 @@ cudaError_t launch_tc_gemm(const CUtensorMap& amap, const CUtensorMap& bmap, con
                            int splits, float* part, int* done, int* exits, int M, int N, int K, int* err, int sms,
                            cudaStream_t st);
 
-// The current device's error word (kernels record bounded-wait timeouts there).
+// The current device's error word (kernels record bounded-wait timeouts and
+// out-of-range indices there).
 int device_error_word(int** out);
+// The same and the SM count.
+int device_error_word_and_sms(int** out, int* sms);
 
 // ---- elementwise / quantisation ----
 cudaError_t launch_e4m3_from_f32(const float* x, int64_t n, uint8_t* q, cudaStream_t st, int sms);
@@ -135,5 +138,71 @@ cudaError_t launch_quant_weight_block128(const float* w, int64_t N, int64_t K, u
                                          cudaStream_t st);
 cudaError_t launch_swiglu_interleaved(const uint16_t* gu, int64_t M, int64_t I, uint16_t* h,
                                       cudaStream_t st, int sms);
+
+// ---- QK norm + rotation, 4-bit cache, attention over it ----
+// A [T][H][D] bf16 tensor whose token and head strides (in elements) are free.
+struct HeadsIn {
+    const uint16_t* p;
+    int64_t ts, hs;
+    int heads;
+};
+struct HeadsOut {
+    uint16_t* p;
+    int64_t ts, hs;
+};
+// The paged 4-bit cache (layout: r9q_kv4.cuh).
+struct Kv4Cache {
+    uint8_t* k;
+    uint32_t* kp;
+    uint8_t* v;
+    uint32_t* vp;
+    int64_t pages;
+    int heads, page;
+};
+struct RopeParams {
+    const float *wq, *wk;        // norm weights [D]
+    const float *cos, *sin;      // [npos][rot / 2]
+    const int64_t* pos;          // [T]
+    int64_t T, npos;
+    int rot;
+    float eps;
+    int interleaved;
+    int* err;
+};
+cudaError_t launch_qk_norm_rope(int D, const HeadsIn& q, const HeadsIn& k, const RopeParams& p, const HeadsOut& qo,
+                                const HeadsOut& ko, cudaStream_t st);
+// The same pass, with K (normalised and rotated) and V (as it is) quantised into the cache.
+cudaError_t launch_qk_norm_rope_kv4(int D, const HeadsIn& q, const HeadsIn& k, const HeadsIn& v, const RopeParams& p,
+                                    const HeadsOut& qo, const Kv4Cache& c, const int64_t* slots, cudaStream_t st);
+cudaError_t launch_kv4_append(int D, const HeadsIn& k, const HeadsIn& v, int64_t T, const Kv4Cache& c,
+                              const int64_t* slots, int* err, cudaStream_t st);
+cudaError_t launch_kv4_gather(int D, const Kv4Cache& c, const int64_t* slots, int64_t T, uint16_t* k, uint16_t* v,
+                              int* err, cudaStream_t st);
+// Gradient; `part`: qk_norm_rope_bwd_blocks(sms) x 2 x D floats, `done`: one zeroed counter (left at zero).
+int qk_norm_rope_bwd_blocks(int sms);
+cudaError_t launch_qk_norm_rope_bwd(int D, const HeadsIn& dqo, const HeadsIn& dko, const HeadsIn& q, const HeadsIn& k,
+                                    const RopeParams& p, const HeadsOut& dq, const HeadsOut& dk, float* dwq,
+                                    float* dwk, float* part, int* done, int sms, cudaStream_t st);
+
+struct Kv4AttnParams {
+    const uint16_t* q;           // [B][Lq][Hq][D], last dimension contiguous
+    int64_t q_bs, q_ts, q_hs;
+    Kv4Cache c;
+    const int32_t* table;        // [B][max_pages]
+    const int32_t* lens;         // [B]
+    uint16_t* o;                 // [B][Lq][Hq][D] contiguous
+    float* lse;                  // [B][Lq][Hq] or nullptr
+    float* part;                 // split partials
+    int* done;                   // one counter per CTA, zero between calls
+    int* err;
+    int B, Lq, G, max_pages, window;
+    float scale_log2;            // softmax scale * log2(e)
+};
+// CTAs of the launch, and floats of `part` for them.
+int kv4_attention_ctas(int D, int64_t rows, int sms);
+size_t kv4_attention_part_floats(int D, int64_t rows, int sms);
+// Workspace bytes of R9Q_OP_QK_NORM_ROPE_BWD and R9Q_OP_KV4_ATTENTION (M rows, N = D).
+size_t decode_workspace(int op, int64_t M, int64_t N, int* rc);
+cudaError_t launch_kv4_attention(int D, const Kv4AttnParams& p, int sms, cudaStream_t st);
 
 }  // namespace r9q

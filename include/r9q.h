@@ -240,10 +240,117 @@ int r9q_gate_up_swiglu_down_noalloc(const void* x_bf16,
                                     void* y_bf16, int64_t M, int64_t H, int64_t I, int64_t H_out,
                                     uint8_t* hq_out, float* hs_out, int flags, void* stream);
 
+/* ---- The attention block of a decode layer: between the QKV GEMM and the
+ * output GEMM.  The pages have no counterpart.
+ *
+ * Head tensors are bf16 [T][H][D], D = 64 or 128, with free token and head
+ * strides in elements (multiples of 8, so that every vector is 16-byte aligned;
+ * slices of the QKV GEMM's output are such tensors).  Outputs may not overlap
+ * inputs, and an output's own vectors may not overlap one another; the q and k
+ * outputs may be slices of one buffer.  T = 0 is a no-op (the gradient then
+ * writes zeros to dwq and dwk).
+ * Positions, slots and page numbers are read on the device.  One that is out of
+ * range reads and writes nothing out of bounds: it sets the device error word to
+ * R9Q_ERR_ARG (r9q_last_device_error), and its token's outputs are NaN (a
+ * position), or it is passed over (a slot, a page).
+ *
+ * RMS norm of every query and key head, and the position rotation, in one pass:
+ *   y = w x / sqrt(mean(x^2) + eps), then each pair (a, b) of the first rot
+ *   elements becomes (a cos - b sin, b cos + a sin), with (cos, sin) row pos[t],
+ *   column i of the tables fp32 [npos][rot/2] for pair i.  Pairs are elements
+ *   (i, i + rot/2), or with R9Q_ROPE_INTERLEAVED (2i, 2i + 1).
+ * wq, wk fp32 [D]; rot a multiple of 16, 0..D (0: norm only; cos, sin and pos may
+ * then be NULL); cos and sin 16-byte aligned; pos int64 [T].  fp32 inside, one
+ * rounding to bf16. */
+#define R9Q_ROPE_INTERLEAVED 1
+int r9q_qk_norm_rope(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts, int64_t k_hs,
+                     const float* wq, const float* wk, const float* cos, const float* sin, const int64_t* pos,
+                     void* q_out, int64_t qo_ts, int64_t qo_hs, void* k_out, int64_t ko_ts, int64_t ko_hs,
+                     int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t npos, float eps, int flags,
+                     void* stream);
+
+/* Its gradient: from dq_out, dk_out and the forward's inputs, dq and dk (bf16)
+ * and the weights' gradients dwq, dwk fp32 [D], summed over tokens and heads in
+ * fp32 in an order that does not depend on timing.  All outputs are overwritten.
+ * workspace: r9q_workspace_bytes(R9Q_OP_QK_NORM_ROPE_BWD, T, D, ...), zeroed
+ * before its first use and left with a zero header by every call, as for
+ * r9q_gemm_fp8_block_qa; one workspace can serve all these calls on a stream. */
+int r9q_qk_norm_rope_bwd(const void* dq_out, int64_t dqo_ts, int64_t dqo_hs, const void* dk_out, int64_t dko_ts,
+                         int64_t dko_hs, const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts,
+                         int64_t k_hs, const float* wq, const float* wk, const float* cos, const float* sin,
+                         const int64_t* pos, void* dq, int64_t dq_ts, int64_t dq_hs, void* dk, int64_t dk_ts,
+                         int64_t dk_hs, float* dwq, float* dwk, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                         int64_t rot, int64_t npos, float eps, int flags, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* The paged 4-bit key-value cache.  A page holds `page` tokens (a multiple of
+ * 16) of all Hk heads.  A token's head vector x is held as D codes of 4 bits and
+ * a bf16 pair: lowest = bf16(min x), step = bf16((max x - min x) / 15),
+ * code = clamp(rint((x - lowest) / step), 0, 15) (0 where step = 0), each step in
+ * fp32; it stands for lowest + step * code.  A vector that holds a NaN or an
+ * infinity is kept as NaN.
+ *   kc  u8   [pages][Hk][page][D/2]: byte i holds elements 2i (low nibble), 2i+1
+ *   vc  u8   [pages][Hk][page/16][D/64][8 r][4 j][4 m][4 b]: token t of 16 has
+ *            j = (t % 8) / 2, b = 2 (t % 2) + t / 8; element 64c + 16m + 8n + r is
+ *            nibble n of byte [c][r][j][m][b]
+ *   kp, vp   bf16 [pages][Hk][page][2]: (step, lowest)
+ * kc, vc 16-byte, kp, vp 4-byte aligned.  Slot s is token s % page of page
+ * s / page; a negative slot is padding, which is not written, and read as zero.
+ * Slots of one call that are written twice hold either token.
+ *
+ * r9q_kv4_append quantises k and v (bf16 [T][Hk][D]) into the cache at slots
+ * int64 [T].  r9q_qk_norm_rope_kv4 is r9q_qk_norm_rope that writes the keys, and
+ * v as it is, to the cache instead of k_out; the keys are quantised from their
+ * fp32 values, without a rounding to bf16 in between.  r9q_kv4_gather reads
+ * tokens back as bf16 k, v [T][Hk][D] (contiguous, 16-byte aligned). */
+int r9q_qk_norm_rope_kv4(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts, int64_t k_hs,
+                         const void* v, int64_t v_ts, int64_t v_hs, const float* wq, const float* wk,
+                         const float* cos, const float* sin, const int64_t* pos, void* q_out, int64_t qo_ts,
+                         int64_t qo_hs, uint8_t* kc, void* kp, uint8_t* vc, void* vp, const int64_t* slots,
+                         int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t rot, int64_t npos, int64_t pages,
+                         int64_t page, float eps, int flags, void* stream);
+int r9q_kv4_append(const void* k, int64_t k_ts, int64_t k_hs, const void* v, int64_t v_ts, int64_t v_hs,
+                   uint8_t* kc, void* kp, uint8_t* vc, void* vp, const int64_t* slots, int64_t T, int64_t Hk,
+                   int64_t D, int64_t pages, int64_t page, void* stream);
+int r9q_kv4_gather(const uint8_t* kc, const void* kp, const uint8_t* vc, const void* vp, const int64_t* slots,
+                   int64_t T, int64_t Hk, int64_t D, int64_t pages, int64_t page, void* k, void* v, void* stream);
+
+/* Attention of the last Lq tokens of B sequences over their cached keys and
+ * values, the new tokens' own among them (append first).
+ *   q  bf16 [B][Lq][Hq][D] with free strides (multiples of 8 elements);
+ *   block_table int32 [B][max_pages]: the page of each `page` tokens of a sequence
+ *      (entries that hold no visible token are not used);
+ *   seq_lens int32 [B]: tokens in the cache, the new ones included; 0 for an unused
+ *      place of the batch.  Both on the device.
+ *   o  bf16 [B][Lq][Hq][D], lse fp32 [B][Lq][Hq] or NULL, contiguous.
+ * New token i of a sequence of length n stands at p = n - Lq + i and sees the keys
+ * at max(0, p - window + 1) .. p (window 0: all up to p); with s_t = scale q.k_t
+ *   o = sum_t exp(s_t) v_t / sum_t exp(s_t),   lse = log sum_t exp(s_t).
+ * A token that sees nothing (p < 0) gets o = 0, lse = -infinity.  Query head h
+ * uses key-value head h / (Hq / Hk).  Keys that a token does not see do not reach
+ * its result, whatever they hold (NaN and infinities too).  scale > 0.
+ * Scores, sums and accumulators are fp32; weights are rounded to fp16.  The
+ * result does not depend on timing; its last bits depend on the lengths of the
+ * whole batch (they decide where the work is cut).
+ * Built for few rows Lq * Hq / Hk of a key-value head: each 16 of them read the
+ * codes again.  workspace: r9q_workspace_bytes(R9Q_OP_KV4_ATTENTION,
+ * Lq * Hq / Hk, D, ...), zeroed before its first use and left with a zero header
+ * by every call, as for r9q_gemm_fp8_block_qa.
+ * Errors of all of these: R9Q_ERR_NULL, R9Q_ERR_DIM, R9Q_ERR_ALIGN (pointers,
+ * strides), R9Q_ERR_ARG (flags, eps, scale, overlap), R9Q_ERR_WORKSPACE,
+ * R9Q_ERR_DEVICE, R9Q_ERR_LAUNCH. */
+int r9q_kv4_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, const uint8_t* kc, const void* kp,
+                      const uint8_t* vc, const void* vp, const int32_t* block_table, const int32_t* seq_lens,
+                      void* o, float* lse, int64_t B, int64_t Lq, int64_t Hq, int64_t Hk, int64_t D, int64_t pages,
+                      int64_t page, int64_t max_pages, int64_t window, float scale, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
 /* Workspace query. */
 #define R9Q_OP_GEMM_W8A8            1   /* (M, N, K) */
 #define R9Q_OP_GEMM_W8BF16          2   /* (M, N, K) */
 #define R9Q_OP_GATE_UP_SWIGLU_DOWN  3   /* (M, N=I, K=H, N2=H_out, flags) */
+#define R9Q_OP_QK_NORM_ROPE_BWD     4   /* (M=T, N=D) */
+#define R9Q_OP_KV4_ATTENTION        5   /* (M=Lq*Hq/Hk, N=D) */
 /* Writes the bytes of device workspace the call needs (0 = none) to *bytes. */
 int r9q_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int64_t N2, int flags,
                         size_t* bytes);
