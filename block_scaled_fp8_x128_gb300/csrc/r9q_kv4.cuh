@@ -45,7 +45,7 @@ __device__ __forceinline__ float group_max(float v) {
 }
 
 // Quantises a head vector held by NL = D/8 adjacent lanes, 8 elements each.
-// lowest = bf16(min), step = bf16((max - min) / 15), both rounded to nearest (a
+// lowest = bf16(min), step = bf16((max - min) fl32(1/15)), both rounded to nearest (a
 // 16-bit pair keeps the cost at 4 bytes a vector, and codes are taken against
 // the rounded pair, so its rounding only moves the grid by a fraction of a
 // step); code = clamp(rint((x - lowest) / step), 0, 15) with the IEEE fp32
@@ -66,7 +66,7 @@ __device__ __forceinline__ uint32_t kv4_quantise(const float (&x)[8], uint32_t& 
     lo = -group_max<NL>(-lo);
     bad = group_sum<NL>(bad);
     const float low = bf16_round(lo) + bad;
-    const float step = bf16_round(__fdiv_rn(hi - lo, 15.0f)) + bad;
+    const float step = bf16_round(__fmul_rn(hi - lo, 1.0f / 15.0f)) + bad;
     pair = pack_bf16x2(step, low);
     uint32_t codes = 0;
     if (step > 0.0f) {

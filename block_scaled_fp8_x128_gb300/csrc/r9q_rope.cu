@@ -110,6 +110,72 @@ __device__ __forceinline__ void fold_weight(Turn& u, const float* w, int lane, i
     }
 }
 
+// Sum of the squares of a head vector in a fixed order, one rounding a step: 32
+// partial sums of every 32nd square, in their order, then a binary tree over
+// neighbouring partial sums.  Lanes that are D/32 lanes' worth of elements apart
+// hold a partial sum's terms; they exchange them so that each forms 32 / NL of
+// the partial sums.
+template <int NL>
+__device__ __forceinline__ float sum_squares_in_order(const float (&x)[8], int l) {
+    float q[8], s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(x[i], x[i]);
+    if constexpr (NL == 8) {                              // lanes l, l ^ 4: four partial sums each, two terms
+        const bool up = l & 4;
+        float p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float other = __shfl_xor_sync(0xffffffffu, up ? q[i] : q[4 + i], 4);
+            p[i] = __fadd_rn(up ? q[4 + i] : q[i], other);
+        }
+        s = __fadd_rn(__fadd_rn(p[0], p[1]), __fadd_rn(p[2], p[3]));
+        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 4));
+    } else {                                              // lanes l, l ^ 4, l ^ 8, l ^ 12: two partial sums, four terms
+        const bool hi = l & 8, lo = l & 4;
+        float a[4], b[4];                                 // elements 4 hi .. 4 hi + 3 of this lane and of l ^ 8
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = hi ? q[4 + i] : q[i];
+            b[i] = __shfl_xor_sync(0xffffffffu, hi ? q[i] : q[4 + i], 8);
+        }
+        float p[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float a1 = __shfl_xor_sync(0xffffffffu, lo ? a[i] : a[2 + i], 4);
+            const float b1 = __shfl_xor_sync(0xffffffffu, lo ? b[i] : b[2 + i], 4);
+            const float a0 = lo ? a[2 + i] : a[i], b0 = lo ? b[2 + i] : b[i];
+            // the terms by their lanes: l & 3, + 4, + 8, + 12
+            const float t0 = hi ? (lo ? b1 : b0) : (lo ? a1 : a0), t1 = hi ? (lo ? b0 : b1) : (lo ? a0 : a1);
+            const float t2 = hi ? (lo ? a1 : a0) : (lo ? b1 : b0), t3 = hi ? (lo ? a0 : a1) : (lo ? b0 : b1);
+            p[i] = __fadd_rn(__fadd_rn(__fadd_rn(t0, t1), t2), t3);
+        }
+        s = __fadd_rn(p[0], p[1]);                        // partial sums 8 (l & 3) + 4 hi + 2 lo, and the next
+        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 4));
+        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 8));
+    }
+    s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 1));
+    return __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 2));
+}
+
+// A key on its way to 4 bits.  A code flips where its value lies within an fp32
+// rounding of the middle between two codes, so the keys' value is fixed to the
+// last bit: (x r) w, the two products of the rotation and their sum each round
+// once, and the sum of squares has a fixed order.  An evaluation of the formula
+// step by step in fp32 gives the same codes.
+template <int NL>
+__device__ __forceinline__ void norm_rope_in_order(float (&y)[8], const float (&w)[8], const Turn& u, int lane,
+                                                   const RopeParams& p) {
+    const float mean = __fmul_rn(sum_squares_in_order<NL>(y, lane & (NL - 1)), 1.0f / (8 * NL));
+    const float r = rsqrtf(__fadd_rn(mean, p.eps));
+    float z[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(__fmul_rn(y[e], r), w[e]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = p.interleaved ? y[e ^ 1] : __shfl_sync(0xffffffffu, y[e], u.src);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = __fadd_rn(__fmul_rn(y[e], u.c[e]), __fmul_rn(z[e], u.s[e]));
+}
+
 enum Pass { kRope, kRopeCache, kAppend };
 
 struct ForwardArgs {
@@ -172,10 +238,17 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const ForwardArgs a) 
     Place place = {-1, 0};
     if (PASS != kRope && kind > 0) place = find_slot(a.c, a.slots[t], lane, a.rope.err);
     const bool turned = PASS != kAppend && kind < 2;
+    const bool in_order = PASS == kRopeCache && kind == 1;
     Turn u;
+    float w[8];
     if (turned) {
         u = load_turn<D>(a.rope, t, lane);
-        fold_weight<D>(u, kind == 0 ? a.rope.wq : a.rope.wk, lane, a.rope.interleaved);
+        if (in_order) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = a.rope.wk[8 * l + e];
+        } else {
+            fold_weight<D>(u, kind == 0 ? a.rope.wq : a.rope.wk, lane, a.rope.interleaved);
+        }
     }
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
@@ -183,7 +256,9 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const ForwardArgs a) 
         if (part * HPW + i * NV >= in.heads) break;      // the same for the whole warp
         float y[8];
         unpack8(x[i], y);
-        if (turned) {
+        if (in_order) {
+            norm_rope_in_order<NL>(y, w, u, lane, a.rope);
+        } else if (turned) {
             float xp[8], ss = 0.0f;
             unpack8(partner(x[i], u, a.rope.interleaved), xp);
 #pragma unroll

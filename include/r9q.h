@@ -285,7 +285,7 @@ int r9q_qk_norm_rope_bwd(const void* dq_out, int64_t dqo_ts, int64_t dqo_hs, con
 
 /* The paged 4-bit key-value cache.  A page holds `page` tokens (a multiple of
  * 16) of all Hk heads.  A token's head vector x is held as D codes of 4 bits and
- * a bf16 pair: lowest = bf16(min x), step = bf16((max x - min x) / 15),
+ * a bf16 pair: lowest = bf16(min x), step = bf16((max x - min x) * fl32(1/15)),
  * code = clamp(rint((x - lowest) / step), 0, 15) (0 where step = 0), each step in
  * fp32; it stands for lowest + step * code.  A vector that holds a NaN or an
  * infinity is kept as NaN.
@@ -300,9 +300,13 @@ int r9q_qk_norm_rope_bwd(const void* dq_out, int64_t dqo_ts, int64_t dqo_hs, con
  *
  * r9q_kv4_append quantises k and v (bf16 [T][Hk][D]) into the cache at slots
  * int64 [T].  r9q_qk_norm_rope_kv4 is r9q_qk_norm_rope that writes the keys, and
- * v as it is, to the cache instead of k_out; the keys are quantised from their
- * fp32 values, without a rounding to bf16 in between.  r9q_kv4_gather reads
- * tokens back as bf16 k, v [T][Hk][D] (contiguous, 16-byte aligned). */
+ * v as it is, to the cache instead of k_out.  The keys are quantised from their
+ * fp32 values, without a rounding to bf16 in between, and these are fixed to the
+ * last bit so that the codes are reproducible: each step rounds once ((x r) w, the
+ * rotation's two products, their sum), r = rsqrtf(sum / D + eps), and the sum of
+ * squares is that of 32 partial sums, of every 32nd square in order, added as a
+ * binary tree of neighbours.  r9q_kv4_gather reads tokens back as bf16 k, v
+ * [T][Hk][D] (contiguous, 16-byte aligned). */
 int r9q_qk_norm_rope_kv4(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts, int64_t k_hs,
                          const void* v, int64_t v_ts, int64_t v_hs, const float* wq, const float* wk,
                          const float* cos, const float* sin, const int64_t* pos, void* q_out, int64_t qo_ts,

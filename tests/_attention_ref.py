@@ -47,7 +47,7 @@ def quantise32(x):
     x = np.ascontiguousarray(x, np.float32)
     with np.errstate(all="ignore"):
         lo, hi = x.min(-1, keepdims=True), x.max(-1, keepdims=True)
-        low, step = to_bf16(lo), to_bf16((hi - lo) / np.float32(15))
+        low, step = to_bf16(lo), to_bf16((hi - lo) * np.float32(1 / 15))
         q = np.where(step > 0, (x - low) / np.where(step > 0, step, np.float32(1)), np.float32(0))
         codes = np.clip(np.rint(q), 0, 15)
     return np.where(np.isfinite(codes), codes, 0).astype(np.int64), step, low
