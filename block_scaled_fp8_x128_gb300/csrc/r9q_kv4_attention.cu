@@ -18,18 +18,21 @@
 // [2^13, 2^14), where fp16 holds bf16 values exactly down to 2^-27 of it.  The
 // weights P sv are rounded to fp16 (11 bits; bf16 would keep 8).  To keep them in
 // its range a row's weights are taken not against its largest score alone but
-// against m2 = largest score - 14 + E, E the exponent of the largest step its keys
-// have had: they stay under 2^15, and 2^-28 of the largest still has full precision.
+// against m2 = largest score - 8 + E, E the exponent of the largest step its keys have had.
+// m2 moves only when a score passes it by 2^6 (or a step is larger than any before):
+// weights stay under 2^15, 2^-22 of the largest still has full precision, and most steps
+// neither reduce a maximum over the warp nor touch the accumulators.
 // Both sums use the same weights, so the power of two cancels.  Scores, maxima,
 // sums and accumulators are fp32.
 //
-// Work is cut in groups of 16 keys.  All CTAs are resident; each takes an equal,
-// contiguous range of the groups of all (sequence, kv head, row chunk) items,
-// counted on the device from the lengths, so ragged batches and single long
-// sequences fill the GPU alike.  The four warps of a CTA take 32-key steps of its
-// range in turn, each with its own running maximum, and meet in shared memory at
-// the item's end.  An item that several CTAs share leaves fp32 partials; the CTA
-// that arrives last joins them in CTA order.
+// Work is cut in groups of 16 keys, on the device, from the lengths, so that ragged
+// batches and single long sequences fill the GPU alike.  All CTAs are resident.  With
+// few items (sequence, kv head, row chunk) each is cut into equal parts, one a CTA;
+// with many, each CTA takes an equal, contiguous range of all items' groups, its ends
+// moved to an item's end where that is near.  The four warps of a CTA take 32-key steps of a part in
+// turn, each with its own running reference, and meet in shared memory at its end.
+// An item that several CTAs share leaves fp32 partials; the CTA that arrives last
+// joins them in CTA order.
 //
 // HBM bound (136 bytes a token and head at D = 128).  Lanes copy exactly the
 // bytes they will use (cp.async, 16 bytes, a ring of stages in shared memory per
@@ -43,13 +46,17 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 32;                    // keys a warp takes at a time: two groups of 16
-constexpr int kStages = 4;
-constexpr int kMinGroups = 8;                // groups a CTA takes at least: one step for each warp
+constexpr int kMinGroups = 2 * kWarps;       // groups a CTA takes at least: one step for each warp
 constexpr int kMinExponent = 67;             // value steps under 2^-60 count as that (keeps the sums finite)
+constexpr int kHeadroom = 8;                 // weights at the reference score are 2^8 to 2^9
+constexpr float kSlack = 6.0f;               // powers of two a score may pass the reference by
 constexpr float kLn2 = 0.69314718055994531f;
+constexpr uint32_t kNoGroup = 0xFFFFFFFFu;
 
+constexpr int stages(int D) { return D == 64 ? 4 : 4; }
+constexpr int ctas_per_sm(int D, int NT) { return (D == 64 ? 4 : 3) - (NT - 1); }
 constexpr int stage_bytes(int D) { return kStep * D + kStep * 8; }
-constexpr int ring_bytes(int D) { return kWarps * kStages * stage_bytes(D); }
+constexpr int ring_bytes(int D) { return kWarps * stages(D) * stage_bytes(D); }
 constexpr int out_stride(int D) { return D + 4; }      // floats a row of the CTA's exchange takes
 constexpr int exchange_bytes(int D, int NT) { return kWarps * 8 * NT * (out_stride(D) + 2) * 4; }
 constexpr int work_bytes(int D, int NT) {              // the rings, and after them the exchange in their place
@@ -57,11 +64,10 @@ constexpr int work_bytes(int D, int NT) {              // the rings, and after t
 }
 // What the threads of a CTA tell one another about its range.
 struct Shared {
-    long long scan[kWarps], first;
+    long long scan[2][kWarps], first;
     int seq, last;
 };
 constexpr int smem_bytes(int D, int NT) { return work_bytes(D, NT) + (int)sizeof(Shared); }
-constexpr int ctas_per_sm(int D, int NT) { return (D == 64 ? 4 : 3) - (NT - 1); }
 
 template <int N>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
@@ -97,11 +103,12 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __noinline__ long long div64(long long a, long long b) { return a / b; }
 
-// A sequence's keys: [lo, len) are seen by at least one new token.
+// A sequence's keys and the groups an item of it has.
 struct Span {
     int len, g0;             // tokens; first group that holds a visible key
-    int groups;              // groups of an item of it, at least one (an empty one writes zeros)
+    int groups;              // at least one (an empty sequence's items write zeros)
 };
 __device__ __forceinline__ Span span_of(const Kv4AttnParams& p, int b) {
     Span s;
@@ -119,9 +126,23 @@ __device__ __forceinline__ Span span_of(const Kv4AttnParams& p, int b) {
     return s;
 }
 
-// What a column's weights are taken against (m2 above); 0 while it has seen no key.
-__device__ __forceinline__ float reference(float m, float fr, int es) {
-    return m > -__builtin_huge_valf() ? fmaf(m, fr, (float)(es - 127 - 14)) : 0.0f;
+// The CTA's inclusive scan of one value a thread; `total` over all.
+__device__ __forceinline__ long long cta_scan(long long v, long long (&sums)[kWarps], long long& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+    }
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) v += sums[w];
+        total += sums[w];
+    }
+    return v;
 }
 
 // The log of the sum of exponentials, from the sum of weights l and their reference m.
@@ -129,12 +150,191 @@ __device__ __forceinline__ float log_sum_exp(float m, float l) {
     return l > 0.0f || l != l ? (m + log2f(l)) * kLn2 : __int_as_float(0xFF800000);
 }
 
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// A warp's state for NT tiles of 8 rows; a lane has columns (rows of the query)
+// 2j and 2j + 1 of each.
+template <int D, int NT>
+struct State {
+    uint32_t qf[NT][D / 16][2];              // query fragments
+    float fr[NT][2], qs[NT][2];              // score = fr (sk acc + lk qs)
+    int hi[NT][2], lo[NT][2];                // keys that the column sees: [lo, hi]
+    float acc[NT][D / 16][4], l[NT][2], ml[NT][2];
+    float top[NT][2], lim[NT][2], ref[NT][2];    // largest score / fr at the last move, when to move, reference m2
+    int es[NT][2], es_min;                   // exponent field that stands for the columns' values
+};
+
+// One step: 32 keys in the stage `st`, of which groups `bits` were loaded.
+// MASKED: some column does not see some key, or a group is missing.
+template <int D, int NT, bool MASKED>
+__device__ __forceinline__ void attend(State<D, NT>& s, const uint8_t* st, int key0, uint32_t bits, int len, int lane) {
+    constexpr int KW = D / 32, MT = D / 16;
+    const int r = lane >> 2;
+    // pairs of the lane's keys r + 8h of group i
+    const uint4 kp = *reinterpret_cast<const uint4*>(st + kStep * D + r * 16);
+    uint4 vp = *reinterpret_cast<const uint4*>(st + kStep * D + kStep * 4 + r * 16);
+    uint32_t kq[2][2] = {{kp.x, kp.y}, {kp.z, kp.w}}, vq[2][2] = {{vp.x, vp.y}, {vp.z, vp.w}};
+    if (MASKED) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (!((bits >> i) & 1u) || key0 + 16 * i + 8 * h + r >= len) kq[i][h] = vq[i][h] = 0u;
+    }
+
+    // ---- scores over fr ----
+    float sc[NT][2][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t k0[KW], k1[KW];
+        const uint8_t* kb = st + i * 16 * (D / 2) + lane * (KW * 4);
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+            k0[w] = reinterpret_cast<const uint32_t*>(kb)[w];
+            k1[w] = reinterpret_cast<const uint32_t*>(kb + 8 * (D / 2))[w];
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sc[nt][i][c] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+            const uint32_t x0 = k0[w] >> 8, x1 = k1[w] >> 8;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                mma_f16_16816(sc[nt][i], k0[w] & 0x000F000Fu, k1[w] & 0x000F000Fu, k0[w] & 0x00F000F0u,
+                              k1[w] & 0x00F000F0u, s.qf[nt][2 * w][0], s.qf[nt][2 * w][1]);
+                mma_f16_16816(sc[nt][i], x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x00F000F0u,
+                              s.qf[nt][2 * w + 1][0], s.qf[nt][2 * w + 1][1]);
+            }
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t pair = kq[i][c >> 1];
+                float v = fmaf(bf16_lo(pair), sc[nt][i][c], bf16_hi(pair) * s.qs[nt][c & 1]);
+                if (MASKED) {
+                    const int key = key0 + 16 * i + 8 * (c >> 1) + r;
+                    if (key > s.hi[nt][c & 1] || key < s.lo[nt][c & 1] || !((bits >> i) & 1u)) v = kNegInf;
+                }
+                sc[nt][i][c] = v;
+            }
+
+    // ---- does the reference hold? ----
+    // The exponent of a key's values: that of its step, or of its lowest value when that is over 2^10 steps
+    // (the sum of p lv is kept in the same scale).
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) any = __vmaxu2(any, vq[i][h] & 0x7FFF7FFFu);
+    int e = max((int)((any & 0xFFFFu) >> 7), (int)(any >> 23) - 10);
+    float x[NT][2];
+    bool move = MASKED || e > s.es_min;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            x[nt][c] = fmaxf(fmaxf(sc[nt][0][c], sc[nt][0][c + 2]), fmaxf(sc[nt][1][c], sc[nt][1][c + 2]));
+            move = move || x[nt][c] > s.lim[nt][c];
+        }
+    if (__any_sync(0xffffffffu, move)) {
+        int ek[2][2];                        // by key; none for a pair that is not finite
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int xs = (int)(vq[i][h] >> 7) & 255, xl = (int)(vq[i][h] >> 23) & 255;
+                ek[i][h] = xs == 255 || xl == 255 ? 0 : max(xs, xl - 10);
+            }
+        s.es_min = 255;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                int ec = 0;                  // only of keys that the column sees
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (!MASKED || sc[nt][i][2 * h + c] != kNegInf) ec = max(ec, ek[i][h]);
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    x[nt][c] = fmaxf(x[nt][c], __shfl_xor_sync(0xffffffffu, x[nt][c], o));
+                    ec = max(ec, __shfl_xor_sync(0xffffffffu, ec, o));
+                }
+                const float before = s.top[nt][c], now = fmaxf(before, x[nt][c]), old = s.ref[nt][c];
+                s.es[nt][c] = max(s.es[nt][c], ec);
+                s.es_min = min(s.es_min, s.es[nt][c]);
+                s.top[nt][c] = now;
+                s.lim[nt][c] = now + kSlack / s.fr[nt][c];
+                float alpha = 0.0f;          // nothing seen before: the sums are zero
+                if (now > kNegInf) {
+                    s.ref[nt][c] = fmaf(now, s.fr[nt][c], (float)(s.es[nt][c] - 127 - kHeadroom));
+                    if (before > kNegInf) alpha = ex2(old - s.ref[nt][c]);
+                }
+                s.l[nt][c] *= alpha;
+                s.ml[nt][c] *= alpha;
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    s.acc[nt][t][c] *= alpha;
+                    s.acc[nt][t][c + 2] *= alpha;
+                }
+            }
+    }
+
+    // ---- weights ----
+    uint32_t pf[NT][2][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float w[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float v = sc[nt][i][2 * h + c];
+                    const float pr = ex2(fmaf(v, s.fr[nt][c], -s.ref[nt][c]));
+                    float sv = bf16_lo(vq[i][h]), lv = bf16_hi(vq[i][h]);
+                    if (MASKED && v == kNegInf) sv = lv = 0.0f;         // not 0 * infinity
+                    w[c] = pr * sv;
+                    s.l[nt][c] += pr;
+                    s.ml[nt][c] = fmaf(pr, lv, s.ml[nt][c]);
+                }
+                pf[nt][i][h] = transpose_8x8(pack_f16x2(w[0], w[1]));
+            }
+
+    // ---- values ----
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint8_t* vb = st + kStep * (D / 2) + i * 16 * (D / 2) + lane * 16;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            const uint4 q4 = *reinterpret_cast<const uint4*>(vb + c * 512);
+            const uint32_t q[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const uint32_t y = q[m] >> 8;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_f16_16816(s.acc[nt][4 * c + m], q[m] & 0x000F000Fu, q[m] & 0x00F000F0u, y & 0x000F000Fu,
+                                  y & 0x00F000F0u, pf[nt][i][0], pf[nt][i][1]);
+            }
+        }
+    }
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_kernel(const Kv4AttnParams p) {
     constexpr int KW = D / 32;               // 32-bit words of a key that a lane holds
     constexpr int MT = D / 16;               // 16-element tiles
     constexpr int R = 8 * NT;                // rows of a chunk
-    constexpr float kNegInf = -__builtin_huge_valf();
+    constexpr int ST = stages(D);
     extern __shared__ __align__(16) uint8_t smem[];
     Shared& sh = *reinterpret_cast<Shared*>(smem + work_bytes(D, NT));
 
@@ -142,37 +342,40 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
     const int r = lane >> 2, j = lane & 3;
     const int rows = p.Lq * p.G, chunks = (rows + R - 1) / R;
     const int items_per_seq = p.c.heads * chunks;
+    const long long items = (long long)p.B * items_per_seq, ctas = gridDim.x;
 
-    // ---- this CTA's range of groups [u0, u1) and the sequence it begins in ----
+    // ---- what this CTA does ----
     const int per_thread = (p.B + kThreads - 1) / kThreads;
     const int b_first = tid * per_thread, b_end = min(p.B, b_first + per_thread);
-    long long mine = 0;
-    for (int b = b_first; b < b_end; ++b) mine += (long long)span_of(p, b).groups * items_per_seq;
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+    long long mine = 0, total;
+    for (int b = b_first; b < b_end; ++b) mine += span_of(p, b).groups;
+    mine *= items_per_seq;
+    long long upto = cta_scan(mine, sh.scan[0], total);
+    const bool parted = 2 * items <= ctas;   // one part of one item a CTA
+    long long per;                           // groups of a part, or of a CTA's range
+    if (parted) {
+        // sum of ceil(groups / per) over the items is at most total / per + items <= ctas
+        per = (total + ctas - items - 1) / (ctas - items);
+        if (per < kMinGroups) per = kMinGroups;
+        mine = 0;                            // from here on: parts
+        for (int b = b_first; b < b_end; ++b) mine += (span_of(p, b).groups + (int)per - 1) / (int)per;
+        mine *= items_per_seq;
+        upto = cta_scan(mine, sh.scan[1], total);
+    } else {
+        per = div64(total + ctas - 1, ctas);
+        if (per < kMinGroups) per = kMinGroups;
     }
-    if (lane == 31) sh.scan[warp] = incl;
-    __syncthreads();
-    long long before = incl - mine, total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sh.scan[w];
-        total += sh.scan[w];
-    }
-    long long per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < kMinGroups) per = kMinGroups;
-    const long long u0 = (long long)blockIdx.x * per;
-    const long long u1 = u0 + per < total ? u0 + per : total;
-    if (u0 >= total) return;
-    if (u0 >= before && u0 < before + mine) {
-        long long at = before;
+    // An end of a range inside an item goes to the item's end where that is within `snap` groups of it.
+    auto snap_of = [&](int groups) { return min(min(8, (int)min(per / 4, 8ll)), (groups - 1) / 2); };
+    long long u = parted ? blockIdx.x : blockIdx.x * per;
+    if (u >= total) return;
+    if (u >= upto - mine && u < upto) {
+        long long at = upto - mine;
         int b = b_first;
         for (;; ++b) {
-            const long long n = (long long)span_of(p, b).groups * items_per_seq;
-            if (u0 < at + n) break;
+            const int g = span_of(p, b).groups;
+            const long long n = (long long)(parted ? (g + (int)per - 1) / (int)per : g) * items_per_seq;
+            if (u < at + n) break;
             at += n;
         }
         sh.seq = b;
@@ -180,30 +383,99 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
     }
     __syncthreads();
     int b = sh.seq;
-    long long seq_first = sh.first;           // first unit of sequence b
+    Span sp = span_of(p, b);
+    long long seq_first = sh.first;          // first part or group of sequence b
+    int parts = parted ? (sp.groups + (int)per - 1) / (int)per : 0;
+    int even = parted ? (sp.groups + parts - 1) / parts : 0;    // groups of this sequence's parts
+    if (parted) parts = (sp.groups + even - 1) / even;
+    // (rounding may leave the last parts counted above without groups)
+    const int parts_counted = parted ? (sp.groups + (int)per - 1) / (int)per : 0;
+    long long range_end = 0;
+    auto moved = [&](long long x, long long first, int groups) {      // where the end x of a range goes
+        const long long item_at = first + div64(x - first, groups) * groups;
+        const int snap = snap_of(groups);
+        return x - item_at <= snap ? item_at : item_at + groups - x <= snap ? item_at + groups : x;
+    };
+    if (!parted) {
+        const long long end = u + per;
+        u = moved(u, seq_first, sp.groups);
+        // the end may lie in a later sequence
+        if (end >= total) {
+            range_end = total;
+        } else {
+            long long first = seq_first;
+            int be = b, g = sp.groups;
+            while (end >= first + (long long)g * items_per_seq) {
+                first += (long long)g * items_per_seq;
+                g = span_of(p, ++be).groups;
+            }
+            range_end = moved(end, first, g);
+        }
+    }
 
-    uint8_t* ring = smem + warp * (kStages * stage_bytes(D));
+    uint8_t* ring = smem + warp * (ST * stage_bytes(D));
     const uint32_t ring_u = smem_u32(ring);
     const int gpp = p.c.page >> 4;           // groups of a page
+    const uint8_t* k_lane = p.c.k + lane * (KW * 4);
+    const uint8_t* v_lane = p.c.v + lane * 16;
+    const uint32_t* pair_lane = (lane < 16 ? p.c.kp : p.c.vp) + (lane & 15);
+    const uint32_t pair_dst = kStep * D + (lane >> 4) * (kStep * 4) + ((lane & 7) * 4 + ((lane >> 3) & 1)) * 4;
 
-    long long u = u0;
-    Span sp = span_of(p, b);
-    while (u < u1) {
-        while (u >= seq_first + (long long)sp.groups * items_per_seq) {
-            seq_first += (long long)sp.groups * items_per_seq;
-            sp = span_of(p, ++b);
+    for (;;) {
+        int item, g_begin, g_end, c0, c1;    // the part, and the CTAs that share its item
+        if (parted) {
+            const int at = (int)(u - seq_first);
+            item = at / parts_counted;
+            const int part = at - item * parts_counted;
+            if (part >= parts) return;
+            g_begin = part * even;
+            g_end = min(sp.groups, g_begin + even);
+            c0 = (int)(seq_first + (long long)item * parts_counted);
+            c1 = c0 + parts - 1;
+        } else {
+            if (u >= range_end) return;
+            while (u >= seq_first + (long long)sp.groups * items_per_seq) {
+                seq_first += (long long)sp.groups * items_per_seq;
+                sp = span_of(p, ++b);
+            }
+            item = (int)div64(u - seq_first, sp.groups);
+            const long long first = seq_first + (long long)item * sp.groups;
+            g_begin = (int)(u - first);
+            g_end = (int)min((long long)sp.groups, range_end - first);
+            const int snap = snap_of(sp.groups);
+            c0 = (int)div64(first + snap, per);
+            c1 = (int)div64(first + sp.groups - snap - 1, per);
+            u = first + g_end;
         }
-        const int item = (int)((u - seq_first) / sp.groups);
-        const long long item_first = seq_first + (long long)item * sp.groups, item_end = item_first + sp.groups;
+        const bool whole = g_begin == 0 && g_end == sp.groups;
+        const bool begins = g_begin == 0;
+        g_begin += sp.g0;
+        g_end += sp.g0;
         const int hk = item / chunks, chunk = item - hk * chunks;
-        const long long seg_end = item_end < u1 ? item_end : u1;
-        const int g_begin = sp.g0 + (int)(u - item_first), g_end = sp.g0 + (int)(seg_end - item_first);
-        const bool whole = u == item_first && seg_end == item_end;
+
+        // ---- the warp's steps ----
+        const int steps_all = (g_end - g_begin + 1) >> 1;
+        const int steps = steps_all > warp ? (steps_all - warp + kWarps - 1) / kWarps : 0;
+        const int32_t* table = p.table + (int64_t)b * p.max_pages;
+        const int gmax = min(g_end, (sp.len + 15) >> 4);
+        // Lane x holds the cache's token index of the x-th group of the next 16 steps, and of the 16 after them.
+        auto groups_of = [&](int first_step) {
+            const int g = g_begin + 2 * ((first_step + (lane >> 1)) * kWarps + warp) + (lane & 1);
+            uint32_t at = kNoGroup;
+            if (g < gmax) {
+                const int pg = g / gpp, page = table[pg];
+                if (page >= 0 && page < p.c.pages)
+                    at = ((uint32_t)page * p.c.heads + hk) * p.c.page + (g - pg * gpp) * 16;
+                else
+                    record_error(p.err, kErrArg);
+            }
+            return at;
+        };
+        uint32_t groups_now = 0, groups_next = groups_of(0);
 
         // ---- query fragments and this lane's two columns of every tile ----
-        uint32_t qf[NT][MT][2];
-        float fr[NT][2], qs[NT][2];          // score = fr (sk acc + lk qs)
-        int hi[NT][2], lo[NT][2];            // a column's keys: [lo, hi]
+        State<D, NT> s;
+        s.es_min = kMinExponent;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = chunk * R + nt * 8 + r;
@@ -224,356 +496,164 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
 #pragma unroll
                 for (int x = 0; x < D / 8; ++x) raw[x] = 0;
             }
-            float amax = 0.0f, sum = 0.0f;
+            float sum = 0.0f;
+            uint32_t big = 0;
 #pragma unroll
             for (int x = 0; x < D / 8; ++x) {
-                amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(raw[x])), fabsf(bf16_hi(raw[x]))));
+                big = __vmaxu2(big, raw[x] & 0x7FFF7FFFu);
                 sum += bf16_lo(raw[x]) + bf16_hi(raw[x]);
             }
+            big = max(big >> 16, big & 0xFFFFu);           // the largest magnitude, as bf16 bits
 #pragma unroll
             for (int o = 1; o < 4; o <<= 1) {
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
                 sum += __shfl_xor_sync(0xffffffffu, sum, o);
             }
-            // power of two that brings amax to [2^13, 2^14); 1 for a row of zeros
-            int e = (int)(__float_as_uint(amax) >> 23);
-            int up = e == 0 ? 0 : 13 - (e - 127);
-            up = up > 100 ? 100 : up;
-            const float f = __uint_as_float((uint32_t)(127 + (up < -126 ? -126 : up)) << 23);
+            // power of two that brings it to [2^13, 2^14); 1 for a row of zeros
+            const int e = (int)(big >> 7);
+            const int up = e == 0 ? 0 : min(13 - (e - 127), 100);
+            const float f = __uint_as_float((uint32_t)(127 + up) << 23), f16 = f * 0.0625f;
 #pragma unroll
             for (int w = 0; w < KW; ++w) {
                 // elements 8w .. 8w+7 of the lane's quarter; a word's bytes 0 and 2 give 0, 4 (low) and 1, 5 (high),
                 // bytes 1 and 3 give 2, 6 and 3, 7
                 const uint32_t* q = raw + 4 * w;
-                const float f16 = f * 0.0625f;
-                qf[nt][2 * w][0] = pack_f16x2(bf16_lo(q[0]) * f, bf16_lo(q[2]) * f);
-                qf[nt][2 * w][1] = pack_f16x2(bf16_hi(q[0]) * f16, bf16_hi(q[2]) * f16);
-                qf[nt][2 * w + 1][0] = pack_f16x2(bf16_lo(q[1]) * f, bf16_lo(q[3]) * f);
-                qf[nt][2 * w + 1][1] = pack_f16x2(bf16_hi(q[1]) * f16, bf16_hi(q[3]) * f16);
+                s.qf[nt][2 * w][0] = pack_f16x2(bf16_lo(q[0]) * f, bf16_lo(q[2]) * f);
+                s.qf[nt][2 * w][1] = pack_f16x2(bf16_hi(q[0]) * f16, bf16_hi(q[2]) * f16);
+                s.qf[nt][2 * w + 1][0] = pack_f16x2(bf16_lo(q[1]) * f, bf16_lo(q[3]) * f);
+                s.qf[nt][2 * w + 1][1] = pack_f16x2(bf16_hi(q[1]) * f16, bf16_hi(q[3]) * f16);
             }
-            const float row_fr = fminf(p.scale_log2 * (16777216.0f / f), 3e38f), row_qs = sum * f * (1.0f / 16777216.0f);
+            const float over = __uint_as_float((uint32_t)(127 - up) << 23);       // 1 / f
+            const float row_fr = fminf(p.scale_log2 * over * 0x1p24f, 3e38f), row_qs = sum * f * 0x1p-24f;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int col = 2 * j + c;
-                fr[nt][c] = __shfl_sync(0xffffffffu, row_fr, col * 4);
-                qs[nt][c] = __shfl_sync(0xffffffffu, row_qs, col * 4);
-                const int crow = chunk * R + nt * 8 + col;
-                const int ci = (crow < rows ? crow : rows - 1) / p.G;
-                hi[nt][c] = sp.len - p.Lq + ci;
-                lo[nt][c] = p.window > 0 ? hi[nt][c] - p.window + 1 : 0;
+                s.fr[nt][c] = __shfl_sync(0xffffffffu, row_fr, col * 4);
+                s.qs[nt][c] = __shfl_sync(0xffffffffu, row_qs, col * 4);
+                const int ci = min(chunk * R + nt * 8 + col, rows - 1) / p.G;
+                s.hi[nt][c] = sp.len - p.Lq + ci;
+                s.lo[nt][c] = p.window > 0 ? s.hi[nt][c] - p.window + 1 : 0;
+                s.top[nt][c] = s.lim[nt][c] = kNegInf;
+                s.ref[nt][c] = s.l[nt][c] = s.ml[nt][c] = 0.0f;
+                s.es[nt][c] = kMinExponent;
             }
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s.acc[nt][t][c] = 0.0f;
         }
         // keys that all rows of the chunk see
         const int i_first = chunk * R / p.G, i_last = (min(rows, chunk * R + R) - 1) / p.G;
         const int all_hi = sp.len - p.Lq + i_first, all_lo = p.window > 0 ? sp.len - p.Lq + i_last - p.window + 1 : 0;
 
-        float acc[NT][MT][4], m[NT][2], l[NT][2], ml[NT][2];
-        int es[NT][2];                       // exponent field that stands for the columns' values so far
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[nt][t][c] = 0.0f;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                m[nt][c] = kNegInf;
-                l[nt][c] = ml[nt][c] = 0.0f;
-                es[nt][c] = kMinExponent;
-            }
-        }
-
-        // ---- the warp's steps ----
-        const int steps_all = (g_end - g_begin + 1) >> 1;
-        const int steps = steps_all > warp ? (steps_all - warp + kWarps - 1) / kWarps : 0;
-        const int32_t* table = p.table + (int64_t)b * p.max_pages;
-        // lane x holds the page of the x-th group of the next 16 steps (-1: none), and of the 16 after them
-        const int gmax = min(g_end, (sp.len + 15) >> 4);
-        auto page_of = [&](int first_step) {
-            const int g = g_begin + 2 * ((first_step + (lane >> 1)) * kWarps + warp) + (lane & 1);
-            int page = -1;
-            if (g < gmax) {
-                page = table[g / gpp];
-                if (page < 0 || page >= p.c.pages) {
-                    record_error(p.err, kErrArg);
-                    page = -1;
-                }
-            }
-            return page;
-        };
-        int pages_now = steps > 0 ? page_of(0) : -1, pages_next = -1;
         uint32_t have = 0;                   // two bits a step in flight: which of its groups were loaded
-        auto issue = [&](int n) {
-            if (n < steps) {
-                if ((n & 15) == 0) {
-                    if (n > 0) pages_now = pages_next;
-                    pages_next = n + 16 < steps ? page_of(n + 16) : -1;
+        uint32_t put = ring_u;               // stage that is loaded next
+        const uint8_t* get = ring;           // stage that is used next
+        for (int n = 1 - ST; n < steps; ++n) {
+            if (n >= 0) {
+                cp_wait<ST - 2>();
+                __syncwarp();
+            }
+            const int ahead = n + ST - 1;
+            const uint32_t bits = have >> (2 * (ST - 2)) & 3u;
+            have <<= 2;
+            if (ahead < steps) {
+                if ((ahead & 15) == 0) {
+                    groups_now = groups_next;
+                    if (ahead + 16 < steps) groups_next = groups_of(ahead + 16);
                 }
-                const uint32_t st = ring_u + (n % kStages) * stage_bytes(D);
-                uint32_t bits = 0;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int page = __shfl_sync(0xffffffffu, pages_now, 2 * (n & 15) + i);
-                    if (page >= 0) {
-                        bits |= 1u << i;
-                        const int g = g_begin + 2 * (n * kWarps + warp) + i;
-                        const int at = (g % gpp) * 16;
-                        const int64_t head = (int64_t)page * p.c.heads + hk;
-                        const int64_t base = head * kv4_head_bytes(p.c.page, D) + (int64_t)at * (D / 2);
+                    const uint32_t at = __shfl_sync(0xffffffffu, groups_now, 2 * (ahead & 15) + i);
+                    if (at != kNoGroup) {
+                        have |= 1u << i;
+                        const uint8_t* ks = k_lane + (uint64_t)at * (D / 2);
+                        const uint8_t* vs = v_lane + (uint64_t)at * (D / 2);
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            cp_async<KW * 4>(st + i * 16 * (D / 2) + h * 8 * (D / 2) + lane * (KW * 4),
-                                             p.c.k + base + h * 8 * (D / 2) + lane * (KW * 4));
+                            cp_async<KW * 4>(put + i * 16 * (D / 2) + h * 8 * (D / 2) + lane * (KW * 4),
+                                             ks + h * 8 * (D / 2));
 #pragma unroll
                         for (int c = 0; c < D / 64; ++c)
-                            cp_async<16>(st + kStep * (D / 2) + i * 16 * (D / 2) + c * 512 + lane * 16,
-                                         p.c.v + base + c * 512 + lane * 16);
-                        const uint32_t* pair = (lane < 16 ? p.c.kp : p.c.vp) + head * p.c.page + at + (lane & 15);
-                        cp_async<4>(st + kStep * D + (lane >> 4) * (kStep * 4) + i * 64 + (lane & 15) * 4, pair);
+                            cp_async<16>(put + kStep * (D / 2) + i * 16 * (D / 2) + c * 512 + lane * 16, vs + c * 512);
+                        cp_async<4>(put + pair_dst + i * 8, pair_lane + at);
                     }
                 }
-                have = (have << 2) | bits;
-            } else {
-                have <<= 2;
+                put = put == ring_u + (ST - 1) * stage_bytes(D) ? ring_u : put + stage_bytes(D);
             }
             cp_commit();
-        };
-#pragma unroll
-        for (int n = 0; n < kStages - 1; ++n) issue(n);
-
-        for (int n = 0; n < steps; ++n) {
-            cp_wait<kStages - 2>();
-            __syncwarp();
-            const uint32_t bits = (have >> (2 * (kStages - 2))) & 3u;
-            issue(n + kStages - 1);
-            const uint8_t* st = ring + (n % kStages) * stage_bytes(D);
+            if (n < 0) continue;
             const int key0 = (g_begin + 2 * (n * kWarps + warp)) << 4;
-
-            // pairs of the lane's keys r + 8h of group i
-            float sk[2][2], lk[2][2], sv[2][2], lv[2][2];
-            const uint32_t* kp = reinterpret_cast<const uint32_t*>(st + kStep * D);
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t a = kp[16 * i + 8 * h + r], v = kp[kStep + 16 * i + 8 * h + r];
-                    sk[i][h] = bf16_lo(a);
-                    lk[i][h] = bf16_hi(a);
-                    sv[i][h] = bf16_lo(v);
-                    lv[i][h] = bf16_hi(v);
-                }
-            const bool plain = bits == 3u && key0 >= all_lo && key0 + kStep - 1 <= all_hi;
-            if (!plain) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int key = key0 + 16 * i + 8 * h + r;
-                        if (!((bits >> i) & 1u) || key >= sp.len) sk[i][h] = lk[i][h] = sv[i][h] = lv[i][h] = 0.0f;
-                    }
-            }
-            // ---- scores ----
-            float s[NT][2][4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t k0[KW], k1[KW];
-                const uint8_t* kb = st + i * 16 * (D / 2) + lane * (KW * 4);
-#pragma unroll
-                for (int w = 0; w < KW; ++w) {
-                    k0[w] = reinterpret_cast<const uint32_t*>(kb)[w];
-                    k1[w] = reinterpret_cast<const uint32_t*>(kb + 8 * (D / 2))[w];
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) s[nt][i][c] = 0.0f;
-#pragma unroll
-                for (int w = 0; w < KW; ++w) {
-                    const uint32_t x0 = k0[w] >> 8, x1 = k1[w] >> 8;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16_16816(s[nt][i], k0[w] & 0x000F000Fu, k1[w] & 0x000F000Fu, k0[w] & 0x00F000F0u,
-                                      k1[w] & 0x00F000F0u, qf[nt][2 * w][0], qf[nt][2 * w][1]);
-                        mma_f16_16816(s[nt][i], x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u,
-                                      x1 & 0x00F000F0u, qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int h = c >> 1;
-                        float v = fmaf(sk[i][h], s[nt][i][c], lk[i][h] * qs[nt][c & 1]);
-                        if (!plain) {
-                            const int key = key0 + 16 * i + 8 * h + r;
-                            if (key > hi[nt][c & 1] || key < lo[nt][c & 1] || !((bits >> i) & 1u)) v = kNegInf;
-                        }
-                        s[nt][i][c] = v;
-                    }
-
-            // ---- running maximum, weights ----
-            // The exponent of a key's values: that of its step, or of its lowest value when that is over 2^10 steps
-            // (the sum of p lv is kept in the same scale); none for a pair that is not finite.
-            int ek[2][2], e = 0;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int xs = (int)(__float_as_uint(sv[i][h]) >> 23) & 255;
-                    const int xl = (int)(__float_as_uint(lv[i][h]) >> 23) & 255;
-                    ek[i][h] = xs == 255 || xl == 255 ? 0 : max(xs, xl - 10);
-                    e = max(e, ek[i][h]);
-                }
-            if (plain) e = __reduce_max_sync(0xffffffffu, e);
-            float alpha[NT][2];
-            bool moved = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float x = fmaxf(fmaxf(s[nt][0][c], s[nt][0][c + 2]), fmaxf(s[nt][1][c], s[nt][1][c + 2]));
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-                    int ec = e;
-                    if (!plain) {            // only the keys that the column sees
-                        ec = 0;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                if (s[nt][i][2 * h + c] != kNegInf) ec = max(ec, ek[i][h]);
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) ec = max(ec, __shfl_xor_sync(0xffffffffu, ec, o));
-                    }
-                    const float mn = fmaxf(m[nt][c], x);
-                    const int en = max(es[nt][c], ec);
-                    const bool up = mn > m[nt][c] || en > es[nt][c];
-                    // nothing seen before (m = -inf): the sums are zero, and so is the factor
-                    alpha[nt][c] = up ? ex2(mn > kNegInf ? fmaf(m[nt][c] - mn, fr[nt][c], (float)(es[nt][c] - en)) : 0.0f)
-                                      : 1.0f;
-                    moved = moved || up;
-                    m[nt][c] = mn;
-                    es[nt][c] = en;
-                }
-            if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        l[nt][c] *= alpha[nt][c];
-                        ml[nt][c] *= alpha[nt][c];
-#pragma unroll
-                        for (int t = 0; t < MT; ++t) {
-                            acc[nt][t][c] *= alpha[nt][c];
-                            acc[nt][t][c + 2] *= alpha[nt][c];
-                        }
-                    }
-            }
-            uint32_t pf[NT][2][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float m2[2];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) m2[c] = reference(m[nt][c], fr[nt][c], es[nt][c]);
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float w[2];
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const float sc = s[nt][i][2 * h + c];
-                            const float pr = ex2(fmaf(sc, fr[nt][c], -m2[c]));
-                            w[c] = pr * sv[i][h];
-                            float add = pr * lv[i][h];
-                            if (!plain && sc == kNegInf) w[c] = add = 0.0f;     // not 0 * infinity
-                            l[nt][c] += pr;
-                            ml[nt][c] += add;
-                        }
-                        pf[nt][i][h] = transpose_8x8(pack_f16x2(w[0], w[1]));
-                    }
-            }
-
-            // ---- values ----
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint8_t* vb = st + kStep * (D / 2) + i * 16 * (D / 2) + lane * 16;
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    const uint4 q4 = *reinterpret_cast<const uint4*>(vb + c * 512);
-                    const uint32_t q[4] = {q4.x, q4.y, q4.z, q4.w};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint32_t y = q[x] >> 8;
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma_f16_16816(acc[nt][4 * c + x], q[x] & 0x000F000Fu, q[x] & 0x00F000F0u, y & 0x000F000Fu,
-                                          y & 0x00F000F0u, pf[nt][i][0], pf[nt][i][1]);
-                    }
-                }
-            }
+            if (bits == 3u && key0 >= all_lo && key0 + kStep - 1 <= all_hi)
+                attend<D, NT, false>(s, get, key0, bits, sp.len, lane);
+            else
+                attend<D, NT, true>(s, get, key0, bits, sp.len, lane);
+            get = get == ring + (ST - 1) * stage_bytes(D) ? ring : get + stage_bytes(D);
         }
         cp_wait<0>();
 
-        // ---- the warps' sums meet: rows' maxima, then weighted accumulators ----
+        // ---- the warps' sums meet ----
         __syncthreads();                     // the ring is free
-        float* ex_m = reinterpret_cast<float*>(smem);                  // [kWarps][R]
+        float* ex_m = reinterpret_cast<float*>(smem);                  // [kWarps][R] references
         float* ex_l = ex_m + kWarps * R;
         float* ex_o = ex_l + kWarps * R;                               // [kWarps][R][out_stride]
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
+                float l = s.l[nt][c], ml = s.ml[nt][c];
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) {
-                    l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], o);
-                    ml[nt][c] += __shfl_xor_sync(0xffffffffu, ml[nt][c], o);
+                    l += __shfl_xor_sync(0xffffffffu, l, o);
+                    ml += __shfl_xor_sync(0xffffffffu, ml, o);
                 }
                 const int row = nt * 8 + 2 * j + c;
                 if (r == 0) {
-                    ex_m[warp * R + row] = m[nt][c] > kNegInf ? reference(m[nt][c], fr[nt][c], es[nt][c]) : kNegInf;
-                    ex_l[warp * R + row] = l[nt][c];
+                    ex_m[warp * R + row] = s.top[nt][c] > kNegInf ? s.ref[nt][c] : kNegInf;
+                    ex_l[warp * R + row] = l;
                 }
                 float* o = ex_o + (warp * R + row) * out_stride(D);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
-                    o[16 * t + r] = fmaf(acc[nt][t][c], 0x1p24f, ml[nt][c]);
-                    o[16 * t + 8 + r] = fmaf(acc[nt][t][c + 2], 0x1p20f, ml[nt][c]);
+                    o[16 * t + r] = fmaf(s.acc[nt][t][c], 0x1p24f, ml);
+                    o[16 * t + 8 + r] = fmaf(s.acc[nt][t][c + 2], 0x1p20f, ml);
                 }
             }
         __syncthreads();
 
         const int live = min(R, rows - chunk * R);
-        // a thread takes two elements of every (kThreads / (D / 2))-th row
-        const int ed = (tid % (D / 2)) * 2;
-        const int cta = blockIdx.x;
-        const size_t slot_floats = (size_t)R * (D + 2);
-        for (int row = tid / (D / 2); row < live; row += kThreads / (D / 2)) {
-            float top = kNegInf, sum = 0.0f, x0 = 0.0f, x1 = 0.0f;
+        // a thread takes four elements of every (kThreads / (D / 4))-th row
+        const int ed = (tid % (D / 4)) * 4, row0 = tid / (D / 4);
+        constexpr int ROWS = kThreads / (D / 4);
+        constexpr size_t kSlot = (size_t)R * (D + 2);      // floats of a partial: [R][D], references, sums
+        auto finish = [&](int row, float4 x, float sum, float top) {
+            const int grow = chunk * R + row, i = grow / p.G;
+            const int64_t out = ((int64_t)b * p.Lq + i) * (p.c.heads * p.G) + hk * p.G + (grow - i * p.G);
+            const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+            *reinterpret_cast<uint2*>(p.o + out * D + ed) =
+                make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+            if (p.lse && ed == 0) p.lse[out] = log_sum_exp(top, sum);
+        };
+        // slot 1: the item begins in this CTA; slot 0: it began in an earlier one
+        float* part = p.part + ((size_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kSlot;
+#pragma unroll 1
+        for (int row = row0; row < live; row += ROWS) {
+            float top = kNegInf, sum = 0.0f;
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ex_m[w * R + row]);
             const float base = top > kNegInf ? top : 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float k = ex2(ex_m[w * R + row] - base);
-                const float2 v = *reinterpret_cast<const float2*>(ex_o + (w * R + row) * out_stride(D) + ed);
+                const float4 v = *reinterpret_cast<const float4*>(ex_o + (w * R + row) * out_stride(D) + ed);
                 sum = fmaf(k, ex_l[w * R + row], sum);
-                x0 = fmaf(k, v.x, x0);
-                x1 = fmaf(k, v.y, x1);
+                x = make_float4(fmaf(k, v.x, x.x), fmaf(k, v.y, x.y), fmaf(k, v.z, x.z), fmaf(k, v.w, x.w));
             }
             if (whole) {
-                const int grow = chunk * R + row, i = grow / p.G;
-                const int64_t out = ((int64_t)b * p.Lq + i) * (p.c.heads * p.G) + hk * p.G + (grow - i * p.G);
-                const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-                *reinterpret_cast<uint32_t*>(p.o + out * D + ed) = pack_bf16x2(x0 * inv, x1 * inv);
-                if (p.lse && ed == 0) p.lse[out] = log_sum_exp(top, sum);
+                finish(row, x, sum, top);
             } else {
-                // slot 1: the item begins in this CTA; slot 0: it began in an earlier one
-                float* part = p.part + ((size_t)cta * 2 + (u == item_first ? 1 : 0)) * slot_floats;
-                *reinterpret_cast<float2*>(part + row * D + ed) = make_float2(x0, x1);
+                *reinterpret_cast<float4*>(part + row * D + ed) = x;
                 if (ed == 0) {
                     part[R * D + row] = top;
                     part[R * D + R + row] = sum;
@@ -581,7 +661,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
             }
         }
         if (!whole) {
-            const int c0 = (int)(item_first / per), c1 = (int)((item_end - 1) / per);
             __threadfence();
             __syncthreads();
             if (tid == 0) {
@@ -591,30 +670,70 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
             }
             __syncthreads();
             if (sh.last) {
+                // The partials' weights first, in shared memory, then the weighted sum: the warps that hold a row's
+                // elements take every ROWS-th partial each (several rows of loads in flight) and meet at the end.
                 __threadfence();
-                for (int row = tid / (D / 2); row < live; row += kThreads / (D / 2)) {
-                    float top = kNegInf, sum = 0.0f, x0 = 0.0f, x1 = 0.0f;
-                    for (int c = c0; c <= c1; ++c)
-                        top = fmaxf(top, __ldcg(p.part + ((size_t)c * 2 + (c == c0)) * slot_floats + R * D + row));
-                    const float base = top > kNegInf ? top : 0.0f;
-                    for (int c = c0; c <= c1; ++c) {
-                        const float* part = p.part + ((size_t)c * 2 + (c == c0)) * slot_floats;
-                        const float k = ex2(__ldcg(part + R * D + row) - base);
-                        const float2 v = __ldcg(reinterpret_cast<const float2*>(part + row * D + ed));
-                        sum = fmaf(k, __ldcg(part + R * D + R + row), sum);
-                        x0 = fmaf(k, v.x, x0);
-                        x1 = fmaf(k, v.y, x1);
+                const int n = c1 - c0 + 1;
+                float* wt = reinterpret_cast<float*>(smem);            // [n][R] weights, then [R] sums and references
+                auto slot = [&](int c) { return p.part + ((size_t)(c0 + c) * 2 + (c == 0 ? 1 : 0)) * kSlot; };
+                float* total_l = wt + (size_t)n * R;
+                float* total_m = total_l + R;
+                for (int row = warp; row < R; row += kWarps) {
+                    float top = kNegInf, sum = 0.0f;
+                    for (int c = lane; c < n; c += 32) {
+                        const float m = row < live ? __ldcg(slot(c) + R * D + row) : kNegInf;
+                        wt[c * R + row] = m;
+                        top = fmaxf(top, m);
                     }
-                    const int grow = chunk * R + row, i = grow / p.G;
-                    const int64_t out = ((int64_t)b * p.Lq + i) * (p.c.heads * p.G) + hk * p.G + (grow - i * p.G);
-                    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-                    *reinterpret_cast<uint32_t*>(p.o + out * D + ed) = pack_bf16x2(x0 * inv, x1 * inv);
-                    if (p.lse && ed == 0) p.lse[out] = log_sum_exp(top, sum);
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    const float base = top > kNegInf ? top : 0.0f;
+                    for (int c = lane; c < n; c += 32) {
+                        const float k = ex2(wt[c * R + row] - base);
+                        wt[c * R + row] = k;
+                        if (row < live) sum = fmaf(k, __ldcg(slot(c) + R * D + R + row), sum);
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (lane == 0) {
+                        total_l[row] = sum;
+                        total_m[row] = top;
+                    }
+                }
+                __syncthreads();
+                float4 x[R];
+#pragma unroll
+                for (int row = 0; row < R; ++row) x[row] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+                for (int c = row0; c < n; c += ROWS) {
+                    const float* src = slot(c) + ed;
+#pragma unroll
+                    for (int row = 0; row < R; ++row)
+                        if (row < live) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + row * D));
+                            const float k = wt[c * R + row];
+                            x[row] = make_float4(fmaf(k, v.x, x[row].x), fmaf(k, v.y, x[row].y), fmaf(k, v.z, x[row].z),
+                                                 fmaf(k, v.w, x[row].w));
+                        }
+                }
+                float* meet = total_m + R;                             // [ROWS][R][D]
+#pragma unroll
+                for (int row = 0; row < R; ++row)
+                    *reinterpret_cast<float4*>(meet + ((size_t)row0 * R + row) * D + ed) = x[row];
+                __syncthreads();
+                for (int row = row0; row < live; row += ROWS) {
+                    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int k = 0; k < ROWS; ++k) {
+                        const float4 v = *reinterpret_cast<const float4*>(meet + ((size_t)k * R + row) * D + ed);
+                        y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+                    }
+                    finish(row, y, total_l[row], total_m[row]);
                 }
             }
         }
+        if (parted) return;
         __syncthreads();                     // the exchange is free for the next item's ring
-        u = seg_end;
     }
 }
 
