@@ -75,9 +75,11 @@ RopeParams rope_params(const float* wq, const float* wk, const float* cos, const
     return p;
 }
 
-int check_cache(const void* k, const void* kp, const void* v, const void* vp, int64_t pages, int64_t page) {
+int check_cache(const void* k, const void* kp, const void* v, const void* vp, int64_t pages, int64_t heads,
+                int64_t page) {
     if (!k || !kp || !v || !vp) return R9Q_ERR_NULL;
     if (pages < 1 || pages > INT_MAX || page < 16 || page % 16 || page > 65536) return R9Q_ERR_DIM;
+    if (pages * page > ((int64_t)1 << 32) / heads) return R9Q_ERR_DIM;      // (the kernels count vectors in 32 bits)
     return aligned(k, 16) && aligned(v, 16) && aligned(kp, 4) && aligned(vp, 4) ? R9Q_OK : R9Q_ERR_ALIGN;
 }
 Kv4Cache cache_of(const void* k, const void* kp, const void* v, const void* vp, int64_t pages, int64_t heads,
@@ -247,7 +249,7 @@ int r9q_qk_norm_rope_kv4(const void* q, int64_t q_ts, int64_t q_hs, const void* 
     if (!rc) rc = check_heads(k, T, k_ts, Hk, k_hs);
     if (!rc) rc = check_heads(v, T, v_ts, Hk, v_hs);
     if (!rc) rc = check_heads(q_out, T, qo_ts, Hq, qo_hs);
-    if (!rc) rc = check_cache(kc, kp, vc, vp, pages, page);
+    if (!rc) rc = check_cache(kc, kp, vc, vp, pages, Hk, page);
     if (!rc && !slots) rc = R9Q_ERR_NULL;
     if (!rc && !aligned(slots, 8)) rc = R9Q_ERR_ALIGN;
     if (rc) return rc;
@@ -275,7 +277,7 @@ int r9q_kv4_append(const void* k, int64_t k_ts, int64_t k_hs, const void* v, int
     if (T == 0) return R9Q_OK;
     int rc = check_heads(k, T, k_ts, Hk, k_hs);
     if (!rc) rc = check_heads(v, T, v_ts, Hk, v_hs);
-    if (!rc) rc = check_cache(kc, kp, vc, vp, pages, page);
+    if (!rc) rc = check_cache(kc, kp, vc, vp, pages, Hk, page);
     if (!rc && !slots) rc = R9Q_ERR_NULL;
     if (!rc && !aligned(slots, 8)) rc = R9Q_ERR_ALIGN;
     if (rc) return rc;
@@ -294,7 +296,7 @@ int r9q_kv4_gather(const uint8_t* kc, const void* kp, const uint8_t* vc, const v
                    int64_t T, int64_t Hk, int64_t D, int64_t pages, int64_t page, void* k, void* v, void* stream) {
     if (!dims_ok(T, Hk, D)) return R9Q_ERR_DIM;
     if (T == 0) return R9Q_OK;
-    int rc = check_cache(kc, kp, vc, vp, pages, page);
+    int rc = check_cache(kc, kp, vc, vp, pages, Hk, page);
     if (!rc && (!slots || !k || !v)) rc = R9Q_ERR_NULL;
     if (!rc && (!aligned(slots, 8) || !aligned(k, 16) || !aligned(v, 16))) rc = R9Q_ERR_ALIGN;
     if (rc) return rc;
@@ -320,7 +322,7 @@ int r9q_kv4_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, c
     int rc = check_heads(q, Lq, q_ts, Hq, q_hs);
     if (!rc && !stride_ok(B, q_bs)) rc = R9Q_ERR_ARG;
     if (!rc && !stride_aligned(B, q_bs)) rc = R9Q_ERR_ALIGN;
-    if (!rc) rc = check_cache(kc, kp, vc, vp, pages, page);
+    if (!rc) rc = check_cache(kc, kp, vc, vp, pages, Hk, page);
     if (rc) return rc;
     if (!seq_lens || !o || (max_pages > 0 && !block_table)) return R9Q_ERR_NULL;
     if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4)) return R9Q_ERR_ALIGN;
@@ -364,6 +366,8 @@ int r9q_kv4_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, c
     p.max_pages = (int)max_pages;
     // a window longer than any sequence is none
     p.window = window > max_pages * page ? 0 : (int)window;
+    p.room = (int)(max_pages * page);
+    p.reach = p.window > 0 ? (int)(p.window > INT_MAX - Lq ? INT_MAX : p.window + Lq - 1) : INT_MAX;
     p.scale_log2 = scale * 1.4426950408889634f;
     return status(launch_kv4_attention((int)D, p, sms, static_cast<cudaStream_t>(stream)));
 }

@@ -184,6 +184,11 @@ cudaError_t launch_qk_norm_rope_bwd(int D, const HeadsIn& dqo, const HeadsIn& dk
                                     const RopeParams& p, const HeadsOut& dq, const HeadsOut& dk, float* dwq,
                                     float* dwk, float* part, int* done, int sms, cudaStream_t st);
 
+// Division by a value known at the launch (0 <= n < 2^31).
+struct FastDiv {
+    uint32_t m;
+    int l, d;
+};
 struct Kv4AttnParams {
     const uint16_t* q;           // [B][Lq][Hq][D], last dimension contiguous
     int64_t q_bs, q_ts, q_hs;
@@ -196,7 +201,9 @@ struct Kv4AttnParams {
     int* done;                   // one counter per CTA, zero between calls
     int* err;
     int B, Lq, G, max_pages, window;
+    int room, reach;             // tokens that max_pages hold; the most tokens that the new ones of a sequence see
     float scale_log2;            // softmax scale * log2(e)
+    FastDiv chunks, group, page_groups;      // row chunks, G, groups of 16 tokens of a page (set by the launcher)
 };
 // CTAs of the launch, and floats of `part` for them.
 int kv4_attention_ctas(int D, int64_t rows, int sms);

@@ -17,11 +17,11 @@
 // The queries are scaled by a power of two per row to a largest element in
 // [2^13, 2^14), where fp16 holds bf16 values exactly down to 2^-27 of it.  The
 // weights P sv are rounded to fp16 (11 bits; bf16 would keep 8).  To keep them in
-// its range a row's weights are taken not against its largest score alone but
-// against m2 = largest score - 8 + E, E the exponent of the largest step its keys have had.
-// m2 moves only when a score passes it by 2^6 (or a step is larger than any before):
-// weights stay under 2^15, 2^-22 of the largest still has full precision, and most steps
-// neither reduce a maximum over the warp nor touch the accumulators.
+// its range a row's weights are taken not against its largest score alone but against
+// largest score - 8 + E, E the exponent of the largest step its keys have had.  This
+// reference moves only when a weight passes it by 2^6 (or a step is larger than any
+// before): weights stay under 2^15, 2^-22 of the largest still has full precision, and
+// most steps neither reduce a maximum over the warp nor touch the accumulators.
 // Both sums use the same weights, so the power of two cancels.  Scores, maxima,
 // sums and accumulators are fp32.
 //
@@ -29,8 +29,9 @@
 // batches and single long sequences fill the GPU alike.  All CTAs are resident.  With
 // few items (sequence, kv head, row chunk) each is cut into equal parts, one a CTA;
 // with many, each CTA takes an equal, contiguous range of all items' groups, its ends
-// moved to an item's end where that is near.  The four warps of a CTA take 32-key steps of a part in
-// turn, each with its own running reference, and meet in shared memory at its end.
+// moved to an item's end where that is near.  The four warps of a CTA take 32-key
+// steps of a part in turn, each with its own reference, and meet in shared memory at
+// its end.
 // An item that several CTAs share leaves fp32 partials; the CTA that arrives last
 // joins them in CTA order.
 //
@@ -49,7 +50,10 @@ constexpr int kStep = 32;                    // keys a warp takes at a time: two
 constexpr int kMinGroups = 2 * kWarps;       // groups a CTA takes at least: one step for each warp
 constexpr int kMinExponent = 67;             // value steps under 2^-60 count as that (keeps the sums finite)
 constexpr int kHeadroom = 8;                 // weights at the reference score are 2^8 to 2^9
-constexpr float kSlack = 6.0f;               // powers of two a score may pass the reference by
+constexpr int kSlack = 6;                    // powers of two a lane's weights may pass it by
+// A lowest value counts as a step of 2^-10 of it: the sums of p lv are kept in the weights' scale.
+constexpr int kLowestBits = 10;
+constexpr float kLowestShare = 1.0f / (1 << kLowestBits);
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr uint32_t kNoGroup = 0xFFFFFFFFu;
 
@@ -59,8 +63,17 @@ constexpr int stage_bytes(int D) { return kStep * D + kStep * 8; }
 constexpr int ring_bytes(int D) { return kWarps * stages(D) * stage_bytes(D); }
 constexpr int out_stride(int D) { return D + 4; }      // floats a row of the CTA's exchange takes
 constexpr int exchange_bytes(int D, int NT) { return kWarps * 8 * NT * (out_stride(D) + 2) * 4; }
-constexpr int work_bytes(int D, int NT) {              // the rings, and after them the exchange in their place
-    return ring_bytes(D) > exchange_bytes(D, NT) ? ring_bytes(D) : exchange_bytes(D, NT);
+constexpr int kMaxSms = 160;                           // more are left idle
+// Joining n partials of R rows: [n][R] weights, [R] sums and references, then [n][R] sums, whose place the warps'
+// joined rows take (kThreads float4).
+constexpr int join_bytes(int D, int NT) {
+    const int n = kMaxSms * ctas_per_sm(D, NT) * 8 * NT * 4, meet = kThreads * 8 * NT * 16;
+    return n + 2 * 8 * NT * 4 + (n > meet ? n : meet);
+}
+constexpr int work_bytes(int D, int NT) {              // the rings, and after them the others in their place
+    int n = ring_bytes(D);
+    n = n > exchange_bytes(D, NT) ? n : exchange_bytes(D, NT);
+    return n > join_bytes(D, NT) ? n : join_bytes(D, NT);
 }
 // What the threads of a CTA tell one another about its range.
 struct Shared {
@@ -88,6 +101,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 // Transposes an 8x8 matrix of 16-bit values held two to a lane.
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
     uint32_t r;
@@ -103,24 +121,27 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The quotient of 0 <= n < 2^31 by a divisor prepared on the host.
+__device__ __forceinline__ int operator/(int n, const FastDiv& d) {
+    return (int)(__umulhi((uint32_t)n * 2u, d.m) >> d.l);
+}
 __device__ __noinline__ long long div64(long long a, long long b) { return a / b; }
 
-// A sequence's keys and the groups an item of it has.
+// A sequence's keys and the groups an item of it has.  `room`: tokens that its pages
+// can hold; `reach`: the most tokens that its new ones see.
 struct Span {
     int len, g0;             // tokens; first group that holds a visible key
     int groups;              // at least one (an empty sequence's items write zeros)
 };
-__device__ __forceinline__ Span span_of(const Kv4AttnParams& p, int b) {
+__device__ __noinline__ Span span_of(const int32_t* at, int room, int reach, int* err) {
     Span s;
-    const int64_t room = (int64_t)p.max_pages * p.c.page;
-    int len = p.lens[b];
+    int len = *at;
     if (len < 0 || len > room) {
-        if (threadIdx.x == 0) record_error(p.err, kErrArg);
-        len = len < 0 ? 0 : (int)room;
+        if (threadIdx.x == 0) record_error(err, kErrArg);
+        len = len < 0 ? 0 : room;
     }
     s.len = len;
-    const int64_t lo = p.window > 0 ? (int64_t)len - p.Lq - p.window + 1 : 0;
-    s.g0 = lo > 0 ? (int)(lo >> 4) : 0;
+    s.g0 = len > reach ? (len - reach) >> 4 : 0;
     const int n = ((len + 15) >> 4) - s.g0;
     s.groups = n > 0 ? n : 1;
     return s;
@@ -145,7 +166,8 @@ __device__ __forceinline__ long long cta_scan(long long v, long long (&sums)[kWa
     return v;
 }
 
-// The log of the sum of exponentials, from the sum of weights l and their reference m.
+// The log of the sum of exponentials, from the sum of weights l and their reference m
+// (both of powers of two).
 __device__ __forceinline__ float log_sum_exp(float m, float l) {
     return l > 0.0f || l != l ? (m + log2f(l)) * kLn2 : __int_as_float(0xFF800000);
 }
@@ -160,15 +182,74 @@ struct State {
     float fr[NT][2], qs[NT][2];              // score = fr (sk acc + lk qs)
     int hi[NT][2], lo[NT][2];                // keys that the column sees: [lo, hi]
     float acc[NT][D / 16][4], l[NT][2], ml[NT][2];
-    float top[NT][2], lim[NT][2], ref[NT][2];    // largest score / fr at the last move, when to move, reference m2
-    int es[NT][2], es_min;                   // exponent field that stands for the columns' values
+    // A weight is 2^((score - top) + shift) with the largest score and the values' exponent of the last move; taken
+    // as a difference first, so that it holds for scores of any size.
+    float top[NT][2], shift[NT][2];          // (top over fr; both 0 while the column has seen no key)
+    int es[NT][2];                           // exponent field that stands for the column's values so far
+    float bound[NT][2], sv_bound;            // when to move: a lane's weights of a step, a step (or share of a lowest)
+    uint32_t seen;                           // columns that have seen a key
 };
+
+// Takes the columns' references to the largest score and the largest values they have
+// seen, this step's included, and what was summed against the old ones with them.
+template <int D, int NT, bool MASKED>
+__device__ __forceinline__ void move_reference(State<D, NT>& s, const float (&sc)[NT][2][4],
+                                               const uint32_t (&vq)[2][2]) {
+    int ek[2][2];                            // the exponent of a key's values; none for a pair that is not finite
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int xs = (int)(vq[i][h] >> 7) & 255, xl = (int)(vq[i][h] >> 23) & 255;
+            ek[i][h] = xs == 255 || xl == 255 ? 0 : max(xs, xl - kLowestBits);
+        }
+    int es_min = 255;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const uint32_t bit = 1u << (2 * nt + c);
+            float x = max3(max3(sc[nt][0][c], sc[nt][0][c + 2], sc[nt][1][c]), sc[nt][1][c + 2],
+                           s.seen & bit ? s.top[nt][c] : kNegInf);
+            int e = s.es[nt][c];             // only of keys that the column sees
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (!MASKED || sc[nt][i][2 * h + c] != kNegInf) e = max(e, ek[i][h]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
+            }
+            float alpha = 0.0f;              // nothing seen before: the sums are zero
+            s.bound[nt][c] = 0.0f;           // (nothing seen now either: no weight is over 0)
+            if (x > kNegInf) {
+                const float shift = (float)(kHeadroom + 127 - e);
+                if (s.seen & bit) alpha = ex2(fmaf(s.top[nt][c] - x, s.fr[nt][c], shift - s.shift[nt][c]));
+                s.seen |= bit;
+                s.top[nt][c] = x;
+                s.shift[nt][c] = shift;
+                s.bound[nt][c] = ex2(shift + kSlack);
+            }
+            s.es[nt][c] = e;
+            es_min = min(es_min, e);
+            s.l[nt][c] *= alpha;
+            s.ml[nt][c] *= alpha;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) {
+                s.acc[nt][t][c] *= alpha;
+                s.acc[nt][t][c + 2] *= alpha;
+            }
+        }
+    s.sv_bound = __uint_as_float((uint32_t)(es_min + 1) << 23);          // the next power of two
+}
 
 // One step: 32 keys in the stage `st`, of which groups `bits` were loaded.
 // MASKED: some column does not see some key, or a group is missing.
 template <int D, int NT, bool MASKED>
 __device__ __forceinline__ void attend(State<D, NT>& s, const uint8_t* st, int key0, uint32_t bits, int len, int lane) {
-    constexpr int KW = D / 32, MT = D / 16;
+    constexpr int KW = D / 32;
     const int r = lane >> 2;
     // pairs of the lane's keys r + 8h of group i
     const uint4 kp = *reinterpret_cast<const uint4*>(st + kStep * D + r * 16);
@@ -224,73 +305,37 @@ __device__ __forceinline__ void attend(State<D, NT>& s, const uint8_t* st, int k
                 sc[nt][i][c] = v;
             }
 
-    // ---- does the reference hold? ----
-    // The exponent of a key's values: that of its step, or of its lowest value when that is over 2^10 steps
-    // (the sum of p lv is kept in the same scale).
-    uint32_t any = 0;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) any = __vmaxu2(any, vq[i][h] & 0x7FFF7FFFu);
-    int e = max((int)((any & 0xFFFFu) >> 7), (int)(any >> 23) - 10);
-    float x[NT][2];
-    bool move = MASKED || e > s.es_min;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            x[nt][c] = fmaxf(fmaxf(sc[nt][0][c], sc[nt][0][c + 2]), fmaxf(sc[nt][1][c], sc[nt][1][c + 2]));
-            move = move || x[nt][c] > s.lim[nt][c];
-        }
-    if (__any_sync(0xffffffffu, move)) {
-        int ek[2][2];                        // by key; none for a pair that is not finite
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int xs = (int)(vq[i][h] >> 7) & 255, xl = (int)(vq[i][h] >> 23) & 255;
-                ek[i][h] = xs == 255 || xl == 255 ? 0 : max(xs, xl - 10);
-            }
-        s.es_min = 255;
+    // ---- weights, once the reference holds ----
+    // It does while no step is larger than any before, and no weight passes its bound; weights are not negative, so
+    // a lane checks the sum of its four of a column, which it needs in any case.
+    const float sv_max = max3(max3(bf16_lo(vq[0][0]), bf16_lo(vq[0][1]), bf16_lo(vq[1][0])), bf16_lo(vq[1][1]),
+                              max3(fabsf(bf16_hi(vq[0][0])), fabsf(bf16_hi(vq[0][1])),
+                                   max3(fabsf(bf16_hi(vq[1][0])), fabsf(bf16_hi(vq[1][1])), 0.0f)) * kLowestShare);
+    bool move = MASKED || sv_max > s.sv_bound;
+    float pr[NT][2][4], sum[NT][2];
+#pragma unroll 1
+    for (int pass = 0;; ++pass) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                int ec = 0;                  // only of keys that the column sees
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        if (!MASKED || sc[nt][i][2 * h + c] != kNegInf) ec = max(ec, ek[i][h]);
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) {
-                    x[nt][c] = fmaxf(x[nt][c], __shfl_xor_sync(0xffffffffu, x[nt][c], o));
-                    ec = max(ec, __shfl_xor_sync(0xffffffffu, ec, o));
-                }
-                const float before = s.top[nt][c], now = fmaxf(before, x[nt][c]), old = s.ref[nt][c];
-                s.es[nt][c] = max(s.es[nt][c], ec);
-                s.es_min = min(s.es_min, s.es[nt][c]);
-                s.top[nt][c] = now;
-                s.lim[nt][c] = now + kSlack / s.fr[nt][c];
-                float alpha = 0.0f;          // nothing seen before: the sums are zero
-                if (now > kNegInf) {
-                    s.ref[nt][c] = fmaf(now, s.fr[nt][c], (float)(s.es[nt][c] - 127 - kHeadroom));
-                    if (before > kNegInf) alpha = ex2(old - s.ref[nt][c]);
-                }
-                s.l[nt][c] *= alpha;
-                s.ml[nt][c] *= alpha;
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    s.acc[nt][t][c] *= alpha;
-                    s.acc[nt][t][c + 2] *= alpha;
-                }
+                        pr[nt][i][2 * h + c] =
+                            ex2(fmaf(sc[nt][i][2 * h + c] - s.top[nt][c], s.fr[nt][c], s.shift[nt][c]));
+                sum[nt][c] = (pr[nt][0][c] + pr[nt][0][c + 2]) + (pr[nt][1][c] + pr[nt][1][c + 2]);
+                move = move || sum[nt][c] > s.bound[nt][c];
             }
+        if (pass > 0 || !__any_sync(0xffffffffu, move)) break;
+        move_reference<D, NT, MASKED>(s, sc, vq);
     }
-
-    // ---- weights ----
     uint32_t pf[NT][2][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) s.l[nt][c] += sum[nt][c];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -298,16 +343,14 @@ __device__ __forceinline__ void attend(State<D, NT>& s, const uint8_t* st, int k
                 float w[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float v = sc[nt][i][2 * h + c];
-                    const float pr = ex2(fmaf(v, s.fr[nt][c], -s.ref[nt][c]));
                     float sv = bf16_lo(vq[i][h]), lv = bf16_hi(vq[i][h]);
-                    if (MASKED && v == kNegInf) sv = lv = 0.0f;         // not 0 * infinity
-                    w[c] = pr * sv;
-                    s.l[nt][c] += pr;
-                    s.ml[nt][c] = fmaf(pr, lv, s.ml[nt][c]);
+                    if (MASKED && sc[nt][i][2 * h + c] == kNegInf) sv = lv = 0.0f;      // not 0 * infinity
+                    w[c] = pr[nt][i][2 * h + c] * sv;
+                    s.ml[nt][c] = fmaf(pr[nt][i][2 * h + c], lv, s.ml[nt][c]);
                 }
                 pf[nt][i][h] = transpose_8x8(pack_f16x2(w[0], w[1]));
             }
+    }
 
     // ---- values ----
 #pragma unroll
@@ -340,15 +383,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = lane >> 2, j = lane & 3;
-    const int rows = p.Lq * p.G, chunks = (rows + R - 1) / R;
+    const int rows = p.Lq * p.G, chunks = p.chunks.d;
     const int items_per_seq = p.c.heads * chunks;
     const long long items = (long long)p.B * items_per_seq, ctas = gridDim.x;
 
     // ---- what this CTA does ----
+    auto span = [&](int b) { return span_of(p.lens + b, p.room, p.reach, p.err); };
     const int per_thread = (p.B + kThreads - 1) / kThreads;
     const int b_first = tid * per_thread, b_end = min(p.B, b_first + per_thread);
     long long mine = 0, total;
-    for (int b = b_first; b < b_end; ++b) mine += span_of(p, b).groups;
+#pragma unroll 1
+    for (int b = b_first; b < b_end; ++b) mine += span(b).groups;
     mine *= items_per_seq;
     long long upto = cta_scan(mine, sh.scan[0], total);
     const bool parted = 2 * items <= ctas;   // one part of one item a CTA
@@ -358,7 +403,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
         per = (total + ctas - items - 1) / (ctas - items);
         if (per < kMinGroups) per = kMinGroups;
         mine = 0;                            // from here on: parts
-        for (int b = b_first; b < b_end; ++b) mine += (span_of(p, b).groups + (int)per - 1) / (int)per;
+#pragma unroll 1
+        for (int b = b_first; b < b_end; ++b) mine += (span(b).groups + (int)per - 1) / (int)per;
         mine *= items_per_seq;
         upto = cta_scan(mine, sh.scan[1], total);
     } else {
@@ -372,8 +418,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
     if (u >= upto - mine && u < upto) {
         long long at = upto - mine;
         int b = b_first;
+#pragma unroll 1
         for (;; ++b) {
-            const int g = span_of(p, b).groups;
+            const int g = span(b).groups;
             const long long n = (long long)(parted ? (g + (int)per - 1) / (int)per : g) * items_per_seq;
             if (u < at + n) break;
             at += n;
@@ -383,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
     }
     __syncthreads();
     int b = sh.seq;
-    Span sp = span_of(p, b);
+    Span sp = span(b);
     long long seq_first = sh.first;          // first part or group of sequence b
     int parts = parted ? (sp.groups + (int)per - 1) / (int)per : 0;
     int even = parted ? (sp.groups + parts - 1) / parts : 0;    // groups of this sequence's parts
@@ -405,9 +452,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
         } else {
             long long first = seq_first;
             int be = b, g = sp.groups;
+#pragma unroll 1
             while (end >= first + (long long)g * items_per_seq) {
                 first += (long long)g * items_per_seq;
-                g = span_of(p, ++be).groups;
+                g = span(++be).groups;
             }
             range_end = moved(end, first, g);
         }
@@ -415,7 +463,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
 
     uint8_t* ring = smem + warp * (ST * stage_bytes(D));
     const uint32_t ring_u = smem_u32(ring);
-    const int gpp = p.c.page >> 4;           // groups of a page
     const uint8_t* k_lane = p.c.k + lane * (KW * 4);
     const uint8_t* v_lane = p.c.v + lane * 16;
     const uint32_t* pair_lane = (lane < 16 ? p.c.kp : p.c.vp) + (lane & 15);
@@ -434,9 +481,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
             c1 = c0 + parts - 1;
         } else {
             if (u >= range_end) return;
+#pragma unroll 1
             while (u >= seq_first + (long long)sp.groups * items_per_seq) {
                 seq_first += (long long)sp.groups * items_per_seq;
-                sp = span_of(p, ++b);
+                sp = span(++b);
             }
             item = (int)div64(u - seq_first, sp.groups);
             const long long first = seq_first + (long long)item * sp.groups;
@@ -451,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
         const bool begins = g_begin == 0;
         g_begin += sp.g0;
         g_end += sp.g0;
-        const int hk = item / chunks, chunk = item - hk * chunks;
+        const int hk = item / p.chunks, chunk = item - hk * chunks;
 
         // ---- the warp's steps ----
         const int steps_all = (g_end - g_begin + 1) >> 1;
@@ -463,9 +511,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
             const int g = g_begin + 2 * ((first_step + (lane >> 1)) * kWarps + warp) + (lane & 1);
             uint32_t at = kNoGroup;
             if (g < gmax) {
-                const int pg = g / gpp, page = table[pg];
+                const int pg = g / p.page_groups, page = table[pg];
                 if (page >= 0 && page < p.c.pages)
-                    at = ((uint32_t)page * p.c.heads + hk) * p.c.page + (g - pg * gpp) * 16;
+                    at = ((uint32_t)page * p.c.heads + hk) * p.c.page + (g - pg * p.page_groups.d) * 16;
                 else
                     record_error(p.err, kErrArg);
             }
@@ -475,13 +523,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
 
         // ---- query fragments and this lane's two columns of every tile ----
         State<D, NT> s;
-        s.es_min = kMinExponent;
+        s.sv_bound = -1.0f;                  // the first step moves the references
+        s.seen = 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = chunk * R + nt * 8 + r;
             uint32_t raw[D / 8];
             if (row < rows) {
-                const int i = row / p.G, head = hk * p.G + (row - i * p.G);
+                const int i = row / p.group, head = hk * p.G + (row - i * p.G);
                 const uint4* src = reinterpret_cast<const uint4*>(p.q + b * p.q_bs + i * p.q_ts + head * p.q_hs +
                                                                   j * (D / 4));
 #pragma unroll
@@ -530,11 +579,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
                 const int col = 2 * j + c;
                 s.fr[nt][c] = __shfl_sync(0xffffffffu, row_fr, col * 4);
                 s.qs[nt][c] = __shfl_sync(0xffffffffu, row_qs, col * 4);
-                const int ci = min(chunk * R + nt * 8 + col, rows - 1) / p.G;
+                const int ci = min(chunk * R + nt * 8 + col, rows - 1) / p.group;
                 s.hi[nt][c] = sp.len - p.Lq + ci;
                 s.lo[nt][c] = p.window > 0 ? s.hi[nt][c] - p.window + 1 : 0;
-                s.top[nt][c] = s.lim[nt][c] = kNegInf;
-                s.ref[nt][c] = s.l[nt][c] = s.ml[nt][c] = 0.0f;
+                s.top[nt][c] = s.shift[nt][c] = s.bound[nt][c] = s.l[nt][c] = s.ml[nt][c] = 0.0f;
                 s.es[nt][c] = kMinExponent;
             }
 #pragma unroll
@@ -543,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
                 for (int c = 0; c < 4; ++c) s.acc[nt][t][c] = 0.0f;
         }
         // keys that all rows of the chunk see
-        const int i_first = chunk * R / p.G, i_last = (min(rows, chunk * R + R) - 1) / p.G;
+        const int i_first = chunk * R / p.group, i_last = (min(rows, chunk * R + R) - 1) / p.group;
         const int all_hi = sp.len - p.Lq + i_first, all_lo = p.window > 0 ? sp.len - p.Lq + i_last - p.window + 1 : 0;
 
         uint32_t have = 0;                   // two bits a step in flight: which of its groups were loaded
@@ -609,7 +657,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
                 }
                 const int row = nt * 8 + 2 * j + c;
                 if (r == 0) {
-                    ex_m[warp * R + row] = s.top[nt][c] > kNegInf ? s.ref[nt][c] : kNegInf;
+                    ex_m[warp * R + row] =
+                        s.seen >> (2 * nt + c) & 1u ? fmaf(s.top[nt][c], s.fr[nt][c], -s.shift[nt][c]) : kNegInf;
                     ex_l[warp * R + row] = l;
                 }
                 float* o = ex_o + (warp * R + row) * out_stride(D);
@@ -627,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
         constexpr int ROWS = kThreads / (D / 4);
         constexpr size_t kSlot = (size_t)R * (D + 2);      // floats of a partial: [R][D], references, sums
         auto finish = [&](int row, float4 x, float sum, float top) {
-            const int grow = chunk * R + row, i = grow / p.G;
+            const int grow = chunk * R + row, i = grow / p.group;
             const int64_t out = ((int64_t)b * p.Lq + i) * (p.c.heads * p.G) + hk * p.G + (grow - i * p.G);
             const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
             *reinterpret_cast<uint2*>(p.o + out * D + ed) =
@@ -674,24 +723,25 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
                 // elements take every ROWS-th partial each (several rows of loads in flight) and meet at the end.
                 __threadfence();
                 const int n = c1 - c0 + 1;
-                float* wt = reinterpret_cast<float*>(smem);            // [n][R] weights, then [R] sums and references
+                float* wt = reinterpret_cast<float*>(smem);
                 auto slot = [&](int c) { return p.part + ((size_t)(c0 + c) * 2 + (c == 0 ? 1 : 0)) * kSlot; };
-                float* total_l = wt + (size_t)n * R;
-                float* total_m = total_l + R;
+                float *total_l = wt + n * R, *total_m = total_l + R, *sums = total_m + R, *meet = sums;
+                for (int k = tid; k < n * R; k += kThreads) {
+                    const float* from = slot(k / R) + R * D + k % R;
+                    wt[k] = k % R < live ? __ldcg(from) : kNegInf;
+                    sums[k] = k % R < live ? __ldcg(from + R) : 0.0f;
+                }
+                __syncthreads();
                 for (int row = warp; row < R; row += kWarps) {
                     float top = kNegInf, sum = 0.0f;
-                    for (int c = lane; c < n; c += 32) {
-                        const float m = row < live ? __ldcg(slot(c) + R * D + row) : kNegInf;
-                        wt[c * R + row] = m;
-                        top = fmaxf(top, m);
-                    }
+                    for (int c = lane; c < n; c += 32) top = fmaxf(top, wt[c * R + row]);
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
                     const float base = top > kNegInf ? top : 0.0f;
                     for (int c = lane; c < n; c += 32) {
                         const float k = ex2(wt[c * R + row] - base);
                         wt[c * R + row] = k;
-                        if (row < live) sum = fmaf(k, __ldcg(slot(c) + R * D + R + row), sum);
+                        sum = fmaf(k, sums[c * R + row], sum);
                     }
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -716,7 +766,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
                                                  fmaf(k, v.w, x[row].w));
                         }
                 }
-                float* meet = total_m + R;                             // [ROWS][R][D]
 #pragma unroll
                 for (int row = 0; row < R; ++row)
                     *reinterpret_cast<float4*>(meet + ((size_t)row0 * R + row) * D + ed) = x[row];
@@ -737,19 +786,30 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
     }
 }
 
+int used_sms(int sms) { return sms < kMaxSms ? sms : kMaxSms; }
 int row_tiles(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
+FastDiv fast_div(int d) {
+    int l = 0;
+    while ((1ll << l) < d) ++l;
+    return {(uint32_t)(((1ull << (31 + l)) + d - 1) / d), l, d};
+}
+
 template <int D, int NT>
-cudaError_t launch(const Kv4AttnParams& p, int sms, cudaStream_t st) {
+cudaError_t launch(Kv4AttnParams p, int sms, cudaStream_t st) {
+    const int rows = p.Lq * p.G;
+    p.chunks = fast_div((rows + 8 * NT - 1) / (8 * NT));
+    p.group = fast_div(p.G);
+    p.page_groups = fast_div(p.c.page / 16);
     cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kv4_attention_kernel<D, NT>), smem_bytes(D, NT));
     if (e != cudaSuccess) return e;
-    kv4_attention_kernel<D, NT><<<sms * ctas_per_sm(D, NT), kThreads, smem_bytes(D, NT), st>>>(p);
+    kv4_attention_kernel<D, NT><<<used_sms(sms) * ctas_per_sm(D, NT), kThreads, smem_bytes(D, NT), st>>>(p);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-int kv4_attention_ctas(int D, int64_t rows, int sms) { return sms * ctas_per_sm(D, row_tiles(rows)); }
+int kv4_attention_ctas(int D, int64_t rows, int sms) { return used_sms(sms) * ctas_per_sm(D, row_tiles(rows)); }
 
 size_t kv4_attention_part_floats(int D, int64_t rows, int sms) {
     return (size_t)kv4_attention_ctas(D, rows, sms) * 2 * (8 * row_tiles(rows)) * (D + 2);
