@@ -28,8 +28,9 @@
 // Work is cut in groups of 16 keys, on the device, from the lengths, so that ragged
 // batches and single long sequences fill the GPU alike.  All CTAs are resident.  With
 // few items (sequence, kv head, row chunk) each is cut into equal parts, one a CTA;
-// with many, each CTA takes an equal, contiguous range of all items' groups, its ends
-// moved to an item's end where that is near.  The four warps of a CTA take 32-key
+// with many, each CTA takes an equal, contiguous range of all items' groups (each item
+// counting some more for what it costs to begin), its ends moved to an item's end where
+// that is near.  The four warps of a CTA take 32-key
 // steps of a part in turn, each with its own reference, and meet in shared memory at
 // its end.
 // An item that several CTAs share leaves fp32 partials; the CTA that arrives last
@@ -48,6 +49,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 32;                    // keys a warp takes at a time: two groups of 16
 constexpr int kMinGroups = 2 * kWarps;       // groups a CTA takes at least: one step for each warp
+constexpr int kItemCost = 24;                // groups that take as long as beginning and ending an item
 constexpr int kMinExponent = 67;             // value steps under 2^-60 count as that (keeps the sums finite)
 constexpr int kHeadroom = 8;                 // weights at the reference score are 2^8 to 2^9
 constexpr int kSlack = 6;                    // powers of two a lane's weights may pass it by
@@ -388,15 +390,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
     const long long items = (long long)p.B * items_per_seq, ctas = gridDim.x;
 
     // ---- what this CTA does ----
+    const bool parted = 2 * items <= ctas;   // one part of one item a CTA
+    const int begin_cost = parted ? 0 : kItemCost;
     auto span = [&](int b) { return span_of(p.lens + b, p.room, p.reach, p.err); };
     const int per_thread = (p.B + kThreads - 1) / kThreads;
     const int b_first = tid * per_thread, b_end = min(p.B, b_first + per_thread);
     long long mine = 0, total;
 #pragma unroll 1
-    for (int b = b_first; b < b_end; ++b) mine += span(b).groups;
+    for (int b = b_first; b < b_end; ++b) mine += span(b).groups + begin_cost;
     mine *= items_per_seq;
     long long upto = cta_scan(mine, sh.scan[0], total);
-    const bool parted = 2 * items <= ctas;   // one part of one item a CTA
     long long per;                           // groups of a part, or of a CTA's range
     if (parted) {
         // sum of ceil(groups / per) over the items is at most total / per + items <= ctas
@@ -421,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
 #pragma unroll 1
         for (;; ++b) {
             const int g = span(b).groups;
-            const long long n = (long long)(parted ? (g + (int)per - 1) / (int)per : g) * items_per_seq;
+            const long long n = (long long)(parted ? (g + (int)per - 1) / (int)per : g + begin_cost) * items_per_seq;
             if (u < at + n) break;
             at += n;
         }
@@ -439,9 +442,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
     const int parts_counted = parted ? (sp.groups + (int)per - 1) / (int)per : 0;
     long long range_end = 0;
     auto moved = [&](long long x, long long first, int groups) {      // where the end x of a range goes
-        const long long item_at = first + div64(x - first, groups) * groups;
-        const int snap = snap_of(groups);
-        return x - item_at <= snap ? item_at : item_at + groups - x <= snap ? item_at + groups : x;
+        const int n = groups + begin_cost, snap = snap_of(groups);
+        const long long item_at = first + div64(x - first, n) * n;
+        return x - item_at <= begin_cost + snap ? item_at : item_at + n - x <= snap ? item_at + n : x;
     };
     if (!parted) {
         const long long end = u + per;
@@ -453,8 +456,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
             long long first = seq_first;
             int be = b, g = sp.groups;
 #pragma unroll 1
-            while (end >= first + (long long)g * items_per_seq) {
-                first += (long long)g * items_per_seq;
+            while (end >= first + (long long)(g + begin_cost) * items_per_seq) {
+                first += (long long)(g + begin_cost) * items_per_seq;
                 g = span(++be).groups;
             }
             range_end = moved(end, first, g);
@@ -482,18 +485,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
         } else {
             if (u >= range_end) return;
 #pragma unroll 1
-            while (u >= seq_first + (long long)sp.groups * items_per_seq) {
-                seq_first += (long long)sp.groups * items_per_seq;
+            while (u >= seq_first + (long long)(sp.groups + begin_cost) * items_per_seq) {
+                seq_first += (long long)(sp.groups + begin_cost) * items_per_seq;
                 sp = span(++b);
             }
-            item = (int)div64(u - seq_first, sp.groups);
-            const long long first = seq_first + (long long)item * sp.groups;
-            g_begin = (int)(u - first);
-            g_end = (int)min((long long)sp.groups, range_end - first);
-            const int snap = snap_of(sp.groups);
-            c0 = (int)div64(first + snap, per);
-            c1 = (int)div64(first + sp.groups - snap - 1, per);
-            u = first + g_end;
+            const int n = sp.groups + begin_cost, snap = snap_of(sp.groups);
+            item = (int)div64(u - seq_first, n);
+            const long long first = seq_first + (long long)item * n;
+            g_begin = max(0, (int)(u - first) - begin_cost);
+            g_end = (int)min((long long)n, range_end - first) - begin_cost;
+            c0 = (int)div64(first + begin_cost + snap, per);
+            c1 = (int)div64(first + n - snap - 1, per);
+            u = first + begin_cost + g_end;
         }
         const bool whole = g_begin == 0 && g_end == sp.groups;
         const bool begins = g_begin == 0;
