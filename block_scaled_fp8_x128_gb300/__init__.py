@@ -362,52 +362,73 @@ def r9q_kv4_cache(pages: int, heads: int, page: int, dim: int, device=None) -> K
     return KV4Cache(k, kp, torch.zeros_like(k), torch.zeros_like(kp))
 
 
-def _heads(t, name, shape):
-    """(pointer, token stride, head stride) of a bf16 [T][H][D] tensor with contiguous vectors."""
-    _expect(t, torch.bfloat16, shape, name)
-    if not t.is_cuda:
-        raise ValueError("tensor must be on a CUDA device")
+# These calls last microseconds on the GPU, so their checks are kept short: one look at a
+# tensor that is as it should be, and the reason only when it is not.
+_BF16, _F32, _I32T, _I64T, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_handle(device_index, stream):
+    """The handle of `stream`, or of the current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(device_index) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _refuse(t, dtype, shape, name):
+    _expect(t, dtype, shape, name)
+    _ptr(t)
+    raise ValueError(f"{name}: the last dimension must be contiguous")
+
+
+def _at(t, dtype, shape, name):
+    """The address of a contiguous device tensor of this type and shape."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _refuse(t, dtype, shape, name)
+
+
+def _heads(t, shape, name):
+    """(address, token stride, head stride) of a bf16 [T][H][D] device tensor with contiguous vectors."""
     ts, hs, es = t.stride()
-    if es != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr(), ts, hs
+    if t.dtype is _BF16 and t.shape == shape and t.is_cuda and es == 1:
+        return t.data_ptr(), ts, hs
+    return _refuse(t, _BF16, shape, name)
 
 
-def _cache_args(cache, heads, dim):
-    """The cache's pointers, its pages and their tokens."""
-    pages, _, page, _ = cache.k.shape
+def _cache_at(cache, heads, dim):
+    """The addresses of the cache's parts, its pages and their tokens."""
+    k, kp, v, vp = cache
+    pages, _, page, _ = k.shape
     codes, pairs = (pages, heads, page, dim // 2), (pages, heads, page, 2)
-    _expect(cache.k, torch.uint8, codes, "cache.k")
-    _expect(cache.v, torch.uint8, codes, "cache.v")
-    _expect(cache.kp, torch.bfloat16, pairs, "cache.kp")
-    _expect(cache.vp, torch.bfloat16, pairs, "cache.vp")
-    return (_ptr(cache.k), _ptr(cache.kp), _ptr(cache.v), _ptr(cache.vp)), pages, page
+    return (_at(k, _U8, codes, "cache.k"), _at(kp, _BF16, pairs, "cache.kp"), _at(v, _U8, codes, "cache.v"),
+            _at(vp, _BF16, pairs, "cache.vp")), pages, page
 
 
-def _rope_args(wq, wk, cos, sin, positions, T, D):
-    """The weights', tables' and positions' pointers, rot and the tables' rows."""
-    _expect(wq, torch.float32, (D,), "wq")
-    _expect(wk, torch.float32, (D,), "wk")
+def _rope_at(wq, wk, cos, sin, positions, T, D):
+    """The addresses of the weights, tables and positions, rot and the tables' rows."""
+    w = _at(wq, _F32, (D,), "wq"), _at(wk, _F32, (D,), "wk")
     if cos is None:
-        return (_ptr(wq), _ptr(wk), None, None, None), 0, 0
-    npos, half = cos.shape
-    _expect(cos, torch.float32, (npos, half), "cos")
-    _expect(sin, torch.float32, (npos, half), "sin")
-    _expect(positions, torch.int64, (T,), "positions")
-    return (_ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin), _ptr(positions)), 2 * half, npos
+        return (*w, None, None, None), 0, 0
+    npos, half = table = cos.shape
+    return (*w, _at(cos, _F32, table, "cos"), _at(sin, _F32, table, "sin"),
+            _at(positions, _I64T, (T,), "positions")), 2 * half, npos
 
 
 _WS_BYTES: dict = {}
 
 
-def _op_workspace(op, M, N, workspace, device, stream):
-    """(pointer, bytes) of the caller's workspace, or of the stream's own."""
+def _op_workspace(op, M, N, workspace, device, handle, stream):
+    """(address, bytes) of the caller's workspace, or of the stream's own."""
     if workspace is None:
         key = (op, M, N, device.index)
         need = _WS_BYTES.get(key)
         if need is None:
             need = _WS_BYTES[key] = r9q_workspace_bytes(op, M, N, 0)
-        workspace = _stream_workspace(need, device, stream)
+        workspace = _WORKSPACES.get((device.index, handle))
+        if workspace is None or workspace.numel() < need:
+            workspace = _stream_workspace(need, device, stream)
+        return workspace.data_ptr(), workspace.numel()
     return _ptr(workspace), workspace.numel() * workspace.element_size()
 
 
@@ -417,16 +438,21 @@ def r9q_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, wq: torch.Tensor, wk: tor
                      q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
     """RMS norm of the heads of q bf16 [T][Hq][D] and k bf16 [T][Hk][D] (any token and head strides) and the
     rotation by cos, sin fp32 [npos][rot/2] at positions int64 [T] (None: norm only); returns (q_out, k_out)."""
-    T, Hq, D = q.shape
-    Hk = k.shape[1]
-    rope, rot, npos = _rope_args(wq, wk, cos, sin, positions, T, D)
+    T, Hq, D = qs = q.shape
+    _, Hk, _ = ks = k.shape
+    if ks != (T, Hk, D):
+        raise ValueError(f"k: expected shape {(T, Hk, D)}, got {tuple(ks)}")
+    rope, rot, npos = _rope_at(wq, wk, cos, sin, positions, T, D)
+    device = q.device
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        q_out = torch.empty(qs, dtype=_BF16, device=device)
     if k_out is None:
-        k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=q.device)
-    _check(_lib.r9q_qk_norm_rope(*_heads(q, "q", (T, Hq, D)), *_heads(k, "k", (T, Hk, D)), *rope,
-                                 *_heads(q_out, "q_out", (T, Hq, D)), *_heads(k_out, "k_out", (T, Hk, D)),
-                                 T, Hq, Hk, D, rot, npos, eps, int(interleaved), _stream(stream)), "r9q_qk_norm_rope")
+        k_out = torch.empty(ks, dtype=_BF16, device=device)
+    rc = _lib.r9q_qk_norm_rope(*_heads(q, qs, "q"), *_heads(k, ks, "k"), *rope, *_heads(q_out, qs, "q_out"),
+                               *_heads(k_out, ks, "k_out"), T, Hq, Hk, D, rot, npos, eps, 1 if interleaved else 0,
+                               _stream_handle(device.index, stream))
+    if rc:
+        _check(rc, "r9q_qk_norm_rope")
     return q_out, k_out
 
 
@@ -438,25 +464,28 @@ def r9q_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Te
                          workspace: torch.Tensor | None = None, stream=None):
     """The gradient of r9q_qk_norm_rope; returns (dq, dk, dwq, dwk).  workspace: as for r9q_gemm_fp8_block_qa
     (zero-filled before its first use; omitted: the stream's own)."""
-    T, Hq, D = q.shape
-    Hk = k.shape[1]
-    rope, rot, npos = _rope_args(wq, wk, cos, sin, positions, T, D)
+    T, Hq, D = qs = q.shape
+    _, Hk, _ = ks = k.shape
+    if ks != (T, Hk, D):
+        raise ValueError(f"k: expected shape {(T, Hk, D)}, got {tuple(ks)}")
+    rope, rot, npos = _rope_at(wq, wk, cos, sin, positions, T, D)
+    device = q.device
     if dq is None:
-        dq = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        dq = torch.empty(qs, dtype=_BF16, device=device)
     if dk is None:
-        dk = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=q.device)
+        dk = torch.empty(ks, dtype=_BF16, device=device)
     if dwq is None:
-        dwq = torch.empty(D, dtype=torch.float32, device=q.device)
+        dwq = torch.empty(D, dtype=_F32, device=device)
     if dwk is None:
-        dwk = torch.empty(D, dtype=torch.float32, device=q.device)
-    _expect(dwq, torch.float32, (D,), "dwq")
-    _expect(dwk, torch.float32, (D,), "dwk")
-    ws, wsb = _op_workspace(R9Q_OP_QK_NORM_ROPE_BWD, 1, D, workspace, q.device, stream)
-    _check(_lib.r9q_qk_norm_rope_bwd(*_heads(dq_out, "dq_out", (T, Hq, D)), *_heads(dk_out, "dk_out", (T, Hk, D)),
-                                     *_heads(q, "q", (T, Hq, D)), *_heads(k, "k", (T, Hk, D)), *rope,
-                                     *_heads(dq, "dq", (T, Hq, D)), *_heads(dk, "dk", (T, Hk, D)), _ptr(dwq),
-                                     _ptr(dwk), T, Hq, Hk, D, rot, npos, eps, int(interleaved), ws, wsb,
-                                     _stream(stream)), "r9q_qk_norm_rope_bwd")
+        dwk = torch.empty(D, dtype=_F32, device=device)
+    handle = _stream_handle(device.index, stream)
+    ws, wsb = _op_workspace(R9Q_OP_QK_NORM_ROPE_BWD, 1, D, workspace, device, handle, stream)
+    rc = _lib.r9q_qk_norm_rope_bwd(*_heads(dq_out, qs, "dq_out"), *_heads(dk_out, ks, "dk_out"), *_heads(q, qs, "q"),
+                                   *_heads(k, ks, "k"), *rope, *_heads(dq, qs, "dq"), *_heads(dk, ks, "dk"),
+                                   _at(dwq, _F32, (D,), "dwq"), _at(dwk, _F32, (D,), "dwk"), T, Hq, Hk, D, rot, npos,
+                                   eps, 1 if interleaved else 0, ws, wsb, handle)
+    if rc:
+        _check(rc, "r9q_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
 
 
@@ -466,45 +495,51 @@ def r9q_qk_norm_rope_kv4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, wq: 
                          q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """r9q_qk_norm_rope with the keys, and v bf16 [T][Hk][D] as it is, written to the cache at slots int64 [T]
     (page * tokens of a page + place; negative: padding); returns q_out."""
-    T, Hq, D = q.shape
-    Hk = k.shape[1]
-    rope, rot, npos = _rope_args(wq, wk, cos, sin, positions, T, D)
-    ptrs, pages, page = _cache_args(cache, Hk, D)
-    _expect(slots, torch.int64, (T,), "slots")
+    T, Hq, D = qs = q.shape
+    _, Hk, _ = ks = k.shape
+    if ks != (T, Hk, D):
+        raise ValueError(f"k: expected shape {(T, Hk, D)}, got {tuple(ks)}")
+    rope, rot, npos = _rope_at(wq, wk, cos, sin, positions, T, D)
+    parts, pages, page = _cache_at(cache, Hk, D)
+    device = q.device
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    _check(_lib.r9q_qk_norm_rope_kv4(*_heads(q, "q", (T, Hq, D)), *_heads(k, "k", (T, Hk, D)),
-                                     *_heads(v, "v", (T, Hk, D)), *rope, *_heads(q_out, "q_out", (T, Hq, D)), *ptrs,
-                                     _ptr(slots), T, Hq, Hk, D, rot, npos, pages, page, eps, int(interleaved),
-                                     _stream(stream)), "r9q_qk_norm_rope_kv4")
+        q_out = torch.empty(qs, dtype=_BF16, device=device)
+    rc = _lib.r9q_qk_norm_rope_kv4(*_heads(q, qs, "q"), *_heads(k, ks, "k"), *_heads(v, ks, "v"), *rope,
+                                   *_heads(q_out, qs, "q_out"), *parts, _at(slots, _I64T, (T,), "slots"), T, Hq, Hk, D,
+                                   rot, npos, pages, page, eps, 1 if interleaved else 0,
+                                   _stream_handle(device.index, stream))
+    if rc:
+        _check(rc, "r9q_qk_norm_rope_kv4")
     return q_out
 
 
 def r9q_kv4_append(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, slots: torch.Tensor, stream=None) -> None:
     """Writes k and v bf16 [T][Hk][D] to the cache at slots int64 [T] (negative: padding)."""
-    T, Hk, D = k.shape
-    ptrs, pages, page = _cache_args(cache, Hk, D)
-    _expect(slots, torch.int64, (T,), "slots")
-    _check(_lib.r9q_kv4_append(*_heads(k, "k", (T, Hk, D)), *_heads(v, "v", (T, Hk, D)), *ptrs, _ptr(slots), T, Hk, D,
-                               pages, page, _stream(stream)), "r9q_kv4_append")
+    T, Hk, D = ks = k.shape
+    parts, pages, page = _cache_at(cache, Hk, D)
+    rc = _lib.r9q_kv4_append(*_heads(k, ks, "k"), *_heads(v, ks, "v"), *parts, _at(slots, _I64T, (T,), "slots"), T, Hk,
+                             D, pages, page, _stream_handle(k.device.index, stream))
+    if rc:
+        _check(rc, "r9q_kv4_append")
 
 
 def r9q_kv4_gather(cache: KV4Cache, slots: torch.Tensor, k: torch.Tensor | None = None,
                    v: torch.Tensor | None = None, stream=None):
     """The tokens at slots int64 [T] as bf16 (k, v) [T][Hk][D]; zeros for padding."""
-    T = slots.shape[0]
+    T, = slots.shape
     _, Hk, _, half = cache.k.shape
-    D = 2 * half
-    ptrs, pages, page = _cache_args(cache, Hk, D)
-    _expect(slots, torch.int64, (T,), "slots")
+    shape = (T, Hk, 2 * half)
+    parts, pages, page = _cache_at(cache, Hk, 2 * half)
+    device = slots.device
     if k is None:
-        k = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=slots.device)
+        k = torch.empty(shape, dtype=_BF16, device=device)
     if v is None:
-        v = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=slots.device)
-    _expect(k, torch.bfloat16, (T, Hk, D), "k")
-    _expect(v, torch.bfloat16, (T, Hk, D), "v")
-    _check(_lib.r9q_kv4_gather(*ptrs, _ptr(slots), T, Hk, D, pages, page, _ptr(k), _ptr(v), _stream(stream)),
-           "r9q_kv4_gather")
+        v = torch.empty(shape, dtype=_BF16, device=device)
+    rc = _lib.r9q_kv4_gather(*parts, _at(slots, _I64T, (T,), "slots"), T, Hk, 2 * half, pages, page,
+                             _at(k, _BF16, shape, "k"), _at(v, _BF16, shape, "v"),
+                             _stream_handle(device.index, stream))
+    if rc:
+        _check(rc, "r9q_kv4_gather")
     return k, v
 
 
@@ -516,29 +551,27 @@ def r9q_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tenso
     over the cache: block_table int32 [B][max_pages], seq_lens int32 [B] (new tokens included).  scale: 1/sqrt(D) by
     default.  Returns o bf16 [B][Lq][Hq][D], or (o, lse fp32 [B][Lq][Hq]) with return_lse.  workspace: as for
     r9q_gemm_fp8_block_qa (zero-filled before its first use; omitted: the stream's own)."""
-    B, Lq, Hq, D = q.shape
-    Hk = cache.k.shape[1]
-    ptrs, pages, page = _cache_args(cache, Hk, D)
-    _expect(q, torch.bfloat16, (B, Lq, Hq, D), "q")
-    if not q.is_cuda:
-        raise ValueError("tensor must be on a CUDA device")
+    B, Lq, Hq, D = qs = q.shape
     bs, ts, hs, es = q.stride()
-    if es != 1:
-        raise ValueError("q: the last dimension must be contiguous")
+    Hk = cache.k.shape[1]
+    parts, pages, page = _cache_at(cache, Hk, D)
+    if not (q.dtype is _BF16 and q.is_cuda and es == 1):
+        _refuse(q, _BF16, qs, "q")
     if Hk < 1 or Hq % Hk:
         raise ValueError("q's heads must be a multiple of the cache's")
     max_pages = block_table.shape[1]
-    _expect(block_table, torch.int32, (B, max_pages), "block_table")
-    _expect(seq_lens, torch.int32, (B,), "seq_lens")
+    device = q.device
     if out is None:
-        out = torch.empty((B, Lq, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty(qs, dtype=_BF16, device=device)
     if lse is None and return_lse:
-        lse = torch.empty((B, Lq, Hq), dtype=torch.float32, device=q.device)
-    _expect(out, torch.bfloat16, (B, Lq, Hq, D), "out")
-    _expect(lse, torch.float32, (B, Lq, Hq), "lse")
-    ws, wsb = _op_workspace(R9Q_OP_KV4_ATTENTION, max(1, Lq * Hq // Hk), D, workspace, q.device, stream)
-    _check(_lib.r9q_kv4_attention(q.data_ptr(), bs, ts, hs, *ptrs, _ptr(block_table), _ptr(seq_lens), _ptr(out),
-                                  _ptr(lse), B, Lq, Hq, Hk, D, pages, page, max_pages, window,
-                                  D ** -0.5 if scale is None else scale, ws, wsb, _stream(stream)),
-           "r9q_kv4_attention")
+        lse = torch.empty((B, Lq, Hq), dtype=_F32, device=device)
+    handle = _stream_handle(device.index, stream)
+    ws, wsb = _op_workspace(R9Q_OP_KV4_ATTENTION, max(1, Lq * Hq // Hk), D, workspace, device, handle, stream)
+    rc = _lib.r9q_kv4_attention(q.data_ptr(), bs, ts, hs, *parts,
+                                _at(block_table, _I32T, (B, max_pages), "block_table"),
+                                _at(seq_lens, _I32T, (B,), "seq_lens"), _at(out, _BF16, qs, "out"),
+                                None if lse is None else _at(lse, _F32, (B, Lq, Hq), "lse"), B, Lq, Hq, Hk, D, pages,
+                                page, max_pages, window, D ** -0.5 if scale is None else scale, ws, wsb, handle)
+    if rc:
+        _check(rc, "r9q_kv4_attention")
     return (out, lse) if return_lse else out
