@@ -25,6 +25,16 @@
 
 namespace r9q {
 
+// The quotient of 0 <= n < 2^31 by a divisor prepared on the host.
+__device__ __forceinline__ int operator/(int n, const FastDiv& d) {
+    return (int)(__umulhi((uint32_t)n * 2u, d.m) >> d.l);
+}
+inline FastDiv fast_div(int d) {
+    int l = 0;
+    while ((1ll << l) < d) ++l;
+    return {(uint32_t)(((1ull << (31 + l)) + d - 1) / d), l, d};
+}
+
 __host__ __device__ __forceinline__ int64_t kv4_head_bytes(int page, int D) { return (int64_t)page * (D / 2); }
 
 // Byte of token t (0..15) inside a group's [j][m][b] block, m = 0.
@@ -44,44 +54,55 @@ __device__ __forceinline__ float group_max(float v) {
     return v;
 }
 
+// The largest of three; NaN if one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Quantises a head vector held by NL = D/8 adjacent lanes, 8 elements each.
 // lowest = bf16(min), step = bf16((max - min) fl32(1/15)), both rounded to nearest (a
 // 16-bit pair keeps the cost at 4 bytes a vector, and codes are taken against
 // the rounded pair, so its rounding only moves the grid by a fraction of a
 // step); code = clamp(rint((x - lowest) / step), 0, 15) with the IEEE fp32
 // quotient (quot_exact, or the division where the step is tiny).  A constant
-// vector has step 0 and codes 0.  A vector with a NaN or an infinity gets a NaN
-// pair: it reads back as NaN, like the vector it came from.  Returns the lane's 8
+// vector has step 0 and codes 0.  A vector with a NaN or an infinity, or a range
+// over fp32's, gets a NaN pair: it reads back as NaN.  Returns the lane's 8
 // codes, element i in bits 4i..4i+3.
 template <int NL>
 __device__ __forceinline__ uint32_t kv4_quantise(const float (&x)[8], uint32_t& pair) {
-    float lo = x[0], hi = x[0], bad = 0.0f;
+    float hi = max3_nan(max3_nan(max3_nan(x[0], x[1], x[2]), x[3], x[4]), max3_nan(x[5], x[6], x[7]), x[0]);
+    float lo = max3_nan(max3_nan(max3_nan(-x[0], -x[1], -x[2]), -x[3], -x[4]), max3_nan(-x[5], -x[6], -x[7]), -x[0]);
+#pragma unroll
+    for (int o = NL / 2; o > 0; o >>= 1) {
+        const float h = __shfl_xor_sync(0xffffffffu, hi, o), l = __shfl_xor_sync(0xffffffffu, lo, o);
+        hi = max3_nan(hi, h, h);
+        lo = max3_nan(lo, l, l);
+    }
+    lo = -lo;
+    const float range = hi - lo;
+    if (!(range < __int_as_float(0x7F800000))) {         // a NaN, an infinity, or no range that fp32 holds
+        pair = 0x7FC07FC0u;
+        return 0u;
+    }
+    const float low = bf16_round(lo), step = bf16_round(__fmul_rn(range, 1.0f / 15.0f));
+    pair = pack_bf16x2(step, low);
+    if (!(step > 0.0f)) return 0u;
+    float q[8];
+    const bool small = step < kQuotExactMinScale;
+    const float r = __frcp_rn(step);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        lo = fminf(lo, x[i]);
-        hi = fmaxf(hi, x[i]);
-        bad = fmaf(x[i], 0.0f, bad);               // NaN as soon as one element is not finite
+        const float d = x[i] - low;
+        const float t = small ? __fdiv_rn(d, step) : quot_exact(d, step, r);
+        // 2^23 + t rounds t to the nearest even integer
+        q[i] = __fadd_rn(__fadd_rn(fminf(fmaxf(t, 0.0f), 15.0f), 8388608.0f), -8388608.0f);
     }
-    hi = group_max<NL>(hi);
-    lo = -group_max<NL>(-lo);
-    bad = group_sum<NL>(bad);
-    const float low = bf16_round(lo) + bad;
-    const float step = bf16_round(__fmul_rn(hi - lo, 1.0f / 15.0f)) + bad;
-    pair = pack_bf16x2(step, low);
-    uint32_t codes = 0;
-    if (step > 0.0f) {
-        const bool small = step < kQuotExactMinScale;
-        const float r = __frcp_rn(step);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float d = x[i] - low;
-            const float t = small ? __fdiv_rn(d, step) : quot_exact(d, step, r);
-            // 2^23 + t rounds t to the nearest even integer, left in the low bits
-            const float c = __fadd_rn(fminf(fmaxf(t, 0.0f), 15.0f), 8388608.0f);
-            codes |= (__float_as_uint(c) & 15u) << (4 * i);
-        }
-    }
-    return codes;
+    // four codes make an integer below 2^16, exactly; adding 2^23 leaves it in the low bits
+    const float a = fmaf(fmaf(fmaf(q[3], 16.0f, q[2]), 16.0f, q[1]), 16.0f, q[0]) + 8388608.0f;
+    const float b = fmaf(fmaf(fmaf(q[7], 16.0f, q[6]), 16.0f, q[5]), 16.0f, q[4]) + 8388608.0f;
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
 }
 
 // Stores the codes of a head vector, lane l of NL = D/8 holding elements 8l..8l+7.

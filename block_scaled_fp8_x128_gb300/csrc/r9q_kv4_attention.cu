@@ -123,10 +123,6 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// The quotient of 0 <= n < 2^31 by a divisor prepared on the host.
-__device__ __forceinline__ int operator/(int n, const FastDiv& d) {
-    return (int)(__umulhi((uint32_t)n * 2u, d.m) >> d.l);
-}
 __device__ __noinline__ long long div64(long long a, long long b) { return a / b; }
 
 // A sequence's keys and the groups an item of it has.  `room`: tokens that its pages
@@ -791,12 +787,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
 
 int used_sms(int sms) { return sms < kMaxSms ? sms : kMaxSms; }
 int row_tiles(int64_t rows) { return rows <= 8 ? 1 : 2; }
-
-FastDiv fast_div(int d) {
-    int l = 0;
-    while ((1ll << l) < d) ++l;
-    return {(uint32_t)(((1ull << (31 + l)) + d - 1) / d), l, d};
-}
 
 template <int D, int NT>
 cudaError_t launch(Kv4AttnParams p, int sms, cudaStream_t st) {

@@ -12,9 +12,11 @@
 // same register).
 //
 // HBM bound: each input and output once.  A head vector takes D/8 lanes of 16
-// bytes; a warp takes kUnroll x (32 / (D/8)) heads of one token with all loads in
-// flight before the first is used.  Neighbouring warps of a block share a token, so
-// the rows of the cos and sin tables come from L1 after the first.
+// bytes; a warp takes kUnroll x (32 / (D/8)) heads of one token at a time, all of a
+// round's loads in flight before the round before it is worked on.  Warps of a block
+// share a token where they can, so that the rows of the cos and sin tables come from L1
+// after the first.  Elements are worked on in pairs (packed fp32, two IEEE results an
+// instruction).
 #include "r9q_kv4.cuh"
 
 namespace r9q {
@@ -23,28 +25,86 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
+constexpr int kMaxRounds = 2;
+constexpr int64_t kEnoughWarps = 152 * 48;
 
 template <int D>
-constexpr int heads_per_warp() { return kUnroll * (256 / D); }
+constexpr int heads_a_round() { return kUnroll * (256 / D); }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// ---- packed pairs of fp32 ----
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 parts_of(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// Eight elements as four pairs.
+struct Eight {
+    uint64_t v[4];
+};
+__device__ __forceinline__ Eight unpack(const uint4& q) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    Eight r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.v[i] = pair_of(bf16_lo(w[i]), bf16_hi(w[i]));
+    return r;
+}
+__device__ __forceinline__ uint4 pack(const Eight& x) {
+    uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(w[i]);
-        x[2 * i + 1] = bf16_hi(w[i]);
+        const float2 f = parts_of(x.v[i]);
+        w[i] = pack_bf16x2(f.x, f.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float dot(const Eight& a, const Eight& b) {
+    uint64_t s = mul2(a.v[0], b.v[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) s = fma2(a.v[i], b.v[i], s);
+    const float2 f = parts_of(s);
+    return f.x + f.y;
+}
+__device__ __forceinline__ void spread(const Eight& x, float (&y)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = parts_of(x.v[i]);
+        y[2 * i] = f.x;
+        y[2 * i + 1] = f.y;
     }
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                      pack_bf16x2(x[6], x[7]));
+// Eight floats at p, `wide`: on 16-byte boundaries.
+__device__ __forceinline__ Eight load8(const float* p, bool wide) {
+    float4 a, b;
+    if (wide) {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *reinterpret_cast<const float4*>(p + 4);
+    } else {
+        a = make_float4(p[0], p[1], p[2], p[3]);
+        b = make_float4(p[4], p[5], p[6], p[7]);
+    }
+    return {{pair_of(a.x, a.y), pair_of(a.z, a.w), pair_of(b.x, b.y), pair_of(b.z, b.w)}};
 }
 
 // A lane's part of the rotation: the lane that holds its pairs' other elements
 // and its eight cos and signed sin (-sin for the first element of a pair).
 struct Turn {
     int src;
-    float c[8], s[8];
+    Eight c, s;
 };
 template <int D>
 __device__ __forceinline__ Turn load_turn(const RopeParams& p, int64_t t, int lane) {
@@ -52,13 +112,14 @@ __device__ __forceinline__ Turn load_turn(const RopeParams& p, int64_t t, int la
     Turn u;
     u.src = lane;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u.c[i] = 1.0f, u.s[i] = 0.0f;
+    for (int i = 0; i < 4; ++i) u.c.v[i] = pair_of(1.0f, 1.0f), u.s.v[i] = 0;
     if (p.rot == 0) return u;
     const int64_t pos = p.pos[t];
     if (pos < 0 || pos >= p.npos) {
         if (lane == 0) record_error(p.err, kErrArg);
+        const float nan = __int_as_float(0x7FC00000);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u.c[i] = u.s[i] = __int_as_float(0x7FC00000);
+        for (int i = 0; i < 4; ++i) u.c.v[i] = u.s.v[i] = pair_of(nan, nan);
         return u;
     }
     if (d0 >= p.rot) return u;
@@ -68,24 +129,19 @@ __device__ __forceinline__ Turn load_turn(const RopeParams& p, int64_t t, int la
         const float4 a = *reinterpret_cast<const float4*>(cs + d0 / 2), b = *reinterpret_cast<const float4*>(sn + d0 / 2);
         const float c4[4] = {a.x, a.y, a.z, a.w}, s4[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            u.c[i] = c4[i / 2];
-            u.s[i] = i & 1 ? s4[i / 2] : -s4[i / 2];
+        for (int i = 0; i < 4; ++i) {
+            u.c.v[i] = pair_of(c4[i], c4[i]);
+            u.s.v[i] = pair_of(-s4[i], s4[i]);
         }
     } else {
         const bool second = d0 >= half;
         const int at = second ? d0 - half : d0;
         u.src = second ? lane - half / 8 : lane + half / 8;
+        u.c = load8(cs + at, true);
+        u.s = load8(sn + at, true);
+        if (!second) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float4 a = *reinterpret_cast<const float4*>(cs + at + 4 * k);
-            const float4 b = *reinterpret_cast<const float4*>(sn + at + 4 * k);
-            const float c4[4] = {a.x, a.y, a.z, a.w}, s4[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                u.c[4 * k + i] = c4[i];
-                u.s[4 * k + i] = second ? s4[i] : -s4[i];
-            }
+            for (int i = 0; i < 4; ++i) u.s.v[i] ^= 0x8000000080000000ull;
         }
     }
     return u;
@@ -102,11 +158,14 @@ __device__ __forceinline__ uint4 partner(const uint4& v, const Turn& u, int inte
 // w c and w' s' for the lane's elements, in place of c and s.
 template <int D>
 __device__ __forceinline__ void fold_weight(Turn& u, const float* w, int lane, int interleaved) {
-    const int d0 = 8 * (lane & (D / 8 - 1)), e0 = 8 * (u.src & (D / 8 - 1));
+    const bool wide = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
+    const Eight own = load8(w + 8 * (lane & (D / 8 - 1)), wide);
+    const Eight other = interleaved ? own : load8(w + 8 * (u.src & (D / 8 - 1)), wide);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        u.c[i] *= w[d0 + i];
-        u.s[i] *= interleaved ? w[d0 + (i ^ 1)] : w[e0 + i];
+    for (int i = 0; i < 4; ++i) {
+        u.c.v[i] = mul2(u.c.v[i], own.v[i]);
+        const float2 o = parts_of(other.v[i]);
+        u.s.v[i] = mul2(u.s.v[i], interleaved ? pair_of(o.y, o.x) : other.v[i]);
     }
 }
 
@@ -163,8 +222,12 @@ __device__ __forceinline__ float sum_squares_in_order(const float (&x)[8], int l
 // once, and the sum of squares has a fixed order.  An evaluation of the formula
 // step by step in fp32 gives the same codes.
 template <int NL>
-__device__ __forceinline__ void norm_rope_in_order(float (&y)[8], const float (&w)[8], const Turn& u, int lane,
+__device__ __forceinline__ void norm_rope_in_order(float (&y)[8], const Eight& weight, const Turn& u, int lane,
                                                    const RopeParams& p) {
+    float w[8], cs[8], sn[8];
+    spread(weight, w);
+    spread(u.c, cs);
+    spread(u.s, sn);
     const float mean = __fmul_rn(sum_squares_in_order<NL>(y, lane & (NL - 1)), 1.0f / (8 * NL));
     const float r = rsqrtf(__fadd_rn(mean, p.eps));
     float z[8];
@@ -173,7 +236,7 @@ __device__ __forceinline__ void norm_rope_in_order(float (&y)[8], const float (&
 #pragma unroll
     for (int e = 0; e < 8; ++e) z[e] = p.interleaved ? y[e ^ 1] : __shfl_sync(0xffffffffu, y[e], u.src);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = __fadd_rn(__fmul_rn(y[e], u.c[e]), __fmul_rn(z[e], u.s[e]));
+    for (int e = 0; e < 8; ++e) y[e] = __fadd_rn(__fmul_rn(y[e], cs[e]), __fmul_rn(z[e], sn[e]));
 }
 
 enum Pass { kRope, kRopeCache, kAppend };
@@ -185,7 +248,9 @@ struct ForwardArgs {
     Kv4Cache c;
     const int64_t* slots;
     int64_t T;
-    int nq, nk, nv;          // warps a token's query, key and value heads take
+    int rounds;              // of heads a warp takes
+    int nq, nk;              // warps that a token's query and key heads take
+    FastDiv parts;           // and all its heads
 };
 
 // Where a token goes: its page and place, or page -1 for padding and for a slot
@@ -210,13 +275,12 @@ __device__ __forceinline__ Place find_slot(const Kv4Cache& c, int64_t slot, int 
 
 template <int D, int PASS>
 __global__ void __launch_bounds__(kThreads) forward_kernel(const ForwardArgs a) {
-    constexpr int NL = D / 8, NV = 32 / NL, HPW = heads_per_warp<D>();
+    constexpr int NL = D / 8, NV = 32 / NL, HR = heads_a_round<D>();
     const int lane = threadIdx.x & 31, l = lane & (NL - 1), sub = lane / NL;
-    const int parts = a.nq + a.nk + a.nv;
-    const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t t = unit / parts;
+    const int unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int t = unit / a.parts;
     if (t >= a.T) return;
-    int part = (int)(unit - t * parts);
+    int part = unit - t * a.parts.d;
     int kind = 0;                                        // 0 query, 1 key, 2 value
     if (part >= a.nq) {
         part -= a.nq;
@@ -227,78 +291,92 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const ForwardArgs a) 
         }
     }
     const HeadsIn& in = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-    const int h0 = part * HPW + sub;
-    uint4 x[kUnroll];
+    int h0 = part * a.rounds * HR;                       // the round's first head
+    const int end = min(in.heads, h0 + a.rounds * HR);
+    const uint16_t* src = in.p + t * in.ts + (h0 + sub) * in.hs + 8 * l;
+    uint4 next[kUnroll];
+    auto load = [&](int h) {
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-        const int h = h0 + i * NV;
-        x[i] = h < in.heads ? *reinterpret_cast<const uint4*>(in.p + t * in.ts + h * in.hs + 8 * l)
-                            : make_uint4(0u, 0u, 0u, 0u);
-    }
+        for (int i = 0; i < kUnroll; ++i)
+            next[i] = h + i * NV + sub < end ? *reinterpret_cast<const uint4*>(src + i * NV * in.hs)
+                                             : make_uint4(0u, 0u, 0u, 0u);
+        src += HR * in.hs;
+    };
+    load(h0);
     Place place = {-1, 0};
     if (PASS != kRope && kind > 0) place = find_slot(a.c, a.slots[t], lane, a.rope.err);
     const bool turned = PASS != kAppend && kind < 2;
     const bool in_order = PASS == kRopeCache && kind == 1;
     Turn u;
-    float w[8];
+    Eight w;
     if (turned) {
         u = load_turn<D>(a.rope, t, lane);
-        if (in_order) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = a.rope.wk[8 * l + e];
-        } else {
+        if (in_order)
+            w = load8(a.rope.wk + 8 * l, (reinterpret_cast<uintptr_t>(a.rope.wk) & 15) == 0);
+        else
             fold_weight<D>(u, kind == 0 ? a.rope.wq : a.rope.wk, lane, a.rope.interleaved);
-        }
     }
+    const bool cached = PASS == kAppend || (PASS == kRopeCache && kind > 0);
+    const HeadsOut& out = kind == 0 ? a.qo : a.ko;
+    uint16_t* dst = cached ? nullptr : out.p + t * out.ts + (h0 + sub) * out.hs + 8 * l;
+    for (; h0 < end; h0 += HR) {
+        uint4 x[kUnroll];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-        const int h = h0 + i * NV;
-        if (part * HPW + i * NV >= in.heads) break;      // the same for the whole warp
-        float y[8];
-        unpack8(x[i], y);
-        if (in_order) {
-            norm_rope_in_order<NL>(y, w, u, lane, a.rope);
-        } else if (turned) {
-            float xp[8], ss = 0.0f;
-            unpack8(partner(x[i], u, a.rope.interleaved), xp);
+        for (int i = 0; i < kUnroll; ++i) x[i] = next[i];
+        if (h0 + HR < end) load(h0 + HR);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-            const float r = rsqrtf(group_sum<NL>(ss) * (1.0f / D) + a.rope.eps);
+        for (int i = 0; i < kUnroll; ++i) {
+            if (h0 + i * NV >= end) break;               // the same for the whole warp
+            const int h = h0 + i * NV + sub;
+            Eight y = unpack(x[i]);
+            if (turned && !in_order) {
+                const Eight xp = unpack(partner(x[i], u, a.rope.interleaved));
+                const float r = rsqrtf(group_sum<NL>(dot(y, y)) * (1.0f / D) + a.rope.eps);
+                const uint64_t rr = pair_of(r, r);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = r * fmaf(y[e], u.c[e], xp[e] * u.s[e]);
-        }
-        if (PASS == kRope || (PASS == kRopeCache && kind == 0)) {
-            const HeadsOut& out = kind == 0 ? a.qo : a.ko;
-            if (h < in.heads) *reinterpret_cast<uint4*>(out.p + t * out.ts + h * out.hs + 8 * l) = pack8(y);
-        } else {
-            uint32_t pair;
-            const uint32_t codes = kv4_quantise<NL>(y, pair);
-            const bool live = h < in.heads && place.page >= 0;
-            const int64_t head = place.page * a.c.heads + h;
-            if (kind == 1) {
-                if (live) {
-                    kv4_store_k(a.c.k + head * kv4_head_bytes(a.c.page, D) + (int64_t)place.at * (D / 2), l, codes);
-                    if (l == 0) a.c.kp[head * a.c.page + place.at] = pair;
-                }
+                for (int e = 0; e < 4; ++e) y.v[e] = mul2(rr, fma2(y.v[e], u.c.v[e], mul2(xp.v[e], u.s.v[e])));
+            }
+            if (!cached) {
+                if (h < end) *reinterpret_cast<uint4*>(dst + i * NV * out.hs) = pack(y);
             } else {
-                kv4_store_v(live ? a.c.v + head * kv4_head_bytes(a.c.page, D) + (int64_t)(place.at >> 4) * (8 * D)
-                                 : nullptr,
-                            place.at & 15, l, codes);
-                if (live && l == 0) a.c.vp[head * a.c.page + place.at] = pair;
+                float z[8];
+                spread(y, z);
+                if (in_order) norm_rope_in_order<NL>(z, w, u, lane, a.rope);
+                uint32_t pair;
+                const uint32_t codes = kv4_quantise<NL>(z, pair);
+                const bool live = h < end && place.page >= 0;
+                const int64_t head = place.page * a.c.heads + h;
+                if (kind == 1) {
+                    if (live) {
+                        kv4_store_k(a.c.k + head * kv4_head_bytes(a.c.page, D) + (int64_t)place.at * (D / 2), l, codes);
+                        if (l == 0) a.c.kp[head * a.c.page + place.at] = pair;
+                    }
+                } else {
+                    kv4_store_v(live ? a.c.v + head * kv4_head_bytes(a.c.page, D) + (int64_t)(place.at >> 4) * (8 * D)
+                                     : nullptr,
+                                place.at & 15, l, codes);
+                    if (live && l == 0) a.c.vp[head * a.c.page + place.at] = pair;
+                }
             }
         }
+        if (!cached) dst += HR * out.hs;
     }
 }
 
 template <int D, int PASS>
 cudaError_t launch_forward(ForwardArgs a, cudaStream_t st) {
-    constexpr int HPW = heads_per_warp<D>();
-    a.nq = PASS == kAppend ? 0 : (a.q.heads + HPW - 1) / HPW;
-    a.nk = (a.k.heads + HPW - 1) / HPW;
-    a.nv = PASS == kRope ? 0 : (a.v.heads + HPW - 1) / HPW;
-    const int64_t warps = a.T * (a.nq + a.nk + a.nv);
-    const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    constexpr int HR = heads_a_round<D>();
+    auto warps = [&](int heads) { return (heads + a.rounds * HR - 1) / (a.rounds * HR); };
+    // Two rounds a warp share the token's set-up where that still leaves every SM its fill of warps.
+    for (a.rounds = kMaxRounds;; a.rounds /= 2) {
+        a.nq = PASS == kAppend ? 0 : warps(a.q.heads);
+        a.nk = warps(a.k.heads);
+        const int parts = a.nq + a.nk + (PASS == kRope ? 0 : warps(a.v.heads));
+        a.parts = fast_div(parts);
+        if (a.rounds == 1 || a.T * parts >= kEnoughWarps) break;
+    }
+    const int64_t blocks = (a.T * a.parts.d + kThreads / 32 - 1) / (kThreads / 32);
+    if (blocks > INT32_MAX / (kThreads / 32)) return cudaErrorInvalidValue;
     forward_kernel<D, PASS><<<(unsigned)blocks, kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
@@ -335,11 +413,12 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const Kv4Cache c, cons
     if (h >= c.heads) return;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        float y[8];
+        const uint64_t step = pair_of(bf16_lo(pair[s]), bf16_lo(pair[s])), low = pair_of(bf16_hi(pair[s]), bf16_hi(pair[s]));
+        Eight y;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            y[i] = fmaf(bf16_lo(pair[s]), (float)((codes[s] >> (4 * i)) & 15u), bf16_hi(pair[s]));
-        *reinterpret_cast<uint4*>((s == 0 ? k : v) + (t * c.heads + h) * D + 8 * l) = pack8(y);
+        for (int i = 0; i < 4; ++i)
+            y.v[i] = fma2(step, pair_of((float)(codes[s] >> (8 * i) & 15u), (float)(codes[s] >> (8 * i + 4) & 15u)), low);
+        *reinterpret_cast<uint4*>((s == 0 ? k : v) + (t * c.heads + h) * D + 8 * l) = pack(y);
     }
 }
 
@@ -348,119 +427,135 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const Kv4Cache c, cons
 // With g = R^T dy (the turn by the opposite angle) and xh = x r:
 //   dw = sum over tokens and heads of g xh,
 //   dx = r (w g - xh mean(w g xh)) = r w g - x r^3 sum(w g x) / D.
-// r is computed again from x: that reads nothing that dx does not need.  Blocks
-// of 16 warps walk the (token, part) units in a fixed order, each lane summing
-// its elements' dw in 32 bits; a block's sum goes to `part`, and the block that
-// finishes last adds the blocks' sums in their order, so dw does not depend on
-// timing.
+// r is computed again from x: that reads nothing that dx does not need.  One block of
+// 16 warps an SM walks the (token, part) units of the query heads, then of the key
+// heads, in a fixed order, each lane summing its elements' dw in 32 bits; a block's
+// sums go to `part`, and the block that finishes last adds the blocks' sums in their
+// order, so dw does not depend on timing.
+struct BackwardArgs {
+    HeadsIn dqo, dko, q, k;
+    RopeParams rope;
+    HeadsOut dq, dk;
+    float *dwq, *dwk, *part;
+    int* done;
+    FastDiv q_parts, k_parts;    // units that a token's query and key heads take
+};
 constexpr int kBwdThreads = 512;
-constexpr int kBwdUnroll = 2;
+constexpr int kBwdUnroll = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kBwdThreads) backward_kernel(const HeadsIn dqo, const HeadsIn dko, const HeadsIn q,
-                                                               const HeadsIn k, const RopeParams p, const HeadsOut dq,
-                                                               const HeadsOut dk, float* dwq, float* dwk, float* part,
-                                                               int* done) {
-    constexpr int NL = D / 8, NV = 32 / NL, HPW = kBwdUnroll * NV, NW = kBwdThreads / 32;
+__global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const BackwardArgs a) {
+    constexpr int NL = D / 8, NV = 32 / NL, HR = kBwdUnroll * NV, NW = kBwdThreads / 32;
+    __shared__ __align__(16) float sums[NW * 128];       // the warps' sums [NW][D]; at the end four floats a thread
+    const RopeParams& p = a.rope;
     const int lane = threadIdx.x & 31, l = lane & (NL - 1), sub = lane / NL, warp = threadIdx.x >> 5;
-    const int nq = (q.heads + HPW - 1) / HPW, nk = (k.heads + HPW - 1) / HPW, parts = nq + nk;
-    float dw[2][8];
+#pragma unroll 1
+    for (int kind = 0; kind < 2; ++kind) {
+        const HeadsIn& gin = kind ? a.dko : a.dqo;
+        const HeadsIn& xin = kind ? a.k : a.q;
+        const HeadsOut& out = kind ? a.dk : a.dq;
+        const FastDiv& parts = kind ? a.k_parts : a.q_parts;
+        const float* wp = kind ? p.wk : p.wq;
+        const Eight w = load8(wp + 8 * l, (reinterpret_cast<uintptr_t>(wp) & 15) == 0);
+        Eight dw = {{0, 0, 0, 0}};
+        const int units = (int)p.T * parts.d, stride = gridDim.x * NW;
+        // the last blocks take the key heads' first units, which their share of the query heads leaves room for
+        int unit = (kind ? gridDim.x - 1 - blockIdx.x : blockIdx.x) * NW + warp;
+        uint4 gn[kBwdUnroll], xn[kBwdUnroll];
+        auto load = [&](int at) {
+            const int t = at / parts, h0 = (at - t * parts.d) * HR + sub;
+            const uint16_t* gp = gin.p + t * gin.ts + h0 * gin.hs + 8 * l;
+            const uint16_t* xp = xin.p + t * xin.ts + h0 * xin.hs + 8 * l;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.0f;
-    const int64_t units = p.T * parts, stride = (int64_t)gridDim.x * NW;
-    for (int64_t unit = (int64_t)blockIdx.x * NW + warp; unit < units; unit += stride) {
-        const int64_t t = unit / parts;
-        int pt = (int)(unit - t * parts);
-        const bool key = pt >= nq;
-        if (key) pt -= nq;
-        const HeadsIn& gin = key ? dko : dqo;
-        const HeadsIn& xin = key ? k : q;
-        const HeadsOut& out = key ? dk : dq;
-        const int h0 = pt * HPW + sub;
-        uint4 gv[kBwdUnroll], xv[kBwdUnroll];
+            for (int i = 0; i < kBwdUnroll; ++i) {
+                gn[i] = xn[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (h0 + i * NV < xin.heads) {
+                    gn[i] = *reinterpret_cast<const uint4*>(gp + i * NV * gin.hs);
+                    xn[i] = *reinterpret_cast<const uint4*>(xp + i * NV * xin.hs);
+                }
+            }
+        };
+        if (unit < units) load(unit);
+        for (; unit < units; unit += stride) {
+            const int t = unit / parts, h0 = (unit - t * parts.d) * HR + sub;
+            const Turn u = load_turn<D>(p, t, lane);
+            uint16_t* dst = out.p + t * out.ts + h0 * out.hs + 8 * l;
+            uint4 gv[kBwdUnroll], xv[kBwdUnroll];
 #pragma unroll
-        for (int i = 0; i < kBwdUnroll; ++i) {
-            const int h = h0 + i * NV;
-            gv[i] = xv[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (h < xin.heads) {
-                gv[i] = *reinterpret_cast<const uint4*>(gin.p + t * gin.ts + h * gin.hs + 8 * l);
-                xv[i] = *reinterpret_cast<const uint4*>(xin.p + t * xin.ts + h * xin.hs + 8 * l);
+            for (int i = 0; i < kBwdUnroll; ++i) {
+                gv[i] = gn[i];
+                xv[i] = xn[i];
+            }
+            if (unit + stride < units) load(unit + stride);
+#pragma unroll
+            for (int i = 0; i < kBwdUnroll; ++i) {
+                if (h0 - sub + i * NV >= xin.heads) break;               // the same for the whole warp
+                Eight g = unpack(gv[i]), wg;
+                const Eight gp = unpack(partner(gv[i], u, p.interleaved)), x = unpack(xv[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    g.v[e] = fma2(g.v[e], u.c.v[e], mul2(gp.v[e], u.s.v[e] ^ 0x8000000080000000ull));
+                    wg.v[e] = mul2(w.v[e], g.v[e]);
+                }
+                const float ss = group_sum<NL>(dot(x, x)), sg = group_sum<NL>(dot(wg, x));
+                const float r = rsqrtf(ss * (1.0f / D) + p.eps);
+                const float m = -r * r * r * sg * (1.0f / D);
+                const uint64_t rr = pair_of(r, r), mm = pair_of(m, m);
+                Eight y;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    dw.v[e] = fma2(g.v[e], mul2(x.v[e], rr), dw.v[e]);
+                    y.v[e] = fma2(wg.v[e], rr, mul2(x.v[e], mm));
+                }
+                if (h0 + i * NV < xin.heads) *reinterpret_cast<uint4*>(dst + i * NV * out.hs) = pack(y);
             }
         }
-        const Turn u = load_turn<D>(p, t, lane);
-        const float* wp = (key ? p.wk : p.wq) + 8 * l;
-        float w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = wp[e];
-#pragma unroll
-        for (int i = 0; i < kBwdUnroll; ++i) {
-            const int h = h0 + i * NV;
-            float g[8], gp[8], x[8], ss = 0.0f, sg = 0.0f;
-            unpack8(gv[i], g);
-            unpack8(partner(gv[i], u, p.interleaved), gp);
-            unpack8(xv[i], x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                g[e] = fmaf(g[e], u.c[e], -gp[e] * u.s[e]);
-                ss = fmaf(x[e], x[e], ss);
-                sg = fmaf(w[e] * g[e], x[e], sg);
-            }
-            ss = group_sum<NL>(ss);
-            sg = group_sum<NL>(sg);
-            const float r = rsqrtf(ss * (1.0f / D) + p.eps);
-            const float m = r * r * r * sg * (1.0f / D);
-            float y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float gx = g[e] * (x[e] * r);
-                if (key) dw[1][e] += gx;
-                else dw[0][e] += gx;
-                y[e] = fmaf(r * w[e], g[e], -x[e] * m);
-            }
-            if (h < xin.heads) *reinterpret_cast<uint4*>(out.p + t * out.ts + h * out.hs + 8 * l) = pack8(y);
-        }
-    }
-    // the block's sum: over the warp's NV vectors, then over the warps
-    __shared__ float sums[NW][2 * D];
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
+        // the block's sum: over the warp's NV vectors, then over the warps
+        float f[8];
+        spread(dw, f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float v = dw[s][e];
 #pragma unroll
-            for (int o = NL; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (sub == 0) sums[warp][s * D + 8 * l + e] = v;
+            for (int o = NL; o < 32; o <<= 1) f[e] += __shfl_xor_sync(0xffffffffu, f[e], o);
+            if (sub == 0) sums[warp * D + 8 * l + e] = f[e];
         }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * D; i += kBwdThreads) {
-        float v = 0.0f;
+        __syncthreads();
+        if (threadIdx.x < D) {
+            float v = 0.0f;
 #pragma unroll
-        for (int w2 = 0; w2 < NW; ++w2) v += sums[w2][i];
-        part[(int64_t)blockIdx.x * 2 * D + i] = v;
+            for (int k = 0; k < NW; ++k) v += sums[k * D + threadIdx.x];
+            a.part[((int64_t)blockIdx.x * 2 + kind) * D + threadIdx.x] = v;
+        }
+        __syncthreads();
     }
     __threadfence();
     __syncthreads();
     __shared__ int last;
-    if (threadIdx.x == 0) last = atomicAdd(done, 1) == (int)gridDim.x - 1;
+    if (threadIdx.x == 0) last = atomicAdd(a.done, 1) == (int)gridDim.x - 1;
     __syncthreads();
     if (!last) return;
     __threadfence();
-    constexpr int ROWS = kBwdThreads / (2 * D);          // threads that share a column
-    const int col = threadIdx.x % (2 * D), row = threadIdx.x / (2 * D);
-    float v = 0.0f;
-    for (int b = row; b < (int)gridDim.x; b += ROWS) v += __ldcg(part + (int64_t)b * 2 * D + col);
-    float* flat = &sums[0][0];
-    __syncthreads();
+    // a thread adds four columns of every ROWS-th block's sums, many loads in flight
+    constexpr int COLS = 2 * D / 4, ROWS = kBwdThreads / COLS;
+    const int col = threadIdx.x % COLS, row = threadIdx.x / COLS;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 10
+    for (int b = row; b < (int)gridDim.x; b += ROWS) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part + (int64_t)b * 2 * D) + col);
+        v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+    }
+    float4* flat = reinterpret_cast<float4*>(sums);
+    static_assert(sizeof(sums) >= kBwdThreads * sizeof(float4), "room for every thread's sums");
     flat[threadIdx.x] = v;
     __syncthreads();
     if (threadIdx.x < 2 * D) {
-        v = 0.0f;
+        const float* s = sums + threadIdx.x;
+        float x = 0.0f;
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) v += flat[i * 2 * D + col];
-        if (col < D) dwq[col] = v;
-        else dwk[col - D] = v;
+        for (int i = 0; i < ROWS; ++i) x += s[i * 2 * D];
+        (threadIdx.x < D ? a.dwq : a.dwk - D)[threadIdx.x] = x;
     }
-    if (threadIdx.x == 0) *done = 0;
+    if (threadIdx.x == 0) *a.done = 0;
 }
 
 }  // namespace
@@ -513,19 +608,20 @@ cudaError_t launch_kv4_gather(int D, const Kv4Cache& c, const int64_t* slots, in
     return cudaGetLastError();
 }
 
-int qk_norm_rope_bwd_blocks(int sms) { return 2 * sms; }
+int qk_norm_rope_bwd_blocks(int sms) { return sms; }
 
 cudaError_t launch_qk_norm_rope_bwd(int D, const HeadsIn& dqo, const HeadsIn& dko, const HeadsIn& q, const HeadsIn& k,
                                     const RopeParams& p, const HeadsOut& dq, const HeadsOut& dk, float* dwq,
                                     float* dwk, float* part, int* done, int sms, cudaStream_t st) {
-    const int hpw = kBwdUnroll * (256 / D), nw = kBwdThreads / 32;
-    const int64_t units = p.T * ((q.heads + hpw - 1) / hpw + (k.heads + hpw - 1) / hpw);
+    const int hr = kBwdUnroll * (256 / D), nw = kBwdThreads / 32;
+    BackwardArgs a = {dqo, dko, q, k, p, dq, dk, dwq, dwk, part, done, fast_div((q.heads + hr - 1) / hr),
+                      fast_div((k.heads + hr - 1) / hr)};
+    const int64_t units = p.T * (a.q_parts.d + a.k_parts.d);
+    if (units > INT32_MAX / 2) return cudaErrorInvalidValue;
     const int64_t want = (units + nw - 1) / nw, cap = qk_norm_rope_bwd_blocks(sms);
     const unsigned grid = (unsigned)(want < cap ? want : cap);
-    if (D == 64)
-        backward_kernel<64><<<grid, kBwdThreads, 0, st>>>(dqo, dko, q, k, p, dq, dk, dwq, dwk, part, done);
-    else
-        backward_kernel<128><<<grid, kBwdThreads, 0, st>>>(dqo, dko, q, k, p, dq, dk, dwq, dwk, part, done);
+    if (D == 64) backward_kernel<64><<<grid, kBwdThreads, 0, st>>>(a);
+    else backward_kernel<128><<<grid, kBwdThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 

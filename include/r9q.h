@@ -288,7 +288,7 @@ int r9q_qk_norm_rope_bwd(const void* dq_out, int64_t dqo_ts, int64_t dqo_hs, con
  * a bf16 pair: lowest = bf16(min x), step = bf16((max x - min x) * fl32(1/15)),
  * code = clamp(rint((x - lowest) / step), 0, 15) (0 where step = 0), each step in
  * fp32; it stands for lowest + step * code.  A vector that holds a NaN or an
- * infinity is kept as NaN.
+ * infinity, or whose range is over fp32's, is kept as NaN.
  *   kc  u8   [pages][Hk][page][D/2]: byte i holds elements 2i (low nibble), 2i+1
  *   vc  u8   [pages][Hk][page/16][D/64][8 r][4 j][4 m][4 b]: token t of 16 has
  *            j = (t % 8) / 2, b = 2 (t % 2) + t / 8; element 64c + 16m + 8n + r is
