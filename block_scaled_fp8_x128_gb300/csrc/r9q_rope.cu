@@ -7,16 +7,17 @@
 // x' the pair's other element
 //   out = r (x (w c) + x' (w' s')),   s' = -sin for a, +sin for b,
 // and w c, w' s' depend on the token and the element only: a warp forms them
-// once and uses them for all its heads of the token.  x' comes from the lane
-// that holds it, one shuffle of the packed bf16 input (adjacent pairs: from the
-// same register).
+// once and uses them for all its heads of the token.
 //
-// HBM bound: each input and output once.  A head vector takes D/8 lanes of 16
-// bytes; a warp takes kUnroll x (32 / (D/8)) heads of one token at a time, all of a
-// round's loads in flight before the round before it is worked on.  Warps of a block
-// share a token where they can, so that the rows of the cos and sin tables come from L1
-// after the first.  Elements are worked on in pairs (packed fp32, two IEEE results an
-// instruction).
+// HBM bound: each input and output once.  A head vector takes D/8 lanes, 16 bytes
+// each.  Where the whole vector turns in pairs (i, i + D/2), the common case, a lane
+// takes four elements of either half (two 8-byte accesses), so that it holds both of
+// each pair; otherwise it takes eight in a row and x' comes from the lane that holds
+// it, by a shuffle of the packed input (adjacent pairs: from the same register).  A
+// warp takes kUnroll x (32 / (D/8)) heads of one token at a time, all their loads in
+// flight; warps of a block share a token where they can, so that the rows of the cos
+// and sin tables come from L1 after the first.  Elements are worked on two at a time
+// (packed fp32, two IEEE results an instruction).
 #include "r9q_kv4.cuh"
 
 namespace r9q {
@@ -87,33 +88,60 @@ __device__ __forceinline__ void spread(const Eight& x, float (&y)[8]) {
         y[2 * i + 1] = f.y;
     }
 }
-// Eight floats at p, `wide`: on 16-byte boundaries.
-__device__ __forceinline__ Eight load8(const float* p, bool wide) {
-    float4 a, b;
-    if (wide) {
-        a = *reinterpret_cast<const float4*>(p);
-        b = *reinterpret_cast<const float4*>(p + 4);
+// The lane's elements of a head vector: the first four at first(l), the others at
+// second(l).  SPLIT: four of either half, else eight in a row.
+template <int D, bool SPLIT>
+__device__ __forceinline__ int first(int l) { return SPLIT ? 4 * l : 8 * l; }
+template <int D, bool SPLIT>
+__device__ __forceinline__ int second(int l) { return SPLIT ? D / 2 + 4 * l : 8 * l + 4; }
+
+template <int D, bool SPLIT>
+__device__ __forceinline__ uint4 load_bf16(const uint16_t* head, int l) {
+    if (!SPLIT) return *reinterpret_cast<const uint4*>(head + 8 * l);
+    const uint2 a = *reinterpret_cast<const uint2*>(head + first<D, SPLIT>(l));
+    const uint2 b = *reinterpret_cast<const uint2*>(head + second<D, SPLIT>(l));
+    return make_uint4(a.x, a.y, b.x, b.y);
+}
+template <int D, bool SPLIT>
+__device__ __forceinline__ void store_bf16(uint16_t* head, int l, const uint4& v) {
+    if (SPLIT) {
+        *reinterpret_cast<uint2*>(head + first<D, SPLIT>(l)) = make_uint2(v.x, v.y);
+        *reinterpret_cast<uint2*>(head + second<D, SPLIT>(l)) = make_uint2(v.z, v.w);
     } else {
-        a = make_float4(p[0], p[1], p[2], p[3]);
-        b = make_float4(p[4], p[5], p[6], p[7]);
+        *reinterpret_cast<uint4*>(head + 8 * l) = v;
     }
+}
+// Four floats at p, on a 16-byte boundary or not.
+__device__ __forceinline__ float4 load4(const float* p, bool wide) {
+    return wide ? *reinterpret_cast<const float4*>(p) : make_float4(p[0], p[1], p[2], p[3]);
+}
+__device__ __forceinline__ Eight eight_of(const float4& a, const float4& b) {
     return {{pair_of(a.x, a.y), pair_of(a.z, a.w), pair_of(b.x, b.y), pair_of(b.z, b.w)}};
 }
+template <int D, bool SPLIT>
+__device__ __forceinline__ Eight load_weight(const float* w, int l) {
+    const bool wide = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
+    return eight_of(load4(w + first<D, SPLIT>(l), wide), load4(w + second<D, SPLIT>(l), wide));
+}
 
-// A lane's part of the rotation: the lane that holds its pairs' other elements
-// and its eight cos and signed sin (-sin for the first element of a pair).
+// A lane's part of the rotation: its eight cos and signed sin (-sin for the first
+// element of a pair), and without SPLIT the lane that holds its pairs' other elements.
 struct Turn {
     int src;
     Eight c, s;
 };
-template <int D>
+constexpr uint64_t kSigns = 0x8000000080000000ull;
+
+template <int D, bool SPLIT>
 __device__ __forceinline__ Turn load_turn(const RopeParams& p, int64_t t, int lane) {
     const int l = lane & (D / 8 - 1), d0 = 8 * l, half = p.rot / 2;
     Turn u;
     u.src = lane;
+    if (!SPLIT) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u.c.v[i] = pair_of(1.0f, 1.0f), u.s.v[i] = 0;
-    if (p.rot == 0) return u;
+        for (int i = 0; i < 4; ++i) u.c.v[i] = pair_of(1.0f, 1.0f), u.s.v[i] = 0;
+        if (p.rot == 0) return u;
+    }
     const int64_t pos = p.pos[t];
     if (pos < 0 || pos >= p.npos) {
         if (lane == 0) record_error(p.err, kErrArg);
@@ -122,11 +150,19 @@ __device__ __forceinline__ Turn load_turn(const RopeParams& p, int64_t t, int la
         for (int i = 0; i < 4; ++i) u.c.v[i] = u.s.v[i] = pair_of(nan, nan);
         return u;
     }
-    if (d0 >= p.rot) return u;
     const float* cs = p.cos + pos * half;
     const float* sn = p.sin + pos * half;
+    if (SPLIT) {
+        const float4 c = load4(cs + 4 * l, true), s = load4(sn + 4 * l, true);
+        u.c = eight_of(c, c);
+        u.s = eight_of(s, s);
+        u.s.v[0] ^= kSigns;
+        u.s.v[1] ^= kSigns;
+        return u;
+    }
+    if (d0 >= p.rot) return u;
     if (p.interleaved) {
-        const float4 a = *reinterpret_cast<const float4*>(cs + d0 / 2), b = *reinterpret_cast<const float4*>(sn + d0 / 2);
+        const float4 a = load4(cs + d0 / 2, true), b = load4(sn + d0 / 2, true);
         const float c4[4] = {a.x, a.y, a.z, a.w}, s4[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -134,52 +170,79 @@ __device__ __forceinline__ Turn load_turn(const RopeParams& p, int64_t t, int la
             u.s.v[i] = pair_of(-s4[i], s4[i]);
         }
     } else {
-        const bool second = d0 >= half;
-        const int at = second ? d0 - half : d0;
-        u.src = second ? lane - half / 8 : lane + half / 8;
-        u.c = load8(cs + at, true);
-        u.s = load8(sn + at, true);
-        if (!second) {
+        const bool upper = d0 >= half;
+        const int at = upper ? d0 - half : d0;
+        u.src = upper ? lane - half / 8 : lane + half / 8;
+        u.c = eight_of(load4(cs + at, true), load4(cs + at + 4, true));
+        u.s = eight_of(load4(sn + at, true), load4(sn + at + 4, true));
+        if (!upper) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) u.s.v[i] ^= 0x8000000080000000ull;
+            for (int i = 0; i < 4; ++i) u.s.v[i] ^= kSigns;
         }
     }
     return u;
 }
 
-// The other elements of the lane's pairs, as packed bf16.
-__device__ __forceinline__ uint4 partner(const uint4& v, const Turn& u, int interleaved) {
+// The other elements of the lane's pairs; `raw` the lane's elements as packed bf16, x unpacked.
+template <bool SPLIT>
+__device__ __forceinline__ Eight partner(const uint4& v, const Eight& x, const Turn& u, int interleaved) {
+    if (SPLIT) return {{x.v[2], x.v[3], x.v[0], x.v[1]}};
     if (interleaved)
-        return make_uint4(__byte_perm(v.x, 0, 0x1032), __byte_perm(v.y, 0, 0x1032), __byte_perm(v.z, 0, 0x1032),
-                          __byte_perm(v.w, 0, 0x1032));
-    return make_uint4(__shfl_sync(0xffffffffu, v.x, u.src), __shfl_sync(0xffffffffu, v.y, u.src),
-                      __shfl_sync(0xffffffffu, v.z, u.src), __shfl_sync(0xffffffffu, v.w, u.src));
+        return unpack(make_uint4(__byte_perm(v.x, 0, 0x1032), __byte_perm(v.y, 0, 0x1032),
+                                 __byte_perm(v.z, 0, 0x1032), __byte_perm(v.w, 0, 0x1032)));
+    return unpack(make_uint4(__shfl_sync(0xffffffffu, v.x, u.src), __shfl_sync(0xffffffffu, v.y, u.src),
+                             __shfl_sync(0xffffffffu, v.z, u.src), __shfl_sync(0xffffffffu, v.w, u.src)));
 }
 // w c and w' s' for the lane's elements, in place of c and s.
-template <int D>
+template <int D, bool SPLIT>
 __device__ __forceinline__ void fold_weight(Turn& u, const float* w, int lane, int interleaved) {
-    const bool wide = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
-    const Eight own = load8(w + 8 * (lane & (D / 8 - 1)), wide);
-    const Eight other = interleaved ? own : load8(w + 8 * (u.src & (D / 8 - 1)), wide);
+    const Eight own = load_weight<D, SPLIT>(w, lane & (D / 8 - 1));
+    const Eight other = SPLIT ? Eight{{own.v[2], own.v[3], own.v[0], own.v[1]}}
+                        : interleaved ? own : load_weight<D, SPLIT>(w, u.src & (D / 8 - 1));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         u.c.v[i] = mul2(u.c.v[i], own.v[i]);
         const float2 o = parts_of(other.v[i]);
-        u.s.v[i] = mul2(u.s.v[i], interleaved ? pair_of(o.y, o.x) : other.v[i]);
+        u.s.v[i] = mul2(u.s.v[i], !SPLIT && interleaved ? pair_of(o.y, o.x) : other.v[i]);
     }
+}
+__device__ __forceinline__ float inverse_root(float x) {
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 // Sum of the squares of a head vector in a fixed order, one rounding a step: 32
 // partial sums of every 32nd square, in their order, then a binary tree over
-// neighbouring partial sums.  Lanes that are D/32 lanes' worth of elements apart
-// hold a partial sum's terms; they exchange them so that each forms 32 / NL of
-// the partial sums.
-template <int NL>
+// neighbouring partial sums.  The lanes that hold a partial sum's terms exchange
+// them so that each forms its share of the partial sums.
+template <int NL, bool SPLIT>
 __device__ __forceinline__ float sum_squares_in_order(const float (&x)[8], int l) {
     float q[8], s;
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(x[i], x[i]);
-    if constexpr (NL == 8) {                              // lanes l, l ^ 4: four partial sums each, two terms
+    if constexpr (SPLIT && NL == 8) {                     // a lane has four partial sums
+        s = __fadd_rn(__fadd_rn(__fadd_rn(q[0], q[4]), __fadd_rn(q[1], q[5])),
+                      __fadd_rn(__fadd_rn(q[2], q[6]), __fadd_rn(q[3], q[7])));
+        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 1));
+        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 2));
+        return __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 4));
+    } else if constexpr (SPLIT) {                         // lanes l, l ^ 8: two partial sums each, two terms of four
+        const bool up = l & 8;
+        float p[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float a = __shfl_xor_sync(0xffffffffu, up ? q[i] : q[2 + i], 8);
+            const float b = __shfl_xor_sync(0xffffffffu, up ? q[4 + i] : q[6 + i], 8);
+            const float c = up ? q[2 + i] : q[i], d = up ? q[6 + i] : q[4 + i];
+            p[i] = __fadd_rn(__fadd_rn(__fadd_rn(up ? a : c, up ? c : a), up ? b : d), up ? d : b);
+        }
+        s = __fadd_rn(p[0], p[1]);
+        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 8));
+        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 1));
+        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 2));
+        return __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, 4));
+    } else if constexpr (NL == 8) {                       // lanes l, l ^ 4: four partial sums each, two terms
         const bool up = l & 4;
         float p[4];
 #pragma unroll
@@ -221,20 +284,20 @@ __device__ __forceinline__ float sum_squares_in_order(const float (&x)[8], int l
 // last bit: (x r) w, the two products of the rotation and their sum each round
 // once, and the sum of squares has a fixed order.  An evaluation of the formula
 // step by step in fp32 gives the same codes.
-template <int NL>
+template <int NL, bool SPLIT>
 __device__ __forceinline__ void norm_rope_in_order(float (&y)[8], const Eight& weight, const Turn& u, int lane,
                                                    const RopeParams& p) {
     float w[8], cs[8], sn[8];
     spread(weight, w);
     spread(u.c, cs);
     spread(u.s, sn);
-    const float mean = __fmul_rn(sum_squares_in_order<NL>(y, lane & (NL - 1)), 1.0f / (8 * NL));
-    const float r = rsqrtf(__fadd_rn(mean, p.eps));
+    const float mean = __fmul_rn(sum_squares_in_order<NL, SPLIT>(y, lane & (NL - 1)), 1.0f / (8 * NL));
+    const float r = inverse_root(__fadd_rn(mean, p.eps));
     float z[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(__fmul_rn(y[e], r), w[e]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) z[e] = p.interleaved ? y[e ^ 1] : __shfl_sync(0xffffffffu, y[e], u.src);
+    for (int e = 0; e < 8; ++e) z[e] = SPLIT ? y[e ^ 4] : p.interleaved ? y[e ^ 1] : __shfl_sync(0xffffffffu, y[e], u.src);
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = __fadd_rn(__fmul_rn(y[e], cs[e]), __fmul_rn(z[e], sn[e]));
 }
@@ -273,8 +336,8 @@ __device__ __forceinline__ Place find_slot(const Kv4Cache& c, int64_t slot, int 
     return r;
 }
 
-template <int D, int PASS>
-__global__ void __launch_bounds__(kThreads) forward_kernel(const ForwardArgs a) {
+template <int D, int PASS, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, PASS == kRope && SPLIT ? 4 : 3) forward_kernel(const ForwardArgs a) {
     constexpr int NL = D / 8, NV = 32 / NL, HR = heads_a_round<D>();
     const int lane = threadIdx.x & 31, l = lane & (NL - 1), sub = lane / NL;
     const int unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -291,75 +354,88 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const ForwardArgs a) 
         }
     }
     const HeadsIn& in = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-    int h0 = part * a.rounds * HR;                       // the round's first head
-    const int end = min(in.heads, h0 + a.rounds * HR);
-    const uint16_t* src = in.p + t * in.ts + (h0 + sub) * in.hs + 8 * l;
-    uint4 next[kUnroll];
-    auto load = [&](int h) {
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i)
-            next[i] = h + i * NV + sub < end ? *reinterpret_cast<const uint4*>(src + i * NV * in.hs)
-                                             : make_uint4(0u, 0u, 0u, 0u);
-        src += HR * in.hs;
-    };
-    load(h0);
-    Place place = {-1, 0};
-    if (PASS != kRope && kind > 0) place = find_slot(a.c, a.slots[t], lane, a.rope.err);
+    int h = part * a.rounds * HR + sub;                  // the lane's first head
+    const int end = min(in.heads, part * a.rounds * HR + a.rounds * HR);
     const bool turned = PASS != kAppend && kind < 2;
-    const bool in_order = PASS == kRopeCache && kind == 1;
+    const uint16_t* src = in.p + t * in.ts + h * in.hs;
+    if (PASS == kRope || (PASS == kRopeCache && kind == 0)) {
+        // ---- bf16 out ----
+        const HeadsOut& out = kind == 0 ? a.qo : a.ko;
+        uint16_t* dst = out.p + t * out.ts + h * out.hs;
+        Turn u;
+        bool ready = false;
+        for (; h - sub < end; h += HR) {
+            uint4 x[kUnroll];
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                x[i] = h + i * NV < end ? load_bf16<D, SPLIT>(src, l) : make_uint4(0u, 0u, 0u, 0u);
+                src += NV * in.hs;
+            }
+            if (!ready) {
+                u = load_turn<D, SPLIT>(a.rope, t, lane);
+                fold_weight<D, SPLIT>(u, kind == 0 ? a.rope.wq : a.rope.wk, lane, a.rope.interleaved);
+                ready = true;
+            }
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                Eight y = unpack(x[i]);
+                const Eight xp = partner<SPLIT>(x[i], y, u, a.rope.interleaved);
+                const float r = inverse_root(fmaf(group_sum<NL>(dot(y, y)), 1.0f / D, a.rope.eps));
+                const uint64_t rr = pair_of(r, r);
+                Eight z;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z.v[e] = mul2(rr, fma2(y.v[e], u.c.v[e], mul2(xp.v[e], u.s.v[e])));
+                if (h + i * NV < end) store_bf16<D, SPLIT>(dst, l, pack(z));
+                dst += NV * out.hs;
+            }
+        }
+        return;
+    }
+    // ---- into the cache: keys normalised and turned (or as they are), values as they are ----
+    const bool key = kind == 1;
+    const Place place = find_slot(a.c, a.slots[t], lane, a.rope.err);
     Turn u;
     Eight w;
     if (turned) {
-        u = load_turn<D>(a.rope, t, lane);
-        if (in_order)
-            w = load8(a.rope.wk + 8 * l, (reinterpret_cast<uintptr_t>(a.rope.wk) & 15) == 0);
-        else
-            fold_weight<D>(u, kind == 0 ? a.rope.wq : a.rope.wk, lane, a.rope.interleaved);
+        u = load_turn<D, SPLIT>(a.rope, t, lane);
+        w = load_weight<D, SPLIT>(a.rope.wk, l);
     }
-    const bool cached = PASS == kAppend || (PASS == kRopeCache && kind > 0);
-    const HeadsOut& out = kind == 0 ? a.qo : a.ko;
-    uint16_t* dst = cached ? nullptr : out.p + t * out.ts + (h0 + sub) * out.hs + 8 * l;
-    for (; h0 < end; h0 += HR) {
+    for (; h - sub < end; h += HR) {
         uint4 x[kUnroll];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) x[i] = next[i];
-        if (h0 + HR < end) load(h0 + HR);
+        for (int i = 0; i < kUnroll; ++i) {
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (h + i * NV < end) x[i] = turned ? load_bf16<D, SPLIT>(src, l) : load_bf16<D, false>(src, l);
+            src += NV * in.hs;
+        }
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-            if (h0 + i * NV >= end) break;               // the same for the whole warp
-            const int h = h0 + i * NV + sub;
-            Eight y = unpack(x[i]);
-            if (turned && !in_order) {
-                const Eight xp = unpack(partner(x[i], u, a.rope.interleaved));
-                const float r = rsqrtf(group_sum<NL>(dot(y, y)) * (1.0f / D) + a.rope.eps);
-                const uint64_t rr = pair_of(r, r);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y.v[e] = mul2(rr, fma2(y.v[e], u.c.v[e], mul2(xp.v[e], u.s.v[e])));
-            }
-            if (!cached) {
-                if (h < end) *reinterpret_cast<uint4*>(dst + i * NV * out.hs) = pack(y);
-            } else {
-                float z[8];
-                spread(y, z);
-                if (in_order) norm_rope_in_order<NL>(z, w, u, lane, a.rope);
-                uint32_t pair;
-                const uint32_t codes = kv4_quantise<NL>(z, pair);
-                const bool live = h < end && place.page >= 0;
-                const int64_t head = place.page * a.c.heads + h;
-                if (kind == 1) {
-                    if (live) {
-                        kv4_store_k(a.c.k + head * kv4_head_bytes(a.c.page, D) + (int64_t)place.at * (D / 2), l, codes);
-                        if (l == 0) a.c.kp[head * a.c.page + place.at] = pair;
+            if (h - sub + i * NV >= end) break;          // the same for the whole warp
+            float z[8];
+            spread(unpack(x[i]), z);
+            if (turned) norm_rope_in_order<NL, SPLIT>(z, w, u, lane, a.rope);
+            uint32_t pair;
+            const uint32_t codes = kv4_quantise<NL>(z, pair);
+            const bool live = h + i * NV < end && place.page >= 0;
+            const int64_t head = place.page * a.c.heads + h + i * NV;
+            if (key) {
+                if (live) {
+                    uint8_t* row = a.c.k + head * kv4_head_bytes(a.c.page, D) + (int64_t)place.at * (D / 2);
+                    if (turned && SPLIT) {               // elements 2i and 2i + 1 share byte i
+                        *reinterpret_cast<uint16_t*>(row + 2 * l) = (uint16_t)codes;
+                        *reinterpret_cast<uint16_t*>(row + D / 4 + 2 * l) = (uint16_t)(codes >> 16);
+                    } else {
+                        kv4_store_k(row, l, codes);
                     }
-                } else {
-                    kv4_store_v(live ? a.c.v + head * kv4_head_bytes(a.c.page, D) + (int64_t)(place.at >> 4) * (8 * D)
-                                     : nullptr,
-                                place.at & 15, l, codes);
-                    if (live && l == 0) a.c.vp[head * a.c.page + place.at] = pair;
+                    if (l == 0) a.c.kp[head * a.c.page + place.at] = pair;
                 }
+            } else {
+                kv4_store_v(live ? a.c.v + head * kv4_head_bytes(a.c.page, D) + (int64_t)(place.at >> 4) * (8 * D)
+                                 : nullptr,
+                            place.at & 15, l, codes);
+                if (live && l == 0) a.c.vp[head * a.c.page + place.at] = pair;
             }
         }
-        if (!cached) dst += HR * out.hs;
     }
 }
 
@@ -367,7 +443,7 @@ template <int D, int PASS>
 cudaError_t launch_forward(ForwardArgs a, cudaStream_t st) {
     constexpr int HR = heads_a_round<D>();
     auto warps = [&](int heads) { return (heads + a.rounds * HR - 1) / (a.rounds * HR); };
-    // Two rounds a warp share the token's set-up where that still leaves every SM its fill of warps.
+    // Several rounds a warp share the token's set-up where that still leaves every SM its fill of warps.
     for (a.rounds = kMaxRounds;; a.rounds /= 2) {
         a.nq = PASS == kAppend ? 0 : warps(a.q.heads);
         a.nk = warps(a.k.heads);
@@ -377,7 +453,10 @@ cudaError_t launch_forward(ForwardArgs a, cudaStream_t st) {
     }
     const int64_t blocks = (a.T * a.parts.d + kThreads / 32 - 1) / (kThreads / 32);
     if (blocks > INT32_MAX / (kThreads / 32)) return cudaErrorInvalidValue;
-    forward_kernel<D, PASS><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    if (PASS != kAppend && a.rope.rot == D && !a.rope.interleaved)
+        forward_kernel<D, PASS, PASS != kAppend><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    else
+        forward_kernel<D, PASS, false><<<(unsigned)blocks, kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
@@ -443,7 +522,7 @@ struct BackwardArgs {
 constexpr int kBwdThreads = 512;
 constexpr int kBwdUnroll = 4;
 
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const BackwardArgs a) {
     constexpr int NL = D / 8, NV = 32 / NL, HR = kBwdUnroll * NV, NW = kBwdThreads / 32;
     __shared__ __align__(16) float sums[NW * 128];       // the warps' sums [NW][D]; at the end four floats a thread
@@ -456,7 +535,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const Backward
         const HeadsOut& out = kind ? a.dk : a.dq;
         const FastDiv& parts = kind ? a.k_parts : a.q_parts;
         const float* wp = kind ? p.wk : p.wq;
-        const Eight w = load8(wp + 8 * l, (reinterpret_cast<uintptr_t>(wp) & 15) == 0);
+        const Eight w = load_weight<D, SPLIT>(wp, l);
         Eight dw = {{0, 0, 0, 0}};
         const int units = (int)p.T * parts.d, stride = gridDim.x * NW;
         // the last blocks take the key heads' first units, which their share of the query heads leaves room for
@@ -464,22 +543,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const Backward
         uint4 gn[kBwdUnroll], xn[kBwdUnroll];
         auto load = [&](int at) {
             const int t = at / parts, h0 = (at - t * parts.d) * HR + sub;
-            const uint16_t* gp = gin.p + t * gin.ts + h0 * gin.hs + 8 * l;
-            const uint16_t* xp = xin.p + t * xin.ts + h0 * xin.hs + 8 * l;
+            const uint16_t* gp = gin.p + t * gin.ts + h0 * gin.hs;
+            const uint16_t* xp = xin.p + t * xin.ts + h0 * xin.hs;
 #pragma unroll
             for (int i = 0; i < kBwdUnroll; ++i) {
                 gn[i] = xn[i] = make_uint4(0u, 0u, 0u, 0u);
                 if (h0 + i * NV < xin.heads) {
-                    gn[i] = *reinterpret_cast<const uint4*>(gp + i * NV * gin.hs);
-                    xn[i] = *reinterpret_cast<const uint4*>(xp + i * NV * xin.hs);
+                    gn[i] = load_bf16<D, SPLIT>(gp, l);
+                    xn[i] = load_bf16<D, SPLIT>(xp, l);
                 }
+                gp += NV * gin.hs;
+                xp += NV * xin.hs;
             }
         };
         if (unit < units) load(unit);
         for (; unit < units; unit += stride) {
             const int t = unit / parts, h0 = (unit - t * parts.d) * HR + sub;
-            const Turn u = load_turn<D>(p, t, lane);
-            uint16_t* dst = out.p + t * out.ts + h0 * out.hs + 8 * l;
+            const Turn u = load_turn<D, SPLIT>(p, t, lane);
+            uint16_t* dst = out.p + t * out.ts + h0 * out.hs;
             uint4 gv[kBwdUnroll], xv[kBwdUnroll];
 #pragma unroll
             for (int i = 0; i < kBwdUnroll; ++i) {
@@ -490,15 +571,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const Backward
 #pragma unroll
             for (int i = 0; i < kBwdUnroll; ++i) {
                 if (h0 - sub + i * NV >= xin.heads) break;               // the same for the whole warp
-                Eight g = unpack(gv[i]), wg;
-                const Eight gp = unpack(partner(gv[i], u, p.interleaved)), x = unpack(xv[i]);
+                const Eight dy = unpack(gv[i]), dp = partner<SPLIT>(gv[i], dy, u, p.interleaved), x = unpack(xv[i]);
+                Eight g, wg;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    g.v[e] = fma2(g.v[e], u.c.v[e], mul2(gp.v[e], u.s.v[e] ^ 0x8000000080000000ull));
+                    g.v[e] = fma2(dy.v[e], u.c.v[e], mul2(dp.v[e], u.s.v[e] ^ kSigns));
                     wg.v[e] = mul2(w.v[e], g.v[e]);
                 }
                 const float ss = group_sum<NL>(dot(x, x)), sg = group_sum<NL>(dot(wg, x));
-                const float r = rsqrtf(ss * (1.0f / D) + p.eps);
+                const float r = inverse_root(fmaf(ss, 1.0f / D, p.eps));
                 const float m = -r * r * r * sg * (1.0f / D);
                 const uint64_t rr = pair_of(r, r), mm = pair_of(m, m);
                 Eight y;
@@ -507,7 +588,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const Backward
                     dw.v[e] = fma2(g.v[e], mul2(x.v[e], rr), dw.v[e]);
                     y.v[e] = fma2(wg.v[e], rr, mul2(x.v[e], mm));
                 }
-                if (h0 + i * NV < xin.heads) *reinterpret_cast<uint4*>(dst + i * NV * out.hs) = pack(y);
+                if (h0 + i * NV < xin.heads) store_bf16<D, SPLIT>(dst, l, pack(y));
+                dst += NV * out.hs;
             }
         }
         // the block's sum: over the warp's NV vectors, then over the warps
@@ -517,7 +599,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const Backward
         for (int e = 0; e < 8; ++e) {
 #pragma unroll
             for (int o = NL; o < 32; o <<= 1) f[e] += __shfl_xor_sync(0xffffffffu, f[e], o);
-            if (sub == 0) sums[warp * D + 8 * l + e] = f[e];
+            if (sub == 0) sums[warp * D + (e < 4 ? first<D, SPLIT>(l) + e : second<D, SPLIT>(l) + e - 4)] = f[e];
         }
         __syncthreads();
         if (threadIdx.x < D) {
@@ -620,8 +702,10 @@ cudaError_t launch_qk_norm_rope_bwd(int D, const HeadsIn& dqo, const HeadsIn& dk
     if (units > INT32_MAX / 2) return cudaErrorInvalidValue;
     const int64_t want = (units + nw - 1) / nw, cap = qk_norm_rope_bwd_blocks(sms);
     const unsigned grid = (unsigned)(want < cap ? want : cap);
-    if (D == 64) backward_kernel<64><<<grid, kBwdThreads, 0, st>>>(a);
-    else backward_kernel<128><<<grid, kBwdThreads, 0, st>>>(a);
+    const bool split = p.rot == D && !p.interleaved;
+    auto kernel = D == 64 ? (split ? backward_kernel<64, true> : backward_kernel<64, false>)
+                          : (split ? backward_kernel<128, true> : backward_kernel<128, false>);
+    kernel<<<grid, kBwdThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
