@@ -132,8 +132,11 @@ struct Turn {
 };
 constexpr uint64_t kSigns = 0x8000000080000000ull;
 
+// (0 where nothing turns: pos may be NULL then)
+__device__ __forceinline__ int64_t load_pos(const RopeParams& p, int t) { return p.rot > 0 ? p.pos[t] : 0; }
+
 template <int D, bool SPLIT>
-__device__ __forceinline__ Turn load_turn(const RopeParams& p, int64_t t, int lane) {
+__device__ __forceinline__ Turn load_turn(const RopeParams& p, int64_t pos, int lane) {
     const int l = lane & (D / 8 - 1), d0 = 8 * l, half = p.rot / 2;
     Turn u;
     u.src = lane;
@@ -142,7 +145,6 @@ __device__ __forceinline__ Turn load_turn(const RopeParams& p, int64_t t, int la
         for (int i = 0; i < 4; ++i) u.c.v[i] = pair_of(1.0f, 1.0f), u.s.v[i] = 0;
         if (p.rot == 0) return u;
     }
-    const int64_t pos = p.pos[t];
     if (pos < 0 || pos >= p.npos) {
         if (lane == 0) record_error(p.err, kErrArg);
         const float nan = __int_as_float(0x7FC00000);
@@ -372,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, PASS == kRope && SPLIT ? 4 : 3) forw
                 src += NV * in.hs;
             }
             if (!ready) {
-                u = load_turn<D, SPLIT>(a.rope, t, lane);
+                u = load_turn<D, SPLIT>(a.rope, load_pos(a.rope, t), lane);
                 fold_weight<D, SPLIT>(u, kind == 0 ? a.rope.wq : a.rope.wk, lane, a.rope.interleaved);
                 ready = true;
             }
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, PASS == kRope && SPLIT ? 4 : 3) forw
     Turn u;
     Eight w;
     if (turned) {
-        u = load_turn<D, SPLIT>(a.rope, t, lane);
+        u = load_turn<D, SPLIT>(a.rope, load_pos(a.rope, t), lane);
         w = load_weight<D, SPLIT>(a.rope.wk, l);
     }
     for (; h - sub < end; h += HR) {
@@ -541,8 +543,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const Backward
         // the last blocks take the key heads' first units, which their share of the query heads leaves room for
         int unit = (kind ? gridDim.x - 1 - blockIdx.x : blockIdx.x) * NW + warp;
         uint4 gn[kBwdUnroll], xn[kBwdUnroll];
+        int64_t pos_next = 0;
         auto load = [&](int at) {
             const int t = at / parts, h0 = (at - t * parts.d) * HR + sub;
+            pos_next = load_pos(p, t);
             const uint16_t* gp = gin.p + t * gin.ts + h0 * gin.hs;
             const uint16_t* xp = xin.p + t * xin.ts + h0 * xin.hs;
 #pragma unroll
@@ -559,7 +563,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const Backward
         if (unit < units) load(unit);
         for (; unit < units; unit += stride) {
             const int t = unit / parts, h0 = (unit - t * parts.d) * HR + sub;
-            const Turn u = load_turn<D, SPLIT>(p, t, lane);
+            const int64_t pos = pos_next;
+            const Turn u = load_turn<D, SPLIT>(p, pos, lane);
             uint16_t* dst = out.p + t * out.ts + h0 * out.hs;
             uint4 gv[kBwdUnroll], xv[kBwdUnroll];
 #pragma unroll
