@@ -326,7 +326,7 @@ int r9q_kv4_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, c
     if (rc) return rc;
     if (!seq_lens || !o || (max_pages > 0 && !block_table)) return R9Q_ERR_NULL;
     if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4)) return R9Q_ERR_ALIGN;
-    if (!(scale > 0.0f) || std::isinf(scale) || max_pages * page > INT_MAX) return R9Q_ERR_ARG;
+    if (!(scale > 0.0f) || std::isinf(scale) || max_pages * page > 0x7FE00000) return R9Q_ERR_ARG;
     const int64_t rows = Lq * (Hq / Hk);
     const size_t need = decode_workspace(R9Q_OP_KV4_ATTENTION, rows, D, &rc);
     if (!workspace || workspace_bytes < need) return R9Q_ERR_WORKSPACE;

@@ -30,7 +30,7 @@
 // few items (sequence, kv head, row chunk) each is cut into equal parts, one a CTA;
 // with many, each CTA takes an equal, contiguous range of all items' groups (each item
 // counting some more for what it costs to begin), its ends moved to an item's end where
-// that is near.  The four warps of a CTA take 32-key
+// that is near.  The warps of a CTA take 32-key
 // steps of a part in turn, each with its own reference, and meet in shared memory at
 // its end.
 // An item that several CTAs share leaves fp32 partials; the CTA that arrives last
@@ -45,10 +45,8 @@ namespace r9q {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 32;                    // keys a warp takes at a time: two groups of 16
-constexpr int kMinGroups = 2 * kWarps;       // groups a CTA takes at least: one step for each warp
+constexpr int kStages = 4;                   // steps in a warp's ring
 constexpr int kItemCost = 24;                // groups that take as long as beginning and ending an item
 constexpr int kMinExponent = 67;             // value steps under 2^-60 count as that (keeps the sums finite)
 constexpr int kHeadroom = 8;                 // weights at the reference score are 2^8 to 2^9
@@ -56,38 +54,59 @@ constexpr int kSlack = 6;                    // powers of two a lane's weights m
 // A lowest value counts as a step of 2^-10 of it: the sums of p lv are kept in the weights' scale.
 constexpr int kLowestBits = 10;
 constexpr float kLowestShare = 1.0f / (1 << kLowestBits);
+constexpr int kNoWindow = 0x7FE00000;        // over any length (Lq is at most 2^20)
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr uint32_t kNoGroup = 0xFFFFFFFFu;
 
-constexpr int stages(int D) { return D == 64 ? 4 : 4; }
-constexpr int ctas_per_sm(int D, int NT) { return (D == 64 ? 4 : 3) - (NT - 1); }
-constexpr int stage_bytes(int D) { return kStep * D + kStep * 8; }
-constexpr int ring_bytes(int D) { return kWarps * stages(D) * stage_bytes(D); }
-constexpr int out_stride(int D) { return D + 4; }      // floats a row of the CTA's exchange takes
-constexpr int exchange_bytes(int D, int NT) { return kWarps * 8 * NT * (out_stride(D) + 2) * 4; }
+// Warps that an SM holds (registers), in CTAs of four, or, WIDE, in one.
+constexpr int sm_warps(int D, int NT) { return 4 * ((D == 64 ? 4 : 3) - (NT - 1)); }
+constexpr int cta_warps(int D, int NT, bool wide) { return wide ? sm_warps(D, NT) : 4; }
+constexpr int ctas_per_sm(int D, int NT, bool wide) { return sm_warps(D, NT) / cta_warps(D, NT, wide); }
 constexpr int kMaxSms = 160;                           // more are left idle
-// Joining n partials of R rows: [n][R] weights, [R] sums and references, then [n][R] sums, whose place the warps'
-// joined rows take (kThreads float4).
-constexpr int join_bytes(int D, int NT) {
-    const int n = kMaxSms * ctas_per_sm(D, NT) * 8 * NT * 4, meet = kThreads * 8 * NT * 16;
-    return n + 2 * 8 * NT * 4 + (n > meet ? n : meet);
-}
-constexpr int work_bytes(int D, int NT) {              // the rings, and after them the others in their place
-    int n = ring_bytes(D);
-    n = n > exchange_bytes(D, NT) ? n : exchange_bytes(D, NT);
-    return n > join_bytes(D, NT) ? n : join_bytes(D, NT);
+
+constexpr int stage_bytes(int D) { return kStep * D + kStep * 8; }
+constexpr int out_stride(int D) { return D + 4; }      // floats a row of the CTA's exchange takes
+constexpr int largest(int a, int b) { return a > b ? a : b; }
+// Shared memory: the rings, and in their place the warps' exchange [warps][R][out_stride] with references and sums,
+// and the joining of n partials of R rows: [n][R] weights, [R] sums and references, then [n][R] sums, whose place the
+// joined rows of the warps take (a float4 of every row a thread).
+constexpr int work_bytes(int D, int NT, bool wide) {
+    const int w = cta_warps(D, NT, wide), n = kMaxSms * ctas_per_sm(D, NT, wide) * 8 * NT * 4;
+    return largest(largest(w * kStages * stage_bytes(D), w * 8 * NT * (out_stride(D) + 2) * 4),
+                   n + 2 * 8 * NT * 4 + largest(n, w * 32 * 8 * NT * 16));
 }
 // What the threads of a CTA tell one another about its range.
 struct Shared {
-    long long scan[2][kWarps], first;
+    long long scan[3][16], first;
     int seq, last;
 };
-constexpr int smem_bytes(int D, int NT) { return work_bytes(D, NT) + (int)sizeof(Shared); }
+constexpr int smem_bytes(int D, int NT, bool wide) { return work_bytes(D, NT, wide) + (int)sizeof(Shared); }
 
-template <int N>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-    if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+// Copies a lane's share of one group of 16 tokens into a stage, if `live`: its two K rows' parts (8 rows apart), its
+// V pieces, and a (step, lowest) pair.
+template <int D>
+__device__ __forceinline__ void copy_group(bool live, uint32_t k_dst, const uint8_t* k, uint32_t v_dst,
+                                           const uint8_t* v, uint32_t pair_dst, const uint32_t* pair) {
+    if constexpr (D == 128) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
+            "@p cp.async.cg.shared.global [%1], [%2], 16;\n\t"
+            "@p cp.async.cg.shared.global [%1+512], [%2+512], 16;\n\t"
+            "@p cp.async.cg.shared.global [%3], [%4], 16;\n\t"
+            "@p cp.async.cg.shared.global [%3+512], [%4+512], 16;\n\t"
+            "@p cp.async.ca.shared.global [%5], [%6], 4;\n\t}" ::"r"((int)live),
+            "r"(k_dst), "l"(k), "r"(v_dst), "l"(v), "r"(pair_dst), "l"(pair)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
+            "@p cp.async.ca.shared.global [%1], [%2], 8;\n\t"
+            "@p cp.async.ca.shared.global [%1+256], [%2+256], 8;\n\t"
+            "@p cp.async.cg.shared.global [%3], [%4], 16;\n\t"
+            "@p cp.async.ca.shared.global [%5], [%6], 4;\n\t}" ::"r"((int)live),
+            "r"(k_dst), "l"(k), "r"(v_dst), "l"(v), "r"(pair_dst), "l"(pair)
+            : "memory");
+    }
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -146,7 +165,8 @@ __device__ __noinline__ Span span_of(const int32_t* at, int room, int reach, int
 }
 
 // The CTA's inclusive scan of one value a thread; `total` over all.
-__device__ __forceinline__ long long cta_scan(long long v, long long (&sums)[kWarps], long long& total) {
+template <int W>
+__device__ __noinline__ long long cta_scan(long long v, long long* sums, long long& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -157,7 +177,7 @@ __device__ __forceinline__ long long cta_scan(long long v, long long (&sums)[kWa
     __syncthreads();
     total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
         if (w < warp) v += sums[w];
         total += sums[w];
     }
@@ -178,12 +198,11 @@ template <int D, int NT>
 struct State {
     uint32_t qf[NT][D / 16][2];              // query fragments
     float fr[NT][2], qs[NT][2];              // score = fr (sk acc + lk qs)
-    int hi[NT][2], lo[NT][2];                // keys that the column sees: [lo, hi]
+    int hi[NT][2];                           // the last key that the column sees
     float acc[NT][D / 16][4], l[NT][2], ml[NT][2];
     // A weight is 2^((score - top) + shift) with the largest score and the values' exponent of the last move; taken
     // as a difference first, so that it holds for scores of any size.
-    float top[NT][2], shift[NT][2];          // (top over fr; both 0 while the column has seen no key)
-    int es[NT][2];                           // exponent field that stands for the column's values so far
+    float top[NT][2], shift[NT][2];          // (top over fr, 0 while the column has seen no key; shift 8 - exponent)
     float bound[NT][2], sv_bound;            // when to move: a lane's weights of a step, a step (or share of a lowest)
     uint32_t seen;                           // columns that have seen a key
 };
@@ -209,7 +228,7 @@ __device__ __forceinline__ void move_reference(State<D, NT>& s, const float (&sc
             const uint32_t bit = 1u << (2 * nt + c);
             float x = max3(max3(sc[nt][0][c], sc[nt][0][c + 2], sc[nt][1][c]), sc[nt][1][c + 2],
                            s.seen & bit ? s.top[nt][c] : kNegInf);
-            int e = s.es[nt][c];             // only of keys that the column sees
+            int e = kHeadroom + 127 - (int)s.shift[nt][c];     // only of keys that the column sees
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -222,15 +241,14 @@ __device__ __forceinline__ void move_reference(State<D, NT>& s, const float (&sc
             }
             float alpha = 0.0f;              // nothing seen before: the sums are zero
             s.bound[nt][c] = 0.0f;           // (nothing seen now either: no weight is over 0)
+            const float shift = (float)(kHeadroom + 127 - e);
             if (x > kNegInf) {
-                const float shift = (float)(kHeadroom + 127 - e);
                 if (s.seen & bit) alpha = ex2(fmaf(s.top[nt][c] - x, s.fr[nt][c], shift - s.shift[nt][c]));
                 s.seen |= bit;
                 s.top[nt][c] = x;
-                s.shift[nt][c] = shift;
                 s.bound[nt][c] = ex2(shift + kSlack);
             }
-            s.es[nt][c] = e;
+            s.shift[nt][c] = shift;
             es_min = min(es_min, e);
             s.l[nt][c] *= alpha;
             s.ml[nt][c] *= alpha;
@@ -246,7 +264,8 @@ __device__ __forceinline__ void move_reference(State<D, NT>& s, const float (&sc
 // One step: 32 keys in the stage `st`, of which groups `bits` were loaded.
 // MASKED: some column does not see some key, or a group is missing.
 template <int D, int NT, bool MASKED>
-__device__ __forceinline__ void attend(State<D, NT>& s, const uint8_t* st, int key0, uint32_t bits, int len, int lane) {
+__device__ __forceinline__ void attend(State<D, NT>& s, const uint8_t* st, int key0, uint32_t bits, int len,
+                                       int window, int lane) {
     constexpr int KW = D / 32;
     const int r = lane >> 2;
     // pairs of the lane's keys r + 8h of group i
@@ -298,7 +317,7 @@ __device__ __forceinline__ void attend(State<D, NT>& s, const uint8_t* st, int k
                 float v = fmaf(bf16_lo(pair), sc[nt][i][c], bf16_hi(pair) * s.qs[nt][c & 1]);
                 if (MASKED) {
                     const int key = key0 + 16 * i + 8 * (c >> 1) + r;
-                    if (key > s.hi[nt][c & 1] || key < s.lo[nt][c & 1] || !((bits >> i) & 1u)) v = kNegInf;
+                    if (key > s.hi[nt][c & 1] || key <= s.hi[nt][c & 1] - window || !((bits >> i) & 1u)) v = kNegInf;
                 }
                 sc[nt][i][c] = v;
             }
@@ -311,8 +330,7 @@ __device__ __forceinline__ void attend(State<D, NT>& s, const uint8_t* st, int k
                                    max3(fabsf(bf16_hi(vq[1][0])), fabsf(bf16_hi(vq[1][1])), 0.0f)) * kLowestShare);
     bool move = MASKED || sv_max > s.sv_bound;
     float pr[NT][2][4], sum[NT][2];
-#pragma unroll 1
-    for (int pass = 0;; ++pass) {
+    auto weigh = [&]() {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -326,8 +344,11 @@ __device__ __forceinline__ void attend(State<D, NT>& s, const uint8_t* st, int k
                 sum[nt][c] = (pr[nt][0][c] + pr[nt][0][c + 2]) + (pr[nt][1][c] + pr[nt][1][c + 2]);
                 move = move || sum[nt][c] > s.bound[nt][c];
             }
-        if (pass > 0 || !__any_sync(0xffffffffu, move)) break;
+    };
+    weigh();
+    if (__any_sync(0xffffffffu, move)) {
         move_reference<D, NT, MASKED>(s, sc, vq);
+        weigh();
     }
     uint32_t pf[NT][2][2];
 #pragma unroll
@@ -370,14 +391,17 @@ __device__ __forceinline__ void attend(State<D, NT>& s, const uint8_t* st, int k
     }
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_kernel(const Kv4AttnParams p) {
+template <int D, int NT, bool WIDE>
+__global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT, WIDE))
+    kv4_attention_kernel(const Kv4AttnParams p) {
+    constexpr int W = cta_warps(D, NT, WIDE), kThreads = 32 * W;
     constexpr int KW = D / 32;               // 32-bit words of a key that a lane holds
     constexpr int MT = D / 16;               // 16-element tiles
     constexpr int R = 8 * NT;                // rows of a chunk
-    constexpr int ST = stages(D);
+    constexpr int ST = kStages;
+    constexpr int kMinGroups = 2 * W;        // groups a CTA takes at least: one step for each warp
     extern __shared__ __align__(16) uint8_t smem[];
-    Shared& sh = *reinterpret_cast<Shared*>(smem + work_bytes(D, NT));
+    Shared& sh = *reinterpret_cast<Shared*>(smem + work_bytes(D, NT, WIDE));
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = lane >> 2, j = lane & 3;
@@ -395,17 +419,23 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
 #pragma unroll 1
     for (int b = b_first; b < b_end; ++b) mine += span(b).groups + begin_cost;
     mine *= items_per_seq;
-    long long upto = cta_scan(mine, sh.scan[0], total);
+    long long upto = cta_scan<W>(mine, sh.scan[0], total);
     long long per;                           // groups of a part, or of a CTA's range
     if (parted) {
-        // sum of ceil(groups / per) over the items is at most total / per + items <= ctas
-        per = (total + ctas - items - 1) / (ctas - items);
-        if (per < kMinGroups) per = kMinGroups;
-        mine = 0;                            // from here on: parts
+        // The even share, if parts of that size are no more than the CTAs; else total / (ctas - items): the sum of
+        // ceil(groups / per) over the items is at most total / per + items.
+        const long long all = total;
+        per = (all + ctas - 1) / ctas;
+        for (int attempt = 1;; ++attempt) {
+            if (per < kMinGroups) per = kMinGroups;
+            mine = 0;                        // from here on: parts
 #pragma unroll 1
-        for (int b = b_first; b < b_end; ++b) mine += (span(b).groups + (int)per - 1) / (int)per;
-        mine *= items_per_seq;
-        upto = cta_scan(mine, sh.scan[1], total);
+            for (int b = b_first; b < b_end; ++b) mine += (span(b).groups + (int)per - 1) / (int)per;
+            mine *= items_per_seq;
+            upto = cta_scan<W>(mine, sh.scan[attempt], total);
+            if (total <= ctas || attempt == 2) break;
+            per = (all + ctas - items - 1) / (ctas - items);
+        }
     } else {
         per = div64(total + ctas - 1, ctas);
         if (per < kMinGroups) per = kMinGroups;
@@ -502,12 +532,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
 
         // ---- the warp's steps ----
         const int steps_all = (g_end - g_begin + 1) >> 1;
-        const int steps = steps_all > warp ? (steps_all - warp + kWarps - 1) / kWarps : 0;
+        const int steps = steps_all > warp ? (steps_all - warp + W - 1) / W : 0;
         const int32_t* table = p.table + (int64_t)b * p.max_pages;
         const int gmax = min(g_end, (sp.len + 15) >> 4);
         // Lane x holds the cache's token index of the x-th group of the next 16 steps, and of the 16 after them.
         auto groups_of = [&](int first_step) {
-            const int g = g_begin + 2 * ((first_step + (lane >> 1)) * kWarps + warp) + (lane & 1);
+            const int g = g_begin + 2 * ((first_step + (lane >> 1)) * W + warp) + (lane & 1);
             uint32_t at = kNoGroup;
             if (g < gmax) {
                 const int pg = g / p.page_groups, page = table[pg];
@@ -580,9 +610,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
                 s.qs[nt][c] = __shfl_sync(0xffffffffu, row_qs, col * 4);
                 const int ci = min(chunk * R + nt * 8 + col, rows - 1) / p.group;
                 s.hi[nt][c] = sp.len - p.Lq + ci;
-                s.lo[nt][c] = p.window > 0 ? s.hi[nt][c] - p.window + 1 : 0;
-                s.top[nt][c] = s.shift[nt][c] = s.bound[nt][c] = s.l[nt][c] = s.ml[nt][c] = 0.0f;
-                s.es[nt][c] = kMinExponent;
+                s.top[nt][c] = s.bound[nt][c] = s.l[nt][c] = s.ml[nt][c] = 0.0f;
+                s.shift[nt][c] = (float)(kHeadroom + 127 - kMinExponent);
             }
 #pragma unroll
             for (int t = 0; t < MT; ++t)
@@ -593,6 +622,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
         const int i_first = chunk * R / p.group, i_last = (min(rows, chunk * R + R) - 1) / p.group;
         const int all_hi = sp.len - p.Lq + i_first, all_lo = p.window > 0 ? sp.len - p.Lq + i_last - p.window + 1 : 0;
 
+        const int window = p.window > 0 ? p.window : kNoWindow;
         uint32_t have = 0;                   // two bits a step in flight: which of its groups were loaded
         uint32_t put = ring_u;               // stage that is loaded next
         const uint8_t* get = ring;           // stage that is used next
@@ -612,38 +642,30 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const uint32_t at = __shfl_sync(0xffffffffu, groups_now, 2 * (ahead & 15) + i);
-                    if (at != kNoGroup) {
-                        have |= 1u << i;
-                        const uint8_t* ks = k_lane + (uint64_t)at * (D / 2);
-                        const uint8_t* vs = v_lane + (uint64_t)at * (D / 2);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            cp_async<KW * 4>(put + i * 16 * (D / 2) + h * 8 * (D / 2) + lane * (KW * 4),
-                                             ks + h * 8 * (D / 2));
-#pragma unroll
-                        for (int c = 0; c < D / 64; ++c)
-                            cp_async<16>(put + kStep * (D / 2) + i * 16 * (D / 2) + c * 512 + lane * 16, vs + c * 512);
-                        cp_async<4>(put + pair_dst + i * 8, pair_lane + at);
-                    }
+                    const bool live = at != kNoGroup;
+                    have |= live ? 1u << i : 0u;
+                    copy_group<D>(live, put + i * 16 * (D / 2) + lane * (KW * 4), k_lane + (uint64_t)at * (D / 2),
+                                  put + kStep * (D / 2) + i * 16 * (D / 2) + lane * 16, v_lane + (uint64_t)at * (D / 2),
+                                  put + pair_dst + i * 8, pair_lane + at);
                 }
                 put = put == ring_u + (ST - 1) * stage_bytes(D) ? ring_u : put + stage_bytes(D);
             }
             cp_commit();
             if (n < 0) continue;
-            const int key0 = (g_begin + 2 * (n * kWarps + warp)) << 4;
+            const int key0 = (g_begin + 2 * (n * W + warp)) << 4;
             if (bits == 3u && key0 >= all_lo && key0 + kStep - 1 <= all_hi)
-                attend<D, NT, false>(s, get, key0, bits, sp.len, lane);
+                attend<D, NT, false>(s, get, key0, bits, sp.len, window, lane);
             else
-                attend<D, NT, true>(s, get, key0, bits, sp.len, lane);
+                attend<D, NT, true>(s, get, key0, bits, sp.len, window, lane);
             get = get == ring + (ST - 1) * stage_bytes(D) ? ring : get + stage_bytes(D);
         }
         cp_wait<0>();
 
         // ---- the warps' sums meet ----
         __syncthreads();                     // the ring is free
-        float* ex_m = reinterpret_cast<float*>(smem);                  // [kWarps][R] references
-        float* ex_l = ex_m + kWarps * R;
-        float* ex_o = ex_l + kWarps * R;                               // [kWarps][R][out_stride]
+        float* ex_m = reinterpret_cast<float*>(smem);                  // [W][R] references
+        float* ex_l = ex_m + W * R;
+        float* ex_o = ex_l + W * R;                               // [W][R][out_stride]
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -689,10 +711,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
             float top = kNegInf, sum = 0.0f;
             float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ex_m[w * R + row]);
+            for (int w = 0; w < W; ++w) top = fmaxf(top, ex_m[w * R + row]);
             const float base = top > kNegInf ? top : 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < W; ++w) {
                 const float k = ex2(ex_m[w * R + row] - base);
                 const float4 v = *reinterpret_cast<const float4*>(ex_o + (w * R + row) * out_stride(D) + ed);
                 sum = fmaf(k, ex_l[w * R + row], sum);
@@ -731,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
                     sums[k] = k % R < live ? __ldcg(from + R) : 0.0f;
                 }
                 __syncthreads();
-                for (int row = warp; row < R; row += kWarps) {
+                for (int row = warp; row < R; row += W) {
                     float top = kNegInf, sum = 0.0f;
                     for (int c = lane; c < n; c += 32) top = fmaxf(top, wt[c * R + row]);
 #pragma unroll
@@ -788,21 +810,34 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) kv4_attention_ke
 int used_sms(int sms) { return sms < kMaxSms ? sms : kMaxSms; }
 int row_tiles(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
+template <int D, int NT, bool WIDE>
+cudaError_t launch(const Kv4AttnParams& p, int sms, cudaStream_t st) {
+    const void* kernel = reinterpret_cast<const void*>(kv4_attention_kernel<D, NT, WIDE>);
+    cudaError_t e = ensure_dynamic_smem(kernel, smem_bytes(D, NT, WIDE));
+    if (e != cudaSuccess) return e;
+    kv4_attention_kernel<D, NT, WIDE>
+        <<<used_sms(sms) * ctas_per_sm(D, NT, WIDE), 32 * cta_warps(D, NT, WIDE), smem_bytes(D, NT, WIDE), st>>>(p);
+    return cudaGetLastError();
+}
+
 template <int D, int NT>
 cudaError_t launch(Kv4AttnParams p, int sms, cudaStream_t st) {
-    const int rows = p.Lq * p.G;
-    p.chunks = fast_div((rows + 8 * NT - 1) / (8 * NT));
+    p.chunks = fast_div((p.Lq * p.G + 8 * NT - 1) / (8 * NT));
     p.group = fast_div(p.G);
     p.page_groups = fast_div(p.c.page / 16);
-    cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kv4_attention_kernel<D, NT>), smem_bytes(D, NT));
-    if (e != cudaSuccess) return e;
-    kv4_attention_kernel<D, NT><<<used_sms(sms) * ctas_per_sm(D, NT), kThreads, smem_bytes(D, NT), st>>>(p);
-    return cudaGetLastError();
+    // Few long items: one CTA an SM leaves a third as many partials to join.  Many items, or ones too short to give
+    // such a CTA's warps two steps each: more and smaller CTAs.
+    const int64_t items = (int64_t)p.B * p.c.heads * p.chunks.d, ctas = used_sms(sms);
+    const bool wide = 8 * items <= ctas && items * (p.room / 16) >= ctas * 4 * cta_warps(D, NT, true);
+    return wide ? launch<D, NT, true>(p, sms, st) : launch<D, NT, false>(p, sms, st);
 }
 
 }  // namespace
 
-int kv4_attention_ctas(int D, int64_t rows, int sms) { return used_sms(sms) * ctas_per_sm(D, row_tiles(rows)); }
+// (of the launch with more of them)
+int kv4_attention_ctas(int D, int64_t rows, int sms) {
+    return used_sms(sms) * ctas_per_sm(D, row_tiles(rows), false);
+}
 
 size_t kv4_attention_part_floats(int D, int64_t rows, int sms) {
     return (size_t)kv4_attention_ctas(D, rows, sms) * 2 * (8 * row_tiles(rows)) * (D + 2);
