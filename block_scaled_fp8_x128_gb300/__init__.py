@@ -2,7 +2,8 @@
 
 Argument marshalling only: each function takes torch tensors, checks dtype,
 shape and device, and calls the C entry point of the same name in
-``include/r9q.h`` on the current CUDA stream.  Every step of the computation
+``include/r9q.h`` on the current CUDA stream, through ctypes or, for the
+attention block's calls, through ``_calls.so``.  Every step of the computation
 runs in the library's CUDA kernels; there is no fallback.  Importing this
 package raises if ``libr9q.so`` has not been built (``build.py``).
 """
@@ -21,6 +22,8 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"libr9q.so not built at {LIB_PATH}; run block_scaled_fp8_x128_gb300/build.py")
 
 _lib = ctypes.CDLL(LIB_PATH)
+
+from . import _calls  # noqa: E402  (built beside libr9q.so, which it needs)
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -63,6 +66,7 @@ for _name, (_args, _res) in _SIGS.items():
 
 EXPORTED = tuple(_SIGS)
 
+R9Q_ERR_WORKSPACE = -4
 R9Q_ERR_TIMEOUT = -6
 R9Q_GROUPED_WEIGHT_ONLY = 1
 R9Q_GROUPED_SWIGLU = 2
@@ -362,74 +366,35 @@ def r9q_kv4_cache(pages: int, heads: int, page: int, dim: int, device=None) -> K
     return KV4Cache(k, kp, torch.zeros_like(k), torch.zeros_like(kp))
 
 
-# These calls last microseconds on the GPU, so their checks are kept short: one look at a
-# tensor that is as it should be, and the reason only when it is not.
-_BF16, _F32, _I32T, _I64T, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+# These calls last microseconds on the GPU: _calls (csrc/r9q_calls.cpp) checks their tensors and makes the C call.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream_handle(device_index, stream):
-    """The handle of `stream`, or of the current stream."""
+def _stream_handle(index, stream):
+    """The handle of `stream`, or of the current stream of the device `index`."""
     if stream is not None:
         return stream.cuda_stream
-    return _raw_stream(device_index) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+    if index is None:
+        raise ValueError("tensor must be on a CUDA device")
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
 
 
-def _refuse(t, dtype, shape, name):
-    _expect(t, dtype, shape, name)
-    _ptr(t)
-    raise ValueError(f"{name}: the last dimension must be contiguous")
+def _checked(r, where):
+    """The outputs of a call, or its code raised."""
+    if r.__class__ is int:
+        _check(r, where)
+    return r
 
 
-def _at(t, dtype, shape, name):
-    """The address of a contiguous device tensor of this type and shape."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
-    return _refuse(t, dtype, shape, name)
-
-
-def _heads(t, shape, name):
-    """(address, token stride, head stride) of a bf16 [T][H][D] device tensor with contiguous vectors."""
-    ts, hs, es = t.stride()
-    if t.dtype is _BF16 and t.shape == shape and t.is_cuda and es == 1:
-        return t.data_ptr(), ts, hs
-    return _refuse(t, _BF16, shape, name)
-
-
-def _cache_at(cache, heads, dim):
-    """The addresses of the cache's parts, its pages and their tokens."""
-    k, kp, v, vp = cache
-    pages, _, page, _ = k.shape
-    codes, pairs = (pages, heads, page, dim // 2), (pages, heads, page, 2)
-    return (_at(k, _U8, codes, "cache.k"), _at(kp, _BF16, pairs, "cache.kp"), _at(v, _U8, codes, "cache.v"),
-            _at(vp, _BF16, pairs, "cache.vp")), pages, page
-
-
-def _rope_at(wq, wk, cos, sin, positions, T, D):
-    """The addresses of the weights, tables and positions, rot and the tables' rows."""
-    w = _at(wq, _F32, (D,), "wq"), _at(wk, _F32, (D,), "wk")
-    if cos is None:
-        return (*w, None, None, None), 0, 0
-    npos, half = table = cos.shape
-    return (*w, _at(cos, _F32, table, "cos"), _at(sin, _F32, table, "sin"),
-            _at(positions, _I64T, (T,), "positions")), 2 * half, npos
-
-
-_WS_BYTES: dict = {}
-
-
-def _op_workspace(op, M, N, workspace, device, handle, stream):
-    """(address, bytes) of the caller's workspace, or of the stream's own."""
-    if workspace is None:
-        key = (op, M, N, device.index)
-        need = _WS_BYTES.get(key)
-        if need is None:
-            need = _WS_BYTES[key] = r9q_workspace_bytes(op, M, N, 0)
-        workspace = _WORKSPACES.get((device.index, handle))
-        if workspace is None or workspace.numel() < need:
-            workspace = _stream_workspace(need, device, stream)
-        return workspace.data_ptr(), workspace.numel()
-    return _ptr(workspace), workspace.numel() * workspace.element_size()
+def _with_workspace(where, op, M, N, call, args, workspace, device, stream):
+    """A call that needs a workspace: the caller's, or the stream's own, made or grown where that does not do."""
+    handle = _stream_handle(device.index, stream)
+    own = workspace if workspace is not None else _WORKSPACES.get((device.index, handle))
+    r = call(*args, own, handle)
+    if workspace is None and r.__class__ is int and r == R9Q_ERR_WORKSPACE:
+        own = _stream_workspace(r9q_workspace_bytes(op, M, N, 0), device, stream)
+        r = call(*args, own, handle)
+    return _checked(r, where)
 
 
 def r9q_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, wq: torch.Tensor, wk: torch.Tensor,
@@ -438,22 +403,8 @@ def r9q_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, wq: torch.Tensor, wk: tor
                      q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
     """RMS norm of the heads of q bf16 [T][Hq][D] and k bf16 [T][Hk][D] (any token and head strides) and the
     rotation by cos, sin fp32 [npos][rot/2] at positions int64 [T] (None: norm only); returns (q_out, k_out)."""
-    T, Hq, D = qs = q.shape
-    _, Hk, _ = ks = k.shape
-    if ks != (T, Hk, D):
-        raise ValueError(f"k: expected shape {(T, Hk, D)}, got {tuple(ks)}")
-    rope, rot, npos = _rope_at(wq, wk, cos, sin, positions, T, D)
-    device = q.device
-    if q_out is None:
-        q_out = torch.empty(qs, dtype=_BF16, device=device)
-    if k_out is None:
-        k_out = torch.empty(ks, dtype=_BF16, device=device)
-    rc = _lib.r9q_qk_norm_rope(*_heads(q, qs, "q"), *_heads(k, ks, "k"), *rope, *_heads(q_out, qs, "q_out"),
-                               *_heads(k_out, ks, "k_out"), T, Hq, Hk, D, rot, npos, eps, 1 if interleaved else 0,
-                               _stream_handle(device.index, stream))
-    if rc:
-        _check(rc, "r9q_qk_norm_rope")
-    return q_out, k_out
+    return _checked(_calls.qk_norm_rope(q, k, wq, wk, cos, sin, positions, eps, interleaved, q_out, k_out,
+                                        _stream_handle(q.device.index, stream)), "r9q_qk_norm_rope")
 
 
 def r9q_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
@@ -464,29 +415,9 @@ def r9q_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Te
                          workspace: torch.Tensor | None = None, stream=None):
     """The gradient of r9q_qk_norm_rope; returns (dq, dk, dwq, dwk).  workspace: as for r9q_gemm_fp8_block_qa
     (zero-filled before its first use; omitted: the stream's own)."""
-    T, Hq, D = qs = q.shape
-    _, Hk, _ = ks = k.shape
-    if ks != (T, Hk, D):
-        raise ValueError(f"k: expected shape {(T, Hk, D)}, got {tuple(ks)}")
-    rope, rot, npos = _rope_at(wq, wk, cos, sin, positions, T, D)
-    device = q.device
-    if dq is None:
-        dq = torch.empty(qs, dtype=_BF16, device=device)
-    if dk is None:
-        dk = torch.empty(ks, dtype=_BF16, device=device)
-    if dwq is None:
-        dwq = torch.empty(D, dtype=_F32, device=device)
-    if dwk is None:
-        dwk = torch.empty(D, dtype=_F32, device=device)
-    handle = _stream_handle(device.index, stream)
-    ws, wsb = _op_workspace(R9Q_OP_QK_NORM_ROPE_BWD, 1, D, workspace, device, handle, stream)
-    rc = _lib.r9q_qk_norm_rope_bwd(*_heads(dq_out, qs, "dq_out"), *_heads(dk_out, ks, "dk_out"), *_heads(q, qs, "q"),
-                                   *_heads(k, ks, "k"), *rope, *_heads(dq, qs, "dq"), *_heads(dk, ks, "dk"),
-                                   _at(dwq, _F32, (D,), "dwq"), _at(dwk, _F32, (D,), "dwk"), T, Hq, Hk, D, rot, npos,
-                                   eps, 1 if interleaved else 0, ws, wsb, handle)
-    if rc:
-        _check(rc, "r9q_qk_norm_rope_bwd")
-    return dq, dk, dwq, dwk
+    return _with_workspace("r9q_qk_norm_rope_bwd", R9Q_OP_QK_NORM_ROPE_BWD, 1, q.shape[-1], _calls.qk_norm_rope_bwd,
+                           (dq_out, dk_out, q, k, wq, wk, cos, sin, positions, eps, interleaved, dq, dk, dwq, dwk),
+                           workspace, q.device, stream)
 
 
 def r9q_qk_norm_rope_kv4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, wq: torch.Tensor, wk: torch.Tensor,
@@ -495,52 +426,20 @@ def r9q_qk_norm_rope_kv4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, wq: 
                          q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """r9q_qk_norm_rope with the keys, and v bf16 [T][Hk][D] as it is, written to the cache at slots int64 [T]
     (page * tokens of a page + place; negative: padding); returns q_out."""
-    T, Hq, D = qs = q.shape
-    _, Hk, _ = ks = k.shape
-    if ks != (T, Hk, D):
-        raise ValueError(f"k: expected shape {(T, Hk, D)}, got {tuple(ks)}")
-    rope, rot, npos = _rope_at(wq, wk, cos, sin, positions, T, D)
-    parts, pages, page = _cache_at(cache, Hk, D)
-    device = q.device
-    if q_out is None:
-        q_out = torch.empty(qs, dtype=_BF16, device=device)
-    rc = _lib.r9q_qk_norm_rope_kv4(*_heads(q, qs, "q"), *_heads(k, ks, "k"), *_heads(v, ks, "v"), *rope,
-                                   *_heads(q_out, qs, "q_out"), *parts, _at(slots, _I64T, (T,), "slots"), T, Hq, Hk, D,
-                                   rot, npos, pages, page, eps, 1 if interleaved else 0,
-                                   _stream_handle(device.index, stream))
-    if rc:
-        _check(rc, "r9q_qk_norm_rope_kv4")
-    return q_out
+    return _checked(_calls.qk_norm_rope_kv4(q, k, v, wq, wk, cos, sin, positions, *cache, slots, eps, interleaved, q_out,
+                                            _stream_handle(q.device.index, stream)), "r9q_qk_norm_rope_kv4")
 
 
 def r9q_kv4_append(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, slots: torch.Tensor, stream=None) -> None:
     """Writes k and v bf16 [T][Hk][D] to the cache at slots int64 [T] (negative: padding)."""
-    T, Hk, D = ks = k.shape
-    parts, pages, page = _cache_at(cache, Hk, D)
-    rc = _lib.r9q_kv4_append(*_heads(k, ks, "k"), *_heads(v, ks, "v"), *parts, _at(slots, _I64T, (T,), "slots"), T, Hk,
-                             D, pages, page, _stream_handle(k.device.index, stream))
-    if rc:
-        _check(rc, "r9q_kv4_append")
+    _checked(_calls.kv4_append(k, v, *cache, slots, _stream_handle(k.device.index, stream)), "r9q_kv4_append")
 
 
 def r9q_kv4_gather(cache: KV4Cache, slots: torch.Tensor, k: torch.Tensor | None = None,
                    v: torch.Tensor | None = None, stream=None):
     """The tokens at slots int64 [T] as bf16 (k, v) [T][Hk][D]; zeros for padding."""
-    T, = slots.shape
-    _, Hk, _, half = cache.k.shape
-    shape = (T, Hk, 2 * half)
-    parts, pages, page = _cache_at(cache, Hk, 2 * half)
-    device = slots.device
-    if k is None:
-        k = torch.empty(shape, dtype=_BF16, device=device)
-    if v is None:
-        v = torch.empty(shape, dtype=_BF16, device=device)
-    rc = _lib.r9q_kv4_gather(*parts, _at(slots, _I64T, (T,), "slots"), T, Hk, 2 * half, pages, page,
-                             _at(k, _BF16, shape, "k"), _at(v, _BF16, shape, "v"),
-                             _stream_handle(device.index, stream))
-    if rc:
-        _check(rc, "r9q_kv4_gather")
-    return k, v
+    return _checked(_calls.kv4_gather(*cache, slots, k, v, _stream_handle(slots.device.index, stream)),
+                    "r9q_kv4_gather")
 
 
 def r9q_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -551,27 +450,8 @@ def r9q_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tenso
     over the cache: block_table int32 [B][max_pages], seq_lens int32 [B] (new tokens included).  scale: 1/sqrt(D) by
     default.  Returns o bf16 [B][Lq][Hq][D], or (o, lse fp32 [B][Lq][Hq]) with return_lse.  workspace: as for
     r9q_gemm_fp8_block_qa (zero-filled before its first use; omitted: the stream's own)."""
-    B, Lq, Hq, D = qs = q.shape
-    bs, ts, hs, es = q.stride()
-    Hk = cache.k.shape[1]
-    parts, pages, page = _cache_at(cache, Hk, D)
-    if not (q.dtype is _BF16 and q.is_cuda and es == 1):
-        _refuse(q, _BF16, qs, "q")
-    if Hk < 1 or Hq % Hk:
-        raise ValueError("q's heads must be a multiple of the cache's")
-    max_pages = block_table.shape[1]
-    device = q.device
-    if out is None:
-        out = torch.empty(qs, dtype=_BF16, device=device)
-    if lse is None and return_lse:
-        lse = torch.empty((B, Lq, Hq), dtype=_F32, device=device)
-    handle = _stream_handle(device.index, stream)
-    ws, wsb = _op_workspace(R9Q_OP_KV4_ATTENTION, max(1, Lq * Hq // Hk), D, workspace, device, handle, stream)
-    rc = _lib.r9q_kv4_attention(q.data_ptr(), bs, ts, hs, *parts,
-                                _at(block_table, _I32T, (B, max_pages), "block_table"),
-                                _at(seq_lens, _I32T, (B,), "seq_lens"), _at(out, _BF16, qs, "out"),
-                                None if lse is None else _at(lse, _F32, (B, Lq, Hq), "lse"), B, Lq, Hq, Hk, D, pages,
-                                page, max_pages, window, D ** -0.5 if scale is None else scale, ws, wsb, handle)
-    if rc:
-        _check(rc, "r9q_kv4_attention")
-    return (out, lse) if return_lse else out
+    _, Lq, Hq, D = q.shape
+    return _with_workspace("r9q_kv4_attention", R9Q_OP_KV4_ATTENTION, max(1, Lq * Hq // max(1, cache.k.shape[1])), D,
+                           _calls.kv4_attention,
+                           (q, *cache, block_table, seq_lens, scale, window, out, lse, return_lse), workspace, q.device,
+                           stream)

@@ -1,18 +1,22 @@
 """Builds libr9q.so in-tree: every CUDA translation unit compiled for sm_103a in
 parallel with nvcc, then linked into one shared library (static cudart, no
 libcuda link: the tensor-map encoder is fetched through the runtime's driver
-entry-point query)."""
+entry-point query).  Beside it _calls.so, the Python side of the calls that last
+microseconds (host C++, against the installed torch)."""
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libr9q.so")
+CALLS = os.path.join(PKG, "_calls.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 NVCC_FLAGS = [
@@ -41,6 +45,23 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_dir() -> str:
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def _calls_compile(src: str, obj: str) -> list[str]:
+    include = os.path.join(_torch_dir(), "include")
+    paths = [include, os.path.join(include, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
+             os.path.join(ROOT, "include")]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", *(f"-I{p}" for p in paths), "-c", src, "-o", obj]
+
+
+def _calls_link(obj: str, out: str) -> list[str]:
+    """It finds libr9q.so beside itself; torch's libraries are those that are loaded."""
+    return ["g++", "-shared", obj, "-o", out, f"-L{PKG}", "-lr9q", f"-L{os.path.join(_torch_dir(), 'lib')}",
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     """Compile (if stale) and return the path of libr9q.so."""
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -57,6 +78,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             if verbose_ptxas:
                 cmd[1:1] = ["-Xptxas", "-v"]
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    calls_src, calls_obj = os.path.join(CSRC, "r9q_calls.cpp"), os.path.join(BUILD_DIR, "r9q_calls.o")
+    if force or _stale(calls_obj, [calls_src, *headers]):
+        procs.append((calls_src, subprocess.Popen(_calls_compile(calls_src, calls_obj), stdout=subprocess.PIPE,
+                                                  stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -67,12 +92,16 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             sys.stderr.write(text)
     if failed:
         msg = "\n".join(f"--- {s}\n{t}" for s, t in failed)
-        raise RuntimeError("nvcc failed:\n" + msg)
+        raise RuntimeError("compilation failed:\n" + msg)
     if force or _stale(LIB, objs):
         tmp = LIB + ".tmp.%d" % os.getpid()
         cmd = [nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-shared", "-o", tmp, *objs]
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
+    if force or _stale(CALLS, [calls_obj]):
+        tmp = CALLS + ".tmp.%d" % os.getpid()
+        subprocess.run(_calls_link(calls_obj, tmp), check=True)
+        os.replace(tmp, CALLS)
     return LIB
 
 
