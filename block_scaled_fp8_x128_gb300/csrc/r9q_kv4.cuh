@@ -40,6 +40,67 @@ __host__ __device__ __forceinline__ int64_t kv4_head_bytes(int page, int D) { re
 // Byte of token t (0..15) inside a group's [j][m][b] block, m = 0.
 __device__ __forceinline__ int kv4_v_token_byte(int t) { return ((t & 7) >> 1) * 16 + 2 * (t & 1) + (t >> 3); }
 
+// ---- packed pairs of fp32 ----
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 parts_of(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// Eight elements as four pairs.
+struct Eight {
+    uint64_t v[4];
+};
+__device__ __forceinline__ Eight unpack(const uint4& q) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    Eight r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.v[i] = pair_of(bf16_lo(w[i]), bf16_hi(w[i]));
+    return r;
+}
+__device__ __forceinline__ uint4 pack(const Eight& x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = parts_of(x.v[i]);
+        w[i] = pack_bf16x2(f.x, f.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float dot(const Eight& a, const Eight& b) {
+    uint64_t s = mul2(a.v[0], b.v[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) s = fma2(a.v[i], b.v[i], s);
+    const float2 f = parts_of(s);
+    return f.x + f.y;
+}
+__device__ __forceinline__ void spread(const Eight& x, float (&y)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = parts_of(x.v[i]);
+        y[2 * i] = f.x;
+        y[2 * i + 1] = f.y;
+    }
+}
 // Reductions over the NL lanes that hold one head vector.
 template <int NL>
 __device__ __forceinline__ float group_sum(float v) {
@@ -66,12 +127,14 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 // 16-bit pair keeps the cost at 4 bytes a vector, and codes are taken against
 // the rounded pair, so its rounding only moves the grid by a fraction of a
 // step); code = clamp(rint((x - lowest) / step), 0, 15) with the IEEE fp32
-// quotient (quot_exact, or the division where the step is tiny).  A constant
+// quotient.  A constant
 // vector has step 0 and codes 0.  A vector with a NaN or an infinity, or a range
 // over fp32's, gets a NaN pair: it reads back as NaN.  Returns the lane's 8
 // codes, element i in bits 4i..4i+3.
 template <int NL>
-__device__ __forceinline__ uint32_t kv4_quantise(const float (&x)[8], uint32_t& pair) {
+__device__ __forceinline__ uint32_t kv4_quantise(const Eight& v, uint32_t& pair) {
+    float x[8];
+    spread(v, x);
     float hi = max3_nan(max3_nan(max3_nan(x[0], x[1], x[2]), x[3], x[4]), max3_nan(x[5], x[6], x[7]), x[0]);
     float lo = max3_nan(max3_nan(max3_nan(-x[0], -x[1], -x[2]), -x[3], -x[4]), max3_nan(-x[5], -x[6], -x[7]), -x[0]);
 #pragma unroll
@@ -82,22 +145,28 @@ __device__ __forceinline__ uint32_t kv4_quantise(const float (&x)[8], uint32_t& 
     }
     lo = -lo;
     const float range = hi - lo;
-    if (!(range < __int_as_float(0x7F800000))) {         // a NaN, an infinity, or no range that fp32 holds
-        pair = 0x7FC07FC0u;
-        return 0u;
-    }
-    const float low = bf16_round(lo), step = bf16_round(__fmul_rn(range, 1.0f / 15.0f));
+    float low = bf16_round(lo), step = bf16_round(__fmul_rn(range, 1.0f / 15.0f));
     pair = pack_bf16x2(step, low);
-    if (!(step > 0.0f)) return 0u;
+    if (!(range < __int_as_float(0x7F800000))) pair = 0x7FC07FC0u;   // a NaN, an infinity, or no range that fp32 holds
+    // The quotient by quot_exact's steps, two at a time (low - x instead of x - low: the same, negated).  A step that
+    // is too small for it is taken 2^100 times as large, and so are the differences: both exactly.
+    const float up = step < kQuotExactMinScale ? 0x1p100f : 1.0f;
+    step *= up;
+    const float r = step > 0.0f ? __frcp_rn(step) : 0.0f;             // step 0: all codes 0
+    const uint64_t one = pair_of(-1.0f, -1.0f), low2 = pair_of(low, low), step2 = pair_of(step, step),
+                   up2 = pair_of(up, up), minus_r = pair_of(-r, -r), magic = pair_of(8388608.0f, 8388608.0f),
+                   back = pair_of(-8388608.0f, -8388608.0f);
     float q[8];
-    const bool small = step < kQuotExactMinScale;
-    const float r = __frcp_rn(step);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float d = x[i] - low;
-        const float t = small ? __fdiv_rn(d, step) : quot_exact(d, step, r);
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t d = mul2(fma2(v.v[i], one, low2), up2);        // low - x
+        const uint64_t y = mul2(d, minus_r), e = fma2(step2, y, d);
+        const float2 f = parts_of(fma2(e, minus_r, y));
         // 2^23 + t rounds t to the nearest even integer
-        q[i] = __fadd_rn(__fadd_rn(fminf(fmaxf(t, 0.0f), 15.0f), 8388608.0f), -8388608.0f);
+        const uint64_t k = pair_of(fminf(fmaxf(f.x, 0.0f), 15.0f), fminf(fmaxf(f.y, 0.0f), 15.0f));
+        const float2 g = parts_of(add2(add2(k, magic), back));
+        q[2 * i] = g.x;
+        q[2 * i + 1] = g.y;
     }
     // four codes make an integer below 2^16, exactly; adding 2^23 leaves it in the low bits
     const float a = fmaf(fmaf(fmaf(q[3], 16.0f, q[2]), 16.0f, q[1]), 16.0f, q[0]) + 8388608.0f;
@@ -120,6 +189,78 @@ __device__ __forceinline__ void kv4_store_v(uint8_t* group, int t, int l, uint32
 #pragma unroll
     for (int i = 0; i < 4; ++i)                                  // r = 4 odd + i
         p[i * 64] = (uint8_t)(((lo >> (4 * i)) & 15u) | (((hi >> (4 * i)) & 15u) << 4));
+}
+
+// ---- a whole group of 16 tokens of one head, two tokens (or more) a round ----
+// With NV = 32 / NL tokens at a time, round i holds token NV i + sub in the lanes sub NL .. sub NL + NL - 1.
+// Lane (sub, l): bytes r = 4 odd .. 4 odd + 3 (odd = l & 1) of element tile m = l >> 1 of every token it holds.
+
+// Four nibbles to the low nibbles of four bytes.
+__device__ __forceinline__ uint32_t nibbles_to_bytes(uint32_t n) {
+    n = (n | (n << 8)) & 0x00FF00FFu;
+    return (n | (n << 4)) & 0x0F0F0F0Fu;
+}
+__device__ __forceinline__ uint32_t bytes_to_nibbles(uint32_t b) {       // (bits 4..7 of each are 0)
+    b = (b | (b >> 4)) & 0x00FF00FFu;
+    return (b | (b >> 8)) & 0x0000FFFFu;
+}
+// The lane's four bytes of a token's element tile, from the tokens' codes (lane l: elements 8l .. 8l+7), and back.
+__device__ __forceinline__ uint32_t kv4_tile_bytes(uint32_t codes, int l) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, codes, 1);
+    const int odd = l & 1;
+    const uint32_t lo = (odd ? other : codes) >> (16 * odd), hi = (odd ? codes : other) >> (16 * odd);
+    return nibbles_to_bytes(lo & 0xFFFFu) | (nibbles_to_bytes(hi & 0xFFFFu) << 4);
+}
+__device__ __forceinline__ uint32_t kv4_tile_codes(uint32_t bytes, int l) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, bytes, 1);
+    const int odd = l & 1;
+    const uint32_t first = (odd ? other : bytes) >> (4 * odd), second = (odd ? bytes : other) >> (4 * odd);
+    return bytes_to_nibbles(first & 0x0F0F0F0Fu) | (bytes_to_nibbles(second & 0x0F0F0F0Fu) << 16);
+}
+
+// D = 128 (two tokens a round, eight rounds): the even tokens are in lanes 0..15, the odd ones in 16..31.  A word of
+// the group is {t = 2j, 2j + 8, 2j + 1, 2j + 9}: two bytes of either half, which swap so that a lane has rows
+// 4 odd + 2 sub and the next of all four j.
+// D = 64 (four tokens a round, four rounds): token 4i + sub; a word's bytes lie in lanes sub = 2 (j & 1) + (t & 1) of
+// rounds j >> 1 and (j >> 1) + 2.
+template <int D>
+__device__ __forceinline__ void kv4_store_v_group(uint8_t* group, int lane, const uint32_t* bytes) {
+    constexpr int NL = D / 8;
+    const int l = lane & (NL - 1), sub = lane / NL, odd = l & 1, m = l >> 1;
+    const int half = D == 128 ? sub : sub & 1;             // which bytes of a word the lane has: tokens of even or odd t
+    uint8_t* p = group + (m >> 2) * 512 + (m & 3) * 4 + (4 * odd + 2 * half) * 64;
+#pragma unroll
+    for (int i = 0; i < (D == 128 ? 4 : 2); ++i) {
+        const uint32_t a = bytes[i], b = bytes[i + (D == 128 ? 4 : 2)];
+        const uint32_t r01 = __byte_perm(a, b, 0x5140), r23 = __byte_perm(a, b, 0x7362);
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, half ? r01 : r23, NL);
+        const uint32_t even = half ? got : r01, odds = half ? r23 : got;
+        const int j = D == 128 ? i : 2 * i + (sub >> 1);
+        *reinterpret_cast<uint32_t*>(p + j * 16) = __byte_perm(even, odds, 0x5410);
+        *reinterpret_cast<uint32_t*>(p + j * 16 + 64) = __byte_perm(even, odds, 0x7632);
+    }
+}
+template <int D>
+__device__ __forceinline__ void kv4_load_v_group(const uint8_t* group, int lane, uint32_t* bytes) {
+    constexpr int NL = D / 8;
+    const int l = lane & (NL - 1), sub = lane / NL, odd = l & 1, m = l >> 1;
+    const int half = D == 128 ? sub : sub & 1;
+    const uint8_t* p = group + (m >> 2) * 512 + (m & 3) * 4 + (4 * odd + 2 * half) * 64;
+    uint32_t w[D / 32][2];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        const int j = D == 128 ? i : 2 * i + (sub >> 1);
+        w[i][0] = *reinterpret_cast<const uint32_t*>(p + j * 16);
+        w[i][1] = *reinterpret_cast<const uint32_t*>(p + j * 16 + 64);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        const uint32_t even = __byte_perm(w[i][0], w[i][1], 0x5410), odds = __byte_perm(w[i][0], w[i][1], 0x7632);
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, half ? even : odds, NL);
+        const uint32_t r01 = half ? got : even, r23 = half ? odds : got;
+        bytes[i] = __byte_perm(r01, r23, 0x6420);
+        bytes[i + D / 32] = __byte_perm(r01, r23, 0x7531);
+    }
 }
 
 __device__ __forceinline__ uint32_t kv4_load_k(const uint8_t* row, int l) {

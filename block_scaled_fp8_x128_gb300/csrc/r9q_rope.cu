@@ -28,66 +28,11 @@ constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
 constexpr int kMaxRounds = 2;
 constexpr int64_t kEnoughWarps = 152 * 48;
+constexpr int kGroupTokens = 512;
 
 template <int D>
 constexpr int heads_a_round() { return kUnroll * (256 / D); }
 
-// ---- packed pairs of fp32 ----
-__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 parts_of(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-// Eight elements as four pairs.
-struct Eight {
-    uint64_t v[4];
-};
-__device__ __forceinline__ Eight unpack(const uint4& q) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    Eight r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r.v[i] = pair_of(bf16_lo(w[i]), bf16_hi(w[i]));
-    return r;
-}
-__device__ __forceinline__ uint4 pack(const Eight& x) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = parts_of(x.v[i]);
-        w[i] = pack_bf16x2(f.x, f.y);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ float dot(const Eight& a, const Eight& b) {
-    uint64_t s = mul2(a.v[0], b.v[0]);
-#pragma unroll
-    for (int i = 1; i < 4; ++i) s = fma2(a.v[i], b.v[i], s);
-    const float2 f = parts_of(s);
-    return f.x + f.y;
-}
-__device__ __forceinline__ void spread(const Eight& x, float (&y)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = parts_of(x.v[i]);
-        y[2 * i] = f.x;
-        y[2 * i + 1] = f.y;
-    }
-}
 // The lane's elements of a head vector: the first four at first(l), the others at
 // second(l).  SPLIT: four of either half, else eight in a row.
 template <int D, bool SPLIT>
@@ -287,9 +232,10 @@ __device__ __forceinline__ float sum_squares_in_order(const float (&x)[8], int l
 // once, and the sum of squares has a fixed order.  An evaluation of the formula
 // step by step in fp32 gives the same codes.
 template <int NL, bool SPLIT>
-__device__ __forceinline__ void norm_rope_in_order(float (&y)[8], const Eight& weight, const Turn& u, int lane,
-                                                   const RopeParams& p) {
-    float w[8], cs[8], sn[8];
+__device__ __forceinline__ Eight norm_rope_in_order(const Eight& x, const Eight& weight, const Turn& u, int lane,
+                                                    const RopeParams& p) {
+    float y[8], w[8], cs[8], sn[8];
+    spread(x, y);
     spread(weight, w);
     spread(u.c, cs);
     spread(u.s, sn);
@@ -302,6 +248,7 @@ __device__ __forceinline__ void norm_rope_in_order(float (&y)[8], const Eight& w
     for (int e = 0; e < 8; ++e) z[e] = SPLIT ? y[e ^ 4] : p.interleaved ? y[e ^ 1] : __shfl_sync(0xffffffffu, y[e], u.src);
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = __fadd_rn(__fmul_rn(y[e], cs[e]), __fmul_rn(z[e], sn[e]));
+    return {{pair_of(y[0], y[1]), pair_of(y[2], y[3]), pair_of(y[4], y[5]), pair_of(y[6], y[7])}};
 }
 
 enum Pass { kRope, kRopeCache, kAppend };
@@ -316,6 +263,9 @@ struct ForwardArgs {
     int rounds;              // of heads a warp takes
     int nq, nk;              // warps that a token's query and key heads take
     FastDiv parts;           // and all its heads
+    // the launch by whole groups of tokens
+    int windows;             // of 16 tokens
+    FastDiv v_heads, k_parts;
 };
 
 // Where a token goes: its page and place, or page -1 for padding and for a slot
@@ -336,6 +286,59 @@ __device__ __forceinline__ Place find_slot(const Kv4Cache& c, int64_t slot, int 
         }
     }
     return r;
+}
+
+// A warp's share of a token's key (or, at(lane's tokens) alone, value) heads h, h + NV, ... below `end`, into the cache:
+// keys normalised and turned (`turned`) or as they are, values as they are.
+template <int D, bool SPLIT>
+__device__ __forceinline__ void write_heads(const ForwardArgs& a, const HeadsIn& in, bool key, bool turned, int t, int h,
+                                            int end, int lane) {
+    constexpr int NL = D / 8, NV = 32 / NL, HR = heads_a_round<D>();
+    const int l = lane & (NL - 1), sub = lane / NL;
+    const uint16_t* src = in.p + t * in.ts + h * in.hs;
+    const Place place = find_slot(a.c, a.slots[t], lane, a.rope.err);
+    Turn u;
+    Eight w;
+    if (turned) {
+        u = load_turn<D, SPLIT>(a.rope, load_pos(a.rope, t), lane);
+        w = load_weight<D, SPLIT>(a.rope.wk, l);
+    }
+    for (; h - sub < end; h += HR) {
+        uint4 x[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (h + i * NV < end) x[i] = turned ? load_bf16<D, SPLIT>(src, l) : load_bf16<D, false>(src, l);
+            src += NV * in.hs;
+        }
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            if (h - sub + i * NV >= end) break;          // the same for the whole warp
+            Eight z = unpack(x[i]);
+            if (turned) z = norm_rope_in_order<NL, SPLIT>(z, w, u, lane, a.rope);
+            uint32_t pair;
+            const uint32_t codes = kv4_quantise<NL>(z, pair);
+            const bool live = h + i * NV < end && place.page >= 0;
+            const int64_t head = place.page * a.c.heads + h + i * NV;
+            if (key) {
+                if (live) {
+                    uint8_t* row = a.c.k + head * kv4_head_bytes(a.c.page, D) + (int64_t)place.at * (D / 2);
+                    if (turned && SPLIT) {               // elements 2i and 2i + 1 share byte i
+                        *reinterpret_cast<uint16_t*>(row + 2 * l) = (uint16_t)codes;
+                        *reinterpret_cast<uint16_t*>(row + D / 4 + 2 * l) = (uint16_t)(codes >> 16);
+                    } else {
+                        kv4_store_k(row, l, codes);
+                    }
+                    if (l == 0) a.c.kp[head * a.c.page + place.at] = pair;
+                }
+            } else {
+                kv4_store_v(live ? a.c.v + head * kv4_head_bytes(a.c.page, D) + (int64_t)(place.at >> 4) * (8 * D)
+                                 : nullptr,
+                            place.at & 15, l, codes);
+                if (live && l == 0) a.c.vp[head * a.c.page + place.at] = pair;
+            }
+        }
+    }
 }
 
 template <int D, int PASS, bool SPLIT>
@@ -393,72 +396,118 @@ __global__ void __launch_bounds__(kThreads, PASS == kRope && SPLIT ? 4 : 3) forw
         }
         return;
     }
-    // ---- into the cache: keys normalised and turned (or as they are), values as they are ----
-    const bool key = kind == 1;
-    const Place place = find_slot(a.c, a.slots[t], lane, a.rope.err);
-    Turn u;
-    Eight w;
-    if (turned) {
-        u = load_turn<D, SPLIT>(a.rope, load_pos(a.rope, t), lane);
-        w = load_weight<D, SPLIT>(a.rope.wk, l);
+    write_heads<D, SPLIT>(a, in, kind == 1, turned, t, h, end, lane);
+}
+
+// The 16 tokens of a window, if they are a whole group of the cache in order: the group's place, else page -1.
+__device__ __forceinline__ Place group_of(const Kv4Cache& c, const int64_t* slots, int64_t t0, int64_t T, int lane) {
+    Place r = {-1, 0};
+    if (t0 + 16 > T) return r;
+    const int64_t slot = slots[t0 + (lane & 15)], first = __shfl_sync(0xffffffffu, slot, 0);
+    const bool group = first >= 0 && first % 16 == 0 && slot == first + (lane & 15);
+    if (!__all_sync(0xffffffffu, group)) return r;
+    const int64_t page = first / c.page;
+    if (page >= c.pages) return r;                       // (the tokens, one by one, record the error)
+    r.page = page;
+    r.at = (int)(first - page * c.page);
+    return r;
+}
+
+// The cache's part for many tokens.  Value warps take one head of 16 tokens at a time: where these are a group of the
+// cache, as all but the ends of a prompt's chunk are, they put whole words together and store those, not a byte at a
+// time (8192 tokens of 8 heads: 4.2 M partial sectors written become 0.3 M).  Key warps as above.
+template <int D, bool TURNED, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 3) cache_kernel(const ForwardArgs a) {
+    constexpr int NL = D / 8, NV = 32 / NL, HR = heads_a_round<D>(), ROUNDS = 16 / NV;
+    const int lane = threadIdx.x & 31, l = lane & (NL - 1), sub = lane / NL;
+    int unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (unit >= a.windows * a.v_heads.d) {
+        unit -= a.windows * a.v_heads.d;
+        const int t = unit / a.k_parts;
+        if (t >= a.T) return;
+        const int h = (unit - t * a.k_parts.d) * a.rounds * HR;
+        write_heads<D, SPLIT>(a, a.k, true, TURNED, t, h + sub, min(a.k.heads, h + a.rounds * HR), lane);
+        return;
     }
-    for (; h - sub < end; h += HR) {
-        uint4 x[kUnroll];
+    const int window = unit / a.v_heads, h = unit - window * a.v_heads.d;
+    const int64_t t0 = (int64_t)window * 16;
+    uint4 x[ROUNDS];
+    const uint16_t* src = a.v.p + (t0 + sub) * a.v.ts + h * a.v.hs + 8 * l;
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            x[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (h + i * NV < end) x[i] = turned ? load_bf16<D, SPLIT>(src, l) : load_bf16<D, false>(src, l);
-            src += NV * in.hs;
-        }
+    for (int i = 0; i < ROUNDS; ++i)
+        x[i] = t0 + i * NV + sub < a.T ? *reinterpret_cast<const uint4*>(src + i * NV * a.v.ts)
+                                       : make_uint4(0u, 0u, 0u, 0u);
+    const Place place = group_of(a.c, a.slots, t0, a.T, lane);
+    uint32_t codes[ROUNDS], pairs[ROUNDS];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            if (h - sub + i * NV >= end) break;          // the same for the whole warp
-            float z[8];
-            spread(unpack(x[i]), z);
-            if (turned) norm_rope_in_order<NL, SPLIT>(z, w, u, lane, a.rope);
-            uint32_t pair;
-            const uint32_t codes = kv4_quantise<NL>(z, pair);
-            const bool live = h + i * NV < end && place.page >= 0;
-            const int64_t head = place.page * a.c.heads + h + i * NV;
-            if (key) {
-                if (live) {
-                    uint8_t* row = a.c.k + head * kv4_head_bytes(a.c.page, D) + (int64_t)place.at * (D / 2);
-                    if (turned && SPLIT) {               // elements 2i and 2i + 1 share byte i
-                        *reinterpret_cast<uint16_t*>(row + 2 * l) = (uint16_t)codes;
-                        *reinterpret_cast<uint16_t*>(row + D / 4 + 2 * l) = (uint16_t)(codes >> 16);
-                    } else {
-                        kv4_store_k(row, l, codes);
-                    }
-                    if (l == 0) a.c.kp[head * a.c.page + place.at] = pair;
-                }
-            } else {
-                kv4_store_v(live ? a.c.v + head * kv4_head_bytes(a.c.page, D) + (int64_t)(place.at >> 4) * (8 * D)
-                                 : nullptr,
-                            place.at & 15, l, codes);
-                if (live && l == 0) a.c.vp[head * a.c.page + place.at] = pair;
-            }
+    for (int i = 0; i < ROUNDS; ++i) codes[i] = kv4_quantise<NL>(unpack(x[i]), pairs[i]);
+    if (place.page >= 0) {
+        const int64_t head = place.page * a.c.heads + h;
+#pragma unroll
+        for (int i = 0; i < ROUNDS; ++i) codes[i] = kv4_tile_bytes(codes[i], l);
+        kv4_store_v_group<D>(a.c.v + head * kv4_head_bytes(a.c.page, D) + (int64_t)place.at * (D / 2), lane, codes);
+        uint32_t pair = pairs[0];
+#pragma unroll
+        for (int i = 1; i < ROUNDS; ++i) pair = l == i ? pairs[i] : pair;
+        if (l < ROUNDS) a.c.vp[head * a.c.page + place.at + l * NV + sub] = pair;
+        return;
+    }
+#pragma unroll 1
+    for (int i = 0; i < ROUNDS; ++i) {                   // token by token
+        uint32_t code = codes[0], pair = pairs[0];
+#pragma unroll
+        for (int k = 1; k < ROUNDS; ++k) {
+            code = i == k ? codes[k] : code;
+            pair = i == k ? pairs[k] : pair;
         }
+        const int64_t t = t0 + i * NV + sub;
+        Place one = {-1, 0};
+        if (t < a.T) one = find_slot(a.c, a.slots[t], l, a.rope.err);
+        const bool live = one.page >= 0;
+        const int64_t head = one.page * a.c.heads + h;
+        kv4_store_v(live ? a.c.v + head * kv4_head_bytes(a.c.page, D) + (int64_t)(one.at >> 4) * (8 * D) : nullptr,
+                    one.at & 15, l, code);
+        if (live && l == 0) a.c.vp[head * a.c.page + one.at] = pair;
     }
 }
 
 template <int D, int PASS>
 cudaError_t launch_forward(ForwardArgs a, cudaStream_t st) {
     constexpr int HR = heads_a_round<D>();
+    const bool split = PASS != kAppend && a.rope.rot == D && !a.rope.interleaved;
     auto warps = [&](int heads) { return (heads + a.rounds * HR - 1) / (a.rounds * HR); };
+    auto blocks_of = [](int64_t n) { return (n + kThreads / 32 - 1) / (kThreads / 32); };
+    // Many tokens into the cache: the queries by themselves (they need fewer registers, so more of them are in
+    // flight), keys and values by groups of tokens.  Few tokens: one launch, a token's heads side by side.
+    const bool groups = PASS != kRope && a.T >= kGroupTokens;
     // Several rounds a warp share the token's set-up where that still leaves every SM its fill of warps.
     for (a.rounds = kMaxRounds;; a.rounds /= 2) {
         a.nq = PASS == kAppend ? 0 : warps(a.q.heads);
-        a.nk = warps(a.k.heads);
-        const int parts = a.nq + a.nk + (PASS == kRope ? 0 : warps(a.v.heads));
-        a.parts = fast_div(parts);
+        a.nk = groups ? 0 : warps(a.k.heads);
+        const int parts = a.nq + a.nk + (PASS == kRope || groups ? 0 : warps(a.v.heads));
+        a.parts = fast_div(parts > 0 ? parts : 1);
         if (a.rounds == 1 || a.T * parts >= kEnoughWarps) break;
     }
-    const int64_t blocks = (a.T * a.parts.d + kThreads / 32 - 1) / (kThreads / 32);
+    const int64_t blocks = blocks_of(a.T * a.parts.d);
     if (blocks > INT32_MAX / (kThreads / 32)) return cudaErrorInvalidValue;
-    if (PASS != kAppend && a.rope.rot == D && !a.rope.interleaved)
+    if (groups) {
+        if (PASS == kRopeCache) {
+            if (split) forward_kernel<D, kRope, true><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+            else forward_kernel<D, kRope, false><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+        }
+        a.rounds = 1;
+        a.windows = (int)((a.T + 15) / 16);
+        a.v_heads = fast_div(a.v.heads);
+        a.k_parts = fast_div(warps(a.k.heads));
+        const int64_t n = blocks_of((int64_t)a.windows * a.v.heads + a.T * a.k_parts.d);
+        if (n > INT32_MAX / (kThreads / 32)) return cudaErrorInvalidValue;
+        if (split) cache_kernel<D, PASS == kRopeCache, PASS == kRopeCache><<<(unsigned)n, kThreads, 0, st>>>(a);
+        else cache_kernel<D, PASS == kRopeCache, false><<<(unsigned)n, kThreads, 0, st>>>(a);
+    } else if (split) {
         forward_kernel<D, PASS, PASS != kAppend><<<(unsigned)blocks, kThreads, 0, st>>>(a);
-    else
+    } else {
         forward_kernel<D, PASS, false><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    }
     return cudaGetLastError();
 }
 
@@ -469,37 +518,85 @@ cudaError_t launch_forward_d(int D, const ForwardArgs& a, cudaStream_t st) {
 
 // ------------------------------------------------------------- read-back --
 
-// bf16(lowest + step * code) of the tokens at `slots`, zeros for padding.
+// bf16(lowest + step * code).
+__device__ __forceinline__ uint4 kv4_values(uint32_t codes, uint32_t pair) {
+    const uint64_t step = pair_of(bf16_lo(pair), bf16_lo(pair)), low = pair_of(bf16_hi(pair), bf16_hi(pair));
+    Eight y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        // 2^23 + code, as its bits, less 2^23
+        const uint32_t a = 0x4B000000u | (codes >> (8 * i) & 15u), b = 0x4B000000u | (codes >> (8 * i + 4) & 15u);
+        const uint64_t c = add2(pair_of(__uint_as_float(a), __uint_as_float(b)), pair_of(-8388608.0f, -8388608.0f));
+        y.v[i] = fma2(step, c, low);
+    }
+    return pack(y);
+}
+
+// The tokens at `slots`, zeros for padding: a warp takes NV heads of one token.
 template <int D>
-__global__ void __launch_bounds__(kThreads) gather_kernel(const Kv4Cache c, const int64_t* slots, int64_t T,
-                                                          uint16_t* k, uint16_t* v, int* err) {
-    constexpr int NL = D / 8, NV = 32 / NL;
-    const int lane = threadIdx.x & 31, l = lane & (NL - 1), sub = lane / NL;
-    const int parts = (c.heads + NV - 1) / NV;
-    const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t t = unit / parts;
-    if (t >= T) return;
-    const int h = (int)(unit - t * parts) * NV + sub;
-    const Place place = find_slot(c, slots[t], lane, err);
-    const bool live = place.page >= 0 && h < c.heads;
+__device__ __forceinline__ void gather_token(const Kv4Cache& c, const Place& place, int64_t t, int h, bool mine, int l,
+                                             uint16_t* k, uint16_t* v) {
+    const bool live = place.page >= 0 && mine;
     const int64_t head = place.page * c.heads + h;
-    uint32_t codes[2] = {0, 0}, pair[2] = {0, 0};
+    uint32_t codes = 0, pair[2] = {0, 0};
     if (live) {
-        codes[0] = kv4_load_k(c.k + head * kv4_head_bytes(c.page, D) + (int64_t)place.at * (D / 2), l);
+        codes = kv4_load_k(c.k + head * kv4_head_bytes(c.page, D) + (int64_t)place.at * (D / 2), l);
         pair[0] = c.kp[head * c.page + place.at];
         pair[1] = c.vp[head * c.page + place.at];
     }
-    codes[1] = kv4_load_v(live ? c.v + head * kv4_head_bytes(c.page, D) + (int64_t)(place.at >> 4) * (8 * D) : nullptr,
-                          place.at & 15, l);
-    if (h >= c.heads) return;
+    const uint32_t vcodes = kv4_load_v(
+        live ? c.v + head * kv4_head_bytes(c.page, D) + (int64_t)(place.at >> 4) * (8 * D) : nullptr, place.at & 15, l);
+    if (!mine) return;
+    *reinterpret_cast<uint4*>(k + (t * c.heads + h) * D + 8 * l) = kv4_values(codes, pair[0]);
+    *reinterpret_cast<uint4*>(v + (t * c.heads + h) * D + 8 * l) = kv4_values(vcodes, pair[1]);
+}
+template <int D>
+__global__ void __launch_bounds__(kThreads) gather_kernel(const Kv4Cache c, const int64_t* slots, int64_t T,
+                                                          const FastDiv parts, uint16_t* k, uint16_t* v, int* err) {
+    constexpr int NL = D / 8, NV = 32 / NL;
+    const int lane = threadIdx.x & 31, l = lane & (NL - 1), sub = lane / NL;
+    const int unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int t = unit / parts;
+    if (t >= T) return;
+    const int h = (unit - t * parts.d) * NV + sub;
+    gather_token<D>(c, find_slot(c, slots[t], lane, err), t, h, h < c.heads, l, k, v);
+}
+
+// Many tokens: a warp takes one head of 16 of them, word by word where they are a group of the cache.
+template <int D>
+__global__ void __launch_bounds__(kThreads) gather_groups_kernel(const Kv4Cache c, const int64_t* slots, int64_t T,
+                                                                 const FastDiv heads, uint16_t* k, uint16_t* v,
+                                                                 int* err) {
+    constexpr int NL = D / 8, NV = 32 / NL, ROUNDS = 16 / NV;
+    const int lane = threadIdx.x & 31, l = lane & (NL - 1), sub = lane / NL;
+    const int unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int window = unit / heads, h = unit - window * heads.d;
+    const int64_t t0 = (int64_t)window * 16;
+    if (t0 >= T) return;
+    const Place place = group_of(c, slots, t0, T, lane);
+    if (place.page < 0) {
+#pragma unroll 1
+        for (int i = 0; i < ROUNDS; ++i) {
+            const int64_t t = t0 + i * NV + sub;
+            Place one = {-1, 0};
+            if (t < T) one = find_slot(c, slots[t], l, err);
+            gather_token<D>(c, one, t, h, t < T, l, k, v);
+        }
+        return;
+    }
+    const int64_t head = place.page * c.heads + h;
+    const uint8_t* rows = c.k + head * kv4_head_bytes(c.page, D) + (int64_t)place.at * (D / 2);
+    uint32_t codes[ROUNDS], bytes[ROUNDS];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const uint64_t step = pair_of(bf16_lo(pair[s]), bf16_lo(pair[s])), low = pair_of(bf16_hi(pair[s]), bf16_hi(pair[s]));
-        Eight y;
+    for (int i = 0; i < ROUNDS; ++i) codes[i] = kv4_load_k(rows + (i * NV + sub) * (D / 2), l);
+    kv4_load_v_group<D>(c.v + head * kv4_head_bytes(c.page, D) + (int64_t)place.at * (D / 2), lane, bytes);
+    const uint32_t kp = c.kp[head * c.page + place.at + (lane & 15)], vp = c.vp[head * c.page + place.at + (lane & 15)];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            y.v[i] = fma2(step, pair_of((float)(codes[s] >> (8 * i) & 15u), (float)(codes[s] >> (8 * i + 4) & 15u)), low);
-        *reinterpret_cast<uint4*>((s == 0 ? k : v) + (t * c.heads + h) * D + 8 * l) = pack(y);
+    for (int i = 0; i < ROUNDS; ++i) {
+        const int64_t at = ((t0 + i * NV + sub) * c.heads + h) * D + 8 * l;
+        *reinterpret_cast<uint4*>(k + at) = kv4_values(codes[i], __shfl_sync(0xffffffffu, kp, i * NV + sub));
+        *reinterpret_cast<uint4*>(v + at) =
+            kv4_values(kv4_tile_codes(bytes[i], l), __shfl_sync(0xffffffffu, vp, i * NV + sub));
     }
 }
 
@@ -687,11 +784,15 @@ cudaError_t launch_kv4_append(int D, const HeadsIn& k, const HeadsIn& v, int64_t
 
 cudaError_t launch_kv4_gather(int D, const Kv4Cache& c, const int64_t* slots, int64_t T, uint16_t* k, uint16_t* v,
                               int* err, cudaStream_t st) {
+    const bool groups = T >= kGroupTokens;
     const int nv = 256 / D;
-    const int64_t warps = T * ((c.heads + nv - 1) / nv), blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    if (D == 64) gather_kernel<64><<<(unsigned)blocks, kThreads, 0, st>>>(c, slots, T, k, v, err);
-    else gather_kernel<128><<<(unsigned)blocks, kThreads, 0, st>>>(c, slots, T, k, v, err);
+    const int64_t warps = groups ? (T + 15) / 16 * c.heads : T * ((c.heads + nv - 1) / nv);
+    const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
+    if (blocks > INT32_MAX / (kThreads / 32)) return cudaErrorInvalidValue;
+    auto kernel = D == 64 ? (groups ? gather_groups_kernel<64> : gather_kernel<64>)
+                          : (groups ? gather_groups_kernel<128> : gather_kernel<128>);
+    kernel<<<(unsigned)blocks, kThreads, 0, st>>>(c, slots, T, fast_div(groups ? c.heads : (c.heads + nv - 1) / nv), k, v,
+                                                  err);
     return cudaGetLastError();
 }
 

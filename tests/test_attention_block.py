@@ -527,3 +527,81 @@ def test_refusals():
         r9q.r9q_qk_norm_rope(*(torch.zeros((2, 2, 128), dtype=torch.bfloat16),) * 2, *(torch.ones(128),) * 2)
     with pytest.raises(ValueError):
         r9q.r9q_kv4_cache(2, 2, 20, 128, device="cpu")
+
+
+# ------------------------------------------------- many tokens at a time --
+
+def prompt_slots(T, page, pages, how, seed):
+    """Places of T tokens: page after page from the start of one, from its fourth token, or anywhere; padding in it."""
+    order = np.random.default_rng(seed).permutation(pages)
+    t = np.arange(T) + (3 if how == "late" else 0)
+    slots = order[t // page] * page + t % page
+    if how == "anywhere":
+        slots = np.random.default_rng(seed).permutation(pages * page)[:T]
+    if how != "aligned":
+        slots[[7, T // 2]] = -1
+    return slots
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,D,page", [(512, 2, 128, 16), (777, 3, 128, 48), (1000, 1, 64, 16), (515, 5, 64, 64)])
+@pytest.mark.parametrize("how", ["aligned", "late", "anywhere"])
+def test_append_and_gather_of_a_prompt(r9q, T, H, D, page, how):
+    """As test_append_and_gather, at sizes where whole groups of 16 tokens are put together."""
+    pages = T // page + 2
+    slots = prompt_slots(T, page, pages, how, T)
+    kv = rand((T, 2 * H, D), 91, 2.0).to(dev())
+    kv[3, 0] = 1.0
+    k, v = kv[:, :H], kv[:, H:]
+    cache = r9q.r9q_kv4_cache(pages, H, page, D)
+    for t in cache:
+        t.view(torch.uint8).fill_(0x5A)
+    r9q.r9q_kv4_append(k, v, cache, on(slots))
+    kc, vc, kp, vp = codes_of(cache)
+    kept = slots >= 0
+    p, at = slots[kept] // page, slots[kept] % page
+    written = np.zeros((pages, page), bool)
+    written[p, at] = True
+    gk, gv = r9q.r9q_kv4_gather(cache, on(slots))
+    for x, codes, pair, got in ((k, kc, kp, gk), (v, vc, vp, gv)):
+        ec, es, el = ref.quantise32(np64(x).astype(np.float32)[kept])
+        assert np.array_equal(codes[p, :, at], ec)
+        assert np.array_equal(pair[p, :, at], np.concatenate([es, el], -1).astype(np.float64))
+        assert set(np.unique(codes.transpose(0, 2, 1, 3)[~written])) <= {5, 10}
+        e = el + es * ec
+        got = np64(got)
+        assert (np.abs(got[kept] - e) <= U * np.abs(e) * 1.01).all() and (got[~kept] == 0).all()
+    assert r9q.r9q_last_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,Hq,Hk,D,rot,inter", [(520, 4, 2, 128, 128, False), (700, 3, 1, 64, 64, False),
+                                                (513, 2, 2, 128, 64, True), (600, 5, 1, 64, 32, False)])
+def test_norm_rope_of_a_prompt_into_cache(r9q, T, Hq, Hk, D, rot, inter):
+    """The same cache, bit for bit, as from the tokens a few at a time (which the tests above hold to 64 bits)."""
+    page, pages = 16, T // 16 + 2
+    q, k, v, wq, wk, cos, sin, pos = rope_inputs(T, Hq, Hk, D, rot, 95)
+    args = rope_args(wq, wk, cos, sin, pos)
+    slots = on(prompt_slots(T, page, pages, "late" if T % 2 else "aligned", T))
+    a, b = r9q.r9q_kv4_cache(pages, Hk, page, D), r9q.r9q_kv4_cache(pages, Hk, page, D)
+    qo = r9q.r9q_qk_norm_rope_kv4(q, k, v, *args, a, slots, interleaved=inter)
+    for i in range(0, T, 100):
+        s = slice(i, min(T, i + 100))
+        part = r9q.r9q_qk_norm_rope_kv4(q[s], k[s], v[s], *args[:4], args[4][s].contiguous(), b, slots[s].contiguous(),
+                                        interleaved=inter)
+        assert torch.equal(part, qo[s])
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hk,D", [(4, 1, 128), (16, 1, 128), (7, 1, 64), (12, 1, 64)])
+def test_attention_of_one_long_sequence(r9q, Hq, Hk, D):
+    """Long enough for one CTA an SM (and its partials from every one of them)."""
+    lens, page = [150000], 256
+    cache, table, _ = make_cache(r9q, lens, Hk, D, page, 97, garbage=False)
+    q = rand((1, 1, Hq, D), 98).to(dev())
+    o, lse = r9q.r9q_kv4_attention(q, cache, on(table), on(np.array(lens, np.int32)), return_lse=True)
+    check_attention(r9q, cache, table, lens, q, o, lse)
+    n = on(np.array([1234], np.int32))
+    o, lse = r9q.r9q_kv4_attention(q, cache, on(table), n, return_lse=True)
+    check_attention(r9q, cache, table, [1234], q, o, lse)
