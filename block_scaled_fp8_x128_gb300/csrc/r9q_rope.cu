@@ -265,6 +265,7 @@ struct ForwardArgs {
     FastDiv parts;           // and all its heads
     // the launch by whole groups of tokens
     int windows;             // of 16 tokens
+    uint32_t cache_share;    // of its blocks that are the cache's, in 2^-32
     FastDiv v_heads, k_parts;
 };
 
@@ -341,10 +342,48 @@ __device__ __forceinline__ void write_heads(const ForwardArgs& a, const HeadsIn&
     }
 }
 
+// A warp's share of a token's query or key heads h, h + NV, ... below `end`: normalised and turned, as bf16.
+template <int D, bool SPLIT>
+__device__ __forceinline__ void turn_heads(const RopeParams& p, const HeadsIn& in, const HeadsOut& out,
+                                           const float* weight, int t, int h, int end, int lane) {
+    constexpr int NL = D / 8, NV = 32 / NL, HR = heads_a_round<D>();
+    const int l = lane & (NL - 1), sub = lane / NL;
+    const uint16_t* src = in.p + t * in.ts + h * in.hs;
+    uint16_t* dst = out.p + t * out.ts + h * out.hs;
+    Turn u;
+    bool ready = false;
+    for (; h - sub < end; h += HR) {
+        uint4 x[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            x[i] = h + i * NV < end ? load_bf16<D, SPLIT>(src, l) : make_uint4(0u, 0u, 0u, 0u);
+            src += NV * in.hs;
+        }
+        if (!ready) {                                    // (after the loads are on their way)
+            u = load_turn<D, SPLIT>(p, load_pos(p, t), lane);
+            fold_weight<D, SPLIT>(u, weight, lane, p.interleaved);
+            ready = true;
+        }
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            Eight y = unpack(x[i]);
+            const Eight xp = partner<SPLIT>(x[i], y, u, p.interleaved);
+            const float r = inverse_root(fmaf(group_sum<NL>(dot(y, y)), 1.0f / D, p.eps));
+            const uint64_t rr = pair_of(r, r);
+            Eight z;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z.v[e] = mul2(rr, fma2(y.v[e], u.c.v[e], mul2(xp.v[e], u.s.v[e])));
+            if (h + i * NV < end) store_bf16<D, SPLIT>(dst, l, pack(z));
+            dst += NV * out.hs;
+        }
+    }
+}
+
+// One launch over tokens, their query, key and value heads side by side.
 template <int D, int PASS, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, PASS == kRope && SPLIT ? 4 : 3) forward_kernel(const ForwardArgs a) {
-    constexpr int NL = D / 8, NV = 32 / NL, HR = heads_a_round<D>();
-    const int lane = threadIdx.x & 31, l = lane & (NL - 1), sub = lane / NL;
+    constexpr int NL = D / 8, HR = heads_a_round<D>();
+    const int lane = threadIdx.x & 31, sub = lane / NL;
     const int unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     const int t = unit / a.parts;
     if (t >= a.T) return;
@@ -359,44 +398,12 @@ __global__ void __launch_bounds__(kThreads, PASS == kRope && SPLIT ? 4 : 3) forw
         }
     }
     const HeadsIn& in = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-    int h = part * a.rounds * HR + sub;                  // the lane's first head
+    const int h = part * a.rounds * HR + sub;            // the lane's first head
     const int end = min(in.heads, part * a.rounds * HR + a.rounds * HR);
-    const bool turned = PASS != kAppend && kind < 2;
-    const uint16_t* src = in.p + t * in.ts + h * in.hs;
-    if (PASS == kRope || (PASS == kRopeCache && kind == 0)) {
-        // ---- bf16 out ----
-        const HeadsOut& out = kind == 0 ? a.qo : a.ko;
-        uint16_t* dst = out.p + t * out.ts + h * out.hs;
-        Turn u;
-        bool ready = false;
-        for (; h - sub < end; h += HR) {
-            uint4 x[kUnroll];
-#pragma unroll
-            for (int i = 0; i < kUnroll; ++i) {
-                x[i] = h + i * NV < end ? load_bf16<D, SPLIT>(src, l) : make_uint4(0u, 0u, 0u, 0u);
-                src += NV * in.hs;
-            }
-            if (!ready) {
-                u = load_turn<D, SPLIT>(a.rope, load_pos(a.rope, t), lane);
-                fold_weight<D, SPLIT>(u, kind == 0 ? a.rope.wq : a.rope.wk, lane, a.rope.interleaved);
-                ready = true;
-            }
-#pragma unroll
-            for (int i = 0; i < kUnroll; ++i) {
-                Eight y = unpack(x[i]);
-                const Eight xp = partner<SPLIT>(x[i], y, u, a.rope.interleaved);
-                const float r = inverse_root(fmaf(group_sum<NL>(dot(y, y)), 1.0f / D, a.rope.eps));
-                const uint64_t rr = pair_of(r, r);
-                Eight z;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) z.v[e] = mul2(rr, fma2(y.v[e], u.c.v[e], mul2(xp.v[e], u.s.v[e])));
-                if (h + i * NV < end) store_bf16<D, SPLIT>(dst, l, pack(z));
-                dst += NV * out.hs;
-            }
-        }
-        return;
-    }
-    write_heads<D, SPLIT>(a, in, kind == 1, turned, t, h, end, lane);
+    if (PASS == kRope || (PASS == kRopeCache && kind == 0))
+        turn_heads<D, SPLIT>(a.rope, in, kind == 0 ? a.qo : a.ko, kind == 0 ? a.rope.wq : a.rope.wk, t, h, end, lane);
+    else
+        write_heads<D, SPLIT>(a, in, kind == 1, PASS != kAppend && kind < 2, t, h, end, lane);
 }
 
 // The 16 tokens of a window, if they are a whole group of the cache in order: the group's place, else page -1.
@@ -413,20 +420,30 @@ __device__ __forceinline__ Place group_of(const Kv4Cache& c, const int64_t* slot
     return r;
 }
 
-// The cache's part for many tokens.  Value warps take one head of 16 tokens at a time: where these are a group of the
+// Many tokens into the cache.  Value warps take one head of 16 tokens at a time: where these are a group of the
 // cache, as all but the ends of a prompt's chunk are, they put whole words together and store those, not a byte at a
-// time (8192 tokens of 8 heads: 4.2 M partial sectors written become 0.3 M).  Key warps as above.
+// time (8192 tokens of 8 heads: 4.2 M partial sectors written become 0.3 M).  Key warps as above.  The query heads,
+// which HBM bounds, and the quantising, which instructions bound, are blocks of one grid in turn, so that an SM has both.
 template <int D, bool TURNED, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 3) cache_kernel(const ForwardArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) prompt_kernel(const ForwardArgs a) {
     constexpr int NL = D / 8, NV = 32 / NL, HR = heads_a_round<D>(), ROUNDS = 16 / NV;
-    const int lane = threadIdx.x & 31, l = lane & (NL - 1), sub = lane / NL;
-    int unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, l = lane & (NL - 1), sub = lane / NL, warp = threadIdx.x >> 5;
+    // of every grid / cache_blocks blocks one is the cache's
+    const uint32_t before = __umulhi(blockIdx.x, a.cache_share), upto = __umulhi(blockIdx.x + 1, a.cache_share);
+    if (TURNED && upto == before) {
+        const int unit = (blockIdx.x - before) * (kThreads / 32) + warp, t = unit / a.parts;
+        if (t >= a.T) return;
+        const int h = (unit - t * a.parts.d) * a.rounds * HR;
+        turn_heads<D, SPLIT>(a.rope, a.q, a.qo, a.rope.wq, t, h + sub, min(a.q.heads, h + a.rounds * HR), lane);
+        return;
+    }
+    int unit = (TURNED ? before : blockIdx.x) * (kThreads / 32) + warp;
     if (unit >= a.windows * a.v_heads.d) {
         unit -= a.windows * a.v_heads.d;
         const int t = unit / a.k_parts;
         if (t >= a.T) return;
-        const int h = (unit - t * a.k_parts.d) * a.rounds * HR;
-        write_heads<D, SPLIT>(a, a.k, true, TURNED, t, h + sub, min(a.k.heads, h + a.rounds * HR), lane);
+        const int h = (unit - t * a.k_parts.d) * HR;
+        write_heads<D, SPLIT>(a, a.k, true, TURNED, t, h + sub, min(a.k.heads, h + HR), lane);
         return;
     }
     const int window = unit / a.v_heads, h = unit - window * a.v_heads.d;
@@ -477,10 +494,8 @@ cudaError_t launch_forward(ForwardArgs a, cudaStream_t st) {
     const bool split = PASS != kAppend && a.rope.rot == D && !a.rope.interleaved;
     auto warps = [&](int heads) { return (heads + a.rounds * HR - 1) / (a.rounds * HR); };
     auto blocks_of = [](int64_t n) { return (n + kThreads / 32 - 1) / (kThreads / 32); };
-    // Many tokens into the cache: the queries by themselves (they need fewer registers, so more of them are in
-    // flight), keys and values by groups of tokens.  Few tokens: one launch, a token's heads side by side.
-    const bool groups = PASS != kRope && a.T >= kGroupTokens;
     // Several rounds a warp share the token's set-up where that still leaves every SM its fill of warps.
+    const bool groups = PASS != kRope && a.T >= kGroupTokens;
     for (a.rounds = kMaxRounds;; a.rounds /= 2) {
         a.nq = PASS == kAppend ? 0 : warps(a.q.heads);
         a.nk = groups ? 0 : warps(a.k.heads);
@@ -488,26 +503,27 @@ cudaError_t launch_forward(ForwardArgs a, cudaStream_t st) {
         a.parts = fast_div(parts > 0 ? parts : 1);
         if (a.rounds == 1 || a.T * parts >= kEnoughWarps) break;
     }
-    const int64_t blocks = blocks_of(a.T * a.parts.d);
-    if (blocks > INT32_MAX / (kThreads / 32)) return cudaErrorInvalidValue;
-    if (groups) {
-        if (PASS == kRopeCache) {
-            if (split) forward_kernel<D, kRope, true><<<(unsigned)blocks, kThreads, 0, st>>>(a);
-            else forward_kernel<D, kRope, false><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    const int64_t most = INT32_MAX / (kThreads / 32);
+    int64_t blocks = blocks_of(a.T * a.parts.d);
+    if (blocks > most) return cudaErrorInvalidValue;
+    if constexpr (PASS != kRope) {
+        if (groups) {
+            a.windows = (int)((a.T + 15) / 16);
+            a.v_heads = fast_div(a.v.heads);
+            a.k_parts = fast_div((a.k.heads + HR - 1) / HR);
+            const int64_t cache = blocks_of((int64_t)a.windows * a.v.heads + a.T * a.k_parts.d);
+            if (PASS == kAppend) blocks = 0;
+            blocks += cache;
+            if (blocks > most) return cudaErrorInvalidValue;
+            a.cache_share = (uint32_t)((((uint64_t)cache << 32) + blocks - 1) / blocks);       // (rounded up: all of them)
+            auto kernel = split ? prompt_kernel<D, PASS == kRopeCache, PASS == kRopeCache>
+                                : prompt_kernel<D, PASS == kRopeCache, false>;
+            kernel<<<(unsigned)blocks, kThreads, 0, st>>>(a);
+            return cudaGetLastError();
         }
-        a.rounds = 1;
-        a.windows = (int)((a.T + 15) / 16);
-        a.v_heads = fast_div(a.v.heads);
-        a.k_parts = fast_div(warps(a.k.heads));
-        const int64_t n = blocks_of((int64_t)a.windows * a.v.heads + a.T * a.k_parts.d);
-        if (n > INT32_MAX / (kThreads / 32)) return cudaErrorInvalidValue;
-        if (split) cache_kernel<D, PASS == kRopeCache, PASS == kRopeCache><<<(unsigned)n, kThreads, 0, st>>>(a);
-        else cache_kernel<D, PASS == kRopeCache, false><<<(unsigned)n, kThreads, 0, st>>>(a);
-    } else if (split) {
-        forward_kernel<D, PASS, PASS != kAppend><<<(unsigned)blocks, kThreads, 0, st>>>(a);
-    } else {
-        forward_kernel<D, PASS, false><<<(unsigned)blocks, kThreads, 0, st>>>(a);
     }
+    if (split) forward_kernel<D, PASS, PASS != kAppend><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    else forward_kernel<D, PASS, false><<<(unsigned)blocks, kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
