@@ -75,12 +75,7 @@ constexpr int work_bytes(int D, int NT, bool wide) {
     return largest(largest(w * kStages * stage_bytes(D), w * 8 * NT * (out_stride(D) + 2) * 4),
                    n + 2 * 8 * NT * 4 + largest(n, w * 32 * 8 * NT * 16));
 }
-// What the threads of a CTA tell one another about its range.
-struct Shared {
-    long long scan[3][16], first;
-    int seq, last;
-};
-constexpr int smem_bytes(int D, int NT, bool wide) { return work_bytes(D, NT, wide) + (int)sizeof(Shared); }
+constexpr int smem_bytes(int D, int NT, bool wide) { return work_bytes(D, NT, wide) + 16; }   // and a flag
 
 // Copies a lane's share of one group of 16 tokens into a stage, if `live`: its two K rows' parts (8 rows apart), its
 // V pieces, and a (step, lowest) pair.
@@ -164,23 +159,15 @@ __device__ __noinline__ Span span_of(const int32_t* at, int room, int reach, int
     return s;
 }
 
-// The CTA's inclusive scan of one value a thread; `total` over all.
-template <int W>
-__device__ __noinline__ long long cta_scan(long long v, long long* sums, long long& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// The warp's inclusive scan of one value a lane; `total` over all.
+__device__ __forceinline__ long long warp_scan(long long v, long long& total) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += x;
     }
-    if (lane == 31) sums[warp] = v;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-        if (w < warp) v += sums[w];
-        total += sums[w];
-    }
+    total = __shfl_sync(0xffffffffu, v, 31);
     return v;
 }
 
@@ -401,7 +388,7 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
     constexpr int ST = kStages;
     constexpr int kMinGroups = 2 * W;        // groups a CTA takes at least: one step for each warp
     extern __shared__ __align__(16) uint8_t smem[];
-    Shared& sh = *reinterpret_cast<Shared*>(smem + work_bytes(D, NT, WIDE));
+    int* joins = reinterpret_cast<int*>(smem + work_bytes(D, NT, WIDE));     // the CTA joins an item's partials
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = lane >> 2, j = lane & 3;
@@ -409,17 +396,17 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
     const int items_per_seq = p.c.heads * chunks;
     const long long items = (long long)p.B * items_per_seq, ctas = gridDim.x;
 
-    // ---- what this CTA does ----
+    // ---- what this CTA does: every warp finds it for itself, a lane for every so many sequences ----
     const bool parted = 2 * items <= ctas;   // one part of one item a CTA
     const int begin_cost = parted ? 0 : kItemCost;
     auto span = [&](int b) { return span_of(p.lens + b, p.room, p.reach, p.err); };
-    const int per_thread = (p.B + kThreads - 1) / kThreads;
-    const int b_first = tid * per_thread, b_end = min(p.B, b_first + per_thread);
+    const int per_lane = (p.B + 31) / 32;
+    const int b_first = lane * per_lane, b_end = min(p.B, b_first + per_lane);
     long long mine = 0, total;
 #pragma unroll 1
     for (int b = b_first; b < b_end; ++b) mine += span(b).groups + begin_cost;
     mine *= items_per_seq;
-    long long upto = cta_scan<W>(mine, sh.scan[0], total);
+    long long upto = warp_scan(mine, total);
     long long per;                           // groups of a part, or of a CTA's range
     if (parted) {
         // The even share, if parts of that size are no more than the CTAs; else total / (ctas - items): the sum of
@@ -432,7 +419,7 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
 #pragma unroll 1
             for (int b = b_first; b < b_end; ++b) mine += (span(b).groups + (int)per - 1) / (int)per;
             mine *= items_per_seq;
-            upto = cta_scan<W>(mine, sh.scan[attempt], total);
+            upto = warp_scan(mine, total);
             if (total <= ctas || attempt == 2) break;
             per = (all + ctas - items - 1) / (ctas - items);
         }
@@ -444,23 +431,22 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
     auto snap_of = [&](int groups) { return min(min(8, (int)min(per / 4, 8ll)), (groups - 1) / 2); };
     long long u = parted ? blockIdx.x : blockIdx.x * per;
     if (u >= total) return;
-    if (u >= upto - mine && u < upto) {
-        long long at = upto - mine;
-        int b = b_first;
+    const bool here = u >= upto - mine && u < upto;      // one lane's
+    int b = b_first;
+    long long seq_first = upto - mine;       // first part or group of sequence b
+    if (here) {
 #pragma unroll 1
         for (;; ++b) {
             const int g = span(b).groups;
             const long long n = (long long)(parted ? (g + (int)per - 1) / (int)per : g + begin_cost) * items_per_seq;
-            if (u < at + n) break;
-            at += n;
+            if (u < seq_first + n) break;
+            seq_first += n;
         }
-        sh.seq = b;
-        sh.first = at;
     }
-    __syncthreads();
-    int b = sh.seq;
+    const int owner = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    b = __shfl_sync(0xffffffffu, b, owner);
+    seq_first = __shfl_sync(0xffffffffu, seq_first, owner);
     Span sp = span(b);
-    long long seq_first = sh.first;          // first part or group of sequence b
     int parts = parted ? (sp.groups + (int)per - 1) / (int)per : 0;
     int even = parted ? (sp.groups + parts - 1) / parts : 0;    // groups of this sequence's parts
     if (parted) parts = (sp.groups + even - 1) / even;
@@ -731,18 +717,19 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
             }
         }
         if (!whole) {
-            __threadfence();
             __syncthreads();
             if (tid == 0) {
-                const bool last = atomicAdd(p.done + c0, 1) == c1 - c0;
+                // the barrier has ordered the CTA's writes before this release; the last to arrive acquires all others'
+                int arrived;
+                asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(arrived) : "l"(p.done + c0) : "memory");
+                const bool last = arrived == c1 - c0;
                 if (last) p.done[c0] = 0;
-                sh.last = last;
+                *joins = last;
             }
             __syncthreads();
-            if (sh.last) {
+            if (*joins) {
                 // The partials' weights first, in shared memory, then the weighted sum: the warps that hold a row's
                 // elements take every ROWS-th partial each (several rows of loads in flight) and meet at the end.
-                __threadfence();
                 const int n = c1 - c0 + 1;
                 float* wt = reinterpret_cast<float*>(smem);
                 auto slot = [&](int c) { return p.part + ((size_t)(c0 + c) * 2 + (c == 0 ? 1 : 0)) * kSlot; };

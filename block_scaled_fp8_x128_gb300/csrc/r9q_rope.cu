@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
-constexpr int kMaxRounds = 2;
+constexpr int kMaxRounds = 4;
 constexpr int64_t kEnoughWarps = 152 * 48;
 constexpr int kGroupTokens = 512;
 
