@@ -35,6 +35,38 @@ inline FastDiv fast_div(int d) {
     return {(uint32_t)(((1ull << (31 + l)) + d - 1) / d), l, d};
 }
 
+// Launches a kernel of the attention block so that its CTAs may be set up while the
+// kernel before it in the stream ends.  Each of these kernels begins with
+// begin_chained(): the next one may be set up from then on, and nothing is read or
+// written before all that came before is complete and visible.
+template <typename... Params, typename... Args>
+cudaError_t launch_chained(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t st,
+                           const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+// Arrival of a CTA at a counter, by one thread after a barrier: releases what the CTA's
+// threads wrote before the barrier, and for the last to arrive acquires what the others
+// released.  Returns the arrivals before it.
+__device__ __forceinline__ int arrive(int* counter) {
+    int n;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(n) : "l"(counter) : "memory");
+    return n;
+}
+__device__ __forceinline__ void begin_chained() {
+    pdl_trigger();
+    pdl_wait();
+}
+
 __host__ __device__ __forceinline__ int64_t kv4_head_bytes(int page, int D) { return (int64_t)page * (D / 2); }
 
 // Byte of token t (0..15) inside a group's [j][m][b] block, m = 0.

@@ -388,6 +388,7 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
     constexpr int ST = kStages;
     constexpr int kMinGroups = 2 * W;        // groups a CTA takes at least: one step for each warp
     extern __shared__ __align__(16) uint8_t smem[];
+    begin_chained();
     int* joins = reinterpret_cast<int*>(smem + work_bytes(D, NT, WIDE));     // the CTA joins an item's partials
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -719,10 +720,7 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
         if (!whole) {
             __syncthreads();
             if (tid == 0) {
-                // the barrier has ordered the CTA's writes before this release; the last to arrive acquires all others'
-                int arrived;
-                asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(arrived) : "l"(p.done + c0) : "memory");
-                const bool last = arrived == c1 - c0;
+                const bool last = arrive(p.done + c0) == c1 - c0;
                 if (last) p.done[c0] = 0;
                 *joins = last;
             }
@@ -802,9 +800,8 @@ cudaError_t launch(const Kv4AttnParams& p, int sms, cudaStream_t st) {
     const void* kernel = reinterpret_cast<const void*>(kv4_attention_kernel<D, NT, WIDE>);
     cudaError_t e = ensure_dynamic_smem(kernel, smem_bytes(D, NT, WIDE));
     if (e != cudaSuccess) return e;
-    kv4_attention_kernel<D, NT, WIDE>
-        <<<used_sms(sms) * ctas_per_sm(D, NT, WIDE), 32 * cta_warps(D, NT, WIDE), smem_bytes(D, NT, WIDE), st>>>(p);
-    return cudaGetLastError();
+    return launch_chained(kv4_attention_kernel<D, NT, WIDE>, used_sms(sms) * ctas_per_sm(D, NT, WIDE),
+                          32 * cta_warps(D, NT, WIDE), smem_bytes(D, NT, WIDE), st, p);
 }
 
 template <int D, int NT>

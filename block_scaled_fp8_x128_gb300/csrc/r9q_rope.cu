@@ -382,6 +382,7 @@ __device__ __forceinline__ void turn_heads(const RopeParams& p, const HeadsIn& i
 // One launch over tokens, their query, key and value heads side by side.
 template <int D, int PASS, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, PASS == kRope && SPLIT ? 4 : 3) forward_kernel(const ForwardArgs a) {
+    begin_chained();
     constexpr int NL = D / 8, HR = heads_a_round<D>();
     const int lane = threadIdx.x & 31, sub = lane / NL;
     const int unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -426,6 +427,7 @@ __device__ __forceinline__ Place group_of(const Kv4Cache& c, const int64_t* slot
 // which HBM bounds, and the quantising, which instructions bound, are blocks of one grid in turn, so that an SM has both.
 template <int D, bool TURNED, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 4) prompt_kernel(const ForwardArgs a) {
+    begin_chained();
     constexpr int NL = D / 8, NV = 32 / NL, HR = heads_a_round<D>(), ROUNDS = 16 / NV;
     const int lane = threadIdx.x & 31, l = lane & (NL - 1), sub = lane / NL, warp = threadIdx.x >> 5;
     // of every grid / cache_blocks blocks one is the cache's
@@ -518,13 +520,11 @@ cudaError_t launch_forward(ForwardArgs a, cudaStream_t st) {
             a.cache_share = (uint32_t)((((uint64_t)cache << 32) + blocks - 1) / blocks);       // (rounded up: all of them)
             auto kernel = split ? prompt_kernel<D, PASS == kRopeCache, PASS == kRopeCache>
                                 : prompt_kernel<D, PASS == kRopeCache, false>;
-            kernel<<<(unsigned)blocks, kThreads, 0, st>>>(a);
-            return cudaGetLastError();
+            return launch_chained(kernel, (unsigned)blocks, kThreads, 0, st, a);
         }
     }
-    if (split) forward_kernel<D, PASS, PASS != kAppend><<<(unsigned)blocks, kThreads, 0, st>>>(a);
-    else forward_kernel<D, PASS, false><<<(unsigned)blocks, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_chained(split ? forward_kernel<D, PASS, PASS != kAppend> : forward_kernel<D, PASS, false>,
+                          (unsigned)blocks, kThreads, 0, st, a);
 }
 
 template <int PASS>
@@ -569,6 +569,7 @@ __device__ __forceinline__ void gather_token(const Kv4Cache& c, const Place& pla
 template <int D>
 __global__ void __launch_bounds__(kThreads) gather_kernel(const Kv4Cache c, const int64_t* slots, int64_t T,
                                                           const FastDiv parts, uint16_t* k, uint16_t* v, int* err) {
+    begin_chained();
     constexpr int NL = D / 8, NV = 32 / NL;
     const int lane = threadIdx.x & 31, l = lane & (NL - 1), sub = lane / NL;
     const int unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -583,6 +584,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) gather_groups_kernel(const Kv4Cache c, const int64_t* slots, int64_t T,
                                                                  const FastDiv heads, uint16_t* k, uint16_t* v,
                                                                  int* err) {
+    begin_chained();
     constexpr int NL = D / 8, NV = 32 / NL, ROUNDS = 16 / NV;
     const int lane = threadIdx.x & 31, l = lane & (NL - 1), sub = lane / NL;
     const int unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -639,6 +641,7 @@ constexpr int kBwdUnroll = 4;
 
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const BackwardArgs a) {
+    begin_chained();
     constexpr int NL = D / 8, NV = 32 / NL, HR = kBwdUnroll * NV, NW = kBwdThreads / 32;
     __shared__ __align__(16) float sums[NW * 128];       // the warps' sums [NW][D]; at the end four floats a thread
     const RopeParams& p = a.rope;
@@ -728,18 +731,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const Backward
         }
         __syncthreads();
     }
-    __threadfence();
-    __syncthreads();
     __shared__ int last;
-    if (threadIdx.x == 0) last = atomicAdd(a.done, 1) == (int)gridDim.x - 1;
+    if (threadIdx.x == 0) last = arrive(a.done) == (int)gridDim.x - 1;   // (the loop's barrier is before it)
     __syncthreads();
     if (!last) return;
-    __threadfence();
     // a thread adds four columns of every ROWS-th block's sums, many loads in flight
     constexpr int COLS = 2 * D / 4, ROWS = kBwdThreads / COLS;
     const int col = threadIdx.x % COLS, row = threadIdx.x / COLS;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 10
+#pragma unroll 20
     for (int b = row; b < (int)gridDim.x; b += ROWS) {
         const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part + (int64_t)b * 2 * D) + col);
         v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
@@ -807,9 +807,8 @@ cudaError_t launch_kv4_gather(int D, const Kv4Cache& c, const int64_t* slots, in
     if (blocks > INT32_MAX / (kThreads / 32)) return cudaErrorInvalidValue;
     auto kernel = D == 64 ? (groups ? gather_groups_kernel<64> : gather_kernel<64>)
                           : (groups ? gather_groups_kernel<128> : gather_kernel<128>);
-    kernel<<<(unsigned)blocks, kThreads, 0, st>>>(c, slots, T, fast_div(groups ? c.heads : (c.heads + nv - 1) / nv), k, v,
-                                                  err);
-    return cudaGetLastError();
+    return launch_chained(kernel, (unsigned)blocks, kThreads, 0, st, c, slots, T,
+                          fast_div(groups ? c.heads : (c.heads + nv - 1) / nv), k, v, err);
 }
 
 int qk_norm_rope_bwd_blocks(int sms) { return sms; }
@@ -827,8 +826,7 @@ cudaError_t launch_qk_norm_rope_bwd(int D, const HeadsIn& dqo, const HeadsIn& dk
     const bool split = p.rot == D && !p.interleaved;
     auto kernel = D == 64 ? (split ? backward_kernel<64, true> : backward_kernel<64, false>)
                           : (split ? backward_kernel<128, true> : backward_kernel<128, false>);
-    kernel<<<grid, kBwdThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_chained(kernel, grid, kBwdThreads, 0, st, a);
 }
 
 }  // namespace r9q
