@@ -318,6 +318,8 @@ int r9q_kv4_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, c
     if (!dims_ok(Lq, Hq, D) || !dims_ok(Lq, Hk, D) || B < 0 || Hq % Hk) return R9Q_ERR_DIM;
     if (B > INT_MAX / 64 || Lq > (1 << 20) || B * Lq > INT_MAX || max_pages < 0 || max_pages > INT_MAX || window < 0)
         return R9Q_ERR_DIM;
+    const int64_t rows = Lq * (Hq / Hk);
+    if (rows > (1 << 24) || Hk * rows > ((int64_t)1 << 30)) return R9Q_ERR_DIM;
     if (B == 0 || Lq == 0) return R9Q_OK;
     int rc = check_heads(q, Lq, q_ts, Hq, q_hs);
     if (!rc && !stride_ok(B, q_bs)) rc = R9Q_ERR_ARG;
@@ -327,7 +329,6 @@ int r9q_kv4_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, c
     if (!seq_lens || !o || (max_pages > 0 && !block_table)) return R9Q_ERR_NULL;
     if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4)) return R9Q_ERR_ALIGN;
     if (!(scale > 0.0f) || std::isinf(scale) || max_pages * page > 0x7FE00000) return R9Q_ERR_ARG;
-    const int64_t rows = Lq * (Hq / Hk);
     const size_t need = decode_workspace(R9Q_OP_KV4_ATTENTION, rows, D, &rc);
     if (!workspace || workspace_bytes < need) return R9Q_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return R9Q_ERR_ALIGN;

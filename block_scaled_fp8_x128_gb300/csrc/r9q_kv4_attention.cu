@@ -131,7 +131,7 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
 // D(16x8 f32) += A(16x16 f16, row) * B(16x8 f16, col)
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -269,29 +269,36 @@ __device__ __forceinline__ void attend(State<D, NT>& s, const uint8_t* st, int k
 
     // ---- scores over fr ----
     float sc[NT][2][4];
+    uint32_t k0[2][KW], k1[2][KW];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        uint32_t k0[KW], k1[KW];
         const uint8_t* kb = st + i * 16 * (D / 2) + lane * (KW * 4);
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
-            k0[w] = reinterpret_cast<const uint32_t*>(kb)[w];
-            k1[w] = reinterpret_cast<const uint32_t*>(kb + 8 * (D / 2))[w];
+            k0[i][w] = reinterpret_cast<const uint32_t*>(kb)[w];
+            k1[i][w] = reinterpret_cast<const uint32_t*>(kb + 8 * (D / 2))[w];
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int c = 0; c < 4; ++c) sc[nt][i][c] = 0.0f;
+    }
+    // (the products that add to one accumulator lie apart, so that they need not wait for one another)
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-            const uint32_t x0 = k0[w] >> 8, x1 = k1[w] >> 8;
+    for (int w = 0; w < KW; ++w) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                mma_f16_16816(sc[nt][i], k0[w] & 0x000F000Fu, k1[w] & 0x000F000Fu, k0[w] & 0x00F000F0u,
-                              k1[w] & 0x00F000F0u, s.qf[nt][2 * w][0], s.qf[nt][2 * w][1]);
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mma_f16_16816(sc[nt][i], k0[i][w] & 0x000F000Fu, k1[i][w] & 0x000F000Fu, k0[i][w] & 0x00F000F0u,
+                              k1[i][w] & 0x00F000F0u, s.qf[nt][2 * w][0], s.qf[nt][2 * w][1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t x0 = k0[i][w] >> 8, x1 = k1[i][w] >> 8;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
                 mma_f16_16816(sc[nt][i], x0 & 0x000F000Fu, x1 & 0x000F000Fu, x0 & 0x00F000F0u, x1 & 0x00F000F0u,
                               s.qf[nt][2 * w + 1][0], s.qf[nt][2 * w + 1][1]);
-            }
         }
     }
 #pragma unroll

@@ -605,3 +605,14 @@ def test_attention_of_one_long_sequence(r9q, Hq, Hk, D):
     n = on(np.array([1234], np.int32))
     o, lse = r9q.r9q_kv4_attention(q, cache, on(table), n, return_lse=True)
     check_attention(r9q, cache, table, [1234], q, o, lse)
+
+
+@pytest.mark.gpu
+def test_attention_of_thousands_of_sequences(r9q):
+    """More sequences than threads of a CTA, most of them short or empty."""
+    lens = [int(n) for n in np.random.default_rng(4).integers(0, 20, 2500)]
+    lens[77], lens[2499] = 700, 300
+    cache, table, _ = make_cache(r9q, lens, 1, 64, 16, 101)
+    q = rand((2500, 1, 2, 64), 102).to(dev())
+    o, lse = r9q.r9q_kv4_attention(q, cache, on(table), on(np.array(lens, np.int32)), return_lse=True)
+    check_attention(r9q, cache, table, lens, q, o, lse)
