@@ -58,7 +58,7 @@ constexpr int kNoWindow = 0x7FE00000;        // over any length (Lq is at most 2
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr uint32_t kNoGroup = 0xFFFFFFFFu;
 
-// Warps that an SM holds (registers), in CTAs of four, or, WIDE, in one.
+// The warps that an SM holds (registers) make CTAs of four or, wide, one CTA.
 constexpr int sm_warps(int D, int NT) { return 4 * ((D == 64 ? 4 : 3) - (NT - 1)); }
 constexpr int cta_warps(int D, int NT, bool wide) { return wide ? sm_warps(D, NT) : 4; }
 constexpr int ctas_per_sm(int D, int NT, bool wide) { return sm_warps(D, NT) / cta_warps(D, NT, wide); }
@@ -68,12 +68,10 @@ constexpr int stage_bytes(int D) { return kStep * D + kStep * 8; }
 constexpr int out_stride(int D) { return D + 4; }      // floats a row of the CTA's exchange takes
 constexpr int largest(int a, int b) { return a > b ? a : b; }
 // Shared memory: the rings, and in their place the warps' exchange [warps][R][out_stride] with references and sums,
-// and the joining of n partials of R rows: [n][R] weights, [R] sums and references, then [n][R] sums, whose place the
-// joined rows of the warps take (a float4 of every row a thread).
+// and the joining of partials: references and sums [R] each, then a float4 of every row a thread.
 constexpr int work_bytes(int D, int NT, bool wide) {
-    const int w = cta_warps(D, NT, wide), n = kMaxSms * ctas_per_sm(D, NT, wide) * 8 * NT * 4;
-    return largest(largest(w * kStages * stage_bytes(D), w * 8 * NT * (out_stride(D) + 2) * 4),
-                   n + 2 * 8 * NT * 4 + largest(n, w * 32 * 8 * NT * 16));
+    const int w = cta_warps(D, NT, wide), R = 8 * NT;
+    return largest(largest(w * kStages * stage_bytes(D), w * R * (out_stride(D) + 2) * 4), 2 * R * 4 + w * 32 * R * 16);
 }
 constexpr int smem_bytes(int D, int NT, bool wide) { return work_bytes(D, NT, wide) + 16; }   // and a flag
 
@@ -733,31 +731,26 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
             }
             __syncthreads();
             if (*joins) {
-                // The partials' weights first, in shared memory, then the weighted sum: the warps that hold a row's
-                // elements take every ROWS-th partial each (several rows of loads in flight) and meet at the end.
+                // The rows' references and sums over all partials first, then the weighted sum: the warps that hold a
+                // row's elements take every ROWS-th partial each (all its rows' loads in flight) and meet at the end.
                 const int n = c1 - c0 + 1;
-                float* wt = reinterpret_cast<float*>(smem);
+                float *total_m = reinterpret_cast<float*>(smem), *total_l = total_m + R, *meet = total_l + R;
                 auto slot = [&](int c) { return p.part + ((size_t)(c0 + c) * 2 + (c == 0 ? 1 : 0)) * kSlot; };
-                float *total_l = wt + n * R, *total_m = total_l + R, *sums = total_m + R, *meet = sums;
-                for (int k = tid; k < n * R; k += kThreads) {
-                    const float* from = slot(k / R) + R * D + k % R;
-                    wt[k] = k % R < live ? __ldcg(from) : kNegInf;
-                    sums[k] = k % R < live ? __ldcg(from + R) : 0.0f;
-                }
-                __syncthreads();
                 for (int row = warp; row < R; row += W) {
                     float top = kNegInf, sum = 0.0f;
-                    for (int c = lane; c < n; c += 32) top = fmaxf(top, wt[c * R + row]);
+                    auto join = [&](float m, float l) {
+                        const float both = fmaxf(top, m), base = both > kNegInf ? both : 0.0f;
+                        sum = sum * ex2(top - base) + l * ex2(m - base);
+                        top = both;
+                    };
+                    if (row < live)
+                        for (int c = lane; c < n; c += 32)
+                            join(__ldcg(slot(c) + R * D + row), __ldcg(slot(c) + R * D + R + row));
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    const float base = top > kNegInf ? top : 0.0f;
-                    for (int c = lane; c < n; c += 32) {
-                        const float k = ex2(wt[c * R + row] - base);
-                        wt[c * R + row] = k;
-                        sum = fmaf(k, sums[c * R + row], sum);
+                    for (int o = 16; o > 0; o >>= 1) {
+                        const float m = __shfl_xor_sync(0xffffffffu, top, o), l = __shfl_xor_sync(0xffffffffu, sum, o);
+                        join(m, l);
                     }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     if (lane == 0) {
                         total_l[row] = sum;
                         total_m[row] = top;
@@ -765,8 +758,12 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
                 }
                 __syncthreads();
                 float4 x[R];
+                float base[R];
 #pragma unroll
-                for (int row = 0; row < R; ++row) x[row] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int row = 0; row < R; ++row) {
+                    x[row] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    base[row] = total_m[row] > kNegInf ? total_m[row] : 0.0f;
+                }
 #pragma unroll 2
                 for (int c = row0; c < n; c += ROWS) {
                     const float* src = slot(c) + ed;
@@ -774,7 +771,7 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
                     for (int row = 0; row < R; ++row)
                         if (row < live) {
                             const float4 v = __ldcg(reinterpret_cast<const float4*>(src + row * D));
-                            const float k = wt[c * R + row];
+                            const float k = ex2(__ldcg(slot(c) + R * D + row) - base[row]);
                             x[row] = make_float4(fmaf(k, v.x, x[row].x), fmaf(k, v.y, x[row].y), fmaf(k, v.z, x[row].z),
                                                  fmaf(k, v.w, x[row].w));
                         }
@@ -816,8 +813,10 @@ cudaError_t launch(Kv4AttnParams p, int sms, cudaStream_t st) {
     p.chunks = fast_div((p.Lq * p.G + 8 * NT - 1) / (8 * NT));
     p.group = fast_div(p.G);
     p.page_groups = fast_div(p.c.page / 16);
-    // Few long items: one CTA an SM leaves a third as many partials to join.  Many items, or ones too short to give
-    // such a CTA's warps two steps each: more and smaller CTAs.
+    // Few long items: one CTA an SM leaves a third as many partials to join (one sequence of 131072 tokens 32.1 us
+    // against 38.9, two of 16000 16.9 against 19.6).  Many items, or ones too short to give such a CTA's warps two
+    // steps each: more and smaller CTAs (64 sequences of up to 16384 tokens 110 us against 132, 100 of 30 13.8 against
+    // 25.4).
     const int64_t items = (int64_t)p.B * p.c.heads * p.chunks.d, ctas = used_sms(sms);
     const bool wide = 8 * items <= ctas && items * (p.room / 16) >= ctas * 4 * cta_warps(D, NT, true);
     return wide ? launch<D, NT, true>(p, sms, st) : launch<D, NT, false>(p, sms, st);
