@@ -25,21 +25,13 @@
 // Both sums use the same weights, so the power of two cancels.  Scores, maxima,
 // sums and accumulators are fp32.
 //
-// Work is cut in groups of 16 keys, on the device, from the lengths, so that ragged
-// batches and single long sequences fill the GPU alike.  All CTAs are resident.  With
-// few items (sequence, kv head, row chunk) each is cut into equal parts, one a CTA;
-// with many, each CTA takes an equal, contiguous range of all items' groups (each item
-// counting some more for what it costs to begin), its ends moved to an item's end where
-// that is near.  The warps of a CTA take 32-key
-// steps of a part in turn, each with its own reference, and meet in shared memory at
-// its end.
-// An item that several CTAs share leaves fp32 partials; the CTA that arrives last
-// joins them in CTA order.
+// The warps of a CTA take 32-key steps of a part in turn, each with its own reference,
+// and meet in shared memory at its end.
 //
 // HBM bound (136 bytes a token and head at D = 128).  Lanes copy exactly the
 // bytes they will use (cp.async, 16 bytes, a ring of stages in shared memory per
 // warp), so a stage needs no barrier.
-#include "r9q_kv4.cuh"
+#include "r9q_kv4_attention.cuh"
 
 namespace r9q {
 
@@ -47,79 +39,22 @@ namespace {
 
 constexpr int kStep = 32;                    // keys a warp takes at a time: two groups of 16
 constexpr int kStages = 4;                   // steps in a warp's ring
-constexpr int kItemCost = 24;                // groups that take as long as beginning and ending an item
-constexpr int kMinExponent = 67;             // value steps under 2^-60 count as that (keeps the sums finite)
-constexpr int kHeadroom = 8;                 // weights at the reference score are 2^8 to 2^9
-constexpr int kSlack = 6;                    // powers of two a lane's weights may pass it by
-// A lowest value counts as a step of 2^-10 of it: the sums of p lv are kept in the weights' scale.
-constexpr int kLowestBits = 10;
-constexpr float kLowestShare = 1.0f / (1 << kLowestBits);
-constexpr int kNoWindow = 0x7FE00000;        // over any length (Lq is at most 2^20)
-constexpr float kLn2 = 0.69314718055994531f;
-constexpr uint32_t kNoGroup = 0xFFFFFFFFu;
 
 // The warps that an SM holds (registers) make CTAs of four or, wide, one CTA.
 constexpr int sm_warps(int D, int NT) { return 4 * ((D == 64 ? 4 : 3) - (NT - 1)); }
 constexpr int cta_warps(int D, int NT, bool wide) { return wide ? sm_warps(D, NT) : 4; }
 constexpr int ctas_per_sm(int D, int NT, bool wide) { return sm_warps(D, NT) / cta_warps(D, NT, wide); }
-constexpr int kMaxSms = 160;                           // more are left idle
 
 constexpr int stage_bytes(int D) { return kStep * D + kStep * 8; }
 constexpr int out_stride(int D) { return D + 4; }      // floats a row of the CTA's exchange takes
-constexpr int largest(int a, int b) { return a > b ? a : b; }
 // Shared memory: the rings, and in their place the warps' exchange [warps][R][out_stride] with references and sums,
-// and the joining of partials: references and sums [R] each, then a float4 of every row a thread.
+// and the joining of partials.
 constexpr int work_bytes(int D, int NT, bool wide) {
     const int w = cta_warps(D, NT, wide), R = 8 * NT;
-    return largest(largest(w * kStages * stage_bytes(D), w * R * (out_stride(D) + 2) * 4), 2 * R * 4 + w * 32 * R * 16);
+    return largest(largest(w * kStages * stage_bytes(D), w * R * (out_stride(D) + 2) * 4), join_bytes(R, w * 32, R));
 }
 constexpr int smem_bytes(int D, int NT, bool wide) { return work_bytes(D, NT, wide) + 16; }   // and a flag
 
-// Copies a lane's share of one group of 16 tokens into a stage, if `live`: its two K rows' parts (8 rows apart), its
-// V pieces, and a (step, lowest) pair.
-template <int D>
-__device__ __forceinline__ void copy_group(bool live, uint32_t k_dst, const uint8_t* k, uint32_t v_dst,
-                                           const uint8_t* v, uint32_t pair_dst, const uint32_t* pair) {
-    if constexpr (D == 128) {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
-            "@p cp.async.cg.shared.global [%1], [%2], 16;\n\t"
-            "@p cp.async.cg.shared.global [%1+512], [%2+512], 16;\n\t"
-            "@p cp.async.cg.shared.global [%3], [%4], 16;\n\t"
-            "@p cp.async.cg.shared.global [%3+512], [%4+512], 16;\n\t"
-            "@p cp.async.ca.shared.global [%5], [%6], 4;\n\t}" ::"r"((int)live),
-            "r"(k_dst), "l"(k), "r"(v_dst), "l"(v), "r"(pair_dst), "l"(pair)
-            : "memory");
-    } else {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t"
-            "@p cp.async.ca.shared.global [%1], [%2], 8;\n\t"
-            "@p cp.async.ca.shared.global [%1+256], [%2+256], 8;\n\t"
-            "@p cp.async.cg.shared.global [%3], [%4], 16;\n\t"
-            "@p cp.async.ca.shared.global [%5], [%6], 4;\n\t}" ::"r"((int)live),
-            "r"(k_dst), "l"(k), "r"(v_dst), "l"(v), "r"(pair_dst), "l"(pair)
-            : "memory");
-    }
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
 // Transposes an 8x8 matrix of 16-bit values held two to a lane.
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
     uint32_t r;
@@ -135,48 +70,6 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __noinline__ long long div64(long long a, long long b) { return a / b; }
-
-// A sequence's keys and the groups an item of it has.  `room`: tokens that its pages
-// can hold; `reach`: the most tokens that its new ones see.
-struct Span {
-    int len, g0;             // tokens; first group that holds a visible key
-    int groups;              // at least one (an empty sequence's items write zeros)
-};
-__device__ __noinline__ Span span_of(const int32_t* at, int room, int reach, int* err) {
-    Span s;
-    int len = *at;
-    if (len < 0 || len > room) {
-        if (threadIdx.x == 0) record_error(err, kErrArg);
-        len = len < 0 ? 0 : room;
-    }
-    s.len = len;
-    s.g0 = len > reach ? (len - reach) >> 4 : 0;
-    const int n = ((len + 15) >> 4) - s.g0;
-    s.groups = n > 0 ? n : 1;
-    return s;
-}
-
-// The warp's inclusive scan of one value a lane; `total` over all.
-__device__ __forceinline__ long long warp_scan(long long v, long long& total) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += x;
-    }
-    total = __shfl_sync(0xffffffffu, v, 31);
-    return v;
-}
-
-// The log of the sum of exponentials, from the sum of weights l and their reference m
-// (both of powers of two).
-__device__ __forceinline__ float log_sum_exp(float m, float l) {
-    return l > 0.0f || l != l ? (m + log2f(l)) * kLn2 : __int_as_float(0xFF800000);
-}
-
-constexpr float kNegInf = -__builtin_huge_valf();
-
 // A warp's state for NT tiles of 8 rows; a lane has columns (rows of the query)
 // 2j and 2j + 1 of each.
 template <int D, int NT>
@@ -398,90 +291,9 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = lane >> 2, j = lane & 3;
-    const int rows = p.Lq * p.G, chunks = p.chunks.d;
-    const int items_per_seq = p.c.heads * chunks;
-    const long long items = (long long)p.B * items_per_seq, ctas = gridDim.x;
-
-    // ---- what this CTA does: every warp finds it for itself, a lane for every so many sequences ----
-    const bool parted = 2 * items <= ctas;   // one part of one item a CTA
-    const int begin_cost = parted ? 0 : kItemCost;
-    auto span = [&](int b) { return span_of(p.lens + b, p.room, p.reach, p.err); };
-    const int per_lane = (p.B + 31) / 32;
-    const int b_first = lane * per_lane, b_end = min(p.B, b_first + per_lane);
-    long long mine = 0, total;
-#pragma unroll 1
-    for (int b = b_first; b < b_end; ++b) mine += span(b).groups + begin_cost;
-    mine *= items_per_seq;
-    long long upto = warp_scan(mine, total);
-    long long per;                           // groups of a part, or of a CTA's range
-    if (parted) {
-        // The even share, if parts of that size are no more than the CTAs; else total / (ctas - items): the sum of
-        // ceil(groups / per) over the items is at most total / per + items.
-        const long long all = total;
-        per = (all + ctas - 1) / ctas;
-        for (int attempt = 1;; ++attempt) {
-            if (per < kMinGroups) per = kMinGroups;
-            mine = 0;                        // from here on: parts
-#pragma unroll 1
-            for (int b = b_first; b < b_end; ++b) mine += (span(b).groups + (int)per - 1) / (int)per;
-            mine *= items_per_seq;
-            upto = warp_scan(mine, total);
-            if (total <= ctas || attempt == 2) break;
-            per = (all + ctas - items - 1) / (ctas - items);
-        }
-    } else {
-        per = div64(total + ctas - 1, ctas);
-        if (per < kMinGroups) per = kMinGroups;
-    }
-    // An end of a range inside an item goes to the item's end where that is within `snap` groups of it.
-    auto snap_of = [&](int groups) { return min(min(8, (int)min(per / 4, 8ll)), (groups - 1) / 2); };
-    long long u = parted ? blockIdx.x : blockIdx.x * per;
-    if (u >= total) return;
-    const bool here = u >= upto - mine && u < upto;      // one lane's
-    int b = b_first;
-    long long seq_first = upto - mine;       // first part or group of sequence b
-    if (here) {
-#pragma unroll 1
-        for (;; ++b) {
-            const int g = span(b).groups;
-            const long long n = (long long)(parted ? (g + (int)per - 1) / (int)per : g + begin_cost) * items_per_seq;
-            if (u < seq_first + n) break;
-            seq_first += n;
-        }
-    }
-    const int owner = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-    b = __shfl_sync(0xffffffffu, b, owner);
-    seq_first = __shfl_sync(0xffffffffu, seq_first, owner);
-    Span sp = span(b);
-    int parts = parted ? (sp.groups + (int)per - 1) / (int)per : 0;
-    int even = parted ? (sp.groups + parts - 1) / parts : 0;    // groups of this sequence's parts
-    if (parted) parts = (sp.groups + even - 1) / even;
-    // (rounding may leave the last parts counted above without groups)
-    const int parts_counted = parted ? (sp.groups + (int)per - 1) / (int)per : 0;
-    long long range_end = 0;
-    auto moved = [&](long long x, long long first, int groups) {      // where the end x of a range goes
-        const int n = groups + begin_cost, snap = snap_of(groups);
-        const long long item_at = first + div64(x - first, n) * n;
-        return x - item_at <= begin_cost + snap ? item_at : item_at + n - x <= snap ? item_at + n : x;
-    };
-    if (!parted) {
-        const long long end = u + per;
-        u = moved(u, seq_first, sp.groups);
-        // the end may lie in a later sequence
-        if (end >= total) {
-            range_end = total;
-        } else {
-            long long first = seq_first;
-            int be = b, g = sp.groups;
-#pragma unroll 1
-            while (end >= first + (long long)(g + begin_cost) * items_per_seq) {
-                first += (long long)(g + begin_cost) * items_per_seq;
-                g = span(++be).groups;
-            }
-            range_end = moved(end, first, g);
-        }
-    }
-
+    const int rows = p.Lq * p.G;
+    Walk walk;
+    if (!walk.start(p, kMinGroups)) return;
     uint8_t* ring = smem + warp * (ST * stage_bytes(D));
     const uint32_t ring_u = smem_u32(ring);
     const uint8_t* k_lane = p.c.k + lane * (KW * 4);
@@ -489,38 +301,10 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
     const uint32_t* pair_lane = (lane < 16 ? p.c.kp : p.c.vp) + (lane & 15);
     const uint32_t pair_dst = kStep * D + (lane >> 4) * (kStep * 4) + ((lane & 7) * 4 + ((lane >> 3) & 1)) * 4;
 
-    for (;;) {
-        int item, g_begin, g_end, c0, c1;    // the part, and the CTAs that share its item
-        if (parted) {
-            const int at = (int)(u - seq_first);
-            item = at / parts_counted;
-            const int part = at - item * parts_counted;
-            if (part >= parts) return;
-            g_begin = part * even;
-            g_end = min(sp.groups, g_begin + even);
-            c0 = (int)(seq_first + (long long)item * parts_counted);
-            c1 = c0 + parts - 1;
-        } else {
-            if (u >= range_end) return;
-#pragma unroll 1
-            while (u >= seq_first + (long long)(sp.groups + begin_cost) * items_per_seq) {
-                seq_first += (long long)(sp.groups + begin_cost) * items_per_seq;
-                sp = span(++b);
-            }
-            const int n = sp.groups + begin_cost, snap = snap_of(sp.groups);
-            item = (int)div64(u - seq_first, n);
-            const long long first = seq_first + (long long)item * n;
-            g_begin = max(0, (int)(u - first) - begin_cost);
-            g_end = (int)min((long long)n, range_end - first) - begin_cost;
-            c0 = (int)div64(first + begin_cost + snap, per);
-            c1 = (int)div64(first + n - snap - 1, per);
-            u = first + begin_cost + g_end;
-        }
-        const bool whole = g_begin == 0 && g_end == sp.groups;
-        const bool begins = g_begin == 0;
-        g_begin += sp.g0;
-        g_end += sp.g0;
-        const int hk = item / p.chunks, chunk = item - hk * chunks;
+    Part it;
+    while (walk.next(p, it)) {
+        const Span& sp = walk.sp;
+        const int b = it.b, hk = it.hk, chunk = it.chunk, g_begin = it.g_begin, g_end = it.g_end;
 
         // ---- the warp's steps ----
         const int steps_all = (g_end - g_begin + 1) >> 1;
@@ -530,15 +314,7 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
         // Lane x holds the cache's token index of the x-th group of the next 16 steps, and of the 16 after them.
         auto groups_of = [&](int first_step) {
             const int g = g_begin + 2 * ((first_step + (lane >> 1)) * W + warp) + (lane & 1);
-            uint32_t at = kNoGroup;
-            if (g < gmax) {
-                const int pg = g / p.page_groups, page = table[pg];
-                if (page >= 0 && page < p.c.pages)
-                    at = ((uint32_t)page * p.c.heads + hk) * p.c.page + (g - pg * p.page_groups.d) * 16;
-                else
-                    record_error(p.err, kErrArg);
-            }
-            return at;
+            return g < gmax ? find_group(p, table, g, hk) : kNoGroup;
         };
         uint32_t groups_now = 0, groups_next = groups_of(0);
 
@@ -687,17 +463,7 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
         // a thread takes four elements of every (kThreads / (D / 4))-th row
         const int ed = (tid % (D / 4)) * 4, row0 = tid / (D / 4);
         constexpr int ROWS = kThreads / (D / 4);
-        constexpr size_t kSlot = (size_t)R * (D + 2);      // floats of a partial: [R][D], references, sums
-        auto finish = [&](int row, float4 x, float sum, float top) {
-            const int grow = chunk * R + row, i = grow / p.group;
-            const int64_t out = ((int64_t)b * p.Lq + i) * (p.c.heads * p.G) + hk * p.G + (grow - i * p.G);
-            const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-            *reinterpret_cast<uint2*>(p.o + out * D + ed) =
-                make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-            if (p.lse && ed == 0) p.lse[out] = log_sum_exp(top, sum);
-        };
-        // slot 1: the item begins in this CTA; slot 0: it began in an earlier one
-        float* part = p.part + ((size_t)blockIdx.x * 2 + (begins ? 1 : 0)) * kSlot;
+        float* part = partial_of<D, R>(p, blockIdx.x, it.begins);
 #pragma unroll 1
         for (int row = row0; row < live; row += ROWS) {
             float top = kNegInf, sum = 0.0f;
@@ -712,8 +478,8 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
                 sum = fmaf(k, ex_l[w * R + row], sum);
                 x = make_float4(fmaf(k, v.x, x.x), fmaf(k, v.y, x.y), fmaf(k, v.z, x.z), fmaf(k, v.w, x.w));
             }
-            if (whole) {
-                finish(row, x, sum, top);
+            if (it.whole) {
+                finish_row<D>(p, it, chunk * R + row, ed, x, sum, top);
             } else {
                 *reinterpret_cast<float4*>(part + row * D + ed) = x;
                 if (ed == 0) {
@@ -722,7 +488,9 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
                 }
             }
         }
-        if (!whole) {
+        if (!it.whole) {
+            int c0, c1;
+            walk.sharers(c0, c1);
             __syncthreads();
             if (tid == 0) {
                 const bool last = arrive(p.done + c0) == c1 - c0;
@@ -730,73 +498,13 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
                 *joins = last;
             }
             __syncthreads();
-            if (*joins) {
-                // The rows' references and sums over all partials first, then the weighted sum: the warps that hold a
-                // row's elements take every ROWS-th partial each (all its rows' loads in flight) and meet at the end.
-                const int n = c1 - c0 + 1;
-                float *total_m = reinterpret_cast<float*>(smem), *total_l = total_m + R, *meet = total_l + R;
-                auto slot = [&](int c) { return p.part + ((size_t)(c0 + c) * 2 + (c == 0 ? 1 : 0)) * kSlot; };
-                for (int row = warp; row < R; row += W) {
-                    float top = kNegInf, sum = 0.0f;
-                    auto join = [&](float m, float l) {
-                        const float both = fmaxf(top, m), base = both > kNegInf ? both : 0.0f;
-                        sum = sum * ex2(top - base) + l * ex2(m - base);
-                        top = both;
-                    };
-                    if (row < live)
-                        for (int c = lane; c < n; c += 32)
-                            join(__ldcg(slot(c) + R * D + row), __ldcg(slot(c) + R * D + R + row));
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) {
-                        const float m = __shfl_xor_sync(0xffffffffu, top, o), l = __shfl_xor_sync(0xffffffffu, sum, o);
-                        join(m, l);
-                    }
-                    if (lane == 0) {
-                        total_l[row] = sum;
-                        total_m[row] = top;
-                    }
-                }
-                __syncthreads();
-                float4 x[R];
-                float base[R];
-#pragma unroll
-                for (int row = 0; row < R; ++row) {
-                    x[row] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    base[row] = total_m[row] > kNegInf ? total_m[row] : 0.0f;
-                }
-#pragma unroll 2
-                for (int c = row0; c < n; c += ROWS) {
-                    const float* src = slot(c) + ed;
-#pragma unroll
-                    for (int row = 0; row < R; ++row)
-                        if (row < live) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + row * D));
-                            const float k = ex2(__ldcg(slot(c) + R * D + row) - base[row]);
-                            x[row] = make_float4(fmaf(k, v.x, x[row].x), fmaf(k, v.y, x[row].y), fmaf(k, v.z, x[row].z),
-                                                 fmaf(k, v.w, x[row].w));
-                        }
-                }
-#pragma unroll
-                for (int row = 0; row < R; ++row)
-                    *reinterpret_cast<float4*>(meet + ((size_t)row0 * R + row) * D + ed) = x[row];
-                __syncthreads();
-                for (int row = row0; row < live; row += ROWS) {
-                    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                    for (int k = 0; k < ROWS; ++k) {
-                        const float4 v = *reinterpret_cast<const float4*>(meet + ((size_t)k * R + row) * D + ed);
-                        y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
-                    }
-                    finish(row, y, total_l[row], total_m[row]);
-                }
-            }
+            if (*joins) join_partials<D, R, kThreads>(p, it, c0, c1, live, reinterpret_cast<float*>(smem));
         }
-        if (parted) return;
+        if (walk.parted) return;
         __syncthreads();                     // the exchange is free for the next item's ring
     }
 }
 
-int used_sms(int sms) { return sms < kMaxSms ? sms : kMaxSms; }
 int row_tiles(int64_t rows) { return rows <= 8 ? 1 : 2; }
 
 template <int D, int NT, bool WIDE>
