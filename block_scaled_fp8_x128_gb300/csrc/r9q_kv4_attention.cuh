@@ -76,7 +76,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-__device__ __noinline__ long long div64(long long a, long long b) { return a / b; }
+static __device__ __noinline__ long long div64(long long a, long long b) { return a / b; }
 
 // A sequence's keys and the groups an item of it has.  `room`: tokens that its pages
 // can hold; `reach`: the most tokens that its new ones see.
@@ -84,7 +84,7 @@ struct Span {
     int len, g0;             // tokens; first group that holds a visible key
     int groups;              // at least one (an empty sequence's items write zeros)
 };
-__device__ __noinline__ Span span_of(const int32_t* at, int room, int reach, int* err) {
+static __device__ __noinline__ Span span_of(const int32_t* at, int room, int reach, int* err) {
     Span s;
     int len = *at;
     if (len < 0 || len > room) {
