@@ -208,11 +208,6 @@ struct Kv4AttnParams {
 // CTAs of the launch, and floats of `part` for them.
 int kv4_attention_ctas(int D, int64_t rows, int sms);
 size_t kv4_attention_part_floats(int D, int64_t rows, int sms);
-// More than 16 rows of a key-value head, D = 128: the tcgen05 kernel, in chunks of 32 rows.
-constexpr bool kv4_attention_uses_tc(int D, int64_t rows) { return D == 128 && rows > 16; }
-constexpr int kv4_attention_tc_rows(int64_t rows) { return 32; }
-constexpr int kv4_attention_tc_ctas(int chunk_rows) { return chunk_rows == 32 ? 2 : 1; }     // an SM
-cudaError_t launch_kv4_attention_tc(const Kv4AttnParams& p, int sms, cudaStream_t st);
 // Workspace bytes of R9Q_OP_QK_NORM_ROPE_BWD and R9Q_OP_KV4_ATTENTION (M rows, N = D).
 size_t decode_workspace(int op, int64_t M, int64_t N, int* rc);
 cudaError_t launch_kv4_attention(int D, const Kv4AttnParams& p, int sms, cudaStream_t st);

@@ -534,17 +534,14 @@ cudaError_t launch(Kv4AttnParams p, int sms, cudaStream_t st) {
 
 // (of the launch with more of them)
 int kv4_attention_ctas(int D, int64_t rows, int sms) {
-    if (kv4_attention_uses_tc(D, rows)) return used_sms(sms) * kv4_attention_tc_ctas(kv4_attention_tc_rows(rows));
     return used_sms(sms) * ctas_per_sm(D, row_tiles(rows), false);
 }
 
 size_t kv4_attention_part_floats(int D, int64_t rows, int sms) {
-    const int chunk = kv4_attention_uses_tc(D, rows) ? kv4_attention_tc_rows(rows) : 8 * row_tiles(rows);
-    return (size_t)kv4_attention_ctas(D, rows, sms) * 2 * chunk * (D + 2);
+    return (size_t)kv4_attention_ctas(D, rows, sms) * 2 * (8 * row_tiles(rows)) * (D + 2);
 }
 
 cudaError_t launch_kv4_attention(int D, const Kv4AttnParams& p, int sms, cudaStream_t st) {
-    if (kv4_attention_uses_tc(D, (int64_t)p.Lq * p.G)) return launch_kv4_attention_tc(p, sms, st);
     const bool one = row_tiles((int64_t)p.Lq * p.G) == 1;
     if (D == 64) return one ? launch<64, 1>(p, sms, st) : launch<64, 2>(p, sms, st);
     return one ? launch<128, 1>(p, sms, st) : launch<128, 2>(p, sms, st);

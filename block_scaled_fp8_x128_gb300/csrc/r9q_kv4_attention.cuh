@@ -1,7 +1,6 @@
-// What the two kernels of the attention over the 4-bit cache share (few rows:
-// r9q_kv4_attention.cu, many: r9q_kv4_attention_tc.cu): how the work is cut, the copies
-// of a group of 16 tokens, the partial results of an item that several CTAs have, and
-// how they are joined.
+// The frame of the attention over the 4-bit cache (r9q_kv4_attention.cu): how the work is
+// cut, the copies of a group of 16 tokens, the partial results of an item that several
+// CTAs have, and how they are joined.
 //
 // An item is a sequence's row chunk (R query rows that share a key-value head); its work
 // is counted in groups of 16 keys.  Work is cut on the device, from the lengths, so that ragged
