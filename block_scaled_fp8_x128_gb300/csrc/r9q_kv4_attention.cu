@@ -51,7 +51,7 @@ constexpr int out_stride(int D) { return D + 4; }      // floats a row of the CT
 // and the joining of partials.
 constexpr int work_bytes(int D, int NT, bool wide) {
     const int w = cta_warps(D, NT, wide), R = 8 * NT;
-    return largest(largest(w * kStages * stage_bytes(D), w * R * (out_stride(D) + 2) * 4), join_bytes(R, w * 32, R));
+    return largest(largest(w * kStages * stage_bytes(D), w * R * (out_stride(D) + 2) * 4), join_bytes(R, w * 32));
 }
 constexpr int smem_bytes(int D, int NT, bool wide) { return work_bytes(D, NT, wide) + 16; }   // and a flag
 

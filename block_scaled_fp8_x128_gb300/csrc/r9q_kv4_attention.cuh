@@ -293,9 +293,7 @@ __device__ __forceinline__ float* partial_of(const Kv4AttnParams& p, int cta, bo
 }
 
 // Shared memory of join_partials.
-template <int R>
-constexpr int kJoinRows = R <= 16 ? R : 8;   // rows that a thread has at a time
-constexpr int join_bytes(int R, int threads, int rows) { return 2 * R * 4 + threads * rows * 16; }
+constexpr int join_bytes(int R, int threads) { return 2 * R * 4 + threads * R * 16; }
 
 // Joins an item's partials, all threads of the CTA that arrived last: the rows' references and sums over all partials
 // first, then the weighted sum.  The warps that hold a row's elements take every ROWS-th partial each (all the rows'
@@ -303,7 +301,7 @@ constexpr int join_bytes(int R, int threads, int rows) { return 2 * R * 4 + thre
 template <int D, int R, int THREADS>
 __device__ __forceinline__ void join_partials(const Kv4AttnParams& p, const Part& it, int c0, int c1, int live,
                                               float* smem) {
-    constexpr int ROWS = THREADS / (D / 4), RB = kJoinRows<R>;
+    constexpr int ROWS = THREADS / (D / 4);
     const int tid = threadIdx.x, lane = tid & 31, ed = (tid % (D / 4)) * 4, row0 = tid / (D / 4), n = c1 - c0 + 1;
     float *total_m = smem, *total_l = total_m + R, *meet = total_l + R;
     auto slot = [&](int c) { return partial_of<D, R>(p, c0 + c, c == 0); };
@@ -327,41 +325,36 @@ __device__ __forceinline__ void join_partials(const Kv4AttnParams& p, const Part
         }
     }
     __syncthreads();
-#pragma unroll 1
-    for (int rb = 0; rb < live; rb += RB) {
-        float4 x[RB];
-        float base[RB];
+    float4 x[R];
+    float base[R];
 #pragma unroll
-        for (int row = 0; row < RB; ++row) {
-            x[row] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            base[row] = total_m[rb + row] > kNegInf ? total_m[rb + row] : 0.0f;
-        }
+    for (int row = 0; row < R; ++row) {
+        x[row] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        base[row] = total_m[row] > kNegInf ? total_m[row] : 0.0f;
+    }
 #pragma unroll 2
-        for (int c = row0; c < n; c += ROWS) {
-            const float* src = slot(c) + rb * D + ed;
+    for (int c = row0; c < n; c += ROWS) {
+        const float* src = slot(c) + ed;
 #pragma unroll
-            for (int row = 0; row < RB; ++row)
-                if (rb + row < live) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(src + row * D));
-                    const float k = ex2(__ldcg(slot(c) + R * D + rb + row) - base[row]);
-                    x[row] = make_float4(fmaf(k, v.x, x[row].x), fmaf(k, v.y, x[row].y), fmaf(k, v.z, x[row].z),
-                                         fmaf(k, v.w, x[row].w));
-                }
-        }
-#pragma unroll
-        for (int row = 0; row < RB; ++row)
-            *reinterpret_cast<float4*>(meet + ((size_t)row0 * RB + row) * D + ed) = x[row];
-        __syncthreads();
-        for (int row = row0; row < RB && rb + row < live; row += ROWS) {
-            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int k = 0; k < ROWS; ++k) {
-                const float4 v = *reinterpret_cast<const float4*>(meet + ((size_t)k * RB + row) * D + ed);
-                y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+        for (int row = 0; row < R; ++row)
+            if (row < live) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(src + row * D));
+                const float k = ex2(__ldcg(slot(c) + R * D + row) - base[row]);
+                x[row] = make_float4(fmaf(k, v.x, x[row].x), fmaf(k, v.y, x[row].y), fmaf(k, v.z, x[row].z),
+                                     fmaf(k, v.w, x[row].w));
             }
-            finish_row<D>(p, it, it.chunk * R + rb + row, ed, y, total_l[rb + row], total_m[rb + row]);
+    }
+#pragma unroll
+    for (int row = 0; row < R; ++row) *reinterpret_cast<float4*>(meet + ((size_t)row0 * R + row) * D + ed) = x[row];
+    __syncthreads();
+    for (int row = row0; row < live; row += ROWS) {
+        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(meet + ((size_t)k * R + row) * D + ed);
+            y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
         }
-        __syncthreads();
+        finish_row<D>(p, it, it.chunk * R + row, ed, y, total_l[row], total_m[row]);
     }
 }
 

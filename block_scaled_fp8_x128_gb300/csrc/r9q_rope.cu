@@ -130,6 +130,36 @@ __device__ __forceinline__ Turn load_turn(const RopeParams& p, int64_t pos, int 
     return u;
 }
 
+// What load_turn() reads, to be loaded ahead: nothing without SPLIT, where turn_of() loads.
+struct Angles {
+    float4 c, s;
+};
+template <int D, bool SPLIT>
+__device__ __forceinline__ Angles load_angles(const RopeParams& p, int64_t pos, int l, int lane) {
+    Angles x = {};
+    if (!SPLIT) return x;
+    if (pos < 0 || pos >= p.npos) {
+        if (lane == 0) record_error(p.err, kErrArg);
+        const float nan = __int_as_float(0x7FC00000);
+        x.c = x.s = make_float4(nan, nan, nan, nan);
+        return x;
+    }
+    x.c = load4(p.cos + pos * (D / 2) + 4 * l, true);
+    x.s = load4(p.sin + pos * (D / 2) + 4 * l, true);
+    return x;
+}
+template <int D, bool SPLIT>
+__device__ __forceinline__ Turn turn_of(const RopeParams& p, const Angles& x, int64_t pos, int lane) {
+    if (!SPLIT) return load_turn<D, SPLIT>(p, pos, lane);
+    Turn u;
+    u.src = lane;
+    u.c = eight_of(x.c, x.c);
+    u.s = eight_of(x.s, x.s);
+    u.s.v[0] ^= kSigns;
+    u.s.v[1] ^= kSigns;
+    return u;
+}
+
 // The other elements of the lane's pairs; `raw` the lane's elements as packed bf16, x unpacked.
 template <bool SPLIT>
 __device__ __forceinline__ Eight partner(const uint4& v, const Eight& x, const Turn& u, int interleaved) {
@@ -623,76 +653,125 @@ __global__ void __launch_bounds__(kThreads) gather_groups_kernel(const Kv4Cache 
 // With g = R^T dy (the turn by the opposite angle) and xh = x r:
 //   dw = sum over tokens and heads of g xh,
 //   dx = r (w g - xh mean(w g xh)) = r w g - x r^3 sum(w g x) / D.
-// r is computed again from x: that reads nothing that dx does not need.  One block of
-// 16 warps an SM walks the (token, part) units of the query heads, then of the key
-// heads, in a fixed order, each lane summing its elements' dw in 32 bits; a block's
-// sums go to `part`, and the block that finishes last adds the blocks' sums in their
-// order, so dw does not depend on timing.
+// r is computed again from x: that reads nothing that dx does not need.  A unit is a
+// token's query or key heads, kBwdUnroll loads of a warp at a time; the warps of one
+// block an SM take equal, contiguous ranges of all units, so that a token's angles are
+// loaded once, and ahead.  A warp copies its next unit's dy and x to shared memory while it works
+// on one, and each lane sums its elements' dw in 32 bits; a block's sums go to `part`,
+// and the block that finishes last adds the blocks' sums in their order, all loads in
+// flight, so dw does not depend on timing.
+//
+// Bound: HBM, once the batch is long.  12 warps have 168 registers each, which lets
+// the four vectors' reductions overlap.  32 + 8 heads of 128 (us, 12 warps / 16): 256
+// tokens 5.6/5.9, 1024 9.2/10.2, 4096 25.4/24.4, 16384 81/84 (8 warps: 98; the bytes
+// alone: 75).  A third stage makes no difference, and loads into registers one
+// unit ahead, in place of the copies, took 35 at 4096.  Of the 25, about 5 are the
+// launch, the first loads and the last block's sums.
 struct BackwardArgs {
     HeadsIn dqo, dko, q, k;
     RopeParams rope;
     HeadsOut dq, dk;
     float *dwq, *dwk, *part;
     int* done;
-    FastDiv q_parts, k_parts;    // units that a token's query and key heads take
+    FastDiv parts;               // units of a token: those of its query heads, then of its key heads
+    int q_parts, per_warp, more; // a warp has per_warp units, the first `more` warps one more
 };
-constexpr int kBwdThreads = 512;
+constexpr int kBwdThreads = 384;
 constexpr int kBwdUnroll = 4;
+constexpr int kBwdStages = 2;
+constexpr int kBwdStage = kBwdUnroll * 1024;                 // bytes: the warp's parts of dy and x
+constexpr int kBwdSmem = kBwdThreads / 32 * kBwdStages * kBwdStage;
+static_assert(kBwdSmem >= kBwdThreads / 32 * 256 * 4 && kBwdSmem >= kBwdThreads * 16, "room for the sums");
+
+// 16 bytes of each to shared memory, zeros where not `live`.
+__device__ __forceinline__ void copy16(bool live, uint32_t g_dst, const void* g, uint32_t x_dst, const void* x) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %4;\n\tcp.async.cg.shared.global [%2], [%3], 16, %4;" ::"r"(
+                     g_dst),
+                 "l"(g), "r"(x_dst), "l"(x), "r"(live ? 16 : 0)
+                 : "memory");
+}
 
 template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const BackwardArgs a) {
     begin_chained();
     constexpr int NL = D / 8, NV = 32 / NL, HR = kBwdUnroll * NV, NW = kBwdThreads / 32;
-    __shared__ __align__(16) float sums[NW * 128];       // the warps' sums [NW][D]; at the end four floats a thread
+    extern __shared__ __align__(16) uint8_t smem[];          // the ring; at the end the warps' sums, then four a thread
+    float* sums = reinterpret_cast<float*>(smem);
     const RopeParams& p = a.rope;
     const int lane = threadIdx.x & 31, l = lane & (NL - 1), sub = lane / NL, warp = threadIdx.x >> 5;
-#pragma unroll 1
-    for (int kind = 0; kind < 2; ++kind) {
-        const HeadsIn& gin = kind ? a.dko : a.dqo;
-        const HeadsIn& xin = kind ? a.k : a.q;
-        const HeadsOut& out = kind ? a.dk : a.dq;
-        const FastDiv& parts = kind ? a.k_parts : a.q_parts;
-        const float* wp = kind ? p.wk : p.wq;
-        const Eight w = load_weight<D, SPLIT>(wp, l);
-        Eight dw = {{0, 0, 0, 0}};
-        const int units = (int)p.T * parts.d, stride = gridDim.x * NW;
-        // the last blocks take the key heads' first units, which their share of the query heads leaves room for
-        int unit = (kind ? gridDim.x - 1 - blockIdx.x : blockIdx.x) * NW + warp;
-        uint4 gn[kBwdUnroll], xn[kBwdUnroll];
-        int64_t pos_next = 0;
-        auto load = [&](int at) {
-            const int t = at / parts, h0 = (at - t * parts.d) * HR + sub;
-            pos_next = load_pos(p, t);
-            const uint16_t* gp = gin.p + t * gin.ts + h0 * gin.hs;
-            const uint16_t* xp = xin.p + t * xin.ts + h0 * xin.hs;
+    const int id = blockIdx.x * NW + warp, begin = id * a.per_warp + min(id, a.more),
+              end = begin + a.per_warp + (id < a.more ? 1 : 0);
+    Eight dw = {{0, 0, 0, 0}}, dw_other = dw;                // of the unit's kind, and of the other
+    int kind = 0;
+    if (begin < end) {
+        int t = begin / a.parts, part = begin - t * a.parts.d;
+        // the ring: kBwdStages units of the warp, [g, x][i][lane] 16 bytes each
+        const uint32_t ring = smem_u32(smem) + warp * (kBwdStages * kBwdStage) + lane * 16;
+        int t_ahead = t, part_ahead = part, ahead = begin, fill = 0;
+        auto issue = [&] {
+            if (ahead < end) {
+                const bool key = part_ahead >= a.q_parts;
+                const HeadsIn& gin = key ? a.dko : a.dqo;
+                const HeadsIn& xin = key ? a.k : a.q;
+                const int h = (key ? part_ahead - a.q_parts : part_ahead) * HR + sub;
+                const uint16_t* gp = gin.p + t_ahead * gin.ts + h * gin.hs + 8 * l;
+                const uint16_t* xp = xin.p + t_ahead * xin.ts + h * xin.hs + 8 * l;
+                const uint32_t to = ring + fill * kBwdStage;
 #pragma unroll
-            for (int i = 0; i < kBwdUnroll; ++i) {
-                gn[i] = xn[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (h0 + i * NV < xin.heads) {
-                    gn[i] = load_bf16<D, SPLIT>(gp, l);
-                    xn[i] = load_bf16<D, SPLIT>(xp, l);
+                for (int i = 0; i < kBwdUnroll; ++i) {
+                    copy16(h + i * NV < xin.heads, to + i * 512, gp, to + (kBwdUnroll + i) * 512, xp);
+                    gp += NV * gin.hs;
+                    xp += NV * xin.hs;
                 }
-                gp += NV * gin.hs;
-                xp += NV * xin.hs;
+                ++ahead;
+                fill = fill == kBwdStages - 1 ? 0 : fill + 1;
+                if (++part_ahead == a.parts.d) {
+                    part_ahead = 0;
+                    ++t_ahead;
+                }
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        if (unit < units) load(unit);
-        for (; unit < units; unit += stride) {
-            const int t = unit / parts, h0 = (unit - t * parts.d) * HR + sub;
-            const int64_t pos = pos_next;
-            const Turn u = load_turn<D, SPLIT>(p, pos, lane);
-            uint16_t* dst = out.p + t * out.ts + h0 * out.hs;
-            uint4 gv[kBwdUnroll], xv[kBwdUnroll];
 #pragma unroll
-            for (int i = 0; i < kBwdUnroll; ++i) {
-                gv[i] = gn[i];
-                xv[i] = xn[i];
+        for (int i = 0; i < kBwdStages - 1; ++i) issue();
+        const uint8_t* stage = smem + warp * (kBwdStages * kBwdStage) + sub * (512 / NV);
+        int at = 0;
+        int64_t pos = load_pos(p, t), pos_next = t + 1 < p.T ? load_pos(p, t + 1) : 0;
+        Angles angles = load_angles<D, SPLIT>(p, pos, l, lane);
+        Turn u;
+        Eight w;
+        bool new_token = true, new_kind = true;
+        kind = part >= a.q_parts;
+#pragma unroll 1
+        for (int unit = begin; unit < end; ++unit) {
+            if (new_token) {
+                u = turn_of<D, SPLIT>(p, angles, pos, lane);
+                if (unit > begin) pos_next = t + 1 < p.T ? load_pos(p, t + 1) : 0;
             }
-            if (unit + stride < units) load(unit + stride);
+            if (new_kind) w = load_weight<D, SPLIT>(kind ? p.wk : p.wq, l);
+            const HeadsOut& out = kind ? a.dk : a.dq;
+            const int h0 = (kind ? part - a.q_parts : part) * HR, mine = (kind ? a.k : a.q).heads - h0;
+            uint16_t* dst = out.p + t * out.ts + (h0 + sub) * out.hs;
+            const int64_t dst_step = NV * out.hs;
+            // the next unit
+            int t_next = t, part_next = part + 1;
+            if (part_next == a.parts.d) {
+                part_next = 0;
+                ++t_next;
+            }
+            if (unit + 1 < end && t_next != t) angles = load_angles<D, SPLIT>(p, pos_next, l, lane);
+            __syncwarp();
+            issue();
+            asm volatile("cp.async.wait_group %0;" ::"n"(kBwdStages - 1) : "memory");
+            __syncwarp();
+            const uint8_t* from = stage + at * kBwdStage;
+            at = at == kBwdStages - 1 ? 0 : at + 1;
 #pragma unroll
             for (int i = 0; i < kBwdUnroll; ++i) {
-                if (h0 - sub + i * NV >= xin.heads) break;               // the same for the whole warp
-                const Eight dy = unpack(gv[i]), dp = partner<SPLIT>(gv[i], dy, u, p.interleaved), x = unpack(xv[i]);
+                if (i * NV >= mine) break;                   // the same for the whole warp
+                const uint16_t* head = reinterpret_cast<const uint16_t*>(from + i * 512);
+                const uint4 gv = load_bf16<D, SPLIT>(head, l), xv = load_bf16<D, SPLIT>(head + kBwdUnroll * 256, l);
+                const Eight dy = unpack(gv), dp = partner<SPLIT>(gv, dy, u, p.interleaved), x = unpack(xv);
                 Eight g, wg;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -709,43 +788,69 @@ __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const Backward
                     dw.v[e] = fma2(g.v[e], mul2(x.v[e], rr), dw.v[e]);
                     y.v[e] = fma2(wg.v[e], rr, mul2(x.v[e], mm));
                 }
-                if (h0 + i * NV < xin.heads) store_bf16<D, SPLIT>(dst, l, pack(y));
-                dst += NV * out.hs;
+                if (sub + i * NV < mine) store_bf16<D, SPLIT>(dst, l, pack(y));
+                dst += dst_step;
             }
+            const int kind_next = part_next >= a.q_parts;
+            new_token = t_next != t;
+            new_kind = kind_next != kind;
+            if (new_kind) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t other = dw.v[e];
+                    dw.v[e] = dw_other.v[e];
+                    dw_other.v[e] = other;
+                }
+            }
+            if (new_token) pos = pos_next;
+            t = t_next;
+            part = part_next;
+            kind = kind_next;
         }
-        // the block's sum: over the warp's NV vectors, then over the warps
+    }
+    __syncthreads();
+    // the block's sums: over the warp's NV vectors, then over the warps
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
         float f[8];
-        spread(dw, f);
+        spread(k == kind ? dw : dw_other, f);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
 #pragma unroll
             for (int o = NL; o < 32; o <<= 1) f[e] += __shfl_xor_sync(0xffffffffu, f[e], o);
-            if (sub == 0) sums[warp * D + (e < 4 ? first<D, SPLIT>(l) + e : second<D, SPLIT>(l) + e - 4)] = f[e];
+            if (sub == 0)
+                sums[(warp * 2 + k) * D + (e < 4 ? first<D, SPLIT>(l) + e : second<D, SPLIT>(l) + e - 4)] = f[e];
         }
-        __syncthreads();
-        if (threadIdx.x < D) {
-            float v = 0.0f;
-#pragma unroll
-            for (int k = 0; k < NW; ++k) v += sums[k * D + threadIdx.x];
-            a.part[((int64_t)blockIdx.x * 2 + kind) * D + threadIdx.x] = v;
-        }
-        __syncthreads();
     }
-    __shared__ int last;
-    if (threadIdx.x == 0) last = arrive(a.done) == (int)gridDim.x - 1;   // (the loop's barrier is before it)
     __syncthreads();
-    if (!last) return;
+    if (threadIdx.x < 2 * D) {
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) v += sums[k * 2 * D + threadIdx.x];
+        a.part[(int64_t)blockIdx.x * 2 * D + threadIdx.x] = v;
+    }
+    __syncthreads();
+    bool last = false;
+    if (threadIdx.x == 0) last = arrive(a.done) == (int)gridDim.x - 1;
+    if (!__syncthreads_or(last)) return;
     // a thread adds four columns of every ROWS-th block's sums, many loads in flight
     constexpr int COLS = 2 * D / 4, ROWS = kBwdThreads / COLS;
     const int col = threadIdx.x % COLS, row = threadIdx.x / COLS;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 20
-    for (int b = row; b < (int)gridDim.x; b += ROWS) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part + (int64_t)b * 2 * D) + col);
-        v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+    constexpr int FLIGHT = (152 + ROWS - 1) / ROWS;
+#pragma unroll 1
+    for (int b = row; b < (int)gridDim.x; b += FLIGHT * ROWS) {
+        float4 x[FLIGHT];
+#pragma unroll
+        for (int i = 0; i < FLIGHT; ++i) {
+            x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (b + i * ROWS < (int)gridDim.x)
+                x[i] = __ldcg(reinterpret_cast<const float4*>(a.part + (int64_t)(b + i * ROWS) * 2 * D) + col);
+        }
+#pragma unroll
+        for (int i = 0; i < FLIGHT; ++i) v = make_float4(v.x + x[i].x, v.y + x[i].y, v.z + x[i].z, v.w + x[i].w);
     }
     float4* flat = reinterpret_cast<float4*>(sums);
-    static_assert(sizeof(sums) >= kBwdThreads * sizeof(float4), "room for every thread's sums");
     flat[threadIdx.x] = v;
     __syncthreads();
     if (threadIdx.x < 2 * D) {
@@ -817,16 +922,20 @@ cudaError_t launch_qk_norm_rope_bwd(int D, const HeadsIn& dqo, const HeadsIn& dk
                                     const RopeParams& p, const HeadsOut& dq, const HeadsOut& dk, float* dwq,
                                     float* dwk, float* part, int* done, int sms, cudaStream_t st) {
     const int hr = kBwdUnroll * (256 / D), nw = kBwdThreads / 32;
-    BackwardArgs a = {dqo, dko, q, k, p, dq, dk, dwq, dwk, part, done, fast_div((q.heads + hr - 1) / hr),
-                      fast_div((k.heads + hr - 1) / hr)};
-    const int64_t units = p.T * (a.q_parts.d + a.k_parts.d);
+    const int q_parts = (q.heads + hr - 1) / hr, k_parts = (k.heads + hr - 1) / hr;
+    const int64_t units = p.T * (q_parts + k_parts);
     if (units > INT32_MAX / 2) return cudaErrorInvalidValue;
     const int64_t want = (units + nw - 1) / nw, cap = qk_norm_rope_bwd_blocks(sms);
     const unsigned grid = (unsigned)(want < cap ? want : cap);
+    const int warps = (int)grid * nw;
+    const BackwardArgs a = {dqo,  dko,  q,   k,  p, dq, dk, dwq, dwk, part, done, fast_div(q_parts + k_parts), q_parts,
+                            (int)(units / warps), (int)(units % warps)};
     const bool split = p.rot == D && !p.interleaved;
     auto kernel = D == 64 ? (split ? backward_kernel<64, true> : backward_kernel<64, false>)
                           : (split ? backward_kernel<128, true> : backward_kernel<128, false>);
-    return launch_chained(kernel, grid, kBwdThreads, 0, st, a);
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), kBwdSmem);
+    if (e != cudaSuccess) return e;
+    return launch_chained(kernel, grid, kBwdThreads, kBwdSmem, st, a);
 }
 
 }  // namespace r9q
