@@ -305,10 +305,13 @@ struct Place {
     int64_t page;
     int at;
 };
+__device__ __forceinline__ int64_t page_of(const Kv4Cache& c, int64_t slot) {      // slot >= 0
+    return slot >> 32 ? slot / c.page : (int64_t)((uint32_t)slot / (uint32_t)c.page);
+}
 __device__ __forceinline__ Place find_slot(const Kv4Cache& c, int64_t slot, int lane, int* err) {
     Place r = {-1, 0};
     if (slot >= 0) {
-        const int64_t page = slot / c.page;
+        const int64_t page = page_of(c, slot);
         if (page < c.pages) {
             r.page = page;
             r.at = (int)(slot - page * c.page);
@@ -327,6 +330,16 @@ __device__ __forceinline__ void write_heads(const ForwardArgs& a, const HeadsIn&
     constexpr int NL = D / 8, NV = 32 / NL, HR = heads_a_round<D>();
     const int l = lane & (NL - 1), sub = lane / NL;
     const uint16_t* src = in.p + t * in.ts + h * in.hs;
+    uint4 x[kUnroll];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (h + i * NV < end) x[i] = turned ? load_bf16<D, SPLIT>(src, l) : load_bf16<D, false>(src, l);
+            src += NV * in.hs;
+        }
+    };
+    load(h);                                             // (on its way first)
     const Place place = find_slot(a.c, a.slots[t], lane, a.rope.err);
     Turn u;
     Eight w;
@@ -335,13 +348,6 @@ __device__ __forceinline__ void write_heads(const ForwardArgs& a, const HeadsIn&
         w = load_weight<D, SPLIT>(a.rope.wk, l);
     }
     for (; h - sub < end; h += HR) {
-        uint4 x[kUnroll];
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            x[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (h + i * NV < end) x[i] = turned ? load_bf16<D, SPLIT>(src, l) : load_bf16<D, false>(src, l);
-            src += NV * in.hs;
-        }
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
             if (h - sub + i * NV >= end) break;          // the same for the whole warp
@@ -369,6 +375,7 @@ __device__ __forceinline__ void write_heads(const ForwardArgs& a, const HeadsIn&
                 if (live && l == 0) a.c.vp[head * a.c.page + place.at] = pair;
             }
         }
+        if (h - sub + HR < end) load(h + HR);
     }
 }
 
@@ -444,7 +451,7 @@ __device__ __forceinline__ Place group_of(const Kv4Cache& c, const int64_t* slot
     const int64_t slot = slots[t0 + (lane & 15)], first = __shfl_sync(0xffffffffu, slot, 0);
     const bool group = first >= 0 && first % 16 == 0 && slot == first + (lane & 15);
     if (!__all_sync(0xffffffffu, group)) return r;
-    const int64_t page = first / c.page;
+    const int64_t page = page_of(c, first);
     if (page >= c.pages) return r;                       // (the tokens, one by one, record the error)
     r.page = page;
     r.at = (int)(first - page * c.page);
