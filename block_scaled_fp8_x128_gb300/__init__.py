@@ -402,7 +402,8 @@ def r9q_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, wq: torch.Tensor, wk: tor
                      positions: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
                      q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
     """RMS norm of the heads of q bf16 [T][Hq][D] and k bf16 [T][Hk][D] (any token and head strides) and the
-    rotation by cos, sin fp32 [npos][rot/2] at positions int64 [T] (None: norm only); returns (q_out, k_out)."""
+    rotation by cos, sin fp32 [npos][rot/2] at positions int64 [T] (None: norm only); returns (q_out, k_out), which
+    are parts of one allocation where neither was given."""
     return _checked(_calls.qk_norm_rope(q, k, wq, wk, cos, sin, positions, eps, interleaved, q_out, k_out,
                                         _stream_handle(q.device.index, stream)), "r9q_qk_norm_rope")
 
@@ -413,7 +414,8 @@ def r9q_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Te
                          interleaved: bool = False, dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
                          dwq: torch.Tensor | None = None, dwk: torch.Tensor | None = None,
                          workspace: torch.Tensor | None = None, stream=None):
-    """The gradient of r9q_qk_norm_rope; returns (dq, dk, dwq, dwk).  workspace: as for r9q_gemm_fp8_block_qa
+    """The gradient of r9q_qk_norm_rope; returns (dq, dk, dwq, dwk), of two allocations (dq and dk, dwq and dwk)
+    where they were not given.  workspace: as for r9q_gemm_fp8_block_qa
     (zero-filled before its first use; omitted: the stream's own)."""
     return _with_workspace("r9q_qk_norm_rope_bwd", R9Q_OP_QK_NORM_ROPE_BWD, 1, q.shape[-1], _calls.qk_norm_rope_bwd,
                            (dq_out, dk_out, q, k, wq, wk, cos, sin, positions, eps, interleaved, dq, dk, dwq, dwk),
@@ -437,7 +439,8 @@ def r9q_kv4_append(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, slots: tor
 
 def r9q_kv4_gather(cache: KV4Cache, slots: torch.Tensor, k: torch.Tensor | None = None,
                    v: torch.Tensor | None = None, stream=None):
-    """The tokens at slots int64 [T] as bf16 (k, v) [T][Hk][D]; zeros for padding."""
+    """The tokens at slots int64 [T] as bf16 (k, v) [T][Hk][D] (parts of one allocation where neither was given);
+    zeros for padding."""
     return _checked(_calls.kv4_gather(*cache, slots, k, v, _stream_handle(slots.device.index, stream)),
                     "r9q_kv4_gather")
 

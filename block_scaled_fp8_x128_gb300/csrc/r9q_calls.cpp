@@ -9,7 +9,8 @@
 // shape, layout or device raises as the rest of the binding does.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/core/Tensor.h>
+#include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdarg>
@@ -97,10 +98,30 @@ bool truth(PyObject* o) {
 }
 void* stream(PyObject* o) { return reinterpret_cast<void*>(integer(o)); }
 
+// New contiguous tensors from torch's allocator, without the dispatcher.  Those of one call that live together share an
+// allocation: each costs about a microsecond, as much as all checks of a call.
+using Storage = c10::intrusive_ptr<c10::StorageImpl>;
+size_t elements(at::IntArrayRef shape) {
+    size_t n = 1;
+    for (int64_t s : shape) n *= (size_t)s;
+    return n;
+}
+Storage allocate(size_t bytes, at::Device device) {
+    const c10::DeviceGuard guard(device);
+    return c10::make_intrusive<c10::StorageImpl>(c10::StorageImpl::use_byte_size_t(), bytes,
+                                                 c10::GetAllocator(device.type()), /*resizable=*/true);
+}
+PyObject* part(Storage storage, size_t from, at::ScalarType type, at::IntArrayRef shape) {
+    at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+        std::move(storage), c10::DispatchKeySet(c10::DispatchKey::CUDA), c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    t.unsafeGetTensorImpl()->set_storage_offset((int64_t)from);
+    return THPVariable_Wrap(std::move(t));
+}
 // An output: the caller's, or a new one.  A new reference.
 PyObject* output(PyObject* o, at::ScalarType type, at::IntArrayRef shape, at::Device device) {
     if (o != Py_None) return Py_NewRef(o);
-    return THPVariable_Wrap(at::empty(shape, at::TensorOptions().dtype(type).device(device)));
+    return part(allocate(elements(shape) * c10::elementSize(type), device), 0, type, shape);
 }
 // Outputs that are let go unless they are returned.
 struct Outputs {
@@ -110,6 +131,19 @@ struct Outputs {
         for (int i = 0; i < n; ++i) Py_XDECREF(o[i]);
     }
     PyObject* add(PyObject* x) { return o[n++] = x; }
+    // Two of one type: the caller's, or both new, of one allocation.
+    void add(PyObject* a, at::IntArrayRef a_shape, PyObject* b, at::IntArrayRef b_shape, at::ScalarType type,
+             at::Device device) {
+        if (a != Py_None || b != Py_None) {
+            add(output(a, type, a_shape, device));
+            add(output(b, type, b_shape, device));
+            return;
+        }
+        const size_t size = c10::elementSize(type), from = (elements(a_shape) * size + 255) / 256 * 256 / size;
+        const Storage storage = allocate((from + elements(b_shape)) * size, device);
+        add(part(storage, 0, type, a_shape));
+        add(part(storage, from, type, b_shape));
+    }
     PyObject* done(int rc) {
         if (rc) return PyLong_FromLong(rc);
         if (n == 0) Py_RETURN_NONE;
@@ -193,8 +227,8 @@ PyObject* qk_norm_rope(PyObject* const* a) {
     const Heads qh = heads(a[0], "q", {T, Hq, D}, dev), kh = heads(a[1], "k", {T, Hk, D}, dev);
     const Rope r = rope(a + 2, T, D, dev);
     Outputs out;
-    const Heads qo = heads(out.add(output(a[9], at::kBFloat16, s, dev)), "q_out", {T, Hq, D}, dev);
-    const Heads ko = heads(out.add(output(a[10], at::kBFloat16, ks, dev)), "k_out", {T, Hk, D}, dev);
+    out.add(a[9], s, a[10], ks, at::kBFloat16, dev);
+    const Heads qo = heads(out.o[0], "q_out", {T, Hq, D}, dev), ko = heads(out.o[1], "k_out", {T, Hk, D}, dev);
     return out.done(r9q_qk_norm_rope(qh.p, qh.ts, qh.hs, kh.p, kh.ts, kh.hs, r.wq, r.wk, r.cos, r.sin, r.pos, qo.p, qo.ts,
                                      qo.hs, ko.p, ko.ts, ko.hs, T, Hq, Hk, D, r.rot, r.npos, number(a[7]),
                                      truth(a[8]) ? R9Q_ROPE_INTERLEAVED : 0, stream(a[11])));
@@ -211,10 +245,11 @@ PyObject* qk_norm_rope_bwd(PyObject* const* a) {
     const Rope r = rope(a + 4, T, D, dev);
     const Workspace w = workspace(a[15], dev);
     Outputs out;
-    const Heads dq = heads(out.add(output(a[11], at::kBFloat16, s, dev)), "dq", {T, Hq, D}, dev);
-    const Heads dk = heads(out.add(output(a[12], at::kBFloat16, ks, dev)), "dk", {T, Hk, D}, dev);
-    float* dwq = static_cast<float*>(address(out.add(output(a[13], at::kFloat, {D}, dev)), "dwq", at::kFloat, {D}, dev));
-    float* dwk = static_cast<float*>(address(out.add(output(a[14], at::kFloat, {D}, dev)), "dwk", at::kFloat, {D}, dev));
+    out.add(a[11], s, a[12], ks, at::kBFloat16, dev);
+    out.add(a[13], {D}, a[14], {D}, at::kFloat, dev);
+    const Heads dq = heads(out.o[0], "dq", {T, Hq, D}, dev), dk = heads(out.o[1], "dk", {T, Hk, D}, dev);
+    float* dwq = static_cast<float*>(address(out.o[2], "dwq", at::kFloat, {D}, dev));
+    float* dwk = static_cast<float*>(address(out.o[3], "dwk", at::kFloat, {D}, dev));
     return out.done(r9q_qk_norm_rope_bwd(gq.p, gq.ts, gq.hs, gk.p, gk.ts, gk.hs, qh.p, qh.ts, qh.hs, kh.p, kh.ts, kh.hs,
                                          r.wq, r.wk, r.cos, r.sin, r.pos, dq.p, dq.ts, dq.hs, dk.p, dk.ts, dk.hs, dwq,
                                          dwk, T, Hq, Hk, D, r.rot, r.npos, number(a[9]),
@@ -264,8 +299,9 @@ PyObject* kv4_gather(PyObject* const* a) {
     const int64_t* slots = static_cast<const int64_t*>(address(a[4], "slots", at::kLong, {T}, dev));
     const Shape shape = {T, c.heads, c.dim};
     Outputs out;
-    void* k = address(out.add(output(a[5], at::kBFloat16, {T, c.heads, c.dim}, dev)), "k", at::kBFloat16, shape, dev);
-    void* v = address(out.add(output(a[6], at::kBFloat16, {T, c.heads, c.dim}, dev)), "v", at::kBFloat16, shape, dev);
+    out.add(a[5], shape, a[6], shape, at::kBFloat16, dev);
+    void* k = address(out.o[0], "k", at::kBFloat16, shape, dev);
+    void* v = address(out.o[1], "v", at::kBFloat16, shape, dev);
     return out.done(r9q_kv4_gather(c.k, c.kp, c.v, c.vp, slots, T, c.heads, c.dim, c.pages, c.page, k, v, stream(a[7])));
 }
 
