@@ -386,13 +386,14 @@ def _checked(r, where):
     return r
 
 
-def _with_workspace(where, op, M, N, call, args, workspace, device, stream):
-    """A call that needs a workspace: the caller's, or the stream's own, made or grown where that does not do."""
+def _with_workspace(where, op, size, call, args, workspace, device, stream):
+    """A call that needs a workspace: the caller's, or the stream's own, made or grown where that does not do.
+    size(): the M and N that r9q_workspace_bytes takes."""
     handle = _stream_handle(device.index, stream)
     own = workspace if workspace is not None else _WORKSPACES.get((device.index, handle))
     r = call(*args, own, handle)
     if workspace is None and r.__class__ is int and r == R9Q_ERR_WORKSPACE:
-        own = _stream_workspace(r9q_workspace_bytes(op, M, N, 0), device, stream)
+        own = _stream_workspace(r9q_workspace_bytes(op, *size(), 0), device, stream)
         r = call(*args, own, handle)
     return _checked(r, where)
 
@@ -417,7 +418,8 @@ def r9q_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Te
     """The gradient of r9q_qk_norm_rope; returns (dq, dk, dwq, dwk), of two allocations (dq and dk, dwq and dwk)
     where they were not given.  workspace: as for r9q_gemm_fp8_block_qa
     (zero-filled before its first use; omitted: the stream's own)."""
-    return _with_workspace("r9q_qk_norm_rope_bwd", R9Q_OP_QK_NORM_ROPE_BWD, 1, q.shape[-1], _calls.qk_norm_rope_bwd,
+    return _with_workspace("r9q_qk_norm_rope_bwd", R9Q_OP_QK_NORM_ROPE_BWD, lambda: (1, q.shape[-1]),
+                           _calls.qk_norm_rope_bwd,
                            (dq_out, dk_out, q, k, wq, wk, cos, sin, positions, eps, interleaved, dq, dk, dwq, dwk),
                            workspace, q.device, stream)
 
@@ -453,8 +455,8 @@ def r9q_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tenso
     over the cache: block_table int32 [B][max_pages], seq_lens int32 [B] (new tokens included).  scale: 1/sqrt(D) by
     default.  Returns o bf16 [B][Lq][Hq][D], or (o, lse fp32 [B][Lq][Hq]) with return_lse.  workspace: as for
     r9q_gemm_fp8_block_qa (zero-filled before its first use; omitted: the stream's own)."""
-    _, Lq, Hq, D = q.shape
-    return _with_workspace("r9q_kv4_attention", R9Q_OP_KV4_ATTENTION, max(1, Lq * Hq // max(1, cache.k.shape[1])), D,
+    return _with_workspace("r9q_kv4_attention", R9Q_OP_KV4_ATTENTION,
+                           lambda: (max(1, q.shape[1] * q.shape[2] // cache.k.shape[1]), q.shape[3]),
                            _calls.kv4_attention,
                            (q, *cache, block_table, seq_lens, scale, window, out, lse, return_lse), workspace, q.device,
                            stream)
