@@ -205,8 +205,7 @@ struct Kv4AttnParams {
     float scale_log2;            // softmax scale * log2(e)
     FastDiv chunks, group, page_groups;      // row chunks, G, groups of 16 tokens of a page (set by the launcher)
 };
-// CTAs of the launch, and floats of `part` for them.
-int kv4_attention_ctas(int D, int64_t rows, int sms);
+// Floats of `part` for any launch with so many rows.
 size_t kv4_attention_part_floats(int D, int64_t rows, int sms);
 // Workspace bytes of R9Q_OP_QK_NORM_ROPE_BWD and R9Q_OP_KV4_ATTENTION (M rows, N = D).
 size_t decode_workspace(int op, int64_t M, int64_t N, int* rc);

@@ -31,6 +31,8 @@
 // HBM bound (136 bytes a token and head at D = 128).  Lanes copy exactly the
 // bytes they will use (cp.async, 16 bytes, a ring of stages in shared memory per
 // warp), so a stage needs no barrier.
+#include <algorithm>
+
 #include "r9q_kv4_attention.cuh"
 
 namespace r9q {
@@ -505,7 +507,23 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
     }
 }
 
-int row_tiles(int64_t rows) { return rows <= 8 ? 1 : 2; }
+// Tiles of eight rows that a chunk has.  Two take each code through the registers for twice the rows, in 1.62 times the
+// time of one (1.74 at D = 64), and have fewer warps an SM, so that an item's beginning and end weigh more: 32 (40) groups of
+// a CTA against kItemCost.  Both add up, with the groups that the pages can hold, to a time for either; us, one
+// tile / two: 16 rows, 16 sequences of 4000 tokens 37.3/32.4, 2 of them 13.2/17.0, 64 of 300 24.1/23.0; 24 rows 48.3/48.8
+// and, of 300, 30.6/37.3; 32 rows of 8191 100.0/81.1; 40 rows of 4000 69.4/67.0, of 300 44.7/54.4.  (8 key-value heads
+// of 128.)
+int row_tiles(int D, const Kv4AttnParams& p, int sms) {
+    const int64_t rows = (int64_t)p.Lq * p.G, seqs = (int64_t)p.B * p.c.heads;
+    if (rows <= 8) return 1;
+    const float groups = (float)(std::min(p.room, p.reach) / 16 + 1);
+    auto time = [&](int tiles, float group, float item) {
+        const float items = (float)(seqs * ((rows + 8 * tiles - 1) / (8 * tiles)));
+        return items * groups * group / (float)ctas_per_sm(D, 1, false) +
+               item * std::max((float)used_sms(sms), items / (float)ctas_per_sm(D, tiles, false));
+    };
+    return time(1, 1.0f, (float)kItemCost) <= time(2, D == 64 ? 1.74f : 1.62f, D == 64 ? 40.0f : 32.0f) ? 1 : 2;
+}
 
 template <int D, int NT, bool WIDE>
 cudaError_t launch(const Kv4AttnParams& p, int sms, cudaStream_t st) {
@@ -532,17 +550,15 @@ cudaError_t launch(Kv4AttnParams p, int sms, cudaStream_t st) {
 
 }  // namespace
 
-// (of the launch with more of them)
-int kv4_attention_ctas(int D, int64_t rows, int sms) {
-    return used_sms(sms) * ctas_per_sm(D, row_tiles(rows), false);
-}
-
 size_t kv4_attention_part_floats(int D, int64_t rows, int sms) {
-    return (size_t)kv4_attention_ctas(D, rows, sms) * 2 * (8 * row_tiles(rows)) * (D + 2);
+    size_t most = 0;
+    for (int tiles = 1; tiles <= (rows <= 8 ? 1 : 2); ++tiles)
+        most = std::max(most, (size_t)used_sms(sms) * ctas_per_sm(D, tiles, false) * 2 * (8 * tiles) * (D + 2));
+    return most;
 }
 
 cudaError_t launch_kv4_attention(int D, const Kv4AttnParams& p, int sms, cudaStream_t st) {
-    const bool one = row_tiles((int64_t)p.Lq * p.G) == 1;
+    const bool one = row_tiles(D, p, sms) == 1;
     if (D == 64) return one ? launch<64, 1>(p, sms, st) : launch<64, 2>(p, sms, st);
     return one ? launch<128, 1>(p, sms, st) : launch<128, 2>(p, sms, st);
 }

@@ -25,10 +25,18 @@ namespace r9q {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 4;                   // 8192 tokens of 32 + 8 heads of 128: 43.4 us, with two 53.1
+// A warp takes up to so many rounds of heads of its token, which share its set-up, as long as that leaves
+// kEnoughWarps (of the 32 + 8 heads; us, one round / this rule): 512 tokens 4.5/4.5 (four rounds: 6.6), 1024 7.5/6.5, 2048
+// 13.2/10.4, 4096 26.6/22.3, 8192 48.6/43.4.
 constexpr int kMaxRounds = 4;
-constexpr int64_t kEnoughWarps = 152 * 48;
-constexpr int kGroupTokens = 512;
+constexpr int64_t kEnoughWarps = 152 * 24;
+// Tokens from which a warp writes (reads back) a head of 16 tokens at a time where they fill a group of the cache,
+// instead of a token's heads.  Writes and read-backs of 8 heads of 128 together, us, by tokens / by groups: writing,
+// 512 tokens 9.2/10.5, 1024 13.0/12.9, 2048 17.7/16.3, 4096 33.2/27.0; reading, 4096 27.0/28.9, 8192 48.3/47.2, 16384
+// 89.4/83.6.
+constexpr int kGroupTokens = 1024;
+constexpr int kGatherGroupTokens = 8192;
 
 template <int D>
 constexpr int heads_a_round() { return kUnroll * (256 / D); }
@@ -912,7 +920,7 @@ cudaError_t launch_kv4_append(int D, const HeadsIn& k, const HeadsIn& v, int64_t
 
 cudaError_t launch_kv4_gather(int D, const Kv4Cache& c, const int64_t* slots, int64_t T, uint16_t* k, uint16_t* v,
                               int* err, cudaStream_t st) {
-    const bool groups = T >= kGroupTokens;
+    const bool groups = T >= kGatherGroupTokens;
     const int nv = 256 / D;
     const int64_t warps = groups ? (T + 15) / 16 * c.heads : T * ((c.heads + nv - 1) / nv);
     const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);

@@ -616,3 +616,77 @@ def test_attention_of_thousands_of_sequences(r9q):
     q = rand((2500, 1, 2, 64), 102).to(dev())
     o, lse = r9q.r9q_kv4_attention(q, cache, on(table), on(np.array(lens, np.int32)), return_lse=True)
     check_attention(r9q, cache, table, lens, q, o, lse)
+
+
+# ------------------------------------- variants that sizes of these orders take --
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,D,page", [(1024, 2, 128, 16), (1777, 3, 128, 48), (8192, 1, 64, 16), (8205, 2, 128, 64)])
+@pytest.mark.parametrize("how", ["aligned", "late", "anywhere"])
+def test_append_and_gather_of_a_long_prompt(r9q, T, H, D, page, how):
+    """At sizes where writes, and for the longest read-backs too, take a group of the cache at a time."""
+    test_append_and_gather_of_a_prompt(r9q, T, H, D, page, how)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,Hq,Hk,D,rot,inter", [(1040, 4, 2, 128, 128, False), (1301, 3, 1, 64, 64, False),
+                                                (1025, 2, 2, 128, 64, True), (1200, 5, 1, 64, 32, False)])
+def test_norm_rope_of_a_long_prompt_into_cache(r9q, T, Hq, Hk, D, rot, inter):
+    test_norm_rope_of_a_prompt_into_cache(r9q, T, Hq, Hk, D, rot, inter)
+
+
+def room_for(table, page, tokens):
+    """The table with places for so many tokens a sequence: what it could hold decides how the work is laid out."""
+    return np.pad(table, ((0, 0), (0, tokens // page - table.shape[1])), constant_values=-1)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,Lq,Hq,Hk,D,page,window", [
+    ([1], 1, 9, 1, 128, 16, 0), ([260], 1, 16, 1, 128, 80, 0), ([2, 700, 0, 31], 4, 8, 2, 128, 32, 0),
+    ([300, 40], 5, 12, 4, 64, 16, 0), ([0, 33, 1000], 2, 14, 2, 64, 48, 100), ([200, 90], 5, 16, 2, 128, 16, 0),
+    ([600], 17, 4, 2, 128, 64, 40), ([90], 90, 4, 2, 128, 16, 0), ([61], 40, 1, 1, 64, 16, 3),
+])
+@pytest.mark.parametrize("copies", [1, 20])
+def test_attention_of_many_rows(r9q, lens, Lq, Hq, Hk, D, page, window, copies):
+    """More than eight rows of a key-value head, in two tiles (a batch with room for long sequences), in few items and in
+    many; and the same numbers, to rounding, in one."""
+    lens = lens * copies
+    cache, table, _ = make_cache(r9q, lens, Hk, D, page, 111)
+    q = rand((len(lens), Lq, Hq, D), 112).to(dev())
+    n = on(np.array(lens, np.int32))
+    for t in (room_for(table, page, 1 << 20), table):
+        o, lse = r9q.r9q_kv4_attention(q, cache, on(t), n, window=window, return_lse=True)
+        assert r9q.r9q_last_device_error() == 0
+        check_attention(r9q, cache, table, lens, q, o, lse, window)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q_scale,v_scale,scale", [(1e-30, 1e-25, None), (1e4, 1e20, 1e-5), (30.0, 1e-3, None),
+                                                   (1.0, 0.0, 2.0)])
+def test_attention_magnitudes_of_many_rows(r9q, q_scale, v_scale, scale):
+    lens = [300, 17]
+    cache, table, _ = make_cache(r9q, lens, 2, 128, 16, 121, v_scale=v_scale)
+    q = rand((2, 4, 8, 128), 122, q_scale).to(dev())
+    o, lse = r9q.r9q_kv4_attention(q, cache, on(room_for(table, 16, 1 << 20)), on(np.array(lens, np.int32)), scale=scale,
+                                   return_lse=True)
+    check_attention(r9q, cache, table, lens, q, o, lse, scale=scale)
+
+
+@pytest.mark.gpu
+def test_what_is_masked_does_not_reach_the_result_of_many_rows(r9q):
+    n, Lq, Hq, Hk, D, page = 100, 3, 8, 2, 128, 16
+    cache, table, slots = make_cache(r9q, [n], Hk, D, page, 131)
+    q = rand((1, Lq, Hq, D), 132).to(dev())
+    args = (q, cache, on(room_for(table, page, 1 << 20)), on(np.array([n], np.int32)))
+    base = r9q.r9q_kv4_attention(*args, return_lse=True)
+    last = on(slots[-1:])
+    for x in (-3.3895313892515355e38, 1e30, float("inf"), float("nan")):
+        k = rand((1, Hk, D), 133).to(dev())
+        v = k.clone()
+        k[0, 0, 3], v[0, 0, 5] = x, x
+        r9q.r9q_kv4_append(k, v, cache, last)
+        o, lse = r9q.r9q_kv4_attention(*args, return_lse=True)
+        assert torch.equal(o[:, :2], base[0][:, :2]) and torch.equal(lse[:, :2], base[1][:, :2]), x
+        assert bool(torch.isfinite(o[:, 2, 4:]).all())
+        if x != x or x == float("inf"):
+            assert bool(torch.isnan(o[:, 2, :4]).all())
