@@ -42,20 +42,23 @@ namespace {
 constexpr int kStep = 32;                    // keys a warp takes at a time: two groups of 16
 constexpr int kStages = 4;                   // steps in a warp's ring
 
-// The warps that an SM holds (registers) make CTAs of four or, wide, one CTA.
+// The warps that an SM holds (registers) make CTAs of two or four, or one CTA.
+enum Width { kNarrow, kMiddle, kWide };
 constexpr int sm_warps(int D, int NT) { return 4 * ((D == 64 ? 4 : 3) - (NT - 1)); }
-constexpr int cta_warps(int D, int NT, bool wide) { return wide ? sm_warps(D, NT) : 4; }
-constexpr int ctas_per_sm(int D, int NT, bool wide) { return sm_warps(D, NT) / cta_warps(D, NT, wide); }
+constexpr int cta_warps(int D, int NT, Width w) { return w == kWide ? sm_warps(D, NT) : w == kMiddle ? 4 : 2; }
+constexpr int ctas_per_sm(int D, int NT, Width w) { return sm_warps(D, NT) / cta_warps(D, NT, w); }
 
+// Groups of a CTA that take as long as beginning and ending an item.
+constexpr int item_cost(int NT, Width w) { return NT == 1 && w == kNarrow ? 16 : 24; }
 constexpr int stage_bytes(int D) { return kStep * D + kStep * 8; }
 constexpr int out_stride(int D) { return D + 4; }      // floats a row of the CTA's exchange takes
 // Shared memory: the rings, and in their place the warps' exchange [warps][R][out_stride] with references and sums,
 // and the joining of partials.
-constexpr int work_bytes(int D, int NT, bool wide) {
-    const int w = cta_warps(D, NT, wide), R = 8 * NT;
+constexpr int work_bytes(int D, int NT, Width width) {
+    const int w = cta_warps(D, NT, width), R = 8 * NT;
     return largest(largest(w * kStages * stage_bytes(D), w * R * (out_stride(D) + 2) * 4), join_bytes(R, w * 32));
 }
-constexpr int smem_bytes(int D, int NT, bool wide) { return work_bytes(D, NT, wide) + 16; }   // and a flag
+constexpr int smem_bytes(int D, int NT, Width w) { return work_bytes(D, NT, w) + 16; }   // and a flag
 
 // Transposes an 8x8 matrix of 16-bit values held two to a lane.
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
@@ -278,10 +281,10 @@ __device__ __forceinline__ void attend(State<D, NT>& s, const uint8_t* st, int k
     }
 }
 
-template <int D, int NT, bool WIDE>
-__global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT, WIDE))
+template <int D, int NT, Width WIDTH>
+__global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDTH), ctas_per_sm(D, NT, WIDTH))
     kv4_attention_kernel(const Kv4AttnParams p) {
-    constexpr int W = cta_warps(D, NT, WIDE), kThreads = 32 * W;
+    constexpr int W = cta_warps(D, NT, WIDTH), kThreads = 32 * W;
     constexpr int KW = D / 32;               // 32-bit words of a key that a lane holds
     constexpr int MT = D / 16;               // 16-element tiles
     constexpr int R = 8 * NT;                // rows of a chunk
@@ -289,13 +292,13 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
     constexpr int kMinGroups = 2 * W;        // groups a CTA takes at least: one step for each warp
     extern __shared__ __align__(16) uint8_t smem[];
     begin_chained();
-    int* joins = reinterpret_cast<int*>(smem + work_bytes(D, NT, WIDE));     // the CTA joins an item's partials
+    int* joins = reinterpret_cast<int*>(smem + work_bytes(D, NT, WIDTH));     // the CTA joins an item's partials
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = lane >> 2, j = lane & 3;
     const int rows = p.Lq * p.G;
     Walk walk;
-    if (!walk.start(p, kMinGroups)) return;
+    if (!walk.start(p, kMinGroups, item_cost(NT, WIDTH))) return;
     uint8_t* ring = smem + warp * (ST * stage_bytes(D));
     const uint32_t ring_u = smem_u32(ring);
     const uint8_t* k_lane = p.c.k + lane * (KW * 4);
@@ -508,30 +511,29 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDE), ctas_per_sm(D, NT
 }
 
 // Tiles of eight rows that a chunk has.  Two take each code through the registers for twice the rows, in 1.62 times the
-// time of one (1.74 at D = 64), and have fewer warps an SM, so that an item's beginning and end weigh more: 32 (40) groups of
-// a CTA against kItemCost.  Both add up, with the groups that the pages can hold, to a time for either; us, one
-// tile / two: 16 rows, 16 sequences of 4000 tokens 37.3/32.4, 2 of them 13.2/17.0, 64 of 300 24.1/23.0; 24 rows 48.3/48.8
-// and, of 300, 30.6/37.3; 32 rows of 8191 100.0/81.1; 40 rows of 4000 69.4/67.0, of 300 44.7/54.4.  (8 key-value heads
-// of 128.)
+// time of one (1.74 at D = 64), and have fewer warps an SM, so that an item's beginning and end weigh more: 32 (40)
+// groups of a CTA against 24.  Both add up, with the groups that the pages can hold, to a time for either; us, one tile /
+// two, 64/8 heads of 128: 16 rows, 16 sequences of 4000 tokens 37.3/32.3, 2 of them 13.1/16.9, 64 of 300 23.6/19.2; 24
+// rows 48.1/48.9 and, of 300, 25.5/29.4; 32 rows of 8191 100.0/81.1; 40 rows of 4000 71.9/66.5, of 300 35.6/41.1.
 int row_tiles(int D, const Kv4AttnParams& p, int sms) {
     const int64_t rows = (int64_t)p.Lq * p.G, seqs = (int64_t)p.B * p.c.heads;
     if (rows <= 8) return 1;
     const float groups = (float)(std::min(p.room, p.reach) / 16 + 1);
     auto time = [&](int tiles, float group, float item) {
         const float items = (float)(seqs * ((rows + 8 * tiles - 1) / (8 * tiles)));
-        return items * groups * group / (float)ctas_per_sm(D, 1, false) +
-               item * std::max((float)used_sms(sms), items / (float)ctas_per_sm(D, tiles, false));
+        return items * groups * group / (float)ctas_per_sm(D, 1, kMiddle) +
+               item * std::max((float)used_sms(sms), items / (float)ctas_per_sm(D, tiles, kMiddle));
     };
-    return time(1, 1.0f, (float)kItemCost) <= time(2, D == 64 ? 1.74f : 1.62f, D == 64 ? 40.0f : 32.0f) ? 1 : 2;
+    return time(1, 1.0f, 24.0f) <= time(2, D == 64 ? 1.74f : 1.62f, D == 64 ? 40.0f : 32.0f) ? 1 : 2;
 }
 
-template <int D, int NT, bool WIDE>
+template <int D, int NT, Width WIDTH>
 cudaError_t launch(const Kv4AttnParams& p, int sms, cudaStream_t st) {
-    const void* kernel = reinterpret_cast<const void*>(kv4_attention_kernel<D, NT, WIDE>);
-    cudaError_t e = ensure_dynamic_smem(kernel, smem_bytes(D, NT, WIDE));
+    const void* kernel = reinterpret_cast<const void*>(kv4_attention_kernel<D, NT, WIDTH>);
+    cudaError_t e = ensure_dynamic_smem(kernel, smem_bytes(D, NT, WIDTH));
     if (e != cudaSuccess) return e;
-    return launch_chained(kv4_attention_kernel<D, NT, WIDE>, used_sms(sms) * ctas_per_sm(D, NT, WIDE),
-                          32 * cta_warps(D, NT, WIDE), smem_bytes(D, NT, WIDE), st, p);
+    return launch_chained(kv4_attention_kernel<D, NT, WIDTH>, used_sms(sms) * ctas_per_sm(D, NT, WIDTH),
+                          32 * cta_warps(D, NT, WIDTH), smem_bytes(D, NT, WIDTH), st, p);
 }
 
 template <int D, int NT>
@@ -540,12 +542,16 @@ cudaError_t launch(Kv4AttnParams p, int sms, cudaStream_t st) {
     p.group = fast_div(p.G);
     p.page_groups = fast_div(p.c.page / 16);
     // Few long items: one CTA an SM leaves a third as many partials to join (one sequence of 131072 tokens 32.1 us
-    // against 38.9, two of 16000 16.9 against 19.6).  Many items, or ones too short to give such a CTA's warps two
-    // steps each: more and smaller CTAs (64 sequences of up to 16384 tokens 110 us against 132, 100 of 30 13.8 against
-    // 25.4).
+    // against 38.9, two of 16000 16.9 against 19.6).  More, or ones too short to give such a CTA's warps two steps
+    // each: CTAs of four warps (64 sequences of up to 16384 tokens 110 us against 132).  More items than such CTAs:
+    // of two warps, which begin and end twice as many items at a time (us, four warps / two; sequences x tokens, 32 or
+    // 64/8 heads: 100 x 30 13.5/9.2, 256 x 300 31.9/26.8, 256 x 1000 51.3/45.7, 64 x 4 new of 4000 122/92, 64 x 16384
+    // 107.7/106.9; with fewer items: 32 x 1000 13.7/14.6, 2 x 4000 12.3/22.6, 16 x 4 new of 8191 80.9/86.4).
     const int64_t items = (int64_t)p.B * p.c.heads * p.chunks.d, ctas = used_sms(sms);
-    const bool wide = 8 * items <= ctas && items * (p.room / 16) >= ctas * 4 * cta_warps(D, NT, true);
-    return wide ? launch<D, NT, true>(p, sms, st) : launch<D, NT, false>(p, sms, st);
+    if (8 * items <= ctas && items * (p.room / 16) >= ctas * 4 * cta_warps(D, NT, kWide))
+        return launch<D, NT, kWide>(p, sms, st);
+    return items > ctas * ctas_per_sm(D, NT, kMiddle) ? launch<D, NT, kNarrow>(p, sms, st)
+                                                      : launch<D, NT, kMiddle>(p, sms, st);
 }
 
 }  // namespace
@@ -553,7 +559,7 @@ cudaError_t launch(Kv4AttnParams p, int sms, cudaStream_t st) {
 size_t kv4_attention_part_floats(int D, int64_t rows, int sms) {
     size_t most = 0;
     for (int tiles = 1; tiles <= (rows <= 8 ? 1 : 2); ++tiles)
-        most = std::max(most, (size_t)used_sms(sms) * ctas_per_sm(D, tiles, false) * 2 * (8 * tiles) * (D + 2));
+        most = std::max(most, (size_t)used_sms(sms) * ctas_per_sm(D, tiles, kNarrow) * 2 * (8 * tiles) * (D + 2));
     return most;
 }
 

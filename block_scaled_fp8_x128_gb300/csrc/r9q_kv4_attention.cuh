@@ -15,7 +15,6 @@
 
 namespace r9q {
 
-constexpr int kItemCost = 24;                // groups that take as long as beginning and ending an item
 constexpr int kMinExponent = 67;             // value steps under 2^-60 count as that (keeps the sums finite)
 constexpr int kHeadroom = 8;                 // weights at the reference score are 2^8 to 2^9
 constexpr int kSlack = 6;                    // powers of two they may pass it by
@@ -142,13 +141,14 @@ struct Walk {
         return x - item_at <= begin_cost + s ? item_at : item_at + n - x <= s ? item_at + n : x;
     }
 
-    // False: nothing.  min_groups: the groups that a CTA takes at least.
-    __device__ __forceinline__ bool start(const Kv4AttnParams& p, int min_groups) {
+    // False: nothing.  min_groups: the groups that a CTA takes at least; item_cost: those that take it as long as
+    // beginning and ending an item.
+    __device__ __forceinline__ bool start(const Kv4AttnParams& p, int min_groups, int item_cost) {
         const int lane = threadIdx.x & 31;
         items_per_seq = p.c.heads * p.chunks.d;
         const long long items = (long long)p.B * items_per_seq, ctas = gridDim.x;
         parted = 2 * items <= ctas;
-        begin_cost = parted ? 0 : kItemCost;
+        begin_cost = parted ? 0 : item_cost;
         const int per_lane = (p.B + 31) / 32, b_first = lane * per_lane, b_end = min(p.B, b_first + per_lane);
         long long mine = 0, total;
 #pragma unroll 1
