@@ -28,9 +28,20 @@
 // The warps of a CTA take 32-key steps of a part in turn, each with its own reference,
 // and meet in shared memory at its end.
 //
-// HBM bound (136 bytes a token and head at D = 128).  Lanes copy exactly the
-// bytes they will use (cp.async, 16 bytes, a ring of stages in shared memory per
-// warp), so a stage needs no barrier.
+// Lanes copy exactly the bytes they will use (cp.async, 16 bytes, a ring of stages in
+// shared memory per warp), so a stage needs no barrier.
+//
+// What bounds it.  Up to 8 rows: HBM (136 bytes a token and head at D = 128) and the
+// taking apart of the codes, 64 masks for 16 tokens of a head, alike: 64 sequences of up
+// to 16384 tokens, 64/8 heads, take 107 us, 5.5 TB/s (the bytes alone 87, the kernel without
+// its arithmetic 95, without its copies 106).  More rows: instructions (16 sequences of 8191
+// tokens with 4 new ones 81 us, 212 TFLOP/s; the products alone 29).  Small batches:
+// latency, about 5.6 us from launch to the result for one short sequence, and with
+// parts to join about 9.  A step's score products formed before the last step's weights, and
+// the queries in shared memory for a third more warps, were slower (113 and 97 us,
+// against 108 and 81).  So was tcgen05 with the codes as an operand in tensor memory, for 32
+// rows: 103 us against 81, since converting them and two barriers a tile of 128 keys cost
+// more than the products save.
 #include <algorithm>
 
 #include "r9q_kv4_attention.cuh"
@@ -40,7 +51,7 @@ namespace r9q {
 namespace {
 
 constexpr int kStep = 32;                    // keys a warp takes at a time: two groups of 16
-constexpr int kStages = 4;                   // steps in a warp's ring
+constexpr int kStages = 4;                   // steps in a warp's ring (three, and a CTA more an SM: 128 us against 115)
 
 // The warps that an SM holds (registers) make CTAs of two or four, or one CTA.
 enum Width { kNarrow, kMiddle, kWide };
