@@ -331,7 +331,7 @@ __device__ __forceinline__ Place find_slot(const Kv4Cache& c, int64_t slot, int 
     return r;
 }
 
-// A warp's share of a token's key (or, at(lane's tokens) alone, value) heads h, h + NV, ... below `end`, into the cache:
+// A warp's share of a token's key or value heads h, h + NV, ... below `end`, into the cache:
 // keys normalised and turned (`turned`) or as they are, values as they are.
 template <int D, bool SPLIT>
 __device__ __forceinline__ void write_heads(const ForwardArgs& a, const HeadsIn& in, bool key, bool turned, int t, int h,
