@@ -690,3 +690,40 @@ def test_what_is_masked_does_not_reach_the_result_of_many_rows(r9q):
         assert bool(torch.isfinite(o[:, 2, 4:]).all())
         if x != x or x == float("inf"):
             assert bool(torch.isnan(o[:, 2, :4]).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,Hq,Hk,D,rot,inter", [(1500, 19, 3, 128, 64, False), (1100, 40, 9, 64, 64, True),
+                                                (3333, 1, 9, 128, 128, False), (2000, 7, 7, 64, 0, False)])
+def test_norm_rope_grad_of_long_batches(r9q, T, Hq, Hk, D, rot, inter):
+    """Several units a warp, which cross tokens and go from query to key heads and back, and last ones of odd sizes."""
+    test_norm_rope_grad(r9q, T, Hq, Hk, D, rot, inter)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,rot,inter", [(128, 128, False), (64, 32, False), (128, 128, True)])
+def test_norm_rope_grad_layouts_and_bad_positions(r9q, D, rot, inter):
+    T, Hq, Hk = 2100, 6, 2
+    q, k, _, wq, wk, cos, sin, pos = rope_inputs(T, Hq, Hk, D, rot, 141, npos=500)
+    dq, dk = rand((T, Hq, D), 142).to(dev()), rand((T, Hk, D), 143).to(dev())
+    args = rope_args(wq, wk, cos, sin, pos)
+    want = r9q.r9q_qk_norm_rope_bwd(dq, dk, q, k, *args, interleaved=inter)
+    # slices of one buffer, for what is read and for what is written, on another stream
+    x = torch.cat([q, k, dq, dk], 1)
+    out = torch.full((T, Hq + Hk + 1, D), 7.0, dtype=torch.bfloat16, device=dev())
+    dwq, dwk = torch.empty(D, device=dev()), torch.empty(D, device=dev())
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    r9q.r9q_qk_norm_rope_bwd(x[:, Hq + Hk:2 * Hq + Hk], x[:, 2 * Hq + Hk:], x[:, :Hq], x[:, Hq:Hq + Hk], *args,
+                             interleaved=inter, dq=out[:, :Hq], dk=out[:, Hq:Hq + Hk], dwq=dwq, dwk=dwk, stream=st)
+    st.synchronize()
+    got = (out[:, :Hq], out[:, Hq:Hq + Hk], dwq, dwk)
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and bool((out[:, -1] == 7).all())
+    bad = args[4].clone()
+    bad[0], bad[1234], bad[-1] = 500, -1, 1 << 40
+    got = r9q.r9q_qk_norm_rope_bwd(dq, dk, q, k, *args[:4], bad, interleaved=inter)
+    assert r9q.r9q_last_device_error() == -8
+    kept = torch.ones(T, dtype=torch.bool, device=dev())
+    kept[[0, 1234, -1]] = False
+    for a, b in zip(want[:2], got[:2]):
+        assert torch.equal(a[kept], b[kept]) and bool(torch.isnan(b[~kept]).all())
