@@ -453,8 +453,9 @@ def r9q_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tenso
                       workspace: torch.Tensor | None = None, stream=None):
     """Attention of the last Lq tokens of each sequence, q bf16 [B][Lq][Hq][D] (any batch, token and head strides),
     over the cache: block_table int32 [B][max_pages], seq_lens int32 [B] (new tokens included).  scale: 1/sqrt(D) by
-    default.  Returns o bf16 [B][Lq][Hq][D], or (o, lse fp32 [B][Lq][Hq]) with return_lse.  workspace: as for
-    r9q_gemm_fp8_block_qa (zero-filled before its first use; omitted: the stream's own)."""
+    default.  Returns o bf16 [B][Lq][Hq][D], or with return_lse (o, lse fp32 [B][Lq][Hq]), parts of one allocation where
+    neither was given.  workspace: as for r9q_gemm_fp8_block_qa (zero-filled before its first use; omitted: the stream's
+    own)."""
     return _with_workspace("r9q_kv4_attention", R9Q_OP_KV4_ATTENTION,
                            lambda: (max(1, q.shape[1] * q.shape[2] // cache.k.shape[1]), q.shape[3]),
                            _calls.kv4_attention,

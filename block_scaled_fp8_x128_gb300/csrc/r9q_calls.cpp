@@ -131,18 +131,19 @@ struct Outputs {
         for (int i = 0; i < n; ++i) Py_XDECREF(o[i]);
     }
     PyObject* add(PyObject* x) { return o[n++] = x; }
-    // Two of one type: the caller's, or both new, of one allocation.
-    void add(PyObject* a, at::IntArrayRef a_shape, PyObject* b, at::IntArrayRef b_shape, at::ScalarType type,
-             at::Device device) {
+    // Two: the caller's, or both new, of one allocation.
+    void add(PyObject* a, at::IntArrayRef a_shape, at::ScalarType a_type, PyObject* b, at::IntArrayRef b_shape,
+             at::ScalarType b_type, at::Device device) {
         if (a != Py_None || b != Py_None) {
-            add(output(a, type, a_shape, device));
-            add(output(b, type, b_shape, device));
+            add(output(a, a_type, a_shape, device));
+            add(output(b, b_type, b_shape, device));
             return;
         }
-        const size_t size = c10::elementSize(type), from = (elements(a_shape) * size + 255) / 256 * 256 / size;
+        const size_t size = c10::elementSize(b_type);
+        const size_t from = (elements(a_shape) * c10::elementSize(a_type) + 255) / 256 * (256 / size);
         const Storage storage = allocate((from + elements(b_shape)) * size, device);
-        add(part(storage, 0, type, a_shape));
-        add(part(storage, from, type, b_shape));
+        add(part(storage, 0, a_type, a_shape));
+        add(part(storage, from, b_type, b_shape));
     }
     PyObject* done(int rc) {
         if (rc) return PyLong_FromLong(rc);
@@ -227,7 +228,7 @@ PyObject* qk_norm_rope(PyObject* const* a) {
     const Heads qh = heads(a[0], "q", {T, Hq, D}, dev), kh = heads(a[1], "k", {T, Hk, D}, dev);
     const Rope r = rope(a + 2, T, D, dev);
     Outputs out;
-    out.add(a[9], s, a[10], ks, at::kBFloat16, dev);
+    out.add(a[9], s, at::kBFloat16, a[10], ks, at::kBFloat16, dev);
     const Heads qo = heads(out.o[0], "q_out", {T, Hq, D}, dev), ko = heads(out.o[1], "k_out", {T, Hk, D}, dev);
     return out.done(r9q_qk_norm_rope(qh.p, qh.ts, qh.hs, kh.p, kh.ts, kh.hs, r.wq, r.wk, r.cos, r.sin, r.pos, qo.p, qo.ts,
                                      qo.hs, ko.p, ko.ts, ko.hs, T, Hq, Hk, D, r.rot, r.npos, number(a[7]),
@@ -245,8 +246,8 @@ PyObject* qk_norm_rope_bwd(PyObject* const* a) {
     const Rope r = rope(a + 4, T, D, dev);
     const Workspace w = workspace(a[15], dev);
     Outputs out;
-    out.add(a[11], s, a[12], ks, at::kBFloat16, dev);
-    out.add(a[13], {D}, a[14], {D}, at::kFloat, dev);
+    out.add(a[11], s, at::kBFloat16, a[12], ks, at::kBFloat16, dev);
+    out.add(a[13], {D}, at::kFloat, a[14], {D}, at::kFloat, dev);
     const Heads dq = heads(out.o[0], "dq", {T, Hq, D}, dev), dk = heads(out.o[1], "dk", {T, Hk, D}, dev);
     float* dwq = static_cast<float*>(address(out.o[2], "dwq", at::kFloat, {D}, dev));
     float* dwk = static_cast<float*>(address(out.o[3], "dwk", at::kFloat, {D}, dev));
@@ -299,7 +300,7 @@ PyObject* kv4_gather(PyObject* const* a) {
     const int64_t* slots = static_cast<const int64_t*>(address(a[4], "slots", at::kLong, {T}, dev));
     const Shape shape = {T, c.heads, c.dim};
     Outputs out;
-    out.add(a[5], shape, a[6], shape, at::kBFloat16, dev);
+    out.add(a[5], shape, at::kBFloat16, a[6], shape, at::kBFloat16, dev);
     void* k = address(out.o[0], "k", at::kBFloat16, shape, dev);
     void* v = address(out.o[1], "v", at::kBFloat16, shape, dev);
     return out.done(r9q_kv4_gather(c.k, c.kp, c.v, c.vp, slots, T, c.heads, c.dim, c.pages, c.page, k, v, stream(a[7])));
@@ -323,14 +324,12 @@ PyObject* kv4_attention(PyObject* const* a) {
     const Workspace w = workspace(a[12], dev);
     const bool with_lse = truth(a[11]);
     Outputs out;
-    void* o = address(out.add(output(a[9], at::kBFloat16, s, dev)), "out", at::kBFloat16, {B, Lq, Hq, D}, dev);
-    float* lse = nullptr;
-    if (with_lse || a[10] != Py_None) {
-        PyObject* l = output(a[10], at::kFloat, {B, Lq, Hq}, dev);
-        Outputs keep;
-        (with_lse ? out : keep).add(l);
-        lse = static_cast<float*>(address(l, "lse", at::kFloat, {B, Lq, Hq}, dev));
-    }
+    if (with_lse)
+        out.add(a[9], s, at::kBFloat16, a[10], {B, Lq, Hq}, at::kFloat, dev);
+    else
+        out.add(output(a[9], at::kBFloat16, s, dev));
+    void* o = address(out.o[0], "out", at::kBFloat16, {B, Lq, Hq, D}, dev);
+    float* lse = static_cast<float*>(address(with_lse ? out.o[1] : a[10], "lse", at::kFloat, {B, Lq, Hq}, dev));
     return out.done(r9q_kv4_attention(q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), c.k, c.kp, c.v, c.vp, table,
                                       lens, o, lse, B, Lq, Hq, c.heads, D, c.pages, c.page, width, integer(a[8]), scale,
                                       w.p, w.bytes, stream(a[13])));
