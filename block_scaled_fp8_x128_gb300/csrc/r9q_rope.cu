@@ -797,7 +797,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const Backward
                     wg.v[e] = mul2(w.v[e], g.v[e]);
                 }
                 const float ss = group_sum<NL>(dot(x, x)), sg = group_sum<NL>(dot(wg, x));
-                const float r = inverse_root(fmaf(ss, 1.0f / D, p.eps));
+                // lanes without a head hold zeros, of which eps 0 makes an infinite r: they add 0 g to dw
+                const bool live = sub + i * NV < mine;
+                const float r = live ? inverse_root(fmaf(ss, 1.0f / D, p.eps)) : 0.0f;
                 const float m = -r * r * r * sg * (1.0f / D);
                 const uint64_t rr = pair_of(r, r), mm = pair_of(m, m);
                 Eight y;
@@ -806,7 +808,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) backward_kernel(const Backward
                     dw.v[e] = fma2(g.v[e], mul2(x.v[e], rr), dw.v[e]);
                     y.v[e] = fma2(wg.v[e], rr, mul2(x.v[e], mm));
                 }
-                if (sub + i * NV < mine) store_bf16<D, SPLIT>(dst, l, pack(y));
+                if (live) store_bf16<D, SPLIT>(dst, l, pack(y));
                 dst += dst_step;
             }
             const int kind_next = part_next >= a.q_parts;

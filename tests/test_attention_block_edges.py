@@ -1,0 +1,53 @@
+"""The attention block at the ends of what its calls accept, against 64 bits: eps of zero, inputs far from one,
+other streams and devices, workspaces of captured graphs, the codes of keys to the last bit."""
+import numpy as np
+import pytest
+import torch
+
+import _attention_ref as ref
+from _helpers import dev
+from test_attention_block import U, np64, on, r9q, rand, rope_args, tables  # noqa: F401  (r9q: the fixture)
+
+
+# (T, Hq, Hk, D, rot, interleaved): head counts that leave lanes of a warp without a head, and some that do not
+HEADS = [(5, 14, 2, 64, 32, True), (777, 14, 2, 64, 64, False), (9, 5, 1, 64, 0, False), (3, 8, 8, 64, 64, False),
+         (5, 3, 1, 128, 128, False), (1100, 7, 5, 128, 64, True), (4, 1, 1, 128, 96, False), (6, 8, 4, 128, 128, False)]
+
+
+def grad_case(T, Hq, Hk, D, rot, scale, seed):
+    """Queries, keys, their outputs' gradients, weights, and the angles of T positions."""
+    x = [rand((T, h, D), seed + i, scale).to(dev()) for i, h in enumerate((Hq, Hk))]
+    dy = [rand((T, h, D), seed + 2 + i).to(dev()) for i, h in enumerate((Hq, Hk))]
+    g = np.random.default_rng(seed)
+    w = [g.normal(1, 0.3, D).astype(np.float32) for _ in range(2)]
+    pos = g.integers(0, 5000, T)
+    cos, sin = tables(5000, rot) if rot else (None, None)
+    return x, dy, w, cos, sin, pos
+
+
+def check_grad(r9q, T, Hq, Hk, D, rot, inter, scale, eps, seed):
+    """Bounds: dx = r (w g - xh mean(w g xh)), xh = x r, in fp32 and then one rounding to bf16.  g is two products, the
+    mean D of them, r and xh carry a few roundings each: 2^-19 of the terms' largest sums.  dw: 2^-20 sum |terms|."""
+    x, dy, w, cos, sin, pos = grad_case(T, Hq, Hk, D, rot, scale, seed)
+    out = r9q.r9q_qk_norm_rope_bwd(*dy, *x, *rope_args(*w, cos, sin, pos), eps=eps, interleaved=inter)
+    c, s = (None, None) if cos is None else (cos[pos].astype(np.float64), sin[pos].astype(np.float64))
+    for i in range(2):
+        xi, gi, wi = np64(x[i]), np64(dy[i]), w[i].astype(np.float64)
+        ex, ew, mass = ref.norm_rope_grad(gi, xi, w[i], c, s, eps, inter)
+        terms = np.abs(gi)
+        if c is not None:
+            own = ref.rotate(gi, c, 0 * s, inter)
+            terms = np.abs(own) + np.abs(ref.rotate(gi, c, -s, inter) - own)
+        r = 1 / np.sqrt((xi * xi).mean(-1, keepdims=True) + eps)
+        t = terms * np.abs(wi)
+        big = r * (t.max(-1, keepdims=True) +
+                   np.abs(xi * r).max(-1, keepdims=True) * (t * np.abs(xi * r)).mean(-1, keepdims=True))
+        assert (np.abs(np64(out[i]) - ex) <= U * np.abs(ex) * 1.01 + 2.0 ** -19 * big).all()
+        assert (np.abs(np64(out[2 + i]) - ew) <= 2.0 ** -20 * mass).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,Hq,Hk,D,rot,inter", HEADS)
+def test_gradient_with_eps_of_zero(r9q, T, Hq, Hk, D, rot, inter):  # noqa: F811
+    """Lanes that have no head add nothing to the weights' gradients, though 1 / sqrt(0) is infinite."""
+    check_grad(r9q, T, Hq, Hk, D, rot, inter, 1.0, 0.0, 201)
