@@ -51,3 +51,36 @@ def check_grad(r9q, T, Hq, Hk, D, rot, inter, scale, eps, seed):
 def test_gradient_with_eps_of_zero(r9q, T, Hq, Hk, D, rot, inter):  # noqa: F811
     """Lanes that have no head add nothing to the weights' gradients, though 1 / sqrt(0) is infinite."""
     check_grad(r9q, T, Hq, Hk, D, rot, inter, 1.0, 0.0, 201)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,Hq,Hk,D,rot,inter", HEADS)
+@pytest.mark.parametrize("scale,eps", [(1e-14, 0.0), (1e-12, 0.0), (1e-6, 1e-6), (1e10, 1e-6), (1e14, 1e-6), (1e15, 0.0),
+                                       (1e17, 1e-6)])
+def test_gradient_of_inputs_far_from_one(r9q, T, Hq, Hk, D, rot, inter, scale, eps):  # noqa: F811
+    check_grad(r9q, T, Hq, Hk, D, rot, inter, scale, eps, 211)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,Hq,Hk,D,rot,inter", HEADS)
+@pytest.mark.parametrize("scale,eps", [(1.0, 0.0), (1e-14, 0.0), (1e-6, 1e-6), (1e10, 1e-6), (1e17, 1e-6)])
+def test_norm_of_inputs_far_from_one(r9q, T, Hq, Hk, D, rot, inter, scale, eps):  # noqa: F811
+    """u |y| + 2^-20 of the head's largest element, as for inputs near one."""
+    x, _, w, cos, sin, pos = grad_case(T, Hq, Hk, D, rot, scale, 221)
+    out = r9q.r9q_qk_norm_rope(*x, *rope_args(*w, cos, sin, pos), eps=eps, interleaved=inter)
+    c, s = (None, None) if cos is None else (cos[pos], sin[pos])
+    for xi, wi, y in zip(x, w, out):
+        e = ref.norm_rope(np64(xi), wi, c, s, eps, inter)
+        assert (np.abs(np64(y) - e) <= U * np.abs(e) * 1.01 + 2.0 ** -20 * np.abs(e).max(-1, keepdims=True)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("eps", [1e-6, 1e-30])
+def test_gradient_of_zero_vectors(r9q, eps):  # noqa: F811
+    """dx = w dy / sqrt(eps), however large 1 / sqrt(eps) is, and nothing for dw."""
+    T, H, D = 3, 5, 128
+    x, dy = torch.zeros((T, H, D), dtype=torch.bfloat16, device=dev()), rand((T, H, D), 231).to(dev())
+    w = on(np.random.default_rng(231).normal(1, 0.3, D).astype(np.float32))
+    dq, _, dwq, _ = r9q.r9q_qk_norm_rope_bwd(dy, dy, x, x, w, w, eps=eps)
+    e = np64(dy) * np64(w) / np.sqrt(float(np.float32(eps)))
+    assert (np.abs(np64(dq) - e) <= (U * 1.01 + 2.0 ** -20) * np.abs(e)).all() and bool((dwq == 0).all())
