@@ -367,16 +367,24 @@ def r9q_kv4_cache(pages: int, heads: int, page: int, dim: int, device=None) -> K
 
 
 # These calls last microseconds on the GPU: _calls (csrc/r9q_calls.cpp) checks their tensors and makes the C call.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _stream_handle(index, stream):
-    """The handle of `stream`, or of the current stream of the device `index`."""
-    if stream is not None:
-        return stream.cuda_stream
+def _elsewhere(device, stream, call, *args):
+    """call(*args, stream=None) with the tensors' device and the given stream current: the C call launches on the current
+    device, and new outputs belong to the current stream."""
+    index = device.index
     if index is None:
         raise ValueError("tensor must be on a CUDA device")
-    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+    if stream is None:
+        with torch.cuda.device(index):
+            return call(*args, stream=None)
+    if stream.device.index != index:
+        raise ValueError("stream is of another device than the tensors")
+    with torch.cuda.stream(stream):
+        return call(*args, stream=None)
 
 
 def _checked(r, where):
@@ -389,11 +397,14 @@ def _checked(r, where):
 def _with_workspace(where, op, size, call, args, workspace, device, stream):
     """A call that needs a workspace: the caller's, or the stream's own, made or grown where that does not do.
     size(): the M and N that r9q_workspace_bytes takes."""
-    handle = _stream_handle(device.index, stream)
-    own = workspace if workspace is not None else _WORKSPACES.get((device.index, handle))
+    index = device.index
+    if stream is not None or index is None or index != _current_device():
+        return _elsewhere(device, stream, _with_workspace, where, op, size, call, args, workspace, device)
+    handle = _raw_stream(index)
+    own = workspace if workspace is not None else _WORKSPACES.get((index, handle))
     r = call(*args, own, handle)
     if workspace is None and r.__class__ is int and r == R9Q_ERR_WORKSPACE:
-        own = _stream_workspace(r9q_workspace_bytes(op, *size(), 0), device, stream)
+        own = _stream_workspace(r9q_workspace_bytes(op, *size(), 0), device)
         r = call(*args, own, handle)
     return _checked(r, where)
 
@@ -405,8 +416,12 @@ def r9q_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, wq: torch.Tensor, wk: tor
     """RMS norm of the heads of q bf16 [T][Hq][D] and k bf16 [T][Hk][D] (any token and head strides) and the
     rotation by cos, sin fp32 [npos][rot/2] at positions int64 [T] (None: norm only); returns (q_out, k_out), which
     are parts of one allocation where neither was given."""
+    index = q.device.index
+    if stream is not None or index is None or index != _current_device():
+        return _elsewhere(q.device, stream, r9q_qk_norm_rope, q, k, wq, wk, cos, sin, positions, eps, interleaved, q_out,
+                          k_out)
     return _checked(_calls.qk_norm_rope(q, k, wq, wk, cos, sin, positions, eps, interleaved, q_out, k_out,
-                                        _stream_handle(q.device.index, stream)), "r9q_qk_norm_rope")
+                                        _raw_stream(index)), "r9q_qk_norm_rope")
 
 
 def r9q_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
@@ -430,21 +445,30 @@ def r9q_qk_norm_rope_kv4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, wq: 
                          q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """r9q_qk_norm_rope with the keys, and v bf16 [T][Hk][D] as it is, written to the cache at slots int64 [T]
     (page * tokens of a page + place; negative: padding); returns q_out."""
+    index = q.device.index
+    if stream is not None or index is None or index != _current_device():
+        return _elsewhere(q.device, stream, r9q_qk_norm_rope_kv4, q, k, v, wq, wk, cos, sin, positions, cache, slots, eps,
+                          interleaved, q_out)
     return _checked(_calls.qk_norm_rope_kv4(q, k, v, wq, wk, cos, sin, positions, *cache, slots, eps, interleaved, q_out,
-                                            _stream_handle(q.device.index, stream)), "r9q_qk_norm_rope_kv4")
+                                            _raw_stream(index)), "r9q_qk_norm_rope_kv4")
 
 
 def r9q_kv4_append(k: torch.Tensor, v: torch.Tensor, cache: KV4Cache, slots: torch.Tensor, stream=None) -> None:
     """Writes k and v bf16 [T][Hk][D] to the cache at slots int64 [T] (negative: padding)."""
-    _checked(_calls.kv4_append(k, v, *cache, slots, _stream_handle(k.device.index, stream)), "r9q_kv4_append")
+    index = k.device.index
+    if stream is not None or index is None or index != _current_device():
+        return _elsewhere(k.device, stream, r9q_kv4_append, k, v, cache, slots)
+    _checked(_calls.kv4_append(k, v, *cache, slots, _raw_stream(index)), "r9q_kv4_append")
 
 
 def r9q_kv4_gather(cache: KV4Cache, slots: torch.Tensor, k: torch.Tensor | None = None,
                    v: torch.Tensor | None = None, stream=None):
     """The tokens at slots int64 [T] as bf16 (k, v) [T][Hk][D] (parts of one allocation where neither was given);
     zeros for padding."""
-    return _checked(_calls.kv4_gather(*cache, slots, k, v, _stream_handle(slots.device.index, stream)),
-                    "r9q_kv4_gather")
+    index = slots.device.index
+    if stream is not None or index is None or index != _current_device():
+        return _elsewhere(slots.device, stream, r9q_kv4_gather, cache, slots, k, v)
+    return _checked(_calls.kv4_gather(*cache, slots, k, v, _raw_stream(index)), "r9q_kv4_gather")
 
 
 def r9q_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, seq_lens: torch.Tensor,

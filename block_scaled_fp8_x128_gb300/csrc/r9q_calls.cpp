@@ -6,7 +6,8 @@
 // is: each function takes its arguments by position, makes the outputs that are None
 // and calls the entry point of include/r9q.h of the same name.  It returns the outputs,
 // or the entry point's code as an int where that is not 0; a tensor of the wrong type,
-// shape, layout or device raises as the rest of the binding does.
+// shape, layout or device raises as the rest of the binding does.  The caller has made the
+// tensors' device and the call's stream the current ones.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -98,7 +99,7 @@ bool truth(PyObject* o) {
 }
 void* stream(PyObject* o) { return reinterpret_cast<void*>(integer(o)); }
 
-// New contiguous tensors from torch's allocator, without the dispatcher.  Those of one call that live together share an
+// New contiguous tensors of the current stream from torch's allocator, without the dispatcher.  Those of one call that live together share an
 // allocation: each costs about a microsecond, as much as all checks of a call.
 using Storage = c10::intrusive_ptr<c10::StorageImpl>;
 size_t elements(at::IntArrayRef shape) {

@@ -84,3 +84,80 @@ def test_gradient_of_zero_vectors(r9q, eps):  # noqa: F811
     dq, _, dwq, _ = r9q.r9q_qk_norm_rope_bwd(dy, dy, x, x, w, w, eps=eps)
     e = np64(dy) * np64(w) / np.sqrt(float(np.float32(eps)))
     assert (np.abs(np64(dq) - e) <= (U * 1.01 + 2.0 ** -20) * np.abs(e)).all() and bool((dwq == 0).all())
+
+
+# ----------------------------------------------------- streams and devices --
+
+def attention_inputs(r9q, Hq=4, Hk=2, D=128, n=40, seed=241):  # noqa: F811
+    """One sequence in a cache: (q, cache, table, lengths)."""
+    cache = r9q.r9q_kv4_cache(-(-n // 16), Hk, 16, D)
+    kv = rand((n, 2 * Hk, D), seed).to(dev())
+    r9q.r9q_kv4_append(kv[:, :Hk], kv[:, Hk:], cache, torch.arange(n, device=dev()))
+    return (rand((1, 1, Hq, D), seed + 1).to(dev()), cache, torch.arange(-(-n // 16), dtype=torch.int32, device=dev())[None],
+            torch.tensor([n], dtype=torch.int32, device=dev()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["rope", "grad", "write", "gather", "attention"])
+def test_outputs_belong_to_the_stream_of_the_call(r9q, name):  # noqa: F811
+    """The current stream still has work on a block that it has let go; outputs of a call on another stream are not
+    made of that block."""
+    T, H, D = 2048, 8, 128
+    x, w = rand((T, H, D), 251).to(dev()), torch.ones(D, device=dev())
+    q, cache, table, lens = attention_inputs(r9q)
+    qs, many = q.expand(4096, 1, 4, D), (table.expand(4096, -1).contiguous(), lens.expand(4096).contiguous())
+    big, slots = r9q.r9q_kv4_cache(T // 16, H, 16, D), torch.arange(T, device=dev())
+    calls = {"rope": lambda **k: r9q.r9q_qk_norm_rope(x, x, w, w, **k),
+             "grad": lambda **k: r9q.r9q_qk_norm_rope_bwd(x, x, x, x, w, w, **k),
+             "write": lambda **k: r9q.r9q_qk_norm_rope_kv4(x, x, x, w, w, None, None, None, big, slots, **k),
+             "gather": lambda **k: r9q.r9q_kv4_gather(big, slots, **k),
+             "attention": lambda **k: r9q.r9q_kv4_attention(qs, cache, *many, return_lse=True, **k)}
+    r9q.r9q_kv4_append(x, x, big, slots)
+    st = torch.cuda.Stream()
+    want = calls[name]()
+    with torch.cuda.stream(st):
+        calls[name]()                                         # (workspaces, and blocks that the stream can have again)
+    torch.cuda.synchronize()
+    want = want if isinstance(want, tuple) else (want,)
+    first = want[0]
+    room = first.untyped_storage().nbytes()
+    block = torch.empty(room, dtype=torch.uint8, device=dev())
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    block.fill_(7)
+    del block
+    got = calls[name](stream=st)
+    got = got if isinstance(got, tuple) else (got,)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.gpu
+def test_calls_run_on_the_device_of_their_tensors(r9q, monkeypatch):  # noqa: F811
+    """With another device current (as the binding sees it), a call makes the tensors' own current; a stream of another
+    device is refused."""
+    x, w = rand((3, 2, 64), 261).to(dev()), torch.ones(64, device=dev())
+    q, cache, table, lens = attention_inputs(r9q)
+    want, o = r9q.r9q_qk_norm_rope(x, x, w, w), r9q.r9q_kv4_attention(q, cache, table, lens)
+    entered, now = [], [1]
+
+    class Device(torch.cuda.device):
+        def __enter__(self):
+            entered.append(self.idx)
+            now.append(self.idx)
+            return super().__enter__()
+
+        def __exit__(self, *error):
+            now.pop()
+            return super().__exit__(*error)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(r9q, "_current_device", lambda: now[-1])
+    got = r9q.r9q_qk_norm_rope(x, x, w, w)
+    assert entered == [0] and all(torch.equal(a, b) for a, b in zip(want, got))
+    assert torch.equal(o, r9q.r9q_kv4_attention(q, cache, table, lens)) and entered == [0, 0] and now == [1]
+
+    class Other:
+        device = torch.device("cuda", 1)
+        cuda_stream = 12345
+    with pytest.raises(ValueError):
+        r9q.r9q_qk_norm_rope(x, x, w, w, stream=Other())
