@@ -33,6 +33,7 @@ _SIGS = {
     "r9q_version": ([], ctypes.c_int),
     "r9q_strerror": ([ctypes.c_int], ctypes.c_char_p),
     "r9q_last_device_error": ([_P], ctypes.c_int),
+    "r9q_stream_capture_id": ([_P, ctypes.POINTER(ctypes.c_ulonglong)], ctypes.c_int),
     "r9q_set_pdl": ([ctypes.c_int], ctypes.c_int),
     "r9q_selftest_wait_timeout": ([ctypes.c_int, _P], ctypes.c_int),
     "r9q_grouped_gemm_fp8": ([_P, ctypes.POINTER(_I64), _I64, _P, _P, _P, _I64, _I64, ctypes.c_int, _P],
@@ -161,21 +162,45 @@ def r9q_set_pdl(enable: bool) -> bool:
 def r9q_last_device_error(stream=None) -> int:
     rc = int(_lib.r9q_last_device_error(_stream(stream)))
     if rc != 0:
-        # a kernel gave up mid-call: its workspace counters may be left non-zero
+        # a kernel may have given up mid-call and left its workspace's counters non-zero (graphs zero their own)
         _WORKSPACES.clear()
     return rc
 
 
-# One zero-filled W8A8 workspace per (device, stream) for calls that pass
-# none.  Every call that completes leaves the workspace's counter header at
-# zero again, so the same tensor serves every later call on that stream
-# (calls on one stream are ordered); it grows when a larger call needs more.
+# One zero-filled workspace per (device, stream) for calls that pass none.  Every call
+# that completes leaves the workspace's counter header at zero again, so the same tensor
+# serves every later call on that stream (calls on one stream are ordered); it grows when
+# a larger call needs more.
 _WORKSPACES: dict = {}
+# A graph keeps the addresses of what it captured, and may be replayed at any time and on
+# any stream, so the calls of a capture have a workspace of their own: from the graph's
+# memory, its header zeroed by a node of the graph.  Here the last one of each stream,
+# {(device, stream): (capture, workspace)}; the graph itself holds the memory.
+_CAPTURED: dict = {}
+_HEADER = 64 * 1024                                           # the counters, zero between calls
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+
+
+def r9q_stream_capture_id(stream=None) -> int:
+    """The id of the capture that the stream is part of, 0 if none."""
+    out = ctypes.c_ulonglong(0)
+    _check(_lib.r9q_stream_capture_id(_stream(stream), ctypes.byref(out)), "r9q_stream_capture_id")
+    return int(out.value)
 
 
 def _stream_workspace(need: int, device: torch.device, stream=None) -> torch.Tensor:
+    """The workspace of the stream, or of the capture that it is part of, made or grown to `need` bytes."""
     s = stream if stream is not None else torch.cuda.current_stream(device)
     key = (device.index, s.cuda_stream)
+    capture = r9q_stream_capture_id(s) if stream is not None or _capturing() else 0
+    if capture:
+        of, ws = _CAPTURED.get(key, (0, None))
+        if of != capture or ws.numel() < need:
+            with torch.cuda.stream(s):
+                ws = torch.empty(need, dtype=torch.uint8, device=device)
+                ws[:_HEADER].zero_()
+            _CAPTURED[key] = (capture, ws)
+        return ws
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < need:
         with torch.cuda.stream(s):                            # zeroed on the stream that uses it
@@ -250,8 +275,9 @@ def r9q_gemm_fp8_block_qa(a: torch.Tensor | None, w: torch.Tensor, ws: torch.Ten
     bytes, zero-filled before its first use (e.g. torch.zeros); the calls keep its counter
     header at zero, so one workspace serves any sequence of calls on one stream.  When omitted,
     the binding reuses one zeroed workspace per (device, stream), allocated (and zero-filled)
-    on the first call that needs it or needs more; pass your own to control that allocation,
-    e.g. before capturing a CUDA graph."""
+    on the first call that needs it or needs more; the calls of a graph capture have one of the
+    graph's own, which the graph zeroes whenever it is replayed.  Pass your own to save that node and to
+    control the allocation."""
     N, K = w.shape
     src = a if a is not None else aq
     if src is None:
@@ -401,7 +427,10 @@ def _with_workspace(where, op, size, call, args, workspace, device, stream):
     if stream is not None or index is None or index != _current_device():
         return _elsewhere(device, stream, _with_workspace, where, op, size, call, args, workspace, device)
     handle = _raw_stream(index)
-    own = workspace if workspace is not None else _WORKSPACES.get((index, handle))
+    own = workspace
+    if own is None:
+        own = (_stream_workspace(r9q_workspace_bytes(op, *size(), 0), device) if _capturing() else
+               _WORKSPACES.get((index, handle)))
     r = call(*args, own, handle)
     if workspace is None and r.__class__ is int and r == R9Q_ERR_WORKSPACE:
         own = _stream_workspace(r9q_workspace_bytes(op, *size(), 0), device)

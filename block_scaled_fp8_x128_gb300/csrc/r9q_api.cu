@@ -446,6 +446,25 @@ int r9q_last_device_error(void* stream) {
     return h;
 }
 
+int r9q_stream_capture_id(void* stream, unsigned long long* id) {
+    if (!id) return R9Q_ERR_NULL;
+    *id = 0;
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long of = 0;
+    const cudaError_t e = cudaStreamGetCaptureInfo(static_cast<cudaStream_t>(stream), &status, &of, nullptr, nullptr,
+                                                   nullptr, nullptr);
+    if (e == cudaErrorStreamCaptureImplicit) {         // the legacy stream while another is captured: it is not
+        (void)cudaGetLastError();
+        return R9Q_OK;
+    }
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return R9Q_ERR_LAUNCH;
+    }
+    if (status != cudaStreamCaptureStatusNone) *id = of;
+    return R9Q_OK;
+}
+
 int r9q_e4m3_from_f32(const float* x, int64_t n, uint8_t* q, void* stream) {
     if (n < 0) return R9Q_ERR_DIM;
     if (n == 0) return R9Q_OK;

@@ -80,7 +80,7 @@ def main():
     warm.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(warm):
         before = layer.lens.clone()
-        layer.step(x)                                    # makes the stream's workspaces
+        layer.step(x)                                    # what a first call sets up once is not part of the graph
         layer.lens.copy_(before)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=warm):

@@ -349,6 +349,11 @@ int r9q_kv4_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, c
                       int64_t page, int64_t max_pages, int64_t window, float scale, void* workspace,
                       size_t workspace_bytes, void* stream);
 
+/* Writes the id of the capture that `stream` is part of to *id, 0 where it is not being
+ * captured.  For callers that keep workspaces by stream: a captured graph keeps the
+ * address of a workspace, so it needs one of its own, zeroed inside the capture. */
+int r9q_stream_capture_id(void* stream, unsigned long long* id);
+
 /* Workspace query. */
 #define R9Q_OP_GEMM_W8A8            1   /* (M, N, K) */
 #define R9Q_OP_GEMM_W8BF16          2   /* (M, N, K) */

@@ -161,3 +161,108 @@ def test_calls_run_on_the_device_of_their_tensors(r9q, monkeypatch):  # noqa: F8
         cuda_stream = 12345
     with pytest.raises(ValueError):
         r9q.r9q_qk_norm_rope(x, x, w, w, stream=Other())
+
+
+# --------------------------------------------- workspaces of captured graphs --
+
+def sequences(r9q, count, n, Hq, Hk, D, Lq, seed):  # noqa: F811
+    """`count` sequences of n tokens, long enough that several CTAs share each: (q, cache, table, lengths)."""
+    page = 64
+    per = -(-n // page)
+    cache = r9q.r9q_kv4_cache(count * per, Hk, page, D)
+    kv = rand((count * per * page, 2 * Hk, D), seed).to(dev())
+    r9q.r9q_kv4_append(kv[:, :Hk], kv[:, Hk:], cache, torch.arange(len(kv), device=dev()))
+    return (rand((count, Lq, Hq, D), seed + 1).to(dev()), cache,
+            torch.arange(count * per, dtype=torch.int32, device=dev()).view(count, per),
+            torch.full((count,), n, dtype=torch.int32, device=dev()))
+
+
+def captured(f, stream=None):
+    """The graph of f() and its outputs."""
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        out = f()
+    return g, out
+
+
+def occupy():
+    """Memory of the stream that is current, full of ones, in blocks of the sizes that workspaces have."""
+    return [torch.full((2 ** k,), -1, dtype=torch.int8, device=dev()) for k in range(16, 26) for _ in range(4)]
+
+
+@pytest.mark.gpu
+def test_a_graph_keeps_its_workspace(r9q):  # noqa: F811
+    """A decode step is captured; then, on the stream it was captured on, a call that needs a larger workspace, an error
+    that lets the workspaces go, and other tensors.  Replays are what they were."""
+    st = torch.cuda.Stream()
+    with torch.cuda.stream(st):
+        few = sequences(r9q, 2, 3000, 8, 2, 128, 1, 271)
+        many = sequences(r9q, 2, 3000, 8, 2, 128, 4, 272)
+        want = r9q.r9q_kv4_attention(*few)
+        x, w = rand((700, 9, 128), 273).to(dev()), torch.ones(128, device=dev())
+        dwant = r9q.r9q_qk_norm_rope_bwd(x, x, x, x, w, w)
+        st.synchronize()
+        g, out = captured(lambda: (r9q.r9q_kv4_attention(*few), *r9q.r9q_qk_norm_rope_bwd(x, x, x, x, w, w)), st)
+        r9q.r9q_kv4_attention(*many)
+        bad = few[2].clone()
+        bad[0, 0] = 1 << 20
+        r9q.r9q_kv4_attention(few[0], few[1], bad, few[3])
+        assert r9q.r9q_last_device_error() == -8
+        kept = occupy()
+        for _ in range(3):
+            for t in out:
+                t.zero_()
+            g.replay()
+            assert all(torch.equal(a, b) for a, b in zip((want, *dwant), out))
+        assert all(bool((t == -1).all()) for t in kept)
+        assert torch.equal(r9q.r9q_kv4_attention(*few), want)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.gpu
+def test_graphs_of_one_stream_stand_alone(r9q):  # noqa: F811
+    """Nothing has run on the stream before it is captured, twice; the second graph is replayed first, the first one is
+    let go, and two graphs run at the same time on two streams."""
+    cases = [sequences(r9q, 1 + i, 5000 + 900 * i, 8, 2, 128, 1, 281 + i) for i in range(3)]
+    want = [r9q.r9q_kv4_attention(*c) for c in cases]
+    gemm = (rand((64, 1024), 291).to(dev()), *r9q.r9q_quant_weight_block128(rand((4096, 1024), 292).float().to(dev())))
+    y = r9q.r9q_gemm_fp8_block_qa(*gemm)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    graphs = [captured(lambda c=c: (r9q.r9q_kv4_attention(*c), r9q.r9q_gemm_fp8_block_qa(*gemm)), st) for c in cases]
+    for i in (1, 0, 2, 1):
+        graphs[i][0].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(graphs[i][1][0], want[i]) and torch.equal(graphs[i][1][1], y)
+    graphs[0] = None
+    kept = occupy()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for i in (1, 2):
+            graphs[i][1][0].zero_()
+        torch.cuda.synchronize()
+        for i, s in zip((1, 2), streams):
+            with torch.cuda.stream(s):
+                for _ in range(5):
+                    graphs[i][0].replay()
+        torch.cuda.synchronize()
+        for i in (1, 2):
+            assert torch.equal(graphs[i][1][0], want[i]) and torch.equal(graphs[i][1][1], y)
+    assert all(bool((t == -1).all()) for t in kept)
+
+
+@pytest.mark.gpu
+def test_capture_ids(r9q):  # noqa: F811
+    st, seen = torch.cuda.Stream(), []
+    torch.ones(1, device=dev())
+    with torch.cuda.stream(st):
+        assert r9q.r9q_stream_capture_id() == 0
+        for _ in range(2):
+            captured(lambda: (seen.append(r9q.r9q_stream_capture_id()), seen.append(r9q.r9q_stream_capture_id(st)),
+                              torch.ones(1, device=dev())), st)
+        assert r9q.r9q_stream_capture_id() == 0
+    assert seen[0] == seen[1] != 0 and seen[2] == seen[3] != 0 and seen[0] != seen[2]
+
+
+def test_capture_id_refusal(r9q):  # noqa: F811
+    assert r9q._lib.r9q_stream_capture_id(None, None) == -1
