@@ -12,6 +12,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/util/Exception.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdarg>
@@ -346,7 +347,14 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
         return CALL(args);
     } catch (const Raised&) {
         return nullptr;
-    } catch (const std::exception& e) {          // torch's own (out of memory, for one)
+    } catch (const c10::OutOfMemoryError& e) {   // as torch raises it: torch.OutOfMemoryError
+        PyObject* torch = PyImport_ImportModule("torch");
+        PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+        if (type) PyErr_SetString(type, e.what_without_backtrace());
+        Py_XDECREF(type);
+        Py_XDECREF(torch);
+        return nullptr;
+    } catch (const std::exception& e) {          // another of torch's own
         PyErr_SetString(PyExc_RuntimeError, e.what());
         return nullptr;
     }

@@ -163,6 +163,20 @@ def test_calls_run_on_the_device_of_their_tensors(r9q, monkeypatch):  # noqa: F8
         r9q.r9q_qk_norm_rope(x, x, w, w, stream=Other())
 
 
+@pytest.mark.gpu
+def test_out_of_memory_is_torch_s(r9q):  # noqa: F811
+    """Outputs that do not fit (of a small share of the memory that the process may have): the error that torch raises."""
+    cache, slots = r9q.r9q_kv4_cache(4, 8, 16, 128), torch.zeros(2_000_000, dtype=torch.int64, device=dev())
+    torch.cuda.set_per_process_memory_fraction(0.01)
+    try:
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            r9q.r9q_kv4_gather(cache, slots)                  # 8 GB
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    k, v = r9q.r9q_kv4_gather(cache, slots[:16])
+    assert k.shape == (16, 8, 128) and r9q.r9q_last_device_error() == 0
+
+
 # --------------------------------------------- workspaces of captured graphs --
 
 def sequences(r9q, count, n, Hq, Hk, D, Lq, seed):  # noqa: F811
