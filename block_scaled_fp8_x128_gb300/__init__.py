@@ -372,6 +372,7 @@ def r9q_gate_up_swiglu_down_noalloc(x: torch.Tensor, w_gu: torch.Tensor, s_gu: t
 
 
 # ---- the attention block of a decode layer ----
+# Of these calls r9q_qk_norm_rope is recorded by autograd; the others' outputs carry no gradient.
 
 class KV4Cache(NamedTuple):
     """The paged 4-bit key-value cache (layout: include/r9q.h).  k uint8 [pages][Hk][page][D/2], v uint8 of the
@@ -438,17 +439,44 @@ def _with_workspace(where, op, size, call, args, workspace, device, stream):
     return _checked(r, where)
 
 
+def _readable(t):
+    """t as the kernels read head tensors: contiguous vectors on 16-byte boundaries."""
+    ok = t.stride(2) == 1 and t.stride(0) % 8 == 0 and t.stride(1) % 8 == 0 and t.data_ptr() % 16 == 0
+    return t if ok else t.contiguous()
+
+
+class _NormRope(torch.autograd.Function):
+    """r9q_qk_norm_rope with r9q_qk_norm_rope_bwd as its gradient (to q, k, wq and wk)."""
+
+    @staticmethod
+    def forward(ctx, q, k, wq, wk, cos, sin, positions, eps, interleaved):
+        ctx.save_for_backward(q, k, wq, wk, cos, sin, positions)
+        ctx.how = (eps, interleaved)
+        return _checked(_calls.qk_norm_rope(q, k, wq, wk, cos, sin, positions, eps, interleaved, None, None,
+                                            _raw_stream(q.device.index)), "r9q_qk_norm_rope")
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        return (*r9q_qk_norm_rope_bwd(_readable(dq_out), _readable(dk_out), *ctx.saved_tensors, *ctx.how),
+                None, None, None, None, None)
+
+
 def r9q_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, wq: torch.Tensor, wk: torch.Tensor,
                      cos: torch.Tensor | None = None, sin: torch.Tensor | None = None,
                      positions: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
                      q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
     """RMS norm of the heads of q bf16 [T][Hq][D] and k bf16 [T][Hk][D] (any token and head strides) and the
     rotation by cos, sin fp32 [npos][rot/2] at positions int64 [T] (None: norm only); returns (q_out, k_out), which
-    are parts of one allocation where neither was given."""
+    are parts of one allocation where neither was given.  Then they carry the gradient to q, k, wq and wk where one of
+    these requires it; a call that is given an output is not recorded."""
     index = q.device.index
     if stream is not None or index is None or index != _current_device():
         return _elsewhere(q.device, stream, r9q_qk_norm_rope, q, k, wq, wk, cos, sin, positions, eps, interleaved, q_out,
                           k_out)
+    if ((q.requires_grad or k.requires_grad or wq.requires_grad or wk.requires_grad) and torch.is_grad_enabled() and
+            q_out is None and k_out is None):
+        return _NormRope.apply(q, k, wq, wk, cos, sin, positions, eps, interleaved)
     return _checked(_calls.qk_norm_rope(q, k, wq, wk, cos, sin, positions, eps, interleaved, q_out, k_out,
                                         _raw_stream(index)), "r9q_qk_norm_rope")
 

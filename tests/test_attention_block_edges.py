@@ -86,6 +86,57 @@ def test_gradient_of_zero_vectors(r9q, eps):  # noqa: F811
     assert (np.abs(np64(dq) - e) <= (U * 1.01 + 2.0 ** -20) * np.abs(e)).all() and bool((dwq == 0).all())
 
 
+# ---------------------------------------------------------------- autograd --
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,Hq,Hk,D,rot,inter", HEADS)
+def test_autograd(r9q, T, Hq, Hk, D, rot, inter):  # noqa: F811
+    """backward() of a call gives what r9q_qk_norm_rope_bwd gives (which the tests above hold to 64 bits): of slices of
+    one tensor, with gradients of any layout, and from one output alone."""
+    x, dy, w, cos, sin, pos = grad_case(T, Hq, Hk, D, rot, 1.5, 301)
+    x, dy = [t + 0 for t in x], [t + 0 for t in dy]
+    qk = torch.cat(x, 1).requires_grad_()
+    wq, wk, *angles = rope_args(*w, cos, sin, pos)
+    wq.requires_grad_(), wk.requires_grad_()
+    q, k = qk[:, :Hq], qk[:, Hq:]
+    plain = r9q.r9q_qk_norm_rope(*x, wq.detach(), wk.detach(), *angles, eps=1e-5, interleaved=inter)
+    out = r9q.r9q_qk_norm_rope(q, k, wq, wk, *angles, eps=1e-5, interleaved=inter)
+    assert all(torch.equal(a, b) and a.requires_grad and not b.requires_grad for a, b in zip(out, plain))
+    for far in (dy, [d.transpose(1, 2).contiguous().transpose(1, 2) for d in dy]):
+        got = torch.autograd.grad(out, (qk, wq, wk), far, retain_graph=True)
+        want = r9q.r9q_qk_norm_rope_bwd(*dy, *x, wq, wk, *angles, eps=1e-5, interleaved=inter)
+        assert torch.equal(got[0], torch.cat(want[:2], 1)) and torch.equal(got[1], want[2]) and torch.equal(got[2], want[3])
+    got = torch.autograd.grad(out[0].float().sum(), (qk, wq, wk))          # (a gradient of stride 0, none for the keys)
+    ones, none = torch.ones_like(x[0]), torch.zeros_like(x[1])
+    want = r9q.r9q_qk_norm_rope_bwd(ones, none, *x, wq, wk, *angles, eps=1e-5, interleaved=inter)
+    assert torch.equal(got[0], torch.cat(want[:2], 1)) and torch.equal(got[1], want[2]) and bool((got[2] == 0).all())
+    with torch.no_grad():
+        assert not r9q.r9q_qk_norm_rope(q, k, wq, wk, *angles, eps=1e-5, interleaved=inter)[0].requires_grad
+
+
+@pytest.mark.gpu
+def test_autograd_trains_and_refuses_a_second_derivative(r9q):  # noqa: F811
+    """Steps down the gradient of ((norm(x) - t)^2).sum() lower it, on a stream of their own; what is not recorded says so."""
+    T, H, D = 40, 3, 64
+    with torch.cuda.stream(torch.cuda.Stream()):
+        x, t = rand((T, H, D), 311).to(dev()), rand((T, H, D), 312, 0.5).to(dev())
+        w = torch.ones(D, device=dev(), requires_grad=True)
+        losses = []
+        for _ in range(5):
+            q, k = r9q.r9q_qk_norm_rope(x, x, w, w)
+            loss = ((q.float() - t.float()) ** 2).mean() + ((k.float() - t.float()) ** 2).mean()
+            g, = torch.autograd.grad(loss, w)
+            losses.append(loss.item())
+            w = (w - 5 * g).detach().requires_grad_()
+        assert all(b < a for a, b in zip(losses, losses[1:]))
+        y = r9q.r9q_qk_norm_rope(x, x, w, w)[0]
+        g, = torch.autograd.grad(y.float().square().sum(), w, create_graph=True)
+        with pytest.raises(RuntimeError):
+            g.sum().backward()
+        buf = torch.empty_like(x)
+        assert not r9q.r9q_qk_norm_rope(x, x, w, w, q_out=buf)[0].requires_grad
+
+
 # ----------------------------------------------------- streams and devices --
 
 def attention_inputs(r9q, Hq=4, Hk=2, D=128, n=40, seed=241):  # noqa: F811
