@@ -5,11 +5,13 @@ shape and device, and calls the C entry point of the same name in
 ``include/r9q.h`` on the current CUDA stream, through ctypes or, for the
 attention block's calls, through ``_calls.so``.  Every step of the computation
 runs in the library's CUDA kernels; there is no fallback.  Importing this
-package raises if ``libr9q.so`` has not been built (``build.py``).
+package raises if ``libr9q.so`` has not been built (``build.py``), and the
+attention block's calls if ``_calls.so`` has not been, for this torch.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 from typing import NamedTuple
 
@@ -23,7 +25,20 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-from . import _calls  # noqa: E402  (built beside libr9q.so, which it needs)
+
+class _Unloaded:
+    """Stands for the module _calls, and loads it when an attention call first needs it: the rest does without it."""
+
+    def __getattr__(self, name):
+        module = importlib.import_module("._calls", __name__)    # (takes this object's place)
+        if module.torch_version != torch.__version__:
+            globals()["_calls"] = self
+            raise ImportError(f"_calls.so was built for torch {module.torch_version}, this is {torch.__version__}: "
+                              "run build.py")
+        return getattr(module, name)
+
+
+_calls = _Unloaded()
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64

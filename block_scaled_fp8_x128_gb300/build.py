@@ -8,6 +8,7 @@ from __future__ import annotations
 import glob
 import importlib.util
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -49,11 +50,26 @@ def _torch_dir() -> str:
     return importlib.util.find_spec("torch").submodule_search_locations[0]
 
 
+def _torch_version() -> str:
+    text = open(os.path.join(_torch_dir(), "version.py")).read()
+    return re.search(r"^__version__ = ['\"](.+)['\"]", text, re.M).group(1)
+
+
+def _built_for() -> str:
+    """What _calls.so depends on beside its sources."""
+    return f"torch {_torch_version()} {sys.implementation.cache_tag}\n"
+
+
+def _other_than(path: str, text: str) -> bool:
+    return not os.path.exists(path) or open(path).read() != text
+
+
 def _calls_compile(src: str, obj: str) -> list[str]:
     include = os.path.join(_torch_dir(), "include")
     paths = [include, os.path.join(include, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
              os.path.join(ROOT, "include")]
-    return ["g++", "-O2", "-std=c++17", "-fPIC", *(f"-I{p}" for p in paths), "-c", src, "-o", obj]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", f'-DR9Q_TORCH_VERSION="{_torch_version()}"', *(f"-I{p}" for p in paths),
+            "-c", src, "-o", obj]
 
 
 def _calls_link(obj: str, out: str) -> list[str]:
@@ -79,7 +95,9 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
                 cmd[1:1] = ["-Xptxas", "-v"]
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     calls_src, calls_obj = os.path.join(CSRC, "r9q_calls.cpp"), os.path.join(BUILD_DIR, "r9q_calls.o")
-    if force or _stale(calls_obj, [calls_src, *headers]):
+    record = os.path.join(BUILD_DIR, "r9q_calls.for")
+    other = _other_than(record, _built_for())
+    if force or other or _stale(calls_obj, [calls_src, *headers]):
         procs.append((calls_src, subprocess.Popen(_calls_compile(calls_src, calls_obj), stdout=subprocess.PIPE,
                                                   stderr=subprocess.STDOUT)))
     failed = []
@@ -90,18 +108,22 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             failed.append((src, text))
         elif verbose_ptxas and text:
             sys.stderr.write(text)
-    if failed:
-        msg = "\n".join(f"--- {s}\n{t}" for s, t in failed)
-        raise RuntimeError("compilation failed:\n" + msg)
+    msg = "compilation failed:\n" + "\n".join(f"--- {s}\n{t}" for s, t in failed)
+    if any(s != calls_src for s, _ in failed):
+        raise RuntimeError(msg)
     if force or _stale(LIB, objs):
         tmp = LIB + ".tmp.%d" % os.getpid()
         cmd = [nvcc, "-gencode", "arch=compute_103a,code=sm_103a", "-shared", "-o", tmp, *objs]
         subprocess.run(cmd, check=True)
         os.replace(tmp, LIB)
-    if force or _stale(CALLS, [calls_obj]):
+    if failed:                                                # libr9q.so is there for what does without _calls.so
+        raise RuntimeError(msg)
+    if force or other or _stale(CALLS, [calls_obj]):
         tmp = CALLS + ".tmp.%d" % os.getpid()
         subprocess.run(_calls_link(calls_obj, tmp), check=True)
         os.replace(tmp, CALLS)
+        with open(record, "w") as f:
+            f.write(_built_for())
     return LIB
 
 

@@ -374,4 +374,8 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, g_methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls(void) { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__calls(void) {
+    PyObject* m = PyModule_Create(&g_module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", R9Q_TORCH_VERSION)) Py_CLEAR(m);      // what it was built for
+    return m;
+}
