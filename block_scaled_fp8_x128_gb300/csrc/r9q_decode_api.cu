@@ -1,6 +1,7 @@
 // C ABI of the attention operators (declared in include/r9q.h): QK norm with
 // rotation, its gradient, the paged 4-bit cache and the attention over it.
 // Argument checks and dispatch, as in r9q_api.cu.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -58,6 +59,13 @@ int check_rope(const float* wq, const float* wk, const float* cos, const float* 
         return R9Q_ERR_ALIGN;
     return R9Q_OK;
 }
+// An output over what the rotation reads.
+bool rope_meets(const float* wq, const float* wk, const float* cos, const float* sin, const int64_t* pos, int64_t T,
+                int64_t D, int64_t rot, int64_t npos, const Extent& x) {
+    if (meet(bytes_of(wq, D * 4), x) || meet(bytes_of(wk, D * 4), x)) return true;
+    const int64_t table = std::min(npos, (int64_t)1 << 40) * rot * 2;          // (rot / 2 floats a row)
+    return rot > 0 && (meet(bytes_of(cos, table), x) || meet(bytes_of(sin, table), x) || meet(bytes_of(pos, T * 8), x));
+}
 RopeParams rope_params(const float* wq, const float* wk, const float* cos, const float* sin, const int64_t* pos,
                        int64_t T, int64_t rot, int64_t npos, float eps, int flags, int* err) {
     RopeParams p = {};
@@ -99,6 +107,14 @@ bool cache_meets(const Kv4Cache& c, int64_t D, const Extent& x) {
     const int64_t vectors = c.pages * c.heads * c.page;
     return meet(bytes_of(c.k, vectors * (D / 2)), x) || meet(bytes_of(c.v, vectors * (D / 2)), x) ||
            meet(bytes_of(c.kp, vectors * 4), x) || meet(bytes_of(c.vp, vectors * 4), x);
+}
+bool cache_meets_rope(const Kv4Cache& c, int64_t D, const float* wq, const float* wk, const float* cos, const float* sin,
+                      const int64_t* pos, int64_t T, int64_t rot, int64_t npos) {
+    const int64_t vectors = c.pages * c.heads * c.page;
+    for (const Extent& x : {bytes_of(c.k, vectors * (D / 2)), bytes_of(c.v, vectors * (D / 2)), bytes_of(c.kp, vectors * 4),
+                            bytes_of(c.vp, vectors * 4)})
+        if (rope_meets(wq, wk, cos, sin, pos, T, D, rot, npos, x)) return true;
+    return false;
 }
 bool cache_overlaps_itself(const Kv4Cache& c, int64_t D) {
     const int64_t vectors = c.pages * c.heads * c.page;
@@ -167,9 +183,11 @@ int r9q_qk_norm_rope(const void* q, int64_t q_ts, int64_t q_hs, const void* k, i
     if (!spread(T, Hq, D, qo_ts, qo_hs) || !spread(T, Hk, D, ko_ts, ko_hs)) return R9Q_ERR_ARG;
     const Extent in[2] = {extent(q, T, Hq, D, q_ts, q_hs), extent(k, T, Hk, D, k_ts, k_hs)};
     const Extent out[2] = {extent(q_out, T, Hq, D, qo_ts, qo_hs), extent(k_out, T, Hk, D, ko_ts, ko_hs)};
-    for (const Extent& i : in)
-        for (const Extent& o : out)
+    for (const Extent& o : out) {
+        if (rope_meets(wq, wk, cos, sin, pos, T, D, rot, npos, o)) return R9Q_ERR_ARG;
+        for (const Extent& i : in)
             if (meet(i, o)) return R9Q_ERR_ARG;
+    }
     int *err = nullptr, sms = 0;
     rc = device_error_word_and_sms(&err, &sms);
     if (rc) return rc;
@@ -207,14 +225,15 @@ int r9q_qk_norm_rope_bwd(const void* dq_out, int64_t dqo_ts, int64_t dqo_hs, con
     if (!rc) rc = check_heads(dk, T, dk_ts, Hk, dk_hs);
     if (rc) return rc;
     if (!spread(T, Hq, D, dq_ts, dq_hs) || !spread(T, Hk, D, dk_ts, dk_hs)) return R9Q_ERR_ARG;
-    const Extent in[6] = {extent(dq_out, T, Hq, D, dqo_ts, dqo_hs), extent(dk_out, T, Hk, D, dko_ts, dko_hs),
-                          extent(q, T, Hq, D, q_ts, q_hs), extent(k, T, Hk, D, k_ts, k_hs), bytes_of(wq, D * 4),
-                          bytes_of(wk, D * 4)};
+    const Extent in[4] = {extent(dq_out, T, Hq, D, dqo_ts, dqo_hs), extent(dk_out, T, Hk, D, dko_ts, dko_hs),
+                          extent(q, T, Hq, D, q_ts, q_hs), extent(k, T, Hk, D, k_ts, k_hs)};
     const Extent out[4] = {extent(dq, T, Hq, D, dq_ts, dq_hs), extent(dk, T, Hk, D, dk_ts, dk_hs),
                            bytes_of(dwq, D * 4), bytes_of(dwk, D * 4)};
-    for (const Extent& o : out)
+    for (const Extent& o : out) {
+        if (rope_meets(wq, wk, cos, sin, pos, T, D, rot, npos, o)) return R9Q_ERR_ARG;
         for (const Extent& i : in)
             if (meet(i, o)) return R9Q_ERR_ARG;
+    }
     if (meet(out[2], out[3]) || meet(out[0], out[2]) || meet(out[0], out[3]) || meet(out[1], out[2]) ||
         meet(out[1], out[3]))
         return R9Q_ERR_ARG;
@@ -224,6 +243,7 @@ int r9q_qk_norm_rope_bwd(const void* dq_out, int64_t dqo_ts, int64_t dqo_hs, con
     if (!workspace || workspace_bytes < need) return R9Q_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return R9Q_ERR_ALIGN;
     const Extent ws = bytes_of(workspace, (int64_t)need);
+    if (rope_meets(wq, wk, cos, sin, pos, T, D, rot, npos, ws)) return R9Q_ERR_ARG;
     for (const Extent& i : in)
         if (meet(i, ws)) return R9Q_ERR_ARG;
     for (const Extent& o : out)
@@ -261,6 +281,10 @@ int r9q_qk_norm_rope_kv4(const void* q, int64_t q_ts, int64_t q_hs, const void* 
     for (const Extent& i : in)
         if (meet(i, out) || cache_meets(c, D, i)) return R9Q_ERR_ARG;
     if (cache_meets(c, D, out) || cache_overlaps_itself(c, D)) return R9Q_ERR_ARG;
+    const Extent at = bytes_of(slots, T * 8);
+    if (meet(at, out) || cache_meets(c, D, at) || rope_meets(wq, wk, cos, sin, pos, T, D, rot, npos, out) ||
+        cache_meets_rope(c, D, wq, wk, cos, sin, pos, T, rot, npos))
+        return R9Q_ERR_ARG;
     int *err = nullptr, sms = 0;
     rc = device_error_word_and_sms(&err, &sms);
     if (rc) return rc;
@@ -283,7 +307,7 @@ int r9q_kv4_append(const void* k, int64_t k_ts, int64_t k_hs, const void* v, int
     if (rc) return rc;
     const Kv4Cache c = cache_of(kc, kp, vc, vp, pages, Hk, page);
     if (cache_meets(c, D, extent(k, T, Hk, D, k_ts, k_hs)) || cache_meets(c, D, extent(v, T, Hk, D, v_ts, v_hs)) ||
-        cache_overlaps_itself(c, D))
+        cache_meets(c, D, bytes_of(slots, T * 8)) || cache_overlaps_itself(c, D))
         return R9Q_ERR_ARG;
     int *err = nullptr, sms = 0;
     rc = device_error_word_and_sms(&err, &sms);
@@ -302,7 +326,8 @@ int r9q_kv4_gather(const uint8_t* kc, const void* kp, const uint8_t* vc, const v
     if (rc) return rc;
     const Kv4Cache c = cache_of(kc, kp, vc, vp, pages, Hk, page);
     const Extent ke = bytes_of(k, 2 * T * Hk * D), ve = bytes_of(v, 2 * T * Hk * D);
-    if (meet(ke, ve) || cache_meets(c, D, ke) || cache_meets(c, D, ve)) return R9Q_ERR_ARG;
+    const Extent at = bytes_of(slots, T * 8);
+    if (meet(ke, ve) || meet(ke, at) || meet(ve, at) || cache_meets(c, D, ke) || cache_meets(c, D, ve)) return R9Q_ERR_ARG;
     int *err = nullptr, sms = 0;
     rc = device_error_word_and_sms(&err, &sms);
     if (rc) return rc;

@@ -331,3 +331,40 @@ def test_capture_ids(r9q):  # noqa: F811
 
 def test_capture_id_refusal(r9q):  # noqa: F811
     assert r9q._lib.r9q_stream_capture_id(None, None) == -1
+
+
+# ----------------------------------------------------------------- refusals --
+
+def test_outputs_over_weights_tables_positions_and_slots_are_refused(r9q):  # noqa: F811
+    """On the host, before any CUDA call (the pointers are not addresses)."""
+    lib, M, ARG = r9q._lib, 1 << 24, -8
+    at = {"wq": 11 * M, "wk": 12 * M, "cos": 13 * M, "sin": 14 * M, "pos": 15 * M, "slots": 16 * M}
+
+    def rope(**over):
+        p = {"q_out": 3 * M, "k_out": 4 * M, **over}
+        return lib.r9q_qk_norm_rope(M, 512, 128, 2 * M, 512, 128, at["wq"], at["wk"], at["cos"], at["sin"], at["pos"],
+                                    p["q_out"], 512, 128, p["k_out"], 512, 128, 4, 4, 2, 128, 128, 9, 1e-6, 0, None)
+
+    def grad(**over):
+        p = {"dq": 5 * M, "dk": 6 * M, "dwq": 7 * M, "dwk": 8 * M, "ws": 20 * M, **over}
+        return lib.r9q_qk_norm_rope_bwd(M, 512, 128, 2 * M, 512, 128, 3 * M, 512, 128, 4 * M, 512, 128, at["wq"], at["wk"],
+                                        at["cos"], at["sin"], at["pos"], p["dq"], 512, 128, p["dk"], 512, 128, p["dwq"],
+                                        p["dwk"], 4, 4, 2, 128, 128, 9, 1e-6, 0, p["ws"], 1 << 22, None)
+
+    def write(**over):
+        p = {"q_out": 4 * M, "kc": 5 * M, "kp": 6 * M, "vc": 7 * M, "vp": 8 * M, **over}
+        return lib.r9q_qk_norm_rope_kv4(M, 512, 128, 2 * M, 256, 128, 3 * M, 256, 128, at["wq"], at["wk"], at["cos"],
+                                        at["sin"], at["pos"], p["q_out"], 512, 128, p["kc"], p["kp"], p["vc"], p["vp"],
+                                        at["slots"], 4, 4, 2, 128, 128, 9, 4, 16, 1e-6, 0, None)
+    for name in ("wq", "wk", "cos", "sin", "pos"):
+        assert all(rope(**{o: at[name]}) == ARG for o in ("q_out", "k_out")), name
+        assert all(write(**{o: at[name]}) == ARG for o in ("q_out", "kc", "kp", "vc", "vp")), name
+        assert all(grad(**{o: at[name]}) == ARG for o in ("dq", "dk", "dwq", "dwk")), name
+    assert all(write(**{o: at["slots"]}) == ARG for o in ("q_out", "kc", "kp", "vc", "vp"))
+    append = (M, 256, 128, 2 * M, 256, 128)
+    for i in range(4):
+        c = [5 * M, 6 * M, 7 * M, 8 * M]
+        c[i] = at["slots"]
+        assert lib.r9q_kv4_append(*append, *c, at["slots"], 4, 2, 128, 4, 16, None) == ARG
+    for k, v in ((at["slots"], 2 * M), (M, at["slots"])):
+        assert lib.r9q_kv4_gather(5 * M, 6 * M, 7 * M, 8 * M, at["slots"], 4, 2, 128, 4, 16, k, v, None) == ARG
