@@ -137,6 +137,80 @@ def test_autograd_trains_and_refuses_a_second_derivative(r9q):  # noqa: F811
         assert not r9q.r9q_qk_norm_rope(x, x, w, w, q_out=buf)[0].requires_grad
 
 
+# --------------------------------------------------- the keys' codes, exactly --
+
+def key_in_order(x, w, c, s, eps, inter):
+    """x fp32 [T][H][D], c and s fp32 [T][rot/2] or None: norm and rotation in fp32 with the roundings that include/r9q.h
+    fixes.  Only the root is the GPU's (torch.rsqrt, which is rsqrtf)."""
+    f32 = np.float32
+    q = x * x
+    sums = q[..., :32]
+    for i in range(32, q.shape[-1], 32):
+        sums = sums + q[..., i:i + 32]
+    while sums.shape[-1] > 1:
+        sums = sums[..., 0::2] + sums[..., 1::2]
+    t = sums * f32(1 / x.shape[-1]) + f32(eps)
+    r = torch.rsqrt(on(t)).cpu().numpy()
+    y = (x * r) * w
+    assert y.dtype == np.float32
+    if c is None:
+        return y
+    c, s, half = c[:, None], s[:, None], c.shape[-1]
+    a, b = (slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if inter else (slice(0, half), slice(half, 2 * half))
+    z = y.copy()
+    z[..., a] = y[..., a] * c - y[..., b] * s
+    z[..., b] = y[..., b] * c + y[..., a] * s
+    assert z.dtype == np.float32
+    return z
+
+
+def check_codes(r9q, k, w, cos, sin, pos, inter):  # noqa: F811
+    """Codes and pairs of keys k, written few or many at a time, against key_in_order."""
+    T, Hk, D = k.shape
+    cache, slots = r9q.r9q_kv4_cache(-(-T // 16), Hk, 16, D), torch.arange(T, device=dev())
+    r9q.r9q_qk_norm_rope_kv4(k, k, k, *rope_args(w, w, cos, sin, pos), cache, slots, eps=1e-6, interleaved=inter)
+    c, s = (None, None) if cos is None else (cos[pos], sin[pos])
+    codes, step, low = ref.quantise32(key_in_order(k.float().cpu().numpy(), w, c, s, 1e-6, inter))
+    at = np.arange(T)
+    kb = cache.k.cpu().numpy()[at // 16, :, at % 16]
+    assert np.array_equal(kb & 15, codes[..., 0::2]) and np.array_equal(kb >> 4, codes[..., 1::2])
+    pair = cache.kp.float().cpu().numpy()[at // 16, :, at % 16]
+    assert np.array_equal(pair, np.concatenate([step, low], -1))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hk,D,rot,inter", [(3, 128, 128, False), (2, 128, 128, True), (2, 128, 64, False),
+                                           (1, 128, 0, False), (3, 64, 64, False), (5, 64, 64, True), (1, 64, 32, False),
+                                           (2, 64, 48, True)])
+@pytest.mark.parametrize("T", [40, 1025])
+def test_codes_of_keys_are_those_of_the_stated_roundings(r9q, Hk, D, rot, inter, T):  # noqa: F811
+    """Every code and pair, ties included, from few tokens and from a prompt: on the stated order of the sum of squares,
+    single roundings and no fused product."""
+    (_, k), _, (_, w), cos, sin, pos = grad_case(T, 1, Hk, D, rot, 1.5, 321)
+    k[3] = 0
+    check_codes(r9q, k, w, cos, sin, pos, inter)
+
+
+def near_one(T, H, D, rot, seed):
+    """Keys of elements of many sizes, which their weights and angles make nearly equal, so that a step of the codes is
+    some thousand units of fp32 and not a million: another order of the sum or a fused product moves several of the codes."""
+    g = np.random.default_rng(seed)
+    size = np.exp2(g.uniform(-6, 6, D)).astype(np.float32)
+    k = torch.from_numpy((size * (1 + g.integers(0, 3, (T, H, D)) / 128)).astype(np.float32)).to(torch.bfloat16).to(dev())
+    w = ((1 + g.normal(0, 2.0 ** -8, D)) / size).astype(np.float32)
+    cos = (1 - np.abs(g.normal(0, 2.0 ** -9, (500, rot // 2)))).astype(np.float32)
+    sin = g.normal(0, 2.0 ** -8, (500, rot // 2)).astype(np.float32)
+    return k, w, cos, sin, g.integers(0, 500, T)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hk,D,rot,inter", [(8, 128, 128, False), (8, 64, 64, False), (8, 128, 128, True), (8, 64, 32, False),
+                                           (8, 128, 64, True)])
+@pytest.mark.parametrize("T", [900, 1500])
+def test_codes_of_keys_near_one_are_those_of_the_stated_roundings(r9q, Hk, D, rot, inter, T):  # noqa: F811
+    check_codes(r9q, *near_one(T, Hk, D, rot, 331), inter)
+
+
 # ----------------------------------------------------- streams and devices --
 
 def attention_inputs(r9q, Hq=4, Hk=2, D=128, n=40, seed=241):  # noqa: F811
