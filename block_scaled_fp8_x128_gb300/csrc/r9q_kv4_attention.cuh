@@ -69,6 +69,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+// Takes 7.5 times the fp16 values in the halves of w from a and b, one rounding each.
+__device__ __forceinline__ void less_mid(float& a, float& b, uint32_t w) {
+    asm("{\n\t.reg .b16 l, h, k;\n\tmov.b32 {l, h}, %2;\n\tmov.b16 k, 0xC780;\n\tfma.rn.f32.f16 %0, l, k, %0;\n\t"
+        "fma.rn.f32.f16 %1, h, k, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(w));                               // (0xC780: -7.5)
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));

@@ -211,6 +211,32 @@ def test_codes_of_keys_near_one_are_those_of_the_stated_roundings(r9q, Hk, D, ro
     check_codes(r9q, *near_one(T, Hk, D, rot, 331), inter)
 
 
+# ------------------------------------------------------------- long sequences --
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,D,batch", [(1, 128, 2000), (2, 64, 2000), (12, 128, 1000), (16, 64, 1000)])
+def test_sums_over_long_sequences_do_not_drift(r9q, Hq, D, batch):  # noqa: F811
+    """Queries of zero: every weight is the same power of two, exact in any format, and the result the mean of 100,000
+    values, a three-hundredth of one.  So many sequences that a warp has half of one (3125 groups of 16 keys).  Partial
+    sums of both signs are of the order of sqrt(n) terms, and err by 2^-23 of that each, in all 2^-23 sqrt(3125) = 2^-17 of
+    a term: of the values' range.  (Sums of one sign, cut off, would drift by n / 2 units: 2^-14.)"""
+    n, page = 100_000, 256
+    per = -(-n // page)
+    cache = r9q.r9q_kv4_cache(per, 1, page, D)
+    v = rand((n, 1, D), 341).to(dev())
+    slots = torch.arange(n, device=dev())
+    r9q.r9q_kv4_append(v, v, cache, slots)
+    q = torch.zeros((batch, 1, Hq, D), dtype=torch.bfloat16, device=dev())
+    table = torch.arange(per, dtype=torch.int32, device=dev()).expand(batch, per).contiguous()    # (all the same pages)
+    o, lse = r9q.r9q_kv4_attention(q, cache, table, torch.full((batch,), n, dtype=torch.int32, device=dev()), return_lse=True)
+    codes, pair = cache.v.cpu().numpy(), cache.vp.double().cpu().numpy()
+    _, vc = ref.cache_codes(cache.k.cpu().numpy(), codes, page, D)
+    e = (pair[:, 0, :, 1:] + pair[:, 0, :, :1] * vc[:, 0]).reshape(-1, D)[:n].mean(0)
+    spread = 15 * pair[:, 0, :, 0].reshape(-1)[:n].mean()
+    assert (np.abs(np64(o) - e) <= U * np.abs(e) * 1.01 + 2.0 ** -17 * spread).all()
+    assert (np.abs(np64(lse) - np.log(n)) <= 2.0 ** -17).all()
+
+
 # ----------------------------------------------------- streams and devices --
 
 def attention_inputs(r9q, Hq=4, Hk=2, D=128, n=40, seed=241):  # noqa: F811
