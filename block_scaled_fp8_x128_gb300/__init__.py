@@ -443,14 +443,11 @@ def _with_workspace(where, op, size, call, args, workspace, device, stream):
     if stream is not None or index is None or index != _current_device():
         return _elsewhere(device, stream, _with_workspace, where, op, size, call, args, workspace, device)
     handle = _raw_stream(index)
-    own = workspace
-    if own is None:
-        own = (_stream_workspace(r9q_workspace_bytes(op, *size(), 0), device) if _capturing() else
-               _WORKSPACES.get((index, handle)))
-    r = call(*args, own, handle)
-    if workspace is None and r.__class__ is int and r == R9Q_ERR_WORKSPACE:
+    theirs = workspace is not None
+    r = call(*args, workspace if theirs else _WORKSPACES.get((index, handle)), theirs, handle)
+    if not theirs and r.__class__ is int and r in (_calls.CAPTURED, R9Q_ERR_WORKSPACE):
         own = _stream_workspace(r9q_workspace_bytes(op, *size(), 0), device)
-        r = call(*args, own, handle)
+        r = call(*args, own, True, handle)
     return _checked(r, where)
 
 
@@ -489,11 +486,10 @@ def r9q_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, wq: torch.Tensor, wk: tor
     if stream is not None or index is None or index != _current_device():
         return _elsewhere(q.device, stream, r9q_qk_norm_rope, q, k, wq, wk, cos, sin, positions, eps, interleaved, q_out,
                           k_out)
-    if ((q.requires_grad or k.requires_grad or wq.requires_grad or wk.requires_grad) and torch.is_grad_enabled() and
-            q_out is None and k_out is None):
+    r = _calls.qk_norm_rope(q, k, wq, wk, cos, sin, positions, eps, interleaved, q_out, k_out, _raw_stream(index))
+    if r.__class__ is int and r == _calls.RECORDED:
         return _NormRope.apply(q, k, wq, wk, cos, sin, positions, eps, interleaved)
-    return _checked(_calls.qk_norm_rope(q, k, wq, wk, cos, sin, positions, eps, interleaved, q_out, k_out,
-                                        _raw_stream(index)), "r9q_qk_norm_rope")
+    return _checked(r, "r9q_qk_norm_rope")
 
 
 def r9q_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,

@@ -5,13 +5,15 @@
 // Python take, so the checks are made here, on the tensors themselves.  Nothing else
 // is: each function takes its arguments by position, makes the outputs that are None
 // and calls the entry point of include/r9q.h of the same name.  It returns the outputs,
-// or the entry point's code as an int where that is not 0; a tensor of the wrong type,
+// or the entry point's code as an int where that is not 0, or one of the codes below where
+// the call has to be made another way (nothing has been done then); a tensor of the wrong type,
 // shape, layout or device raises as the rest of the binding does.  The caller has made the
 // tensors' device and the call's stream the current ones.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <c10/util/Exception.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -24,6 +26,11 @@
 namespace {
 
 struct Raised {};            // a Python error is set
+
+// The call is to be recorded by autograd.
+constexpr int kRecorded = 1;
+// The stream is being captured, and the workspace is not the caller's own: the capture needs one of its own.
+constexpr int kCaptured = 2;
 
 [[noreturn]] void raise(PyObject* type, const char* format, ...) {
     va_list args;
@@ -219,7 +226,13 @@ Workspace workspace(PyObject* o, at::Device device) {
     return w;
 }
 
+bool captured(PyObject* theirs, PyObject* on) {          // not the caller's workspace, on a stream that is captured
+    unsigned long long id = 0;
+    return !truth(theirs) && r9q_stream_capture_id(stream(on), &id) == R9Q_OK && id != 0;
+}
+
 // ---- the calls ----
+// workspace, theirs: the workspace, and whether it is the caller's own.
 
 // q, k, wq, wk, cos, sin, positions, eps, interleaved, q_out, k_out, stream
 PyObject* qk_norm_rope(PyObject* const* a) {
@@ -229,6 +242,9 @@ PyObject* qk_norm_rope(PyObject* const* a) {
     const int64_t T = s[0], Hq = s[1], D = s[2], Hk = ks[1];
     const Heads qh = heads(a[0], "q", {T, Hq, D}, dev), kh = heads(a[1], "k", {T, Hk, D}, dev);
     const Rope r = rope(a + 2, T, D, dev);
+    if (a[9] == Py_None && a[10] == Py_None && c10::GradMode::is_enabled() &&
+        (q.requires_grad() || k.requires_grad() || tensor(a[2], "wq").requires_grad() || tensor(a[3], "wk").requires_grad()))
+        return PyLong_FromLong(kRecorded);
     Outputs out;
     out.add(a[9], s, at::kBFloat16, a[10], ks, at::kBFloat16, dev);
     const Heads qo = heads(out.o[0], "q_out", {T, Hq, D}, dev), ko = heads(out.o[1], "k_out", {T, Hk, D}, dev);
@@ -237,8 +253,9 @@ PyObject* qk_norm_rope(PyObject* const* a) {
                                      truth(a[8]) ? R9Q_ROPE_INTERLEAVED : 0, stream(a[11])));
 }
 
-// dq_out, dk_out, q, k, wq, wk, cos, sin, positions, eps, interleaved, dq, dk, dwq, dwk, workspace, stream
+// dq_out, dk_out, q, k, wq, wk, cos, sin, positions, eps, interleaved, dq, dk, dwq, dwk, workspace, theirs, stream
 PyObject* qk_norm_rope_bwd(PyObject* const* a) {
+    if (captured(a[16], a[17])) return PyLong_FromLong(kCaptured);
     const at::Tensor &q = tensor(a[2], "q"), &k = tensor(a[3], "k");
     const at::Device dev = q.device();
     const at::IntArrayRef s = sizes(q, "q", 3), ks = sizes(k, "k", 3);
@@ -256,7 +273,7 @@ PyObject* qk_norm_rope_bwd(PyObject* const* a) {
     return out.done(r9q_qk_norm_rope_bwd(gq.p, gq.ts, gq.hs, gk.p, gk.ts, gk.hs, qh.p, qh.ts, qh.hs, kh.p, kh.ts, kh.hs,
                                          r.wq, r.wk, r.cos, r.sin, r.pos, dq.p, dq.ts, dq.hs, dk.p, dk.ts, dk.hs, dwq,
                                          dwk, T, Hq, Hk, D, r.rot, r.npos, number(a[9]),
-                                         truth(a[10]) ? R9Q_ROPE_INTERLEAVED : 0, w.p, w.bytes, stream(a[16])));
+                                         truth(a[10]) ? R9Q_ROPE_INTERLEAVED : 0, w.p, w.bytes, stream(a[17])));
 }
 
 // q, k, v, wq, wk, cos, sin, positions, cache.k, .kp, .v, .vp, slots, eps, interleaved, q_out, stream
@@ -308,8 +325,9 @@ PyObject* kv4_gather(PyObject* const* a) {
     return out.done(r9q_kv4_gather(c.k, c.kp, c.v, c.vp, slots, T, c.heads, c.dim, c.pages, c.page, k, v, stream(a[7])));
 }
 
-// q, cache.k, .kp, .v, .vp, block_table, seq_lens, scale, window, out, lse, return_lse, workspace, stream
+// q, cache.k, .kp, .v, .vp, block_table, seq_lens, scale, window, out, lse, return_lse, workspace, theirs, stream
 PyObject* kv4_attention(PyObject* const* a) {
+    if (captured(a[13], a[14])) return PyLong_FromLong(kCaptured);
     const at::Tensor& q = tensor(a[0], "q");
     const at::Device dev = q.device();
     const at::IntArrayRef s = sizes(q, "q", 4);
@@ -334,7 +352,7 @@ PyObject* kv4_attention(PyObject* const* a) {
     float* lse = static_cast<float*>(address(with_lse ? out.o[1] : a[10], "lse", at::kFloat, {B, Lq, Hq}, dev));
     return out.done(r9q_kv4_attention(q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), c.k, c.kp, c.v, c.vp, table,
                                       lens, o, lse, B, Lq, Hq, c.heads, D, c.pages, c.page, width, integer(a[8]), scale,
-                                      w.p, w.bytes, stream(a[13])));
+                                      w.p, w.bytes, stream(a[14])));
 }
 
 template <PyObject* (*CALL)(PyObject* const*), int N>
@@ -364,11 +382,11 @@ PyMethodDef method(const char* name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<CALL, N>)), METH_FASTCALL, nullptr};
 }
 PyMethodDef g_methods[] = {method<qk_norm_rope, 12>("qk_norm_rope"),
-                           method<qk_norm_rope_bwd, 17>("qk_norm_rope_bwd"),
+                           method<qk_norm_rope_bwd, 18>("qk_norm_rope_bwd"),
                            method<qk_norm_rope_kv4, 17>("qk_norm_rope_kv4"),
                            method<kv4_append, 8>("kv4_append"),
                            method<kv4_gather, 8>("kv4_gather"),
-                           method<kv4_attention, 14>("kv4_attention"),
+                           method<kv4_attention, 15>("kv4_attention"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
@@ -376,6 +394,8 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, g_methods,
 
 PyMODINIT_FUNC PyInit__calls(void) {
     PyObject* m = PyModule_Create(&g_module);
-    if (m && PyModule_AddStringConstant(m, "torch_version", R9Q_TORCH_VERSION)) Py_CLEAR(m);      // what it was built for
+    if (m && (PyModule_AddStringConstant(m, "torch_version", R9Q_TORCH_VERSION) ||                  // what it was built for
+              PyModule_AddIntConstant(m, "RECORDED", kRecorded) || PyModule_AddIntConstant(m, "CAPTURED", kCaptured)))
+        Py_CLEAR(m);
     return m;
 }
