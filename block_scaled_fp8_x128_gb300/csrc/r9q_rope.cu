@@ -34,11 +34,13 @@ constexpr int kUnroll = 4;                   // 8192 tokens of 32 + 8 heads of 1
 // 13.2/10.4, 4096 26.6/22.3, 8192 48.6/43.4.
 constexpr int kMaxRounds = 4;
 constexpr int64_t kEnoughWarps = 152 * 24;
-// Tokens from which a warp writes (reads back) a head of 16 tokens at a time where they fill a group of the cache,
-// instead of a token's heads.  Writes and read-backs of 8 heads of 128 together, us, by tokens / by groups: writing,
-// 512 tokens 9.2/10.5, 1024 13.0/12.9, 2048 17.7/16.3, 4096 33.2/27.0; reading, 4096 27.0/28.9, 8192 48.3/47.2, 16384
-// 89.4/83.6.
+// Tokens from which a warp takes a head of 16 tokens at a time, which it can where they fill a group of the cache,
+// instead of a token's heads.  8 heads of 128 (writes: and 32 query heads), us, by tokens / by groups / by groups where the
+// call's windows of 16 tokens lie across two groups each, which then go token by token: writing 1024 tokens 8.7/8.2/11.4,
+// 2048 13.8/12.4/14.7, 4096 27.0/20.6/22.7, 8192 49.5/37.3/40.4; appending 1024 4.7/7.1/12.4, 2048 6.4/7.1/10.2, 4096
+// 9.9/8.6/12.3, 8192 18.6/15.3/19.5; reading 4096 5.4/5.9/9.6, 8192 9.6/8.0/13.6.
 constexpr int kGroupTokens = 1024;
+constexpr int kAppendGroupTokens = 4096;
 constexpr int kGatherGroupTokens = 8192;
 
 template <int D>
@@ -546,7 +548,7 @@ cudaError_t launch_forward(ForwardArgs a, cudaStream_t st) {
     auto warps = [&](int heads) { return (heads + a.rounds * HR - 1) / (a.rounds * HR); };
     auto blocks_of = [](int64_t n) { return (n + kThreads / 32 - 1) / (kThreads / 32); };
     // (kMaxRounds, kEnoughWarps)
-    const bool groups = PASS != kRope && a.T >= kGroupTokens;
+    const bool groups = PASS != kRope && a.T >= (PASS == kAppend ? kAppendGroupTokens : kGroupTokens);
     for (a.rounds = kMaxRounds;; a.rounds /= 2) {
         a.nq = PASS == kAppend ? 0 : warps(a.q.heads);
         a.nk = groups ? 0 : warps(a.k.heads);
