@@ -122,6 +122,15 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor of the stream that the call runs on: what the current one still does with a block that it has let go,
+    or does next with one that this call lets go, does not meet the kernel."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _expect(t, dtype, shape, name):
     if t is None:
         return
@@ -155,7 +164,7 @@ def r9q_grouped_gemm_fp8(a: torch.Tensor, offsets, w: torch.Tensor, ws: torch.Te
     _expect(ws, torch.float32, (E, N // 128, K // 128), "ws")
     ncols = N // 2 if flags & R9Q_GROUPED_SWIGLU else N
     if y is None:
-        y = torch.empty((Mtot, ncols), dtype=torch.bfloat16, device=a.device)
+        y = _empty((Mtot, ncols), torch.bfloat16, a.device, stream)
     _expect(y, torch.bfloat16, (Mtot, ncols), "y")
     arr = (_I64 * (E + 1))(*off)
     _check(_lib.r9q_grouped_gemm_fp8(_ptr(a), arr, E, _ptr(w), _ptr(ws), _ptr(y), N, K, int(flags), _stream(stream)),
@@ -227,7 +236,7 @@ def _stream_workspace(need: int, device: torch.device, stream=None) -> torch.Ten
 def r9q_e4m3_from_f32(x: torch.Tensor, q: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     _expect(x, torch.float32, x.shape, "x")
     if q is None:
-        q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        q = _empty(x.shape, torch.uint8, x.device, stream)
     _expect(q, torch.uint8, x.shape, "q")
     _check(_lib.r9q_e4m3_from_f32(_ptr(x), x.numel(), _ptr(q), _stream(stream)), "r9q_e4m3_from_f32")
     return q
@@ -238,9 +247,9 @@ def r9q_quant_group128(x: torch.Tensor, xq: torch.Tensor | None = None, xs: torc
     M, K = x.shape
     _expect(x, torch.bfloat16, (M, K), "x")
     if xq is None:
-        xq = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        xq = _empty((M, K), torch.uint8, x.device, stream)
     if xs is None:
-        xs = torch.empty((M, K // 128), dtype=torch.float32, device=x.device)
+        xs = _empty((M, K // 128), torch.float32, x.device, stream)
     _expect(xq, torch.uint8, (M, K), "xq")
     _expect(xs, torch.float32, (M, K // 128), "xs")
     _check(_lib.r9q_quant_group128(_ptr(x), M, K, _ptr(xq), _ptr(xs), _stream(stream)), "r9q_quant_group128")
@@ -253,7 +262,7 @@ def r9q_swiglu_interleaved(gu: torch.Tensor, h: torch.Tensor | None = None, stre
     I = I2 // 2
     _expect(gu, torch.bfloat16, (M, 2 * I), "gu")
     if h is None:
-        h = torch.empty((M, I), dtype=torch.bfloat16, device=gu.device)
+        h = _empty((M, I), torch.bfloat16, gu.device, stream)
     _expect(h, torch.bfloat16, (M, I), "h")
     _check(_lib.r9q_swiglu_interleaved(_ptr(gu), M, I, _ptr(h), _stream(stream)), "r9q_swiglu_interleaved")
     return h
@@ -264,9 +273,9 @@ def r9q_quant_weight_block128(w: torch.Tensor, wq: torch.Tensor | None = None, w
     N, K = w.shape
     _expect(w, torch.float32, (N, K), "w")
     if wq is None:
-        wq = torch.empty((N, K), dtype=torch.uint8, device=w.device)
+        wq = _empty((N, K), torch.uint8, w.device, stream)
     if ws is None:
-        ws = torch.empty((N // 128, K // 128), dtype=torch.float32, device=w.device)
+        ws = _empty((N // 128, K // 128), torch.float32, w.device, stream)
     _expect(wq, torch.uint8, (N, K), "wq")
     _expect(ws, torch.float32, (N // 128, K // 128), "ws")
     _check(_lib.r9q_quant_weight_block128(_ptr(w), N, K, _ptr(wq), _ptr(ws), _stream(stream)),
@@ -304,7 +313,7 @@ def r9q_gemm_fp8_block_qa(a: torch.Tensor | None, w: torch.Tensor, ws: torch.Ten
     _expect(w, torch.uint8, (N, K), "w")
     _expect(ws, torch.float32, (N // 128, K // 128), "ws")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=w.device)
+        y = _empty((M, N), torch.bfloat16, w.device, stream)
     _expect(y, torch.bfloat16, (M, N), "y")
     if workspace is None:
         need = r9q_workspace_bytes(R9Q_OP_GEMM_W8A8, M, N, K)
@@ -324,7 +333,7 @@ def r9q_gemm_fp8w_bf16a(a: torch.Tensor, w: torch.Tensor, ws: torch.Tensor, y: t
     _expect(w, torch.uint8, (N, K), "w")
     _expect(ws, torch.float32, (N // 128, K // 128), "ws")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=w.device)
+        y = _empty((M, N), torch.bfloat16, w.device, stream)
     _expect(y, torch.bfloat16, (M, N), "y")
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib.r9q_gemm_fp8w_bf16a(_ptr(a), _ptr(w), _ptr(ws), _ptr(y), M, N, K, _ptr(workspace), wsb,
@@ -348,12 +357,12 @@ def r9q_gate_up_swiglu_down(x: torch.Tensor, w_gu: torch.Tensor, s_gu: torch.Ten
     _expect(hq, torch.uint8, (M, I), "hq")
     _expect(hs, torch.float32, (M, I // 128), "hs")
     if y is None:
-        y = torch.empty((M, H_out), dtype=torch.bfloat16, device=x.device)
+        y = _empty((M, H_out), torch.bfloat16, x.device, stream)
     _expect(y, torch.bfloat16, (M, H_out), "y")
     if workspace is None:
         need = r9q_workspace_bytes(R9Q_OP_GATE_UP_SWIGLU_DOWN, M, I, H, H_out, flags)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            workspace = _empty(need, torch.uint8, x.device, stream)
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib.r9q_gate_up_swiglu_down(_ptr(x), _ptr(w_gu), _ptr(s_gu), _ptr(w_dn), _ptr(s_dn), _ptr(y),
                                         M, H, I, H_out, _ptr(h), _ptr(hq), _ptr(hs), int(flags),
@@ -378,7 +387,7 @@ def r9q_gate_up_swiglu_down_noalloc(x: torch.Tensor, w_gu: torch.Tensor, s_gu: t
     _expect(hq, torch.uint8, (M, I), "hq")
     _expect(hs, torch.float32, (M, I // 128), "hs")
     if y is None:
-        y = torch.empty((M, H_out), dtype=torch.bfloat16, device=x.device)
+        y = _empty((M, H_out), torch.bfloat16, x.device, stream)
     _expect(y, torch.bfloat16, (M, H_out), "y")
     _check(_lib.r9q_gate_up_swiglu_down_noalloc(_ptr(x), _ptr(w_gu), _ptr(s_gu), _ptr(w_dn), _ptr(s_dn), _ptr(y),
                                                 M, H, I, H_out, _ptr(hq), _ptr(hs), int(flags), _stream(stream)),
