@@ -40,11 +40,14 @@
 //
 // What bounds it.  Up to 8 rows: HBM (136 bytes a token and head at D = 128) and the
 // taking apart of the codes, 64 masks for 16 tokens of a head, alike: 64 sequences of up
-// to 16384 tokens, 64/8 heads, take 107 us, 5.5 TB/s (the bytes alone 87, the kernel without
-// its arithmetic 95, without its copies 106).  More rows: instructions (16 sequences of 8191
-// tokens with 4 new ones 81 us, 212 TFLOP/s; the products alone 29).  Small batches:
-// latency, about 5.6 us from launch to the result for one short sequence, and with
-// parts to join about 9.  A step's score products formed before the last step's weights, and
+// to 16384 tokens, 64/8 heads, take 108 us, 5.4 TB/s (the bytes alone 87).  More rows:
+// latency at low occupancy, eight warps an SM of 255 registers, 44 % of the issue slots (16
+// sequences of 8191 tokens with 4 new ones 82 us, 208 TFLOP/s; the products alone 29), and
+// every chunk takes the codes apart again.  Small batches:
+// latency, about 5.7 us from launch to the result for one short sequence, and with
+// parts to join about 9.  A prompt's chunks each walk the whole sequence: the keys past a
+// chunk's last row, or before its window, are masked and not left out.
+// A step's score products formed before the last step's weights, and
 // the queries in shared memory for a third more warps, were slower (113 and 97 us,
 // against 108 and 81).  So was tcgen05 with the codes as an operand in tensor memory, for 32
 // rows: 103 us against 81, since converting them and two barriers a tile of 128 keys cost
@@ -540,7 +543,9 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDTH), ctas_per_sm(D, N
 // time of one (1.74 at D = 64), and have fewer warps an SM, so that an item's beginning and end weigh more: 32 (40)
 // groups of a CTA against 24.  Both add up, with the groups that the pages can hold, to a time for either; us, one tile /
 // two, 64/8 heads of 128: 16 rows, 16 sequences of 4000 tokens 37.3/32.3, 2 of them 13.1/16.9, 64 of 300 23.6/19.2; 24
-// rows 48.1/48.9 and, of 300, 25.5/29.4; 32 rows of 8191 100.0/81.1; 40 rows of 4000 71.9/66.5, of 300 35.6/41.1.
+// rows 48.1/48.9 and, of 300, 25.5/29.4; 32 rows of 8191 100.0/81.1; 40 rows of 4000 71.9/66.5, of 300 35.6/41.1.  (What
+// the pages can hold stands for the lengths, which only the device knows: all these have tables as wide as the longest
+// sequence.  16 sequences of 300 with 16 rows in a table of 131072 tokens take two tiles, 14.7 us against 12.0.)
 int row_tiles(int D, const Kv4AttnParams& p, int sms) {
     const int64_t rows = (int64_t)p.Lq * p.G, seqs = (int64_t)p.B * p.c.heads;
     if (rows <= 8) return 1;
@@ -572,7 +577,9 @@ cudaError_t launch(Kv4AttnParams p, int sms, cudaStream_t st) {
     // each: CTAs of four warps (64 sequences of up to 16384 tokens 110 us against 132).  More items than such CTAs:
     // of two warps, which begin and end twice as many items at a time (us, four warps / two; sequences x tokens, 32 or
     // 64/8 heads: 100 x 30 13.5/9.2, 256 x 300 31.9/26.8, 256 x 1000 51.3/45.7, 64 x 4 new of 4000 122/92, 64 x 16384
-    // 107.7/106.9; with fewer items: 32 x 1000 13.7/14.6, 2 x 4000 12.3/22.6, 16 x 4 new of 8191 80.9/86.4).
+    // 107.7/106.9; with fewer items: 32 x 1000 13.7/14.6, 2 x 4000 12.3/22.6, 16 x 4 new of 8191 80.9/86.4).  Again by what
+    // the pages can hold: two sequences of 300 in a table of 131072 tokens have one CTA an SM, 6.5 us (four warps, as in a
+    // table of their length, 8.9), one of 77 5.8 (5.4); 8 or 64 of 1000 take the same in either table.
     const int64_t items = (int64_t)p.B * p.c.heads * p.chunks.d, ctas = used_sms(sms);
     if (8 * items <= ctas && items * (p.room / 16) >= ctas * 4 * cta_warps(D, NT, kWide))
         return launch<D, NT, kWide>(p, sms, st);

@@ -9,8 +9,8 @@
 // and w c, w' s' depend on the token and the element only: a warp forms them
 // once and uses them for all its heads of the token.
 //
-// HBM bound: each input and output once (8192 tokens of 32 + 8 heads of 128: 43.3 us,
-// 6.3 TB/s; eight tokens: 2.2 us, the launch).  A head vector takes D/8 lanes, 16 bytes
+// HBM bound: each input and output once (8192 tokens of 32 + 32 heads of 128: 43.4 us,
+// 6.3 TB/s, 92 % of the copy rate; of 32 + 8: 32.8 us, 5.2 TB/s; eight tokens: 2.2 us, the launch).  A head vector takes D/8 lanes, 16 bytes
 // each.  Where the whole vector turns in pairs (i, i + D/2), the common case, a lane
 // takes four elements of either half (two 8-byte accesses), so that it holds both of
 // each pair; otherwise it takes eight in a row and x' comes from the lane that holds
@@ -28,10 +28,11 @@ namespace r9q {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;                   // 8192 tokens of 32 + 8 heads of 128: 43.4 us, with two 53.1
+constexpr int kUnroll = 4;                   // 8192 tokens of 32 + 32 heads of 128: 43.4 us, with two 48.5 (32 + 8: 32.8/34.7)
 // A warp takes up to so many rounds of heads of its token, which share its set-up, as long as that leaves
-// kEnoughWarps (of the 32 + 8 heads; us, one round / this rule): 512 tokens 4.5/4.5 (four rounds: 6.6), 1024 7.5/6.5, 2048
-// 13.2/10.4, 4096 26.6/22.3, 8192 48.6/43.4.
+// kEnoughWarps.  Us, one round / always four / this rule, 32 + 32 heads of 128: 512 tokens 3.5/6.6/3.5, 1024 5.4/8.1/5.4,
+// 2048 13.1/10.3/10.3, 4096 26.0/22.3/22.3, 8192 48.5/43.4/43.4; 32 + 8: 1024 4.5/6.0/4.5, 2048 7.5/7.2/7.2, 4096
+// 16.6/15.9/15.9, 8192 32.3/32.8/32.8.
 constexpr int kMaxRounds = 4;
 constexpr int64_t kEnoughWarps = 152 * 24;
 // Tokens from which a warp takes a head of 16 tokens at a time, which it can where they fill a group of the cache,
@@ -272,8 +273,9 @@ __device__ __forceinline__ float sum_squares_in_order(const float (&x)[8], int l
 // A key on its way to 4 bits.  A code flips where its value lies within an fp32
 // rounding of the middle between two codes, so the keys' value is fixed to the
 // last bit: (x r) w, the two products of the rotation and their sum each round
-// once, and the sum of squares has a fixed order.  An evaluation of the formula
-// step by step in fp32 gives the same codes.
+// once, and the sum of squares has sum_squares_in_order's order.  An evaluation in
+// fp32 in that order gives the same codes; another order would do as well, but moves
+// about one code in a million.
 template <int NL, bool SPLIT>
 __device__ __forceinline__ Eight norm_rope_in_order(const Eight& x, const Eight& weight, const Turn& u, int lane,
                                                     const RopeParams& p) {
@@ -471,11 +473,13 @@ __device__ __forceinline__ Place group_of(const Kv4Cache& c, const int64_t* slot
     return r;
 }
 
-// Many tokens into the cache.  Value warps take one head of 16 tokens at a time: where these are a group of the
-// cache, as all but the ends of a prompt's chunk are, they put whole words together and store those, not a byte at a
-// time (8192 tokens of 8 heads: 4.2 M partial sectors written become 0.3 M).  Key warps as above.  The query heads,
-// which HBM bounds, and the quantising, which instructions bound, are blocks of one grid in turn, so that an SM has both.
-// 8192 tokens of 32 + 8 + 8 heads of 128: 38.6 us, 63 % of the issue slots; its bytes alone would take 26.
+// Many tokens into the cache.  Value warps take one head of 16 tokens of the call at a time: where these are a group of
+// the cache they put whole words together and store those, not a byte at a time (8192 tokens of 8 heads: 4.2 M partial
+// sectors written become 0.3 M).  That holds for a prompt whose first token in the call begins a group; one that begins
+// elsewhere, or after others in the call whose lengths are no multiples of 16, goes token by token here (kGroupTokens has
+// the times).  Key warps as above.  The query heads, which HBM bounds, and the quantising are blocks of one grid in
+// turn, so that an SM has both.  8192 tokens of 32 + 8 + 8 heads of 128: 37.3 us; its bytes alone would take 26.  63 % of
+// the issue slots, and the 44 % of the warps that registers leave wait for loads most.
 template <int D, bool TURNED, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 4) prompt_kernel(const ForwardArgs a) {
     begin_chained();
@@ -600,7 +604,8 @@ __device__ __forceinline__ uint4 kv4_values(uint32_t codes, uint32_t pair) {
 }
 
 // The tokens at `slots`, zeros for padding: a warp takes NV heads of one token, or (gather_groups_kernel) a head of 16
-// tokens where they are a group of the cache.  HBM bound by what it writes: 8192 tokens of 8 heads of 128 take about 9 us.
+// tokens where they are a group of the cache.  8192 tokens of 8 heads of 128, 42 MB: 8.0 us, where the bytes would take
+// 6.2; a warp loads, converts and stores once, and nothing of its own overlaps its wait.
 template <int D>
 __device__ __forceinline__ void gather_token(const Kv4Cache& c, const Place& place, int64_t t, int h, bool mine, int l,
                                              uint16_t* k, uint16_t* v) {
@@ -681,7 +686,7 @@ __global__ void __launch_bounds__(kThreads) gather_groups_kernel(const Kv4Cache 
 // token's query or key heads, kBwdUnroll loads of a warp at a time; the warps of one
 // block an SM take equal, contiguous ranges of all units, so that a token's angles are
 // loaded once, and ahead.  The projection takes a second reduction after r; in whole units the
-// first ones of all vectors overlap (4096 tokens 24.1 us; one vector after another 26.7, 16,384
+// first ones of all vectors overlap (4096 tokens 24.0 us; one vector after another 26.7, 16,384
 // 80.0 and 84.4).  A warp copies its next unit's dy and x to shared memory while it works
 // on one, and each lane sums its elements' dw in 32 bits; a block's sums go to `part`,
 // and the block that finishes last adds the blocks' sums in their order, all loads in
@@ -689,10 +694,9 @@ __global__ void __launch_bounds__(kThreads) gather_groups_kernel(const Kv4Cache 
 //
 // Bound: HBM, once the batch is long.  12 warps have 168 registers each, which lets
 // the four vectors' reductions overlap.  32 + 8 heads of 128 (us, 12 warps / 16): 256
-// tokens 5.6/5.9, 1024 9.2/10.2, 4096 25.4/24.4, 16384 81/84 (8 warps: 98; the bytes
-// alone: 75).  A third stage makes no difference, and loads into registers one
-// unit ahead, in place of the copies, took 35 at 4096.  Of the 25, about 5 are the
-// launch, the first loads and the last block's sums.
+// tokens 5.5/5.8, 1024 8.6/9.8, 4096 24.0/25.4, 16384 80.0/87.5 (the bytes alone: 75);
+// with few heads 16 are a little faster (8192 tokens of 14 + 2 heads of 64 16.9/16.1).
+// Of the 24, about 5 are the launch, the first loads and the last block's sums.
 struct BackwardArgs {
     HeadsIn dqo, dko, q, k;
     RopeParams rope;

@@ -247,7 +247,8 @@ int r9q_gate_up_swiglu_down_noalloc(const void* x_bf16,
  * strides in elements (multiples of 8, so that every vector is 16-byte aligned;
  * slices of the QKV GEMM's output are such tensors).  Outputs may not overlap
  * inputs, and an output's own vectors may not overlap one another; the q and k
- * outputs may be slices of one buffer.  T = 0 is a no-op (the gradient then
+ * outputs may be slices of one buffer.  Inputs are all that a call reads: weights,
+ * tables, positions and slots too.  T = 0 is a no-op (the gradient then
  * writes zeros to dwq and dwk).
  * Positions, slots and page numbers are read on the device.  One that is out of
  * range reads and writes nothing out of bounds: it sets the device error word to
@@ -261,7 +262,8 @@ int r9q_gate_up_swiglu_down_noalloc(const void* x_bf16,
  *   (i, i + rot/2), or with R9Q_ROPE_INTERLEAVED (2i, 2i + 1).
  * wq, wk fp32 [D]; rot a multiple of 16, 0..D (0: norm only; cos, sin and pos may
  * then be NULL); cos and sin 16-byte aligned; pos int64 [T].  fp32 inside, one
- * rounding to bf16. */
+ * rounding to bf16.  eps >= 0; mean(x^2) + eps is to be a normal fp32 number (a
+ * vector of zeros with eps 0 gives NaN). */
 #define R9Q_ROPE_INTERLEAVED 1
 int r9q_qk_norm_rope(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts, int64_t k_hs,
                      const float* wq, const float* wk, const float* cos, const float* sin, const int64_t* pos,
@@ -333,11 +335,12 @@ int r9q_kv4_gather(const uint8_t* kc, const void* kp, const uint8_t* vc, const v
  * A token that sees nothing (p < 0) gets o = 0, lse = -infinity.  Query head h
  * uses key-value head h / (Hq / Hk).  Keys that a token does not see do not reach
  * its result, whatever they hold (NaN and infinities too).  scale > 0.
- * Scores, sums and accumulators are fp32; weights are rounded to fp16.  The
+ * Scores, sums and accumulators are fp32; weights (times the values' steps) are
+ * rounded to fp16, which moves a result by about 2e-4 of its size before it is rounded to bf16.  The
  * result does not depend on timing; its last bits depend on the lengths of the
  * whole batch and on max_pages (they decide where the work is cut).
  * Built for few rows Lq * Hq / Hk of a key-value head: each 8 or 16 of them read
- * the codes again.  workspace: r9q_workspace_bytes(R9Q_OP_KV4_ATTENTION,
+ * the codes again, of all keys that any new token of the sequence sees.  workspace: r9q_workspace_bytes(R9Q_OP_KV4_ATTENTION,
  * Lq * Hq / Hk, D, ...), zeroed before its first use and left with a zero header
  * by every call, as for r9q_gemm_fp8_block_qa.
  * Errors of all of these: R9Q_ERR_NULL, R9Q_ERR_DIM, R9Q_ERR_ALIGN (pointers,
