@@ -10,7 +10,8 @@
 // once and uses them for all its heads of the token.
 //
 // HBM bound: each input and output once (8192 tokens of 32 + 32 heads of 128: 43.4 us,
-// 6.3 TB/s, 92 % of the copy rate; of 32 + 8: 32.8 us, 5.2 TB/s; eight tokens: 2.2 us, the launch).  A head vector takes D/8 lanes, 16 bytes
+// 6.3 TB/s, 92 % of the copy rate; of 32 + 8: 32.8 us, 5.2 TB/s; eight tokens: 2.2 us,
+// the launch).  A head vector takes D/8 lanes, 16 bytes
 // each.  Where the whole vector turns in pairs (i, i + D/2), the common case, a lane
 // takes four elements of either half (two 8-byte accesses), so that it holds both of
 // each pair; otherwise it takes eight in a row and x' comes from the lane that holds

@@ -336,13 +336,14 @@ int r9q_kv4_gather(const uint8_t* kc, const void* kp, const uint8_t* vc, const v
  * uses key-value head h / (Hq / Hk).  Keys that a token does not see do not reach
  * its result, whatever they hold (NaN and infinities too).  scale > 0.
  * Scores, sums and accumulators are fp32; weights (times the values' steps) are
- * rounded to fp16, which moves a result by about 2e-4 of its size before it is rounded to bf16.  The
- * result does not depend on timing; its last bits depend on the lengths of the
+ * rounded to fp16, which moves a result by about 2e-4 of its size before it is
+ * rounded to bf16.  The result does not depend on timing; its last bits depend on the lengths of the
  * whole batch and on max_pages (they decide where the work is cut).
  * Built for few rows Lq * Hq / Hk of a key-value head: each 8 or 16 of them read
- * the codes again, of all keys that any new token of the sequence sees.  workspace: r9q_workspace_bytes(R9Q_OP_KV4_ATTENTION,
- * Lq * Hq / Hk, D, ...), zeroed before its first use and left with a zero header
- * by every call, as for r9q_gemm_fp8_block_qa.
+ * the codes again, of all keys that any new token of the sequence sees.
+ * workspace: r9q_workspace_bytes(R9Q_OP_KV4_ATTENTION, Lq * Hq / Hk, D, ...), zeroed
+ * before its first use and left with a zero header by every call, as for
+ * r9q_gemm_fp8_block_qa.
  * Errors of all of these: R9Q_ERR_NULL, R9Q_ERR_DIM, R9Q_ERR_ALIGN (pointers,
  * strides), R9Q_ERR_ARG (flags, eps, scale, overlap), R9Q_ERR_WORKSPACE,
  * R9Q_ERR_DEVICE, R9Q_ERR_LAUNCH. */
