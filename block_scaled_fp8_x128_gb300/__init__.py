@@ -3,7 +3,7 @@
 Argument marshalling only: each function takes torch tensors, checks dtype,
 shape and device, and calls the C entry point of the same name in
 ``include/r9q.h`` on the current CUDA stream, through ctypes or, for the
-attention block's calls, through ``_calls.so``.  Every step of the computation
+sequence operators' calls, through ``_calls.so``.  Every step of the computation
 runs in the library's CUDA kernels; there is no fallback.  Importing this
 package raises if ``libr9q.so`` has not been built (``build.py``), and the
 attention block's calls if ``_calls.so`` has not been, for this torch.
@@ -74,6 +74,15 @@ _SIGS = {
     "r9q_kv4_append": ([_P, _I64, _I64] * 2 + [_P] * 5 + [_I64] * 5 + [_P], ctypes.c_int),
     "r9q_kv4_gather": ([_P] * 5 + [_I64] * 5 + [_P] * 3, ctypes.c_int),
     "r9q_kv4_attention": ([_P] + [_I64] * 3 + [_P] * 8 + [_I64] * 9 + [ctypes.c_float, _P, _SZ, _P], ctypes.c_int),
+    "r9q_kv4_tree_attention": ([_P] + [_I64] * 3 + [_P] * 9 + [_I64] * 9 + [ctypes.c_float, _P, _SZ, _P], ctypes.c_int),
+    "r9q_kv4_move": ([_P] * 6 + [_I64] * 6 + [_P], ctypes.c_int),
+    "r9q_gated_delta": ([_P, _I64, _I64] * 3 + [_P] * 6 + [_I64] * 6 + [ctypes.c_float] * 2 + [ctypes.c_int, _P],
+                        ctypes.c_int),
+    "r9q_gated_delta_step": ([_P, _I64, _I64, _I64] * 3 + [_P] * 5 + [_I64] * 6 + [ctypes.c_float] * 2 +
+                             [ctypes.c_int, _P], ctypes.c_int),
+    "r9q_gated_delta_tree": ([_P, _I64, _I64, _I64] * 3 + [_P] * 6 + [_I64] * 6 + [ctypes.c_float] * 2 + [_P],
+                             ctypes.c_int),
+    "r9q_gated_delta_commit": ([_P, _I64, _I64, _I64] * 2 + [_P] * 5 + [_I64] * 7 + [ctypes.c_float, _P], ctypes.c_int),
 }
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -94,6 +103,7 @@ R9Q_OP_GATE_UP_SWIGLU_DOWN = 3
 R9Q_OP_QK_NORM_ROPE_BWD = 4
 R9Q_OP_KV4_ATTENTION = 5
 R9Q_ROPE_INTERLEAVED = 1
+R9Q_DELTA_FROM_ZERO = 1
 
 
 class R9QError(RuntimeError):
@@ -562,3 +572,81 @@ def r9q_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tenso
                            _calls.kv4_attention,
                            (q, *cache, block_table, seq_lens, scale, window, out, lse, return_lse), workspace, q.device,
                            stream)
+
+
+def r9q_kv4_tree_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                           parents: torch.Tensor, scale: float | None = None, window: int = 0,
+                           out: torch.Tensor | None = None, lse: torch.Tensor | None = None, return_lse: bool = False,
+                           workspace: torch.Tensor | None = None, stream=None):
+    """r9q_kv4_attention with the last Lq (at most 64) tokens of each sequence as the nodes of a tree: parents int32
+    [B][Lq], each node's parent before it (0 .. i - 1), -1 the sequence's token before the tree, -2 no node.  A node sees
+    what is before the tree, its ancestors and itself.  Workspace, outputs and the rest as there."""
+    return _with_workspace("r9q_kv4_tree_attention", R9Q_OP_KV4_ATTENTION,
+                           lambda: (max(1, q.shape[1] * q.shape[2] // cache.k.shape[1]), q.shape[3]),
+                           _calls.kv4_tree_attention,
+                           (q, *cache, block_table, seq_lens, parents, scale, window, out, lse, return_lse), workspace,
+                           q.device, stream)
+
+
+def r9q_kv4_move(cache: KV4Cache, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """Copies tokens of the cache from slots src to slots dst, int64 [rows][n] (n at most 64; negative: passed over).  All
+    of a row is read before any of it is written; rows may not write what another row reads or writes."""
+    index = src.device.index
+    if stream is not None or index is None or index != _current_device():
+        return _elsewhere(src.device, stream, r9q_kv4_move, cache, src, dst)
+    _checked(_calls.kv4_move(*cache, src, dst, _raw_stream(index)), "r9q_kv4_move")
+
+
+# ---- the gated delta rule ----
+# state fp32 [n_states][Hv][D][D] (values, keys) is read and written in place; the outputs carry no gradient.
+
+def r9q_gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                    state: torch.Tensor, slots: torch.Tensor, cu_seqlens: torch.Tensor, scale: float | None = None,
+                    eps: float = 1e-6, from_zero: bool = False, out: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """The gated delta rule over packed sequences: q, k bf16 [T][Hk][D], v bf16 [T][Hv][D] (any token and head strides),
+    g (log of the decay), beta fp32 [T][Hv]; sequence b has the tokens cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32
+    [B + 1]) and the state slots[b] (int32 [B]; negative: no sequence), which begins at zero with from_zero.  Keys and
+    queries are brought to unit length.  scale: 1/sqrt(D) by default.  Returns o bf16 [T][Hv][D]; rows of no sequence
+    are left as they are."""
+    index = k.device.index
+    if stream is not None or index is None or index != _current_device():
+        return _elsewhere(k.device, stream, r9q_gated_delta, q, k, v, g, beta, state, slots, cu_seqlens, scale, eps,
+                          from_zero, out)
+    return _checked(_calls.gated_delta(q, k, v, g, beta, state, slots, cu_seqlens, scale, eps, from_zero, out,
+                                       _raw_stream(index)), "r9q_gated_delta")
+
+
+def r9q_gated_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                         state: torch.Tensor, slots: torch.Tensor, scale: float | None = None, eps: float = 1e-6,
+                         from_zero: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The newest tokens of B sequences: r9q_gated_delta with q, k bf16 [B][Lq][Hk][D], v [B][Lq][Hv][D] (any batch, token
+    and head strides), g, beta fp32 [B][Lq][Hv]; returns o bf16 [B][Lq][Hv][D]."""
+    index = k.device.index
+    if stream is not None or index is None or index != _current_device():
+        return _elsewhere(k.device, stream, r9q_gated_delta_step, q, k, v, g, beta, state, slots, scale, eps, from_zero, out)
+    return _checked(_calls.gated_delta_step(q, k, v, g, beta, state, slots, None, scale, eps, from_zero, out,
+                                            _raw_stream(index)), "r9q_gated_delta_step")
+
+
+def r9q_gated_delta_tree(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                         state: torch.Tensor, slots: torch.Tensor, parents: torch.Tensor, scale: float | None = None,
+                         eps: float = 1e-6, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Drafted tokens: r9q_gated_delta_step along every path of a tree of Lq (at most 64) nodes, parents int32 [B][Lq] as
+    for r9q_kv4_tree_attention.  The states are not written; r9q_gated_delta_commit does that."""
+    index = k.device.index
+    if stream is not None or index is None or index != _current_device():
+        return _elsewhere(k.device, stream, r9q_gated_delta_tree, q, k, v, g, beta, state, slots, parents, scale, eps, out)
+    return _checked(_calls.gated_delta_tree(q, k, v, g, beta, state, slots, parents, scale, eps, False, out,
+                                            _raw_stream(index)), "r9q_gated_delta_tree")
+
+
+def r9q_gated_delta_commit(k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, state: torch.Tensor,
+                           slots: torch.Tensor, path: torch.Tensor, eps: float = 1e-6, stream=None) -> None:
+    """Takes the states on along an accepted path of the tree that k, v, g and beta are of: path int32 [B][P] (P at most
+    64), nodes from the tree's beginning on, until the first negative one."""
+    index = k.device.index
+    if stream is not None or index is None or index != _current_device():
+        return _elsewhere(k.device, stream, r9q_gated_delta_commit, k, v, g, beta, state, slots, path, eps)
+    _checked(_calls.gated_delta_commit(k, v, g, beta, state, slots, path, eps, _raw_stream(index)),
+             "r9q_gated_delta_commit")

@@ -1,5 +1,5 @@
-// The Python side of the attention block's calls (QK norm with rotation, the 4-bit
-// cache, the attention over it): checks of the tensors and the C call.
+// The Python side of the sequence operators' calls (QK norm with rotation, the 4-bit
+// cache, the attention over it, the gated delta rule): checks of the tensors and the C call.
 //
 // These kernels run for a few microseconds, as long as a dozen attribute reads in
 // Python take, so the checks are made here, on the tensors themselves.  Nothing else
@@ -325,9 +325,12 @@ PyObject* kv4_gather(PyObject* const* a) {
     return out.done(r9q_kv4_gather(c.k, c.kp, c.v, c.vp, slots, T, c.heads, c.dim, c.pages, c.page, k, v, stream(a[7])));
 }
 
-// q, cache.k, .kp, .v, .vp, block_table, seq_lens, scale, window, out, lse, return_lse, workspace, theirs, stream
-PyObject* kv4_attention(PyObject* const* a) {
-    if (captured(a[13], a[14])) return PyLong_FromLong(kCaptured);
+// q, cache.k, .kp, .v, .vp, block_table, seq_lens, parents, scale, window, out, lse, return_lse, workspace, theirs, stream
+// (parents: of a tree's nodes; not of r9q_kv4_attention)
+template <bool TREE>
+PyObject* attention(PyObject* const* a) {
+    PyObject* const* c_args = a + (TREE ? 8 : 7);            // from scale on
+    if (captured(c_args[6], c_args[7])) return PyLong_FromLong(kCaptured);
     const at::Tensor& q = tensor(a[0], "q");
     const at::Device dev = q.device();
     const at::IntArrayRef s = sizes(q, "q", 4);
@@ -340,19 +343,124 @@ PyObject* kv4_attention(PyObject* const* a) {
     const int64_t width = sizes(tensor(a[5], "block_table"), "block_table", 2)[1];
     const int32_t* table = static_cast<const int32_t*>(address(a[5], "block_table", at::kInt, {B, width}, dev));
     const int32_t* lens = static_cast<const int32_t*>(address(a[6], "seq_lens", at::kInt, {B}, dev));
-    const float scale = a[7] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : number(a[7]);
-    const Workspace w = workspace(a[12], dev);
-    const bool with_lse = truth(a[11]);
+    const float scale = c_args[0] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : number(c_args[0]);
+    const Workspace w = workspace(c_args[5], dev);
+    const bool with_lse = truth(c_args[4]);
     Outputs out;
     if (with_lse)
-        out.add(a[9], s, at::kBFloat16, a[10], {B, Lq, Hq}, at::kFloat, dev);
+        out.add(c_args[2], s, at::kBFloat16, c_args[3], {B, Lq, Hq}, at::kFloat, dev);
     else
-        out.add(output(a[9], at::kBFloat16, s, dev));
+        out.add(output(c_args[2], at::kBFloat16, s, dev));
     void* o = address(out.o[0], "out", at::kBFloat16, {B, Lq, Hq, D}, dev);
-    float* lse = static_cast<float*>(address(with_lse ? out.o[1] : a[10], "lse", at::kFloat, {B, Lq, Hq}, dev));
+    float* lse = static_cast<float*>(address(with_lse ? out.o[1] : c_args[3], "lse", at::kFloat, {B, Lq, Hq}, dev));
+    if constexpr (TREE) {
+        const int32_t* parents = static_cast<const int32_t*>(address(a[7], "parents", at::kInt, {B, Lq}, dev));
+        return out.done(r9q_kv4_tree_attention(q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), c.k, c.kp, c.v, c.vp,
+                                               table, lens, parents, o, lse, B, Lq, Hq, c.heads, D, c.pages, c.page, width,
+                                               integer(c_args[1]), scale, w.p, w.bytes, stream(c_args[7])));
+    }
     return out.done(r9q_kv4_attention(q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), c.k, c.kp, c.v, c.vp, table,
-                                      lens, o, lse, B, Lq, Hq, c.heads, D, c.pages, c.page, width, integer(a[8]), scale,
-                                      w.p, w.bytes, stream(a[14])));
+                                      lens, o, lse, B, Lq, Hq, c.heads, D, c.pages, c.page, width, integer(c_args[1]),
+                                      scale, w.p, w.bytes, stream(c_args[7])));
+}
+
+// cache.k, .kp, .v, .vp, src, dst, stream
+PyObject* kv4_move(PyObject* const* a) {
+    const at::Tensor& src = tensor(a[4], "src");
+    const at::Device dev = src.device();
+    const at::IntArrayRef s = sizes(src, "src", 2);
+    const int64_t rows = s[0], n = s[1];
+    const Cache c = cache(a, dev);
+    const int64_t* from = static_cast<const int64_t*>(address(a[4], "src", at::kLong, {rows, n}, dev));
+    const int64_t* to = static_cast<const int64_t*>(address(a[5], "dst", at::kLong, {rows, n}, dev));
+    return Outputs().done(r9q_kv4_move(c.k, c.kp, c.v, c.vp, from, to, rows, n, c.heads, c.dim, c.pages, c.page,
+                                       stream(a[6])));
+}
+
+// A [B][Lq][H][D] bf16 tensor with contiguous vectors.
+struct Tokens {
+    void* p;
+    int64_t bs, ts, hs;
+};
+Tokens tokens(PyObject* o, const char* name, Shape shape, at::Device device) {
+    const at::Tensor& t = checked(o, name, at::kBFloat16, shape, device);
+    if (t.size(3) > 1 && t.stride(3) != 1) raise(PyExc_ValueError, "%s: the last dimension must be contiguous", name);
+    return {t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)};
+}
+// The states, and the sequences' slots in them.
+struct States {
+    float* p;
+    int64_t n;
+    const int32_t* slots;
+};
+States states(PyObject* state, PyObject* slots, int64_t B, int64_t Hv, int64_t D, at::Device device) {
+    States r = {};
+    r.n = sizes(tensor(state, "state"), "state", 4)[0];
+    r.p = static_cast<float*>(address(state, "state", at::kFloat, {r.n, Hv, D, D}, device));
+    r.slots = static_cast<const int32_t*>(address(slots, "slots", at::kInt, {B}, device));
+    return r;
+}
+float scale_of(PyObject* o, int64_t D) { return o == Py_None ? (float)(1.0 / std::sqrt((double)D)) : number(o); }
+const float* rates(PyObject* o, const char* name, Shape shape, at::Device device) {
+    return static_cast<const float*>(address(o, name, at::kFloat, shape, device));
+}
+
+// q, k, v, g, beta, state, slots, cu_seqlens, scale, eps, from_zero, out, stream
+PyObject* gated_delta(PyObject* const* a) {
+    const at::Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    const at::Device dev = k.device();
+    const at::IntArrayRef ks = sizes(k, "k", 3), s = sizes(v, "v", 3);
+    const int64_t T = ks[0], Hk = ks[1], D = ks[2], Hv = s[1];
+    const Heads qh = heads(a[0], "q", {T, Hk, D}, dev), kh = heads(a[1], "k", {T, Hk, D}, dev);
+    const Heads vh = heads(a[2], "v", {T, Hv, D}, dev);
+    const float *g = rates(a[3], "g", {T, Hv}, dev), *beta = rates(a[4], "beta", {T, Hv}, dev);
+    const int64_t B = sizes(tensor(a[6], "slots"), "slots", 1)[0];
+    const States st = states(a[5], a[6], B, Hv, D, dev);
+    const int32_t* cu = static_cast<const int32_t*>(address(a[7], "cu_seqlens", at::kInt, {B + 1}, dev));
+    Outputs out;
+    void* o = address(out.add(output(a[11], at::kBFloat16, s, dev)), "out", at::kBFloat16, {T, Hv, D}, dev);
+    return out.done(r9q_gated_delta(qh.p, qh.ts, qh.hs, kh.p, kh.ts, kh.hs, vh.p, vh.ts, vh.hs, g, beta, cu, st.slots, st.p,
+                                    o, T, B, Hk, Hv, D, st.n, scale_of(a[8], D), number(a[9]),
+                                    truth(a[10]) ? R9Q_DELTA_FROM_ZERO : 0, stream(a[12])));
+}
+
+// q, k, v, g, beta, state, slots, parents (of a tree; None of a step), scale, eps, from_zero, out, stream
+template <bool TREE>
+PyObject* delta_tokens(PyObject* const* a) {
+    const at::Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    const at::Device dev = k.device();
+    const at::IntArrayRef ks = sizes(k, "k", 4), s = sizes(v, "v", 4);
+    const int64_t B = ks[0], Lq = ks[1], Hk = ks[2], D = ks[3], Hv = s[2];
+    const Tokens qt = tokens(a[0], "q", {B, Lq, Hk, D}, dev), kt = tokens(a[1], "k", {B, Lq, Hk, D}, dev);
+    const Tokens vt = tokens(a[2], "v", {B, Lq, Hv, D}, dev);
+    const float *g = rates(a[3], "g", {B, Lq, Hv}, dev), *beta = rates(a[4], "beta", {B, Lq, Hv}, dev);
+    const States st = states(a[5], a[6], B, Hv, D, dev);
+    const int32_t* parents = static_cast<const int32_t*>(address(a[7], "parents", at::kInt, {B, Lq}, dev));
+    Outputs out;
+    void* o = address(out.add(output(a[11], at::kBFloat16, s, dev)), "out", at::kBFloat16, {B, Lq, Hv, D}, dev);
+    const float scale = scale_of(a[8], D), eps = number(a[9]);
+    if constexpr (TREE)
+        return out.done(r9q_gated_delta_tree(qt.p, qt.bs, qt.ts, qt.hs, kt.p, kt.bs, kt.ts, kt.hs, vt.p, vt.bs, vt.ts,
+                                             vt.hs, g, beta, parents, st.slots, st.p, o, B, Lq, Hk, Hv, D, st.n, scale, eps,
+                                             stream(a[12])));
+    return out.done(r9q_gated_delta_step(qt.p, qt.bs, qt.ts, qt.hs, kt.p, kt.bs, kt.ts, kt.hs, vt.p, vt.bs, vt.ts, vt.hs, g,
+                                         beta, st.slots, st.p, o, B, Lq, Hk, Hv, D, st.n, scale, eps,
+                                         truth(a[10]) ? R9Q_DELTA_FROM_ZERO : 0, stream(a[12])));
+}
+
+// k, v, g, beta, state, slots, path, eps, stream
+PyObject* gated_delta_commit(PyObject* const* a) {
+    const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
+    const at::Device dev = k.device();
+    const at::IntArrayRef ks = sizes(k, "k", 4), s = sizes(v, "v", 4);
+    const int64_t B = ks[0], Lq = ks[1], Hk = ks[2], D = ks[3], Hv = s[2];
+    const Tokens kt = tokens(a[0], "k", {B, Lq, Hk, D}, dev), vt = tokens(a[1], "v", {B, Lq, Hv, D}, dev);
+    const float *g = rates(a[2], "g", {B, Lq, Hv}, dev), *beta = rates(a[3], "beta", {B, Lq, Hv}, dev);
+    const States st = states(a[4], a[5], B, Hv, D, dev);
+    const int64_t P = sizes(tensor(a[6], "path"), "path", 2)[1];
+    const int32_t* path = static_cast<const int32_t*>(address(a[6], "path", at::kInt, {B, P}, dev));
+    return Outputs().done(r9q_gated_delta_commit(kt.p, kt.bs, kt.ts, kt.hs, vt.p, vt.bs, vt.ts, vt.hs, g, beta, path,
+                                                 st.slots, st.p, B, Lq, P, Hk, Hv, D, st.n, number(a[7]), stream(a[8])));
 }
 
 template <PyObject* (*CALL)(PyObject* const*), int N>
@@ -386,7 +494,13 @@ PyMethodDef g_methods[] = {method<qk_norm_rope, 12>("qk_norm_rope"),
                            method<qk_norm_rope_kv4, 17>("qk_norm_rope_kv4"),
                            method<kv4_append, 8>("kv4_append"),
                            method<kv4_gather, 8>("kv4_gather"),
-                           method<kv4_attention, 15>("kv4_attention"),
+                           method<attention<false>, 15>("kv4_attention"),
+                           method<attention<true>, 16>("kv4_tree_attention"),
+                           method<kv4_move, 7>("kv4_move"),
+                           method<gated_delta, 13>("gated_delta"),
+                           method<delta_tokens<false>, 13>("gated_delta_step"),
+                           method<delta_tokens<true>, 13>("gated_delta_tree"),
+                           method<gated_delta_commit, 9>("gated_delta_commit"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

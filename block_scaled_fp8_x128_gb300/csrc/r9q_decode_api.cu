@@ -1,5 +1,6 @@
-// C ABI of the attention operators (declared in include/r9q.h): QK norm with
-// rotation, its gradient, the paged 4-bit cache and the attention over it.
+// C ABI of the sequence operators (declared in include/r9q.h): QK norm with
+// rotation, its gradient, the paged 4-bit cache and the attention over it, and the
+// gated delta rule.
 // Argument checks and dispatch, as in r9q_api.cu.
 #include <algorithm>
 #include <climits>
@@ -335,11 +336,11 @@ int r9q_kv4_gather(const uint8_t* kc, const void* kp, const uint8_t* vc, const v
                                     static_cast<cudaStream_t>(stream)));
 }
 
-int r9q_kv4_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, const uint8_t* kc, const void* kp,
-                      const uint8_t* vc, const void* vp, const int32_t* block_table, const int32_t* seq_lens, void* o,
-                      float* lse, int64_t B, int64_t Lq, int64_t Hq, int64_t Hk, int64_t D, int64_t pages,
-                      int64_t page, int64_t max_pages, int64_t window, float scale, void* workspace,
-                      size_t workspace_bytes, void* stream) {
+static int attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, const uint8_t* kc, const void* kp,
+                     const uint8_t* vc, const void* vp, const int32_t* block_table, const int32_t* seq_lens,
+                     const int32_t* parents, void* o, float* lse, int64_t B, int64_t Lq, int64_t Hq, int64_t Hk,
+                     int64_t D, int64_t pages, int64_t page, int64_t max_pages, int64_t window, float scale,
+                     void* workspace, size_t workspace_bytes, void* stream) {
     if (!dims_ok(Lq, Hq, D) || !dims_ok(Lq, Hk, D) || B < 0 || Hq % Hk) return R9Q_ERR_DIM;
     if (B > INT_MAX / 64 || Lq > (1 << 20) || B * Lq > INT_MAX || max_pages < 0 || max_pages > INT_MAX || window < 0)
         return R9Q_ERR_DIM;
@@ -352,7 +353,9 @@ int r9q_kv4_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, c
     if (!rc) rc = check_cache(kc, kp, vc, vp, pages, Hk, page);
     if (rc) return rc;
     if (!seq_lens || !o || (max_pages > 0 && !block_table)) return R9Q_ERR_NULL;
-    if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4)) return R9Q_ERR_ALIGN;
+    if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+        !aligned(parents, 4))
+        return R9Q_ERR_ALIGN;
     if (!(scale > 0.0f) || std::isinf(scale) || max_pages * page > 0x7FE00000) return R9Q_ERR_ARG;
     const size_t need = decode_workspace(R9Q_OP_KV4_ATTENTION, rows, D, &rc);
     if (!workspace || workspace_bytes < need) return R9Q_ERR_WORKSPACE;
@@ -360,12 +363,14 @@ int r9q_kv4_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, c
     const Kv4Cache c = cache_of(kc, kp, vc, vp, pages, Hk, page);
     const Extent qe = bytes_of(q, (B > 1 ? 2 * (B - 1) * q_bs : 0) +
                                       (int64_t)(extent(q, Lq, Hq, D, q_ts, q_hs).hi - reinterpret_cast<uintptr_t>(q)));
-    const Extent tables[2] = {bytes_of(block_table, B * max_pages * 4), bytes_of(seq_lens, B * 4)};
+    const Extent tables[3] = {bytes_of(block_table, B * max_pages * 4), bytes_of(seq_lens, B * 4),
+                              bytes_of(parents, B * Lq * 4)};
     const Extent out[3] = {bytes_of(o, 2 * B * Lq * Hq * D), bytes_of(lse, 4 * B * Lq * Hq),
                            bytes_of(workspace, (int64_t)need)};
     for (int i = 0; i < 3; ++i) {
         if (out[i].lo == 0) continue;                         // no lse
-        if (meet(out[i], qe) || meet(out[i], tables[0]) || meet(out[i], tables[1]) || cache_meets(c, D, out[i]))
+        if (meet(out[i], qe) || meet(out[i], tables[0]) || meet(out[i], tables[1]) || meet(out[i], tables[2]) ||
+            cache_meets(c, D, out[i]))
             return R9Q_ERR_ARG;
         for (int n = 0; n < i; ++n)
             if (meet(out[i], out[n])) return R9Q_ERR_ARG;
@@ -381,6 +386,7 @@ int r9q_kv4_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, c
     p.c = c;
     p.table = block_table;
     p.lens = seq_lens;
+    p.parents = parents;
     p.o = static_cast<uint16_t*>(o);
     p.lse = lse;
     p.done = static_cast<int*>(workspace);
@@ -396,6 +402,171 @@ int r9q_kv4_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, c
     p.reach = p.window > 0 ? (int)(p.window > INT_MAX - Lq ? INT_MAX : p.window + Lq - 1) : INT_MAX;
     p.scale_log2 = scale * 1.4426950408889634f;
     return status(launch_kv4_attention((int)D, p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int r9q_kv4_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, const uint8_t* kc, const void* kp,
+                      const uint8_t* vc, const void* vp, const int32_t* block_table, const int32_t* seq_lens, void* o,
+                      float* lse, int64_t B, int64_t Lq, int64_t Hq, int64_t Hk, int64_t D, int64_t pages,
+                      int64_t page, int64_t max_pages, int64_t window, float scale, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+    return attention(q, q_bs, q_ts, q_hs, kc, kp, vc, vp, block_table, seq_lens, nullptr, o, lse, B, Lq, Hq, Hk, D, pages,
+                     page, max_pages, window, scale, workspace, workspace_bytes, stream);
+}
+
+int r9q_kv4_tree_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, const uint8_t* kc, const void* kp,
+                           const uint8_t* vc, const void* vp, const int32_t* block_table, const int32_t* seq_lens,
+                           const int32_t* parents, void* o, float* lse, int64_t B, int64_t Lq, int64_t Hq, int64_t Hk,
+                           int64_t D, int64_t pages, int64_t page, int64_t max_pages, int64_t window, float scale,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+    if (Lq > kMostNodes) return R9Q_ERR_DIM;
+    if (!parents && B > 0 && Lq > 0) return R9Q_ERR_NULL;
+    return attention(q, q_bs, q_ts, q_hs, kc, kp, vc, vp, block_table, seq_lens, parents, o, lse, B, Lq, Hq, Hk, D, pages,
+                     page, max_pages, window, scale, workspace, workspace_bytes, stream);
+}
+
+int r9q_kv4_move(uint8_t* kc, void* kp, uint8_t* vc, void* vp, const int64_t* src, const int64_t* dst, int64_t rows,
+                 int64_t n, int64_t Hk, int64_t D, int64_t pages, int64_t page, void* stream) {
+    if (!dims_ok(rows, Hk, D) || n < 0 || n > kMostNodes || rows * Hk > INT_MAX) return R9Q_ERR_DIM;
+    if (rows == 0 || n == 0) return R9Q_OK;
+    int rc = check_cache(kc, kp, vc, vp, pages, Hk, page);
+    if (!rc && (!src || !dst)) rc = R9Q_ERR_NULL;
+    if (!rc && (!aligned(src, 8) || !aligned(dst, 8))) rc = R9Q_ERR_ALIGN;
+    if (rc) return rc;
+    const Kv4Cache c = cache_of(kc, kp, vc, vp, pages, Hk, page);
+    if (cache_meets(c, D, bytes_of(src, rows * n * 8)) || cache_meets(c, D, bytes_of(dst, rows * n * 8)) ||
+        cache_overlaps_itself(c, D))
+        return R9Q_ERR_ARG;
+    int *err = nullptr, sms = 0;
+    rc = device_error_word_and_sms(&err, &sms);
+    if (rc) return rc;
+    return status(launch_kv4_move((int)D, c, src, dst, rows, (int)n, err, static_cast<cudaStream_t>(stream)));
+}
+
+// The tokens and states of the gated delta rule's calls: checks them and launches.  cu == nullptr: Lq tokens of each
+// sequence.  q and o: not of a commit.
+static int gated_delta(DeltaMode mode, const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, const void* k,
+                       int64_t k_bs, int64_t k_ts, int64_t k_hs, const void* v, int64_t v_bs, int64_t v_ts, int64_t v_hs,
+                       const float* g, const float* beta, const int32_t* cu, const int32_t* parents,
+                       const int32_t* path, int64_t P, const int32_t* slots, float* state, void* o, int64_t T, int64_t B,
+                       int64_t Lq, int64_t Hk, int64_t Hv, int64_t D, int64_t n_states, float scale, float eps, int flags,
+                       void* stream) {
+    const int64_t tokens = cu ? T : Lq, batch = cu ? 1 : B;                    // of the strided dimensions
+    if (!dims_ok(tokens, Hk, D) || !dims_ok(tokens, Hv, D) || Hv % Hk || B < 0 || P < 0) return R9Q_ERR_DIM;
+    if (B * Hv > INT_MAX / 4 || B * tokens > INT_MAX || n_states < 1 || n_states > INT_MAX) return R9Q_ERR_DIM;
+    if (mode != kDeltaChain && (Lq > kMostNodes || P > kMostNodes)) return R9Q_ERR_DIM;
+    if (flags & ~R9Q_DELTA_FROM_ZERO) return R9Q_ERR_ARG;
+    if (B == 0 || (!cu && Lq == 0) || (mode == kDeltaCommit && P == 0)) return R9Q_OK;
+    const bool asks = mode != kDeltaCommit;
+    if (!slots || !state || (mode == kDeltaTree && !parents) || (mode == kDeltaCommit && !path)) return R9Q_ERR_NULL;
+    if (!aligned(state, 16) || !aligned(g, 4) || !aligned(beta, 4) || !aligned(cu, 4) || !aligned(parents, 4) ||
+        !aligned(path, 4) || !aligned(slots, 4))
+        return R9Q_ERR_ALIGN;
+    struct Input {
+        const void* p;
+        int64_t bs, ts, hs, heads;
+    };
+    const Input in[3] = {{k, k_bs, k_ts, k_hs, Hk}, {v, v_bs, v_ts, v_hs, Hv}, {q, q_bs, q_ts, q_hs, Hk}};
+    const int64_t rows = batch * tokens;
+    Extent read[9];
+    int reads = 0;
+    if (rows > 0) {                                           // (T = 0: only the states count)
+        if (!g || !beta || (asks && !o)) return R9Q_ERR_NULL;
+        for (int i = 0; i < (asks ? 3 : 2); ++i) {
+            int rc = check_heads(in[i].p, tokens, in[i].ts, in[i].heads, in[i].hs);
+            if (!rc && !stride_ok(batch, in[i].bs)) rc = R9Q_ERR_ARG;
+            if (!rc && !stride_aligned(batch, in[i].bs)) rc = R9Q_ERR_ALIGN;
+            if (rc) return rc;
+            const uintptr_t at = reinterpret_cast<uintptr_t>(in[i].p);
+            read[reads++] = bytes_of(in[i].p, (batch > 1 ? 2 * (batch - 1) * in[i].bs : 0) +
+                                                  (int64_t)(extent(in[i].p, tokens, in[i].heads, D, in[i].ts, in[i].hs).hi - at));
+        }
+        if (asks && !aligned(o, 16)) return R9Q_ERR_ALIGN;
+        read[reads++] = bytes_of(g, rows * Hv * 4);
+        read[reads++] = bytes_of(beta, rows * Hv * 4);
+    }
+    if (!(eps >= 0.0f) || std::isinf(eps) || (asks && (!(scale > 0.0f) || std::isinf(scale)))) return R9Q_ERR_ARG;
+    read[reads++] = bytes_of(slots, B * 4);
+    if (cu) read[reads++] = bytes_of(cu, (B + 1) * 4);
+    if (parents) read[reads++] = bytes_of(parents, B * Lq * 4);
+    if (path) read[reads++] = bytes_of(path, B * P * 4);
+    if (n_states > ((int64_t)1 << 56) / (Hv * D * D)) return R9Q_ERR_DIM;
+    const Extent states = bytes_of(state, n_states * Hv * D * D * 4), out = bytes_of(asks ? o : nullptr, rows * Hv * D * 2);
+    for (int i = 0; i < reads; ++i)
+        if (meet(read[i], out) || (mode != kDeltaTree && meet(read[i], states))) return R9Q_ERR_ARG;
+    if (meet(states, out)) return R9Q_ERR_ARG;
+    int *err = nullptr, sms = 0;
+    const int rc = device_error_word_and_sms(&err, &sms);
+    if (rc) return rc;
+    DeltaParams p = {};
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = static_cast<const uint16_t*>(k);
+    p.v = static_cast<const uint16_t*>(v);
+    p.q_bs = q_bs;
+    p.q_ts = q_ts;
+    p.q_hs = q_hs;
+    p.k_bs = k_bs;
+    p.k_ts = k_ts;
+    p.k_hs = k_hs;
+    p.v_bs = v_bs;
+    p.v_ts = v_ts;
+    p.v_hs = v_hs;
+    p.g = g;
+    p.beta = beta;
+    p.state = state;
+    p.o = static_cast<uint16_t*>(o);
+    p.slots = slots;
+    p.cu = cu;
+    p.parents = parents;
+    p.path = path;
+    p.T = T;
+    p.B = (int)B;
+    p.Lq = (int)Lq;
+    p.P = (int)P;
+    p.Hk = (int)Hk;
+    p.Hv = (int)Hv;
+    p.ratio = (int)(Hv / Hk);
+    p.n_states = (int)n_states;
+    p.scale = scale;
+    p.eps = eps;
+    p.from_zero = flags & R9Q_DELTA_FROM_ZERO ? 1 : 0;
+    p.err = err;
+    return status(launch_delta((int)D, mode, p, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int r9q_gated_delta(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts, int64_t k_hs, const void* v,
+                    int64_t v_ts, int64_t v_hs, const float* g, const float* beta, const int32_t* cu_seqlens,
+                    const int32_t* slots, float* state, void* o, int64_t T, int64_t B, int64_t Hk, int64_t Hv, int64_t D,
+                    int64_t n_states, float scale, float eps, int flags, void* stream) {
+    if (!cu_seqlens && B > 0) return R9Q_ERR_NULL;
+    return gated_delta(kDeltaChain, q, 0, q_ts, q_hs, k, 0, k_ts, k_hs, v, 0, v_ts, v_hs, g, beta, cu_seqlens, nullptr,
+                       nullptr, 0, slots, state, o, T, B, 0, Hk, Hv, D, n_states, scale, eps, flags, stream);
+}
+
+int r9q_gated_delta_step(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_bs,
+                         int64_t k_ts, int64_t k_hs, const void* v, int64_t v_bs, int64_t v_ts, int64_t v_hs,
+                         const float* g, const float* beta, const int32_t* slots, float* state, void* o, int64_t B,
+                         int64_t Lq, int64_t Hk, int64_t Hv, int64_t D, int64_t n_states, float scale, float eps,
+                         int flags, void* stream) {
+    return gated_delta(kDeltaChain, q, q_bs, q_ts, q_hs, k, k_bs, k_ts, k_hs, v, v_bs, v_ts, v_hs, g, beta, nullptr,
+                       nullptr, nullptr, 0, slots, state, o, 0, B, Lq, Hk, Hv, D, n_states, scale, eps, flags, stream);
+}
+
+int r9q_gated_delta_tree(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_bs,
+                         int64_t k_ts, int64_t k_hs, const void* v, int64_t v_bs, int64_t v_ts, int64_t v_hs,
+                         const float* g, const float* beta, const int32_t* parents, const int32_t* slots,
+                         const float* state, void* o, int64_t B, int64_t Lq, int64_t Hk, int64_t Hv, int64_t D,
+                         int64_t n_states, float scale, float eps, void* stream) {
+    return gated_delta(kDeltaTree, q, q_bs, q_ts, q_hs, k, k_bs, k_ts, k_hs, v, v_bs, v_ts, v_hs, g, beta, nullptr, parents,
+                       nullptr, 0, slots, const_cast<float*>(state), o, 0, B, Lq, Hk, Hv, D, n_states, scale, eps, 0,
+                       stream);
+}
+
+int r9q_gated_delta_commit(const void* k, int64_t k_bs, int64_t k_ts, int64_t k_hs, const void* v, int64_t v_bs,
+                           int64_t v_ts, int64_t v_hs, const float* g, const float* beta, const int32_t* path,
+                           const int32_t* slots, float* state, int64_t B, int64_t Lq, int64_t P, int64_t Hk, int64_t Hv,
+                           int64_t D, int64_t n_states, float eps, void* stream) {
+    return gated_delta(kDeltaCommit, nullptr, 0, 0, 0, k, k_bs, k_ts, k_hs, v, v_bs, v_ts, v_hs, g, beta, nullptr, nullptr,
+                       path, P, slots, state, nullptr, 0, B, Lq, Hk, Hv, D, n_states, 1.0f, eps, 0, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,303 @@
+// The gated delta rule over a few tokens a sequence (formulas: r9q_delta.cuh): decode steps,
+// small trees of drafted tokens, accepted paths.
+//
+// The state is what costs: 4 D D bytes a head in and, where it changes, out.  So a
+// sequence's head is cut by rows (values), which do not meet: a warp holds 16 rows of S
+// in registers, row r + 4i in the lanes 8r .. 8r + 7, each with D/8 of its elements.  Groups
+// of up to eight tokens pass over it: all S k and S q first (the eight partial sums of four
+// rows and two products meet in seven shuffles, which leaves one result a lane), then the
+// sums over earlier tokens, then the update with all of the group's u at once.  What does
+// not depend on the row, the products of keys and queries among themselves and the decays,
+// is formed once for the CTA.  In a tree S stays as it is, and the group's sums go over the
+// ancestors of all groups.
+#include "r9q_delta.cuh"
+
+namespace r9q {
+
+namespace {
+
+constexpr int kGroup = 8;                    // tokens at a time
+constexpr int kWarps = 4, kRows = 16;        // of a CTA, of a warp
+constexpr int kThreads = 32 * kWarps;
+
+template <int D, DeltaMode MODE>
+struct Shared {
+    static constexpr int kKept = MODE == kDeltaTree ? kMostNodes : kGroup;      // tokens whose keys and u are kept
+    float kn[kKept][D], qn[kGroup][D];       // of unit length
+    float solve[kGroup][kKept], weigh[kGroup][kKept];        // beta A (k.k), scale A (q.k)
+    float g[kKept], beta[kGroup], fade[kGroup], left[kGroup];        // fade A(i, 0), left A(n, i)
+    float u[kWarps][kKept][kRows];
+    uint64_t above[kMostNodes];              // a node's ancestors, itself among them
+    int parents[kMostNodes];
+    NodeKind kind[kMostNodes];
+};
+
+// 32/8 lanes of a quarter warp hold `N` partial sums each (N 8 or 4); lane c of 8 gets the sum of the c-th (c/2-th).
+template <int N>
+__device__ __forceinline__ float meet8(const float (&x)[N], int c) {
+    float y[N / 2], z[N / 4];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float keep = c & 4 ? x[i + N / 2] : x[i], give = c & 4 ? x[i] : x[i + N / 2];
+        y[i] = keep + __shfl_xor_sync(0xffffffffu, give, 4);
+    }
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+        const float keep = c & 2 ? y[i + N / 4] : y[i], give = c & 2 ? y[i] : y[i + N / 4];
+        z[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+    }
+    if constexpr (N == 4) return z[0] + __shfl_xor_sync(0xffffffffu, z[0], 1);
+    const float keep = c & 1 ? z[N / 4 - 1] : z[0], give = c & 1 ? z[0] : z[N / 4 - 1];
+    return keep + __shfl_xor_sync(0xffffffffu, give, 1);
+}
+
+// A bf16 head vector, D/32 elements a lane, as fp32 of unit length in shared memory.
+template <int D>
+__device__ __forceinline__ void unit_vector(const uint16_t* src, float* dst, float eps, int lane) {
+    float x[D / 32];
+    if constexpr (D == 128) {
+        const uint2 w = reinterpret_cast<const uint2*>(src)[lane];
+        x[0] = bf16_lo(w.x);
+        x[1] = bf16_hi(w.x);
+        x[2] = bf16_lo(w.y);
+        x[3] = bf16_hi(w.y);
+    } else {
+        const uint32_t w = reinterpret_cast<const uint32_t*>(src)[lane];
+        x[0] = bf16_lo(w);
+        x[1] = bf16_hi(w);
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) sum = fmaf(x[i], x[i], sum);
+    const float r = rsqrtf(group_sum<32>(sum) + eps);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) dst[lane * (D / 32) + i] = x[i] * r;
+}
+
+template <int D, DeltaMode MODE>
+__global__ void __launch_bounds__(kThreads) delta_rows_kernel(const DeltaParams p) {
+    constexpr int PARTS = D / (kWarps * kRows), M = D / 32;  // CTAs of a head; 16-byte pieces of a row that a lane has
+    constexpr bool TREE = MODE == kDeltaTree, HAS_Q = MODE != kDeltaCommit;
+    constexpr int KEPT = Shared<D, MODE>::kKept;
+    extern __shared__ __align__(16) uint8_t smem[];
+    Shared<D, MODE>& sh = *reinterpret_cast<Shared<D, MODE>*>(smem);
+    begin_chained();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 7, r = lane >> 3;
+    const int part = blockIdx.x % PARTS, bh = blockIdx.x / PARTS, b = bh / p.Hv, h = bh - b * p.Hv, hk = h / p.ratio;
+    const int row0 = (part * kWarps + warp) * kRows;
+    int n;
+    int64_t row;
+    delta_tokens(p, b, n, row);
+    const int32_t* path = p.path + (int64_t)b * p.P;
+    if constexpr (MODE == kDeltaCommit) {    // the path ends before its first entry that is not a node
+        bool bad = false;
+        uint64_t ends = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = i * 32 + lane, node = at < p.P ? path[at] : -1;
+            ends |= (uint64_t)__ballot_sync(0xffffffffu, node < 0 || node >= p.Lq) << (32 * i);
+            bad = bad || node >= p.Lq;
+        }
+        if (bad) record_error(p.err, kErrArg);
+        n = ends ? __ffsll((long long)ends) - 1 : p.P;
+    }
+    const int first_slot = p.slots[b];       // (its rows are on their way while the slot is checked)
+    float* rows = p.state + (((int64_t)(first_slot >= 0 && first_slot < p.n_states ? first_slot : 0) * p.Hv + h) * D + row0) * D;
+    uint64_t s[4][2 * M];                    // pairs of rows r + 4i
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            ulonglong2 x = make_ulonglong2(0ull, 0ull);
+            if (!p.from_zero) x = *reinterpret_cast<const ulonglong2*>(rows + (r + 4 * i) * D + m * 32 + c * 4);
+            s[i][2 * m] = x.x;
+            s[i][2 * m + 1] = x.y;
+        }
+    const int slot = delta_slot<!TREE>(p, b);
+    if (slot < 0) {                          // no state: outputs of zero, or NaN where it should have been one
+        if constexpr (HAS_Q)
+            for (int x = tid; x < n * (kWarps * kRows); x += kThreads)
+                p.o[((row + x / (kWarps * kRows)) * p.Hv + h) * D + part * kWarps * kRows + x % (kWarps * kRows)] =
+                    slot == -1 ? 0 : 0x7FC0;
+        return;
+    }
+    if constexpr (TREE) {
+        if (tid < n) {
+            sh.parents[tid] = p.parents[(int64_t)b * p.Lq + tid];
+            sh.g[tid] = p.g[(row + tid) * p.Hv + h];
+        }
+        __syncthreads();
+        if (tid < n) {
+            int depth;
+            const NodeKind kind = find_node(sh.parents, tid, kMostNodes, sh.above[tid], depth);
+            if (kind == kBadNode) record_error(p.err, kErrArg);
+            if (kind != kNode) sh.above[tid] = 0;
+            sh.kind[tid] = kind;
+        }
+    }
+    const bool second = HAS_Q && (c & 1);    // the lane gets S q of its row; else S k
+    const int own = row0 + r + 4 * (c >> 1); // that row
+
+#pragma unroll 1
+    for (int base = 0; base < n; base += kGroup) {
+        const int cnt = min(kGroup, n - base), kept = TREE ? base : 0;       // where the group's tokens are kept
+        auto token = [&](int t) { return MODE == kDeltaCommit ? path[base + t] : base + t; };
+        float v[kGroup];
+#pragma unroll
+        for (int t = 0; t < kGroup; ++t)
+            v[t] = t < cnt ? bf16_lo(p.v[b * p.v_bs + (p.cu ? row : 0) * p.v_ts + token(t) * p.v_ts + h * p.v_hs + own]) : 0.0f;
+        __syncthreads();                     // what the last group left is used
+        for (int t = warp; t < cnt; t += kWarps) {
+            const int64_t at = (p.cu ? row : 0) + token(t);
+            unit_vector<D>(p.k + b * p.k_bs + at * p.k_ts + hk * p.k_hs, sh.kn[kept + t], p.eps, lane);
+            if constexpr (HAS_Q) unit_vector<D>(p.q + b * p.q_bs + at * p.q_ts + hk * p.q_hs, sh.qn[t], p.eps, lane);
+        }
+        if (tid < cnt) {
+            const int64_t at = (row + token(tid)) * p.Hv + h;
+            if constexpr (!TREE) sh.g[tid] = p.g[at];
+            sh.beta[tid] = p.beta[at];
+        }
+        __syncthreads();
+        // products among the tokens, a warp for each pair (i, j <= i)
+        const int span = kept + cnt;
+#pragma unroll 1
+        for (int x = warp; x < cnt * span; x += kWarps) {
+            const int i = x / span, j = x - i * span, me = kept + i;
+            if (j > me || (TREE && !(sh.above[me] >> j & 1))) {
+                if (lane == 0) sh.solve[i][j] = sh.weigh[i][j] = 0.0f;
+                continue;
+            }
+            float kk = 0.0f, qk = 0.0f;
+#pragma unroll
+            for (int e = lane; e < D; e += 32) {
+                kk = fmaf(sh.kn[me][e], sh.kn[j][e], kk);
+                if constexpr (HAS_Q) qk = fmaf(sh.qn[i][e], sh.kn[j][e], qk);
+            }
+            kk = group_sum<32>(kk);
+            if constexpr (HAS_Q) qk = group_sum<32>(qk);
+            float sum = 0.0f;                // of the decays after j, up to me
+            for (int t = me; t != j; t = TREE ? sh.parents[t] : t - 1) sum += sh.g[t];
+            const float a = expf(sum);
+            if (lane == 0) {
+                sh.solve[i][j] = j == me ? 0.0f : sh.beta[i] * a * kk;
+                sh.weigh[i][j] = p.scale * a * qk;
+            }
+        }
+        if (tid < cnt) {
+            float before = 0.0f, after = 0.0f;
+            if constexpr (TREE) {
+                if (sh.kind[base + tid] == kNode)
+                    for (int t = base + tid; t >= 0; t = sh.parents[t]) before += sh.g[t];
+            } else {
+                for (int t = 0; t <= tid; ++t) before += sh.g[t];
+                for (int t = tid + 1; t < cnt; ++t) after += sh.g[t];
+            }
+            sh.fade[tid] = expf(before);
+            sh.left[tid] = expf(after);
+        }
+        __syncthreads();
+
+        float val[kGroup], u[kGroup];        // S k or S q, then the sums
+#pragma unroll
+        for (int t = 0; t < kGroup; ++t) {
+            if (t >= cnt) break;
+            float x[HAS_Q ? 8 : 4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint64_t wk = 0, wq = 0;     // (two zeros)
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&sh.kn[kept + t][m * 32 + c * 4]);
+                    wk = fma2(s[i][2 * m], k.x, wk);
+                    wk = fma2(s[i][2 * m + 1], k.y, wk);
+                    if constexpr (HAS_Q) {
+                        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&sh.qn[t][m * 32 + c * 4]);
+                        wq = fma2(s[i][2 * m], q.x, wq);
+                        wq = fma2(s[i][2 * m + 1], q.y, wq);
+                    }
+                }
+                const float2 a = parts_of(wk), d = parts_of(wq);
+                x[HAS_Q ? 2 * i : i] = a.x + a.y;
+                if constexpr (HAS_Q) x[2 * i + 1] = d.x + d.y;
+            }
+            val[t] = meet8(x, c);
+        }
+        float (*mine)[KEPT] = second ? sh.weigh : sh.solve;
+#pragma unroll
+        for (int t = 0; t < kGroup; ++t) {
+            if (t >= cnt) break;
+            float x = sh.fade[t] * val[t];
+            x = second ? p.scale * x : sh.beta[t] * (v[t] - x);
+            const float sign = second ? 1.0f : -1.0f;
+            // (a node takes its ancestors alone: the others may hold anything)
+            const uint64_t above = TREE ? sh.above[base + t] : ~0ull;
+            if constexpr (TREE)
+                for (int j = 0; j < base; ++j)
+                    if (above >> j & 1) x = fmaf(sign * mine[t][j], sh.u[warp][j][r * 4 + (c >> 1)], x);
+#pragma unroll
+            for (int j = 0; j < t; ++j)
+                if (!TREE || (above >> (base + j) & 1)) x = fmaf(sign * mine[t][kept + j], u[j], x);
+            u[t] = HAS_Q ? __shfl_sync(0xffffffffu, x, lane & ~1) : x;
+            if (second) {
+                x = fmaf(mine[t][kept + t], u[t], x);
+                uint32_t out = pack_bf16x2(x, 0.0f);
+                if (TREE && sh.kind[base + t] != kNode) out = sh.kind[base + t] == kNoNode ? 0u : 0x7FC0u;
+                p.o[((row + base + t) * p.Hv + h) * D + own] = (uint16_t)out;
+            }
+            if (!(c & 1)) sh.u[warp][kept + t][r * 4 + (c >> 1)] = TREE ? u[t] : sh.left[t] * u[t];
+        }
+        __syncwarp();
+        if constexpr (!TREE) {
+            const float a = sh.fade[cnt - 1];
+            const uint64_t all = pair_of(a, a);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int m = 0; m < 2 * M; ++m) s[i][m] = mul2(s[i][m], all);
+#pragma unroll
+            for (int t = 0; t < kGroup; ++t) {
+                if (t >= cnt) break;
+                const float4 w = *reinterpret_cast<const float4*>(&sh.u[warp][t][r * 4]);
+                const float x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&sh.kn[t][m * 32 + c * 4]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        s[i][2 * m] = fma2(pair_of(x[i], x[i]), k.x, s[i][2 * m]);
+                        s[i][2 * m + 1] = fma2(pair_of(x[i], x[i]), k.y, s[i][2 * m + 1]);
+                    }
+                }
+            }
+        }
+    }
+    if constexpr (!TREE) {
+        if (n == 0 && !p.from_zero) return;  // as it is
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+                *reinterpret_cast<ulonglong2*>(rows + (r + 4 * i) * D + m * 32 + c * 4) =
+                    make_ulonglong2(s[i][2 * m], s[i][2 * m + 1]);
+    }
+}
+
+template <int D, DeltaMode MODE>
+cudaError_t launch_rows(const DeltaParams& p, cudaStream_t st) {
+    const size_t smem = sizeof(Shared<D, MODE>);
+    const void* kernel = reinterpret_cast<const void*>(delta_rows_kernel<D, MODE>);
+    cudaError_t e = ensure_dynamic_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    return launch_chained(delta_rows_kernel<D, MODE>, (unsigned)p.B * p.Hv * (D / (kWarps * kRows)), kThreads, smem, st, p);
+}
+
+}  // namespace
+
+cudaError_t launch_delta(int D, DeltaMode mode, const DeltaParams& p, int sms, cudaStream_t st) {
+    (void)sms;
+    if (mode == kDeltaChain) return D == 64 ? launch_rows<64, kDeltaChain>(p, st) : launch_rows<128, kDeltaChain>(p, st);
+    if (mode == kDeltaTree) return D == 64 ? launch_rows<64, kDeltaTree>(p, st) : launch_rows<128, kDeltaTree>(p, st);
+    return D == 64 ? launch_rows<64, kDeltaCommit>(p, st) : launch_rows<128, kDeltaCommit>(p, st);
+}
+
+}  // namespace r9q

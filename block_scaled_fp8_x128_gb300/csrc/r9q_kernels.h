@@ -195,6 +195,7 @@ struct Kv4AttnParams {
     Kv4Cache c;
     const int32_t* table;        // [B][max_pages]
     const int32_t* lens;         // [B]
+    const int32_t* parents;      // [B][Lq]: the new tokens are a tree; nullptr: they follow one another
     uint16_t* o;                 // [B][Lq][Hq][D] contiguous
     float* lse;                  // [B][Lq][Hq] or nullptr
     float* part;                 // split partials
@@ -210,5 +211,29 @@ size_t kv4_attention_part_floats(int D, int64_t rows, int sms);
 // Workspace bytes of R9Q_OP_QK_NORM_ROPE_BWD and R9Q_OP_KV4_ATTENTION (M rows, N = D).
 size_t decode_workspace(int op, int64_t M, int64_t N, int* rc);
 cudaError_t launch_kv4_attention(int D, const Kv4AttnParams& p, int sms, cudaStream_t st);
+constexpr int kMostNodes = 64;               // of a tree of drafted tokens, of an accepted path
+// Tokens between places of the cache: rows of `per_row` pairs of slots, a row read before it is written.
+cudaError_t launch_kv4_move(int D, const Kv4Cache& c, const int64_t* src, const int64_t* dst, int64_t rows, int per_row,
+                            int* err, cudaStream_t st);
+
+// ---- gated delta rule ----
+struct DeltaParams {
+    const uint16_t *q, *k, *v;   // [tokens][heads][D], last dimension contiguous
+    int64_t q_bs, q_ts, q_hs, k_bs, k_ts, k_hs, v_bs, v_ts, v_hs;
+    const float *g, *beta;       // [tokens][Hv]
+    float* state;                // [n_states][Hv][D values][D keys]
+    uint16_t* o;                 // [tokens][Hv][D]
+    const int32_t* slots;        // [B]
+    const int32_t* cu;           // [B + 1], or nullptr: Lq tokens each
+    const int32_t* parents;      // [B][Lq] (a tree)
+    const int32_t* path;         // [B][P] (an accepted path)
+    int64_t T;
+    int B, Lq, P, Hk, Hv, ratio, n_states;
+    float scale, eps;
+    int from_zero;
+    int* err;
+};
+enum DeltaMode { kDeltaChain, kDeltaTree, kDeltaCommit };
+cudaError_t launch_delta(int D, DeltaMode mode, const DeltaParams& p, int sms, cudaStream_t st);
 
 }  // namespace r9q

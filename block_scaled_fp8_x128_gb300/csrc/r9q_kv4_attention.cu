@@ -54,6 +54,7 @@
 // more than the products save.
 #include <algorithm>
 
+#include "r9q_delta.cuh"
 #include "r9q_kv4_attention.cuh"
 
 namespace r9q {
@@ -79,7 +80,34 @@ constexpr int work_bytes(int D, int NT, Width width) {
     const int w = cta_warps(D, NT, width), R = 8 * NT;
     return largest(largest(w * kStages * stage_bytes(D), w * R * (out_stride(D) + 2) * 4), join_bytes(R, w * 32));
 }
-constexpr int smem_bytes(int D, int NT, Width w) { return work_bytes(D, NT, w) + 16; }   // and a flag
+// and a flag, and a tree's nodes
+constexpr int smem_bytes(int D, int NT, Width w, bool tree) { return work_bytes(D, NT, w) + 16 + (tree ? kMostNodes * 24 : 0); }
+
+// The tree that a sequence's new tokens are: each node's ancestors (as far as its window reaches) with itself, a bit
+// each, its first visible key before the tree, what its rows are where it is not one, and the parents.
+struct Tree {
+    uint64_t mask[kMostNodes];
+    int first[kMostNodes], instead[kMostNodes], parents[kMostNodes];
+    __device__ __forceinline__ Instead operator()(int i) const { return (Instead)instead[i]; }
+};
+static_assert(sizeof(Tree) <= kMostNodes * 24, "shared memory of a tree");
+// By all threads of the CTA, at least Lq of them, between barriers of theirs.
+__device__ __forceinline__ void find_tree(const Kv4AttnParams& p, int b, int base, Tree& tree) {
+    const int i = threadIdx.x;
+    if (i < p.Lq) tree.parents[i] = p.parents[(int64_t)b * p.Lq + i];
+    __syncthreads();
+    if (i < p.Lq) {
+        uint64_t mask;
+        int depth;
+        const NodeKind kind = find_node(tree.parents, i, p.window > 0 ? p.window : kMostNodes, mask, depth);
+        const bool none = base + p.Lq == 0;  // an unused place of the batch: whatever its parents are
+        if (kind == kBadNode && !none) record_error(p.err, kErrArg);
+        tree.mask[i] = mask;
+        tree.first[i] = p.window > 0 && kind == kNode ? base + depth - p.window + 1 : 0;
+        tree.instead[i] = kind == kNode ? kAsItIs : kind == kNoNode || none ? kNothing : kNan;
+    }
+    __syncthreads();
+}
 
 // Transposes an 8x8 matrix of 16-bit values held two to a lane.
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
@@ -102,7 +130,7 @@ template <int D, int NT>
 struct State {
     uint32_t qf[NT][D / 16][2];              // query fragments
     float fr[NT][2], qs[NT][2];              // score = fr (sk acc + lk qs)
-    int hi[NT][2];                           // the last key that the column sees
+    int hi[NT][2];                           // the last key that the column sees; in a tree the token that it is
     float acc[NT][D / 16][4], l[NT][2], ml[NT][2];
     // A weight is 2^((score - top) + shift) with the largest score and the values' exponent of the last move; taken
     // as a difference first, so that it holds for scores of any size.
@@ -167,9 +195,9 @@ __device__ __forceinline__ void move_reference(State<D, NT>& s, const float (&sc
 
 // One step: 32 keys in the stage `st`, of which groups `bits` were loaded.
 // MASKED: some column does not see some key, or a group is missing.
-template <int D, int NT, bool MASKED>
+template <int D, int NT, bool MASKED, bool TREE>
 __device__ __forceinline__ void attend(State<D, NT>& s, const uint8_t* st, int key0, uint32_t bits, int len,
-                                       int window, int lane) {
+                                       int window, int lane, const Tree* tree, int base) {
     constexpr int KW = D / 32;
     const int r = lane >> 2;
     // pairs of the lane's keys r + 8h of group i
@@ -228,7 +256,14 @@ __device__ __forceinline__ void attend(State<D, NT>& s, const uint8_t* st, int k
                 float v = fmaf(bf16_lo(pair), sc[nt][i][c], bf16_hi(pair) * s.qs[nt][c & 1]);
                 if (MASKED) {
                     const int key = key0 + 16 * i + 8 * (c >> 1) + r;
-                    if (key > s.hi[nt][c & 1] || key <= s.hi[nt][c & 1] - window || !((bits >> i) & 1u)) v = kNegInf;
+                    bool seen;
+                    if constexpr (TREE) {
+                        const int node = s.hi[nt][c & 1], at = key - base;
+                        seen = at < 0 ? key >= tree->first[node] : at < kMostNodes && (tree->mask[node] >> at & 1);
+                    } else {
+                        seen = key <= s.hi[nt][c & 1] && key > s.hi[nt][c & 1] - window;
+                    }
+                    if (!seen || !((bits >> i) & 1u)) v = kNegInf;
                 }
                 sc[nt][i][c] = v;
             }
@@ -310,7 +345,7 @@ __device__ __forceinline__ void attend(State<D, NT>& s, const uint8_t* st, int k
     }
 }
 
-template <int D, int NT, Width WIDTH>
+template <int D, int NT, Width WIDTH, bool TREE>
 __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDTH), ctas_per_sm(D, NT, WIDTH))
     kv4_attention_kernel(const Kv4AttnParams p) {
     constexpr int W = cta_warps(D, NT, WIDTH), kThreads = 32 * W;
@@ -322,6 +357,7 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDTH), ctas_per_sm(D, N
     extern __shared__ __align__(16) uint8_t smem[];
     begin_chained();
     int* joins = reinterpret_cast<int*>(smem + work_bytes(D, NT, WIDTH));     // the CTA joins an item's partials
+    Tree* tree = reinterpret_cast<Tree*>(smem + work_bytes(D, NT, WIDTH) + 16);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r = lane >> 2, j = lane & 3;
@@ -351,6 +387,8 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDTH), ctas_per_sm(D, N
             return g < gmax ? find_group(p, table, g, hk) : kNoGroup;
         };
         uint32_t groups_now = 0, groups_next = groups_of(0);
+        const int base = sp.len - p.Lq;      // the first new token's place
+        if constexpr (TREE) find_tree(p, b, base, *tree);
 
         // ---- query fragments and this lane's two columns of every tile ----
         State<D, NT> s;
@@ -411,7 +449,7 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDTH), ctas_per_sm(D, N
                 s.fr[nt][c] = __shfl_sync(0xffffffffu, row_fr, col * 4);
                 s.qs[nt][c] = __shfl_sync(0xffffffffu, row_qs, col * 4);
                 const int ci = min(chunk * R + nt * 8 + col, rows - 1) / p.group;
-                s.hi[nt][c] = sp.len - p.Lq + ci;
+                s.hi[nt][c] = TREE ? ci : base + ci;
                 s.top[nt][c] = s.bound[nt][c] = s.l[nt][c] = s.ml[nt][c] = 0.0f;
                 s.shift[nt][c] = (float)(kHeadroom + 127 - kMinExponent);
             }
@@ -422,7 +460,8 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDTH), ctas_per_sm(D, N
         }
         // keys that all rows of the chunk see
         const int i_first = chunk * R / p.group, i_last = (min(rows, chunk * R + R) - 1) / p.group;
-        const int all_hi = sp.len - p.Lq + i_first, all_lo = p.window > 0 ? sp.len - p.Lq + i_last - p.window + 1 : 0;
+        const int all_hi = TREE ? base - 1 : base + i_first;
+        const int all_lo = p.window > 0 ? base + (TREE ? p.Lq - 1 : i_last) - p.window + 1 : 0;
 
         const int window = p.window > 0 ? p.window : kNoWindow;
         uint32_t have = 0;                   // two bits a step in flight: which of its groups were loaded
@@ -456,9 +495,9 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDTH), ctas_per_sm(D, N
             if (n < 0) continue;
             const int key0 = (g_begin + 2 * (n * W + warp)) << 4;
             if (bits == 3u && key0 >= all_lo && key0 + kStep - 1 <= all_hi)
-                attend<D, NT, false>(s, get, key0, bits, sp.len, window, lane);
+                attend<D, NT, false, TREE>(s, get, key0, bits, sp.len, window, lane, tree, base);
             else
-                attend<D, NT, true>(s, get, key0, bits, sp.len, window, lane);
+                attend<D, NT, true, TREE>(s, get, key0, bits, sp.len, window, lane, tree, base);
             get = get == ring + (ST - 1) * stage_bytes(D) ? ring : get + stage_bytes(D);
         }
         cp_wait<0>();
@@ -494,6 +533,10 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDTH), ctas_per_sm(D, N
         __syncthreads();
 
         const int live = min(R, rows - chunk * R);
+        auto instead = [&](int i) {
+            if constexpr (TREE) return (*tree)(i);
+            return kAsItIs;
+        };
         // a thread takes four elements of every (kThreads / (D / 4))-th row
         const int ed = (tid % (D / 4)) * 4, row0 = tid / (D / 4);
         constexpr int ROWS = kThreads / (D / 4);
@@ -513,7 +556,7 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDTH), ctas_per_sm(D, N
                 x = make_float4(fmaf(k, v.x, x.x), fmaf(k, v.y, x.y), fmaf(k, v.z, x.z), fmaf(k, v.w, x.w));
             }
             if (it.whole) {
-                finish_row<D>(p, it, chunk * R + row, ed, x, sum, top);
+                finish_row<D>(p, it, chunk * R + row, ed, x, sum, top, instead);
             } else {
                 *reinterpret_cast<float4*>(part + row * D + ed) = x;
                 if (ed == 0) {
@@ -532,7 +575,7 @@ __global__ void __launch_bounds__(32 * cta_warps(D, NT, WIDTH), ctas_per_sm(D, N
                 *joins = last;
             }
             __syncthreads();
-            if (*joins) join_partials<D, R, kThreads>(p, it, c0, c1, live, reinterpret_cast<float*>(smem));
+            if (*joins) join_partials<D, R, kThreads>(p, it, c0, c1, live, reinterpret_cast<float*>(smem), instead);
         }
         if (walk.parted) return;
         __syncthreads();                     // the exchange is free for the next item's ring
@@ -558,13 +601,17 @@ int row_tiles(int D, const Kv4AttnParams& p, int sms) {
     return time(1, 1.0f, 24.0f) <= time(2, D == 64 ? 1.74f : 1.62f, D == 64 ? 40.0f : 32.0f) ? 1 : 2;
 }
 
+template <int D, int NT, Width WIDTH, bool TREE>
+cudaError_t launch(const Kv4AttnParams& p, int sms, cudaStream_t st) {
+    const void* kernel = reinterpret_cast<const void*>(kv4_attention_kernel<D, NT, WIDTH, TREE>);
+    cudaError_t e = ensure_dynamic_smem(kernel, smem_bytes(D, NT, WIDTH, TREE));
+    if (e != cudaSuccess) return e;
+    return launch_chained(kv4_attention_kernel<D, NT, WIDTH, TREE>, used_sms(sms) * ctas_per_sm(D, NT, WIDTH),
+                          32 * cta_warps(D, NT, WIDTH), smem_bytes(D, NT, WIDTH, TREE), st, p);
+}
 template <int D, int NT, Width WIDTH>
 cudaError_t launch(const Kv4AttnParams& p, int sms, cudaStream_t st) {
-    const void* kernel = reinterpret_cast<const void*>(kv4_attention_kernel<D, NT, WIDTH>);
-    cudaError_t e = ensure_dynamic_smem(kernel, smem_bytes(D, NT, WIDTH));
-    if (e != cudaSuccess) return e;
-    return launch_chained(kv4_attention_kernel<D, NT, WIDTH>, used_sms(sms) * ctas_per_sm(D, NT, WIDTH),
-                          32 * cta_warps(D, NT, WIDTH), smem_bytes(D, NT, WIDTH), st, p);
+    return p.parents ? launch<D, NT, WIDTH, true>(p, sms, st) : launch<D, NT, WIDTH, false>(p, sms, st);
 }
 
 template <int D, int NT>

@@ -278,11 +278,25 @@ __device__ __forceinline__ uint32_t find_group(const Kv4AttnParams& p, const int
     return kNoGroup;
 }
 
-// Four elements from ed of a row: o = x / sum, and the row's log of the sum of exponentials.
-template <int D>
-__device__ __forceinline__ void finish_row(const Kv4AttnParams& p, const Part& it, int row, int ed, const float4& x,
-                                           float sum, float top) {
+// What a row is to be in place of its sums.
+enum Instead { kAsItIs, kNothing, kNan };
+struct AsItIs {
+    __device__ __forceinline__ Instead operator()(int) const { return kAsItIs; }
+};
+
+// Four elements from ed of a row: o = x / sum, and the row's log of the sum of exponentials.  `instead`: of the row's
+// token.
+template <int D, typename INSTEAD>
+__device__ __forceinline__ void finish_row(const Kv4AttnParams& p, const Part& it, int row, int ed, float4 x,
+                                           float sum, float top, const INSTEAD& instead) {
     const int i = row / p.group;
+    const Instead other = instead(i);
+    if (other == kNothing) {
+        x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        sum = 0.0f;
+    } else if (other == kNan) {
+        x.x = x.y = x.z = x.w = sum = __int_as_float(0x7FC00000);
+    }
     const int64_t out = ((int64_t)it.b * p.Lq + i) * (p.c.heads * p.G) + it.hk * p.G + (row - i * p.G);
     const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
     *reinterpret_cast<uint2*>(p.o + out * D + ed) =
@@ -305,9 +319,9 @@ constexpr int join_bytes(int R, int threads) { return 2 * R * 4 + threads * R * 
 // Joins an item's partials, all threads of the CTA that arrived last: the rows' references and sums over all partials
 // first, then the weighted sum.  The warps that hold a row's elements take every ROWS-th partial each (all the rows'
 // loads in flight) and meet at the end.
-template <int D, int R, int THREADS>
+template <int D, int R, int THREADS, typename INSTEAD>
 __device__ __forceinline__ void join_partials(const Kv4AttnParams& p, const Part& it, int c0, int c1, int live,
-                                              float* smem) {
+                                              float* smem, const INSTEAD& instead) {
     constexpr int ROWS = THREADS / (D / 4);
     const int tid = threadIdx.x, lane = tid & 31, ed = (tid % (D / 4)) * 4, row0 = tid / (D / 4), n = c1 - c0 + 1;
     float *total_m = smem, *total_l = total_m + R, *meet = total_l + R;
@@ -361,7 +375,7 @@ __device__ __forceinline__ void join_partials(const Kv4AttnParams& p, const Part
             const float4 v = *reinterpret_cast<const float4*>(meet + ((size_t)k * R + row) * D + ed);
             y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
         }
-        finish_row<D>(p, it, it.chunk * R + row, ed, y, total_l[row], total_m[row]);
+        finish_row<D>(p, it, it.chunk * R + row, ed, y, total_l[row], total_m[row], instead);
     }
 }
 

@@ -353,6 +353,81 @@ int r9q_kv4_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, c
                       int64_t page, int64_t max_pages, int64_t window, float scale, void* workspace,
                       size_t workspace_bytes, void* stream);
 
+/* Attention of a tree of drafted tokens: as r9q_kv4_attention, with the Lq (at most 64)
+ * new tokens of a sequence of length n being the nodes of a tree that grows from its token
+ * n - Lq - 1.  Their keys and values are the last Lq tokens of the cache, node i at n - Lq + i.
+ *   parents  int32 [B][Lq] on the device: the node that node i comes from, before it (0 .. i - 1),
+ *      or -1 where that is the sequence's own last token; -2: no node (o = 0, lse = -infinity).
+ * Node i sees the tokens before the tree, its ancestors and itself.  Its position is n - Lq + d
+ * with d its ancestors' number, and a window counts positions: the last `window` of that path.
+ * Another parent, or one that leads to no node, sets the device error word to R9Q_ERR_ARG, and the
+ * node's o and lse are NaN; the parents of a sequence of length 0 are not looked at. */
+int r9q_kv4_tree_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, const uint8_t* kc, const void* kp,
+                           const uint8_t* vc, const void* vp, const int32_t* block_table, const int32_t* seq_lens,
+                           const int32_t* parents, void* o, float* lse, int64_t B, int64_t Lq, int64_t Hq, int64_t Hk,
+                           int64_t D, int64_t pages, int64_t page, int64_t max_pages, int64_t window, float scale,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Moves tokens of the cache: in each of `rows` rows of n (at most 64) pairs, the token at slot src
+ * is copied to slot dst (int64 [rows][n] on the device), codes and pairs as they are.  All of a
+ * row is read before any of it is written, so that an accepted path of a tree may close up over the
+ * nodes between; of two tokens that a row moves to one slot the later stays.  Rows may not write
+ * what another row reads or writes.  A negative slot, on either side: the pair is passed over; one
+ * outside the cache: that too, and the device error word is set. */
+int r9q_kv4_move(uint8_t* kc, void* kp, uint8_t* vc, void* vp, const int64_t* src, const int64_t* dst, int64_t rows,
+                 int64_t n, int64_t Hk, int64_t D, int64_t pages, int64_t page, void* stream);
+
+/* ---- The gated delta rule: layers whose memory of a sequence is a matrix a head.  The pages
+ * name such kernels (releases page, v0.2.4 and v0.2.3: sequence, verification and commit of
+ * drafted tokens, one state record a sequence) and define no arithmetic.
+ *
+ * Value head h (of Hv) uses key head h / (Hv / Hk), with keys and queries brought to unit length,
+ * x / sqrt(sum x^2 + eps).  Its state S, fp32 [D values][D keys], goes through a sequence's tokens as
+ *   S <- exp(g) S + u k^T,   u = beta (v - exp(g) S k),   o = scale S q   (the new S).
+ *   q, k  bf16 [tokens][Hk][D], v bf16 [tokens][Hv][D], D = 64 or 128, with free strides as above
+ *   g, beta  fp32 [tokens][Hv] contiguous; g is the log of the decay, at most 0 (-infinity: the state
+ *      is forgotten); beta the rate, 0 to 1, or to 2
+ *   state  fp32 [n_states][Hv][D][D], 16-byte aligned;  slots int32 [B]: each sequence's state.  A
+ *      negative one is a place of the batch without a sequence: its outputs are 0.  One that is out of
+ *      range, or that an earlier sequence of a call that writes states has, sets the device error
+ *      word to R9Q_ERR_ARG; that sequence's outputs are NaN and no state changes for it.
+ *   o  bf16 [tokens][Hv][D] contiguous
+ * States, sums and accumulators are fp32; sum x^2 + eps is to be a normal fp32 number.  What comes from a NaN
+ * or an infinity stays within its sequence and head.  scale > 0, eps >= 0.  None of these needs a workspace,
+ * and no result depends on timing.
+ *
+ * r9q_gated_delta: packed sequences (prompts, or parts of them).  Sequence b has the tokens
+ * cu_seqlens[b] .. cu_seqlens[b + 1] - 1, int32 [B + 1] on the device, of T; tokens of no sequence
+ * are left as they are.  Offsets that decrease or pass T are an error: no tokens.  With R9Q_DELTA_FROM_ZERO
+ * states begin at zero instead of being read. */
+#define R9Q_DELTA_FROM_ZERO 1
+int r9q_gated_delta(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts, int64_t k_hs, const void* v,
+                    int64_t v_ts, int64_t v_hs, const float* g, const float* beta, const int32_t* cu_seqlens,
+                    const int32_t* slots, float* state, void* o, int64_t T, int64_t B, int64_t Hk, int64_t Hv, int64_t D,
+                    int64_t n_states, float scale, float eps, int flags, void* stream);
+
+/* The Lq newest tokens of each of B sequences: q, k [B][Lq][Hk][D], v, o [B][Lq][Hv][D], g, beta [B][Lq][Hv]. */
+int r9q_gated_delta_step(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_bs,
+                         int64_t k_ts, int64_t k_hs, const void* v, int64_t v_bs, int64_t v_ts, int64_t v_hs,
+                         const float* g, const float* beta, const int32_t* slots, float* state, void* o, int64_t B,
+                         int64_t Lq, int64_t Hk, int64_t Hv, int64_t D, int64_t n_states, float scale, float eps,
+                         int flags, void* stream);
+
+/* Drafted tokens: the Lq (at most 64) tokens of each sequence are the nodes of a tree, with parents as for
+ * r9q_kv4_tree_attention; a node's state comes from its parent's, or from the sequence's.  Only outputs are written;
+ * r9q_gated_delta_commit takes the state on along an accepted path: path int32 [B][P] (P at most 64) on the
+ * device, nodes from the tree's beginning on, until the first negative one.  A node of Lq or more is an error,
+ * and ends the path too. */
+int r9q_gated_delta_tree(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_bs,
+                         int64_t k_ts, int64_t k_hs, const void* v, int64_t v_bs, int64_t v_ts, int64_t v_hs,
+                         const float* g, const float* beta, const int32_t* parents, const int32_t* slots,
+                         const float* state, void* o, int64_t B, int64_t Lq, int64_t Hk, int64_t Hv, int64_t D,
+                         int64_t n_states, float scale, float eps, void* stream);
+int r9q_gated_delta_commit(const void* k, int64_t k_bs, int64_t k_ts, int64_t k_hs, const void* v, int64_t v_bs,
+                           int64_t v_ts, int64_t v_hs, const float* g, const float* beta, const int32_t* path,
+                           const int32_t* slots, float* state, int64_t B, int64_t Lq, int64_t P, int64_t Hk, int64_t Hv,
+                           int64_t D, int64_t n_states, float eps, void* stream);
+
 /* Writes the id of the capture that `stream` is part of to *id, 0 where it is not being
  * captured.  For callers that keep workspaces by stream: a captured graph keeps the
  * address of a workspace, so it needs one of its own, zeroed inside the capture. */
