@@ -494,8 +494,8 @@ static int gated_delta(DeltaMode mode, const void* q, int64_t q_bs, int64_t q_ts
     for (int i = 0; i < reads; ++i)
         if (meet(read[i], out) || (mode != kDeltaTree && meet(read[i], states))) return R9Q_ERR_ARG;
     if (meet(states, out)) return R9Q_ERR_ARG;
-    int *err = nullptr, sms = 0;
-    const int rc = device_error_word_and_sms(&err, &sms);
+    int* err = nullptr;
+    const int rc = device_error_word(&err);
     if (rc) return rc;
     DeltaParams p = {};
     p.q = static_cast<const uint16_t*>(q);
@@ -530,7 +530,7 @@ static int gated_delta(DeltaMode mode, const void* q, int64_t q_bs, int64_t q_ts
     p.eps = eps;
     p.from_zero = flags & R9Q_DELTA_FROM_ZERO ? 1 : 0;
     p.err = err;
-    return status(launch_delta((int)D, mode, p, sms, static_cast<cudaStream_t>(stream)));
+    return status(launch_delta((int)D, mode, p, static_cast<cudaStream_t>(stream)));
 }
 
 int r9q_gated_delta(const void* q, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_ts, int64_t k_hs, const void* v,

@@ -293,8 +293,9 @@ cudaError_t launch_rows(const DeltaParams& p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_delta(int D, DeltaMode mode, const DeltaParams& p, int sms, cudaStream_t st) {
-    (void)sms;
+cudaError_t launch_delta(int D, DeltaMode mode, const DeltaParams& p, cudaStream_t st) {
+    // (packed sequences of a token each are steps)
+    if (mode == kDeltaCommit ? p.P > kGroup : p.cu ? p.T > p.B : p.Lq > kGroup) return launch_delta_chunks(D, mode, p, st);
     if (mode == kDeltaChain) return D == 64 ? launch_rows<64, kDeltaChain>(p, st) : launch_rows<128, kDeltaChain>(p, st);
     if (mode == kDeltaTree) return D == 64 ? launch_rows<64, kDeltaTree>(p, st) : launch_rows<128, kDeltaTree>(p, st);
     return D == 64 ? launch_rows<64, kDeltaCommit>(p, st) : launch_rows<128, kDeltaCommit>(p, st);

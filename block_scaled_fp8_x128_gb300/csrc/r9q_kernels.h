@@ -234,6 +234,8 @@ struct DeltaParams {
     int* err;
 };
 enum DeltaMode { kDeltaChain, kDeltaTree, kDeltaCommit };
-cudaError_t launch_delta(int D, DeltaMode mode, const DeltaParams& p, int sms, cudaStream_t st);
+cudaError_t launch_delta(int D, DeltaMode mode, const DeltaParams& p, cudaStream_t st);
+// Many tokens a sequence, in chunks on the tensor cores.
+cudaError_t launch_delta_chunks(int D, DeltaMode mode, const DeltaParams& p, cudaStream_t st);
 
 }  // namespace r9q
