@@ -5,21 +5,24 @@
 // products is value element v and belongs to one thread: with S [D values][D keys] as the
 // accumulator in tensor memory, for each chunk of keys K, queries Q [64][D]
 //   W = S K^T, Y = S Q^T         [D values][64 tokens]
-//   x_i = beta_i (v_i - A(i, 0) W_i),  u_i = x_i - sum_{j<i} L_ij u_j   (each thread its row, in fp32)
+//   X_i = beta_i (v_i - A(i, 0) W_i),  U = X T^T,  T = (1 + L)^-1
 //   O = A(., 0) Y + U P^T,  S <- A(n, 0) S + (A(n, .) U) K
 // with L_ij = beta_i A(i, j) (k_i.k_j), P_ij = A(i, j) (q_i.k_j) from one product [K; Q] K^T.
 // Keys and queries are the bf16 inputs themselves (exact operands); their lengths go into L, P and
-// the scalars.  What is fp32 (S, u) is an operand in bf16 parts, cut off, not rounded: three parts
+// the scalars.  What is fp32 (S, X, T, u) is an operand in bf16 parts, cut off, not rounded: three parts
 // hold all 24 bits and keep fp32's range, so that nothing needs a scale and a
 // token's values, however large, do not touch those of earlier tokens.  Three parts for what
 // goes into S and u, two (2^-16) where only outputs, which are rounded to bf16, follow.
 //
-// Warps 0-3: the rows.  Warps 4-7: the tokens; they copy K, Q, V (a chunk ahead), and form L and P
-// of the next chunk while the rows work on this one.  Warp 8 issues the products.  In a tree the sums
+// Warps 0-3, the rows: S, X and u into parts, the chain that bounds a sequence's time.  Warps 4-7, the
+// tokens: K, Q, V are copied a chunk ahead, and L and P of the next chunk formed.  Warps 8-11 turn
+// L into T, in fp32 by blocks of 16, 32 and 64 (as a substitution a row's thread would need all of L
+// in its registers: 8300 cycles of shared memory's 128 bytes each for the four warps).  Warps 12-15 write the
+// outputs of the chunk before.  Warp 16 issues the products.  In a tree the sums
 // go over ancestors, and its one chunk leaves the state alone.
 //
-// A value that is not finite would reach earlier tokens (or other branches) through the zeros of P,
-// so u is an operand with zeros in its place, and the outputs that it belongs to are NaN.
+// A value that is not finite would reach earlier tokens (or other branches) through the zeros of T and P.
+// So L's rows, X and u are zero in its place, and the outputs that it belongs to are NaN, as is the state's row.
 #include <cfloat>
 
 #include "r9q_delta.cuh"
@@ -29,17 +32,22 @@ namespace r9q {
 namespace {
 
 constexpr int kChunk = 64;
-constexpr int kRowThreads = 128, kTokenThreads = 128, kThreads = kRowThreads + kTokenThreads + 32;
+constexpr int kGroup = 128;                  // threads of each of the four groups
+constexpr int kThreads = 4 * kGroup + 32;
 constexpr int kLStride = 68;                 // floats between rows of L: eight rows' 16-byte pieces lie in different banks
+constexpr int kMStride = 36;
 
 // Scalars of a chunk's tokens.
 struct Scalars {
-    float r_k[kChunk], r_q[kChunk];          // 1 / length; r_q times the scale
-    float beta[kChunk], fade[kChunk], left[kChunk];          // fade A(i, 0), left A(n, i)
-    float hi[kChunk], lo[kChunk];            // sums of the decays' logarithms to base 2
-    uint64_t above[kChunk];
+    float2 x[kChunk];                        // X = x.x v - x.y W
+    float2 o[kChunk];                        // o = o.x Y + o.y (U P^T)
+    float last[kChunk];                      // A(n, i) / |k_i|
+    float4 decay[kChunk];                    // two parts of the sum of the decays' logarithms (to base 2), 1 / |k|
+    uint64_t above[kChunk], lost[kGroup];    // (of a tree); tokens without a finite u, by row
     int parents[kChunk];
     NodeKind kind[kChunk];
+    uint32_t bad[2];                         // tokens whose row of L is not finite
+    float end;                               // A(n, 0)
 };
 
 template <int D>
@@ -48,19 +56,23 @@ struct Layout {
     static constexpr int kTile = 64 * 128;                   // 64 rows of 128 bytes, swizzled
     static constexpr int kKq = kHalves * 2 * kTile;          // of each 64 elements: K's rows, then Q's
     static constexpr int kInput = kKq + kChunk * D * 2;      // and V [64][D]
-    static constexpr int kL = kChunk * kLStride * 4;
-    static constexpr int kP = 2 * kTile;                     // its two parts
-    static constexpr int kPairs = (kL + kP + (int)sizeof(Scalars) + 1023) / 1024 * 1024;
-    static constexpr int kBytes = 2 * kInput + 2 * kPairs;
-    // tensor memory, columns
-    static constexpr int kS = 0, kParts = D, kW = kParts + 3 * D / 2, kY = kW + 64, kG = kY + 64;
-    static constexpr int kU = kParts, kUleft = kParts + 64;  // u's two parts and (A(n, .) u)'s three, after S's
-    static_assert(kG + 64 <= 512 && kUleft + 96 <= kW + (D == 64 ? 64 : 0), "tensor memory");
+    static constexpr int kP = 2 * kInput;                    // twice P's two parts
+    static constexpr int kT = kP + 4 * kTile;                // twice T's three
+    static constexpr int kL = kT + 6 * kTile;
+    static constexpr int kM = kL + kChunk * kLStride * 4;
+    static constexpr int kScalars = kM + 32 * kMStride * 4;
+    static constexpr int kBars = kScalars + 2 * (int)sizeof(Scalars);
+    // tensor memory, columns.  S's parts are 64 columns apart; X's third takes a place that W alone reads (of S's
+    // third), U that of S's first.  What is read by 32 tokens, W and U, is replaced by two parts of them: of tokens
+    // 32 i on in the columns 32 i and 32 i + 16 on.
+    static constexpr int kS = 0, kParts = 128, kW = kParts + 192, kY = kW + 64, kG = kY + 64;
+    static constexpr int kX2 = kParts + 128, kU = kParts, kUleft = kParts + 64;
+    static_assert(kG + 64 == 512, "tensor memory");
 };
 
 struct Barriers {
-    uint64_t input_full[2], input_free[2], gram_full, gram_read, pairs_full[2], pairs_free[2], s_ready, w_full, y_full,
-        u_ready, s_full, o_full, o_read;
+    uint64_t input_full[2], input_free[2], gram_full, gram_read, pairs_full[2], pairs_free[2], l_free, t_full[2], s_ready,
+        w_full, y_full, x_ready, u_full, u_ready, s_full, o_full, o_read;
     uint32_t tmem;
     int failed;                              // a wait gave up
 };
@@ -122,7 +134,37 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ void token_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Of one group's threads.
+template <int ID>
+__device__ __forceinline__ void group_barrier() {
+    asm volatile("bar.sync %0, 128;" ::"n"(ID) : "memory");
+}
+// The next part of 32 values, two a column.
+__device__ __forceinline__ void take_parts(uint32_t (&y)[16], float (&x)[32]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = take_part(x[2 * i], x[2 * i + 1]);
+}
+__device__ __forceinline__ void store_part(uint32_t taddr, float (&x)[32]) {
+    uint32_t y[16];
+    take_parts(y, x);
+    tmem_st16(taddr, y);
+}
+// The tokens (a bit each) among 32 from t0 on whose value is not finite; those become zero.
+__device__ __forceinline__ uint32_t not_finite(float (&x)[32]) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum = fmaf(x[i], 0.0f, sum);
+    uint32_t m = 0;
+    if (sum != 0.0f) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (!(fabsf(x[i]) <= FLT_MAX)) {
+                m |= 1u << i;
+                x[i] = 0.0f;
+            }
+    }
+    return m;
+}
 
 // Bounded; after one that gave up all others do at once.
 struct Waits {
@@ -144,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
     constexpr int KS = D / 16;               // steps of a product over the keys' elements
     extern __shared__ uint8_t raw[];
     begin_chained();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = tid & (kGroup - 1);
     const int b = blockIdx.x / p.Hv, h = blockIdx.x - b * p.Hv, hk = h / p.ratio;
     int n;
     int64_t row0;
@@ -175,44 +217,46 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
     }
     const int chunks = (n + kChunk - 1) / kChunk;
     uint8_t* smem = raw + (1024u - smem_u32(raw) % 1024u) % 1024u;
-    Barriers& bars = *reinterpret_cast<Barriers*>(smem + Y::kBytes);
+    Barriers& bars = *reinterpret_cast<Barriers*>(smem + Y::kBars);
+    float* const L = reinterpret_cast<float*>(smem + Y::kL);
     auto input = [&](int c) { return smem + (c & 1) * Y::kInput; };
-    auto l_of = [&](int c) { return reinterpret_cast<float*>(smem + 2 * Y::kInput + (c & 1) * Y::kPairs + Y::kP); };
-    auto p_of = [&](int c) { return smem + 2 * Y::kInput + (c & 1) * Y::kPairs; };
-    auto scalars_of = [&](int c) {
-        return reinterpret_cast<Scalars*>(smem + 2 * Y::kInput + (c & 1) * Y::kPairs + Y::kP + Y::kL);
-    };
+    auto p_of = [&](int c) { return smem + Y::kP + (c & 1) * 2 * Y::kTile; };
+    auto t_of = [&](int c) { return smem + Y::kT + (c & 1) * 3 * Y::kTile; };
+    auto scalars_of = [&](int c) { return reinterpret_cast<Scalars*>(smem + Y::kScalars) + (c & 1); };
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.input_full[i], kTokenThreads);
+            mbar_init(&bars.input_full[i], kGroup);
             mbar_init(&bars.input_free[i], 1);
-            mbar_init(&bars.pairs_full[i], kTokenThreads);
-            mbar_init(&bars.pairs_free[i], kRowThreads);
+            mbar_init(&bars.pairs_full[i], kGroup);
+            mbar_init(&bars.pairs_free[i], kGroup);
+            mbar_init(&bars.t_full[i], kGroup);
         }
         mbar_init(&bars.gram_full, 1);
-        mbar_init(&bars.gram_read, kTokenThreads);
-        mbar_init(&bars.s_ready, kRowThreads);
+        mbar_init(&bars.gram_read, kGroup);
+        mbar_init(&bars.l_free, kGroup);
+        mbar_init(&bars.s_ready, kGroup);
         mbar_init(&bars.w_full, 1);
         mbar_init(&bars.y_full, 1);
-        mbar_init(&bars.u_ready, kRowThreads);
+        mbar_init(&bars.x_ready, kGroup);
+        mbar_init(&bars.u_full, 1);
+        mbar_init(&bars.u_ready, kGroup);
         mbar_init(&bars.s_full, 1);
         mbar_init(&bars.o_full, 1);
-        mbar_init(&bars.o_read, kRowThreads);
+        mbar_init(&bars.o_read, kGroup);
         bars.failed = 0;
         fence_mbar_init();
     }
-    if (warp == 8) tmem_alloc(&bars.tmem, 512);
+    if (warp == 16) tmem_alloc(&bars.tmem, 512);
     umma_fence_before();
     __syncthreads();
     umma_fence_after();
-    const uint32_t tmem = bars.tmem;
+    const uint32_t tmem = bars.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const Waits wait = {&bars.failed, p.err};
 
     if (warp < 4) {
         // ---------------------------------------------------------------- rows --
-        const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);
-        const bool live = tid < D;           // (D = 64: the other half of the lanes is zeros)
-        float* row = state + (int64_t)tid * D;
+        const bool live = t < D;             // (D = 64: the other half of the lanes is zeros)
+        float* row = state + (int64_t)t * D;
 #pragma unroll 1
         for (int e = 0; e < D; e += 16) {
             uint32_t x[16];
@@ -227,48 +271,16 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             tmem_st16(mine + Y::kS + e, x);
         }
         tmem_wait_st();
-        uint64_t lost = 0;                   // tokens whose u is not finite
-        uint64_t before = 0;                 // that of the chunk whose outputs are due
-        auto outputs = [&](int c) {
-            const Scalars& sc = *scalars_of(c);
-            wait(&bars.o_full, c & 1);
-            umma_fence_after();
-#pragma unroll 1
-            for (int t0 = 0; t0 < kChunk; t0 += 16) {
-                float y[16], z[16];
-                tmem_ld(mine + Y::kY + t0, y);
-                tmem_ld(mine + Y::kG + t0, z);
-                tmem_wait_ld(y);
-                tmem_wait_ld(z);
-                if (t0 == kChunk - 16) {
-                    umma_fence_before();
-                    mbar_arrive(&bars.o_read);
-                }
-                if (!live) continue;
-#pragma unroll
-                for (int t = 0; t < 16; ++t) {
-                    const int i = t0 + t, token = c * kChunk + i;
-                    if (token >= n) break;
-                    float o = sc.r_q[i] * fmaf(sc.fade[i], y[t], z[t]);
-                    uint32_t out = pack_bf16x2(o, 0.0f);
-                    if (before && (TREE ? (before & sc.above[i]) != 0 : (before & (~0ull >> (63 - i))) != 0)) out = 0x7FC0u;
-                    if (TREE && sc.kind[i] != kNode) out = sc.kind[i] == kNoNode ? 0u : 0x7FC0u;
-                    p.o[((row0 + token) * p.Hv + h) * D + tid] = (uint16_t)out;
-                }
-            }
-        };
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             wait(&bars.pairs_full[c & 1], (c >> 1) & 1);
-            const Scalars& sc = *scalars_of(c);
-            const float* L = l_of(c);
+            Scalars& sc = *scalars_of(c);
             if (c > 0) {
                 wait(&bars.s_full, (c - 1) & 1);
-                if (HAS_Q) wait(&bars.o_full, (c - 1) & 1);  // (u's parts, which it reads, make room for S's)
                 umma_fence_after();
             }
             // S into its parts, and what is left of it at the chunk's end
-            const float left = sc.fade[kChunk - 1];
+            const float left = sc.end;
 #pragma unroll 1
             for (int e = 0; e < D; e += 32) {
                 float s[32];
@@ -283,126 +295,87 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                         tmem_st16(mine + Y::kS + e + half * 16, x);
                     }
                 }
-#pragma unroll
-                for (int part = 0; part < 3; ++part) {
-                    uint32_t x[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = take_part(s[2 * i], s[2 * i + 1]);
-                    tmem_st16(mine + Y::kParts + part * (D / 2) + e / 2, x);
+                uint32_t first[16];
+                take_parts(first, s);
+                store_part(mine + Y::kParts + 64 + e / 2, s);
+                store_part(mine + Y::kParts + 128 + e / 2, s);
+                if (HAS_Q && e == 0 && c > 0) {              // (u's parts, that the last outputs come from, are there)
+                    wait(&bars.o_full, (c - 1) & 1);
+                    umma_fence_after();
                 }
+                tmem_st16(mine + Y::kParts + e / 2, first);
             }
             tmem_wait_st();
             umma_fence_before();
             mbar_arrive(&bars.s_ready);
-            if (HAS_Q && c > 0) {
-                outputs(c - 1);
-                mbar_arrive(&bars.pairs_free[(c - 1) & 1]);
-            } else if (c > 0) {
-                mbar_arrive(&bars.pairs_free[(c - 1) & 1]);
-            }
 
-            // ---- x, then u ----
+            // ---- X ----
             wait(&bars.w_full, c & 1);
             umma_fence_after();
-            uint64_t u[kChunk / 2];
-            const uint16_t* v = reinterpret_cast<const uint16_t*>(input(c) + Y::kKq) + (live ? tid : 0);
-#pragma unroll
+            const uint16_t* v = reinterpret_cast<const uint16_t*>(input(c) + Y::kKq) + (live ? t : 0);
+            uint64_t lost = 0;
+#pragma unroll 1
             for (int t0 = 0; t0 < kChunk; t0 += 32) {
-                float w[32];
-                tmem_ld(mine + Y::kW + t0, w);
-                tmem_wait_ld(w);
+                float x[32];
+                tmem_ld(mine + Y::kW + t0, x);
+                tmem_wait_ld(x);
 #pragma unroll
-                for (int t = 0; t < 32; t += 2) {
-                    float x[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int j = t0 + t + i;
-                        const float val = live ? bf16_lo(v[j * D]) : 0.0f;
-                        x[i] = sc.beta[j] * fmaf(-sc.fade[j] * sc.r_k[j], w[t + i], val);
-                    }
-                    u[(t0 + t) / 2] = pair_of(x[0], x[1]);
+                for (int i = 0; i < 32; i += 2) {
+                    const float4 f = *reinterpret_cast<const float4*>(&sc.x[t0 + i]);
+                    x[i] = fmaf(f.x, bf16_lo(v[(t0 + i) * D]), -f.y * x[i]);
+                    x[i + 1] = fmaf(f.z, bf16_lo(v[(t0 + i + 1) * D]), -f.w * x[i + 1]);
                 }
+                lost |= (uint64_t)not_finite(x) << t0;
+                store_part(mine + Y::kW + t0, x);
+                store_part(mine + Y::kW + t0 + 16, x);
+                store_part(mine + Y::kX2 + t0 / 2, x);
             }
-            lost = 0;
-#pragma unroll
-            for (int i = 0; i < kChunk; ++i) {
-                uint64_t s0 = 0, s1 = 0;
-#pragma unroll
-                for (int j = 0; j < i; j += 4) {             // (L is zero from the diagonal on)
-                    const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(L + i * kLStride + j);
-                    s0 = fma2(l.x, u[j / 2], s0);
-                    if (j + 2 < i) s1 = fma2(l.y, u[j / 2 + 1], s1);
-                }
-                const float2 a = parts_of(s0), d = parts_of(s1), old = parts_of(u[i / 2]);
-                float x = (i & 1 ? old.y : old.x) - ((a.x + a.y) + (d.x + d.y));
-                if constexpr (TREE) {        // another branch is not to get it through a zero of L
-                    if (!(fabsf(x) <= FLT_MAX) || (lost & sc.above[i])) {
-                        lost |= 1ull << i;
-                        x = 0.0f;
+            tmem_wait_st();
+            umma_fence_before();
+            mbar_arrive(&bars.x_ready);
+
+            // ---- u, as an operand ----
+            wait(&bars.u_full, c & 1);
+            umma_fence_after();
+            lost |= *reinterpret_cast<const uint64_t*>(sc.bad);
+#pragma unroll 1
+            for (int t0 = 0; t0 < kChunk; t0 += 32) {
+                float u[32];
+                tmem_ld(mine + Y::kU + t0, u);
+                tmem_wait_ld(u);
+                lost |= (uint64_t)not_finite(u) << t0;
+                if (lost) {                  // with what comes from such a token
+                    if constexpr (TREE) {
+                        for (int i = 0; i < kChunk; ++i)
+                            if (sc.above[i] & lost) lost |= 1ull << i;
+                    } else {
+                        lost = ~0ull << (__ffsll((long long)lost) - 1);
                     }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (lost >> (t0 + i) & 1) u[i] = 0.0f;
                 }
-                u[i / 2] = i & 1 ? pair_of(old.x, x) : pair_of(x, old.y);
-            }
-            if constexpr (!TREE) {
-                uint64_t any = 0;
-#pragma unroll
-                for (int i = 0; i < kChunk / 2; ++i) any = fma2(u[i], 0ull, any);
-                const float2 a = parts_of(any);
-                if (!(a.x == 0.0f && a.y == 0.0f)) {
-#pragma unroll
-                    for (int i = 0; i < kChunk; ++i) {
-                        const float2 x = parts_of(u[i / 2]);
-                        if (!(fabsf(i & 1 ? x.y : x.x) <= FLT_MAX)) lost |= 1ull << i;
-                    }
-                }
-            }
-            before = lost;
-            // ---- u as an operand, in place of S's parts ----
-            if constexpr (HAS_Q) {
-                wait(&bars.y_full, c & 1);
-                umma_fence_after();
-#pragma unroll
-                for (int t0 = 0; t0 < kChunk; t0 += 32) {
+                if constexpr (!TREE) {
                     float x[32];
 #pragma unroll
-                    for (int t = 0; t < 16; ++t) {
-                        const float2 f = parts_of(u[t0 / 2 + t]);
-                        x[2 * t] = f.x;
-                        x[2 * t + 1] = f.y;
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(&sc.last[t0 + i]);
+                        x[i] = f.x * u[i];
+                        x[i + 1] = f.y * u[i + 1];
+                        x[i + 2] = f.z * u[i + 2];
+                        x[i + 3] = f.w * u[i + 3];
                     }
-                    if (lost) {
-#pragma unroll
-                        for (int t = 0; t < 32; ++t)
-                            if (lost >> (t0 + t) & 1) x[t] = 0.0f;
-                    }
-#pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        uint32_t y[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = take_part(x[2 * i], x[2 * i + 1]);
-                        tmem_st16(mine + Y::kU + part * 32 + t0 / 2, y);
-                    }
+                    if (lost >> (t0 + 31) & 1) x[31] = __int_as_float(0x7FC00000);               // into the state
+                    store_part(mine + Y::kUleft + t0 / 2, x);
+                    store_part(mine + Y::kUleft + 32 + t0 / 2, x);
+                    store_part(mine + Y::kUleft + 64 + t0 / 2, x);
+                }
+                if constexpr (HAS_Q) {
+                    store_part(mine + Y::kU + t0, u);
+                    store_part(mine + Y::kU + t0 + 16, u);
                 }
             }
-            if constexpr (!TREE) {
-#pragma unroll
-                for (int t0 = 0; t0 < kChunk; t0 += 32) {
-                    float x[32];
-#pragma unroll
-                    for (int t = 0; t < 16; ++t) {
-                        const float2 f = parts_of(u[t0 / 2 + t]);
-                        x[2 * t] = f.x * (sc.left[t0 + 2 * t] * sc.r_k[t0 + 2 * t]);
-                        x[2 * t + 1] = f.y * (sc.left[t0 + 2 * t + 1] * sc.r_k[t0 + 2 * t + 1]);
-                    }
-#pragma unroll
-                    for (int part = 0; part < 3; ++part) {
-                        uint32_t y[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = take_part(x[2 * i], x[2 * i + 1]);
-                        tmem_st16(mine + Y::kUleft + part * 32 + t0 / 2, y);
-                    }
-                }
-            }
+            sc.lost[t] = lost;
             tmem_wait_st();
             umma_fence_before();
             mbar_arrive(&bars.u_ready);
@@ -421,29 +394,33 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                         reinterpret_cast<float4*>(row + e)[i] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
             }
         }
-        if constexpr (HAS_Q) outputs(chunks - 1);
     } else if (warp < 8) {
         // -------------------------------------------------------------- tokens --
-        const int t = tid - kRowThreads;     // row of [K; Q]
-        const int i = t & 63;
+        const int i = t & 63;                // row of K or of Q
         const bool key = t < 64;
-        const uint32_t mine = tmem + ((uint32_t)((warp - 4) * 32) << 16);
+        // token `at` of the sequence: in K, Q and V, and in g and beta
         auto place = [&](int at) { return MODE == kDeltaCommit ? (int64_t)path[at] : (p.cu ? row0 : 0) + at; };
+        auto rate_of = [&](int at) {
+            return ((MODE == kDeltaCommit ? row0 + path[at] : row0 + at)) * p.Hv + h;
+        };
+        // a thread copies the same 16 bytes of every 128 / (D/8)-th token
+        constexpr int PIECES = D / 8, STEP = kGroup / PIECES;
+        const int piece = t % PIECES, r0 = t / PIECES;
+        const uint32_t tile = (uint32_t)(piece >> 3) * (2 * Y::kTile);
+        const uint16_t* kp = p.k + b * p.k_bs + hk * p.k_hs + piece * 8;
+        const uint16_t* qp = HAS_Q ? p.q + b * p.q_bs + hk * p.q_hs + piece * 8 : nullptr;
+        const uint16_t* vp = p.v + b * p.v_bs + h * p.v_hs + piece * 8;
         auto load = [&](int c) {
             const uint32_t base = smem_u32(input(c));
 #pragma unroll 4
-            for (int x = t; x < 3 * kChunk * (D / 8); x += kTokenThreads) {
-                const int which = x / (kChunk * (D / 8)), y = x % (kChunk * (D / 8)), r = y / (D / 8), piece = y % (D / 8);
-                if (!HAS_Q && which == 1) continue;          // (a commit's Q: rows that nothing uses)
+            for (int r = r0; r < kChunk; r += STEP) {
                 const int at = c * kChunk + r;
-                const int64_t token = at < n ? place(at) : 0;
-                const uint16_t* src = which == 0   ? p.k + b * p.k_bs + token * p.k_ts + hk * p.k_hs
-                                      : which == 1 ? p.q + b * p.q_bs + token * p.q_ts + hk * p.q_hs
-                                                   : p.v + b * p.v_bs + token * p.v_ts + h * p.v_hs;
-                const uint32_t dst = which == 2 ? Y::kKq + r * (D * 2) + piece * 16
-                                                : (piece >> 3) * (2 * Y::kTile) + which * Y::kTile + r * 128 +
-                                                      (((piece & 7) ^ (r & 7)) << 4);
-                copy16(base + dst, at < n ? src + piece * 8 : p.k, at < n);
+                const bool here = at < n;
+                const int64_t token = here ? place(at) : 0;
+                const uint32_t swizzled = tile + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+                copy16(base + swizzled, here ? kp + token * p.k_ts : p.k, here);
+                if (HAS_Q) copy16(base + Y::kTile + swizzled, here ? qp + token * p.q_ts : p.k, here);
+                copy16(base + Y::kKq + r * (D * 2) + piece * 16, here ? vp + token * p.v_ts : p.k, here);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
@@ -452,69 +429,50 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             fence_proxy_async_smem();
             mbar_arrive(&bars.input_full[c & 1]);
         };
+        float g_next = 0.0f, beta_next = 0.0f;
+        auto load_rates = [&](int c) {       // ahead of their use
+            const int at = c * kChunk + i;
+            g_next = at < n ? p.g[rate_of(at)] : 0.0f;
+            beta_next = key && at < n ? p.beta[rate_of(at)] : 0.0f;
+        };
         // L, P and the scalars of chunk c
         auto pairs = [&](int c) {
             Scalars& sc = *scalars_of(c);
-            if (c >= 2) wait(&bars.pairs_free[c & 1], ((c - 2) >> 1) & 1);
             const int at = c * kChunk + i;
-            float g = 0.0f;
-            if (at < n) {
-                const int64_t x = ((MODE == kDeltaCommit ? row0 : p.cu ? 0 : row0) + place(at)) * p.Hv + h;
-                g = p.g[x];
-                if (key) sc.beta[i] = p.beta[x];
-            } else if (key) {
-                sc.beta[i] = 0.0f;
-            }
-            g = g < -200.0f ? -200.0f : g;   // (exp is 0 there; infinities have no differences)
+            const float beta = beta_next, g = g_next < -200.0f ? -200.0f : g_next;   // (exp is 0 there; infinities have no differences)
+            if (c + 1 < chunks) load_rates(c + 1);
+            if (c >= 2) wait(&bars.pairs_free[c & 1], ((c - 2) >> 1) & 1);
+            uint64_t above = ~0ull >> (63 - i);
+            double sum = 0.0, end = 0.0;
             if constexpr (TREE) {
                 if (key) {
-                    sc.hi[i] = g;
+                    sc.last[i] = g;
                     sc.parents[i] = at < n ? p.parents[(int64_t)b * p.Lq + at] : -2;
                 }
-                token_barrier();
-                if (key) {
-                    int depth;
-                    const NodeKind kind = find_node(sc.parents, i, kMostNodes, sc.above[i], depth);
-                    if (kind == kBadNode) record_error(p.err, kErrArg);
-                    if (kind != kNode) sc.above[i] = 0;
-                    sc.kind[i] = kind;
-                    double sum = 0.0;
-                    for (uint64_t m = sc.above[i]; m; m &= m - 1) sum += (double)sc.hi[__ffsll((long long)m) - 1];
-                    sum *= 1.4426950408889634;
-                    token_barrier();
-                    sc.hi[i] = (float)sum;
-                    sc.lo[i] = (float)(sum - (double)sc.hi[i]);
-                    sc.fade[i] = ex2(sc.hi[i]);
-                } else {
-                    token_barrier();
-                }
-            } else if (warp == 4) {          // two tokens a lane
-                const int a = c * kChunk + 2 * lane;
-                double x[2];
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    float gy = a + y < n ? p.g[((MODE == kDeltaCommit ? row0 : p.cu ? 0 : row0) + place(a + y)) * p.Hv + h] : 0.0f;
-                    x[y] = (double)(gy < -200.0f ? -200.0f : gy) * 1.4426950408889634;
-                }
-                double sum = x[0] + x[1];
+                group_barrier<1>();
+                int depth;
+                const NodeKind kind = find_node(sc.parents, i, kMostNodes, above, depth);
+                if (kind == kBadNode && key) record_error(p.err, kErrArg);
+                if (kind != kNode) above = 0;
+                sc.kind[i] = kind;
+                sc.above[i] = above;
+                for (uint64_t m = above; m; m &= m - 1) sum += (double)sc.last[__ffsll((long long)m) - 1];
+                sum *= 1.4426950408889634;
+            } else {                         // a scan over the 64 tokens, whole in each pair of warps
+                sum = (double)g * 1.4426950408889634;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const double y = __shfl_up_sync(0xffffffffu, sum, o);
                     if (lane >= o) sum += y;
                 }
-                const double end = __shfl_sync(0xffffffffu, sum, 31), first = sum - x[1];
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const double z = y ? sum : first;
-                    const int at2 = 2 * lane + y;
-                    sc.hi[at2] = (float)z;
-                    sc.lo[at2] = (float)(z - (double)(float)z);
-                    sc.fade[at2] = ex2((float)z);
-                    sc.left[at2] = ex2((float)(end - z));
-                }
+                double* halves = reinterpret_cast<double*>(sc.parents);      // (a tree's)
+                if (lane == 31) halves[warp & 3] = sum;
+                group_barrier<1>();
+                end = halves[0] + halves[1];
+                if (i >= 32) sum += halves[0];
             }
             // the row's length
-            float sum = 0.0f;
+            float square = 0.0f;
             if (key || HAS_Q) {
                 wait(&bars.input_full[c & 1], (c >> 1) & 1);
                 const uint8_t* rows = input(c) + (key ? 0 : Y::kTile) + i * 128;
@@ -522,37 +480,55 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 for (int x = 0; x < D / 8; ++x) {
                     const uint4 q = *reinterpret_cast<const uint4*>(rows + (x >> 3) * (2 * Y::kTile) + (((x & 7) ^ (i & 7)) << 4));
                     const Eight e = unpack(q);
-                    sum += dot(e, e);
+                    square += dot(e, e);
                 }
             }
-            const float r = rsqrtf(sum + p.eps);
-            if (key)
-                sc.r_k[i] = at < n ? r : 0.0f;
-            else
-                sc.r_q[i] = r * p.scale;
-            token_barrier();
+            const float r = at < n ? rsqrtf(square + p.eps) : 0.0f;
+            const float hi = (float)sum, lo = (float)(sum - (double)hi), fade = ex2(hi);
+            if (key) {
+                sc.decay[i] = make_float4(hi, lo, r, 0.0f);
+                sc.x[i] = make_float2(beta, beta * fade * r);
+                if (!TREE) sc.last[i] = ex2((float)(end - sum)) * r;
+            } else {
+                sc.o[i] = make_float2(r * p.scale * fade, r * p.scale);
+            }
+            if (t == 0) {
+                sc.end = ex2((float)end);
+                sc.bad[0] = sc.bad[1] = 0;
+            }
+            group_barrier<1>();
+            if (c > 0) wait(&bars.l_free, (c - 1) & 1);
             wait(&bars.gram_full, c & 1);
             umma_fence_after();
-            const float hi = sc.hi[i], lo = sc.lo[i], own = key ? sc.beta[i] * sc.r_k[i] : 1.0f;
-            const uint64_t above = TREE ? sc.above[i] : ~0ull >> (63 - i);
-            float* L = l_of(c) + i * kLStride;
+            const float own = key ? beta * r : 1.0f;
+            if (key) above &= ~(1ull << i);
+            float* Li = L + i * kLStride;
             uint8_t* P = p_of(c) + i * 128;
+            float zero = 0.0f;               // NaN where a value of the row is not finite
 #pragma unroll 1
             for (int j0 = 0; j0 < kChunk; j0 += 16) {
                 float x[16];
-                tmem_ld(mine + Y::kG + j0, x);
-                tmem_wait_ld(x);
+                const bool any = TREE || j0 <= (warp & 1) * 32 + 31;         // (else all of the warp's are zero)
+                if (any) {
+                    tmem_ld(mine + Y::kG + j0, x);
+                    tmem_wait_ld(x);
+                    const uint32_t seen = (uint32_t)(above >> j0);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int jj = j0 + j;
-                    const bool seen = (above >> jj & 1) && !(key && jj == i);
-                    const float a = ex2((hi - sc.hi[jj]) + (lo - sc.lo[jj]));
-                    x[j] = seen ? own * a * (sc.r_k[jj] * x[j]) : 0.0f;
+                    for (int j = 0; j < 16; ++j) {
+                        const float4 d = sc.decay[j0 + j];
+                        const float a = ex2((hi - d.x) + (lo - d.y));
+                        x[j] = seen >> j & 1 ? (own * a) * (d.z * x[j]) : 0.0f;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[j] = 0.0f;
                 }
                 if (key) {
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4)
-                        *reinterpret_cast<float4*>(L + j0 + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+                    for (int j = 0; j < 16; j += 4) {
+                        *reinterpret_cast<float4*>(Li + j0 + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+                        zero = fmaf(x[j], 0.0f, fmaf(x[j + 1], 0.0f, fmaf(x[j + 2], 0.0f, fmaf(x[j + 3], 0.0f, zero))));
+                    }
                 } else if constexpr (HAS_Q) {
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
@@ -567,18 +543,21 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                         }
                 }
             }
+            if (key && zero != 0.0f) {
+                atomicOr(&sc.bad[i >> 5], 1u << (i & 31));
+                for (int j = 0; j < kChunk; j += 4) *reinterpret_cast<float4*>(Li + j) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
             umma_fence_before();
             mbar_arrive(&bars.gram_read);
             fence_proxy_async_smem();
             mbar_arrive(&bars.pairs_full[c & 1]);
         };
+        load_rates(0);
         load(0);
         loaded(0);
-        if (chunks > 1) {
-            load(1);
-            loaded(1);
-        }
+        if (chunks > 1) load(1);
         pairs(0);
+        if (chunks > 1) loaded(1);
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             if (c + 1 < chunks) pairs(c + 1);
@@ -587,6 +566,162 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 load(c + 2);
                 loaded(c + 2);
             }
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------------------------ L into T --
+        float* const M = reinterpret_cast<float*>(smem + Y::kM);
+        auto l4 = [&](int r, int col) { return *reinterpret_cast<const float4*>(L + r * kLStride + col); };
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            wait(&bars.pairs_full[c & 1], (c >> 1) & 1);
+            // blocks of 16 on the diagonal, a column a thread
+            if (t < 64) {
+                const int at = t & 48, col = t & 15;
+                float x[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float s = i == col ? 1.0f : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < i; j += 4) {
+                        const float4 l = l4(at + i, at + j);
+                        s = fmaf(-l.x, x[j], s);
+                        if (j + 1 < i) s = fmaf(-l.y, x[j + 1], s);
+                        if (j + 2 < i) s = fmaf(-l.z, x[j + 2], s);
+                        if (j + 3 < i) s = fmaf(-l.w, x[j + 3], s);
+                    }
+                    x[i] = s;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) L[(at + i) * kLStride + at + col] = x[i];
+            }
+            group_barrier<2>();
+            // of 32: the lower left is -T22 (L21 T11)
+            {
+                const int at = (t >> 6) * 32, r = (t & 63) >> 2, col = (t & 3) * 4;
+                float* m = M + (t >> 6) * (16 * kMStride);
+                float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int k = 0; k < 16; k += 4) {
+                    const float4 l = l4(at + 16 + r, at + k);
+                    const float w[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float4 y = l4(at + k + x, at + col);
+                        s = make_float4(fmaf(w[x], y.x, s.x), fmaf(w[x], y.y, s.y), fmaf(w[x], y.z, s.z), fmaf(w[x], y.w, s.w));
+                    }
+                }
+                *reinterpret_cast<float4*>(m + r * kMStride + col) = s;
+                group_barrier<2>();
+                s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int k = 0; k < 16; k += 4) {
+                    const float4 l = l4(at + 16 + r, at + 16 + k);
+                    const float w[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float4 y = *reinterpret_cast<const float4*>(m + (k + x) * kMStride + col);
+                        s = make_float4(fmaf(w[x], y.x, s.x), fmaf(w[x], y.y, s.y), fmaf(w[x], y.z, s.z), fmaf(w[x], y.w, s.w));
+                    }
+                }
+                *reinterpret_cast<float4*>(L + (at + 16 + r) * kLStride + at + col) = make_float4(-s.x, -s.y, -s.z, -s.w);
+            }
+            group_barrier<2>();
+            // of 64, two rows and four columns a thread
+            {
+                const int r = (t >> 3) * 2, col = (t & 7) * 4;
+#pragma unroll
+                for (int pass = 0; pass < 2; ++pass) {
+                    const int most = pass == 0 ? 32 : (warp & 3) * 8 + 8;    // (T22's rows end at the diagonal)
+                    float4 s[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+#pragma unroll 2
+                    for (int k = 0; k < most; k += 4) {
+                        const float4 l0 = l4(32 + r, pass * 32 + k), l1 = l4(33 + r, pass * 32 + k);
+                        const float w[2][4] = {{l0.x, l0.y, l0.z, l0.w}, {l1.x, l1.y, l1.z, l1.w}};
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const float4 y = pass == 0 ? l4(k + x, col)
+                                                       : *reinterpret_cast<const float4*>(M + (k + x) * kMStride + col);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                s[i] = make_float4(fmaf(w[i][x], y.x, s[i].x), fmaf(w[i][x], y.y, s[i].y),
+                                                   fmaf(w[i][x], y.z, s[i].z), fmaf(w[i][x], y.w, s[i].w));
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (pass == 0)
+                            *reinterpret_cast<float4*>(M + (r + i) * kMStride + col) = s[i];
+                        else
+                            *reinterpret_cast<float4*>(L + (32 + r + i) * kLStride + col) =
+                                make_float4(-s[i].x, -s[i].y, -s[i].z, -s[i].w);
+                    }
+                    group_barrier<2>();
+                }
+            }
+            // its parts, half a row a thread
+            {
+                const int r = t >> 1, half = t & 1;
+                uint8_t* T = t_of(c) + r * 128;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float4 a = l4(r, half * 32 + x * 8), d = l4(r, half * 32 + x * 8 + 4);
+                    float y[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
+#pragma unroll
+                    for (int part = 0; part < 3; ++part) {
+                        uint4 w;
+                        w.x = take_part(y[0], y[1]);
+                        w.y = take_part(y[2], y[3]);
+                        w.z = take_part(y[4], y[5]);
+                        w.w = take_part(y[6], y[7]);
+                        *reinterpret_cast<uint4*>(T + part * Y::kTile + (((half * 4 + x) ^ (r & 7)) << 4)) = w;
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&bars.t_full[c & 1]);
+            mbar_arrive(&bars.l_free);
+        }
+    } else if (warp < 16) {
+        // ------------------------------------------------------------- outputs --
+        const bool live = t < D;
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            wait(&bars.o_full, c & 1);
+            umma_fence_after();
+            const Scalars& sc = *scalars_of(c);
+            if constexpr (HAS_Q) {
+                const uint64_t lost = sc.lost[t];
+                uint16_t* o = p.o + ((row0 + c * kChunk) * p.Hv + h) * D + t;
+                const int64_t stride = (int64_t)p.Hv * D;
+                const int most = min(kChunk, n - c * kChunk);
+#pragma unroll 1
+                for (int t0 = 0; t0 < kChunk; t0 += 16) {
+                    float y[16], z[16];
+                    tmem_ld(mine + Y::kY + t0, y);
+                    tmem_ld(mine + Y::kW + t0, z);
+                    tmem_wait_ld(y);
+                    tmem_wait_ld(z);
+                    if (t0 == kChunk - 16) {
+                        umma_fence_before();
+                        mbar_arrive(&bars.o_read);
+                    }
+                    if (!live) continue;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (t0 + i >= most) break;
+                        const float2 f = sc.o[t0 + i];
+                        uint32_t out = pack_bf16x2(fmaf(f.x, y[i], f.y * z[i]), 0.0f);
+                        if (lost >> (t0 + i) & 1) out = 0x7FC0u;
+                        if (TREE && sc.kind[t0 + i] != kNode) out = sc.kind[t0 + i] == kNoNode ? 0u : 0x7FC0u;
+                        *o = (uint16_t)out;
+                        o += stride;
+                    }
+                }
+            } else {
+                mbar_arrive(&bars.o_read);
+            }
+            mbar_arrive(&bars.pairs_free[c & 1]);
         }
     } else if (lane == 0) {
         // ------------------------------------------------------------ products --
@@ -602,36 +737,55 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             }
             umma_commit(&bars.gram_full);
         };
+        // D[tmem] (+)= A[tmem] B^T with lower triangular B [64][64]: its columns from 16 k on are read by row 16 k and later
+        auto triangular = [&](uint32_t d, uint32_t a, int apart, uint32_t b_tile, bool first) {
+#pragma unroll
+            for (int k = 0; k < kChunk / 16; ++k)
+                umma_bf16_tmem(d + 16 * k, a + (k >> 1) * apart + (k & 1) * 8, umma_sdesc_sw128(b_tile + k * (16 * 128 + 32)),
+                               idesc_bf16(64 - 16 * k, false), !first || k > 0);
+        };
         gram(0);
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-            const uint32_t kq = smem_u32(input(c)), pp = smem_u32(p_of(c));
+            const uint32_t kq = smem_u32(input(c)), pp = smem_u32(p_of(c)), tt = smem_u32(t_of(c));
             wait(&bars.s_ready, c & 1);
+            if (c > 0) wait(&bars.o_read, (c - 1) & 1);
             umma_fence_after();
 #pragma unroll
             for (int part = 0; part < 3; ++part)
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
-                    umma_bf16_tmem(tmem + Y::kW, tmem + Y::kParts + part * (D / 2) + k * 8,
+                    umma_bf16_tmem(tmem + Y::kW, tmem + Y::kParts + part * 64 + k * 8,
                                    umma_sdesc_sw128(kq + (k >> 2) * (2 * Y::kTile) + (k & 3) * 32), kById, part + k > 0);
             umma_commit(&bars.w_full);
             if constexpr (HAS_Q) {
-                if (c > 0) {
-                    wait(&bars.o_read, (c - 1) & 1);
-                    umma_fence_after();
-                }
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int k = 0; k < KS; ++k)
-                        umma_bf16_tmem(tmem + Y::kY, tmem + Y::kParts + part * (D / 2) + k * 8,
+                        umma_bf16_tmem(tmem + Y::kY, tmem + Y::kParts + part * 64 + k * 8,
                                        umma_sdesc_sw128(kq + (k >> 2) * (2 * Y::kTile) + Y::kTile + (k & 3) * 32), kById,
                                        part + k > 0);
                 umma_commit(&bars.y_full);
             }
-            wait(&bars.gram_read, c & 1);    // (of this chunk's: its rows are done before u is)
+            if (c + 1 < chunks) {
+                wait(&bars.gram_read, c & 1);
+                umma_fence_after();
+                gram(c + 1);
+            }
+            wait(&bars.x_ready, c & 1);
+            wait(&bars.t_full[c & 1], (c >> 1) & 1);
+            if (HAS_Q) wait(&bars.y_full, c & 1);            // (U takes the place of the parts that Y is of)
             umma_fence_after();
-            if (c + 1 < chunks) gram(c + 1);
+            // parts (X, T): (0, 0), (0, 1), (1, 0), (0, 2), (1, 1), (2, 0)
+            const uint32_t x0 = tmem + Y::kW, x1 = x0 + 16, x2 = tmem + Y::kX2;
+            triangular(tmem + Y::kU, x0, 32, tt, true);
+            triangular(tmem + Y::kU, x0, 32, tt + Y::kTile, false);
+            triangular(tmem + Y::kU, x1, 32, tt, false);
+            triangular(tmem + Y::kU, x0, 32, tt + 2 * Y::kTile, false);
+            triangular(tmem + Y::kU, x1, 32, tt + Y::kTile, false);
+            triangular(tmem + Y::kU, x2, 16, tt, false);
+            umma_commit(&bars.u_full);
             wait(&bars.u_ready, c & 1);
             umma_fence_after();
             if constexpr (!TREE) {
@@ -644,19 +798,12 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 umma_commit(&bars.s_full);
             }
             if constexpr (HAS_Q) {
-                if (c + 1 < chunks) {
-                    wait(&bars.gram_read, (c + 1) & 1);
-                    umma_fence_after();
-                }
                 wait(&bars.pairs_full[c & 1], (c >> 1) & 1);
-#pragma unroll
-                for (int m = 0; m < 3; ++m)                  // parts (0, 0), (0, 1), (1, 0)
-#pragma unroll
-                    for (int k = 0; k < kChunk / 16; ++k)
-                        umma_bf16_tmem(tmem + Y::kG, tmem + Y::kU + (m == 2 ? 32 : 0) + k * 8,
-                                       umma_sdesc_sw128(pp + (m == 1 ? Y::kTile : 0) + k * 32), kById, m + k > 0);
-                umma_commit(&bars.o_full);
+                triangular(tmem + Y::kW, tmem + Y::kU, 32, pp, true);
+                triangular(tmem + Y::kW, tmem + Y::kU, 32, pp + Y::kTile, false);
+                triangular(tmem + Y::kW, tmem + Y::kU + 16, 32, pp, false);
             }
+            umma_commit(&bars.o_full);
             umma_commit(&bars.input_free[c & 1]);
         }
         // all products are done, whatever else gave up
@@ -666,12 +813,12 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
     umma_fence_before();
     __syncthreads();
     umma_fence_after();
-    if (warp == 8) tmem_dealloc(tmem, 512);
+    if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
 template <int D, DeltaMode MODE>
 cudaError_t launch(const DeltaParams& p, cudaStream_t st) {
-    constexpr size_t smem = Layout<D>::kBytes + sizeof(Barriers) + 1024;
+    constexpr size_t smem = Layout<D>::kBars + sizeof(Barriers) + 1024;
     const void* kernel = reinterpret_cast<const void*>(delta_chunks_kernel<D, MODE>);
     cudaError_t e = ensure_dynamic_smem(kernel, smem);
     if (e != cudaSuccess) return e;
