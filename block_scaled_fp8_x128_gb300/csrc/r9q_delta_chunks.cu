@@ -14,12 +14,12 @@
 // token's values, however large, do not touch those of earlier tokens.  Three parts for what
 // goes into S and u, two (2^-16) where only outputs, which are rounded to bf16, follow.
 //
-// Warps 0-3, the rows: S, X and u into parts, the chain that bounds a sequence's time.  Warps 4-7, the
-// tokens: K, Q, V are copied a chunk ahead, and L and P of the next chunk formed.  Warps 8-11 turn
+// Warps 0-7, the rows: S, X and u into parts, the chain that bounds a sequence's time, half the columns each;
+// while W is formed they write the last chunk's outputs.  Warps 8-11, the
+// tokens: K, Q, V are copied a chunk ahead, and L and P of the next chunk formed.  Warps 12-15 turn
 // L into T, in fp32 by blocks of 16, 32 and 64 (as a substitution a row's thread would need all of L
-// in its registers: 8300 cycles of shared memory's 128 bytes each for the four warps).  Warps 12-15 write the
-// outputs of the chunk before.  Warp 16 issues the products.  In a tree the sums
-// go over ancestors, and its one chunk leaves the state alone.
+// in its registers: 8300 cycles of shared memory's 128 bytes each for four warps).  Warp 16 issues the
+// products.  In a tree the sums go over ancestors, and its one chunk leaves the state alone.
 //
 // A value that is not finite would reach earlier tokens (or other branches) through the zeros of T and P.
 // So L's rows, X and u are zero in its place, and the outputs that it belongs to are NaN, as is the state's row.
@@ -32,18 +32,19 @@ namespace r9q {
 namespace {
 
 constexpr int kChunk = 64;
-constexpr int kGroup = 128;                  // threads of each of the four groups
+constexpr int kGroup = 128;                  // threads of the tokens, and of T; twice that the rows
 constexpr int kThreads = 4 * kGroup + 32;
 constexpr int kLStride = 68;                 // floats between rows of L: eight rows' 16-byte pieces lie in different banks
 constexpr int kMStride = 36;
 
 // Scalars of a chunk's tokens.
 struct Scalars {
-    float2 x[kChunk];                        // X = x.x v - x.y W
+    float4 x[kChunk / 2];                    // X = x v + y W, of two tokens: x, x, y, y
     float2 o[kChunk];                        // o = o.x Y + o.y (U P^T)
     float last[kChunk];                      // A(n, i) / |k_i|
     float4 decay[kChunk];                    // two parts of the sum of the decays' logarithms (to base 2), 1 / |k|
-    uint64_t above[kChunk], lost[kGroup];    // (of a tree); tokens without a finite u, by row
+    uint64_t above[kChunk];                  // (of a tree)
+    uint32_t lost[2][kGroup];                // tokens without a finite X or u, by half and row
     int parents[kChunk];
     NodeKind kind[kChunk];
     uint32_t bad[2];                         // tokens whose row of L is not finite
@@ -61,7 +62,8 @@ struct Layout {
     static constexpr int kL = kT + 6 * kTile;
     static constexpr int kM = kL + kChunk * kLStride * 4;
     static constexpr int kScalars = kM + 32 * kMStride * 4;
-    static constexpr int kBars = kScalars + 2 * (int)sizeof(Scalars);
+    static constexpr int kOut = kScalars + 2 * (int)sizeof(Scalars);         // outputs [64][D] on their way
+    static constexpr int kBars = kOut + kChunk * D * 2;
     // tensor memory, columns.  S's parts are 64 columns apart; X's third takes a place that W alone reads (of S's
     // third), U that of S's first.  What is read by 32 tokens, W and U, is replaced by two parts of them: of tokens
     // 32 i on in the columns 32 i and 32 i + 16 on.
@@ -72,17 +74,16 @@ struct Layout {
 
 struct Barriers {
     uint64_t input_full[2], input_free[2], gram_full, gram_read, pairs_full[2], pairs_free[2], l_free, t_full[2], s_ready,
-        w_full, y_full, x_ready, u_full, u_ready, s_full, o_full, o_read;
+        w_full, y_full, x_ready, u_full, u_ready, s_full, o_full;
     uint32_t tmem;
     int failed;                              // a wait gave up
 };
 
-// Two fp32 values to bf16 parts, cut off; the rest stays.
-__device__ __forceinline__ uint32_t take_part(float& a, float& b) {
-    uint32_t r;
-    asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-    a -= bf16_lo(r);
-    b -= bf16_hi(r);
+// Two fp32 values to bf16, cut off; the rest stays.
+__device__ __forceinline__ uint32_t take_part(uint64_t& x) {
+    const uint64_t top = x & 0xFFFF0000FFFF0000ull;
+    const uint32_t r = __byte_perm((uint32_t)x, (uint32_t)(x >> 32), 0x7632);
+    x = fma2(top, 0xBF800000BF800000ull, x);                 // (times -1)
     return r;
 }
 
@@ -140,28 +141,44 @@ __device__ __forceinline__ void group_barrier() {
     asm volatile("bar.sync %0, 128;" ::"n"(ID) : "memory");
 }
 // The next part of 32 values, two a column.
-__device__ __forceinline__ void take_parts(uint32_t (&y)[16], float (&x)[32]) {
+__device__ __forceinline__ void take_parts(uint32_t (&y)[16], uint64_t (&x)[16]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = take_part(x[2 * i], x[2 * i + 1]);
+    for (int i = 0; i < 16; ++i) y[i] = take_part(x[i]);
 }
-__device__ __forceinline__ void store_part(uint32_t taddr, float (&x)[32]) {
+__device__ __forceinline__ void store_part(uint32_t taddr, uint64_t (&x)[16]) {
     uint32_t y[16];
     take_parts(y, x);
     tmem_st16(taddr, y);
 }
-// The tokens (a bit each) among 32 from t0 on whose value is not finite; those become zero.
-__device__ __forceinline__ uint32_t not_finite(float (&x)[32]) {
-    float sum = 0.0f;
+// 32 columns of this thread's lane.
+__device__ __forceinline__ void load_pairs(uint32_t taddr, uint64_t (&x)[16]) {
+    float f[32];
+    tmem_ld(taddr, f);
+    tmem_wait_ld(f);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) sum = fmaf(x[i], 0.0f, sum);
+    for (int i = 0; i < 16; ++i) x[i] = pair_of(f[2 * i], f[2 * i + 1]);
+}
+// Which of 32 values are not finite, a bit each; those become zero.
+__device__ __forceinline__ uint32_t not_finite(uint64_t (&x)[16]) {
+    uint64_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum = fma2(x[i], 0ull, sum);
     uint32_t m = 0;
-    if (sum != 0.0f) {
+    const float2 any = parts_of(sum);
+    if (any.x + any.y != 0.0f) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (!(fabsf(x[i]) <= FLT_MAX)) {
-                m |= 1u << i;
-                x[i] = 0.0f;
+        for (int i = 0; i < 16; ++i) {
+            float2 f = parts_of(x[i]);
+            if (!(fabsf(f.x) <= FLT_MAX)) {
+                m |= 1u << (2 * i);
+                f.x = 0.0f;
             }
+            if (!(fabsf(f.y) <= FLT_MAX)) {
+                m |= 2u << (2 * i);
+                f.y = 0.0f;
+            }
+            x[i] = pair_of(f.x, f.y);
+        }
     }
     return m;
 }
@@ -228,21 +245,20 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             mbar_init(&bars.input_full[i], kGroup);
             mbar_init(&bars.input_free[i], 1);
             mbar_init(&bars.pairs_full[i], kGroup);
-            mbar_init(&bars.pairs_free[i], kGroup);
+            mbar_init(&bars.pairs_free[i], 2 * kGroup);
             mbar_init(&bars.t_full[i], kGroup);
         }
         mbar_init(&bars.gram_full, 1);
         mbar_init(&bars.gram_read, kGroup);
         mbar_init(&bars.l_free, kGroup);
-        mbar_init(&bars.s_ready, kGroup);
+        mbar_init(&bars.s_ready, 2 * kGroup);
         mbar_init(&bars.w_full, 1);
         mbar_init(&bars.y_full, 1);
-        mbar_init(&bars.x_ready, kGroup);
+        mbar_init(&bars.x_ready, 2 * kGroup);
         mbar_init(&bars.u_full, 1);
-        mbar_init(&bars.u_ready, kGroup);
+        mbar_init(&bars.u_ready, 2 * kGroup);
         mbar_init(&bars.s_full, 1);
         mbar_init(&bars.o_full, 1);
-        mbar_init(&bars.o_read, kGroup);
         bars.failed = 0;
         fence_mbar_init();
     }
@@ -253,12 +269,13 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
     const uint32_t tmem = bars.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const Waits wait = {&bars.failed, p.err};
 
-    if (warp < 4) {
+    if (warp < 8) {
         // ---------------------------------------------------------------- rows --
         const bool live = t < D;             // (D = 64: the other half of the lanes is zeros)
+        const int half = warp >> 2, e0 = half * (D / 2), t0 = half * 32;         // the thread's columns and tokens
         float* row = state + (int64_t)t * D;
 #pragma unroll 1
-        for (int e = 0; e < D; e += 16) {
+        for (int e = e0; e < e0 + D / 2; e += 16) {
             uint32_t x[16];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -271,6 +288,59 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             tmem_st16(mine + Y::kS + e, x);
         }
         tmem_wait_st();
+        uint32_t out[16];                    // of chunk c, two tokens each, as bf16
+        auto take_outputs = [&](int c) {
+            const Scalars& sc = *scalars_of(c);
+            wait(&bars.o_full, c & 1);
+            umma_fence_after();
+            float y[32], z[32];
+            tmem_ld(mine + Y::kY + t0, y);
+            tmem_ld(mine + Y::kW + t0, z);
+            tmem_wait_ld(y);
+            tmem_wait_ld(z);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const float4 f = *reinterpret_cast<const float4*>(&sc.o[t0 + i]);
+                out[i / 2] = pack_bf16x2(fmaf(f.x, y[i], f.y * z[i]), fmaf(f.z, y[i + 1], f.w * z[i + 1]));
+            }
+            uint64_t lost = (uint64_t)sc.lost[1][t] << 32 | sc.lost[0][t] | *reinterpret_cast<const uint64_t*>(sc.bad);
+            if (lost) {                      // NaN, and what comes from it
+                if constexpr (TREE) {
+#pragma unroll 1
+                    for (int i = 0; i < kChunk; ++i)
+                        if (sc.above[i] & lost) lost |= 1ull << i;
+                } else {
+                    lost = ~0ull << (__ffsll((long long)lost) - 1);
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (lost >> (t0 + i) & 1) out[i / 2] = i & 1 ? (out[i / 2] & 0xFFFFu) | 0x7FC00000u : (out[i / 2] & 0xFFFF0000u) | 0x7FC0u;
+            }
+            if constexpr (TREE) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const NodeKind kind = sc.kind[t0 + i];
+                    const uint32_t bits = kind == kNoNode ? 0u : 0x7FC07FC0u, m = i & 1 ? 0xFFFF0000u : 0xFFFFu;
+                    if (kind != kNode) out[i / 2] = (out[i / 2] & ~m) | (bits & m);
+                }
+            }
+        };
+        // by way of shared memory, so that a warp writes whole lines
+        auto write_outputs = [&](int c) {
+            uint16_t* stage = reinterpret_cast<uint16_t*>(smem + Y::kOut);
+            if (live)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) stage[(t0 + i) * D + t] = (uint16_t)(out[i / 2] >> (16 * (i & 1)));
+            asm volatile("bar.sync 3, 256;" ::: "memory");
+            const int most = min(kChunk, n - c * kChunk) * (D / 8);
+            uint16_t* o = p.o + ((row0 + c * kChunk) * p.Hv + h) * D;
+#pragma unroll
+            for (int x = tid; x < kChunk * (D / 8); x += 2 * kGroup)
+                if (x < most)
+                    *reinterpret_cast<uint4*>(o + (int64_t)(x / (D / 8)) * p.Hv * D + x % (D / 8) * 8) =
+                        *reinterpret_cast<const uint4*>(stage + x * 8);
+            mbar_arrive(&bars.pairs_free[c & 1]);
+        };
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             wait(&bars.pairs_full[c & 1], (c >> 1) & 1);
@@ -281,55 +351,61 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             }
             // S into its parts, and what is left of it at the chunk's end
             const float left = sc.end;
+            const uint64_t left2 = pair_of(left, left);
 #pragma unroll 1
-            for (int e = 0; e < D; e += 32) {
-                float s[32];
-                tmem_ld(mine + Y::kS + e, s);
-                tmem_wait_ld(s);
+            for (int e = e0; e < e0 + D / 2; e += 32) {
+                uint64_t s[16];
+                load_pairs(mine + Y::kS + e, s);
                 if constexpr (!TREE) {
-                    uint32_t x[16];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t x[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(left * s[half * 16 + i]);
-                        tmem_st16(mine + Y::kS + e + half * 16, x);
+                        for (int j = 0; j < 8; ++j) {
+                            const float2 f = parts_of(mul2(left2, s[i * 8 + j]));
+                            x[2 * j] = __float_as_uint(f.x);
+                            x[2 * j + 1] = __float_as_uint(f.y);
+                        }
+                        tmem_st16(mine + Y::kS + e + i * 16, x);
                     }
                 }
                 uint32_t first[16];
                 take_parts(first, s);
                 store_part(mine + Y::kParts + 64 + e / 2, s);
                 store_part(mine + Y::kParts + 128 + e / 2, s);
-                if (HAS_Q && e == 0 && c > 0) {              // (u's parts, that the last outputs come from, are there)
+                if (HAS_Q && e == e0 && c > 0) {             // (u's parts, that the last outputs come from, are there)
                     wait(&bars.o_full, (c - 1) & 1);
                     umma_fence_after();
                 }
                 tmem_st16(mine + Y::kParts + e / 2, first);
             }
+            if (HAS_Q && c > 0) take_outputs(c - 1);
             tmem_wait_st();
             umma_fence_before();
             mbar_arrive(&bars.s_ready);
+            if (c > 0) {
+                if constexpr (HAS_Q)
+                    write_outputs(c - 1);
+                else
+                    mbar_arrive(&bars.pairs_free[(c - 1) & 1]);
+            }
 
             // ---- X ----
+            const uint16_t* v = reinterpret_cast<const uint16_t*>(input(c) + Y::kKq) + t0 * D + (live ? t : 0);
             wait(&bars.w_full, c & 1);
             umma_fence_after();
-            const uint16_t* v = reinterpret_cast<const uint16_t*>(input(c) + Y::kKq) + (live ? t : 0);
-            uint64_t lost = 0;
-#pragma unroll 1
-            for (int t0 = 0; t0 < kChunk; t0 += 32) {
-                float x[32];
-                tmem_ld(mine + Y::kW + t0, x);
-                tmem_wait_ld(x);
+            uint64_t x[16];
+            load_pairs(mine + Y::kW + t0, x);
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    const float4 f = *reinterpret_cast<const float4*>(&sc.x[t0 + i]);
-                    x[i] = fmaf(f.x, bf16_lo(v[(t0 + i) * D]), -f.y * x[i]);
-                    x[i + 1] = fmaf(f.z, bf16_lo(v[(t0 + i + 1) * D]), -f.w * x[i + 1]);
-                }
-                lost |= (uint64_t)not_finite(x) << t0;
-                store_part(mine + Y::kW + t0, x);
-                store_part(mine + Y::kW + t0 + 16, x);
-                store_part(mine + Y::kX2 + t0 / 2, x);
+            for (int i = 0; i < 16; ++i) {
+                const float4 f = *reinterpret_cast<const float4*>(&sc.x[t0 / 2 + i]);
+                const uint64_t val = pair_of(bf16_lo(v[2 * i * D]), bf16_lo(v[(2 * i + 1) * D]));
+                x[i] = fma2(pair_of(f.z, f.w), x[i], mul2(pair_of(f.x, f.y), val));
             }
+            uint32_t lost = not_finite(x);
+            store_part(mine + Y::kW + t0, x);
+            store_part(mine + Y::kW + t0 + 16, x);
+            store_part(mine + Y::kX2 + t0 / 2, x);
             tmem_wait_st();
             umma_fence_before();
             mbar_arrive(&bars.x_ready);
@@ -337,45 +413,26 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             // ---- u, as an operand ----
             wait(&bars.u_full, c & 1);
             umma_fence_after();
-            lost |= *reinterpret_cast<const uint64_t*>(sc.bad);
-#pragma unroll 1
-            for (int t0 = 0; t0 < kChunk; t0 += 32) {
-                float u[32];
-                tmem_ld(mine + Y::kU + t0, u);
-                tmem_wait_ld(u);
-                lost |= (uint64_t)not_finite(u) << t0;
-                if (lost) {                  // with what comes from such a token
-                    if constexpr (TREE) {
-                        for (int i = 0; i < kChunk; ++i)
-                            if (sc.above[i] & lost) lost |= 1ull << i;
-                    } else {
-                        lost = ~0ull << (__ffsll((long long)lost) - 1);
-                    }
+            load_pairs(mine + Y::kU + t0, x);
+            lost |= not_finite(x);
+            sc.lost[half][t] = lost;
+            if constexpr (!TREE) {
+                uint64_t y[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (lost >> (t0 + i) & 1) u[i] = 0.0f;
+                for (int i = 0; i < 16; i += 2) {
+                    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&sc.last[t0 + 2 * i]);
+                    y[i] = mul2(f.x, x[i]);
+                    y[i + 1] = mul2(f.y, x[i + 1]);
                 }
-                if constexpr (!TREE) {
-                    float x[32];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(&sc.last[t0 + i]);
-                        x[i] = f.x * u[i];
-                        x[i + 1] = f.y * u[i + 1];
-                        x[i + 2] = f.z * u[i + 2];
-                        x[i + 3] = f.w * u[i + 3];
-                    }
-                    if (lost >> (t0 + 31) & 1) x[31] = __int_as_float(0x7FC00000);               // into the state
-                    store_part(mine + Y::kUleft + t0 / 2, x);
-                    store_part(mine + Y::kUleft + 32 + t0 / 2, x);
-                    store_part(mine + Y::kUleft + 64 + t0 / 2, x);
-                }
-                if constexpr (HAS_Q) {
-                    store_part(mine + Y::kU + t0, u);
-                    store_part(mine + Y::kU + t0 + 16, u);
-                }
+                if (lost | sc.bad[0] | sc.bad[1]) y[0] = pair_of(__int_as_float(0x7FC00000), 0.0f);     // into the state
+                store_part(mine + Y::kUleft + t0 / 2, y);
+                store_part(mine + Y::kUleft + 32 + t0 / 2, y);
+                store_part(mine + Y::kUleft + 64 + t0 / 2, y);
             }
-            sc.lost[t] = lost;
+            if constexpr (HAS_Q) {
+                store_part(mine + Y::kU + t0, x);
+                store_part(mine + Y::kU + t0 + 16, x);
+            }
             tmem_wait_st();
             umma_fence_before();
             mbar_arrive(&bars.u_ready);
@@ -384,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             wait(&bars.s_full, (chunks - 1) & 1);
             umma_fence_after();
 #pragma unroll 1
-            for (int e = 0; e < D; e += 32) {
+            for (int e = e0; e < e0 + D / 2; e += 32) {
                 float s[32];
                 tmem_ld(mine + Y::kS + e, s);
                 tmem_wait_ld(s);
@@ -394,7 +451,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                         reinterpret_cast<float4*>(row + e)[i] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
             }
         }
-    } else if (warp < 8) {
+        if constexpr (HAS_Q) {
+            take_outputs(chunks - 1);
+            write_outputs(chunks - 1);
+        }
+    } else if (warp < 12) {
         // -------------------------------------------------------------- tokens --
         const int i = t & 63;                // row of K or of Q
         const bool key = t < 64;
@@ -439,14 +500,18 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
         auto pairs = [&](int c) {
             Scalars& sc = *scalars_of(c);
             const int at = c * kChunk + i;
-            const float beta = beta_next, g = g_next < -200.0f ? -200.0f : g_next;   // (exp is 0 there; infinities have no differences)
+            // Sums of the decays' logarithms to base 2 in units of 2^-40, so that differences are exact.  (exp(-200) is 0, and
+            // infinities have no differences; a NaN goes into the rate, and from there to all that follows.)
+            const float beta = g_next == g_next ? beta_next : g_next;
+            const long long g = __float2ll_rn(fminf(fmaxf(g_next, -200.0f), 200.0f) * (1.4426950408889634f * 0x1p40f));
             if (c + 1 < chunks) load_rates(c + 1);
             if (c >= 2) wait(&bars.pairs_free[c & 1], ((c - 2) >> 1) & 1);
             uint64_t above = ~0ull >> (63 - i);
-            double sum = 0.0, end = 0.0;
+            long long sum = 0, end = 0;
             if constexpr (TREE) {
+                long long* rates = reinterpret_cast<long long*>(sc.decay);
                 if (key) {
-                    sc.last[i] = g;
+                    rates[i] = g;
                     sc.parents[i] = at < n ? p.parents[(int64_t)b * p.Lq + at] : -2;
                 }
                 group_barrier<1>();
@@ -456,16 +521,16 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 if (kind != kNode) above = 0;
                 sc.kind[i] = kind;
                 sc.above[i] = above;
-                for (uint64_t m = above; m; m &= m - 1) sum += (double)sc.last[__ffsll((long long)m) - 1];
-                sum *= 1.4426950408889634;
+                for (uint64_t m = above; m; m &= m - 1) sum += rates[__ffsll((long long)m) - 1];
+                group_barrier<1>();
             } else {                         // a scan over the 64 tokens, whole in each pair of warps
-                sum = (double)g * 1.4426950408889634;
+                sum = g;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const double y = __shfl_up_sync(0xffffffffu, sum, o);
+                    const long long y = __shfl_up_sync(0xffffffffu, sum, o);
                     if (lane >= o) sum += y;
                 }
-                double* halves = reinterpret_cast<double*>(sc.parents);      // (a tree's)
+                long long* halves = reinterpret_cast<long long*>(sc.parents);        // (a tree's)
                 if (lane == 31) halves[warp & 3] = sum;
                 group_barrier<1>();
                 end = halves[0] + halves[1];
@@ -484,16 +549,19 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 }
             }
             const float r = at < n ? rsqrtf(square + p.eps) : 0.0f;
-            const float hi = (float)sum, lo = (float)(sum - (double)hi), fade = ex2(hi);
+            // (the sum is under 2^55: its upper word is exact as a float)
+            const float hi = (float)(int)(sum >> 32) * 0x1p-8f, lo = (float)(uint32_t)sum * 0x1p-40f, fade = ex2(hi + lo);
             if (key) {
                 sc.decay[i] = make_float4(hi, lo, r, 0.0f);
-                sc.x[i] = make_float2(beta, beta * fade * r);
-                if (!TREE) sc.last[i] = ex2((float)(end - sum)) * r;
+                float* x = reinterpret_cast<float*>(&sc.x[i / 2]) + (i & 1);
+                x[0] = beta;
+                x[2] = -(beta * fade * r);
+                if (!TREE) sc.last[i] = ex2((float)(end - sum) * 0x1p-40f) * r;
             } else {
                 sc.o[i] = make_float2(r * p.scale * fade, r * p.scale);
             }
             if (t == 0) {
-                sc.end = ex2((float)end);
+                sc.end = ex2((float)end * 0x1p-40f);
                 sc.bad[0] = sc.bad[1] = 0;
             }
             group_barrier<1>();
@@ -531,16 +599,20 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                     }
                 } else if constexpr (HAS_Q) {
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
+                    for (int half = 0; half < 2; ++half) {
+                        uint64_t y[4];
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
+                        for (int j = 0; j < 4; ++j) y[j] = pair_of(x[8 * half + 2 * j], x[8 * half + 2 * j + 1]);
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
                             uint4 w;
-                            w.x = take_part(x[8 * half], x[8 * half + 1]);
-                            w.y = take_part(x[8 * half + 2], x[8 * half + 3]);
-                            w.z = take_part(x[8 * half + 4], x[8 * half + 5]);
-                            w.w = take_part(x[8 * half + 6], x[8 * half + 7]);
+                            w.x = take_part(y[0]);
+                            w.y = take_part(y[1]);
+                            w.z = take_part(y[2]);
+                            w.w = take_part(y[3]);
                             *reinterpret_cast<uint4*>(P + part * Y::kTile + (((j0 / 8 + half) ^ (i & 7)) << 4)) = w;
                         }
+                    }
                 }
             }
             if (key && zero != 0.0f) {
@@ -567,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 loaded(c + 2);
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // ------------------------------------------------------------ L into T --
         float* const M = reinterpret_cast<float*>(smem + Y::kM);
         auto l4 = [&](int r, int col) { return *reinterpret_cast<const float4*>(L + r * kLStride + col); };
@@ -666,14 +738,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const float4 a = l4(r, half * 32 + x * 8), d = l4(r, half * 32 + x * 8 + 4);
-                    float y[8] = {a.x, a.y, a.z, a.w, d.x, d.y, d.z, d.w};
+                    uint64_t y[4] = {pair_of(a.x, a.y), pair_of(a.z, a.w), pair_of(d.x, d.y), pair_of(d.z, d.w)};
 #pragma unroll
                     for (int part = 0; part < 3; ++part) {
                         uint4 w;
-                        w.x = take_part(y[0], y[1]);
-                        w.y = take_part(y[2], y[3]);
-                        w.z = take_part(y[4], y[5]);
-                        w.w = take_part(y[6], y[7]);
+                        w.x = take_part(y[0]);
+                        w.y = take_part(y[1]);
+                        w.z = take_part(y[2]);
+                        w.w = take_part(y[3]);
                         *reinterpret_cast<uint4*>(T + part * Y::kTile + (((half * 4 + x) ^ (r & 7)) << 4)) = w;
                     }
                 }
@@ -681,47 +753,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             fence_proxy_async_smem();
             mbar_arrive(&bars.t_full[c & 1]);
             mbar_arrive(&bars.l_free);
-        }
-    } else if (warp < 16) {
-        // ------------------------------------------------------------- outputs --
-        const bool live = t < D;
-#pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-            wait(&bars.o_full, c & 1);
-            umma_fence_after();
-            const Scalars& sc = *scalars_of(c);
-            if constexpr (HAS_Q) {
-                const uint64_t lost = sc.lost[t];
-                uint16_t* o = p.o + ((row0 + c * kChunk) * p.Hv + h) * D + t;
-                const int64_t stride = (int64_t)p.Hv * D;
-                const int most = min(kChunk, n - c * kChunk);
-#pragma unroll 1
-                for (int t0 = 0; t0 < kChunk; t0 += 16) {
-                    float y[16], z[16];
-                    tmem_ld(mine + Y::kY + t0, y);
-                    tmem_ld(mine + Y::kW + t0, z);
-                    tmem_wait_ld(y);
-                    tmem_wait_ld(z);
-                    if (t0 == kChunk - 16) {
-                        umma_fence_before();
-                        mbar_arrive(&bars.o_read);
-                    }
-                    if (!live) continue;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (t0 + i >= most) break;
-                        const float2 f = sc.o[t0 + i];
-                        uint32_t out = pack_bf16x2(fmaf(f.x, y[i], f.y * z[i]), 0.0f);
-                        if (lost >> (t0 + i) & 1) out = 0x7FC0u;
-                        if (TREE && sc.kind[t0 + i] != kNode) out = sc.kind[t0 + i] == kNoNode ? 0u : 0x7FC0u;
-                        *o = (uint16_t)out;
-                        o += stride;
-                    }
-                }
-            } else {
-                mbar_arrive(&bars.o_read);
-            }
-            mbar_arrive(&bars.pairs_free[c & 1]);
         }
     } else if (lane == 0) {
         // ------------------------------------------------------------ products --
@@ -749,7 +780,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
         for (int c = 0; c < chunks; ++c) {
             const uint32_t kq = smem_u32(input(c)), pp = smem_u32(p_of(c)), tt = smem_u32(t_of(c));
             wait(&bars.s_ready, c & 1);
-            if (c > 0) wait(&bars.o_read, (c - 1) & 1);
             umma_fence_after();
 #pragma unroll
             for (int part = 0; part < 3; ++part)
