@@ -79,11 +79,22 @@ struct Barriers {
     int failed;                              // a wait gave up
 };
 
-// Two fp32 values to bf16, cut off; the rest stays.
+// Two fp32 values to bf16, cut off; the rest stays.  (The rest as fused multiply-adds of the bf16 values themselves: taking
+// them apart with masks instead keeps the logic pipe, at half rate, busier than any other.)
 __device__ __forceinline__ uint32_t take_part(uint64_t& x) {
-    const uint64_t top = x & 0xFFFF0000FFFF0000ull;
-    const uint32_t r = __byte_perm((uint32_t)x, (uint32_t)(x >> 32), 0x7632);
-    x = fma2(top, 0xBF800000BF800000ull, x);                 // (times -1)
+    uint32_t r;
+    float2 f = parts_of(x);
+    asm("{\n\t.reg .b16 l, h, k;\n\tcvt.rz.bf16x2.f32 %0, %2, %1;\n\tmov.b32 {l, h}, %0;\n\tmov.b16 k, 0xBF80;\n\t"
+        "fma.rn.f32.bf16 %1, l, k, %1;\n\tfma.rn.f32.bf16 %2, h, k, %2;\n\t}"                 // (0xBF80: -1)
+        : "=&r"(r), "+f"(f.x), "+f"(f.y));
+    x = pair_of(f.x, f.y);
+    return r;
+}
+// The last part: nothing stays.
+__device__ __forceinline__ uint32_t last_part(uint64_t x) {
+    uint32_t r;
+    const float2 f = parts_of(x);
+    asm("cvt.rz.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(f.x), "f"(f.y));
     return r;
 }
 
@@ -140,14 +151,16 @@ template <int ID>
 __device__ __forceinline__ void group_barrier() {
     asm volatile("bar.sync %0, 128;" ::"n"(ID) : "memory");
 }
-// The next part of 32 values, two a column.
+// The next part of 32 values, two a column; LAST: nothing stays.
+template <bool LAST = false>
 __device__ __forceinline__ void take_parts(uint32_t (&y)[16], uint64_t (&x)[16]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = take_part(x[i]);
+    for (int i = 0; i < 16; ++i) y[i] = LAST ? last_part(x[i]) : take_part(x[i]);
 }
+template <bool LAST = false>
 __device__ __forceinline__ void store_part(uint32_t taddr, uint64_t (&x)[16]) {
     uint32_t y[16];
-    take_parts(y, x);
+    take_parts<LAST>(y, x);
     tmem_st16(taddr, y);
 }
 // 32 columns of this thread's lane.
@@ -372,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 uint32_t first[16];
                 take_parts(first, s);
                 store_part(mine + Y::kParts + 64 + e / 2, s);
-                store_part(mine + Y::kParts + 128 + e / 2, s);
+                store_part<true>(mine + Y::kParts + 128 + e / 2, s);
                 if (HAS_Q && e == e0 && c > 0) {             // (u's parts, that the last outputs come from, are there)
                     wait(&bars.o_full, (c - 1) & 1);
                     umma_fence_after();
@@ -405,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             uint32_t lost = not_finite(x);
             store_part(mine + Y::kW + t0, x);
             store_part(mine + Y::kW + t0 + 16, x);
-            store_part(mine + Y::kX2 + t0 / 2, x);
+            store_part<true>(mine + Y::kX2 + t0 / 2, x);
             tmem_wait_st();
             umma_fence_before();
             mbar_arrive(&bars.x_ready);
@@ -427,11 +440,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 if (lost | sc.bad[0] | sc.bad[1]) y[0] = pair_of(__int_as_float(0x7FC00000), 0.0f);     // into the state
                 store_part(mine + Y::kUleft + t0 / 2, y);
                 store_part(mine + Y::kUleft + 32 + t0 / 2, y);
-                store_part(mine + Y::kUleft + 64 + t0 / 2, y);
+                store_part<true>(mine + Y::kUleft + 64 + t0 / 2, y);
             }
             if constexpr (HAS_Q) {
                 store_part(mine + Y::kU + t0, x);
-                store_part(mine + Y::kU + t0 + 16, x);
+                store_part<true>(mine + Y::kU + t0 + 16, x);
             }
             tmem_wait_st();
             umma_fence_before();
@@ -572,30 +585,33 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             if (key) above &= ~(1ull << i);
             float* Li = L + i * kLStride;
             uint8_t* P = p_of(c) + i * 128;
-            float zero = 0.0f;               // NaN where a value of the row is not finite
+            uint64_t zeros = 0;              // NaN where a value of the row is not finite
+            const int first = (warp & 1) * 32;               // the warp's rows are first .. first + 31
 #pragma unroll 1
             for (int j0 = 0; j0 < kChunk; j0 += 16) {
                 float x[16];
-                const bool any = TREE || j0 <= (warp & 1) * 32 + 31;         // (else all of the warp's are zero)
-                if (any) {
+                if (!TREE && j0 >= first + 32) {             // nothing of it is seen
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[j] = 0.0f;
+                } else {
                     tmem_ld(mine + Y::kG + j0, x);
                     tmem_wait_ld(x);
-                    const uint32_t seen = (uint32_t)(above >> j0);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const float4 d = sc.decay[j0 + j];
-                        const float a = ex2((hi - d.x) + (lo - d.y));
-                        x[j] = seen >> j & 1 ? (own * a) * (d.z * x[j]) : 0.0f;
+                        x[j] = (own * ex2((hi - d.x) + (lo - d.y))) * (d.z * x[j]);
                     }
-                } else {
+                    if (TREE || j0 >= first) {
+                        const uint32_t seen = (uint32_t)(above >> j0);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) x[j] = 0.0f;
+                        for (int j = 0; j < 16; ++j) x[j] = seen >> j & 1 ? x[j] : 0.0f;
+                    }
                 }
                 if (key) {
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
                         *reinterpret_cast<float4*>(Li + j0 + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-                        zero = fmaf(x[j], 0.0f, fmaf(x[j + 1], 0.0f, fmaf(x[j + 2], 0.0f, fmaf(x[j + 3], 0.0f, zero))));
+                        zeros = fma2(pair_of(x[j], x[j + 1]), 0ull, fma2(pair_of(x[j + 2], x[j + 3]), 0ull, zeros));
                     }
                 } else if constexpr (HAS_Q) {
 #pragma unroll
@@ -606,16 +622,17 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
 #pragma unroll
                         for (int part = 0; part < 2; ++part) {
                             uint4 w;
-                            w.x = take_part(y[0]);
-                            w.y = take_part(y[1]);
-                            w.z = take_part(y[2]);
-                            w.w = take_part(y[3]);
+                            w.x = part == 1 ? last_part(y[0]) : take_part(y[0]);
+                            w.y = part == 1 ? last_part(y[1]) : take_part(y[1]);
+                            w.z = part == 1 ? last_part(y[2]) : take_part(y[2]);
+                            w.w = part == 1 ? last_part(y[3]) : take_part(y[3]);
                             *reinterpret_cast<uint4*>(P + part * Y::kTile + (((j0 / 8 + half) ^ (i & 7)) << 4)) = w;
                         }
                     }
                 }
             }
-            if (key && zero != 0.0f) {
+            const float2 zero = parts_of(zeros);
+            if (key && zero.x + zero.y != 0.0f) {
                 atomicOr(&sc.bad[i >> 5], 1u << (i & 31));
                 for (int j = 0; j < kChunk; j += 4) *reinterpret_cast<float4*>(Li + j) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
@@ -742,10 +759,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
 #pragma unroll
                     for (int part = 0; part < 3; ++part) {
                         uint4 w;
-                        w.x = take_part(y[0]);
-                        w.y = take_part(y[1]);
-                        w.z = take_part(y[2]);
-                        w.w = take_part(y[3]);
+                        w.x = part == 2 ? last_part(y[0]) : take_part(y[0]);
+                        w.y = part == 2 ? last_part(y[1]) : take_part(y[1]);
+                        w.z = part == 2 ? last_part(y[2]) : take_part(y[2]);
+                        w.w = part == 2 ? last_part(y[3]) : take_part(y[3]);
                         *reinterpret_cast<uint4*>(T + part * Y::kTile + (((half * 4 + x) ^ (r & 7)) << 4)) = w;
                     }
                 }
