@@ -39,7 +39,7 @@ constexpr int kMStride = 36;
 
 // Scalars of a chunk's tokens.
 struct Scalars {
-    float4 x[kChunk / 2];                    // X = x v + y W, of two tokens: x, x, y, y
+    ulonglong2 x[kChunk / 2];                // X = x v + y W, pairs of two tokens
     float2 o[kChunk];                        // o = o.x Y + o.y (U P^T)
     float last[kChunk];                      // A(n, i) / |k_i|
     float4 decay[kChunk];                    // two parts of the sum of the decays' logarithms (to base 2), 1 / |k|
@@ -64,17 +64,19 @@ struct Layout {
     static constexpr int kScalars = kM + 32 * kMStride * 4;
     static constexpr int kOut = kScalars + 2 * (int)sizeof(Scalars);         // outputs [64][D] on their way
     static constexpr int kBars = kOut + kChunk * D * 2;
-    // tensor memory, columns.  S's parts are 64 columns apart; X's third takes a place that W alone reads (of S's
-    // third), U that of S's first.  What is read by 32 tokens, W and U, is replaced by two parts of them: of tokens
-    // 32 i on in the columns 32 i and 32 i + 16 on.
+    // tensor memory, columns.  S's parts are 64 columns apart.  X's third part takes a place that W alone reads (of S's
+    // third), U, in two sums, those of S's first and second.  What 32 tokens' columns are read of, W and the products K K^T and
+    // Q K^T, is replaced by two parts of X and of u: of tokens 32 i on in the columns 32 i and 32 i + 16 on.  (A product
+    // takes at least 55 cycles, 80 with N = 128: so W and Y are one, and U's sums.)
     static constexpr int kS = 0, kParts = 128, kW = kParts + 192, kY = kW + 64, kG = kY + 64;
-    static constexpr int kX2 = kParts + 128, kU = kParts, kUleft = kParts + 64;
+    // (A(n, .) u's first two parts then lie where S's third was, its third as those.)
+    static constexpr int kX2 = kParts + 128, kU = kParts, kUleft = kParts + 128;
     static_assert(kG + 64 == 512, "tensor memory");
 };
 
 struct Barriers {
     uint64_t input_full[2], input_free[2], gram_full, gram_read, pairs_full[2], pairs_free[2], l_free, t_full[2], s_ready,
-        w_full, y_full, x_ready, u_full, u_ready, s_full, o_full;
+        w_full, x_ready, u_full, u_ready, s_full, o_full;
     uint32_t tmem;
     int failed;                              // a wait gave up
 };
@@ -266,7 +268,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
         mbar_init(&bars.l_free, kGroup);
         mbar_init(&bars.s_ready, 2 * kGroup);
         mbar_init(&bars.w_full, 1);
-        mbar_init(&bars.y_full, 1);
         mbar_init(&bars.x_ready, 2 * kGroup);
         mbar_init(&bars.u_full, 1);
         mbar_init(&bars.u_ready, 2 * kGroup);
@@ -386,10 +387,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 take_parts(first, s);
                 store_part(mine + Y::kParts + 64 + e / 2, s);
                 store_part<true>(mine + Y::kParts + 128 + e / 2, s);
-                if (HAS_Q && e == e0 && c > 0) {             // (u's parts, that the last outputs come from, are there)
-                    wait(&bars.o_full, (c - 1) & 1);
-                    umma_fence_after();
-                }
                 tmem_st16(mine + Y::kParts + e / 2, first);
             }
             if (HAS_Q && c > 0) take_outputs(c - 1);
@@ -405,16 +402,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
 
             // ---- X ----
             const uint16_t* v = reinterpret_cast<const uint16_t*>(input(c) + Y::kKq) + t0 * D + (live ? t : 0);
+            uint64_t own[16], x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) own[i] = mul2(sc.x[t0 / 2 + i].x, pair_of(bf16_lo(v[2 * i * D]), bf16_lo(v[(2 * i + 1) * D])));
             wait(&bars.w_full, c & 1);
             umma_fence_after();
-            uint64_t x[16];
             load_pairs(mine + Y::kW + t0, x);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float4 f = *reinterpret_cast<const float4*>(&sc.x[t0 / 2 + i]);
-                const uint64_t val = pair_of(bf16_lo(v[2 * i * D]), bf16_lo(v[(2 * i + 1) * D]));
-                x[i] = fma2(pair_of(f.z, f.w), x[i], mul2(pair_of(f.x, f.y), val));
-            }
+            for (int i = 0; i < 16; ++i) x[i] = fma2(sc.x[t0 / 2 + i].y, x[i], own[i]);
             uint32_t lost = not_finite(x);
             store_part(mine + Y::kW + t0, x);
             store_part(mine + Y::kW + t0 + 16, x);
@@ -424,27 +419,41 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             mbar_arrive(&bars.x_ready);
 
             // ---- u, as an operand ----
+            uint64_t last[16];
+            if constexpr (!TREE)
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&sc.last[t0 + 2 * i]);
+                    last[i] = f.x;
+                    last[i + 1] = f.y;
+                }
             wait(&bars.u_full, c & 1);
             umma_fence_after();
-            load_pairs(mine + Y::kU + t0, x);
+            {
+                uint64_t y[16];
+                load_pairs(mine + Y::kU + t0, x);
+                load_pairs(mine + Y::kU + 64 + t0, y);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = add2(x[i], y[i]);
+            }
             lost |= not_finite(x);
             sc.lost[half][t] = lost;
             if constexpr (!TREE) {
                 uint64_t y[16];
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&sc.last[t0 + 2 * i]);
-                    y[i] = mul2(f.x, x[i]);
-                    y[i + 1] = mul2(f.y, x[i + 1]);
-                }
+                for (int i = 0; i < 16; ++i) y[i] = mul2(last[i], x[i]);
                 if (lost | sc.bad[0] | sc.bad[1]) y[0] = pair_of(__int_as_float(0x7FC00000), 0.0f);     // into the state
                 store_part(mine + Y::kUleft + t0 / 2, y);
                 store_part(mine + Y::kUleft + 32 + t0 / 2, y);
-                store_part<true>(mine + Y::kUleft + 64 + t0 / 2, y);
+                store_part<true>(mine + Y::kU + t0, y);
             }
             if constexpr (HAS_Q) {
-                store_part(mine + Y::kU + t0, x);
-                store_part<true>(mine + Y::kU + t0 + 16, x);
+                if (c + 1 < chunks) {                        // (the next chunk's K K^T and Q K^T are read)
+                    wait(&bars.gram_read, (c + 1) & 1);
+                    umma_fence_after();
+                }
+                store_part(mine + Y::kG + t0, x);
+                store_part<true>(mine + Y::kG + t0 + 16, x);
             }
             tmem_wait_st();
             umma_fence_before();
@@ -785,12 +794,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             }
             umma_commit(&bars.gram_full);
         };
-        // D[tmem] (+)= A[tmem] B^T with lower triangular B [64][64]: its columns from 16 k on are read by row 16 k and later
-        auto triangular = [&](uint32_t d, uint32_t a, int apart, uint32_t b_tile, bool first) {
+        // D[tmem] (+)= A[tmem] B^T with B [N][64]; A's tokens from 32 on `apart` columns after the others
+        auto by_tokens = [&](uint32_t d, uint32_t a, int apart, uint32_t b_tile, uint32_t idesc, bool first) {
 #pragma unroll
             for (int k = 0; k < kChunk / 16; ++k)
-                umma_bf16_tmem(d + 16 * k, a + (k >> 1) * apart + (k & 1) * 8, umma_sdesc_sw128(b_tile + k * (16 * 128 + 32)),
-                               idesc_bf16(64 - 16 * k, false), !first || k > 0);
+                umma_bf16_tmem(d, a + (k >> 1) * apart + (k & 1) * 8, umma_sdesc_sw128(b_tile + k * 32), idesc, !first || k > 0);
         };
         gram(0);
 #pragma unroll 1
@@ -798,23 +806,15 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             const uint32_t kq = smem_u32(input(c)), pp = smem_u32(p_of(c)), tt = smem_u32(t_of(c));
             wait(&bars.s_ready, c & 1);
             umma_fence_after();
+            // W, with three parts of S, and Y beside it, with two
 #pragma unroll
             for (int part = 0; part < 3; ++part)
 #pragma unroll
                 for (int k = 0; k < KS; ++k)
                     umma_bf16_tmem(tmem + Y::kW, tmem + Y::kParts + part * 64 + k * 8,
-                                   umma_sdesc_sw128(kq + (k >> 2) * (2 * Y::kTile) + (k & 3) * 32), kById, part + k > 0);
+                                   umma_sdesc_sw128(kq + (k >> 2) * (2 * Y::kTile) + (k & 3) * 32),
+                                   HAS_Q && part < 2 ? idesc_bf16(128, false) : kById, part + k > 0);
             umma_commit(&bars.w_full);
-            if constexpr (HAS_Q) {
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int k = 0; k < KS; ++k)
-                        umma_bf16_tmem(tmem + Y::kY, tmem + Y::kParts + part * 64 + k * 8,
-                                       umma_sdesc_sw128(kq + (k >> 2) * (2 * Y::kTile) + Y::kTile + (k & 3) * 32), kById,
-                                       part + k > 0);
-                umma_commit(&bars.y_full);
-            }
             if (c + 1 < chunks) {
                 wait(&bars.gram_read, c & 1);
                 umma_fence_after();
@@ -822,16 +822,12 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             }
             wait(&bars.x_ready, c & 1);
             wait(&bars.t_full[c & 1], (c >> 1) & 1);
-            if (HAS_Q) wait(&bars.y_full, c & 1);            // (U takes the place of the parts that Y is of)
             umma_fence_after();
-            // parts (X, T): (0, 0), (0, 1), (1, 0), (0, 2), (1, 1), (2, 0)
-            const uint32_t x0 = tmem + Y::kW, x1 = x0 + 16, x2 = tmem + Y::kX2;
-            triangular(tmem + Y::kU, x0, 32, tt, true);
-            triangular(tmem + Y::kU, x0, 32, tt + Y::kTile, false);
-            triangular(tmem + Y::kU, x1, 32, tt, false);
-            triangular(tmem + Y::kU, x0, 32, tt + 2 * Y::kTile, false);
-            triangular(tmem + Y::kU, x1, 32, tt + Y::kTile, false);
-            triangular(tmem + Y::kU, x2, 16, tt, false);
+            // parts (X, T): (0, 0) and (0, 1), (1, 0) and (1, 1), (0, 2), (2, 0)
+            by_tokens(tmem + Y::kU, tmem + Y::kW, 32, tt, idesc_bf16(128, false), true);
+            by_tokens(tmem + Y::kU, tmem + Y::kW + 16, 32, tt, idesc_bf16(128, false), false);
+            by_tokens(tmem + Y::kU, tmem + Y::kW, 32, tt + 2 * Y::kTile, kById, false);
+            by_tokens(tmem + Y::kU, tmem + Y::kX2, 16, tt, kById, false);
             umma_commit(&bars.u_full);
             wait(&bars.u_ready, c & 1);
             umma_fence_after();
@@ -840,15 +836,16 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 for (int part = 0; part < 3; ++part)
 #pragma unroll
                     for (int k = 0; k < kChunk / 16; ++k)
-                        umma_bf16_tmem(tmem + Y::kS, tmem + Y::kUleft + part * 32 + k * 8,
+                        umma_bf16_tmem(tmem + Y::kS,
+                                       tmem + (part < 2 ? Y::kUleft + part * 32 + k * 8 : Y::kU + (k >> 1) * 32 + (k & 1) * 8),
                                        sdesc_n_contiguous(kq + k * 2048, 2 * Y::kTile), kUpdate, true);
                 umma_commit(&bars.s_full);
             }
             if constexpr (HAS_Q) {
                 wait(&bars.pairs_full[c & 1], (c >> 1) & 1);
-                triangular(tmem + Y::kW, tmem + Y::kU, 32, pp, true);
-                triangular(tmem + Y::kW, tmem + Y::kU, 32, pp + Y::kTile, false);
-                triangular(tmem + Y::kW, tmem + Y::kU + 16, 32, pp, false);
+                by_tokens(tmem + Y::kW, tmem + Y::kG, 32, pp, kById, true);
+                by_tokens(tmem + Y::kW, tmem + Y::kG, 32, pp + Y::kTile, kById, false);
+                by_tokens(tmem + Y::kW, tmem + Y::kG + 16, 32, pp, kById, false);
             }
             umma_commit(&bars.o_full);
             umma_commit(&bars.input_free[c & 1]);
