@@ -36,13 +36,14 @@ constexpr int kGroup = 128;                  // threads of the tokens, and of T;
 constexpr int kThreads = 4 * kGroup + 32;
 constexpr int kLStride = 68;                 // floats between rows of L: eight rows' 16-byte pieces lie in different banks
 constexpr int kMStride = 36;
+constexpr int kSorted = 256;                 // sequences that are put in order
 
 // Scalars of a chunk's tokens.
 struct Scalars {
     ulonglong2 x[kChunk / 2];                // X = x v + y W, pairs of two tokens
-    float2 o[kChunk];                        // o = o.x Y + o.y (U P^T)
+    float fade[kChunk], o[kChunk];           // o = o (fade Y + U P^T)
     float last[kChunk];                      // A(n, i) / |k_i|
-    float4 decay[kChunk];                    // two parts of the sum of the decays' logarithms (to base 2), 1 / |k|
+    float4 decay[kChunk];                    // two parts of the sum of the decays' logarithms (to base 2); 1 / |k|
     uint64_t above[kChunk];                  // (of a tree)
     uint32_t lost[2][kGroup];                // tokens without a finite X or u, by half and row
     int parents[kChunk];
@@ -58,16 +59,16 @@ struct Layout {
     static constexpr int kKq = kHalves * 2 * kTile;          // of each 64 elements: K's rows, then Q's
     static constexpr int kInput = kKq + kChunk * D * 2;      // and V [64][D]
     static constexpr int kP = 2 * kInput;                    // twice P's two parts
-    static constexpr int kT = kP + 4 * kTile;                // twice T's three
-    static constexpr int kL = kT + 6 * kTile;
-    static constexpr int kM = kL + kChunk * kLStride * 4;
+    static constexpr int kT = kP + 4 * kTile;                // T's three
+    static constexpr int kL = kT + 3 * kTile;                // L, twice
+    static constexpr int kM = kL + 2 * kChunk * kLStride * 4;
     static constexpr int kScalars = kM + 32 * kMStride * 4;
     static constexpr int kOut = kScalars + 2 * (int)sizeof(Scalars);         // outputs [64][D] on their way
     static constexpr int kBars = kOut + kChunk * D * 2;
     // tensor memory, columns.  S's parts are 64 columns apart.  X's third part takes a place that W alone reads (of S's
-    // third), U, in two sums, those of S's first and second.  What 32 tokens' columns are read of, W and the products K K^T and
-    // Q K^T, is replaced by two parts of X and of u: of tokens 32 i on in the columns 32 i and 32 i + 16 on.  (A product
-    // takes at least 55 cycles, 80 with N = 128: so W and Y are one, and U's sums.)
+    // third), U, in two sums, those of S's first and second.  W is replaced by two parts of X and they by two of u: of
+    // tokens 32 i on in the columns 32 i and 32 i + 16 on; U P^T adds to A(., 0) Y.  (A product takes at least 55 cycles,
+    // 80 with N = 128: so W and Y are one, and U's sums.)
     static constexpr int kS = 0, kParts = 128, kW = kParts + 192, kY = kW + 64, kG = kY + 64;
     // (A(n, .) u's first two parts then lie where S's third was, its third as those.)
     static constexpr int kX2 = kParts + 128, kU = kParts, kUleft = kParts + 128;
@@ -75,7 +76,7 @@ struct Layout {
 };
 
 struct Barriers {
-    uint64_t input_full[2], input_free[2], gram_full, gram_read, pairs_full[2], pairs_free[2], l_free, t_full[2], s_ready,
+    uint64_t input_full[2], q_free[2], v_free[2], k_free[2], gram_full, gram_read, pairs_full[2], pairs_free[2], l_free[2], t_full, s_ready,
         w_full, x_ready, u_full, u_ready, s_full, o_full;
     uint32_t tmem;
     int failed;                              // a wait gave up
@@ -219,7 +220,23 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
     extern __shared__ uint8_t raw[];
     begin_chained();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = tid & (kGroup - 1);
-    const int b = blockIdx.x / p.Hv, h = blockIdx.x - b * p.Hv, hk = h / p.ratio;
+    const int rank = blockIdx.x / p.Hv, h = blockIdx.x - rank * p.Hv, hk = h / p.ratio;
+    // The longest sequences first, so that no long one begins when the others end (16 of 64 to 2000 tokens, 512 heads:
+    // FIGURES); the order of many is not worth finding.
+    int b = rank;
+    if (p.cu && p.B <= kSorted) {
+        int* lens = reinterpret_cast<int*>(raw);
+        for (int x = tid; x < p.B; x += kThreads) lens[x] = p.cu[x + 1] - p.cu[x];
+        __syncthreads();
+        for (int x = tid; x < p.B; x += kThreads) {
+            int before = 0;
+            for (int y = 0; y < p.B; ++y) before += lens[y] > lens[x] || (lens[y] == lens[x] && y < x);
+            if (before == rank) lens[kSorted] = x;
+        }
+        __syncthreads();
+        b = lens[kSorted];
+        __syncthreads();
+    }
     int n;
     int64_t row0;
     delta_tokens(p, b, n, row0);
@@ -250,22 +267,24 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
     const int chunks = (n + kChunk - 1) / kChunk;
     uint8_t* smem = raw + (1024u - smem_u32(raw) % 1024u) % 1024u;
     Barriers& bars = *reinterpret_cast<Barriers*>(smem + Y::kBars);
-    float* const L = reinterpret_cast<float*>(smem + Y::kL);
     auto input = [&](int c) { return smem + (c & 1) * Y::kInput; };
     auto p_of = [&](int c) { return smem + Y::kP + (c & 1) * 2 * Y::kTile; };
-    auto t_of = [&](int c) { return smem + Y::kT + (c & 1) * 3 * Y::kTile; };
+    auto l_of = [&](int c) { return reinterpret_cast<float*>(smem + Y::kL) + (c & 1) * (kChunk * kLStride); };
+    uint8_t* const parts_of_t = smem + Y::kT;
     auto scalars_of = [&](int c) { return reinterpret_cast<Scalars*>(smem + Y::kScalars) + (c & 1); };
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.input_full[i], kGroup);
-            mbar_init(&bars.input_free[i], 1);
+            mbar_init(&bars.q_free[i], 1);
+            mbar_init(&bars.v_free[i], 1);
+            mbar_init(&bars.k_free[i], 1);
             mbar_init(&bars.pairs_full[i], kGroup);
             mbar_init(&bars.pairs_free[i], 2 * kGroup);
-            mbar_init(&bars.t_full[i], kGroup);
+            mbar_init(&bars.l_free[i], kGroup);
         }
         mbar_init(&bars.gram_full, 1);
         mbar_init(&bars.gram_read, kGroup);
-        mbar_init(&bars.l_free, kGroup);
+        mbar_init(&bars.t_full, kGroup);
         mbar_init(&bars.s_ready, 2 * kGroup);
         mbar_init(&bars.w_full, 1);
         mbar_init(&bars.x_ready, 2 * kGroup);
@@ -307,15 +326,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             const Scalars& sc = *scalars_of(c);
             wait(&bars.o_full, c & 1);
             umma_fence_after();
-            float y[32], z[32];
+            float y[32];
             tmem_ld(mine + Y::kY + t0, y);
-            tmem_ld(mine + Y::kW + t0, z);
             tmem_wait_ld(y);
-            tmem_wait_ld(z);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
+            for (int i = 0; i < 32; i += 4) {
                 const float4 f = *reinterpret_cast<const float4*>(&sc.o[t0 + i]);
-                out[i / 2] = pack_bf16x2(fmaf(f.x, y[i], f.y * z[i]), fmaf(f.z, y[i + 1], f.w * z[i + 1]));
+                out[i / 2] = pack_bf16x2(f.x * y[i], f.y * y[i + 1]);
+                out[i / 2 + 1] = pack_bf16x2(f.z * y[i + 2], f.w * y[i + 3]);
             }
             uint64_t lost = (uint64_t)sc.lost[1][t] << 32 | sc.lost[0][t] | *reinterpret_cast<const uint64_t*>(sc.bad);
             if (lost) {                      // NaN, and what comes from it
@@ -418,42 +436,52 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             umma_fence_before();
             mbar_arrive(&bars.x_ready);
 
-            // ---- u, as an operand ----
-            uint64_t last[16];
-            if constexpr (!TREE)
+            // ---- Y, as it goes into the outputs ----
+            if constexpr (HAS_Q) {
+                load_pairs(mine + Y::kY + t0, x);
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&sc.last[t0 + 2 * i]);
-                    last[i] = f.x;
-                    last[i + 1] = f.y;
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t y[16];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 f = parts_of(mul2(*reinterpret_cast<const uint64_t*>(&sc.fade[t0 + 16 * i + 2 * j]), x[i * 8 + j]));
+                        y[2 * j] = __float_as_uint(f.x);
+                        y[2 * j + 1] = __float_as_uint(f.y);
+                    }
+                    tmem_st16(mine + Y::kY + t0 + i * 16, y);
                 }
+            }
+
+            // ---- u, as an operand ----
             wait(&bars.u_full, c & 1);
             umma_fence_after();
-            {
-                uint64_t y[16];
-                load_pairs(mine + Y::kU + t0, x);
-                load_pairs(mine + Y::kU + 64 + t0, y);
+            load_pairs(mine + Y::kU + t0, x);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = add2(x[i], y[i]);
+            for (int i = 0; i < 2; ++i) {
+                float y[16];
+                tmem_ld(mine + Y::kU + 64 + t0 + i * 16, y);
+                tmem_wait_ld(y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[i * 8 + j] = add2(x[i * 8 + j], pair_of(y[2 * j], y[2 * j + 1]));
             }
             lost |= not_finite(x);
             sc.lost[half][t] = lost;
             if constexpr (!TREE) {
                 uint64_t y[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = mul2(last[i], x[i]);
+                for (int i = 0; i < 16; i += 2) {
+                    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&sc.last[t0 + 2 * i]);
+                    y[i] = mul2(f.x, x[i]);
+                    y[i + 1] = mul2(f.y, x[i + 1]);
+                }
                 if (lost | sc.bad[0] | sc.bad[1]) y[0] = pair_of(__int_as_float(0x7FC00000), 0.0f);     // into the state
                 store_part(mine + Y::kUleft + t0 / 2, y);
                 store_part(mine + Y::kUleft + 32 + t0 / 2, y);
                 store_part<true>(mine + Y::kU + t0, y);
             }
             if constexpr (HAS_Q) {
-                if (c + 1 < chunks) {                        // (the next chunk's K K^T and Q K^T are read)
-                    wait(&bars.gram_read, (c + 1) & 1);
-                    umma_fence_after();
-                }
-                store_part(mine + Y::kG + t0, x);
-                store_part<true>(mine + Y::kG + t0 + 16, x);
+                store_part(mine + Y::kW + t0, x);
+                store_part<true>(mine + Y::kW + t0 + 16, x);
             }
             tmem_wait_st();
             umma_fence_before();
@@ -493,18 +521,35 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
         const uint16_t* kp = p.k + b * p.k_bs + hk * p.k_hs + piece * 8;
         const uint16_t* qp = HAS_Q ? p.q + b * p.q_bs + hk * p.q_hs + piece * 8 : nullptr;
         const uint16_t* vp = p.v + b * p.v_bs + h * p.v_hs + piece * 8;
-        auto load = [&](int c) {
-            const uint32_t base = smem_u32(input(c));
-#pragma unroll 4
-            for (int r = r0; r < kChunk; r += STEP) {
-                const int at = c * kChunk + r;
-                const bool here = at < n;
-                const int64_t token = here ? place(at) : 0;
-                const uint32_t swizzled = tile + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
-                copy16(base + swizzled, here ? kp + token * p.k_ts : p.k, here);
-                if (HAS_Q) copy16(base + Y::kTile + swizzled, here ? qp + token * p.q_ts : p.k, here);
-                copy16(base + Y::kKq + r * (D * 2) + piece * 16, here ? vp + token * p.v_ts : p.k, here);
+        enum { kKeys, kQueries, kValues };
+        auto load = [&](int what, int c) {
+            const uint32_t base = smem_u32(input(c)) + (what == kValues ? Y::kKq + r0 * (D * 2) + piece * 16
+                                                                        : tile + what * Y::kTile + r0 * 128);
+            const uint16_t* src = what == kKeys ? kp : what == kQueries ? qp : vp;
+            const int64_t stride = what == kKeys ? p.k_ts : what == kQueries ? p.q_ts : p.v_ts;
+            if (c * kChunk + kChunk <= n && MODE != kDeltaCommit) {
+                src += place(c * kChunk + r0) * stride;
+#pragma unroll
+                for (int x = 0; x < kChunk / STEP; ++x) {
+                    const uint32_t dst = what == kValues ? base + x * (STEP * D * 2)
+                                                         : base + x * (STEP * 128) + (((piece & 7) ^ ((r0 + x * STEP) & 7)) << 4);
+                    copy16(dst, src, true);
+                    src += STEP * stride;
+                }
+            } else {                         // zeros behind the last token
+#pragma unroll 1
+                for (int x = 0; x < kChunk / STEP; ++x) {
+                    const int at = c * kChunk + r0 + x * STEP;
+                    const uint32_t dst = what == kValues ? base + x * (STEP * D * 2)
+                                                         : base + x * (STEP * 128) + (((piece & 7) ^ ((r0 + x * STEP) & 7)) << 4);
+                    copy16(dst, at < n ? src + place(at) * stride : p.k, at < n);
+                }
             }
+        };
+        auto load_all = [&](int c) {
+            load(kKeys, c);
+            if (HAS_Q) load(kQueries, c);
+            load(kValues, c);
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         auto loaded = [&](int c) {
@@ -527,6 +572,19 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             const float beta = g_next == g_next ? beta_next : g_next;
             const long long g = __float2ll_rn(fminf(fmaxf(g_next, -200.0f), 200.0f) * (1.4426950408889634f * 0x1p40f));
             if (c + 1 < chunks) load_rates(c + 1);
+            // the row's length
+            wait(&bars.input_full[c & 1], (c >> 1) & 1);
+            float square = 0.0f;
+            if (key || HAS_Q) {
+                const uint8_t* row = input(c) + t * 128;     // (K's rows, then Q's)
+#pragma unroll
+                for (int x = 0; x < D / 8; ++x) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(row + (x >> 3) * (2 * Y::kTile) + (((x & 7) ^ (t & 7)) << 4));
+                    const Eight e = unpack(q);
+                    square += dot(e, e);
+                }
+            }
+            const float r = at < n ? rsqrtf(square + p.eps) : 0.0f;
             if (c >= 2) wait(&bars.pairs_free[c & 1], ((c - 2) >> 1) & 1);
             uint64_t above = ~0ull >> (63 - i);
             long long sum = 0, end = 0;
@@ -558,19 +616,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 end = halves[0] + halves[1];
                 if (i >= 32) sum += halves[0];
             }
-            // the row's length
-            float square = 0.0f;
-            if (key || HAS_Q) {
-                wait(&bars.input_full[c & 1], (c >> 1) & 1);
-                const uint8_t* rows = input(c) + (key ? 0 : Y::kTile) + i * 128;
-#pragma unroll
-                for (int x = 0; x < D / 8; ++x) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(rows + (x >> 3) * (2 * Y::kTile) + (((x & 7) ^ (i & 7)) << 4));
-                    const Eight e = unpack(q);
-                    square += dot(e, e);
-                }
-            }
-            const float r = at < n ? rsqrtf(square + p.eps) : 0.0f;
             // (the sum is under 2^55: its upper word is exact as a float)
             const float hi = (float)(int)(sum >> 32) * 0x1p-8f, lo = (float)(uint32_t)sum * 0x1p-40f, fade = ex2(hi + lo);
             if (key) {
@@ -580,19 +625,20 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 x[2] = -(beta * fade * r);
                 if (!TREE) sc.last[i] = ex2((float)(end - sum) * 0x1p-40f) * r;
             } else {
-                sc.o[i] = make_float2(r * p.scale * fade, r * p.scale);
+                sc.fade[i] = fade;
+                sc.o[i] = r * p.scale;
             }
             if (t == 0) {
                 sc.end = ex2((float)end * 0x1p-40f);
                 sc.bad[0] = sc.bad[1] = 0;
             }
             group_barrier<1>();
-            if (c > 0) wait(&bars.l_free, (c - 1) & 1);
+            if (c >= 2) wait(&bars.l_free[c & 1], ((c - 2) >> 1) & 1);
             wait(&bars.gram_full, c & 1);
             umma_fence_after();
             const float own = key ? beta * r : 1.0f;
             if (key) above &= ~(1ull << i);
-            float* Li = L + i * kLStride;
+            float* Li = l_of(c) + i * kLStride;
             uint8_t* P = p_of(c) + i * 128;
             uint64_t zeros = 0;              // NaN where a value of the row is not finite
             const int first = (warp & 1) * 32;               // the warp's rows are first .. first + 31
@@ -651,27 +697,34 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             mbar_arrive(&bars.pairs_full[c & 1]);
         };
         load_rates(0);
-        load(0);
+        load_all(0);
         loaded(0);
-        if (chunks > 1) load(1);
-        pairs(0);
+        if (chunks > 1) load_all(1);
         if (chunks > 1) loaded(1);
+        pairs(0);
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             if (c + 1 < chunks) pairs(c + 1);
-            if (c + 2 < chunks) {
-                wait(&bars.input_free[c & 1], (c >> 1) & 1);
-                load(c + 2);
+            if (c + 2 < chunks) {            // each as soon as this chunk's is used
+                wait(&bars.q_free[c & 1], (c >> 1) & 1);
+                if (HAS_Q) load(kQueries, c + 2);
+                wait(&bars.v_free[c & 1], (c >> 1) & 1);
+                load(kValues, c + 2);
+                wait(&bars.k_free[c & 1], (c >> 1) & 1);
+                load(kKeys, c + 2);
+                asm volatile("cp.async.commit_group;" ::: "memory");
                 loaded(c + 2);
             }
         }
     } else if (warp < 16) {
         // ------------------------------------------------------------ L into T --
         float* const M = reinterpret_cast<float*>(smem + Y::kM);
-        auto l4 = [&](int r, int col) { return *reinterpret_cast<const float4*>(L + r * kLStride + col); };
+        auto pairs4 = [](const float* at) { return *reinterpret_cast<const ulonglong2*>(at); };
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             wait(&bars.pairs_full[c & 1], (c >> 1) & 1);
+            float* const L = l_of(c);
+            auto l4 = [&](int r, int col) { return *reinterpret_cast<const float4*>(L + r * kLStride + col); };
             // blocks of 16 on the diagonal, a column a thread
             if (t < 64) {
                 const int at = t & 48, col = t & 15;
@@ -698,69 +751,62 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             {
                 const int at = (t >> 6) * 32, r = (t & 63) >> 2, col = (t & 3) * 4;
                 float* m = M + (t >> 6) * (16 * kMStride);
-                float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-                for (int k = 0; k < 16; k += 4) {
-                    const float4 l = l4(at + 16 + r, at + k);
-                    const float w[4] = {l.x, l.y, l.z, l.w};
+                for (int pass = 0; pass < 2; ++pass) {
+                    uint64_t s[2] = {};
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float4 y = l4(at + k + x, at + col);
-                        s = make_float4(fmaf(w[x], y.x, s.x), fmaf(w[x], y.y, s.y), fmaf(w[x], y.z, s.z), fmaf(w[x], y.w, s.w));
+                    for (int k = 0; k < 16; k += 4) {
+                        const float4 l = l4(at + 16 + r, at + pass * 16 + k);
+                        const float w[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const ulonglong2 y = pass == 0 ? pairs4(L + (at + k + x) * kLStride + at + col)
+                                                           : pairs4(m + (k + x) * kMStride + col);
+                            const uint64_t f = pass == 0 ? pair_of(w[x], w[x]) : pair_of(-w[x], -w[x]);
+                            s[0] = fma2(f, y.x, s[0]);
+                            s[1] = fma2(f, y.y, s[1]);
+                        }
                     }
+                    float* out = pass == 0 ? m + r * kMStride + col : L + (at + 16 + r) * kLStride + at + col;
+                    *reinterpret_cast<ulonglong2*>(out) = make_ulonglong2(s[0], s[1]);
+                    group_barrier<2>();
                 }
-                *reinterpret_cast<float4*>(m + r * kMStride + col) = s;
-                group_barrier<2>();
-                s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int k = 0; k < 16; k += 4) {
-                    const float4 l = l4(at + 16 + r, at + 16 + k);
-                    const float w[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float4 y = *reinterpret_cast<const float4*>(m + (k + x) * kMStride + col);
-                        s = make_float4(fmaf(w[x], y.x, s.x), fmaf(w[x], y.y, s.y), fmaf(w[x], y.z, s.z), fmaf(w[x], y.w, s.w));
-                    }
-                }
-                *reinterpret_cast<float4*>(L + (at + 16 + r) * kLStride + at + col) = make_float4(-s.x, -s.y, -s.z, -s.w);
             }
-            group_barrier<2>();
             // of 64, two rows and four columns a thread
             {
                 const int r = (t >> 3) * 2, col = (t & 7) * 4;
 #pragma unroll
                 for (int pass = 0; pass < 2; ++pass) {
                     const int most = pass == 0 ? 32 : (warp & 3) * 8 + 8;    // (T22's rows end at the diagonal)
-                    float4 s[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+                    uint64_t s[2][2] = {};
 #pragma unroll 2
                     for (int k = 0; k < most; k += 4) {
                         const float4 l0 = l4(32 + r, pass * 32 + k), l1 = l4(33 + r, pass * 32 + k);
                         const float w[2][4] = {{l0.x, l0.y, l0.z, l0.w}, {l1.x, l1.y, l1.z, l1.w}};
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const float4 y = pass == 0 ? l4(k + x, col)
-                                                       : *reinterpret_cast<const float4*>(M + (k + x) * kMStride + col);
+                            const ulonglong2 y = pass == 0 ? pairs4(L + (k + x) * kLStride + col) : pairs4(M + (k + x) * kMStride + col);
 #pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                s[i] = make_float4(fmaf(w[i][x], y.x, s[i].x), fmaf(w[i][x], y.y, s[i].y),
-                                                   fmaf(w[i][x], y.z, s[i].z), fmaf(w[i][x], y.w, s[i].w));
+                            for (int i = 0; i < 2; ++i) {
+                                const uint64_t f = pass == 0 ? pair_of(w[i][x], w[i][x]) : pair_of(-w[i][x], -w[i][x]);
+                                s[i][0] = fma2(f, y.x, s[i][0]);
+                                s[i][1] = fma2(f, y.y, s[i][1]);
+                            }
                         }
                     }
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        if (pass == 0)
-                            *reinterpret_cast<float4*>(M + (r + i) * kMStride + col) = s[i];
-                        else
-                            *reinterpret_cast<float4*>(L + (32 + r + i) * kLStride + col) =
-                                make_float4(-s[i].x, -s[i].y, -s[i].z, -s[i].w);
+                        float* out = pass == 0 ? M + (r + i) * kMStride + col : L + (32 + r + i) * kLStride + col;
+                        *reinterpret_cast<ulonglong2*>(out) = make_ulonglong2(s[i][0], s[i][1]);
                     }
                     group_barrier<2>();
                 }
             }
             // its parts, half a row a thread
+            if (c > 0) wait(&bars.v_free[(c - 1) & 1], ((c - 1) >> 1) & 1);      // (the last chunk's are used)
             {
                 const int r = t >> 1, half = t & 1;
-                uint8_t* T = t_of(c) + r * 128;
+                uint8_t* T = parts_of_t + r * 128;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const float4 a = l4(r, half * 32 + x * 8), d = l4(r, half * 32 + x * 8 + 4);
@@ -777,8 +823,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 }
             }
             fence_proxy_async_smem();
-            mbar_arrive(&bars.t_full[c & 1]);
-            mbar_arrive(&bars.l_free);
+            mbar_arrive(&bars.t_full);
+            mbar_arrive(&bars.l_free[c & 1]);
         }
     } else if (lane == 0) {
         // ------------------------------------------------------------ products --
@@ -803,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
         gram(0);
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-            const uint32_t kq = smem_u32(input(c)), pp = smem_u32(p_of(c)), tt = smem_u32(t_of(c));
+            const uint32_t kq = smem_u32(input(c)), pp = smem_u32(p_of(c)), tt = smem_u32(parts_of_t);
             wait(&bars.s_ready, c & 1);
             umma_fence_after();
             // W, with three parts of S, and Y beside it, with two
@@ -815,13 +861,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                                    umma_sdesc_sw128(kq + (k >> 2) * (2 * Y::kTile) + (k & 3) * 32),
                                    HAS_Q && part < 2 ? idesc_bf16(128, false) : kById, part + k > 0);
             umma_commit(&bars.w_full);
+            umma_commit(&bars.q_free[c & 1]);
             if (c + 1 < chunks) {
                 wait(&bars.gram_read, c & 1);
                 umma_fence_after();
                 gram(c + 1);
             }
             wait(&bars.x_ready, c & 1);
-            wait(&bars.t_full[c & 1], (c >> 1) & 1);
+            wait(&bars.t_full, c & 1);
             umma_fence_after();
             // parts (X, T): (0, 0) and (0, 1), (1, 0) and (1, 1), (0, 2), (2, 0)
             by_tokens(tmem + Y::kU, tmem + Y::kW, 32, tt, idesc_bf16(128, false), true);
@@ -829,6 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             by_tokens(tmem + Y::kU, tmem + Y::kW, 32, tt + 2 * Y::kTile, kById, false);
             by_tokens(tmem + Y::kU, tmem + Y::kX2, 16, tt, kById, false);
             umma_commit(&bars.u_full);
+            umma_commit(&bars.v_free[c & 1]);
             wait(&bars.u_ready, c & 1);
             umma_fence_after();
             if constexpr (!TREE) {
@@ -841,17 +889,17 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                                        sdesc_n_contiguous(kq + k * 2048, 2 * Y::kTile), kUpdate, true);
                 umma_commit(&bars.s_full);
             }
+            umma_commit(&bars.k_free[c & 1]);
             if constexpr (HAS_Q) {
                 wait(&bars.pairs_full[c & 1], (c >> 1) & 1);
-                by_tokens(tmem + Y::kW, tmem + Y::kG, 32, pp, kById, true);
-                by_tokens(tmem + Y::kW, tmem + Y::kG, 32, pp + Y::kTile, kById, false);
-                by_tokens(tmem + Y::kW, tmem + Y::kG + 16, 32, pp, kById, false);
+                by_tokens(tmem + Y::kY, tmem + Y::kW, 32, pp, kById, false);
+                by_tokens(tmem + Y::kY, tmem + Y::kW, 32, pp + Y::kTile, kById, false);
+                by_tokens(tmem + Y::kY, tmem + Y::kW + 16, 32, pp, kById, false);
             }
             umma_commit(&bars.o_full);
-            umma_commit(&bars.input_free[c & 1]);
         }
         // all products are done, whatever else gave up
-        if (!mbar_wait(&bars.input_free[(chunks - 1) & 1], ((chunks - 1) >> 1) & 1)) record_error(p.err, kErrTimeout);
+        if (!mbar_wait(&bars.o_full, (chunks - 1) & 1)) record_error(p.err, kErrTimeout);
     }
     __syncwarp();
     umma_fence_before();
