@@ -75,7 +75,7 @@ __device__ __forceinline__ void unit_vector(const uint16_t* src, float* dst, flo
 }
 
 template <int D, DeltaMode MODE>
-__global__ void __launch_bounds__(kThreads) delta_rows_kernel(const DeltaParams p) {
+__global__ void __launch_bounds__(kThreads, MODE == kDeltaTree ? 1 : 4) delta_rows_kernel(const DeltaParams p) {
     constexpr int PARTS = D / (kWarps * kRows), M = D / 32;  // CTAs of a head; 16-byte pieces of a row that a lane has
     constexpr bool TREE = MODE == kDeltaTree, HAS_Q = MODE != kDeltaCommit;
     constexpr int KEPT = Shared<D, MODE>::kKept;
@@ -282,6 +282,96 @@ __global__ void __launch_bounds__(kThreads) delta_rows_kernel(const DeltaParams 
     }
 }
 
+// The eight elements' pairs that a lane has of a bf16 head vector (those of its share of a state's row), and the vector's
+// 1 / length.
+template <int D>
+__device__ __forceinline__ float lane_vector(const uint16_t* src, int c, uint64_t (&x)[D / 16], float eps) {
+    uint64_t sum = 0;
+#pragma unroll
+    for (int m = 0; m < D / 32; ++m) {
+        const uint2 w = *reinterpret_cast<const uint2*>(src + m * 32 + c * 4);
+        x[2 * m] = pair_of(bf16_lo(w.x), bf16_hi(w.x));
+        x[2 * m + 1] = pair_of(bf16_lo(w.y), bf16_hi(w.y));
+        sum = fma2(x[2 * m], x[2 * m], sum);
+        sum = fma2(x[2 * m + 1], x[2 * m + 1], sum);
+    }
+    const float2 f = parts_of(sum);
+    return rsqrtf(group_sum<8>(f.x + f.y) + eps);
+}
+
+// One token a sequence: every warp for itself, without shared memory.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 4) delta_one_kernel(const DeltaParams p) {
+    constexpr int PARTS = D / (kWarps * kRows), M = D / 32;
+    begin_chained();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 7, r = lane >> 3;
+    const int part = blockIdx.x % PARTS, bh = blockIdx.x / PARTS, b = bh / p.Hv, h = bh - b * p.Hv, hk = h / p.ratio;
+    const int row0 = (part * kWarps + warp) * kRows, own = row0 + r + 4 * (c >> 1);
+    const int first_slot = p.slots[b];
+    float* rows = p.state + (((int64_t)(first_slot >= 0 && first_slot < p.n_states ? first_slot : 0) * p.Hv + h) * D + row0) * D;
+    uint64_t s[4][2 * M];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            ulonglong2 x = make_ulonglong2(0ull, 0ull);
+            if (!p.from_zero) x = *reinterpret_cast<const ulonglong2*>(rows + (r + 4 * i) * D + m * 32 + c * 4);
+            s[i][2 * m] = x.x;
+            s[i][2 * m + 1] = x.y;
+        }
+    uint16_t* o = p.o + ((int64_t)b * p.Hv + h) * D + own;
+    const float g = p.g[(int64_t)b * p.Hv + h], beta = p.beta[(int64_t)b * p.Hv + h];
+    const float v = bf16_lo(p.v[b * p.v_bs + h * p.v_hs + own]);
+    uint64_t k[2 * M], q[2 * M];
+    const float rk = lane_vector<D>(p.k + b * p.k_bs + hk * p.k_hs, c, k, p.eps);
+    const float rq = lane_vector<D>(p.q + b * p.q_bs + hk * p.q_hs, c, q, p.eps);
+    const uint64_t rk2 = pair_of(rk, rk);
+    uint64_t kq = 0;
+#pragma unroll
+    for (int m = 0; m < 2 * M; ++m) {
+        k[m] = mul2(k[m], rk2);
+        kq = fma2(k[m], q[m], kq);
+    }
+    const float2 both = parts_of(kq);
+    const float qk = group_sum<8>(both.x + both.y), a = expf(g);
+    const int slot = delta_slot<true>(p, b);
+    if (slot < 0) {
+        if (c & 1) *o = slot == -1 ? 0 : 0x7FC0;
+        return;
+    }
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint64_t wk = 0, wq = 0;
+#pragma unroll
+        for (int m = 0; m < 2 * M; ++m) {
+            wk = fma2(s[i][m], k[m], wk);
+            wq = fma2(s[i][m], q[m], wq);
+        }
+        const float2 d = parts_of(wk), e = parts_of(wq);
+        x[2 * i] = d.x + d.y;
+        x[2 * i + 1] = e.x + e.y;
+    }
+    const float val = a * meet8(x, c);
+    const float u = __shfl_sync(0xffffffffu, beta * (v - val), lane & ~1);
+    if (c & 1) *o = (uint16_t)pack_bf16x2(p.scale * rq * fmaf(qk, u, val), 0.0f);
+    const uint64_t a2 = pair_of(a, a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float w = __shfl_sync(0xffffffffu, u, (lane & 24) | (2 * i));
+        const uint64_t w2 = pair_of(w, w);
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            *reinterpret_cast<ulonglong2*>(rows + (r + 4 * i) * D + m * 32 + c * 4) =
+                make_ulonglong2(fma2(w2, k[2 * m], mul2(a2, s[i][2 * m])), fma2(w2, k[2 * m + 1], mul2(a2, s[i][2 * m + 1])));
+    }
+}
+
+template <int D>
+cudaError_t launch_one(const DeltaParams& p, cudaStream_t st) {
+    return launch_chained(delta_one_kernel<D>, (unsigned)p.B * p.Hv * (D / (kWarps * kRows)), kThreads, 0, st, p);
+}
+
 template <int D, DeltaMode MODE>
 cudaError_t launch_rows(const DeltaParams& p, cudaStream_t st) {
     const size_t smem = sizeof(Shared<D, MODE>);
@@ -296,6 +386,7 @@ cudaError_t launch_rows(const DeltaParams& p, cudaStream_t st) {
 cudaError_t launch_delta(int D, DeltaMode mode, const DeltaParams& p, cudaStream_t st) {
     // (packed sequences of a token each are steps)
     if (mode == kDeltaCommit ? p.P > kGroup : p.cu ? p.T > p.B : p.Lq > kGroup) return launch_delta_chunks(D, mode, p, st);
+    if (mode == kDeltaChain && !p.cu && p.Lq == 1) return D == 64 ? launch_one<64>(p, st) : launch_one<128>(p, st);
     if (mode == kDeltaChain) return D == 64 ? launch_rows<64, kDeltaChain>(p, st) : launch_rows<128, kDeltaChain>(p, st);
     if (mode == kDeltaTree) return D == 64 ? launch_rows<64, kDeltaTree>(p, st) : launch_rows<128, kDeltaTree>(p, st);
     return D == 64 ? launch_rows<64, kDeltaCommit>(p, st) : launch_rows<128, kDeltaCommit>(p, st);
