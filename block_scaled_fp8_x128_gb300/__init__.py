@@ -102,6 +102,7 @@ R9Q_OP_GEMM_W8BF16 = 2
 R9Q_OP_GATE_UP_SWIGLU_DOWN = 3
 R9Q_OP_QK_NORM_ROPE_BWD = 4
 R9Q_OP_KV4_ATTENTION = 5
+R9Q_OP_KV4_TREE_ATTENTION = 6
 R9Q_ROPE_INTERLEAVED = 1
 R9Q_DELTA_FROM_ZERO = 1
 
@@ -457,7 +458,7 @@ def _checked(r, where):
 
 def _with_workspace(where, op, size, call, args, workspace, device, stream):
     """A call that needs a workspace: the caller's, or the stream's own, made or grown where that does not do.
-    size(): the M and N that r9q_workspace_bytes takes."""
+    size(): the M, N and K that r9q_workspace_bytes takes."""
     index = device.index
     if stream is not None or index is None or index != _current_device():
         return _elsewhere(device, stream, _with_workspace, where, op, size, call, args, workspace, device)
@@ -465,7 +466,7 @@ def _with_workspace(where, op, size, call, args, workspace, device, stream):
     theirs = workspace is not None
     r = call(*args, workspace if theirs else _WORKSPACES.get((index, handle)), theirs, handle)
     if not theirs and r.__class__ is int and r in (_calls.CAPTURED, R9Q_ERR_WORKSPACE):
-        own = _stream_workspace(r9q_workspace_bytes(op, *size(), 0), device)
+        own = _stream_workspace(r9q_workspace_bytes(op, *size()), device)
         r = call(*args, own, True, handle)
     return _checked(r, where)
 
@@ -520,7 +521,7 @@ def r9q_qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Te
     """The gradient of r9q_qk_norm_rope; returns (dq, dk, dwq, dwk), of two allocations (dq and dk, dwq and dwk)
     where they were not given.  workspace: as for r9q_gemm_fp8_block_qa
     (zero-filled before its first use; omitted: the stream's own)."""
-    return _with_workspace("r9q_qk_norm_rope_bwd", R9Q_OP_QK_NORM_ROPE_BWD, lambda: (1, q.shape[-1]),
+    return _with_workspace("r9q_qk_norm_rope_bwd", R9Q_OP_QK_NORM_ROPE_BWD, lambda: (1, q.shape[-1], 0),
                            _calls.qk_norm_rope_bwd,
                            (dq_out, dk_out, q, k, wq, wk, cos, sin, positions, eps, interleaved, dq, dk, dwq, dwk),
                            workspace, q.device, stream)
@@ -568,7 +569,7 @@ def r9q_kv4_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.Tenso
     neither was given.  workspace: as for r9q_gemm_fp8_block_qa (zero-filled before its first use; omitted: the stream's
     own)."""
     return _with_workspace("r9q_kv4_attention", R9Q_OP_KV4_ATTENTION,
-                           lambda: (max(1, q.shape[1] * q.shape[2] // cache.k.shape[1]), q.shape[3]),
+                           lambda: (max(1, q.shape[1] * q.shape[2] // cache.k.shape[1]), q.shape[3], 0),
                            _calls.kv4_attention,
                            (q, *cache, block_table, seq_lens, scale, window, out, lse, return_lse), workspace, q.device,
                            stream)
@@ -581,8 +582,9 @@ def r9q_kv4_tree_attention(q: torch.Tensor, cache: KV4Cache, block_table: torch.
     """r9q_kv4_attention with the last Lq (at most 64) tokens of each sequence as the nodes of a tree: parents int32
     [B][Lq], each node's parent before it (0 .. i - 1), -1 the sequence's token before the tree, -2 no node.  A node sees
     what is before the tree, its ancestors and itself.  Workspace, outputs and the rest as there."""
-    return _with_workspace("r9q_kv4_tree_attention", R9Q_OP_KV4_ATTENTION,
-                           lambda: (max(1, q.shape[1] * q.shape[2] // cache.k.shape[1]), q.shape[3]),
+    return _with_workspace("r9q_kv4_tree_attention", R9Q_OP_KV4_TREE_ATTENTION,
+                           lambda: (max(1, q.shape[1] * q.shape[2] // cache.k.shape[1]), q.shape[3],
+                                    max(1, q.shape[0] * cache.k.shape[1])),
                            _calls.kv4_tree_attention,
                            (q, *cache, block_table, seq_lens, parents, scale, window, out, lse, return_lse), workspace,
                            q.device, stream)

@@ -601,9 +601,10 @@ int r9q_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int64_t N2, int
             return R9Q_OK;
         }
         case R9Q_OP_QK_NORM_ROPE_BWD:
-        case R9Q_OP_KV4_ATTENTION: {
+        case R9Q_OP_KV4_ATTENTION:
+        case R9Q_OP_KV4_TREE_ATTENTION: {
             int rc = R9Q_OK;
-            const size_t need = decode_workspace(op, M, N, &rc);
+            const size_t need = decode_workspace(op, M, N, K, &rc);
             if (!rc) *bytes = need;
             return rc;
         }

@@ -147,7 +147,7 @@ int sms_or_default() {
 
 }  // namespace
 
-size_t decode_workspace(int op, int64_t M, int64_t N, int* rc) {
+size_t decode_workspace(int op, int64_t M, int64_t N, int64_t K, int* rc) {
     *rc = R9Q_OK;
     if (N != 64 && N != 128) {
         *rc = R9Q_ERR_DIM;
@@ -158,6 +158,13 @@ size_t decode_workspace(int op, int64_t M, int64_t N, int* rc) {
     if (M < 1) {
         *rc = R9Q_ERR_DIM;
         return 0;
+    }
+    if (op == R9Q_OP_KV4_TREE_ATTENTION && M > kTreeFewRows) {
+        if (K < 1 || K > ((int64_t)1 << 31) / ((M + 127) / 128)) {
+            *rc = R9Q_ERR_DIM;
+            return 0;
+        }
+        return kCounterHeader + kv4_tree_items_bytes(M, K) + kv4_tree_part_floats((int)N, M, sms_or_default()) * 4;
     }
     return kCounterHeader + kv4_attention_part_floats((int)N, M, sms_or_default()) * 4;
 }
@@ -240,7 +247,7 @@ int r9q_qk_norm_rope_bwd(const void* dq_out, int64_t dqo_ts, int64_t dqo_hs, con
         return R9Q_ERR_ARG;
     rc = device_error_word_and_sms(&err, &sms);
     if (rc) return rc;
-    const size_t need = decode_workspace(R9Q_OP_QK_NORM_ROPE_BWD, 1, D, &rc);
+    const size_t need = decode_workspace(R9Q_OP_QK_NORM_ROPE_BWD, 1, D, 1, &rc);
     if (!workspace || workspace_bytes < need) return R9Q_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return R9Q_ERR_ALIGN;
     const Extent ws = bytes_of(workspace, (int64_t)need);
@@ -357,7 +364,8 @@ static int attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, co
         !aligned(parents, 4))
         return R9Q_ERR_ALIGN;
     if (!(scale > 0.0f) || std::isinf(scale) || max_pages * page > 0x7FE00000) return R9Q_ERR_ARG;
-    const size_t need = decode_workspace(R9Q_OP_KV4_ATTENTION, rows, D, &rc);
+    const size_t need = decode_workspace(parents ? R9Q_OP_KV4_TREE_ATTENTION : R9Q_OP_KV4_ATTENTION, rows, D, B * Hk, &rc);
+    if (rc) return rc;
     if (!workspace || workspace_bytes < need) return R9Q_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return R9Q_ERR_ALIGN;
     const Kv4Cache c = cache_of(kc, kp, vc, vp, pages, Hk, page);
@@ -401,6 +409,11 @@ static int attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, co
     p.room = (int)(max_pages * page);
     p.reach = p.window > 0 ? (int)(p.window > INT_MAX - Lq ? INT_MAX : p.window + Lq - 1) : INT_MAX;
     p.scale_log2 = scale * 1.4426950408889634f;
+    if (parents && rows > kTreeFewRows) {
+        uint8_t* items = static_cast<uint8_t*>(workspace) + kCounterHeader;
+        p.part = reinterpret_cast<float*>(items + kv4_tree_items_bytes(rows, B * Hk));
+        return status(launch_kv4_tree_attention((int)D, p, items, sms, static_cast<cudaStream_t>(stream)));
+    }
     return status(launch_kv4_attention((int)D, p, sms, static_cast<cudaStream_t>(stream)));
 }
 

@@ -208,9 +208,15 @@ struct Kv4AttnParams {
 };
 // Floats of `part` for any launch with so many rows.
 size_t kv4_attention_part_floats(int D, int64_t rows, int sms);
-// Workspace bytes of R9Q_OP_QK_NORM_ROPE_BWD and R9Q_OP_KV4_ATTENTION (M rows, N = D).
-size_t decode_workspace(int op, int64_t M, int64_t N, int* rc);
+// Workspace bytes of R9Q_OP_QK_NORM_ROPE_BWD, R9Q_OP_KV4_ATTENTION (M rows, N = D) and R9Q_OP_KV4_TREE_ATTENTION (and
+// K = B * Hk).
+size_t decode_workspace(int op, int64_t M, int64_t N, int64_t K, int* rc);
 cudaError_t launch_kv4_attention(int D, const Kv4AttnParams& p, int sms, cudaStream_t st);
+// Trees with more rows of a key-value head than these: on tcgen05.  `items`: kv4_tree_items_bytes, of B * Hk heads.
+constexpr int kTreeFewRows = 32;
+size_t kv4_tree_items_bytes(int64_t rows, int64_t heads);
+size_t kv4_tree_part_floats(int D, int64_t rows, int sms);
+cudaError_t launch_kv4_tree_attention(int D, const Kv4AttnParams& p, void* items, int sms, cudaStream_t st);
 constexpr int kMostNodes = 64;               // of a tree of drafted tokens, of an accepted path
 // Tokens between places of the cache: rows of `per_row` pairs of slots, a row read before it is written.
 cudaError_t launch_kv4_move(int D, const Kv4Cache& c, const int64_t* src, const int64_t* dst, int64_t rows, int per_row,

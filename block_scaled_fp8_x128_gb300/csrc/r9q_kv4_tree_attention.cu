@@ -1,0 +1,819 @@
+// Attention of a tree of drafted tokens over the paged 4-bit cache, for many rows of a key-value head
+// (nodes times the query heads that share it); few rows take the kernel of r9q_kv4_attention.cu, whose
+// formulas and references these are.
+//
+// With more than a few rows the products are what costs, and they go to tcgen05: a tile of 128
+// rows, a thread each, against tiles of 128 keys.  A CTA has two such streams, which take
+// turns on the tensor cores: two row tiles over the same keys, or with up to 128 rows one row tile
+// over the even and the odd tiles of keys.
+//   S = Q Ck^T     Q in fp16, brought to [2^13, 2^14) by a power of two per row; codes in the low bits of an fp16, the
+//                  subnormal c 2^-24, exactly (of two nibbles one weighs 16 times the other; so do Q's elements, inversely)
+//   score = fr (sk S + lk sum(q))
+//   O += P V'      P the weights in fp16, in S's place in tensor memory; V' = (c - 8) sv 2^(11 - E), fp16, E the exponent of
+//                  the largest step of the tile's keys
+// and what V' leaves out, lv + 8 sv, is summed with the weights in fp32.  Sums of (c - 8), which are near zero, do not
+// drift as those of codes would.  References move as there: a row's weights are taken against top - 8 + E of its own,
+// which moves only when a chunk of 32 weights passes 2^15, and takes what is summed and P with it.
+// Tiles in which some row does not see some key (the tree's own, those at a window's edge or at the sequence's end) keep an
+// exponent for every key, so that no row's arithmetic depends on what it does not see; V' of a key without a finite pair
+// is zero there and everywhere, and rows that see it are NaN.
+//
+// Warps 0-3 and 4-7: the streams.  Warps 8-11 read the codes of a tile ahead into registers, and write K and V' of
+// the one at hand to shared memory.  Warp 12 issues the products.  Work is cut as in r9q_kv4_attention.cuh; an item that several
+// CTAs share is joined by a second kernel, a warp a row.
+#include <algorithm>
+
+#include "r9q_delta.cuh"
+#include "r9q_kv4_attention.cuh"
+
+namespace r9q {
+
+namespace {
+
+constexpr int kTile = 128;                   // keys, and rows
+constexpr int kStreamThreads = 128, kConvertThreads = 128;
+constexpr int kThreads = 2 * kStreamThreads + kConvertThreads + 32;
+constexpr int kTileGroups = kTile / 16;
+constexpr int kRing = 4;                     // tiles whose scalars are kept
+constexpr float kMost = 32768.0f;            // a sum of 32 weights over this moves the reference
+
+// Of a tile's keys.
+struct KeyScalars {
+    float4 k[kTile / 2];                     // of two keys: both steps, both lowest values
+    float mid[kTile];                        // (lv + 8 sv) 2^-exponent
+    float exponent[kTile];                   // biased; all the same where every row sees every key
+    uint16_t v[kTile];                       // steps as fp16, 2^(11 - exponent) times
+    uint32_t bad[4];                         // keys without a finite value pair
+    uint32_t have;                           // groups that were read
+    float one_exponent;
+};
+struct TreeNodes {
+    uint64_t mask[kMostNodes];
+    int first[kMostNodes], instead[kMostNodes], parents[kMostNodes];
+};
+struct Bars {
+    uint64_t q_ready, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_ready[2], o_full[2];
+    uint32_t tmem;
+    int failed;
+};
+template <int D>
+struct Shape {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kHalf = kTile * 128;                // 128 rows of 128 bytes, swizzled
+    static constexpr int kQ = kHalves * kHalf;               // one row tile
+    static constexpr int kV = 2 * D * 128;                   // [2 halves of the keys][D] of 64 keys
+    static constexpr int kAtK = 2 * kQ, kAtV = kAtK + 2 * kQ, kAtScalars = kAtV + 2 * kV;
+    static constexpr int kAtNodes = kAtScalars + kRing * (int)sizeof(KeyScalars);
+    static constexpr int kAtMeet = kAtNodes + (int)sizeof(TreeNodes);        // references and sums of one stream for the other
+    static constexpr int kAtBars = kAtMeet + 2 * kTile * 4;
+    static constexpr size_t kBytes = kAtBars + sizeof(Bars) + 1024;
+    static constexpr int kS = 0, kO = 256;                   // tensor memory: S (and P) of both streams, O of both
+};
+
+__device__ __forceinline__ void umma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void umma_f16_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+// fp16 operands with K contiguous, fp32 accumulator, M = 128.
+constexpr uint32_t idesc_f16(int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | (8u << 24); }
+
+__device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t (&d)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15};" ::"r"(d[0]),
+        "r"(d[1]), "r"(d[2]), "r"(d[3]), "r"(d[4]), "r"(d[5]), "r"(d[6]), "r"(d[7]), "r"(d[8]), "r"(d[9]), "r"(d[10]),
+        "r"(d[11]), "r"(d[12]), "r"(d[13]), "r"(d[14]), "r"(d[15]), "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+template <int ID, int N>
+__device__ __forceinline__ void part_barrier() {
+    asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory");
+}
+
+// Bounded; after one that gave up all others do at once.
+struct Waits {
+    volatile int* failed;
+    int* err;
+    __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) const {
+        if (*failed) return;
+        if (!mbar_wait(bar, parity & 1)) {
+            *failed = 1;
+            record_error(err, kErrTimeout);
+        }
+    }
+};
+
+// Bits [lo, hi) of 32.
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+    lo = min(max(lo, 0), 32);
+    hi = min(max(hi, 0), 32);
+    const uint32_t below_hi = hi == 32 ? 0xFFFFFFFFu : (1u << hi) - 1u, below_lo = lo == 32 ? 0xFFFFFFFFu : (1u << lo) - 1u;
+    return below_hi & ~below_lo;
+}
+
+// The groups of a part, as tiles, and what is known of a tile without looking at its keys.
+struct Tiles {
+    int g_begin, g_end, len, all_lo, base;
+    __device__ __forceinline__ int count() const { return (g_end - g_begin + kTileGroups - 1) / kTileGroups; }
+    __device__ __forceinline__ int first_key(int j) const { return (g_begin + j * kTileGroups) * 16; }
+    // every row sees all of its keys (if all its pages are there)
+    __device__ __forceinline__ bool plain(int j) const {
+        return first_key(j) >= all_lo && first_key(j) + kTile <= base && g_begin + (j + 1) * kTileGroups <= g_end;
+    }
+};
+__device__ __forceinline__ Tiles tiles_of(const Kv4AttnParams& p, const Walk& walk, const Part& it) {
+    const int base = walk.sp.len - p.Lq;
+    return {it.g_begin, it.g_end, walk.sp.len, p.window > 0 ? base + p.Lq - p.window : 0, base};
+}
+
+constexpr int kItemCost = 24;                // groups of a CTA that take as long as beginning and ending an item
+constexpr int kMinGroups = 2 * kTileGroups;  // a tile for each stream
+
+// D: elements of a head.  DUAL: two row tiles over the same keys.
+template <int D, bool DUAL>
+__global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4AttnParams p, int2* items) {
+    using Z = Shape<D>;
+    constexpr int ROWS = DUAL ? 2 * kTile : kTile;
+    extern __shared__ uint8_t raw[];
+    begin_chained();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = tid & 127;
+    Walk walk;
+    if (!walk.start(p, kMinGroups, kItemCost)) return;
+    uint8_t* smem = raw + (1024u - smem_u32(raw) % 1024u) % 1024u;
+    Bars& bars = *reinterpret_cast<Bars*>(smem + Z::kAtBars);
+    auto scalars_of = [&](int tile) { return reinterpret_cast<KeyScalars*>(smem + Z::kAtScalars) + (tile & (kRing - 1)); };
+    if (tid == 0) {
+        mbar_init(&bars.q_ready, 2 * kStreamThreads);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.k_full[i], kConvertThreads);
+            mbar_init(&bars.k_free[i], 1);
+            mbar_init(&bars.v_full[i], kConvertThreads);
+            mbar_init(&bars.v_free[i], 1);
+            mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.p_ready[i], kStreamThreads);
+            mbar_init(&bars.o_full[i], 1);
+        }
+        bars.failed = 0;
+        fence_mbar_init();
+    }
+    if (warp == 12) tmem_alloc(&bars.tmem, 512);
+    umma_fence_before();
+    __syncthreads();
+    umma_fence_after();
+    const uint32_t tmem = bars.tmem;
+    const Waits wait = {&bars.failed, p.err};
+    const int rows = p.Lq * p.G;
+    // Steps of a stream: every tile, or every second one.
+    auto steps_of = [](int tiles, int stream) { return DUAL ? tiles : (tiles + 1 - stream) >> 1; };
+    auto tile_of = [](int step, int stream) { return DUAL ? step : 2 * step + stream; };
+    Part it;
+
+    if (warp < 8) {
+        // ------------------------------------------------------------- streams --
+        const int stream = warp >> 2, half = DUAL ? stream : 0;
+        const uint32_t mine = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t at_s = mine + Z::kS + stream * 128, at_o = mine + Z::kO + stream * 128;
+        TreeNodes& nodes = *reinterpret_cast<TreeNodes*>(smem + Z::kAtNodes);
+        int done = 0, tile0 = 0;             // steps and tiles of earlier parts
+        while (walk.next(p, it)) {
+            const Tiles tiles = tiles_of(p, walk, it);
+            const int n = tiles.count(), steps = steps_of(n, stream);
+            const int row = it.chunk * ROWS + half * kTile + t;              // of the item's rows
+            const bool live = row < rows, warp_live = row - lane < rows;
+            const int node = live ? row / p.group : 0, head = it.hk * p.G + (live ? row - node * p.G : 0);
+            // ---- the tree ----
+            if (tid < p.Lq) nodes.parents[tid] = p.parents[(int64_t)it.b * p.Lq + tid];
+            part_barrier<1, 2 * kStreamThreads>();
+            if (tid < p.Lq) {
+                uint64_t mask;
+                int depth;
+                const NodeKind kind = find_node(nodes.parents, tid, p.window > 0 ? p.window : kMostNodes, mask, depth);
+                const bool none = tiles.len == 0;            // an unused place of the batch: whatever its parents are
+                if (kind == kBadNode && !none) record_error(p.err, kErrArg);
+                nodes.mask[tid] = mask;
+                nodes.first[tid] = p.window > 0 && kind == kNode ? tiles.base + depth - p.window + 1 : 0;
+                nodes.instead[tid] = kind == kNode ? kAsItIs : kind == kNoNode || none ? kNothing : kNan;
+            }
+            // ---- the row's query ----
+            float fr = 0.0f, qs = 0.0f;
+            {
+                uint32_t x[D / 2];
+                const uint4* src = reinterpret_cast<const uint4*>(p.q + it.b * p.q_bs + node * p.q_ts + head * p.q_hs);
+                uint32_t big = 0;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 v = live ? src[i] : make_uint4(0, 0, 0, 0);
+                    x[4 * i] = v.x;
+                    x[4 * i + 1] = v.y;
+                    x[4 * i + 2] = v.z;
+                    x[4 * i + 3] = v.w;
+                }
+#pragma unroll
+                for (int i = 0; i < D / 2; ++i) {
+                    big = __vmaxu2(big, x[i] & 0x7FFF7FFFu);
+                    qs += bf16_lo(x[i]) + bf16_hi(x[i]);
+                }
+                big = max(big >> 16, big & 0xFFFFu);
+                const int e = (int)(big >> 7), up = e == 0 ? 0 : min(13 - (e - 127), 100);
+                const float f = __uint_as_float((uint32_t)(127 + up) << 23), f16 = f * 0.0625f;
+                fr = fminf(p.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23) * 0x1p24f, 3e38f);
+                qs *= f * 0x1p-24f;
+                if (DUAL || stream == 0) {
+                    uint8_t* dst = smem + half * Z::kQ + t * 128;
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {        // (the order in which a word of codes gives its elements)
+                        const uint32_t* q = x + 4 * i;
+                        uint4 w;
+                        w.x = pack_f16x2(bf16_lo(q[0]) * f, bf16_lo(q[2]) * f);
+                        w.y = pack_f16x2(bf16_hi(q[0]) * f16, bf16_hi(q[2]) * f16);
+                        w.z = pack_f16x2(bf16_lo(q[1]) * f, bf16_lo(q[3]) * f);
+                        w.w = pack_f16x2(bf16_hi(q[1]) * f16, bf16_hi(q[3]) * f16);
+                        *reinterpret_cast<uint4*>(dst + (i >> 3) * Z::kHalf + (((i & 7) ^ (t & 7)) << 4)) = w;
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&bars.q_ready);
+            part_barrier<1, 2 * kStreamThreads>();           // (the nodes are there)
+            const uint64_t node_mask = nodes.mask[node];
+            const int first = nodes.first[node];
+
+            float top = 0.0f, l = 0.0f, ml = 0.0f;           // as in r9q_kv4_attention.cu
+            int e_row = kMinExponent;
+            bool seen_any = false, lost = false;
+            const uint64_t fr2 = pair_of(fr, fr), qs2 = pair_of(qs, qs);
+#pragma unroll 1
+            for (int i = 0; i < steps; ++i) {
+                const int j = tile_of(i, stream), tile = tile0 + j;
+                wait(&bars.s_full[stream], done + i);
+                umma_fence_after();
+                const KeyScalars& ks = *scalars_of(tile);
+                const bool plain = tiles.plain(j) && ks.have == 0xFFu;
+                if (warp_live) {
+                    // which of the keys the row sees
+                    uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+                    if (!plain) {
+                        const int key0 = tiles.first_key(j), off = tiles.base - key0;
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const int s = 32 * w - off;
+                            const uint32_t tree = s >= 64 || s <= -32 ? 0u : s >= 0 ? (uint32_t)(node_mask >> s) : (uint32_t)(node_mask << -s);
+                            const uint32_t here = (ks.have >> (2 * w) & 1u ? 0xFFFFu : 0u) | (ks.have >> (2 * w + 1) & 1u ? 0xFFFF0000u : 0u);
+                            seen[w] = (bits_between(first - key0 - 32 * w, off - 32 * w) | tree) & here &
+                                      bits_between(0, tiles.len - key0 - 32 * w);
+                        }
+                    }
+                    lost = lost || ((seen[0] & ks.bad[0]) | (seen[1] & ks.bad[1]) | (seen[2] & ks.bad[2]) | (seen[3] & ks.bad[3])) != 0;
+                    // Scores of 32 keys, over fr.
+                    auto scores = [&](int c, uint64_t (&s)[16]) {
+                        float a[32];
+                        tmem_ld(at_s + c * 32, a);
+                        tmem_wait_ld(a);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&ks.k[c * 16 + x]);
+                            s[x] = fma2(k.x, pair_of(a[2 * x], a[2 * x + 1]), mul2(k.y, qs2));
+                        }
+                    };
+                    // The row's reference to the larger of its own and (best, e); `c`: chunks of P that are written.
+                    float sum = 0.0f, msum = 0.0f;           // of the tile
+                    auto move = [&](float best, int e, int c) {
+                        const float to = seen_any ? fmaxf(top, best) : best;
+                        const bool any = best > kNegInf || best != best;
+                        const int e_to = any ? max(e_row, e) : e_row;
+                        const float alpha = seen_any ? ex2(fmaf(top - (any ? to : top), fr, (float)(e_row - e_to))) : 0.0f;
+                        if (any) {
+                            top = to;
+                            e_row = e_to;
+                            seen_any = true;
+                        }
+                        l *= alpha;
+                        ml *= alpha;
+                        sum *= alpha;
+                        msum *= alpha;
+                        if (i > 0) {                         // O, once the last tile's product is in it
+                            wait(&bars.o_full[stream], done + i - 1);
+                            umma_fence_after();
+#pragma unroll 1
+                            for (int x = 0; x < D; x += 16) {
+                                float o[16];
+                                uint32_t y[16];
+                                tmem_ld(at_o + x, o);
+                                tmem_wait_ld(o);
+#pragma unroll
+                                for (int z = 0; z < 16; ++z) y[z] = __float_as_uint(o[z] * alpha);
+                                tmem_store16(at_o + x, y);
+                            }
+                        }
+#pragma unroll 1
+                        for (int x = 0; x < c; ++x) {
+                            float w[16];
+                            uint32_t y[16];
+                            tmem_ld(at_s + x * 16, w);
+                            tmem_wait_ld(w);
+#pragma unroll
+                            for (int z = 0; z < 16; ++z) {
+                                const uint32_t h = __float_as_uint(w[z]);
+                                uint32_t a2, r;
+                                a2 = pack_f16x2(alpha, alpha);
+                                asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(a2));
+                                y[z] = r;
+                            }
+                            tmem_store16(at_s + x * 16, y);
+                        }
+                        tmem_stored();
+                    };
+                    if (!plain || __any_sync(0xffffffffu, !seen_any)) {       // the largest score and exponent of what the row sees
+                        float best = kNegInf;
+                        int e = 0;
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint64_t s[16];
+                            scores(c, s);
+                            const uint32_t m = c == 0 ? seen[0] : c == 1 ? seen[1] : c == 2 ? seen[2] : seen[3];
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) {
+                                const float2 f = parts_of(s[x / 2]);
+                                const float v = x & 1 ? f.y : f.x;
+                                if (m >> x & 1) {
+                                    best = v != v || best != best ? __int_as_float(0x7FC00000) : fmaxf(best, v);
+                                    e = max(e, (int)ks.exponent[c * 32 + x]);
+                                }
+                            }
+                        }
+                        const bool over = (best - top) * fr + (float)(e - e_row) > (float)kSlack;
+                        const bool rise = (best > kNegInf || best != best) && (!seen_any || !((best - top) * fr <= (float)kSlack) || e > e_row || over);
+                        if (__any_sync(0xffffffffu, rise)) move(rise ? best : kNegInf, e, 0);
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint64_t s[16];
+                        scores(c, s);
+                        const uint32_t m = c == 0 ? seen[0] : c == 1 ? seen[1] : c == 2 ? seen[2] : seen[3];
+                        uint32_t out[16];
+                        float chunk_sum, chunk_mid;
+                        auto weigh = [&]() {
+                            const uint64_t top2 = pair_of(-top, -top);
+                            const float base_shift = plain ? (float)(kHeadroom - e_row) + ks.one_exponent : (float)(kHeadroom - e_row);
+                            uint64_t total = 0, mids = 0;
+#pragma unroll
+                            for (int x = 0; x < 16; x += 2) {
+                                const ulonglong2 mid = *reinterpret_cast<const ulonglong2*>(&ks.mid[c * 32 + 2 * x]);
+                                ulonglong2 ex = make_ulonglong2(0, 0);
+                                if (!plain) ex = *reinterpret_cast<const ulonglong2*>(&ks.exponent[c * 32 + 2 * x]);
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    uint64_t sh = pair_of(base_shift, base_shift);
+                                    const uint64_t own = y ? ex.y : ex.x;
+                                    if (!plain) sh = add2(sh, own);
+                                    const float2 f = parts_of(fma2(add2(s[x + y], top2), fr2, sh));
+                                    float p0 = ex2(f.x), p1 = ex2(f.y);
+                                    if (!plain) {
+                                        p0 = m >> (2 * (x + y)) & 1 ? p0 : 0.0f;
+                                        p1 = m >> (2 * (x + y) + 1) & 1 ? p1 : 0.0f;
+                                    }
+                                    const uint64_t w = pair_of(p0, p1);
+                                    mids = fma2(w, y ? mid.y : mid.x, mids);
+                                    if (plain) {
+                                        total = add2(total, w);
+                                    } else {                 // (weights carry their own key's exponent)
+                                        const float2 q = parts_of(own);
+                                        total = add2(total, mul2(w, pair_of(ex2(127.0f - q.x), ex2(127.0f - q.y))));
+                                    }
+                                    out[x + y] = pack_f16x2(p0, p1);
+                                }
+                            }
+                            const float2 a = parts_of(total), d = parts_of(mids);
+                            chunk_sum = a.x + a.y;
+                            chunk_mid = d.x + d.y;
+                        };
+                        weigh();
+                        if (plain && __any_sync(0xffffffffu, chunk_sum > kMost)) {
+                            float best = kNegInf;
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) {
+                                const float2 f = parts_of(s[x]);
+                                best = max3(best, f.x, f.y);
+                            }
+                            move(chunk_sum > kMost ? best : kNegInf, (int)ks.one_exponent, c);
+                            weigh();
+                        }
+                        sum += chunk_sum;
+                        msum += chunk_mid;
+                        tmem_store16(at_s + c * 16, out);
+                    }
+                    l += plain ? sum * ex2(127.0f - ks.one_exponent) : sum;
+                    ml += msum;
+                    tmem_stored();
+                }
+                umma_fence_before();
+                mbar_arrive(&bars.p_ready[stream]);
+            }
+            // ---- the end of the part ----
+            if (steps > 0) {
+                wait(&bars.o_full[stream], done + steps - 1);
+                umma_fence_after();
+            }
+            if (lost) l = __int_as_float(0x7FC00000);
+            float m = seen_any ? fmaf(top, fr, (float)(e_row - kHeadroom - 127)) : kNegInf;
+            float scale_o = steps > 0 && seen_any ? 0x1p-11f : 0.0f;
+            float total_m = m, total_l = l;
+            float* meet_m = reinterpret_cast<float*>(smem + Z::kAtMeet);
+            float* meet_l = meet_m + kTile;
+            float* meet_o = reinterpret_cast<float*>(smem);                  // [D / 4][128 rows] of four, over Q and K
+            float own_k = 1.0f, other_k = 0.0f;
+            if constexpr (!DUAL) {           // the other stream's sums, by way of shared memory
+                part_barrier<1, 2 * kStreamThreads>();       // (no product reads Q any more)
+                if (stream == 1) {
+                    meet_m[t] = m;
+                    meet_l[t] = l;
+#pragma unroll 1
+                    for (int x = 0; x < D; x += 16) {
+                        float o[16];
+                        tmem_ld(at_o + x, o);
+                        tmem_wait_ld(o);
+#pragma unroll
+                        for (int z = 0; z < 16; z += 4)
+                            reinterpret_cast<float4*>(meet_o)[(x + z) / 4 * kTile + t] =
+                                seen_any ? make_float4(fmaf(o[z], scale_o, ml), fmaf(o[z + 1], scale_o, ml), fmaf(o[z + 2], scale_o, ml), fmaf(o[z + 3], scale_o, ml))
+                                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    }
+                }
+                part_barrier<1, 2 * kStreamThreads>();
+                if (stream == 0) {
+                    const float om = meet_m[t], ol = meet_l[t];
+                    total_m = fmaxf(m, om);
+                    const float base = total_m > kNegInf ? total_m : 0.0f;
+                    own_k = ex2(m - base);
+                    other_k = ex2(om - base);
+                    total_l = l * own_k + ol * other_k;
+                }
+            }
+            if (warp_live && (DUAL || stream == 0)) {
+                const Instead instead = (Instead)nodes.instead[node];
+                float* part = p.part + ((size_t)blockIdx.x * 2 + (it.begins ? 1 : 0)) * ((size_t)ROWS * (D + 2));
+                const int r = half * kTile + t;
+                const int64_t out = ((int64_t)it.b * p.Lq + node) * (p.c.heads * p.G) + head;
+                const float inv = total_l != 0.0f ? 1.0f / total_l : 0.0f;
+#pragma unroll 1
+                for (int x = 0; x < D; x += 16) {
+                    float o[16];
+                    tmem_ld(at_o + x, o);    // (by the whole warp)
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int z = 0; z < 16; ++z) o[z] = steps > 0 && seen_any ? own_k * fmaf(o[z], scale_o, ml) : 0.0f;
+                    if constexpr (!DUAL) {
+#pragma unroll
+                        for (int z = 0; z < 16; z += 4) {
+                            const float4 v = reinterpret_cast<const float4*>(meet_o)[(x + z) / 4 * kTile + t];
+                            o[z] = fmaf(other_k, v.x, o[z]);
+                            o[z + 1] = fmaf(other_k, v.y, o[z + 1]);
+                            o[z + 2] = fmaf(other_k, v.z, o[z + 2]);
+                            o[z + 3] = fmaf(other_k, v.w, o[z + 3]);
+                        }
+                    }
+                    if (!live) continue;
+                    if (it.whole) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int z = 0; z < 8; ++z) {
+                            w[z] = pack_bf16x2(o[2 * z] * inv, o[2 * z + 1] * inv);
+                            if (instead != kAsItIs) w[z] = instead == kNothing ? 0u : 0x7FC07FC0u;
+                        }
+                        uint4* dst = reinterpret_cast<uint4*>(p.o + out * D + x);
+                        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    } else {
+#pragma unroll
+                        for (int z = 0; z < 16; z += 4)
+                            *reinterpret_cast<float4*>(part + (size_t)r * D + x + z) = make_float4(o[z], o[z + 1], o[z + 2], o[z + 3]);
+                    }
+                }
+                if (live && it.whole && p.lse)
+                    p.lse[out] = instead == kNothing ? kNegInf : instead == kNan ? __int_as_float(0x7FC00000) : log_sum_exp(total_m, total_l);
+                if (live && !it.whole) {
+                    part[(size_t)ROWS * D + r] = total_m;
+                    part[(size_t)ROWS * D + ROWS + r] = total_l;
+                }
+            }
+            if (tid == 0 && it.begins) {     // for the kernel that joins: the CTAs that have the item
+                int c0 = 0, c1 = 0;
+                if (!it.whole) walk.sharers(c0, c1);
+                items[(int64_t)it.b * walk.items_per_seq + walk.item] = make_int2(c0, c1);
+            }
+            umma_fence_before();
+            part_barrier<1, 2 * kStreamThreads>();           // (the nodes, Q and what met are free)
+            done += steps;
+            tile0 += n;
+            if (walk.parted) break;
+        }
+    } else if (warp < 12) {
+        // --------------------------------------------------------------- codes --
+        int tile0 = 0;
+        while (walk.next(p, it)) {
+            const Tiles tiles = tiles_of(p, walk, it);
+            const int n = tiles.count(), gmax = min(it.g_end, (tiles.len + 15) >> 4);
+            const int32_t* table = p.table + (int64_t)it.b * p.max_pages;
+            // Thread t: key t; and of the values the eight rows r = t % 8 of half a head or all (D = 64: of two groups).
+            constexpr int VG = kConvertThreads / (8 * (D / 64));             // groups at a time
+            const int vr = t & 7, vc = D == 128 ? (t >> 3) & 1 : 0, vg = t / (8 * (D / 64));
+            static_assert(VG == kTileGroups || VG == 2 * kTileGroups, "groups of a tile");
+            auto group_at = [&](int j, int g) {
+                const int at = it.g_begin + j * kTileGroups + g;
+                return g < kTileGroups && at < gmax ? find_group(p, table, at, it.hk) : kNoGroup;
+            };
+            uint32_t k_at = group_at(0, t >> 4), v_at = group_at(0, vg), k_next = kNoGroup, v_next = kNoGroup;
+            uint4 kq[D / 32], vq[4];
+            uint32_t kp = 0, vp = 0;
+            auto load = [&]() {              // the codes at k_at and v_at
+                if (k_at != kNoGroup) {
+                    const uint4* src = reinterpret_cast<const uint4*>(p.c.k + ((uint64_t)k_at + (t & 15)) * (D / 2));
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) kq[i] = src[i];
+                    kp = p.c.kp[(uint64_t)k_at + (t & 15)];
+                    vp = p.c.vp[(uint64_t)k_at + (t & 15)];
+                }
+                if (v_at != kNoGroup) {
+                    const uint4* src = reinterpret_cast<const uint4*>(p.c.v + (uint64_t)v_at * (D / 2) + vc * 512 + vr * 64);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vq[i] = src[i];
+                }
+            };
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) kq[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vq[i] = make_uint4(0, 0, 0, 0);
+            load();
+            if (n > 1) {
+                k_next = group_at(1, t >> 4);
+                v_next = group_at(1, vg);
+            }
+#pragma unroll 1
+            for (int j = 0; j < n; ++j) {
+                const int tile = tile0 + j, buf = tile & 1;
+                KeyScalars& ks = *scalars_of(tile);
+                uint8_t* K = smem + Z::kAtK + buf * Z::kQ;
+                uint8_t* V = smem + Z::kAtV + buf * Z::kV;
+                if (tile >= 2) wait(&bars.k_free[buf], (tile - 2) >> 1);
+                // ---- the key's pairs ----
+                const bool here = k_at != kNoGroup && tiles.first_key(j) + t < tiles.len;
+                const uint32_t kpair = here ? kp : 0u, vpair = here ? vp : 0u;
+                const int xs = (int)(vpair >> 7) & 255, xl = (int)(vpair >> 23) & 255;
+                const bool bad = xs == 255 || xl == 255;
+                int e = bad ? kMinExponent : min(max(max(xs, xl - kLowestBits), kMinExponent), 253);
+                const uint32_t got = __ballot_sync(0xffffffffu, k_at != kNoGroup), not_good = __ballot_sync(0xffffffffu, bad);
+                if (lane == 0) {
+                    ks.bad[warp & 3] = not_good;
+                    uint8_t* have = reinterpret_cast<uint8_t*>(ks.exponent);         // (for a moment)
+                    have[warp & 3] = (uint8_t)((got & 1u) | (got >> 16 & 1u) << 1);
+                }
+                int most = e;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+                if (lane == 0) reinterpret_cast<int*>(ks.mid)[warp & 3] = most;      // (likewise)
+                part_barrier<2, kConvertThreads>();
+                const uint32_t four = *reinterpret_cast<const uint32_t*>(ks.exponent);
+                const int4 all = *reinterpret_cast<const int4*>(ks.mid);
+                part_barrier<2, kConvertThreads>();
+                const uint32_t have = (four & 3u) | (four >> 6 & 12u) | (four >> 12 & 48u) | (four >> 18 & 192u);
+                const int one = max(max(all.x, all.y), max(all.z, all.w));
+                const bool plain = tiles.plain(j) && have == 0xFFu;
+                if (plain) e = one;
+                float* pair = reinterpret_cast<float*>(&ks.k[t >> 1]) + (t & 1);
+                pair[0] = bf16_lo(kpair);
+                pair[2] = bf16_hi(kpair);
+                const float sv = bad ? 0.0f : bf16_lo(vpair), lv = bad ? 0.0f : bf16_hi(vpair);
+                ks.mid[t] = fmaf(8.0f, sv * __uint_as_float((uint32_t)(254 - e) << 23), lv * __uint_as_float((uint32_t)(254 - e) << 23));
+                ks.exponent[t] = (float)e;
+                // 2^(11 + 127 - e) in two factors, so that neither is out of range
+                ks.v[t] = (uint16_t)pack_f16x2(sv * __uint_as_float((uint32_t)(254 - e) << 23) * 2048.0f, 0.0f);
+                if (t == 0) {
+                    ks.have = have;
+                    ks.one_exponent = (float)one;
+                }
+                // ---- keys: a word's four masks are 16 bytes of the row ----
+                uint8_t* dst = K + t * 128;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint32_t q[4] = {kq[i].x, kq[i].y, kq[i].z, kq[i].w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int word = 4 * i + x;
+                        const uint32_t w = q[x], y = w >> 8;
+                        *reinterpret_cast<uint4*>(dst + (word >> 3) * Z::kHalf + (((word & 7) ^ (t & 7)) << 4)) =
+                            make_uint4(w & 0x000F000Fu, w & 0x00F000F0u, y & 0x000F000Fu, y & 0x00F000F0u);
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&bars.k_full[buf]);
+                // ---- values ----
+                if (tile >= 2) wait(&bars.v_free[buf], (tile - 2) >> 1);
+                part_barrier<2, kConvertThreads>();          // (the steps of all keys)
+                if (vg < kTileGroups) {
+                    const uint4 s0 = *reinterpret_cast<const uint4*>(&ks.v[vg * 16]), s1 = *reinterpret_cast<const uint4*>(&ks.v[vg * 16 + 8]);
+                    const uint32_t lo[4] = {s0.x, s0.y, s0.z, s0.w}, hi[4] = {s1.x, s1.y, s1.z, s1.w};
+                    auto value = [](uint32_t codes, uint32_t magic, uint32_t middle, uint32_t step) {
+                        uint32_t r;
+                        asm("{\n\t.reg .b32 x;\n\tsub.rn.f16x2 x, %1, %2;\n\tmul.rn.f16x2 %0, x, %3;\n\t}" : "=r"(r) : "r"(codes | magic), "r"(middle), "r"(step));
+                        return r;
+                    };
+                    uint8_t* row = V + (vg >> 2) * (D * 128) + (vc * 64 + vr) * 128;
+                    const int at0 = ((vg & 3) * 2) ^ vr, at1 = ((vg & 3) * 2 + 1) ^ vr;
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        uint32_t a[4], c[4], x[4], y[4];     // of tokens 2j, 2j + 1 and 8 on; element r and r + 8
+#pragma unroll
+                        for (int jj = 0; jj < 4; ++jj) {
+                            const uint32_t w = m == 0 ? vq[jj].x : m == 1 ? vq[jj].y : m == 2 ? vq[jj].z : vq[jj].w, h = w >> 8;
+                            // 1024 + code (steps of one), 64 + code (steps of 1/16)
+                            a[jj] = value(w & 0x000F000Fu, 0x64006400u, 0x64086408u, lo[jj]);
+                            c[jj] = value(h & 0x000F000Fu, 0x64006400u, 0x64086408u, hi[jj]);
+                            x[jj] = value(w & 0x00F000F0u, 0x54005400u, 0x54805480u, lo[jj]);
+                            y[jj] = value(h & 0x00F000F0u, 0x54005400u, 0x54805480u, hi[jj]);
+                        }
+                        uint8_t* d0 = row + m * (16 * 128);
+                        *reinterpret_cast<uint4*>(d0 + (at0 << 4)) = make_uint4(a[0], a[1], a[2], a[3]);
+                        *reinterpret_cast<uint4*>(d0 + (at1 << 4)) = make_uint4(c[0], c[1], c[2], c[3]);
+                        *reinterpret_cast<uint4*>(d0 + 8 * 128 + (at0 << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+                        *reinterpret_cast<uint4*>(d0 + 8 * 128 + (at1 << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&bars.v_full[buf]);
+                // the next tile's codes are on their way meanwhile
+                k_at = k_next;
+                v_at = v_next;
+                if (j + 1 < n) load();
+                k_next = j + 2 < n ? group_at(j + 2, t >> 4) : kNoGroup;
+                v_next = j + 2 < n ? group_at(j + 2, vg) : kNoGroup;
+            }
+            tile0 += n;
+            if (walk.parted) break;
+        }
+    } else {
+        // ------------------------------------------------------------ products --
+        constexpr uint32_t kScores = idesc_f16(kTile), kValues = idesc_f16(D);
+        int done[2] = {0, 0}, tile0 = 0, parts = 0;
+        while (walk.next(p, it)) {
+            const int n = tiles_of(p, walk, it).count();
+            if (lane == 0) {
+                wait(&bars.q_ready, parts);
+                umma_fence_after();
+                auto scores = [&](int s, int i) {
+                    const int tile = tile0 + tile_of(i, s), buf = tile & 1;
+                    wait(&bars.k_full[buf], tile >> 1);
+                    umma_fence_after();
+                    const uint32_t q = smem_u32(smem) + (DUAL ? s * Z::kQ : 0), k = smem_u32(smem + Z::kAtK + buf * Z::kQ);
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x)
+                        umma_f16(tmem + Z::kS + s * 128, umma_sdesc_sw128(q + (x >> 2) * Z::kHalf + (x & 3) * 32),
+                                 umma_sdesc_sw128(k + (x >> 2) * Z::kHalf + (x & 3) * 32), kScores, x > 0);
+                    umma_commit(&bars.s_full[s]);
+                    if (!DUAL || s == 1) umma_commit(&bars.k_free[buf]);
+                };
+                auto values = [&](int s, int i) {
+                    const int tile = tile0 + tile_of(i, s), buf = tile & 1;
+                    wait(&bars.v_full[buf], tile >> 1);
+                    wait(&bars.p_ready[s], done[s] + i);
+                    umma_fence_after();
+                    const uint32_t v = smem_u32(smem + Z::kAtV + buf * Z::kV);
+#pragma unroll
+                    for (int x = 0; x < kTile / 16; ++x)
+                        umma_f16_tmem(tmem + Z::kO + s * 128, tmem + Z::kS + s * 128 + x * 8,
+                                      umma_sdesc_sw128(v + (x >> 2) * (D * 128) + (x & 3) * 32), kValues, i > 0 || x > 0);
+                    umma_commit(&bars.o_full[s]);
+                    if (!DUAL || s == 1) umma_commit(&bars.v_free[buf]);
+                };
+                const int steps[2] = {steps_of(n, 0), steps_of(n, 1)};
+                for (int s = 0; s < 2; ++s)
+                    if (steps[s] > 0) scores(s, 0);
+#pragma unroll 1
+                for (int i = 0; i < steps[0]; ++i)
+#pragma unroll 1
+                    for (int s = 0; s < 2; ++s) {
+                        if (i >= steps[s]) continue;
+                        values(s, i);
+                        if (i + 1 < steps[s]) {
+                            wait(&bars.o_full[s], done[s] + i);              // (P is read: S takes its place)
+                            scores(s, i + 1);
+                        }
+                    }
+                // nothing is in flight at the end, whatever gave up
+                for (int s = 0; s < 2; ++s)
+                    if (steps[s] > 0 && !mbar_wait(&bars.o_full[s], (done[s] + steps[s] - 1) & 1)) record_error(p.err, kErrTimeout);
+                done[0] += steps[0];
+                done[1] += steps[1];
+            }
+            tile0 += n;
+            ++parts;
+            __syncwarp();
+            if (walk.parted) break;
+        }
+    }
+    __syncwarp();
+    umma_fence_before();
+    __syncthreads();
+    umma_fence_after();
+    if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+// Items that several CTAs share: a warp a row.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256) join_kernel(const Kv4AttnParams p, const int2* items, int row_blocks) {
+    begin_chained();
+    const int lane = threadIdx.x & 31, item = blockIdx.x / row_blocks;
+    const int r = (blockIdx.x - item * row_blocks) * 8 + (threadIdx.x >> 5);
+    const int2 by = items[item];
+    if (by.x == by.y || r >= ROWS) return;
+    const int chunks = p.chunks.d, per_seq = p.c.heads * chunks, b = item / per_seq, rest = item - b * per_seq;
+    const int hk = rest / chunks, chunk = rest - hk * chunks, row = chunk * ROWS + r;
+    if (row >= p.Lq * p.G) return;
+    const int node = row / p.G, head = hk * p.G + (row - node * p.G);
+    auto slot = [&](int c) { return p.part + ((size_t)c * 2 + (c == by.x ? 1 : 0)) * ((size_t)ROWS * (D + 2)); };
+    const int n = by.y - by.x + 1;
+    float top = kNegInf;
+    for (int c = lane; c < n; c += 32) top = fmaxf(top, slot(by.x + c)[(size_t)ROWS * D + r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float base = top > kNegInf ? top : 0.0f;
+    float sum = 0.0f, x[D / 32] = {};
+#pragma unroll 4
+    for (int c = 0; c < n; ++c) {
+        const float* s = slot(by.x + c);
+        const float k = ex2(s[(size_t)ROWS * D + r] - base);
+        sum = fmaf(k, s[(size_t)ROWS * D + ROWS + r], sum);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) x[i] = fmaf(k, s[(size_t)r * D + lane * (D / 32) + i], x[i]);
+    }
+    // the node, as the other kernel found it
+    const int32_t* parents = p.parents + (int64_t)b * p.Lq;
+    Instead instead = kAsItIs;
+    if (parents[node] == -2)
+        instead = kNothing;
+    else
+        for (int t = node; t >= 0;) {
+            const int up = parents[t];
+            if (up != -1 && (up < 0 || up >= t)) {
+                instead = kNan;
+                break;
+            }
+            t = up;
+        }
+    const int64_t out = ((int64_t)b * p.Lq + node) * (p.c.heads * p.G) + head;
+    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+    uint32_t w[D / 64];
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+        w[i] = pack_bf16x2(x[2 * i] * inv, x[2 * i + 1] * inv);
+        if (instead != kAsItIs) w[i] = instead == kNothing ? 0u : 0x7FC07FC0u;
+        reinterpret_cast<uint32_t*>(p.o + out * D)[lane * (D / 64) + i] = w[i];
+    }
+    if (p.lse && lane == 0)
+        p.lse[out] = instead == kNothing ? kNegInf : instead == kNan ? __int_as_float(0x7FC00000) : log_sum_exp(top, sum);
+}
+
+template <int D, bool DUAL>
+cudaError_t launch(Kv4AttnParams p, int2* items, int sms, cudaStream_t st) {
+    constexpr int ROWS = DUAL ? 2 * kTile : kTile;
+    const void* kernel = reinterpret_cast<const void*>(tree_attention_kernel<D, DUAL>);
+    cudaError_t e = ensure_dynamic_smem(kernel, Shape<D>::kBytes);
+    if (e != cudaSuccess) return e;
+    p.chunks = fast_div((p.Lq * p.G + ROWS - 1) / ROWS);
+    p.group = fast_div(p.G);
+    p.page_groups = fast_div(p.c.page / 16);
+    e = launch_chained(tree_attention_kernel<D, DUAL>, used_sms(sms), kThreads, Shape<D>::kBytes, st, p, items);
+    if (e != cudaSuccess) return e;
+    const int row_blocks = (std::min(ROWS, p.Lq * p.G) + 7) / 8;
+    return launch_chained(join_kernel<D, ROWS>, (unsigned)p.B * p.c.heads * p.chunks.d * row_blocks, 256, 0, st, p,
+                          static_cast<const int2*>(items), row_blocks);
+}
+
+}  // namespace
+
+// Bytes: the items' CTAs, then the partials of two slots a CTA.
+size_t kv4_tree_items_bytes(int64_t rows, int64_t heads) {
+    return (size_t)(heads * ((rows + kTile - 1) / kTile)) * sizeof(int2) / 256 * 256 + 256;
+}
+size_t kv4_tree_part_floats(int D, int64_t rows, int sms) {
+    return (size_t)used_sms(sms) * 2 * (rows > kTile ? 2 * kTile : kTile) * (D + 2);
+}
+
+cudaError_t launch_kv4_tree_attention(int D, const Kv4AttnParams& p, void* items, int sms, cudaStream_t st) {
+    int2* at = static_cast<int2*>(items);
+    const bool dual = p.Lq * p.G > kTile;
+    if (D == 64) return dual ? launch<64, true>(p, at, sms, st) : launch<64, false>(p, at, sms, st);
+    return dual ? launch<128, true>(p, at, sms, st) : launch<128, false>(p, at, sms, st);
+}
+
+}  // namespace r9q

@@ -361,7 +361,10 @@ int r9q_kv4_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, c
  * Node i sees the tokens before the tree, its ancestors and itself.  Its position is n - Lq + d
  * with d its ancestors' number, and a window counts positions: the last `window` of that path.
  * Another parent, or one that leads to no node, sets the device error word to R9Q_ERR_ARG, and the
- * node's o and lse are NaN; the parents of a sequence of length 0 are not looked at. */
+ * node's o and lse are NaN; the parents of a sequence of length 0 are not looked at.  More than 32 rows
+ * Lq * Hq / Hk of a key-value head go to the tensor cores in tiles of 128.  workspace:
+ * r9q_workspace_bytes(R9Q_OP_KV4_TREE_ATTENTION, Lq * Hq / Hk, D, B * Hk, ...), zeroed and left as
+ * r9q_kv4_attention's. */
 int r9q_kv4_tree_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, const uint8_t* kc, const void* kp,
                            const uint8_t* vc, const void* vp, const int32_t* block_table, const int32_t* seq_lens,
                            const int32_t* parents, void* o, float* lse, int64_t B, int64_t Lq, int64_t Hq, int64_t Hk,
@@ -439,6 +442,7 @@ int r9q_stream_capture_id(void* stream, unsigned long long* id);
 #define R9Q_OP_GATE_UP_SWIGLU_DOWN  3   /* (M, N=I, K=H, N2=H_out, flags) */
 #define R9Q_OP_QK_NORM_ROPE_BWD     4   /* (M=T, N=D) */
 #define R9Q_OP_KV4_ATTENTION        5   /* (M=Lq*Hq/Hk, N=D) */
+#define R9Q_OP_KV4_TREE_ATTENTION   6   /* (M=Lq*Hq/Hk, N=D, K=B*Hk) */
 /* Writes the bytes of device workspace the call needs (0 = none) to *bytes. */
 int r9q_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int64_t N2, int flags,
                         size_t* bytes);

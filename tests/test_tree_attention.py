@@ -186,7 +186,7 @@ def test_layouts_a_stream_and_graphs(r9q, n, Hq):  # noqa: F811
     q = buf[:, :, :2 * Hq]
     rest = (cache, on(table), on(np.array(lens, np.int32)), on(random_parents(3, n, 653)))
     want = r9q.r9q_kv4_tree_attention(q.contiguous(), *rest)
-    size = r9q.r9q_workspace_bytes(r9q.R9Q_OP_KV4_ATTENTION, n * Hq, 128, 0)
+    size = r9q.r9q_workspace_bytes(r9q.R9Q_OP_KV4_TREE_ATTENTION, n * Hq, 128, 3 * 2)
     ws = torch.zeros(size, dtype=torch.uint8, device=dev())
     torch.cuda.synchronize()
     st = torch.cuda.Stream()
