@@ -826,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             mbar_arrive(&bars.t_full);
             mbar_arrive(&bars.l_free[c & 1]);
         }
-    } else if (lane == 0) {
+    } else if (elect_one()) {
         // ------------------------------------------------------------ products --
         constexpr uint32_t kById = idesc_bf16(64, false), kUpdate = idesc_bf16(D, true);
         auto gram = [&](int c) {

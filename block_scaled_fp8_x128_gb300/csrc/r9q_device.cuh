@@ -418,6 +418,14 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint3
 
 // ------------------------------------------------------------------ tcgen05 --
 
+// One lane of a whole warp.  (A branch on it, unlike one on the lane's number, lets the compiler keep descriptors in uniform
+// registers: tcgen05.mma with N = 64 and A in tensor memory is issued every 40 cycles instead of every 94.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // Shared-memory matrix descriptor of a K-major operand with the 128-byte
 // swizzle: rows of 128 bytes in 8-row atoms stacked every 1024 bytes (stride
 // byte offset); the leading byte offset is unused for this layout (encoded as

@@ -35,6 +35,12 @@ constexpr int kStreamThreads = 128, kConvertThreads = 128;
 constexpr int kThreads = 2 * kStreamThreads + kConvertThreads + 32;
 constexpr int kTileGroups = kTile / 16;
 constexpr int kRing = 4;                     // tiles whose scalars are kept
+struct Yes {
+    static constexpr bool value = true;
+};
+struct No {
+    static constexpr bool value = false;
+};
 constexpr float kMost = 32768.0f;            // a sum of 32 weights over this moves the reference
 
 // Of a tile's keys.
@@ -356,8 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                         const bool rise = (best > kNegInf || best != best) && (!seen_any || !((best - top) * fr <= (float)kSlack) || e > e_row || over);
                         if (__any_sync(0xffffffffu, rise)) move(rise ? best : kNegInf, e, 0);
                     }
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
+                    // Weights of 32 keys against the reference: as P, and their sums.
+                    auto chunk = [&](int c, auto tag) {
+                        constexpr bool PLAIN = decltype(tag)::value;
                         uint64_t s[16];
                         scores(c, s);
                         const uint32_t m = c == 0 ? seen[0] : c == 1 ? seen[1] : c == 2 ? seen[2] : seen[3];
@@ -365,31 +372,31 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                         float chunk_sum, chunk_mid;
                         auto weigh = [&]() {
                             const uint64_t top2 = pair_of(-top, -top);
-                            const float base_shift = plain ? (float)(kHeadroom - e_row) + ks.one_exponent : (float)(kHeadroom - e_row);
+                            const float sh = (float)(kHeadroom - e_row) + (PLAIN ? ks.one_exponent : 0.0f);
+                            const uint64_t shift2 = pair_of(sh, sh);
                             uint64_t total = 0, mids = 0;
 #pragma unroll
                             for (int x = 0; x < 16; x += 2) {
                                 const ulonglong2 mid = *reinterpret_cast<const ulonglong2*>(&ks.mid[c * 32 + 2 * x]);
                                 ulonglong2 ex = make_ulonglong2(0, 0);
-                                if (!plain) ex = *reinterpret_cast<const ulonglong2*>(&ks.exponent[c * 32 + 2 * x]);
+                                if constexpr (!PLAIN) ex = *reinterpret_cast<const ulonglong2*>(&ks.exponent[c * 32 + 2 * x]);
 #pragma unroll
                                 for (int y = 0; y < 2; ++y) {
-                                    uint64_t sh = pair_of(base_shift, base_shift);
-                                    const uint64_t own = y ? ex.y : ex.x;
-                                    if (!plain) sh = add2(sh, own);
-                                    const float2 f = parts_of(fma2(add2(s[x + y], top2), fr2, sh));
+                                    uint64_t at = shift2;
+                                    if constexpr (!PLAIN) at = add2(at, y ? ex.y : ex.x);
+                                    const float2 f = parts_of(fma2(add2(s[x + y], top2), fr2, at));
                                     float p0 = ex2(f.x), p1 = ex2(f.y);
-                                    if (!plain) {
+                                    if constexpr (!PLAIN) {
                                         p0 = m >> (2 * (x + y)) & 1 ? p0 : 0.0f;
                                         p1 = m >> (2 * (x + y) + 1) & 1 ? p1 : 0.0f;
                                     }
                                     const uint64_t w = pair_of(p0, p1);
                                     mids = fma2(w, y ? mid.y : mid.x, mids);
-                                    if (plain) {
+                                    if constexpr (PLAIN) {
                                         total = add2(total, w);
                                     } else {                 // (weights carry their own key's exponent)
-                                        const float2 q = parts_of(own);
-                                        total = add2(total, mul2(w, pair_of(ex2(127.0f - q.x), ex2(127.0f - q.y))));
+                                        const float2 q = parts_of(y ? ex.y : ex.x);
+                                        total = fma2(w, pair_of(ex2(127.0f - q.x), ex2(127.0f - q.y)), total);
                                     }
                                     out[x + y] = pack_f16x2(p0, p1);
                                 }
@@ -399,19 +406,27 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                             chunk_mid = d.x + d.y;
                         };
                         weigh();
-                        if (plain && __any_sync(0xffffffffu, chunk_sum > kMost)) {
-                            float best = kNegInf;
+                        if constexpr (PLAIN)
+                            if (__any_sync(0xffffffffu, chunk_sum > kMost)) {
+                                float best = kNegInf;
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) {
-                                const float2 f = parts_of(s[x]);
-                                best = max3(best, f.x, f.y);
+                                for (int x = 0; x < 16; ++x) {
+                                    const float2 f = parts_of(s[x]);
+                                    best = max3(best, f.x, f.y);
+                                }
+                                move(chunk_sum > kMost ? best : kNegInf, (int)ks.one_exponent, c);
+                                weigh();
                             }
-                            move(chunk_sum > kMost ? best : kNegInf, (int)ks.one_exponent, c);
-                            weigh();
-                        }
                         sum += chunk_sum;
                         msum += chunk_mid;
                         tmem_store16(at_s + c * 16, out);
+                    };
+                    if (plain) {
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) chunk(c, Yes());
+                    } else {
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) chunk(c, No());
                     }
                     l += plain ? sum * ex2(127.0f - ks.one_exponent) : sum;
                     ml += msum;
@@ -667,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
         int done[2] = {0, 0}, tile0 = 0, parts = 0;
         while (walk.next(p, it)) {
             const int n = tiles_of(p, walk, it).count();
-            if (lane == 0) {
+            if (elect_one()) {
                 wait(&bars.q_ready, parts);
                 umma_fence_after();
                 auto scores = [&](int s, int i) {
