@@ -18,8 +18,8 @@
 // exponent for every key, so that no row's arithmetic depends on what it does not see; V' of a key without a finite pair
 // is zero there and everywhere, and rows that see it are NaN.
 //
-// Warps 0-3 and 4-7: the streams.  Warps 8-11 read the codes of a tile ahead into registers, and write K and V' of
-// the one at hand to shared memory.  Warp 12 issues the products.  Work is cut as in r9q_kv4_attention.cuh; an item that several
+// Warps 0-3 and 4-7: the streams; the first of each issues its products.  Warps 8-11 read the codes of a tile ahead into
+// registers, and write K and V' of the one at hand to shared memory.  Work is cut as in r9q_kv4_attention.cuh; an item that several
 // CTAs share is joined by a second kernel, a warp a row.
 #include <algorithm>
 
@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kTile = 128;                   // keys, and rows
 constexpr int kStreamThreads = 128, kConvertThreads = 128;
-constexpr int kThreads = 2 * kStreamThreads + kConvertThreads + 32;
+constexpr int kThreads = 2 * kStreamThreads + kConvertThreads;
 constexpr int kTileGroups = kTile / 16;
 constexpr int kRing = 4;                     // tiles whose scalars are kept
 struct Yes {
@@ -58,7 +58,7 @@ struct TreeNodes {
     int first[kMostNodes], instead[kMostNodes], parents[kMostNodes];
 };
 struct Bars {
-    uint64_t q_ready, k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_ready[2], o_full[2];
+    uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], o_full[2];
     uint32_t tmem;
     int failed;
 };
@@ -154,26 +154,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
     extern __shared__ uint8_t raw[];
     begin_chained();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = tid & 127;
-    Walk walk;
-    if (!walk.start(p, kMinGroups, kItemCost)) return;
     uint8_t* smem = raw + (1024u - smem_u32(raw) % 1024u) % 1024u;
     Bars& bars = *reinterpret_cast<Bars*>(smem + Z::kAtBars);
     auto scalars_of = [&](int tile) { return reinterpret_cast<KeyScalars*>(smem + Z::kAtScalars) + (tile & (kRing - 1)); };
     if (tid == 0) {
-        mbar_init(&bars.q_ready, 2 * kStreamThreads);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.k_full[i], kConvertThreads);
-            mbar_init(&bars.k_free[i], 1);
+            mbar_init(&bars.k_free[i], DUAL ? 2 : 1);
             mbar_init(&bars.v_full[i], kConvertThreads);
-            mbar_init(&bars.v_free[i], 1);
+            mbar_init(&bars.v_free[i], DUAL ? 2 : 1);
             mbar_init(&bars.s_full[i], 1);
-            mbar_init(&bars.p_ready[i], kStreamThreads);
             mbar_init(&bars.o_full[i], 1);
         }
         bars.failed = 0;
         fence_mbar_init();
     }
-    if (warp == 12) tmem_alloc(&bars.tmem, 512);
+    if (warp == 8) tmem_alloc(&bars.tmem, 512);
+    Walk walk;
+    const bool any = walk.start(p, kMinGroups, kItemCost);
     umma_fence_before();
     __syncthreads();
     umma_fence_after();
@@ -192,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
         const uint32_t at_s = mine + Z::kS + stream * 128, at_o = mine + Z::kO + stream * 128;
         TreeNodes& nodes = *reinterpret_cast<TreeNodes*>(smem + Z::kAtNodes);
         int done = 0, tile0 = 0;             // steps and tiles of earlier parts
-        while (walk.next(p, it)) {
+        while (any && walk.next(p, it)) {
             const Tiles tiles = tiles_of(p, walk, it);
             const int n = tiles.count(), steps = steps_of(n, stream);
             const int row = it.chunk * ROWS + half * kTile + t;              // of the item's rows
@@ -250,8 +248,40 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                 }
             }
             fence_proxy_async_smem();
-            mbar_arrive(&bars.q_ready);
-            part_barrier<1, 2 * kStreamThreads>();           // (the nodes are there)
+            part_barrier<1, 2 * kStreamThreads>();           // (Q and the nodes are there)
+            // ---- the products, by the stream's first warp ----
+            auto issue_scores = [&](int i) {
+                const int tile = tile0 + tile_of(i, stream), buf = tile & 1;
+                wait(&bars.k_full[buf], tile >> 1);
+                umma_fence_after();
+                const uint32_t q = smem_u32(smem) + half * Z::kQ, k = smem_u32(smem) + Z::kAtK + buf * Z::kQ;
+                if (elect_one()) {
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x)
+                        umma_f16(tmem + Z::kS + stream * 128, umma_sdesc_sw128(q + (x >> 2) * Z::kHalf + (x & 3) * 32),
+                                 umma_sdesc_sw128(k + (x >> 2) * Z::kHalf + (x & 3) * 32), idesc_f16(kTile), x > 0);
+                    umma_commit(&bars.s_full[stream]);
+                    umma_commit(&bars.k_free[buf]);
+                }
+                __syncwarp();
+            };
+            auto issue_values = [&](int i) {
+                const int tile = tile0 + tile_of(i, stream), buf = tile & 1;
+                wait(&bars.v_full[buf], tile >> 1);
+                umma_fence_after();
+                const uint32_t v = smem_u32(smem) + Z::kAtV + buf * Z::kV;
+                if (elect_one()) {
+#pragma unroll
+                    for (int x = 0; x < kTile / 16; ++x)
+                        umma_f16_tmem(tmem + Z::kO + stream * 128, tmem + Z::kS + stream * 128 + x * 8,
+                                      umma_sdesc_sw128(v + (x >> 2) * (D * 128) + (x & 3) * 32), idesc_f16(D), i > 0 || x > 0);
+                    umma_commit(&bars.o_full[stream]);
+                    umma_commit(&bars.v_free[buf]);
+                }
+                __syncwarp();
+            };
+            const bool issues = (warp & 3) == 0;
+            if (issues && steps > 0) issue_scores(0);
             const uint64_t node_mask = nodes.mask[node];
             const int first = nodes.first[node];
 
@@ -281,11 +311,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                         }
                     }
                     lost = lost || ((seen[0] & ks.bad[0]) | (seen[1] & ks.bad[1]) | (seen[2] & ks.bad[2]) | (seen[3] & ks.bad[3])) != 0;
-                    // Scores of 32 keys, over fr.
-                    auto scores = [&](int c, uint64_t (&s)[16]) {
-                        float a[32];
-                        tmem_ld(at_s + c * 32, a);
-                        tmem_wait_ld(a);
+                    // Scores of 32 keys, over fr, from their products.
+                    auto scores = [&](int c, const float (&a)[32], uint64_t (&s)[16]) {
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
                             const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&ks.k[c * 16 + x]);
@@ -342,31 +369,37 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                     };
                     if (!plain || __any_sync(0xffffffffu, !seen_any)) {       // the largest score and exponent of what the row sees
                         float best = kNegInf;
-                        int e = 0;
+                        int e = plain ? (int)ks.one_exponent : 0;
+                        bool none = false;                   // a score that is not a number
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
+                            float a[32];
                             uint64_t s[16];
-                            scores(c, s);
+                            tmem_ld(at_s + c * 32, a);
+                            tmem_wait_ld(a);
+                            scores(c, a, s);
                             const uint32_t m = c == 0 ? seen[0] : c == 1 ? seen[1] : c == 2 ? seen[2] : seen[3];
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) {
-                                const float2 f = parts_of(s[x / 2]);
-                                const float v = x & 1 ? f.y : f.x;
-                                if (m >> x & 1) {
-                                    best = v != v || best != best ? __int_as_float(0x7FC00000) : fmaxf(best, v);
-                                    e = max(e, (int)ks.exponent[c * 32 + x]);
-                                }
+                            for (int x = 0; x < 32; x += 2) {
+                                float2 f = parts_of(s[x / 2]);
+                                if (!(m >> x & 1)) f.x = kNegInf;
+                                if (!(m >> x & 2)) f.y = kNegInf;
+                                none = none || f.x != f.x || f.y != f.y;
+                                best = max3(best, f.x, f.y);
                             }
+                            if (!plain)
+                                for (uint32_t x = m; x; x &= x - 1) e = max(e, (int)ks.exponent[c * 32 + __ffs((int)x) - 1]);
                         }
+                        if (none) best = __int_as_float(0x7FC00000);
                         const bool over = (best - top) * fr + (float)(e - e_row) > (float)kSlack;
                         const bool rise = (best > kNegInf || best != best) && (!seen_any || !((best - top) * fr <= (float)kSlack) || e > e_row || over);
                         if (__any_sync(0xffffffffu, rise)) move(rise ? best : kNegInf, e, 0);
                     }
                     // Weights of 32 keys against the reference: as P, and their sums.
-                    auto chunk = [&](int c, auto tag) {
+                    auto chunk = [&](int c, const float (&a)[32], auto tag) {
                         constexpr bool PLAIN = decltype(tag)::value;
                         uint64_t s[16];
-                        scores(c, s);
+                        scores(c, a, s);
                         const uint32_t m = c == 0 ? seen[0] : c == 1 ? seen[1] : c == 2 ? seen[2] : seen[3];
                         uint32_t out[16];
                         float chunk_sum, chunk_mid;
@@ -421,19 +454,45 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                         msum += chunk_mid;
                         tmem_store16(at_s + c * 16, out);
                     };
-                    if (plain) {
+                    float a[32], z[32];
+                    tmem_ld(at_s, a);
+                    tmem_wait_ld(a);
+                    if (plain) {             // a chunk's products are loaded while another's are weighed
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) chunk(c, Yes());
+                        for (int c = 0; c < 4; c += 2) {
+                            tmem_ld(at_s + (c + 1) * 32, z);
+                            chunk(c, a, Yes());
+                            tmem_wait_ld(z);
+                            if (c == 0) tmem_ld(at_s + 64, a);
+                            chunk(c + 1, z, Yes());
+                            if (c == 0) tmem_wait_ld(a);
+                        }
                     } else {
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) chunk(c, No());
+                        for (int c = 0; c < 4; ++c) {
+                            chunk(c, a, No());
+                            if (c < 3) {
+                                tmem_ld(at_s + (c + 1) * 32, a);
+                                tmem_wait_ld(a);
+                            }
+                        }
                     }
                     l += plain ? sum * ex2(127.0f - ks.one_exponent) : sum;
                     ml += msum;
                     tmem_stored();
                 }
                 umma_fence_before();
-                mbar_arrive(&bars.p_ready[stream]);
+                if (stream == 0)
+                    part_barrier<3, kStreamThreads>();
+                else
+                    part_barrier<4, kStreamThreads>();
+                if (issues) {
+                    issue_values(i);
+                    if (i + 1 < steps) {
+                        wait(&bars.o_full[stream], done + i);                // (P is read: S takes its place)
+                        issue_scores(i + 1);
+                    }
+                }
             }
             // ---- the end of the part ----
             if (steps > 0) {
@@ -512,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                     } else {
 #pragma unroll
                         for (int z = 0; z < 16; z += 4)
-                            *reinterpret_cast<float4*>(part + (size_t)r * D + x + z) = make_float4(o[z], o[z + 1], o[z + 2], o[z + 3]);
+                            reinterpret_cast<float4*>(part)[(x + z) / 4 * ROWS + r] = make_float4(o[z], o[z + 1], o[z + 2], o[z + 3]);
                     }
                 }
                 if (live && it.whole && p.lse)
@@ -533,10 +592,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
             tile0 += n;
             if (walk.parted) break;
         }
-    } else if (warp < 12) {
+    } else {
         // --------------------------------------------------------------- codes --
         int tile0 = 0;
-        while (walk.next(p, it)) {
+        while (any && walk.next(p, it)) {
             const Tiles tiles = tiles_of(p, walk, it);
             const int n = tiles.count(), gmax = min(it.g_end, (tiles.len + 15) >> 4);
             const int32_t* table = p.table + (int64_t)it.b * p.max_pages;
@@ -676,107 +735,36 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
             tile0 += n;
             if (walk.parted) break;
         }
-    } else {
-        // ------------------------------------------------------------ products --
-        constexpr uint32_t kScores = idesc_f16(kTile), kValues = idesc_f16(D);
-        int done[2] = {0, 0}, tile0 = 0, parts = 0;
-        while (walk.next(p, it)) {
-            const int n = tiles_of(p, walk, it).count();
-            if (elect_one()) {
-                wait(&bars.q_ready, parts);
-                umma_fence_after();
-                auto scores = [&](int s, int i) {
-                    const int tile = tile0 + tile_of(i, s), buf = tile & 1;
-                    wait(&bars.k_full[buf], tile >> 1);
-                    umma_fence_after();
-                    const uint32_t q = smem_u32(smem) + (DUAL ? s * Z::kQ : 0), k = smem_u32(smem + Z::kAtK + buf * Z::kQ);
-#pragma unroll
-                    for (int x = 0; x < D / 16; ++x)
-                        umma_f16(tmem + Z::kS + s * 128, umma_sdesc_sw128(q + (x >> 2) * Z::kHalf + (x & 3) * 32),
-                                 umma_sdesc_sw128(k + (x >> 2) * Z::kHalf + (x & 3) * 32), kScores, x > 0);
-                    umma_commit(&bars.s_full[s]);
-                    if (!DUAL || s == 1) umma_commit(&bars.k_free[buf]);
-                };
-                auto values = [&](int s, int i) {
-                    const int tile = tile0 + tile_of(i, s), buf = tile & 1;
-                    wait(&bars.v_full[buf], tile >> 1);
-                    wait(&bars.p_ready[s], done[s] + i);
-                    umma_fence_after();
-                    const uint32_t v = smem_u32(smem + Z::kAtV + buf * Z::kV);
-#pragma unroll
-                    for (int x = 0; x < kTile / 16; ++x)
-                        umma_f16_tmem(tmem + Z::kO + s * 128, tmem + Z::kS + s * 128 + x * 8,
-                                      umma_sdesc_sw128(v + (x >> 2) * (D * 128) + (x & 3) * 32), kValues, i > 0 || x > 0);
-                    umma_commit(&bars.o_full[s]);
-                    if (!DUAL || s == 1) umma_commit(&bars.v_free[buf]);
-                };
-                const int steps[2] = {steps_of(n, 0), steps_of(n, 1)};
-                for (int s = 0; s < 2; ++s)
-                    if (steps[s] > 0) scores(s, 0);
-#pragma unroll 1
-                for (int i = 0; i < steps[0]; ++i)
-#pragma unroll 1
-                    for (int s = 0; s < 2; ++s) {
-                        if (i >= steps[s]) continue;
-                        values(s, i);
-                        if (i + 1 < steps[s]) {
-                            wait(&bars.o_full[s], done[s] + i);              // (P is read: S takes its place)
-                            scores(s, i + 1);
-                        }
-                    }
-                // nothing is in flight at the end, whatever gave up
-                for (int s = 0; s < 2; ++s)
-                    if (steps[s] > 0 && !mbar_wait(&bars.o_full[s], (done[s] + steps[s] - 1) & 1)) record_error(p.err, kErrTimeout);
-                done[0] += steps[0];
-                done[1] += steps[1];
-            }
-            tile0 += n;
-            ++parts;
-            __syncwarp();
-            if (walk.parted) break;
-        }
     }
     __syncwarp();
     umma_fence_before();
     __syncthreads();
     umma_fence_after();
-    if (warp == 12) tmem_dealloc(tmem, 512);
+    if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-// Items that several CTAs share: a warp a row.
+// Items that several CTAs share.  A partial is [D / 4][ROWS] of four elements, then the rows' references and sums; a thread
+// joins four elements of a row, a warp those of 32 rows.
+constexpr int kJoinRows = 32, kJoinPieces = 8;
 template <int D, int ROWS>
-__global__ void __launch_bounds__(256) join_kernel(const Kv4AttnParams p, const int2* items, int row_blocks) {
+__global__ void __launch_bounds__(kJoinRows * kJoinPieces) join_kernel(const Kv4AttnParams p, const int2* items, int row_blocks) {
     begin_chained();
-    const int lane = threadIdx.x & 31, item = blockIdx.x / row_blocks;
-    const int r = (blockIdx.x - item * row_blocks) * 8 + (threadIdx.x >> 5);
+    constexpr int PIECES = D / 4 / kJoinPieces;              // blocks that share a row
+    const int x = blockIdx.x / PIECES, item = x / row_blocks;
+    const int r = (x - item * row_blocks) * kJoinRows + (threadIdx.x & 31);
+    const int piece = (blockIdx.x - x * PIECES) * kJoinPieces + (threadIdx.x >> 5);
     const int2 by = items[item];
     if (by.x == by.y || r >= ROWS) return;
     const int chunks = p.chunks.d, per_seq = p.c.heads * chunks, b = item / per_seq, rest = item - b * per_seq;
     const int hk = rest / chunks, chunk = rest - hk * chunks, row = chunk * ROWS + r;
     if (row >= p.Lq * p.G) return;
     const int node = row / p.G, head = hk * p.G + (row - node * p.G);
-    auto slot = [&](int c) { return p.part + ((size_t)c * 2 + (c == by.x ? 1 : 0)) * ((size_t)ROWS * (D + 2)); };
-    const int n = by.y - by.x + 1;
-    float top = kNegInf;
-    for (int c = lane; c < n; c += 32) top = fmaxf(top, slot(by.x + c)[(size_t)ROWS * D + r]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float base = top > kNegInf ? top : 0.0f;
-    float sum = 0.0f, x[D / 32] = {};
-#pragma unroll 4
-    for (int c = 0; c < n; ++c) {
-        const float* s = slot(by.x + c);
-        const float k = ex2(s[(size_t)ROWS * D + r] - base);
-        sum = fmaf(k, s[(size_t)ROWS * D + ROWS + r], sum);
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) x[i] = fmaf(k, s[(size_t)r * D + lane * (D / 32) + i], x[i]);
-    }
     // the node, as the other kernel found it
     const int32_t* parents = p.parents + (int64_t)b * p.Lq;
     Instead instead = kAsItIs;
-    if (parents[node] == -2)
+    if (parents[node] == -2) {
         instead = kNothing;
-    else
+    } else {
         for (int t = node; t >= 0;) {
             const int up = parents[t];
             if (up != -1 && (up < 0 || up >= t)) {
@@ -785,16 +773,28 @@ __global__ void __launch_bounds__(256) join_kernel(const Kv4AttnParams p, const 
             }
             t = up;
         }
+    }
+    auto slot = [&](int c) { return p.part + ((size_t)c * 2 + (c == by.x ? 1 : 0)) * ((size_t)ROWS * (D + 2)); };
+    float top = kNegInf;
+#pragma unroll 4
+    for (int c = by.x; c <= by.y; ++c) top = fmaxf(top, slot(c)[(size_t)ROWS * D + r]);
+    const float base = top > kNegInf ? top : 0.0f;
+    float sum = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int c = by.x; c <= by.y; ++c) {
+        const float* s = slot(c);
+        const float k = ex2(s[(size_t)ROWS * D + r] - base);
+        const float4 v = reinterpret_cast<const float4*>(s)[piece * ROWS + r];
+        sum = fmaf(k, s[(size_t)ROWS * D + ROWS + r], sum);
+        o = make_float4(fmaf(k, v.x, o.x), fmaf(k, v.y, o.y), fmaf(k, v.z, o.z), fmaf(k, v.w, o.w));
+    }
     const int64_t out = ((int64_t)b * p.Lq + node) * (p.c.heads * p.G) + head;
     const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-    uint32_t w[D / 64];
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-        w[i] = pack_bf16x2(x[2 * i] * inv, x[2 * i + 1] * inv);
-        if (instead != kAsItIs) w[i] = instead == kNothing ? 0u : 0x7FC07FC0u;
-        reinterpret_cast<uint32_t*>(p.o + out * D)[lane * (D / 64) + i] = w[i];
-    }
-    if (p.lse && lane == 0)
+    uint2 w = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (instead != kAsItIs) w.x = w.y = instead == kNothing ? 0u : 0x7FC07FC0u;
+    *reinterpret_cast<uint2*>(p.o + out * D + piece * 4) = w;
+    if (p.lse && piece == 0)
         p.lse[out] = instead == kNothing ? kNegInf : instead == kNan ? __int_as_float(0x7FC00000) : log_sum_exp(top, sum);
 }
 
@@ -809,9 +809,9 @@ cudaError_t launch(Kv4AttnParams p, int2* items, int sms, cudaStream_t st) {
     p.page_groups = fast_div(p.c.page / 16);
     e = launch_chained(tree_attention_kernel<D, DUAL>, used_sms(sms), kThreads, Shape<D>::kBytes, st, p, items);
     if (e != cudaSuccess) return e;
-    const int row_blocks = (std::min(ROWS, p.Lq * p.G) + 7) / 8;
-    return launch_chained(join_kernel<D, ROWS>, (unsigned)p.B * p.c.heads * p.chunks.d * row_blocks, 256, 0, st, p,
-                          static_cast<const int2*>(items), row_blocks);
+    const int row_blocks = (std::min(ROWS, p.Lq * p.G) + kJoinRows - 1) / kJoinRows;
+    return launch_chained(join_kernel<D, ROWS>, (unsigned)p.B * p.c.heads * p.chunks.d * row_blocks * (D / 4 / kJoinPieces),
+                          kJoinRows * kJoinPieces, 0, st, p, static_cast<const int2*>(items), row_blocks);
 }
 
 }  // namespace
