@@ -39,7 +39,7 @@ constexpr int kMStride = 36;
 constexpr int kSorted = 256;                 // sequences that are put in order
 
 // Scalars of a chunk's tokens.
-struct Scalars {
+struct alignas(16) Scalars {
     ulonglong2 x[kChunk / 2];                // X = x v + y W, pairs of two tokens
     float fade[kChunk], o[kChunk];           // o = o (fade Y + U P^T)
     float last[kChunk];                      // A(n, i) / |k_i|
@@ -65,6 +65,8 @@ struct Layout {
     static constexpr int kScalars = kM + 32 * kMStride * 4;
     static constexpr int kOut = kScalars + 2 * (int)sizeof(Scalars);         // outputs [64][D] on their way
     static constexpr int kBars = kOut + kChunk * D * 2;
+    static_assert(kL % 16 == 0 && kM % 16 == 0 && kScalars % 16 == 0 && sizeof(Scalars) % 16 == 0 && kOut % 16 == 0 && kBars % 16 == 0,
+                  "16-byte loads");
     // tensor memory, columns.  S's parts are 64 columns apart.  X's third part takes a place that W alone reads (of S's
     // third), U, in two sums, those of S's first and second.  W is replaced by two parts of X and they by two of u: of
     // tokens 32 i on in the columns 32 i and 32 i + 16 on; U P^T adds to A(., 0) Y.  (A product takes at least 55 cycles,

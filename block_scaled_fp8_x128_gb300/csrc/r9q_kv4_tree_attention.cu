@@ -11,7 +11,7 @@
 //   score = fr (sk S + lk sum(q))
 //   O += P V'      P the weights in fp16, in S's place in tensor memory; V' = (c - 8) sv 2^(11 - E), fp16, E the exponent of
 //                  the largest step of the tile's keys
-// and what V' leaves out, lv + 8 sv, is summed with the weights in fp32.  Sums of (c - 8), which are near zero, do not
+// and what V' leaves out, lv + 8 sv, is summed with the weights in fp32 (of fp16 values).  Sums of (c - 8), which are near zero, do not
 // drift as those of codes would.  References move as there: a row's weights are taken against top - 8 + E of its own,
 // which moves only when a chunk of 32 weights passes 2^15, and takes what is summed and P with it.
 // Tiles in which some row does not see some key (the tree's own, those at a window's edge or at the sequence's end) keep an
@@ -44,16 +44,16 @@ struct No {
 constexpr float kMost = 32768.0f;            // a sum of 32 weights over this moves the reference
 
 // Of a tile's keys.
-struct KeyScalars {
-    float4 k[kTile / 2];                     // of two keys: both steps, both lowest values
-    float mid[kTile];                        // (lv + 8 sv) 2^-exponent
+struct alignas(16) KeyScalars {
+    uint32_t k[kTile];                       // the pair, as in the cache
+    uint16_t mid[kTile];                     // (lv + 8 sv) 2^-exponent as fp16: fewer bytes for every row's thread to read
     float exponent[kTile];                   // biased; all the same where every row sees every key
     uint16_t v[kTile];                       // steps as fp16, 2^(11 - exponent) times
     uint32_t bad[4];                         // keys without a finite value pair
     uint32_t have;                           // groups that were read
     float one_exponent;
 };
-struct TreeNodes {
+struct alignas(16) TreeNodes {
     uint64_t mask[kMostNodes];
     int first[kMostNodes], instead[kMostNodes], parents[kMostNodes];
 };
@@ -72,6 +72,7 @@ struct Shape {
     static constexpr int kAtNodes = kAtScalars + kRing * (int)sizeof(KeyScalars);
     static constexpr int kAtMeet = kAtNodes + (int)sizeof(TreeNodes);        // references and sums of one stream for the other
     static constexpr int kAtBars = kAtMeet + 2 * kTile * 4;
+    static_assert(sizeof(KeyScalars) % 16 == 0 && kAtNodes % 16 == 0 && kAtBars % 16 == 0, "16-byte loads");
     static constexpr size_t kBytes = kAtBars + sizeof(Bars) + 1024;
     static constexpr int kS = 0, kO = 256;                   // tensor memory: S (and P) of both streams, O of both
 };
@@ -119,6 +120,14 @@ struct Waits {
         }
     }
 };
+
+// Adds the products of two pairs of fp16 values, exactly, to a and b.
+__device__ __forceinline__ void add_products(float& a, float& b, uint32_t x, uint32_t y) {
+    asm("{\n\t.reg .b16 xl, xh, yl, yh;\n\tmov.b32 {xl, xh}, %2;\n\tmov.b32 {yl, yh}, %3;\n\tfma.rn.f32.f16 %0, xl, yl, %0;\n\t"
+        "fma.rn.f32.f16 %1, xh, yh, %1;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "r"(x), "r"(y));
+}
 
 // Bits [lo, hi) of 32.
 __device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
@@ -285,8 +294,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
             const uint64_t node_mask = nodes.mask[node];
             const int first = nodes.first[node];
 
-            float top = 0.0f, l = 0.0f, ml = 0.0f;           // as in r9q_kv4_attention.cu
-            int e_row = kMinExponent;
+            // l: the sum of 2^(score - top + 8).  O and ml: those weights times 2^(e - e_row), e a key's exponent.
+            float top = 0.0f, l = 0.0f, ml = 0.0f;
+            int e_row = 1;
             bool seen_any = false, lost = false;
             const uint64_t fr2 = pair_of(fr, fr), qs2 = pair_of(qs, qs);
 #pragma unroll 1
@@ -314,27 +324,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                     // Scores of 32 keys, over fr, from their products.
                     auto scores = [&](int c, const float (&a)[32], uint64_t (&s)[16]) {
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) {
-                            const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&ks.k[c * 16 + x]);
-                            s[x] = fma2(k.x, pair_of(a[2 * x], a[2 * x + 1]), mul2(k.y, qs2));
+                        for (int x = 0; x < 16; x += 2) {
+                            const uint4 k = *reinterpret_cast<const uint4*>(&ks.k[c * 32 + 2 * x]);
+                            s[x] = fma2(pair_of(bf16_lo(k.x), bf16_lo(k.y)), pair_of(a[2 * x], a[2 * x + 1]),
+                                        mul2(pair_of(bf16_hi(k.x), bf16_hi(k.y)), qs2));
+                            s[x + 1] = fma2(pair_of(bf16_lo(k.z), bf16_lo(k.w)), pair_of(a[2 * x + 2], a[2 * x + 3]),
+                                            mul2(pair_of(bf16_hi(k.z), bf16_hi(k.w)), qs2));
                         }
                     };
-                    // The row's reference to the larger of its own and (best, e); `c`: chunks of P that are written.
+                    // The row's reference to `to` and its exponent to `to_e`; `c`: chunks of P that are written.
                     float sum = 0.0f, msum = 0.0f;           // of the tile
-                    auto move = [&](float best, int e, int c) {
-                        const float to = seen_any ? fmaxf(top, best) : best;
-                        const bool any = best > kNegInf || best != best;
-                        const int e_to = any ? max(e_row, e) : e_row;
-                        const float alpha = seen_any ? ex2(fmaf(top - (any ? to : top), fr, (float)(e_row - e_to))) : 0.0f;
-                        if (any) {
-                            top = to;
-                            e_row = e_to;
-                            seen_any = true;
-                        }
+                    auto move = [&](float to, int to_e, int c) {
+                        const float alpha = seen_any ? ex2((top - to) * fr) : 0.0f;
+                        const float alpha_w = alpha * ex2((float)(e_row - to_e));
+                        top = to;
+                        e_row = to_e;
                         l *= alpha;
-                        ml *= alpha;
                         sum *= alpha;
-                        msum *= alpha;
+                        ml *= alpha_w;
+                        msum *= alpha_w;
                         if (i > 0) {                         // O, once the last tile's product is in it
                             wait(&bars.o_full[stream], done + i - 1);
                             umma_fence_after();
@@ -345,24 +353,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                                 tmem_ld(at_o + x, o);
                                 tmem_wait_ld(o);
 #pragma unroll
-                                for (int z = 0; z < 16; ++z) y[z] = __float_as_uint(o[z] * alpha);
+                                for (int z = 0; z < 16; ++z) y[z] = __float_as_uint(o[z] * alpha_w);
                                 tmem_store16(at_o + x, y);
                             }
                         }
 #pragma unroll 1
                         for (int x = 0; x < c; ++x) {
+                            const uint32_t both = pack_f16x2(alpha_w, alpha_w);
                             float w[16];
                             uint32_t y[16];
                             tmem_ld(at_s + x * 16, w);
                             tmem_wait_ld(w);
 #pragma unroll
-                            for (int z = 0; z < 16; ++z) {
-                                const uint32_t h = __float_as_uint(w[z]);
-                                uint32_t a2, r;
-                                a2 = pack_f16x2(alpha, alpha);
-                                asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(a2));
-                                y[z] = r;
-                            }
+                            for (int z = 0; z < 16; ++z) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[z]) : "r"(__float_as_uint(w[z])), "r"(both));
                             tmem_store16(at_s + x * 16, y);
                         }
                         tmem_stored();
@@ -390,10 +393,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                             if (!plain)
                                 for (uint32_t x = m; x; x &= x - 1) e = max(e, (int)ks.exponent[c * 32 + __ffs((int)x) - 1]);
                         }
-                        if (none) best = __int_as_float(0x7FC00000);
-                        const bool over = (best - top) * fr + (float)(e - e_row) > (float)kSlack;
-                        const bool rise = (best > kNegInf || best != best) && (!seen_any || !((best - top) * fr <= (float)kSlack) || e > e_row || over);
-                        if (__any_sync(0xffffffffu, rise)) move(rise ? best : kNegInf, e, 0);
+                        // (a score that is not a number makes the row's sums that, whatever the reference)
+                        const bool any = best > kNegInf || none;
+                        const bool up = any && (!seen_any || (best - top) * fr > (float)kSlack);
+                        const int to_e = any ? max(e_row, e) : e_row;
+                        if (__any_sync(0xffffffffu, up || to_e > e_row)) move(up ? (none ? 0.0f : best) : top, to_e, 0);
+                        seen_any = seen_any || any;
+                    } else if (__any_sync(0xffffffffu, (int)ks.one_exponent > e_row)) {
+                        move(top, max(e_row, (int)ks.one_exponent), 0);
                     }
                     // Weights of 32 keys against the reference: as P, and their sums.
                     auto chunk = [&](int c, const float (&a)[32], auto tag) {
@@ -405,38 +412,37 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                         float chunk_sum, chunk_mid;
                         auto weigh = [&]() {
                             const uint64_t top2 = pair_of(-top, -top);
-                            const float sh = (float)(kHeadroom - e_row) + (PLAIN ? ks.one_exponent : 0.0f);
-                            const uint64_t shift2 = pair_of(sh, sh);
-                            uint64_t total = 0, mids = 0;
+                            const uint64_t shift2 = pair_of((float)kHeadroom, (float)kHeadroom);
+                            const float f_all = PLAIN ? ex2(ks.one_exponent - (float)e_row) : 1.0f;
+                            uint64_t total = 0;
+                            float mid0 = 0.0f, mid1 = 0.0f;
+                            uint4 mid;
 #pragma unroll
                             for (int x = 0; x < 16; x += 2) {
-                                const ulonglong2 mid = *reinterpret_cast<const ulonglong2*>(&ks.mid[c * 32 + 2 * x]);
+                                if (x % 4 == 0) mid = *reinterpret_cast<const uint4*>(&ks.mid[c * 32 + 2 * x]);
                                 ulonglong2 ex = make_ulonglong2(0, 0);
                                 if constexpr (!PLAIN) ex = *reinterpret_cast<const ulonglong2*>(&ks.exponent[c * 32 + 2 * x]);
 #pragma unroll
                                 for (int y = 0; y < 2; ++y) {
-                                    uint64_t at = shift2;
-                                    if constexpr (!PLAIN) at = add2(at, y ? ex.y : ex.x);
-                                    const float2 f = parts_of(fma2(add2(s[x + y], top2), fr2, at));
-                                    float p0 = ex2(f.x), p1 = ex2(f.y);
+                                    const float2 at = parts_of(fma2(add2(s[x + y], top2), fr2, shift2));
+                                    float p0 = ex2(at.x), p1 = ex2(at.y), f0 = f_all, f1 = f_all;
                                     if constexpr (!PLAIN) {
                                         p0 = m >> (2 * (x + y)) & 1 ? p0 : 0.0f;
                                         p1 = m >> (2 * (x + y) + 1) & 1 ? p1 : 0.0f;
+                                        const float2 q = parts_of(y ? ex.y : ex.x);          // (unseen keys may have any)
+                                        f0 = ex2(fminf(q.x - (float)e_row, 0.0f));
+                                        f1 = ex2(fminf(q.y - (float)e_row, 0.0f));
                                     }
                                     const uint64_t w = pair_of(p0, p1);
-                                    mids = fma2(w, y ? mid.y : mid.x, mids);
-                                    if constexpr (PLAIN) {
-                                        total = add2(total, w);
-                                    } else {                 // (weights carry their own key's exponent)
-                                        const float2 q = parts_of(y ? ex.y : ex.x);
-                                        total = fma2(w, pair_of(ex2(127.0f - q.x), ex2(127.0f - q.y)), total);
-                                    }
-                                    out[x + y] = pack_f16x2(p0, p1);
+                                    total = add2(total, w);
+                                    const float2 v = parts_of(mul2(w, pair_of(f0, f1)));
+                                    out[x + y] = pack_f16x2(v.x, v.y);
+                                    add_products(mid0, mid1, out[x + y], x % 4 ? (y ? mid.w : mid.z) : (y ? mid.y : mid.x));
                                 }
                             }
-                            const float2 a = parts_of(total), d = parts_of(mids);
-                            chunk_sum = a.x + a.y;
-                            chunk_mid = d.x + d.y;
+                            const float2 both = parts_of(total);
+                            chunk_sum = both.x + both.y;
+                            chunk_mid = mid0 + mid1;
                         };
                         weigh();
                         if constexpr (PLAIN)
@@ -447,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                                     const float2 f = parts_of(s[x]);
                                     best = max3(best, f.x, f.y);
                                 }
-                                move(chunk_sum > kMost ? best : kNegInf, (int)ks.one_exponent, c);
+                                move(chunk_sum > kMost ? fmaxf(top, best) : top, e_row, c);
                                 weigh();
                             }
                         sum += chunk_sum;
@@ -477,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                             }
                         }
                     }
-                    l += plain ? sum * ex2(127.0f - ks.one_exponent) : sum;
+                    l += sum;
                     ml += msum;
                     tmem_stored();
                 }
@@ -500,8 +506,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                 umma_fence_after();
             }
             if (lost) l = __int_as_float(0x7FC00000);
-            float m = seen_any ? fmaf(top, fr, (float)(e_row - kHeadroom - 127)) : kNegInf;
-            float scale_o = steps > 0 && seen_any ? 0x1p-11f : 0.0f;
+            // As partials are: both sums in units of 2^-e for one e, under which they are finite.
+            const int e_out = max(e_row, kMinExponent);
+            const float to_out = ex2((float)(e_row - e_out));
+            l *= ex2((float)(127 - e_out));
+            ml *= to_out;
+            float m = seen_any ? fmaf(top, fr, (float)(e_out - kHeadroom - 127)) : kNegInf;
+            float scale_o = steps > 0 && seen_any ? 0x1p-11f * to_out : 0.0f;
             float total_m = m, total_l = l;
             float* meet_m = reinterpret_cast<float*>(smem + Z::kAtMeet);
             float* meet_l = meet_m + kTile;
@@ -645,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                 const uint32_t kpair = here ? kp : 0u, vpair = here ? vp : 0u;
                 const int xs = (int)(vpair >> 7) & 255, xl = (int)(vpair >> 23) & 255;
                 const bool bad = xs == 255 || xl == 255;
-                int e = bad ? kMinExponent : min(max(max(xs, xl - kLowestBits), kMinExponent), 253);
+                int e = bad ? 1 : min(max(max(xs, xl - kLowestBits), 1), 253);
                 const uint32_t got = __ballot_sync(0xffffffffu, k_at != kNoGroup), not_good = __ballot_sync(0xffffffffu, bad);
                 if (lane == 0) {
                     ks.bad[warp & 3] = not_good;
@@ -664,14 +675,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                 const int one = max(max(all.x, all.y), max(all.z, all.w));
                 const bool plain = tiles.plain(j) && have == 0xFFu;
                 if (plain) e = one;
-                float* pair = reinterpret_cast<float*>(&ks.k[t >> 1]) + (t & 1);
-                pair[0] = bf16_lo(kpair);
-                pair[2] = bf16_hi(kpair);
+                ks.k[t] = kpair;
                 const float sv = bad ? 0.0f : bf16_lo(vpair), lv = bad ? 0.0f : bf16_hi(vpair);
-                ks.mid[t] = fmaf(8.0f, sv * __uint_as_float((uint32_t)(254 - e) << 23), lv * __uint_as_float((uint32_t)(254 - e) << 23));
+                const float down = __uint_as_float((uint32_t)(254 - e) << 23);
+                ks.mid[t] = (uint16_t)pack_f16x2(fmaf(8.0f, sv * down, lv * down), 0.0f);
                 ks.exponent[t] = (float)e;
                 // 2^(11 + 127 - e) in two factors, so that neither is out of range
-                ks.v[t] = (uint16_t)pack_f16x2(sv * __uint_as_float((uint32_t)(254 - e) << 23) * 2048.0f, 0.0f);
+                ks.v[t] = (uint16_t)pack_f16x2(sv * down * 2048.0f, 0.0f);
                 if (t == 0) {
                     ks.have = have;
                     ks.one_exponent = (float)one;
