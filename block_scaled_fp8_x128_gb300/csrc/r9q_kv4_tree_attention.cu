@@ -41,6 +41,7 @@ struct Yes {
 struct No {
     static constexpr bool value = false;
 };
+constexpr float kNear = 4194304.0f;          // 2^22
 constexpr float kMost = 32768.0f;            // a sum of 32 weights over this moves the reference
 
 // Of a tile's keys.
@@ -142,6 +143,8 @@ struct Tiles {
     int g_begin, g_end, len, all_lo, base;
     __device__ __forceinline__ int count() const { return (g_end - g_begin + kTileGroups - 1) / kTileGroups; }
     __device__ __forceinline__ int first_key(int j) const { return (g_begin + j * kTileGroups) * 16; }
+    // some row does not see some of its keys before the tree
+    __device__ __forceinline__ bool edge(int j) const { return first_key(j) < all_lo; }
     // every row sees all of its keys (if all its pages are there)
     __device__ __forceinline__ bool plain(int j) const {
         return first_key(j) >= all_lo && first_key(j) + kTile <= base && g_begin + (j + 1) * kTileGroups <= g_end;
@@ -294,8 +297,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
             const uint64_t node_mask = nodes.mask[node];
             const int first = nodes.first[node];
 
-            // l: the sum of 2^(score - top + 8).  O and ml: those weights times 2^(e - e_row), e a key's exponent.
-            float top = 0.0f, l = 0.0f, ml = 0.0f;
+            // l: the sum of 2^(score - ref + 8), ref = rint(top fr), an integer, so that one fused multiply-add makes the
+            // exponent (for scores under 2^22; larger ones take the difference from top first, and ref = top fr).
+            // O and ml: those weights times 2^(e - e_row), e a key's exponent.
+            float top = 0.0f, ref = 0.0f, l = 0.0f, ml = 0.0f;
             int e_row = 1;
             bool seen_any = false, lost = false;
             const uint64_t fr2 = pair_of(fr, fr), qs2 = pair_of(qs, qs);
@@ -335,9 +340,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                     // The row's reference to `to` and its exponent to `to_e`; `c`: chunks of P that are written.
                     float sum = 0.0f, msum = 0.0f;           // of the tile
                     auto move = [&](float to, int to_e, int c) {
-                        const float alpha = seen_any ? ex2((top - to) * fr) : 0.0f;
+                        const bool near = fabsf(to * fr) < kNear || fabsf(ref) < kNear;
+                        const float to_ref = fabsf(to * fr) < kNear ? rintf(to * fr) : to * fr;
+                        const float alpha = seen_any ? ex2(near ? ref - to_ref : (top - to) * fr) : 0.0f;
                         const float alpha_w = alpha * ex2((float)(e_row - to_e));
                         top = to;
+                        ref = to_ref;
                         e_row = to_e;
                         l *= alpha;
                         sum *= alpha;
@@ -390,8 +398,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                                 none = none || f.x != f.x || f.y != f.y;
                                 best = max3(best, f.x, f.y);
                             }
-                            if (!plain)
-                                for (uint32_t x = m; x; x &= x - 1) e = max(e, (int)ks.exponent[c * 32 + __ffs((int)x) - 1]);
+                            if (!plain) {                    // (keys before the tree share theirs, but at a window's edge)
+                                uint32_t x = m;
+                                if (!tiles.edge(j)) {
+                                    const uint32_t tree = ~bits_between(0, tiles.base - tiles.first_key(j) - 32 * c);
+                                    if (m & ~tree) e = max(e, (int)ks.one_exponent);
+                                    x &= tree;
+                                }
+                                for (; x; x &= x - 1) e = max(e, (int)ks.exponent[c * 32 + __ffs((int)x) - 1]);
+                            }
                         }
                         // (a score that is not a number makes the row's sums that, whatever the reference)
                         const bool any = best > kNegInf || none;
@@ -402,85 +417,119 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                     } else if (__any_sync(0xffffffffu, (int)ks.one_exponent > e_row)) {
                         move(top, max(e_row, (int)ks.one_exponent), 0);
                     }
-                    // Weights of 32 keys against the reference: as P, and their sums.
-                    auto chunk = [&](int c, const float (&a)[32], auto tag) {
-                        constexpr bool PLAIN = decltype(tag)::value;
+                    // Weights of 32 keys against the reference: as P's columns, and their sums.
+                    auto weigh = [&](int c, const float (&a)[32], uint32_t (&out)[16], float& chunk_sum, float& chunk_mid, auto tag) {
+                        constexpr bool FAST = decltype(tag)::value;
                         uint64_t s[16];
                         scores(c, a, s);
                         const uint32_t m = c == 0 ? seen[0] : c == 1 ? seen[1] : c == 2 ? seen[2] : seen[3];
-                        uint32_t out[16];
-                        float chunk_sum, chunk_mid;
-                        auto weigh = [&]() {
-                            const uint64_t top2 = pair_of(-top, -top);
-                            const uint64_t shift2 = pair_of((float)kHeadroom, (float)kHeadroom);
-                            const float f_all = PLAIN ? ex2(ks.one_exponent - (float)e_row) : 1.0f;
-                            uint64_t total = 0;
-                            float mid0 = 0.0f, mid1 = 0.0f;
-                            uint4 mid;
+                        const bool near = fabsf(ref) < kNear;
+                        const uint64_t top2 = pair_of(-top, -top), shift2 = pair_of((float)kHeadroom - ref, (float)kHeadroom - ref);
+                        uint64_t total = 0;
+                        float mid0 = 0.0f, mid1 = 0.0f;
+                        uint4 mid;
 #pragma unroll
-                            for (int x = 0; x < 16; x += 2) {
-                                if (x % 4 == 0) mid = *reinterpret_cast<const uint4*>(&ks.mid[c * 32 + 2 * x]);
-                                ulonglong2 ex = make_ulonglong2(0, 0);
-                                if constexpr (!PLAIN) ex = *reinterpret_cast<const ulonglong2*>(&ks.exponent[c * 32 + 2 * x]);
-#pragma unroll
-                                for (int y = 0; y < 2; ++y) {
-                                    const float2 at = parts_of(fma2(add2(s[x + y], top2), fr2, shift2));
-                                    float p0 = ex2(at.x), p1 = ex2(at.y), f0 = f_all, f1 = f_all;
-                                    if constexpr (!PLAIN) {
-                                        p0 = m >> (2 * (x + y)) & 1 ? p0 : 0.0f;
-                                        p1 = m >> (2 * (x + y) + 1) & 1 ? p1 : 0.0f;
-                                        const float2 q = parts_of(y ? ex.y : ex.x);          // (unseen keys may have any)
-                                        f0 = ex2(fminf(q.x - (float)e_row, 0.0f));
-                                        f1 = ex2(fminf(q.y - (float)e_row, 0.0f));
-                                    }
-                                    const uint64_t w = pair_of(p0, p1);
-                                    total = add2(total, w);
-                                    const float2 v = parts_of(mul2(w, pair_of(f0, f1)));
-                                    out[x + y] = pack_f16x2(v.x, v.y);
-                                    add_products(mid0, mid1, out[x + y], x % 4 ? (y ? mid.w : mid.z) : (y ? mid.y : mid.x));
-                                }
+                        for (int x = 0; x < 16; ++x) {
+                            if (x % 4 == 0) mid = *reinterpret_cast<const uint4*>(&ks.mid[c * 32 + 2 * x]);
+                            uint64_t at = fma2(s[x], fr2, shift2);
+                            if constexpr (!FAST)
+                                if (!near) at = fma2(add2(s[x], top2), fr2, pair_of((float)kHeadroom, (float)kHeadroom));
+                            const float2 f = parts_of(at);
+                            float p0 = ex2(f.x), p1 = ex2(f.y), w0, w1;
+                            if constexpr (FAST) {
+                                w0 = p0;
+                                w1 = p1;
+                            } else {                         // (unseen keys may have any pair)
+                                const float2 ex = *reinterpret_cast<const float2*>(&ks.exponent[c * 32 + 2 * x]);
+                                p0 = m >> (2 * x) & 1 ? p0 : 0.0f;
+                                p1 = m >> (2 * x + 1) & 1 ? p1 : 0.0f;
+                                w0 = p0 * ex2(fminf(ex.x - (float)e_row, 0.0f));
+                                w1 = p1 * ex2(fminf(ex.y - (float)e_row, 0.0f));
                             }
-                            const float2 both = parts_of(total);
-                            chunk_sum = both.x + both.y;
-                            chunk_mid = mid0 + mid1;
-                        };
-                        weigh();
-                        if constexpr (PLAIN)
-                            if (__any_sync(0xffffffffu, chunk_sum > kMost)) {
+                            total = add2(total, pair_of(p0, p1));
+                            out[x] = pack_f16x2(w0, w1);
+                            add_products(mid0, mid1, out[x], x % 4 == 0 ? mid.x : x % 4 == 1 ? mid.y : x % 4 == 2 ? mid.z : mid.w);
+                        }
+                        const float2 both = parts_of(total);
+                        chunk_sum = both.x + both.y;
+                        chunk_mid = mid0 + mid1;
+                    };
+                    // Every row sees all, with the same exponent as its own: a fused multiply-add and nothing else stand
+                    // between a score and its weight.
+                    const bool fast = plain && __all_sync(0xffffffffu, e_row == (int)ks.one_exponent && fabsf(ref) < kNear);
+                    float a[32], z[32];
+                    uint32_t y[16], u[16];
+                    tmem_ld(at_s, a);
+                    if (fast) {              // 64 keys at a time
+#pragma unroll 1
+                        for (int c = 0; c < 4; c += 2) {
+                            float sum0, mid0, sum1, mid1;
+                            tmem_ld(at_s + (c + 1) * 32, z);
+                            tmem_wait_ld(a);
+                            tmem_wait_ld(z);
+                            weigh(c, a, y, sum0, mid0, Yes());
+                            weigh(c + 1, z, u, sum1, mid1, Yes());
+                            const float over = fmaxf(sum0, sum1);
+                            if (__any_sync(0xffffffffu, over > kMost)) {     // (P of these is not written yet, and S is there)
                                 float best = kNegInf;
+#pragma unroll 1
+                                for (int k = c; k < c + 2; ++k) {
+                                    uint64_t s[16];
+                                    tmem_ld(at_s + k * 32, a);
+                                    tmem_wait_ld(a);
+                                    scores(k, a, s);
+#pragma unroll
+                                    for (int x = 0; x < 16; ++x) {
+                                        const float2 f = parts_of(s[x]);
+                                        best = max3(best, f.x, f.y);
+                                    }
+                                }
+                                move(over > kMost ? fmaxf(top, best) : top, e_row, c);
+                                tmem_ld(at_s + c * 32, a);
+                                tmem_wait_ld(a);
+                                weigh(c, a, y, sum0, mid0, No());
+                                tmem_ld(at_s + c * 32 + 32, a);
+                                tmem_wait_ld(a);
+                                weigh(c + 1, a, u, sum1, mid1, No());
+                            }
+                            if (c == 0) tmem_ld(at_s + 64, a);
+                            sum += sum0 + sum1;
+                            msum += mid0 + mid1;
+                            tmem_store16(at_s + c * 16, y);
+                            tmem_store16(at_s + c * 16 + 16, u);
+                        }
+                    } else {
+                        // (the reference holds for all: what the row sees was looked through; or there are other exponents, or scores
+                        // too large for the short way, and it is looked through here)
+                        if (plain) {
+                            float best = kNegInf;
+                            bool none = false;
+#pragma unroll 1
+                            for (int c = 0; c < 4; ++c) {
+                                uint64_t s[16];
+                                if (c > 0) tmem_ld(at_s + c * 32, a);
+                                tmem_wait_ld(a);
+                                scores(c, a, s);
 #pragma unroll
                                 for (int x = 0; x < 16; ++x) {
                                     const float2 f = parts_of(s[x]);
+                                    none = none || f.x != f.x || f.y != f.y;
                                     best = max3(best, f.x, f.y);
                                 }
-                                move(chunk_sum > kMost ? fmaxf(top, best) : top, e_row, c);
-                                weigh();
                             }
-                        sum += chunk_sum;
-                        msum += chunk_mid;
-                        tmem_store16(at_s + c * 16, out);
-                    };
-                    float a[32], z[32];
-                    tmem_ld(at_s, a);
-                    tmem_wait_ld(a);
-                    if (plain) {             // a chunk's products are loaded while another's are weighed
-#pragma unroll 1
-                        for (int c = 0; c < 4; c += 2) {
-                            tmem_ld(at_s + (c + 1) * 32, z);
-                            chunk(c, a, Yes());
-                            tmem_wait_ld(z);
-                            if (c == 0) tmem_ld(at_s + 64, a);
-                            chunk(c + 1, z, Yes());
-                            if (c == 0) tmem_wait_ld(a);
+                            const bool up = (best - top) * fr > (float)kSlack;
+                            if (__any_sync(0xffffffffu, up)) move(up ? best : top, e_row, 0);
+                            tmem_ld(at_s, a);
                         }
-                    } else {
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
-                            chunk(c, a, No());
-                            if (c < 3) {
-                                tmem_ld(at_s + (c + 1) * 32, a);
-                                tmem_wait_ld(a);
-                            }
+                            float sum0, mid0;
+                            tmem_wait_ld(a);
+                            weigh(c, a, y, sum0, mid0, No());
+                            if (c < 3) tmem_ld(at_s + (c + 1) * 32, a);
+                            sum += sum0;
+                            msum += mid0;
+                            tmem_store16(at_s + c * 16, y);
                         }
                     }
                     l += sum;
@@ -511,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
             const float to_out = ex2((float)(e_row - e_out));
             l *= ex2((float)(127 - e_out));
             ml *= to_out;
-            float m = seen_any ? fmaf(top, fr, (float)(e_out - kHeadroom - 127)) : kNegInf;
+            float m = seen_any ? ref + (float)(e_out - kHeadroom - 127) : kNegInf;
             float scale_o = steps > 0 && seen_any ? 0x1p-11f * to_out : 0.0f;
             float total_m = m, total_l = l;
             float* meet_m = reinterpret_cast<float*>(smem + Z::kAtMeet);
@@ -639,6 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
             for (int i = 0; i < D / 32; ++i) kq[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int i = 0; i < 4; ++i) vq[i] = make_uint4(0, 0, 0, 0);
+            int e_part = 1;                  // the largest exponent of a key that all rows see
             load();
             if (n > 1) {
                 k_next = group_at(1, t >> 4);
@@ -663,7 +713,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                     uint8_t* have = reinterpret_cast<uint8_t*>(ks.exponent);         // (for a moment)
                     have[warp & 3] = (uint8_t)((got & 1u) | (got >> 16 & 1u) << 1);
                 }
-                int most = e;
+                // (what every row sees has one exponent, the largest so far)
+                const bool all_see = !tiles.edge(j) && tiles.first_key(j) + t < tiles.base;
+                int most = all_see && here ? e : 1;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
                 if (lane == 0) reinterpret_cast<int*>(ks.mid)[warp & 3] = most;      // (likewise)
@@ -672,9 +724,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                 const int4 all = *reinterpret_cast<const int4*>(ks.mid);
                 part_barrier<2, kConvertThreads>();
                 const uint32_t have = (four & 3u) | (four >> 6 & 12u) | (four >> 12 & 48u) | (four >> 18 & 192u);
-                const int one = max(max(all.x, all.y), max(all.z, all.w));
-                const bool plain = tiles.plain(j) && have == 0xFFu;
-                if (plain) e = one;
+                e_part = max(e_part, max(max(all.x, all.y), max(all.z, all.w)));
+                if (all_see) e = e_part;
                 ks.k[t] = kpair;
                 const float sv = bad ? 0.0f : bf16_lo(vpair), lv = bad ? 0.0f : bf16_hi(vpair);
                 const float down = __uint_as_float((uint32_t)(254 - e) << 23);
@@ -684,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                 ks.v[t] = (uint16_t)pack_f16x2(sv * down * 2048.0f, 0.0f);
                 if (t == 0) {
                     ks.have = have;
-                    ks.one_exponent = (float)one;
+                    ks.one_exponent = (float)e_part;
                 }
                 // ---- keys: a word's four masks are 16 bytes of the row ----
                 uint8_t* dst = K + t * 128;
