@@ -379,16 +379,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                         tmem_stored();
                     };
                     if (!plain || __any_sync(0xffffffffu, !seen_any)) {       // the largest score and exponent of what the row sees
-                        float best = kNegInf;
-                        int e = plain ? (int)ks.one_exponent : 0;
+                        float best = kNegInf, most = plain ? ks.one_exponent : 0.0f;
                         bool none = false;                   // a score that is not a number
+                        float a[32];
+                        tmem_ld(at_s, a);
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
-                            float a[32];
                             uint64_t s[16];
-                            tmem_ld(at_s + c * 32, a);
                             tmem_wait_ld(a);
                             scores(c, a, s);
+                            if (c < 3) tmem_ld(at_s + (c + 1) * 32, a);
                             const uint32_t m = c == 0 ? seen[0] : c == 1 ? seen[1] : c == 2 ? seen[2] : seen[3];
 #pragma unroll
                             for (int x = 0; x < 32; x += 2) {
@@ -398,16 +398,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                                 none = none || f.x != f.x || f.y != f.y;
                                 best = max3(best, f.x, f.y);
                             }
-                            if (!plain) {                    // (keys before the tree share theirs, but at a window's edge)
-                                uint32_t x = m;
-                                if (!tiles.edge(j)) {
-                                    const uint32_t tree = ~bits_between(0, tiles.base - tiles.first_key(j) - 32 * c);
-                                    if (m & ~tree) e = max(e, (int)ks.one_exponent);
-                                    x &= tree;
+                            if (!plain)
+#pragma unroll
+                                for (int x = 0; x < 32; x += 4) {
+                                    const float4 ex = *reinterpret_cast<const float4*>(&ks.exponent[c * 32 + x]);
+                                    most = max3(most, m >> x & 1 ? ex.x : 0.0f, m >> x & 2 ? ex.y : 0.0f);
+                                    most = max3(most, m >> x & 4 ? ex.z : 0.0f, m >> x & 8 ? ex.w : 0.0f);
                                 }
-                                for (; x; x &= x - 1) e = max(e, (int)ks.exponent[c * 32 + __ffs((int)x) - 1]);
-                            }
                         }
+                        const int e = (int)most;
                         // (a score that is not a number makes the row's sums that, whatever the reference)
                         const bool any = best > kNegInf || none;
                         const bool up = any && (!seen_any || (best - top) * fr > (float)kSlack);
