@@ -164,7 +164,9 @@ size_t decode_workspace(int op, int64_t M, int64_t N, int64_t K, int* rc) {
             *rc = R9Q_ERR_DIM;
             return 0;
         }
-        return kCounterHeader + kv4_tree_items_bytes(M, K) + kv4_tree_part_floats((int)N, M, sms_or_default()) * 4;
+        const int sms = sms_or_default();    // (either kernel may take it)
+        return kCounterHeader + std::max(kv4_tree_items_bytes(M, K) + kv4_tree_part_floats((int)N, M, sms) * 4,
+                                         kv4_attention_part_floats((int)N, M, sms) * 4);
     }
     return kCounterHeader + kv4_attention_part_floats((int)N, M, sms_or_default()) * 4;
 }
@@ -409,7 +411,7 @@ static int attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, co
     p.room = (int)(max_pages * page);
     p.reach = p.window > 0 ? (int)(p.window > INT_MAX - Lq ? INT_MAX : p.window + Lq - 1) : INT_MAX;
     p.scale_log2 = scale * 1.4426950408889634f;
-    if (parents && rows > kTreeFewRows) {
+    if (parents && kv4_tree_wide(p)) {
         uint8_t* items = static_cast<uint8_t*>(workspace) + kCounterHeader;
         p.part = reinterpret_cast<float*>(items + kv4_tree_items_bytes(rows, B * Hk));
         return status(launch_kv4_tree_attention((int)D, p, items, sms, static_cast<cudaStream_t>(stream)));

@@ -212,8 +212,10 @@ size_t kv4_attention_part_floats(int D, int64_t rows, int sms);
 // K = B * Hk).
 size_t decode_workspace(int op, int64_t M, int64_t N, int64_t K, int* rc);
 cudaError_t launch_kv4_attention(int D, const Kv4AttnParams& p, int sms, cudaStream_t st);
-// Trees with more rows of a key-value head than these: on tcgen05.  `items`: kv4_tree_items_bytes, of B * Hk heads.
-constexpr int kTreeFewRows = 32;
+// Trees of many rows: on tcgen05 (r9q_kv4_tree_attention.cu), where kv4_tree_wide says so.  `items`: kv4_tree_items_bytes, of
+// B * Hk heads.
+constexpr int kTreeFewRows = 64;             // never up to these
+bool kv4_tree_wide(const Kv4AttnParams& p);
 size_t kv4_tree_items_bytes(int64_t rows, int64_t heads);
 size_t kv4_tree_part_floats(int D, int64_t rows, int sms);
 cudaError_t launch_kv4_tree_attention(int D, const Kv4AttnParams& p, void* items, int sms, cudaStream_t st);

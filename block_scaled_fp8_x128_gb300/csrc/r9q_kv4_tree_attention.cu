@@ -876,6 +876,17 @@ cudaError_t launch(Kv4AttnParams p, int2* items, int sms, cudaStream_t st) {
 
 }  // namespace
 
+// This kernel takes about 25 us for a part's beginning and end (the other about 9), and a quarter to a half of the other's
+// time for a row and key.  So: rows that fill at least half of a tile, and work, in 16 rows of 16 keys, worth the difference
+// (us, the other / this; rows, sequences x heads, tokens; D = 128 but where said): 64 x 128 of 8200 149/158; 80 x 128 of
+// 8200 180/162; 96 x 32 of 4100 45/40, x 128 124/99; 128 x 8 of 8200 34/37, x 64 of 2100 55/42, of 8200 147/96; 147 x 4 of 5000
+// (D = 64) 17/30, x 32 54/52; 256 x 8 of 4100 34/33, of 65600 301/122, x 128 of 8200 533/237; 512 x 128 of 350 120/64.  By
+// what the pages can hold, as the other's rules.
+bool kv4_tree_wide(const Kv4AttnParams& p) {
+    const int64_t rows = (int64_t)p.Lq * p.G, groups = std::min(p.room, p.reach) / 16 + 1;
+    return rows > kTreeFewRows && (int64_t)p.B * p.c.heads * groups * ((rows + 15) / 16) > 36000;
+}
+
 // Bytes: the items' CTAs, then the partials of two slots a CTA.
 size_t kv4_tree_items_bytes(int64_t rows, int64_t heads) {
     return (size_t)(heads * ((rows + kTile - 1) / kTile)) * sizeof(int2) / 256 * 256 + 256;

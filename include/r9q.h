@@ -361,8 +361,8 @@ int r9q_kv4_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, c
  * Node i sees the tokens before the tree, its ancestors and itself.  Its position is n - Lq + d
  * with d its ancestors' number, and a window counts positions: the last `window` of that path.
  * Another parent, or one that leads to no node, sets the device error word to R9Q_ERR_ARG, and the
- * node's o and lse are NaN; the parents of a sequence of length 0 are not looked at.  More than 32 rows
- * Lq * Hq / Hk of a key-value head go to the tensor cores in tiles of 128.  workspace:
+ * node's o and lse are NaN; the parents of a sequence of length 0 are not looked at.  Many rows
+ * Lq * Hq / Hk of a key-value head (over 64, where there is enough to do) go in tiles of 128 to tensor memory.  workspace:
  * r9q_workspace_bytes(R9Q_OP_KV4_TREE_ATTENTION, Lq * Hq / Hk, D, B * Hk, ...), zeroed and left as
  * r9q_kv4_attention's. */
 int r9q_kv4_tree_attention(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, const uint8_t* kc, const void* kp,

@@ -22,6 +22,13 @@ def way_to(parents, i):
     return way[::-1]
 
 
+def widened(table, page, heads, rows):
+    """The table with room for sequences so long that, with more than 64 rows, the call takes the kernel for many (which
+    one does, is decided by what the pages can hold)."""
+    tokens = 16 * (36000 // (len(table) * heads * -(-rows // 16)) + 2)
+    return np.concatenate((table, np.full((len(table), max(0, -(-tokens // page) - table.shape[1])), -1, np.int32)), 1)
+
+
 def check(r9q, cache, table, lens, parents, q, o, lse, window=0, scale=None):  # noqa: F811
     """Each node as the one newest token of the keys that it sees."""
     page, D = cache.k.shape[2], 2 * cache.k.shape[3]
@@ -68,9 +75,14 @@ TREES = [([1], 1, 1, 1, 128, 16, 0), ([9, 0, 24, 70], 8, 8, 2, 128, 16, 0), ([77
 @pytest.mark.gpu
 @pytest.mark.parametrize("lens,n,Hq,Hk,D,page,window", TREES)
 @pytest.mark.parametrize("kind", ["random", "chain", "star"])
-def test_trees(r9q, lens, n, Hq, Hk, D, page, window, kind):  # noqa: F811
+@pytest.mark.parametrize("wide", [False, True])
+def test_trees(r9q, lens, n, Hq, Hk, D, page, window, kind, wide):  # noqa: F811
     B = len(lens)
     cache, table, _ = make_cache(r9q, lens, Hk, D, page, 601)
+    if wide:
+        if n * Hq // Hk <= 64 or window and window < 50:      # (never many; a short window never makes enough to do)
+            return
+        table = widened(table, page, Hk, n * Hq // Hk)
     parents = {"random": random_parents(B, n, 602), "chain": np.tile(np.arange(n) - 1, (B, 1)),
                "star": np.full((B, n), -1)}[kind].astype(np.int32)
     if n > 6:
@@ -89,7 +101,8 @@ def test_trees(r9q, lens, n, Hq, Hk, D, page, window, kind):  # noqa: F811
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("B,length,n,Hq,Hk,D", [(70, 90, 5, 8, 2, 128), (300, 40, 16, 4, 1, 64), (40, 300, 33, 8, 2, 128)])
+@pytest.mark.parametrize("B,length,n,Hq,Hk,D", [(70, 90, 5, 8, 2, 128), (300, 40, 16, 4, 1, 64), (40, 300, 33, 8, 2, 128),
+                                                (320, 200, 17, 8, 1, 64), (90, 700, 20, 32, 4, 128), (170, 500, 64, 2, 1, 128)])
 def test_many_trees(r9q, B, length, n, Hq, Hk, D):  # noqa: F811
     """More of them than CTAs of the kernel at a time."""
     lens = [1 + (i * 37) % length for i in range(B)]
@@ -105,10 +118,12 @@ def test_many_trees(r9q, B, length, n, Hq, Hk, D):  # noqa: F811
 @pytest.mark.gpu
 @pytest.mark.parametrize("q_scale,v_scale,scale", [(1e-30, 1e-25, None), (1e4, 1e20, 1e-5), (30.0, 1e-3, None),
                                                    (1e3, 1.0, 1.0), (0.0, 1.0, None)])
-@pytest.mark.parametrize("n,Hq,D", [(9, 2, 128), (40, 8, 128), (40, 8, 64)])
-def test_magnitudes(r9q, q_scale, v_scale, scale, n, Hq, D):  # noqa: F811
+@pytest.mark.parametrize("n,Hq,D,wide", [(9, 2, 128, False), (40, 8, 128, False), (40, 8, 128, True), (40, 8, 64, True),
+                                          (12, 8, 128, True)])
+def test_magnitudes(r9q, q_scale, v_scale, scale, n, Hq, D, wide):  # noqa: F811
     lens = [150, 700]
     cache, table, _ = make_cache(r9q, lens, 1, D, 32, 621, v_scale=v_scale)
+    table = widened(table, 32, 1, n * Hq) if wide else table
     parents = random_parents(2, n, 622)
     q = rand((2, n, Hq, D), 623, q_scale).to(dev())
     o, lse = r9q.r9q_kv4_tree_attention(q, cache, on(table), on(np.array(lens, np.int32)), on(parents), scale=scale,
@@ -117,12 +132,14 @@ def test_magnitudes(r9q, q_scale, v_scale, scale, n, Hq, D):  # noqa: F811
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("n,Hq,D", [(10, 2, 128), (40, 8, 128), (33, 16, 64)])
-def test_what_a_node_does_not_see(r9q, n, Hq, D):  # noqa: F811
+@pytest.mark.parametrize("n,Hq,D,wide", [(10, 2, 128, False), (40, 8, 128, False), (40, 8, 128, True), (33, 16, 64, True),
+                                          (10, 8, 128, True)])
+def test_what_a_node_does_not_see(r9q, n, Hq, D, wide):  # noqa: F811
     """A node's key and value of huge numbers, infinities or NaN reach that node and what comes from it alone: the others'
     results stay, bit for bit."""
     length, Hk = 200, 2
     cache, table, slots = make_cache(r9q, [length], Hk, D, 16, 631)
+    table = widened(table, 16, Hk, n * Hq) if wide else table
     parents = random_parents(1, n, 632)
     parents[0, 4] = 1
     q = rand((1, n, Hq * Hk, D), 633).to(dev())
@@ -144,11 +161,12 @@ def test_what_a_node_does_not_see(r9q, n, Hq, D):  # noqa: F811
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("n,Hq", [(9, 2), (40, 8)])
-def test_bad_parents_and_tables(r9q, n, Hq):  # noqa: F811
+@pytest.mark.parametrize("n,Hq,wide", [(9, 2, False), (40, 8, False), (40, 8, True), (10, 8, True)])
+def test_bad_parents_and_tables(r9q, n, Hq, wide):  # noqa: F811
     """Parents that are none, and those of an unused place of the batch; a page and a length out of range."""
     lens = [100, 60, 0]
     cache, table, _ = make_cache(r9q, lens, 1, 128, 16, 641)
+    table = widened(table, 16, 1, n * Hq) if wide else table
     q = rand((3, n, Hq, 128), 642).to(dev())
     parents = random_parents(3, n, 643)
     parents[2] = 1 << 20                                      # not looked at
@@ -177,11 +195,12 @@ def test_bad_parents_and_tables(r9q, n, Hq):  # noqa: F811
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("n,Hq", [(9, 2), (40, 8)])
-def test_layouts_a_stream_and_graphs(r9q, n, Hq):  # noqa: F811
+@pytest.mark.parametrize("n,Hq,wide", [(9, 2, False), (40, 8, False), (40, 8, True), (12, 8, True)])
+def test_layouts_a_stream_and_graphs(r9q, n, Hq, wide):  # noqa: F811
     """Strided queries, another stream with a workspace of one's own, and two graphs replayed on two streams."""
     lens = [3000, 999, 450]
     cache, table, _ = make_cache(r9q, lens, 2, 128, 32, 651)
+    table = widened(table, 32, 2, n * Hq) if wide else table
     buf = rand((3, n, 2 * Hq + 3, 128), 652).to(dev())
     q = buf[:, :, :2 * Hq]
     rest = (cache, on(table), on(np.array(lens, np.int32)), on(random_parents(3, n, 653)))
