@@ -4,32 +4,31 @@
 // The state is what costs: 4 D D bytes a head in and, where it changes, out.  So a
 // sequence's head is cut by rows (values), which do not meet: a warp holds 16 rows of S
 // in registers, row r + 4i in the lanes 8r .. 8r + 7, each with D/8 of its elements.  Groups
-// of up to eight tokens pass over it: all S k and S q first (the eight partial sums of four
+// of up to 16 tokens pass over it: S k and S q of eight at a time (the eight partial sums of four
 // rows and two products meet in seven shuffles, which leaves one result a lane), then the
-// sums over earlier tokens, then the update with all of the group's u at once.  What does
+// sums over earlier tokens, at last the update with all of the group's u at once.  What does
 // not depend on the row, the products of keys and queries among themselves and the decays,
-// is formed once for the CTA.  In a tree S stays as it is, and the group's sums go over the
-// ancestors of all groups.
+// is formed once for the CTA, a warp following a token's ancestors and adding up their decays as
+// it goes.  In a tree S stays as it is.
 #include "r9q_delta.cuh"
 
 namespace r9q {
 
 namespace {
 
-constexpr int kGroup = 8;                    // tokens at a time
-constexpr int kWarps = 4, kRows = 16;        // of a CTA, of a warp
-constexpr int kThreads = 32 * kWarps;
+constexpr int kGroup = 16, kAtOnce = 8;      // tokens between updates of S, and that are multiplied with it at a time
+constexpr int kRows = 16;                    // of a warp
+constexpr int warps_of(int D) { return D / kRows; }          // of a CTA, which has a head
 
-template <int D, DeltaMode MODE>
+template <int D>
 struct Shared {
-    static constexpr int kKept = MODE == kDeltaTree ? kMostNodes : kGroup;      // tokens whose keys and u are kept
-    float kn[kKept][D], qn[kGroup][D];       // of unit length
-    float solve[kGroup][kKept], weigh[kGroup][kKept];        // beta A (k.k), scale A (q.k)
-    float g[kKept], beta[kGroup], fade[kGroup], left[kGroup];        // fade A(i, 0), left A(n, i)
-    float u[kWarps][kKept][kRows];
-    uint64_t above[kMostNodes];              // a node's ancestors, itself among them
-    int parents[kMostNodes];
-    NodeKind kind[kMostNodes];
+    float kn[kGroup][D], qn[kGroup][D];      // of unit length
+    float solve[kGroup][kGroup], weigh[kGroup][kGroup];      // beta A (k.k), scale A (q.k), of ancestors
+    float g[kGroup], beta[kGroup], fade[kGroup], left[kGroup];       // fade A(i, 0), left A(n, i)
+    float u[warps_of(D)][kGroup][kRows];
+    int parents[kGroup];
+    uint64_t above[kGroup];                  // a node's ancestors, itself among them
+    NodeKind kind[kGroup];
 };
 
 // 32/8 lanes of a quarter warp hold `N` partial sums each (N 8 or 4); lane c of 8 gets the sum of the c-th (c/2-th).
@@ -75,16 +74,14 @@ __device__ __forceinline__ void unit_vector(const uint16_t* src, float* dst, flo
 }
 
 template <int D, DeltaMode MODE>
-__global__ void __launch_bounds__(kThreads, MODE == kDeltaTree ? 1 : 4) delta_rows_kernel(const DeltaParams p) {
-    constexpr int PARTS = D / (kWarps * kRows), M = D / 32;  // CTAs of a head; 16-byte pieces of a row that a lane has
+__global__ void __launch_bounds__(32 * warps_of(D), D == 64 ? 4 : 2) delta_rows_kernel(const DeltaParams p) {
+    constexpr int W = warps_of(D), M = D / 32;               // warps; 16-byte pieces of a row that a lane has
     constexpr bool TREE = MODE == kDeltaTree, HAS_Q = MODE != kDeltaCommit;
-    constexpr int KEPT = Shared<D, MODE>::kKept;
-    extern __shared__ __align__(16) uint8_t smem[];
-    Shared<D, MODE>& sh = *reinterpret_cast<Shared<D, MODE>*>(smem);
+    __shared__ Shared<D> sh;
     begin_chained();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 7, r = lane >> 3;
-    const int part = blockIdx.x % PARTS, bh = blockIdx.x / PARTS, b = bh / p.Hv, h = bh - b * p.Hv, hk = h / p.ratio;
-    const int row0 = (part * kWarps + warp) * kRows;
+    const int b = blockIdx.x / p.Hv, h = blockIdx.x - b * p.Hv, hk = h / p.ratio;
+    const int row0 = warp * kRows;
     int n;
     int64_t row;
     delta_tokens(p, b, n, row);
@@ -113,152 +110,160 @@ __global__ void __launch_bounds__(kThreads, MODE == kDeltaTree ? 1 : 4) delta_ro
             s[i][2 * m] = x.x;
             s[i][2 * m + 1] = x.y;
         }
-    const int slot = delta_slot<!TREE>(p, b);
-    if (slot < 0) {                          // no state: outputs of zero, or NaN where it should have been one
-        if constexpr (HAS_Q)
-            for (int x = tid; x < n * (kWarps * kRows); x += kThreads)
-                p.o[((row + x / (kWarps * kRows)) * p.Hv + h) * D + part * kWarps * kRows + x % (kWarps * kRows)] =
-                    slot == -1 ? 0 : 0x7FC0;
-        return;
-    }
-    if constexpr (TREE) {
-        if (tid < n) {
-            sh.parents[tid] = p.parents[(int64_t)b * p.Lq + tid];
-            sh.g[tid] = p.g[(row + tid) * p.Hv + h];
-        }
-        __syncthreads();
-        if (tid < n) {
-            int depth;
-            const NodeKind kind = find_node(sh.parents, tid, kMostNodes, sh.above[tid], depth);
-            if (kind == kBadNode) record_error(p.err, kErrArg);
-            if (kind != kNode) sh.above[tid] = 0;
-            sh.kind[tid] = kind;
-        }
-    }
     const bool second = HAS_Q && (c & 1);    // the lane gets S q of its row; else S k
     const int own = row0 + r + 4 * (c >> 1); // that row
+    const int64_t at0 = p.cu ? row : 0;      // the first token in q, k and v
+    int slot = -1;
 
 #pragma unroll 1
-    for (int base = 0; base < n; base += kGroup) {
-        const int cnt = min(kGroup, n - base), kept = TREE ? base : 0;       // where the group's tokens are kept
+    for (int base = 0; base < max(n, 1); base += kGroup) {
+        const int cnt = min(kGroup, n - base);
         auto token = [&](int t) { return MODE == kDeltaCommit ? path[base + t] : base + t; };
-        float v[kGroup];
-#pragma unroll
-        for (int t = 0; t < kGroup; ++t)
-            v[t] = t < cnt ? bf16_lo(p.v[b * p.v_bs + (p.cu ? row : 0) * p.v_ts + token(t) * p.v_ts + h * p.v_hs + own]) : 0.0f;
-        __syncthreads();                     // what the last group left is used
-        for (int t = warp; t < cnt; t += kWarps) {
-            const int64_t at = (p.cu ? row : 0) + token(t);
-            unit_vector<D>(p.k + b * p.k_bs + at * p.k_ts + hk * p.k_hs, sh.kn[kept + t], p.eps, lane);
+        if (base > 0) __syncthreads();       // what the last group left is used
+        for (int t = warp; t < cnt; t += W) {
+            const int64_t at = at0 + token(t);
+            unit_vector<D>(p.k + b * p.k_bs + at * p.k_ts + hk * p.k_hs, sh.kn[t], p.eps, lane);
             if constexpr (HAS_Q) unit_vector<D>(p.q + b * p.q_bs + at * p.q_ts + hk * p.q_hs, sh.qn[t], p.eps, lane);
         }
         if (tid < cnt) {
             const int64_t at = (row + token(tid)) * p.Hv + h;
-            if constexpr (!TREE) sh.g[tid] = p.g[at];
+            sh.g[tid] = p.g[at];
             sh.beta[tid] = p.beta[at];
+            if constexpr (TREE) sh.parents[tid] = p.parents[(int64_t)b * p.Lq + tid];
+        }
+        if (base == 0) {
+            slot = delta_slot<!TREE>(p, b);
+            if (slot < 0) {                  // no state: outputs of zero, or NaN where it should have been one
+                if constexpr (HAS_Q)
+                    for (int64_t x = tid; x < (int64_t)n * D; x += 32 * W)
+                        p.o[((row + x / D) * p.Hv + h) * D + x % D] = slot == -1 ? 0 : 0x7FC0;
+                return;
+            }
         }
         __syncthreads();
-        // products among the tokens, a warp for each pair (i, j <= i)
-        const int span = kept + cnt;
-#pragma unroll 1
-        for (int x = warp; x < cnt * span; x += kWarps) {
-            const int i = x / span, j = x - i * span, me = kept + i;
-            if (j > me || (TREE && !(sh.above[me] >> j & 1))) {
-                if (lane == 0) sh.solve[i][j] = sh.weigh[i][j] = 0.0f;
-                continue;
-            }
-            float kk = 0.0f, qk = 0.0f;
-#pragma unroll
-            for (int e = lane; e < D; e += 32) {
-                kk = fmaf(sh.kn[me][e], sh.kn[j][e], kk);
-                if constexpr (HAS_Q) qk = fmaf(sh.qn[i][e], sh.kn[j][e], qk);
-            }
-            kk = group_sum<32>(kk);
-            if constexpr (HAS_Q) qk = group_sum<32>(qk);
-            float sum = 0.0f;                // of the decays after j, up to me
-            for (int t = me; t != j; t = TREE ? sh.parents[t] : t - 1) sum += sh.g[t];
-            const float a = expf(sum);
-            if (lane == 0) {
-                sh.solve[i][j] = j == me ? 0.0f : sh.beta[i] * a * kk;
-                sh.weigh[i][j] = p.scale * a * qk;
-            }
-        }
-        if (tid < cnt) {
-            float before = 0.0f, after = 0.0f;
+        // products among the tokens, a warp for each: along its ancestors, or the tokens before it
+        for (int i = warp; i < cnt; i += W) {
+            NodeKind kind = kNode;
+            uint64_t above = 0;
             if constexpr (TREE) {
-                if (sh.kind[base + tid] == kNode)
-                    for (int t = base + tid; t >= 0; t = sh.parents[t]) before += sh.g[t];
-            } else {
-                for (int t = 0; t <= tid; ++t) before += sh.g[t];
-                for (int t = tid + 1; t < cnt; ++t) after += sh.g[t];
+                int depth;
+                kind = find_node(sh.parents, i, kMostNodes, above, depth);
+                if (kind == kBadNode && lane == 0) record_error(p.err, kErrArg);
+                if (kind != kNode) above = 0;
+                if (lane == 0) {
+                    sh.kind[i] = kind;
+                    sh.above[i] = above;
+                }
             }
-            sh.fade[tid] = expf(before);
-            sh.left[tid] = expf(after);
+            float k[D / 32], q[D / 32];
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) {
+                k[e] = sh.kn[i][e * 32 + lane];
+                q[e] = HAS_Q ? sh.qn[i][e * 32 + lane] : 0.0f;
+            }
+            const float beta = sh.beta[i];
+            float sum = 0.0f;                // of the decays after j, up to i
+            if (kind == kNode)
+                for (int j = i; j >= 0; j = TREE ? sh.parents[j] : j - 1) {
+                    float kk = 0.0f, qk = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) {
+                        const float x = sh.kn[j][e * 32 + lane];
+                        kk = fmaf(k[e], x, kk);
+                        qk = fmaf(q[e], x, qk);
+                    }
+                    // both sums at once: half the lanes go on with one each
+                    const float give = lane & 16 ? kk : qk, keep = lane & 16 ? qk : kk;
+                    float v = keep + __shfl_xor_sync(0xffffffffu, give, 16);
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                    const float a = expf(sum);
+                    if (lane == 0) sh.solve[i][j] = j == i ? 0.0f : beta * a * v;
+                    if (lane == 16) sh.weigh[i][j] = p.scale * a * v;
+                    sum += sh.g[j];
+                }
+            if (lane == 0) sh.fade[i] = expf(sum);
+            if constexpr (!TREE) {
+                float after = 0.0f;
+                for (int j = i + 1; j < cnt; ++j) after += sh.g[j];
+                if (lane == 0) sh.left[i] = expf(after);
+            }
         }
         __syncthreads();
 
-        float val[kGroup], u[kGroup];        // S k or S q, then the sums
+#pragma unroll 1
+        for (int t0 = 0; t0 < cnt; t0 += kAtOnce) {
+            float v[kAtOnce], val[kAtOnce], u[kAtOnce];      // S k or S q, then the sums
 #pragma unroll
-        for (int t = 0; t < kGroup; ++t) {
-            if (t >= cnt) break;
-            float x[HAS_Q ? 8 : 4];
+            for (int t = 0; t < kAtOnce; ++t)
+                v[t] = t0 + t < cnt ? bf16_lo(p.v[b * p.v_bs + (at0 + token(t0 + t)) * p.v_ts + h * p.v_hs + own]) : 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint64_t wk = 0, wq = 0;     // (two zeros)
+            for (int t = 0; t < kAtOnce; ++t) {
+                if (t0 + t >= cnt) break;
+                float x[HAS_Q ? 8 : 4];
 #pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&sh.kn[kept + t][m * 32 + c * 4]);
-                    wk = fma2(s[i][2 * m], k.x, wk);
-                    wk = fma2(s[i][2 * m + 1], k.y, wk);
-                    if constexpr (HAS_Q) {
-                        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&sh.qn[t][m * 32 + c * 4]);
-                        wq = fma2(s[i][2 * m], q.x, wq);
-                        wq = fma2(s[i][2 * m + 1], q.y, wq);
+                for (int i = 0; i < 4; ++i) {
+                    uint64_t wk = 0, wq = 0; // (two zeros)
+#pragma unroll
+                    for (int m = 0; m < M; ++m) {
+                        const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&sh.kn[t0 + t][m * 32 + c * 4]);
+                        wk = fma2(s[i][2 * m], k.x, wk);
+                        wk = fma2(s[i][2 * m + 1], k.y, wk);
+                        if constexpr (HAS_Q) {
+                            const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&sh.qn[t0 + t][m * 32 + c * 4]);
+                            wq = fma2(s[i][2 * m], q.x, wq);
+                            wq = fma2(s[i][2 * m + 1], q.y, wq);
+                        }
                     }
+                    const float2 a = parts_of(wk), d = parts_of(wq);
+                    x[HAS_Q ? 2 * i : i] = a.x + a.y;
+                    if constexpr (HAS_Q) x[2 * i + 1] = d.x + d.y;
                 }
-                const float2 a = parts_of(wk), d = parts_of(wq);
-                x[HAS_Q ? 2 * i : i] = a.x + a.y;
-                if constexpr (HAS_Q) x[2 * i + 1] = d.x + d.y;
+                val[t] = meet8(x, c);
             }
-            val[t] = meet8(x, c);
-        }
-        float (*mine)[KEPT] = second ? sh.weigh : sh.solve;
-#pragma unroll
-        for (int t = 0; t < kGroup; ++t) {
-            if (t >= cnt) break;
-            float x = sh.fade[t] * val[t];
-            x = second ? p.scale * x : sh.beta[t] * (v[t] - x);
+            float (*mine)[kGroup] = second ? sh.weigh : sh.solve;
             const float sign = second ? 1.0f : -1.0f;
-            // (a node takes its ancestors alone: the others may hold anything)
-            const uint64_t above = TREE ? sh.above[base + t] : ~0ull;
-            if constexpr (TREE)
-                for (int j = 0; j < base; ++j)
-                    if (above >> j & 1) x = fmaf(sign * mine[t][j], sh.u[warp][j][r * 4 + (c >> 1)], x);
 #pragma unroll
-            for (int j = 0; j < t; ++j)
-                if (!TREE || (above >> (base + j) & 1)) x = fmaf(sign * mine[t][kept + j], u[j], x);
-            u[t] = HAS_Q ? __shfl_sync(0xffffffffu, x, lane & ~1) : x;
-            if (second) {
-                x = fmaf(mine[t][kept + t], u[t], x);
-                uint32_t out = pack_bf16x2(x, 0.0f);
-                if (TREE && sh.kind[base + t] != kNode) out = sh.kind[base + t] == kNoNode ? 0u : 0x7FC0u;
-                p.o[((row + base + t) * p.Hv + h) * D + own] = (uint16_t)out;
+            for (int t = 0; t < kAtOnce; ++t) {
+                const int i = t0 + t;
+                if (i >= cnt) break;
+                float x = sh.fade[i] * val[t];
+                x = second ? p.scale * x : sh.beta[i] * (v[t] - x);
+                // (a node takes its ancestors alone: the others may hold anything)
+                const uint64_t above = TREE ? sh.above[i] : ~0ull;
+                for (int j = 0; j < t0; ++j)
+                    if (!TREE || (above >> j & 1)) x = fmaf(sign * mine[i][j], sh.u[warp][j][r * 4 + (c >> 1)], x);
+#pragma unroll
+                for (int j = 0; j < t; ++j)
+                    if (!TREE || (above >> (t0 + j) & 1)) x = fmaf(sign * mine[i][t0 + j], u[j], x);
+                u[t] = HAS_Q ? __shfl_sync(0xffffffffu, x, lane & ~1) : x;
+                if (second) {
+                    uint32_t out = 0;
+                    const NodeKind kind = TREE ? sh.kind[i] : kNode;
+                    if (kind == kNode)
+                        out = pack_bf16x2(fmaf(mine[i][i], u[t], x), 0.0f);
+                    else if (kind == kBadNode)
+                        out = 0x7FC0u;
+                    p.o[((row + base + i) * p.Hv + h) * D + own] = (uint16_t)out;
+                }
+                if (!(c & 1)) sh.u[warp][i][r * 4 + (c >> 1)] = u[t];
             }
-            if (!(c & 1)) sh.u[warp][kept + t][r * 4 + (c >> 1)] = TREE ? u[t] : sh.left[t] * u[t];
+            __syncwarp();
         }
-        __syncwarp();
         if constexpr (!TREE) {
-            const float a = sh.fade[cnt - 1];
-            const uint64_t all = pair_of(a, a);
+            if (cnt > 0) {
+                const float a = sh.fade[cnt - 1];
+                const uint64_t all = pair_of(a, a);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int m = 0; m < 2 * M; ++m) s[i][m] = mul2(s[i][m], all);
-#pragma unroll
-            for (int t = 0; t < kGroup; ++t) {
-                if (t >= cnt) break;
+                    for (int m = 0; m < 2 * M; ++m) s[i][m] = mul2(s[i][m], all);
+            }
+#pragma unroll 4
+            for (int t = 0; t < cnt; ++t) {
+                const float left = sh.left[t];
                 const float4 w = *reinterpret_cast<const float4*>(&sh.u[warp][t][r * 4]);
-                const float x[4] = {w.x, w.y, w.z, w.w};
+                const float x[4] = {left * w.x, left * w.y, left * w.z, left * w.w};
 #pragma unroll
                 for (int m = 0; m < M; ++m) {
                     const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(&sh.kn[t][m * 32 + c * 4]);
@@ -300,6 +305,7 @@ __device__ __forceinline__ float lane_vector(const uint16_t* src, int c, uint64_
 }
 
 // One token a sequence: every warp for itself, without shared memory.
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
 template <int D>
 __global__ void __launch_bounds__(kThreads, 4) delta_one_kernel(const DeltaParams p) {
     constexpr int PARTS = D / (kWarps * kRows), M = D / 32;
@@ -374,11 +380,7 @@ cudaError_t launch_one(const DeltaParams& p, cudaStream_t st) {
 
 template <int D, DeltaMode MODE>
 cudaError_t launch_rows(const DeltaParams& p, cudaStream_t st) {
-    const size_t smem = sizeof(Shared<D, MODE>);
-    const void* kernel = reinterpret_cast<const void*>(delta_rows_kernel<D, MODE>);
-    cudaError_t e = ensure_dynamic_smem(kernel, smem);
-    if (e != cudaSuccess) return e;
-    return launch_chained(delta_rows_kernel<D, MODE>, (unsigned)p.B * p.Hv * (D / (kWarps * kRows)), kThreads, smem, st, p);
+    return launch_chained(delta_rows_kernel<D, MODE>, (unsigned)p.B * p.Hv, 32 * warps_of(D), 0, st, p);
 }
 
 }  // namespace
