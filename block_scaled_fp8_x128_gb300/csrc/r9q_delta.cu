@@ -386,8 +386,19 @@ cudaError_t launch_rows(const DeltaParams& p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_delta(int D, DeltaMode mode, const DeltaParams& p, cudaStream_t st) {
-    // (packed sequences of a token each are steps)
-    if (mode == kDeltaCommit ? p.P > kGroup : p.cu ? p.T > p.B : p.Lq > kGroup) return launch_delta_chunks(D, mode, p, st);
+    // This file's kernel takes about 1 us a token beyond its loads, for all of a wave of CTAs; the one
+    // in chunks 10 to 16 us for up to 64 tokens, with one CTA an SM.  Measured, us here and in chunks, of the
+    // steps of n tokens: one sequence of 32 heads of 128: n = 12 14.7 and 16.0, 16 18.0 and 16.1; 16 sequences: 16
+    // 47 and 61, 24 66 and 61; 64: 16 184 and 219, 24 255 and 222; heads of 64, 16 sequences of 12: 16
+    // 19.6 and 22.7, 24 27.5 and 22.8.  Trees alike: 12 11.8 and 13.5, 16 14.7 and 13.6 alone, 16 of 16 sequences 37 and 51.
+    const bool waves = (int64_t)p.B * p.Hv > 152;
+    bool few = p.Lq <= (waves ? kGroup : 12);
+    // A path is as long as what was accepted, not as its width: of 64 sequences 32 wide 111 and 215 with a third
+    // of it taken, 262 and 221 with all; 48 wide 148 and 217, 377 and 239.
+    if (mode == kDeltaCommit) few = p.P <= 32;
+    // One of the packed sequences may have all of their tokens.  (Of a token each they are steps.)
+    if (p.cu) few = p.T <= max(p.B, 12);
+    if (!few) return launch_delta_chunks(D, mode, p, st);
     if (mode == kDeltaChain && !p.cu && p.Lq == 1) return D == 64 ? launch_one<64>(p, st) : launch_one<128>(p, st);
     if (mode == kDeltaChain) return D == 64 ? launch_rows<64, kDeltaChain>(p, st) : launch_rows<128, kDeltaChain>(p, st);
     if (mode == kDeltaTree) return D == 64 ? launch_rows<64, kDeltaTree>(p, st) : launch_rows<128, kDeltaTree>(p, st);

@@ -36,7 +36,8 @@ def check_state(got, want, bound):
 # (lens, Hk, Hv, D)
 PROMPTS = [([1], 1, 1, 128), ([0], 1, 2, 128), ([7, 1, 0, 64, 65], 2, 4, 128), ([63, 128, 2], 1, 3, 64),
            ([200], 4, 4, 64), ([129, 30, 5], 1, 2, 128), ([31, 17, 16, 15, 33], 2, 2, 64), ([400, 191], 1, 1, 128),
-           ([8, 9, 10, 11], 3, 6, 128), ([1] * 40, 1, 2, 128)]
+           ([8, 9, 10, 11], 3, 6, 128), ([1] * 40, 1, 2, 128), ([0] * 20 + [36] + [0] * 24, 1, 2, 128),
+           ([7, 0, 5], 2, 4, 64)]
 
 
 @pytest.mark.gpu
@@ -120,7 +121,7 @@ def test_trees(r9q, B, n, Hk, Hv, D, kind):  # noqa: F811
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("n,P,Hk,Hv,D", [(5, 3, 2, 4, 128), (8, 1, 1, 1, 64), (20, 13, 1, 2, 128), (64, 64, 1, 1, 128),
-                                         (64, 40, 1, 2, 64), (3, 5, 1, 1, 64)])
+                                         (64, 40, 1, 2, 64), (3, 5, 1, 1, 64), (40, 32, 2, 4, 128), (50, 31, 1, 2, 64)])
 def test_commits(r9q, n, P, Hk, Hv, D):  # noqa: F811
     """Paths of any nodes in any order, none, ending early, and a padded place of the batch."""
     B = 4
