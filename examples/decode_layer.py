@@ -49,17 +49,28 @@ class Layer:
         self.table = torch.arange(batch * per_seq, dtype=torch.int32, device="cuda").view(batch, per_seq)
         self.lens = torch.zeros(batch, dtype=torch.int32, device="cuda")     # tokens in the cache
 
-    def step(self, x):
-        """x bf16 [batch][n][hidden], the n new tokens of every sequence -> the layer's output for them."""
+    def places(self, at):
+        """The cache's slots of each sequence's tokens `at`, int64 [batch][n]."""
+        return self.table.gather(1, at // self.page) * self.page + at % self.page
+
+    def step(self, x, parents=None, depth=None):
+        """x bf16 [batch][n][hidden], the n new tokens of every sequence -> the layer's output for them.  With `parents`
+        they are nodes of a tree of drafts, `depth` [n] their places in its paths (drafted_decoding.py)."""
         batch, n, hidden = x.shape
         rows = x.reshape(batch * n, hidden)
         pos = (self.lens[:, None] + torch.arange(n, dtype=torch.int32, device="cuda")).long()
-        slots = (self.table.gather(1, pos // self.page) * self.page + pos % self.page).view(-1)
+        slots = self.places(pos).view(-1)
+        if parents is not None:
+            pos = (self.lens[:, None] + depth).long()
         qkv = r9q.r9q_gemm_fp8_block_qa(norm(rows), *self.w_qkv).view(batch * n, -1, self.dim)
         q, k, v = qkv.split((self.heads, self.kv, self.kv), 1)
         q = r9q.r9q_qk_norm_rope_kv4(q, k, v, self.wq, self.wk, self.cos, self.sin, pos.view(-1), self.cache, slots)
         self.lens += n
-        o = r9q.r9q_kv4_attention(q.view(batch, n, self.heads, self.dim), self.cache, self.table, self.lens)
+        q = q.view(batch, n, self.heads, self.dim)
+        if parents is None:
+            o = r9q.r9q_kv4_attention(q, self.cache, self.table, self.lens)
+        else:
+            o = r9q.r9q_kv4_tree_attention(q, self.cache, self.table, self.lens, parents)
         h = rows + r9q.r9q_gemm_fp8_block_qa(o.view(batch * n, -1), *self.w_o)
         y = h + r9q.r9q_gate_up_swiglu_down(norm(h), *self.w_gu, *self.w_dn)
         return y.view(batch, n, hidden)
