@@ -195,3 +195,148 @@ def test_example_runs():
                         "30", "--batch", "3", "--depth", "3"], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
     assert "tokens written" in r.stdout
+
+
+# ------------------------------------------------- streams, devices, sizes --
+
+def calls_of(r9q):  # noqa: F811
+    """Each operator that allocates its outputs, on inputs large enough for their blocks to be seen."""
+    B, n = 64, 40
+    per = 4
+    cache = r9q.r9q_kv4_cache(B * per, HK, PAGE, D)
+    every = torch.arange(B * per * PAGE, device=dev())
+    kv = rand((len(every), 2 * HK, D), 31).to(dev())
+    r9q.r9q_kv4_append(kv[:, :HK], kv[:, HK:], cache, every)
+    q = rand((B, n, HQ, D), 32).to(dev())
+    table = torch.arange(B * per, dtype=torch.int32, device=dev()).view(B, per)
+    lens = torch.full((B,), 60, dtype=torch.int32, device=dev())
+    parents = torch.arange(-1, n - 1, dtype=torch.int32, device=dev()).repeat(B, 1)
+    x = [on(t) if isinstance(t, np.ndarray) else t for t in inputs((B, n), KH, VH, D, 33)]
+    flat = [t.flatten(0, 1) for t in x]
+    state = torch.zeros((B, VH, D, D), device=dev())
+    slots = torch.arange(B, dtype=torch.int32, device=dev())
+    cu = torch.arange(B + 1, dtype=torch.int32, device=dev()) * n
+    return {"attention": lambda **k: r9q.r9q_kv4_tree_attention(q, cache, table, lens, parents, return_lse=True, **k),
+            "prompt": lambda **k: r9q.r9q_gated_delta(*flat, state, slots, cu, from_zero=True, **k),
+            "step": lambda **k: r9q.r9q_gated_delta_step(*x, state, slots, from_zero=True, **k),
+            "tree": lambda **k: r9q.r9q_gated_delta_tree(*x, state, slots, parents, **k)}
+
+
+@pytest.mark.parametrize("name", ["attention", "prompt", "step", "tree"])
+def test_outputs_belong_to_the_stream_of_the_call(r9q, name):  # noqa: F811
+    """The current stream still has work on a block that it has let go; outputs of a call on another stream are not
+    made of that block."""
+    call = calls_of(r9q)[name]
+    st = torch.cuda.Stream()
+    want = call()
+    with torch.cuda.stream(st):
+        call()                                                # (workspaces, and blocks that the stream can have again)
+    torch.cuda.synchronize()
+    want = want if isinstance(want, tuple) else (want,)
+    block = torch.empty(want[0].untyped_storage().nbytes(), dtype=torch.uint8, device=dev())
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    block.fill_(7)
+    del block
+    got = call(stream=st)
+    got = got if isinstance(got, tuple) else (got,)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_calls_run_on_the_device_of_their_tensors(r9q, monkeypatch):  # noqa: F811
+    """With another device current (as the binding sees it), a call makes the tensors' own current; a stream of another
+    device is refused."""
+    calls = calls_of(r9q)
+    wants = {name: f() for name, f in calls.items()}
+    entered, now = [], [1]
+
+    class Device(torch.cuda.device):
+        def __enter__(self):
+            entered.append(self.idx)
+            now.append(self.idx)
+            return super().__enter__()
+
+        def __exit__(self, *error):
+            now.pop()
+            return super().__exit__(*error)
+
+    class Other:
+        device = torch.device("cuda", 1)
+        cuda_stream = 12345
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(r9q, "_current_device", lambda: now[-1])
+    for i, (name, f) in enumerate(calls.items()):
+        got, want = f(), wants[name]
+        assert entered == [0] * (i + 1) and now == [1]
+        assert all(torch.equal(a, b) for a, b in zip(*(t if isinstance(t, tuple) else (t,) for t in (got, want))))
+        with pytest.raises(ValueError):
+            f(stream=Other())
+
+
+def test_out_of_memory_is_torch_s(r9q):  # noqa: F811
+    """Outputs that do not fit (of a small share of the memory that the process may have): the error that torch raises."""
+    x = rand((1, 1, 2, 128), 35).to(dev()).expand(1, 6_000_000, 2, 128)
+    g = torch.zeros((1, 1, 2), device=dev())
+    args = (torch.zeros((1, 2, 128, 128), device=dev()), torch.zeros(1, dtype=torch.int32, device=dev()))
+    rates = torch.zeros((1, 6_000_000, 2), device=dev())
+    torch.cuda.set_per_process_memory_fraction(0.01)
+    try:
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            r9q.r9q_gated_delta_step(x, x, x, rates, rates, *args)       # 3 GB
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    o = r9q.r9q_gated_delta_step(x[:, :1], x[:, :1], x[:, :1], g, g, *args)
+    assert o.shape == (1, 1, 2, 128) and r9q.r9q_last_device_error() == 0
+
+
+@pytest.mark.parametrize("n,heads", [(8, 8), (40, 32)])
+def test_cache_past_32_bits(r9q, n, heads):  # noqa: F811
+    """Pages at the end of a cache of more than 2^32 bytes of keys, for few rows and for many; tokens moved between
+    them."""
+    Hk, page, pages = 8, 256, 34000                           # 4.5 GB of keys
+    cache = r9q.r9q_kv4_cache(pages, Hk, page, D)
+    table = np.full((1, 72), -1, np.int32)                    # (so wide that many rows take their own kernel)
+    table[0, :3] = [pages - 1, 5, pages - 2]
+    length = 600
+    t = np.arange(length)
+    slots = table[0, t // page].astype(np.int64) * page + t % page
+    kv = rand((length, 2 * Hk, D), 41).to(dev())
+    r9q.r9q_kv4_append(kv[:, :Hk], kv[:, Hk:], cache, on(slots))
+    q = rand((1, n, heads, D), 42).to(dev())
+    parents = torch.arange(-1, n - 1, dtype=torch.int32, device=dev())[None]
+    o, lse = r9q.r9q_kv4_tree_attention(q, cache, on(table), on(np.array([length], np.int32)), parents, return_lse=True)
+    small = r9q.r9q_kv4_cache(72, Hk, page, D)                # the same tokens in a small one
+    low = np.full((1, 72), -1, np.int32)
+    low[0, :3] = [2, 0, 1]
+    there = low[0, t // page].astype(np.int64) * page + t % page
+    r9q.r9q_kv4_append(kv[:, :Hk], kv[:, Hk:], small, on(there))
+    e, elow = r9q.r9q_kv4_tree_attention(q, small, on(low), on(np.array([length], np.int32)), parents, return_lse=True)
+    assert torch.equal(o, e) and torch.equal(lse, elow)
+    r9q.r9q_kv4_move(cache, on(slots[None, 550:600]), on(slots[None, 10:60]))
+    a, b = (r9q.r9q_kv4_gather(cache, on(slots[s])) for s in (slice(550, 600), slice(10, 60)))
+    c = r9q.r9q_kv4_gather(small, on(there[550:600]))
+    assert all(torch.equal(x, y) and torch.equal(x, z) for x, y, z in zip(a, b, c))
+    assert r9q.r9q_last_device_error() == 0
+
+
+@pytest.mark.parametrize("Lq", [1, 5, 70])
+def test_states_past_32_bits(r9q, Lq):  # noqa: F811
+    """A slot behind 2^32 elements of states."""
+    n = (1 << 32) // (VH * D * D) + 3
+    state = torch.empty((n, VH, D, D), device=dev())          # 17 GB
+    state[n - 1] = 0.25
+    z = [on(t) if isinstance(t, np.ndarray) else t for t in inputs((1, Lq), KH, VH, D, 51)]
+    small = torch.full((1, VH, D, D), 0.25, device=dev())
+    slot = torch.tensor([n - 1], dtype=torch.int32, device=dev())
+    zero = torch.zeros_like(slot)
+    parents = torch.arange(-1, Lq - 1, dtype=torch.int32, device=dev())[None]
+    if Lq <= 64:
+        assert torch.equal(r9q.r9q_gated_delta_tree(*z, state, slot, parents), r9q.r9q_gated_delta_tree(*z, small, zero, parents))
+        path = parents + 1
+        r9q.r9q_gated_delta_commit(*z[1:], state, slot, path)
+        r9q.r9q_gated_delta_commit(*z[1:], small, zero, path)
+        assert torch.equal(state[n - 1:], small)
+    a, b = r9q.r9q_gated_delta_step(*z, state, slot), r9q.r9q_gated_delta_step(*z, small, zero)
+    assert torch.equal(a, b) and torch.equal(state[n - 1:], small)
+    assert r9q.r9q_last_device_error() == 0
