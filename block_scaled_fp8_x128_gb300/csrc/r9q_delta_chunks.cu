@@ -33,7 +33,8 @@ namespace {
 
 constexpr int kChunk = 64;
 constexpr int kGroup = 128;                  // threads of the tokens, and of T; twice that the rows
-constexpr int kThreads = 4 * kGroup + 32;
+constexpr int kLoaders = 64;
+constexpr int kThreads = 4 * kGroup + 32 + kLoaders;      // (at most 20 warps have 96 registers)
 constexpr int kLStride = 68;                 // floats between rows of L: eight rows' 16-byte pieces lie in different banks
 constexpr int kMStride = 36;
 constexpr int kSorted = 256;                 // sequences that are put in order
@@ -57,20 +58,19 @@ struct Layout {
     static constexpr int kHalves = D / 64;
     static constexpr int kTile = 64 * 128;                   // 64 rows of 128 bytes, swizzled
     static constexpr int kKq = kHalves * 2 * kTile;          // of each 64 elements: K's rows, then Q's
-    static constexpr int kInput = kKq + kChunk * D * 2;      // and V [64][D]
-    static constexpr int kP = 2 * kInput;                    // twice P's two parts
+    static constexpr int kV = 3 * kKq;                       // three chunks' of those; V [64][D]
+    static constexpr int kP = kV + kChunk * D * 2;           // twice P's two parts
     static constexpr int kT = kP + 4 * kTile;                // T's three
     static constexpr int kL = kT + 3 * kTile;                // L, twice
     static constexpr int kM = kL + 2 * kChunk * kLStride * 4;
     static constexpr int kScalars = kM + 32 * kMStride * 4;
-    static constexpr int kOut = kScalars + 2 * (int)sizeof(Scalars);         // outputs [64][D] on their way
-    static constexpr int kBars = kOut + kChunk * D * 2;
-    static_assert(kL % 16 == 0 && kM % 16 == 0 && kScalars % 16 == 0 && sizeof(Scalars) % 16 == 0 && kOut % 16 == 0 && kBars % 16 == 0,
+    static constexpr int kBars = kScalars + 4 * (int)sizeof(Scalars);
+    static_assert(kL % 16 == 0 && kM % 16 == 0 && kScalars % 16 == 0 && sizeof(Scalars) % 16 == 0 && kBars % 16 == 0,
                   "16-byte loads");
     // tensor memory, columns.  S's parts are 64 columns apart.  X's third part takes a place that W alone reads (of S's
     // third), U, in two sums, those of S's first and second.  W is replaced by two parts of X and they by two of u: of
-    // tokens 32 i on in the columns 32 i and 32 i + 16 on; U P^T adds to A(., 0) Y.  (A product takes at least 55 cycles,
-    // 80 with N = 128: so W and Y are one, and U's sums.)
+    // tokens 32 i on in the columns 32 i and 32 i + 16 on; U P^T adds to A(., 0) Y.  (A product takes 40 cycles,
+    // 70 with N = 128: so U's sums are one; W is not held up by Y.)
     static constexpr int kS = 0, kParts = 128, kW = kParts + 192, kY = kW + 64, kG = kY + 64;
     // (A(n, .) u's first two parts then lie where S's third was, its third as those.)
     static constexpr int kX2 = kParts + 128, kU = kParts, kUleft = kParts + 128;
@@ -78,8 +78,8 @@ struct Layout {
 };
 
 struct Barriers {
-    uint64_t input_full[2], q_free[2], v_free[2], k_free[2], gram_full, gram_read, pairs_full[2], pairs_free[2], l_free[2], t_full, s_ready,
-        w_full, x_ready, u_full, u_ready, s_full, o_full;
+    uint64_t input_full[3], k_free[3], v_full, gram_full, gram_read, pairs_full[2], l_free[2], o_full[2], t_full, s_ready,
+        w_full, y_free, y_full, x_ready, u_full, u_ready, o_ready, s_full;
     uint32_t tmem;
     int failed;                              // a wait gave up
 };
@@ -201,16 +201,17 @@ __device__ __forceinline__ uint32_t not_finite(uint64_t (&x)[16]) {
     return m;
 }
 
-// Bounded; after one that gave up all others do at once.
+// Bounded; after one that gave up all others do at once.  (As little code as can be, for there are many: the error is recorded
+// at the end.)
 struct Waits {
     volatile int* failed;
-    int* err;
     __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) const {
-        if (*failed) return;
-        if (!mbar_wait(bar, parity)) {
-            *failed = 1;
-            record_error(err, kErrTimeout);
+#pragma unroll 1
+        for (uint32_t i = 0; i < kSpinLimit; ++i) {
+            if (mbar_try_wait(bar, parity)) return;
+            if (*failed) return;
         }
+        *failed = 1;
     }
 };
 
@@ -218,7 +219,6 @@ template <int D, DeltaMode MODE>
 __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaParams p) {
     using Y = Layout<D>;
     constexpr bool TREE = MODE == kDeltaTree, HAS_Q = MODE != kDeltaCommit;
-    constexpr int KS = D / 16;               // steps of a product over the keys' elements
     extern __shared__ uint8_t raw[];
     begin_chained();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = tid & (kGroup - 1);
@@ -270,31 +270,35 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
     const int chunks = (n + kChunk - 1) / kChunk;
     uint8_t* smem = raw + (1024u - smem_u32(raw) % 1024u) % 1024u;
     Barriers& bars = *reinterpret_cast<Barriers*>(smem + Y::kBars);
-    auto input = [&](int c) { return smem + (c & 1) * Y::kInput; };
+    auto input = [&](int c) { return smem + c % 3 * Y::kKq; };
+    auto third = [](int c) { return (uint32_t)(c / 3) & 1; };        // the phase of what there are three of
     auto p_of = [&](int c) { return smem + Y::kP + (c & 1) * 2 * Y::kTile; };
     auto l_of = [&](int c) { return reinterpret_cast<float*>(smem + Y::kL) + (c & 1) * (kChunk * kLStride); };
     uint8_t* const parts_of_t = smem + Y::kT;
-    auto scalars_of = [&](int c) { return reinterpret_cast<Scalars*>(smem + Y::kScalars) + (c & 1); };
+    auto scalars_of = [&](int c) { return reinterpret_cast<Scalars*>(smem + Y::kScalars) + (c & 3); };
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars.input_full[i], kGroup);
-            mbar_init(&bars.q_free[i], 1);
-            mbar_init(&bars.v_free[i], 1);
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&bars.input_full[i], kLoaders);
             mbar_init(&bars.k_free[i], 1);
+        }
+        mbar_init(&bars.v_full, kLoaders);
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.pairs_full[i], kGroup);
-            mbar_init(&bars.pairs_free[i], 2 * kGroup);
             mbar_init(&bars.l_free[i], kGroup);
+            mbar_init(&bars.o_full[i], 1);
         }
         mbar_init(&bars.gram_full, 1);
         mbar_init(&bars.gram_read, kGroup);
         mbar_init(&bars.t_full, kGroup);
         mbar_init(&bars.s_ready, 2 * kGroup);
         mbar_init(&bars.w_full, 1);
+        mbar_init(&bars.y_free, 2 * kGroup);
+        mbar_init(&bars.y_full, 1);
         mbar_init(&bars.x_ready, 2 * kGroup);
         mbar_init(&bars.u_full, 1);
         mbar_init(&bars.u_ready, 2 * kGroup);
+        mbar_init(&bars.o_ready, 2 * kGroup);
         mbar_init(&bars.s_full, 1);
-        mbar_init(&bars.o_full, 1);
         bars.failed = 0;
         fence_mbar_init();
     }
@@ -303,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
     __syncthreads();
     umma_fence_after();
     const uint32_t tmem = bars.tmem, mine = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const Waits wait = {&bars.failed, p.err};
+    const Waits wait = {&bars.failed};
 
     if (warp < 8) {
         // ---------------------------------------------------------------- rows --
@@ -327,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
         uint32_t out[16];                    // of chunk c, two tokens each, as bf16
         auto take_outputs = [&](int c) {
             const Scalars& sc = *scalars_of(c);
-            wait(&bars.o_full, c & 1);
+            wait(&bars.o_full[c & 1], (c >> 1) & 1);
             umma_fence_after();
             float y[32];
             tmem_ld(mine + Y::kY + t0, y);
@@ -338,6 +342,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 out[i / 2] = pack_bf16x2(f.x * y[i], f.y * y[i + 1]);
                 out[i / 2 + 1] = pack_bf16x2(f.z * y[i + 2], f.w * y[i + 3]);
             }
+        };
+        auto mark_outputs = [&](int c) {
+            const Scalars& sc = *scalars_of(c);
             uint64_t lost = (uint64_t)sc.lost[1][t] << 32 | sc.lost[0][t] | *reinterpret_cast<const uint64_t*>(sc.bad);
             if (lost) {                      // NaN, and what comes from it
                 if constexpr (TREE) {
@@ -360,21 +367,25 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 }
             }
         };
-        // by way of shared memory, so that a warp writes whole lines
+        // (A warp writes 64 bytes of a token.)
+        const int64_t o_stride = (int64_t)p.Hv * D;
+        uint16_t* const o_first = HAS_Q ? p.o + ((row0 + t0) * p.Hv + h) * D + t : nullptr;
         auto write_outputs = [&](int c) {
-            uint16_t* stage = reinterpret_cast<uint16_t*>(smem + Y::kOut);
-            if (live)
+            uint16_t* o = o_first + c * kChunk * o_stride;
+            const int most = live ? min(n - c * kChunk - t0, 32) : 0;
+            if (most == 32) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) stage[(t0 + i) * D + t] = (uint16_t)(out[i / 2] >> (16 * (i & 1)));
-            asm volatile("bar.sync 3, 256;" ::: "memory");
-            const int most = min(kChunk, n - c * kChunk) * (D / 8);
-            uint16_t* o = p.o + ((row0 + c * kChunk) * p.Hv + h) * D;
+                for (int i = 0; i < 32; ++i) {
+                    *o = (uint16_t)(out[i / 2] >> (16 * (i & 1)));
+                    o += o_stride;
+                }
+            } else {
 #pragma unroll
-            for (int x = tid; x < kChunk * (D / 8); x += 2 * kGroup)
-                if (x < most)
-                    *reinterpret_cast<uint4*>(o + (int64_t)(x / (D / 8)) * p.Hv * D + x % (D / 8) * 8) =
-                        *reinterpret_cast<const uint4*>(stage + x * 8);
-            mbar_arrive(&bars.pairs_free[c & 1]);
+                for (int i = 0; i < 32; ++i) {
+                    if (i < most) *o = (uint16_t)(out[i / 2] >> (16 * (i & 1)));
+                    o += o_stride;
+                }
+            }
         };
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
@@ -410,27 +421,30 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 store_part<true>(mine + Y::kParts + 128 + e / 2, s);
                 tmem_st16(mine + Y::kParts + e / 2, first);
             }
-            if (HAS_Q && c > 0) take_outputs(c - 1);
             tmem_wait_st();
             umma_fence_before();
             mbar_arrive(&bars.s_ready);
-            if (c > 0) {
-                if constexpr (HAS_Q)
-                    write_outputs(c - 1);
-                else
-                    mbar_arrive(&bars.pairs_free[(c - 1) & 1]);
+            if constexpr (HAS_Q) {
+                if (c > 0) take_outputs(c - 1);
+                umma_fence_before();
+                mbar_arrive(&bars.y_free);
             }
 
             // ---- X ----
-            const uint16_t* v = reinterpret_cast<const uint16_t*>(input(c) + Y::kKq) + t0 * D + (live ? t : 0);
-            uint64_t own[16], x[16];
+            const uint16_t* v = reinterpret_cast<const uint16_t*>(smem + Y::kV) + t0 * D + (live ? t : 0);
+            uint32_t own[16];
+            wait(&bars.v_full, c & 1);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) own[i] = mul2(sc.x[t0 / 2 + i].x, pair_of(bf16_lo(v[2 * i * D]), bf16_lo(v[(2 * i + 1) * D])));
+            for (int i = 0; i < 16; ++i) own[i] = (uint32_t)v[2 * i * D] | (uint32_t)v[(2 * i + 1) * D] << 16;
+            uint64_t x[16];
             wait(&bars.w_full, c & 1);
             umma_fence_after();
             load_pairs(mine + Y::kW + t0, x);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = fma2(sc.x[t0 / 2 + i].y, x[i], own[i]);
+            for (int i = 0; i < 16; ++i) {
+                const ulonglong2 f = sc.x[t0 / 2 + i];
+                x[i] = fma2(f.y, x[i], mul2(f.x, pair_of(bf16_lo(own[i]), bf16_hi(own[i]))));
+            }
             uint32_t lost = not_finite(x);
             store_part(mine + Y::kW + t0, x);
             store_part(mine + Y::kW + t0 + 16, x);
@@ -439,8 +453,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             umma_fence_before();
             mbar_arrive(&bars.x_ready);
 
-            // ---- Y, as it goes into the outputs ----
+            // ---- the last chunk's outputs, and Y as it goes into these ----
             if constexpr (HAS_Q) {
+                if (c > 0) {
+                    mark_outputs(c - 1);
+                    write_outputs(c - 1);
+                }
+                wait(&bars.y_full, c & 1);
+                umma_fence_after();
                 load_pairs(mine + Y::kY + t0, x);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -481,14 +501,17 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 store_part(mine + Y::kUleft + t0 / 2, y);
                 store_part(mine + Y::kUleft + 32 + t0 / 2, y);
                 store_part<true>(mine + Y::kU + t0, y);
+                tmem_wait_st();
+                umma_fence_before();
+                mbar_arrive(&bars.u_ready);
             }
             if constexpr (HAS_Q) {
                 store_part(mine + Y::kW + t0, x);
                 store_part<true>(mine + Y::kW + t0 + 16, x);
+                tmem_wait_st();
+                umma_fence_before();
+                mbar_arrive(&bars.o_ready);
             }
-            tmem_wait_st();
-            umma_fence_before();
-            mbar_arrive(&bars.u_ready);
         }
         if constexpr (!TREE) {
             wait(&bars.s_full, (chunks - 1) & 1);
@@ -506,59 +529,15 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
         }
         if constexpr (HAS_Q) {
             take_outputs(chunks - 1);
+            mark_outputs(chunks - 1);
             write_outputs(chunks - 1);
         }
     } else if (warp < 12) {
         // -------------------------------------------------------------- tokens --
         const int i = t & 63;                // row of K or of Q
         const bool key = t < 64;
-        // token `at` of the sequence: in K, Q and V, and in g and beta
-        auto place = [&](int at) { return MODE == kDeltaCommit ? (int64_t)path[at] : (p.cu ? row0 : 0) + at; };
         auto rate_of = [&](int at) {
             return ((MODE == kDeltaCommit ? row0 + path[at] : row0 + at)) * p.Hv + h;
-        };
-        // a thread copies the same 16 bytes of every 128 / (D/8)-th token
-        constexpr int PIECES = D / 8, STEP = kGroup / PIECES;
-        const int piece = t % PIECES, r0 = t / PIECES;
-        const uint32_t tile = (uint32_t)(piece >> 3) * (2 * Y::kTile);
-        const uint16_t* kp = p.k + b * p.k_bs + hk * p.k_hs + piece * 8;
-        const uint16_t* qp = HAS_Q ? p.q + b * p.q_bs + hk * p.q_hs + piece * 8 : nullptr;
-        const uint16_t* vp = p.v + b * p.v_bs + h * p.v_hs + piece * 8;
-        enum { kKeys, kQueries, kValues };
-        auto load = [&](int what, int c) {
-            const uint32_t base = smem_u32(input(c)) + (what == kValues ? Y::kKq + r0 * (D * 2) + piece * 16
-                                                                        : tile + what * Y::kTile + r0 * 128);
-            const uint16_t* src = what == kKeys ? kp : what == kQueries ? qp : vp;
-            const int64_t stride = what == kKeys ? p.k_ts : what == kQueries ? p.q_ts : p.v_ts;
-            if (c * kChunk + kChunk <= n && MODE != kDeltaCommit) {
-                src += place(c * kChunk + r0) * stride;
-#pragma unroll
-                for (int x = 0; x < kChunk / STEP; ++x) {
-                    const uint32_t dst = what == kValues ? base + x * (STEP * D * 2)
-                                                         : base + x * (STEP * 128) + (((piece & 7) ^ ((r0 + x * STEP) & 7)) << 4);
-                    copy16(dst, src, true);
-                    src += STEP * stride;
-                }
-            } else {                         // zeros behind the last token
-#pragma unroll 1
-                for (int x = 0; x < kChunk / STEP; ++x) {
-                    const int at = c * kChunk + r0 + x * STEP;
-                    const uint32_t dst = what == kValues ? base + x * (STEP * D * 2)
-                                                         : base + x * (STEP * 128) + (((piece & 7) ^ ((r0 + x * STEP) & 7)) << 4);
-                    copy16(dst, at < n ? src + place(at) * stride : p.k, at < n);
-                }
-            }
-        };
-        auto load_all = [&](int c) {
-            load(kKeys, c);
-            if (HAS_Q) load(kQueries, c);
-            load(kValues, c);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-        auto loaded = [&](int c) {
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            fence_proxy_async_smem();
-            mbar_arrive(&bars.input_full[c & 1]);
         };
         float g_next = 0.0f, beta_next = 0.0f;
         auto load_rates = [&](int c) {       // ahead of their use
@@ -576,11 +555,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             const long long g = __float2ll_rn(fminf(fmaxf(g_next, -200.0f), 200.0f) * (1.4426950408889634f * 0x1p40f));
             if (c + 1 < chunks) load_rates(c + 1);
             // the row's length
-            wait(&bars.input_full[c & 1], (c >> 1) & 1);
+            wait(&bars.input_full[c % 3], third(c));
             float square = 0.0f;
             if (key || HAS_Q) {
                 const uint8_t* row = input(c) + t * 128;     // (K's rows, then Q's)
-#pragma unroll
+#pragma unroll 4
                 for (int x = 0; x < D / 8; ++x) {
                     const uint4 q = *reinterpret_cast<const uint4*>(row + (x >> 3) * (2 * Y::kTile) + (((x & 7) ^ (t & 7)) << 4));
                     const Eight e = unpack(q);
@@ -588,7 +567,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 }
             }
             const float r = at < n ? rsqrtf(square + p.eps) : 0.0f;
-            if (c >= 2) wait(&bars.pairs_free[c & 1], ((c - 2) >> 1) & 1);
             uint64_t above = ~0ull >> (63 - i);
             long long sum = 0, end = 0;
             if constexpr (TREE) {
@@ -636,7 +614,10 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 sc.bad[0] = sc.bad[1] = 0;
             }
             group_barrier<1>();
-            if (c >= 2) wait(&bars.l_free[c & 1], ((c - 2) >> 1) & 1);
+            if (c >= 2) {
+                wait(&bars.l_free[c & 1], ((c - 2) >> 1) & 1);
+                wait(&bars.o_full[c & 1], ((c - 2) >> 1) & 1);      // (P; and what used the scalars of chunk c - 3 and before)
+            }
             wait(&bars.gram_full, c & 1);
             umma_fence_after();
             const float own = key ? beta * r : 1.0f;
@@ -700,25 +681,8 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             mbar_arrive(&bars.pairs_full[c & 1]);
         };
         load_rates(0);
-        load_all(0);
-        loaded(0);
-        if (chunks > 1) load_all(1);
-        if (chunks > 1) loaded(1);
-        pairs(0);
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
-            if (c + 1 < chunks) pairs(c + 1);
-            if (c + 2 < chunks) {            // each as soon as this chunk's is used
-                wait(&bars.q_free[c & 1], (c >> 1) & 1);
-                if (HAS_Q) load(kQueries, c + 2);
-                wait(&bars.v_free[c & 1], (c >> 1) & 1);
-                load(kValues, c + 2);
-                wait(&bars.k_free[c & 1], (c >> 1) & 1);
-                load(kKeys, c + 2);
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                loaded(c + 2);
-            }
-        }
+        for (int c = 0; c < chunks; ++c) pairs(c);
     } else if (warp < 16) {
         // ------------------------------------------------------------ L into T --
         float* const M = reinterpret_cast<float*>(smem + Y::kM);
@@ -806,11 +770,11 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 }
             }
             // its parts, half a row a thread
-            if (c > 0) wait(&bars.v_free[(c - 1) & 1], ((c - 1) >> 1) & 1);      // (the last chunk's are used)
+            if (c > 0) wait(&bars.u_full, (c - 1) & 1);      // (the last chunk's are used)
             {
                 const int r = t >> 1, half = t & 1;
                 uint8_t* T = parts_of_t + r * 128;
-#pragma unroll
+#pragma unroll 1
                 for (int x = 0; x < 4; ++x) {
                     const float4 a = l4(r, half * 32 + x * 8), d = l4(r, half * 32 + x * 8 + 4);
                     uint64_t y[4] = {pair_of(a.x, a.y), pair_of(a.z, a.w), pair_of(d.x, d.y), pair_of(d.z, d.w)};
@@ -829,19 +793,79 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             mbar_arrive(&bars.t_full);
             mbar_arrive(&bars.l_free[c & 1]);
         }
+    } else if (warp > 16) {
+        // --------------------------------------------------------------- loads --
+        const int x0 = tid - (4 * kGroup + 32);
+        // A thread copies the same 16 bytes of every 64 / (D/8)-th token.
+        constexpr int PIECES = D / 8, STEP = kLoaders / PIECES;
+        const int piece = x0 % PIECES, r0 = x0 / PIECES;
+        enum { kKeys, kQueries, kValues };
+        auto load = [&](int what, int c) {
+            const bool values = what == kValues;
+            uint32_t dst = values ? smem_u32(smem + Y::kV) + r0 * (D * 2) + piece * 16
+                                  : smem_u32(input(c)) + (piece >> 3) * (2 * Y::kTile) + what * Y::kTile + r0 * 128;
+            const uint16_t* src = (what == kKeys ? p.k + b * p.k_bs + hk * p.k_hs
+                                   : values      ? p.v + b * p.v_bs + h * p.v_hs
+                                                 : p.q + b * p.q_bs + hk * p.q_hs) + piece * 8;
+            const int64_t stride = what == kKeys ? p.k_ts : values ? p.v_ts : p.q_ts;
+            int at = c * kChunk + r0;
+            if (MODE != kDeltaCommit) src += ((p.cu ? row0 : 0) + at) * stride;
+#pragma unroll 4
+            for (int x = 0; x < kChunk / STEP; ++x) {
+                const uint16_t* from = src;
+                if (MODE == kDeltaCommit && at < n) from += path[at] * stride;
+                copy16(dst + (values ? 0 : ((piece & 7) ^ (at & 7)) << 4), at < n ? from : p.k, at < n);     // (zeros behind the last)
+                dst += STEP * (values ? D * 2 : 128);
+                src += MODE == kDeltaCommit ? 0 : STEP * stride;
+                at += STEP;
+            }
+        };
+#pragma unroll 1
+        for (int c = -2; c < chunks; ++c) {
+            if (c >= 0) {
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                mbar_arrive(&bars.v_full);
+            }
+            if (c + 2 < chunks) {            // where chunk c - 1 was
+                if (c > 0) wait(&bars.k_free[(c - 1) % 3], third(c - 1));
+#pragma unroll 1
+                for (int what = kKeys; what <= (HAS_Q ? kQueries : kKeys); ++what) load(what, c + 2);
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_proxy_async_smem();
+                mbar_arrive(&bars.input_full[(c + 2) % 3]);
+            }
+            if (c + 1 < chunks && c >= -1) {
+                if (c >= 0) wait(&bars.x_ready, c & 1);
+                load(kValues, c + 1);
+            }
+        }
     } else if (elect_one()) {
         // ------------------------------------------------------------ products --
         constexpr uint32_t kById = idesc_bf16(64, false), kUpdate = idesc_bf16(D, true);
+        // D[tmem] = A B^T with A the keys' and queries' rows or parts of S, B [64][D]
         auto gram = [&](int c) {
-            wait(&bars.input_full[c & 1], (c >> 1) & 1);
+            wait(&bars.input_full[c % 3], third(c));
+            if (c > 0) wait(&bars.gram_read, (c - 1) & 1);
             umma_fence_after();
             const uint32_t kq = smem_u32(input(c));
+#pragma unroll 1
+            for (int half = 0; half < Y::kHalves; ++half)
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const uint64_t d = umma_sdesc_sw128(kq + (k >> 2) * (2 * Y::kTile) + (k & 3) * 32);
-                umma_bf16(tmem + Y::kG, d, d, kById, k > 0);
-            }
+                for (int k = 0; k < 4; ++k) {
+                    const uint64_t d = umma_sdesc_sw128(kq + half * (2 * Y::kTile) + k * 32);
+                    umma_bf16(tmem + Y::kG, d, d, kById, half + k > 0);
+                }
             umma_commit(&bars.gram_full);
+        };
+        auto by_keys = [&](uint32_t d, uint32_t b_tile, int parts) {
+#pragma unroll 1
+            for (int i = 0; i < parts * Y::kHalves; ++i) {
+                const int part = i / Y::kHalves, half = i % Y::kHalves;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    umma_bf16_tmem(d, tmem + Y::kParts + part * 64 + half * 32 + k * 8,
+                                   umma_sdesc_sw128(b_tile + half * (2 * Y::kTile) + k * 32), kById, i + k > 0);
+            }
         };
         // D[tmem] (+)= A[tmem] B^T with B [N][64]; A's tokens from 32 on `apart` columns after the others
         auto by_tokens = [&](uint32_t d, uint32_t a, int apart, uint32_t b_tile, uint32_t idesc, bool first) {
@@ -849,41 +873,38 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             for (int k = 0; k < kChunk / 16; ++k)
                 umma_bf16_tmem(d, a + (k >> 1) * apart + (k & 1) * 8, umma_sdesc_sw128(b_tile + k * 32), idesc, !first || k > 0);
         };
-        gram(0);
+#pragma unroll 1
+        for (int c = 0; c < min(chunks, 2); ++c) gram(c);
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             const uint32_t kq = smem_u32(input(c)), pp = smem_u32(p_of(c)), tt = smem_u32(parts_of_t);
             wait(&bars.s_ready, c & 1);
             umma_fence_after();
-            // W, with three parts of S, and Y beside it, with two
-#pragma unroll
-            for (int part = 0; part < 3; ++part)
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    umma_bf16_tmem(tmem + Y::kW, tmem + Y::kParts + part * 64 + k * 8,
-                                   umma_sdesc_sw128(kq + (k >> 2) * (2 * Y::kTile) + (k & 3) * 32),
-                                   HAS_Q && part < 2 ? idesc_bf16(128, false) : kById, part + k > 0);
-            umma_commit(&bars.w_full);
-            umma_commit(&bars.q_free[c & 1]);
-            if (c + 1 < chunks) {
-                wait(&bars.gram_read, c & 1);
-                umma_fence_after();
-                gram(c + 1);
+            // W, with three parts of S, then Y, with two
+#pragma unroll 1
+            for (int y = 0; y < (HAS_Q ? 2 : 1); ++y) {
+                if (y) {
+                    umma_commit(&bars.w_full);
+                    wait(&bars.y_free, c & 1);
+                    umma_fence_after();
+                }
+                by_keys(tmem + (y ? Y::kY : Y::kW), kq + y * Y::kTile, 3 - y);
             }
+            umma_commit(HAS_Q ? &bars.y_full : &bars.w_full);
             wait(&bars.x_ready, c & 1);
             wait(&bars.t_full, c & 1);
             umma_fence_after();
             // parts (X, T): (0, 0) and (0, 1), (1, 0) and (1, 1), (0, 2), (2, 0)
-            by_tokens(tmem + Y::kU, tmem + Y::kW, 32, tt, idesc_bf16(128, false), true);
-            by_tokens(tmem + Y::kU, tmem + Y::kW + 16, 32, tt, idesc_bf16(128, false), false);
-            by_tokens(tmem + Y::kU, tmem + Y::kW, 32, tt + 2 * Y::kTile, kById, false);
-            by_tokens(tmem + Y::kU, tmem + Y::kX2, 16, tt, kById, false);
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i)
+                by_tokens(tmem + Y::kU, tmem + (i == 3 ? Y::kX2 : i == 1 ? Y::kW + 16 : Y::kW), i == 3 ? 16 : 32,
+                          tt + (i == 2 ? 2 * Y::kTile : 0), i < 2 ? idesc_bf16(128, false) : kById, i == 0);
             umma_commit(&bars.u_full);
-            umma_commit(&bars.v_free[c & 1]);
-            wait(&bars.u_ready, c & 1);
-            umma_fence_after();
+            if (c + 2 < chunks) gram(c + 2);
             if constexpr (!TREE) {
-#pragma unroll
+                wait(&bars.u_ready, c & 1);
+                umma_fence_after();
+#pragma unroll 1
                 for (int part = 0; part < 3; ++part)
 #pragma unroll
                     for (int k = 0; k < kChunk / 16; ++k)
@@ -892,23 +913,27 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                                        sdesc_n_contiguous(kq + k * 2048, 2 * Y::kTile), kUpdate, true);
                 umma_commit(&bars.s_full);
             }
-            umma_commit(&bars.k_free[c & 1]);
+            umma_commit(&bars.k_free[c % 3]);
             if constexpr (HAS_Q) {
                 wait(&bars.pairs_full[c & 1], (c >> 1) & 1);
-                by_tokens(tmem + Y::kY, tmem + Y::kW, 32, pp, kById, false);
-                by_tokens(tmem + Y::kY, tmem + Y::kW, 32, pp + Y::kTile, kById, false);
-                by_tokens(tmem + Y::kY, tmem + Y::kW + 16, 32, pp, kById, false);
+                wait(&bars.o_ready, c & 1);
+                umma_fence_after();
+                // parts (u, P): (0, 0), (0, 1), (1, 0)
+#pragma unroll 1
+                for (int i = 0; i < 3; ++i)
+                    by_tokens(tmem + Y::kY, tmem + Y::kW + (i == 2 ? 16 : 0), 32, pp + (i == 1 ? Y::kTile : 0), kById, false);
             }
-            umma_commit(&bars.o_full);
+            umma_commit(&bars.o_full[c & 1]);
         }
         // all products are done, whatever else gave up
-        if (!mbar_wait(&bars.o_full, (chunks - 1) & 1)) record_error(p.err, kErrTimeout);
+        if (!mbar_wait(&bars.o_full[(chunks - 1) & 1], ((chunks - 1) >> 1) & 1)) bars.failed = 1;
     }
     __syncwarp();
     umma_fence_before();
     __syncthreads();
     umma_fence_after();
     if (warp == 16) tmem_dealloc(tmem, 512);
+    if (tid == 0 && bars.failed) record_error(p.err, kErrTimeout);
 }
 
 template <int D, DeltaMode MODE>
