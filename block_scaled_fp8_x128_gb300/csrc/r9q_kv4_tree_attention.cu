@@ -112,13 +112,13 @@ __device__ __forceinline__ void part_barrier() {
 // Bounded; after one that gave up all others do at once.
 struct Waits {
     volatile int* failed;
-    int* err;
     __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) const {
-        if (*failed) return;
-        if (!mbar_wait(bar, parity & 1)) {
-            *failed = 1;
-            record_error(err, kErrTimeout);
+#pragma unroll 1
+        for (uint32_t i = 0; i < kSpinLimit; ++i) {
+            if (mbar_try_wait(bar, parity & 1)) return;
+            if (*failed) return;
         }
+        *failed = 1;                         // (recorded at the end)
     }
 };
 
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
     __syncthreads();
     umma_fence_after();
     const uint32_t tmem = bars.tmem;
-    const Waits wait = {&bars.failed, p.err};
+    const Waits wait = {&bars.failed};
     const int rows = p.Lq * p.G;
     // Steps of a stream: every tile, or every second one.
     auto steps_of = [](int tiles, int stream) { return DUAL ? tiles : (tiles + 1 - stream) >> 1; };
@@ -801,6 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
     __syncthreads();
     umma_fence_after();
     if (warp == 8) tmem_dealloc(tmem, 512);
+    if (tid == 0 && bars.failed) record_error(p.err, kErrTimeout);
 }
 
 // Items that several CTAs share.  A partial is [D / 4][ROWS] of four elements, then the rows' references and sums; a thread
