@@ -79,7 +79,7 @@ struct Layout {
 
 struct Barriers {
     uint64_t input_full[3], k_free[3], v_full, gram_full, gram_read, pairs_full[2], l_free[2], o_full[2], t_full, s_ready,
-        w_full, y_free, y_full, x_ready, u_full, u_ready, o_ready, s_full;
+        w_full, y_free, y_full, x_ready, u_full, u_ready, s_full;
     uint32_t tmem;
     int failed;                              // a wait gave up
 };
@@ -132,14 +132,19 @@ __device__ __forceinline__ uint64_t sdesc_n_contiguous(uint32_t saddr, uint32_t 
     d |= (uint64_t)2 << 61;
     return d;
 }
-// 16 columns of this thread's lane.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&d)[16]) {
+// 16 or 8 columns of this thread's lane.
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&d)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
         "%15};" ::"r"(d[0]),
         "r"(d[1]), "r"(d[2]), "r"(d[3]), "r"(d[4]), "r"(d[5]), "r"(d[6]), "r"(d[7]), "r"(d[8]), "r"(d[9]), "r"(d[10]),
         "r"(d[11]), "r"(d[12]), "r"(d[13]), "r"(d[14]), "r"(d[15]), "r"(taddr)
         : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&d)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(d[0]), "r"(d[1]), "r"(d[2]),
+                 "r"(d[3]), "r"(d[4]), "r"(d[5]), "r"(d[6]), "r"(d[7]), "r"(taddr)
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -157,16 +162,16 @@ __device__ __forceinline__ void group_barrier() {
     asm volatile("bar.sync %0, 128;" ::"n"(ID) : "memory");
 }
 // The next part of 32 values, two a column; LAST: nothing stays.
-template <bool LAST = false>
-__device__ __forceinline__ void take_parts(uint32_t (&y)[16], uint64_t (&x)[16]) {
+template <bool LAST = false, int N>
+__device__ __forceinline__ void take_parts(uint32_t (&y)[N], uint64_t (&x)[N]) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = LAST ? last_part(x[i]) : take_part(x[i]);
+    for (int i = 0; i < N; ++i) y[i] = LAST ? last_part(x[i]) : take_part(x[i]);
 }
-template <bool LAST = false>
-__device__ __forceinline__ void store_part(uint32_t taddr, uint64_t (&x)[16]) {
-    uint32_t y[16];
+template <bool LAST = false, int N>
+__device__ __forceinline__ void store_part(uint32_t taddr, uint64_t (&x)[N]) {
+    uint32_t y[N];
     take_parts<LAST>(y, x);
-    tmem_st16(taddr, y);
+    tmem_st(taddr, y);
 }
 // 32 columns of this thread's lane.
 __device__ __forceinline__ void load_pairs(uint32_t taddr, uint64_t (&x)[16]) {
@@ -176,16 +181,17 @@ __device__ __forceinline__ void load_pairs(uint32_t taddr, uint64_t (&x)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = pair_of(f[2 * i], f[2 * i + 1]);
 }
-// Which of 32 values are not finite, a bit each; those become zero.
-__device__ __forceinline__ uint32_t not_finite(uint64_t (&x)[16]) {
+// Which of 2 N values are not finite, a bit each; those become zero.
+template <int N>
+__device__ __forceinline__ uint32_t not_finite(uint64_t (&x)[N]) {
     uint64_t sum = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sum = fma2(x[i], 0ull, sum);
+    for (int i = 0; i < N; ++i) sum = fma2(x[i], 0ull, sum);
     uint32_t m = 0;
     const float2 any = parts_of(sum);
     if (any.x + any.y != 0.0f) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < N; ++i) {
             float2 f = parts_of(x[i]);
             if (!(fabsf(f.x) <= FLT_MAX)) {
                 m |= 1u << (2 * i);
@@ -297,7 +303,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
         mbar_init(&bars.x_ready, 2 * kGroup);
         mbar_init(&bars.u_full, 1);
         mbar_init(&bars.u_ready, 2 * kGroup);
-        mbar_init(&bars.o_ready, 2 * kGroup);
         mbar_init(&bars.s_full, 1);
         bars.failed = 0;
         fence_mbar_init();
@@ -325,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 x[4 * i + 2] = v.z;
                 x[4 * i + 3] = v.w;
             }
-            tmem_st16(mine + Y::kS + e, x);
+            tmem_st(mine + Y::kS + e, x);
         }
         tmem_wait_st();
         uint32_t out[16];                    // of chunk c, two tokens each, as bf16
@@ -412,14 +417,14 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                             x[2 * j] = __float_as_uint(f.x);
                             x[2 * j + 1] = __float_as_uint(f.y);
                         }
-                        tmem_st16(mine + Y::kS + e + i * 16, x);
+                        tmem_st(mine + Y::kS + e + i * 16, x);
                     }
                 }
                 uint32_t first[16];
                 take_parts(first, s);
                 store_part(mine + Y::kParts + 64 + e / 2, s);
                 store_part<true>(mine + Y::kParts + 128 + e / 2, s);
-                tmem_st16(mine + Y::kParts + e / 2, first);
+                tmem_st(mine + Y::kParts + e / 2, first);
             }
             tmem_wait_st();
             umma_fence_before();
@@ -471,47 +476,48 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                         y[2 * j] = __float_as_uint(f.x);
                         y[2 * j + 1] = __float_as_uint(f.y);
                     }
-                    tmem_st16(mine + Y::kY + t0 + i * 16, y);
+                    tmem_st(mine + Y::kY + t0 + i * 16, y);
                 }
             }
 
-            // ---- u, as an operand ----
+            // ---- u, as an operand: with A(n, .) for the state, as it is for the outputs ----
             wait(&bars.u_full, c & 1);
             umma_fence_after();
-            load_pairs(mine + Y::kU + t0, x);
+#pragma unroll 1
+            for (int t1 = t0; t1 < t0 + 32; t1 += 16) {
+                uint64_t u[8];
+                {
+                    float y[16], z[16];
+                    tmem_ld(mine + Y::kU + t1, y);
+                    tmem_ld(mine + Y::kU + 64 + t1, z);
+                    tmem_wait_ld(y);
+                    tmem_wait_ld(z);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float y[16];
-                tmem_ld(mine + Y::kU + 64 + t0 + i * 16, y);
-                tmem_wait_ld(y);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[i * 8 + j] = add2(x[i * 8 + j], pair_of(y[2 * j], y[2 * j + 1]));
-            }
-            lost |= not_finite(x);
-            sc.lost[half][t] = lost;
-            if constexpr (!TREE) {
-                uint64_t y[16];
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&sc.last[t0 + 2 * i]);
-                    y[i] = mul2(f.x, x[i]);
-                    y[i + 1] = mul2(f.y, x[i + 1]);
+                    for (int j = 0; j < 8; ++j) u[j] = add2(pair_of(y[2 * j], y[2 * j + 1]), pair_of(z[2 * j], z[2 * j + 1]));
                 }
-                if (lost | sc.bad[0] | sc.bad[1]) y[0] = pair_of(__int_as_float(0x7FC00000), 0.0f);     // into the state
-                store_part(mine + Y::kUleft + t0 / 2, y);
-                store_part(mine + Y::kUleft + 32 + t0 / 2, y);
-                store_part<true>(mine + Y::kU + t0, y);
-                tmem_wait_st();
-                umma_fence_before();
-                mbar_arrive(&bars.u_ready);
+                lost |= not_finite(u) << (t1 - t0);
+                if constexpr (!TREE) {
+                    uint64_t y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(&sc.last[t1 + 2 * i]);
+                        y[i] = mul2(f.x, u[i]);
+                        y[i + 1] = mul2(f.y, u[i + 1]);
+                    }
+                    if (t1 > t0 && (lost | sc.bad[0] | sc.bad[1])) y[0] = pair_of(__int_as_float(0x7FC00000), 0.0f);     // into the state
+                    store_part(mine + Y::kUleft + t1 / 2, y);
+                    store_part(mine + Y::kUleft + 32 + t1 / 2, y);
+                    store_part<true>(mine + Y::kU + t0 + (t1 - t0) / 2, y);
+                }
+                if constexpr (HAS_Q) {
+                    store_part(mine + Y::kW + t0 + (t1 - t0) / 2, u);
+                    store_part<true>(mine + Y::kW + t0 + 16 + (t1 - t0) / 2, u);
+                }
             }
-            if constexpr (HAS_Q) {
-                store_part(mine + Y::kW + t0, x);
-                store_part<true>(mine + Y::kW + t0 + 16, x);
-                tmem_wait_st();
-                umma_fence_before();
-                mbar_arrive(&bars.o_ready);
-            }
+            sc.lost[half][t] = lost;
+            tmem_wait_st();
+            umma_fence_before();
+            mbar_arrive(&bars.u_ready);
         }
         if constexpr (!TREE) {
             wait(&bars.s_full, (chunks - 1) & 1);
@@ -901,9 +907,9 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                           tt + (i == 2 ? 2 * Y::kTile : 0), i < 2 ? idesc_bf16(128, false) : kById, i == 0);
             umma_commit(&bars.u_full);
             if (c + 2 < chunks) gram(c + 2);
+            wait(&bars.u_ready, c & 1);
+            umma_fence_after();
             if constexpr (!TREE) {
-                wait(&bars.u_ready, c & 1);
-                umma_fence_after();
 #pragma unroll 1
                 for (int part = 0; part < 3; ++part)
 #pragma unroll
@@ -916,8 +922,6 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
             umma_commit(&bars.k_free[c % 3]);
             if constexpr (HAS_Q) {
                 wait(&bars.pairs_full[c & 1], (c >> 1) & 1);
-                wait(&bars.o_ready, c & 1);
-                umma_fence_after();
                 // parts (u, P): (0, 0), (0, 1), (1, 0)
 #pragma unroll 1
                 for (int i = 0; i < 3; ++i)

@@ -276,14 +276,15 @@ def test_calls_run_on_the_device_of_their_tensors(r9q, monkeypatch):  # noqa: F8
 
 def test_out_of_memory_is_torch_s(r9q):  # noqa: F811
     """Outputs that do not fit (of a small share of the memory that the process may have): the error that torch raises."""
-    x = rand((1, 1, 2, 128), 35).to(dev()).expand(1, 6_000_000, 2, 128)
+    x = rand((1, 1, 2, 128), 35).to(dev()).expand(1, 20_000_000, 2, 128)
     g = torch.zeros((1, 1, 2), device=dev())
     args = (torch.zeros((1, 2, 128, 128), device=dev()), torch.zeros(1, dtype=torch.int32, device=dev()))
-    rates = torch.zeros((1, 6_000_000, 2), device=dev())
+    rates = torch.zeros((1, 20_000_000, 2), device=dev())
+    torch.cuda.empty_cache()                                  # (blocks that earlier tests left)
     torch.cuda.set_per_process_memory_fraction(0.01)
     try:
         with pytest.raises(torch.cuda.OutOfMemoryError):
-            r9q.r9q_gated_delta_step(x, x, x, rates, rates, *args)       # 3 GB
+            r9q.r9q_gated_delta_step(x, x, x, rates, rates, *args)       # 10 GB
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     o = r9q.r9q_gated_delta_step(x[:, :1], x[:, :1], x[:, :1], g, g, *args)
