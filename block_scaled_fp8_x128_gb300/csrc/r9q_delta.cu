@@ -10,6 +10,10 @@
 // not depend on the row, the products of keys and queries among themselves and the decays,
 // is formed once for the CTA, a warp following a token's ancestors and adding up their decays as
 // it goes.  In a tree S stays as it is.
+//
+// What bounds it: with one token HBM (128 sequences, 32 heads of 128: 79 us, 6.8 TB/s); with more about 1 us a token
+// for the sums over earlier tokens (16 trees of 16 nodes: 37 us, 64 paths of 5: 53 us, 5.1 TB/s).  A head's CTA of 8 warps
+// against one of 4 warps for half of it: the products among the tokens are formed once (53 -> 37 us).
 #include "r9q_delta.cuh"
 
 namespace r9q {
@@ -388,13 +392,13 @@ cudaError_t launch_rows(const DeltaParams& p, cudaStream_t st) {
 cudaError_t launch_delta(int D, DeltaMode mode, const DeltaParams& p, cudaStream_t st) {
     // This file's kernel takes about 1 us a token beyond its loads, for all of a wave of CTAs; the one
     // in chunks 10 to 16 us for up to 64 tokens, with one CTA an SM.  Measured, us here and in chunks, of the
-    // steps of n tokens: one sequence of 32 heads of 128: n = 12 14.7 and 16.0, 16 18.0 and 16.1; 16 sequences: 16
-    // 47 and 61, 24 66 and 61; 64: 16 184 and 219, 24 255 and 222; heads of 64, 16 sequences of 12: 16
-    // 19.6 and 22.7, 24 27.5 and 22.8.  Trees alike: 12 11.8 and 13.5, 16 14.7 and 13.6 alone, 16 of 16 sequences 37 and 51.
+    // steps of n tokens: one sequence of 32 heads of 128: n = 8 9.8 and 14.7, 12 14.5 and 14.8, 16 18.0 and 14.8; 16
+    // sequences: 16 47 and 56, 24 66 and 56; 64: 16 184 and 200, 24 255 and 203; 12 heads of 64, 16 sequences: 16
+    // 19.7 and 20.8, 24 27 and 21.  Trees alike: one of 12 nodes 11.8 and 12.3, of 16 14.8 and 12.4, 16 of 16 37 and 46.
     const bool waves = (int64_t)p.B * p.Hv > 152;
     bool few = p.Lq <= (waves ? kGroup : 12);
-    // A path is as long as what was accepted, not as its width: of 64 sequences 32 wide 111 and 215 with a third
-    // of it taken, 262 and 221 with all; 48 wide 148 and 217, 377 and 239.
+    // A path is as long as what was accepted, not as its width: of 64 sequences 32 wide 111 and 191 with a third
+    // of it taken, 262 and 201 with all; 48 wide 148 and 195, 378 and 212.
     if (mode == kDeltaCommit) few = p.P <= 32;
     // One of the packed sequences may have all of their tokens.  (Of a token each they are steps.)
     if (p.cu) few = p.T <= max(p.B, 12);

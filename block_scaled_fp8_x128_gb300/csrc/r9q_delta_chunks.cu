@@ -15,11 +15,18 @@
 // goes into S and u, two (2^-16) where only outputs, which are rounded to bf16, follow.
 //
 // Warps 0-7, the rows: S, X and u into parts, the chain that bounds a sequence's time, half the columns each;
-// while W is formed they write the last chunk's outputs.  Warps 8-11, the
-// tokens: K, Q, V are copied a chunk ahead, and L and P of the next chunk formed.  Warps 12-15 turn
+// they take the last chunk's outputs while W is formed and write them during U's products.  Warps 8-11, the
+// tokens: L and P of the next chunk.  Warps 12-15 turn
 // L into T, in fp32 by blocks of 16, 32 and 64 (as a substitution a row's thread would need all of L
 // in its registers: 8300 cycles of shared memory's 128 bytes each for four warps).  Warp 16 issues the
-// products.  In a tree the sums go over ancestors, and its one chunk leaves the state alone.
+// products, 17 and 18 copy K and Q two chunks ahead and V one.  In a tree the sums go over ancestors, and its one chunk
+// leaves the state alone.
+//
+// What bounds it: the chain of one chunk to the next, and the code.  A chunk takes about 9,700 cycles: the update of S 900,
+// its parts 1450, W 1300, X 1000, U 1450, u 2000, the rest between them.  The parts run different code at once; at 185 KB
+// in all it was fetched anew every chunk over a path that the SMs of a group share, and SMs beside busy ones took 1.4 times as
+// long.  So loops are rolled where nothing waits for them, and a wait is a few instructions: 91 KB, 801 -> 641 us for
+// 8192 tokens and 32 heads of 128 (one sequence, 32 SMs), 425 -> 328 for 16 of 64 to 2000 (1.5 TB/s).
 //
 // A value that is not finite would reach earlier tokens (or other branches) through the zeros of T and P.
 // So L's rows, X and u are zero in its place, and the outputs that it belongs to are NaN, as is the state's row.

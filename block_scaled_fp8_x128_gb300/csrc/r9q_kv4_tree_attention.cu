@@ -18,6 +18,10 @@
 // exponent for every key, so that no row's arithmetic depends on what it does not see; V' of a key without a finite pair
 // is zero there and everywhere, and rows that see it are NaN.
 //
+// What bounds it: the softmax's chain of loads, exponentials and stores, with two warps a scheduler (256 rows x 128 heads
+// of 8200 keys, D = 128: 220 us, 630 TFLOP/s; half of the issue slots, tensor cores busy for 30 %; with streams that take turns
+// at it 245, with two threads a row 308, for their registers spill), and 25 us of beginning and end.
+//
 // Warps 0-3 and 4-7: the streams; the first of each issues its products.  Warps 8-11 read the codes of a tile ahead into
 // registers, and write K and V' of the one at hand to shared memory.  Work is cut as in r9q_kv4_attention.cuh; an item that several
 // CTAs share is joined by a second kernel, a warp a row.
@@ -879,9 +883,9 @@ cudaError_t launch(Kv4AttnParams p, int2* items, int sms, cudaStream_t st) {
 
 // This kernel takes about 25 us for a part's beginning and end (the other about 9), and a quarter to a half of the other's
 // time for a row and key.  So: rows that fill at least half of a tile, and work, in 16 rows of 16 keys, worth the difference
-// (us, the other / this; rows, sequences x heads, tokens; D = 128 but where said): 64 x 128 of 8200 149/158; 80 x 128 of
-// 8200 180/162; 96 x 32 of 4100 45/40, x 128 124/99; 128 x 8 of 8200 34/37, x 64 of 2100 55/42, of 8200 147/96; 147 x 4 of 5000
-// (D = 64) 17/30, x 32 54/52; 256 x 8 of 4100 34/33, of 65600 301/122, x 128 of 8200 533/237; 512 x 128 of 350 120/64.  By
+// (us, the other / this; rows, sequences x heads, tokens; D = 128 but where said): 64 x 128 of 8200 149/147; 80 x 128 of
+// 8200 180/151; 96 x 32 of 4100 45/38, x 128 124/92; 128 x 8 of 8200 34/36, x 64 of 2100 55/40, of 8200 146/90; 147 x 4 of 5000
+// (D = 64) 17/30, x 32 53/48; 256 x 8 of 4100 34/32, of 65600 301/111, x 128 of 8200 533/220; 512 x 128 of 350 120/61.  By
 // what the pages can hold, as the other's rules.
 bool kv4_tree_wide(const Kv4AttnParams& p) {
     const int64_t rows = (int64_t)p.Lq * p.G, groups = std::min(p.room, p.reach) / 16 + 1;
