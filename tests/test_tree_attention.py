@@ -232,6 +232,35 @@ def test_layouts_a_stream_and_graphs(r9q, n, Hq, wide):  # noqa: F811
     assert int(ws[:65536].count_nonzero()) == 0
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,Hq,D", [(32, 8, 128), (24, 6, 64), (64, 24, 128)])
+def test_lengths_that_change_under_a_graph(r9q, n, Hq, D):  # noqa: F811
+    """Many rows, one workspace: batches whose lengths differ between replays, places that are empty, fewer tokens than
+    nodes, one long sequence alone; what an earlier replay split or left whole does not show."""
+    most = [2500, 700, 40, 3, 90, 1300]
+    cache, table, _ = make_cache(r9q, most, 2, D, 32, 671)
+    wide = widened(table, 32, 2, n * Hq // 2)
+    parents = random_parents(len(most), n, 672)
+    parents[1, n // 2:] = -2
+    q = rand((len(most), n, Hq, D), 673).to(dev())
+    lens = on(np.array(most, np.int32))
+    args = (q, cache, on(wide), lens, on(parents))
+    r9q.r9q_kv4_tree_attention(*args)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, lse = r9q.r9q_kv4_tree_attention(*args, return_lse=True)
+    for now in (most, [0, 0, 0, 0, 0, 0], [2500, 0, 0, 0, 0, 0], [0, 0, 0, 0, 0, 1300], [1, 2, 3, 3, 64, 128], [700, 700, 40, 0, 0, 129],
+                [0, 16, 0, 0, 0, 0], most):
+        lens.copy_(on(np.array(now, np.int32)))
+        o.fill_(7.0)
+        lse.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert r9q.r9q_last_device_error() == 0
+        check(r9q, cache, table, now, parents, q, o, lse)
+
+
 # ------------------------------------------------------------------ moves --
 
 @pytest.mark.gpu
