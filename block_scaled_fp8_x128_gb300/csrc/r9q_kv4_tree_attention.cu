@@ -620,8 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                             o[z + 3] = fmaf(other_k, v.w, o[z + 3]);
                         }
                     }
-                    if (!live) continue;
-                    if (it.whole) {
+                    if (live && it.whole) {
                         uint32_t w[8];
 #pragma unroll
                         for (int z = 0; z < 8; ++z) {
@@ -631,11 +630,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                         uint4* dst = reinterpret_cast<uint4*>(p.o + out * D + x);
                         dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
                         dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                    } else {
+                    } else if (live) {
 #pragma unroll
                         for (int z = 0; z < 16; z += 4)
                             reinterpret_cast<float4*>(part)[(x + z) / 4 * ROWS + r] = make_float4(o[z], o[z + 1], o[z + 2], o[z + 3]);
                     }
+                    __syncwarp();            // (the next load is by the whole warp again)
                 }
                 if (live && it.whole && p.lse)
                     p.lse[out] = instead == kNothing ? kNegInf : instead == kNan ? __int_as_float(0x7FC00000) : log_sum_exp(total_m, total_l);

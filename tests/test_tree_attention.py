@@ -261,6 +261,25 @@ def test_lengths_that_change_under_a_graph(r9q, n, Hq, D):  # noqa: F811
         check(r9q, cache, table, now, parents, q, o, lse)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,G,D", [(13, 5, 128), (19, 5, 64), (43, 3, 128), (33, 7, 128), (37, 7, 64)])
+@pytest.mark.parametrize("B", [2, 120])
+def test_rows_that_end_inside_a_warp(r9q, n, G, D, B):  # noqa: F811
+    """Many rows, the last warp of a tile partly without: as parts that are joined, and items of a CTA's own."""
+    lens = [n + (i * 53) % 190 for i in range(B)]
+    cache, table, _ = make_cache(r9q, lens, 1, D, 16, 681)
+    table = widened(table, 16, 1, n * G)
+    parents = random_parents(B, n, 682)
+    parents[1, n - 2:] = -2
+    q = rand((B, n, G, D), 683).to(dev())
+    lens = np.array(lens, np.int32)
+    o, lse = r9q.r9q_kv4_tree_attention(q, cache, on(table), on(lens), on(parents), return_lse=True)
+    assert r9q.r9q_last_device_error() == 0
+    some = [0, 1, B // 2, B - 1][:B]
+    check(r9q, cache, table[some], lens[some], parents[some], q[some], o[some], lse[some])
+    assert bool(torch.isfinite(o).all())
+
+
 # ------------------------------------------------------------------ moves --
 
 @pytest.mark.gpu
