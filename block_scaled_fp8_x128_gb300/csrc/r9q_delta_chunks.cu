@@ -211,6 +211,7 @@ __device__ __forceinline__ uint32_t not_finite(uint64_t (&x)[N]) {
             x[i] = pair_of(f.x, f.y);
         }
     }
+    __syncwarp();                            // (a store to tensor memory, by the whole warp, follows)
     return m;
 }
 
@@ -370,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                 for (int i = 0; i < 32; ++i)
                     if (lost >> (t0 + i) & 1) out[i / 2] = i & 1 ? (out[i / 2] & 0xFFFFu) | 0x7FC00000u : (out[i / 2] & 0xFFFF0000u) | 0x7FC0u;
             }
+            __syncwarp();                    // (as there, of Y)
             if constexpr (TREE) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
@@ -512,6 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
                         y[i + 1] = mul2(f.y, u[i + 1]);
                     }
                     if (t1 > t0 && (lost | sc.bad[0] | sc.bad[1])) y[0] = pair_of(__int_as_float(0x7FC00000), 0.0f);     // into the state
+                    __syncwarp();
                     store_part(mine + Y::kUleft + t1 / 2, y);
                     store_part(mine + Y::kUleft + 32 + t1 / 2, y);
                     store_part<true>(mine + Y::kU + t0 + (t1 - t0) / 2, y);

@@ -258,6 +258,78 @@ def test_what_is_not_finite_stays_in_its_branch_and_head(r9q, bad):  # noqa: F81
     assert r9q.r9q_last_device_error() == 0
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("n,at,D", [(12, 2, 128), (40, 0, 128), (40, 39, 64), (64, 29, 64), (64, 35, 128), (64, 63, 128),
+                                    (150, 3, 64), (150, 45, 128), (150, 64, 128), (150, 95, 64), (150, 149, 128)])
+def test_what_is_not_finite_shows_and_stays(r9q, bad, n, at, D):  # noqa: F811
+    """A value, key, rate, decay or query that is not finite, in either half of a chunk, in the first, a middle or the last one:
+    what comes from it is not finite, and the rest stays, bit for bit."""
+    Hk, Hv, m = 2, 4, min(n, 64)                              # m: nodes of a tree
+    q, k, v, g, beta = inputs((n,), Hk, Hv, D, 521)
+    g, beta = on(g), on(beta)
+    parents = random_parents(1, m, 522)
+    below = [at] if at < m else []
+    for i in range(at + 1, m):
+        if parents[0, i] in below:
+            below.append(i)
+    s, slots, cu = some_state(1, Hv, D, 523).to(dev()), on(np.zeros(1, np.int32)), on(np.array([0, n], np.int32))
+
+    def both(*x):
+        state = s.clone()
+        packed = r9q.r9q_gated_delta(*x, state, slots, cu)
+        return packed, state, r9q.r9q_gated_delta_tree(*(t[None, :m].contiguous() for t in x), s, slots, on(parents))[0]
+    want = both(q, k, v, g, beta)
+    for what in range(5):
+        x = [t.clone() for t in (v, k, g, beta, q)]
+        heads, rows, after, branch = [0], slice(None), list(range(at, n)), below
+        if what == 0:
+            x[0][at, 0, 3], rows = bad, slice(3, 4)           # (one value's row)
+        elif what in (1, 4):
+            x[what][at, 0, 3], heads = bad, [0, 1]
+        else:
+            x[what][at, 0] = bad
+        if what == 4:                                         # (nothing comes from a query but its output)
+            after, branch = [at], [at] if at < m else []
+        got = both(x[4], x[1], x[0], x[2], x[3])
+        if not (what == 2 and bad == -float("inf")):          # (which forgets the state)
+            assert not torch.isfinite(got[0][after][:, heads, rows]).any(), what
+            assert not torch.isfinite(got[2][branch][:, heads, rows]).any(), what
+            assert what == 4 or not torch.isfinite(got[1][0, heads][:, rows]).any(), what
+        for o, old, touched, tokens in ((got[0], want[0], after, n), (got[2], want[2], branch, m)):
+            keep = torch.ones((tokens, Hv), dtype=torch.bool)
+            keep[np.ix_(touched, heads)] = False
+            keep = keep.to(dev())
+            assert torch.equal(o[keep], old[keep]), what
+        spared = slice(None) if what == 4 else slice(len(heads), None)
+        assert torch.equal(got[1][0, spared], want[1][0, spared]), what
+    assert r9q.r9q_last_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,D", [(17, 128), (40, 64), (64, 128)])
+def test_bad_parents_of_larger_trees(r9q, n, D):  # noqa: F811
+    """A parent that is not one, in either half of a chunk: its node and what comes from it are NaN, the rest stays."""
+    q, k, v, g, beta = inputs((2, n), 1, 2, D, 531)
+    parents = random_parents(2, n, 532)
+    args, s, slots = (q, k, v, on(g), on(beta)), some_state(2, 2, D, 533).to(dev()), on(np.arange(2, dtype=np.int32))
+    base = r9q.r9q_gated_delta_tree(*args, s, slots, on(parents))
+    assert r9q.r9q_last_device_error() == 0
+    for at in (0, 3, n - 2):
+        for x in (at, at + 1, -3, 1 << 30, -2147483648):
+            p = parents.copy()
+            p[1, at] = x
+            lost = [at]
+            for i in range(at + 1, n):
+                if p[1, i] in lost:
+                    lost.append(i)
+            keep = [i for i in range(n) if i not in lost]
+            o = r9q.r9q_gated_delta_tree(*args, s, slots, on(p))
+            assert r9q.r9q_last_device_error() == -8
+            assert torch.equal(o[0], base[0]) and torch.equal(o[1, keep], base[1, keep])
+            assert bool(torch.isnan(o[1, lost]).all())
+
+
 # ----------------------------------------------- places, layouts, streams --
 
 @pytest.mark.gpu
