@@ -90,18 +90,7 @@ __global__ void __launch_bounds__(32 * warps_of(D), D == 64 ? 4 : 2) delta_rows_
     int64_t row;
     delta_tokens(p, b, n, row);
     const int32_t* path = p.path + (int64_t)b * p.P;
-    if constexpr (MODE == kDeltaCommit) {    // the path ends before its first entry that is not a node
-        bool bad = false;
-        uint64_t ends = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = i * 32 + lane, node = at < p.P ? path[at] : -1;
-            ends |= (uint64_t)__ballot_sync(0xffffffffu, node < 0 || node >= p.Lq) << (32 * i);
-            bad = bad || node >= p.Lq;
-        }
-        if (bad) record_error(p.err, kErrArg);
-        n = ends ? __ffsll((long long)ends) - 1 : p.P;
-    }
+    if constexpr (MODE == kDeltaCommit) n = path_length(p, b);
     const int first_slot = p.slots[b];       // (its rows are on their way while the slot is checked)
     float* rows = p.state + (((int64_t)(first_slot >= 0 && first_slot < p.n_states ? first_slot : 0) * p.Hv + h) * D + row0) * D;
     uint64_t s[4][2 * M];                    // pairs of rows r + 4i

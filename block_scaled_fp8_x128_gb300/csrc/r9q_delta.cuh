@@ -47,6 +47,22 @@ __device__ __forceinline__ void delta_tokens(const DeltaParams& p, int b, int& n
     }
 }
 
+// The nodes of sequence b's path: up to the first entry that is not one, an error where that is Lq or more.  What stands behind
+// it, or in the path of a place without a sequence, is not looked at.  Whole warps call this.
+__device__ __forceinline__ int path_length(const DeltaParams& p, int b) {
+    const int32_t* path = p.path + (int64_t)b * p.P;
+    const int lane = threadIdx.x & 31;
+    uint64_t ends = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int at = i * 32 + lane, node = at < p.P ? path[at] : -1;
+        ends |= (uint64_t)__ballot_sync(0xffffffffu, node < 0 || node >= p.Lq) << (32 * i);
+    }
+    const int n = ends ? __ffsll((long long)ends) - 1 : p.P;
+    if (threadIdx.x == 0 && n < p.P && path[n] >= p.Lq && p.slots[b] >= 0) record_error(p.err, kErrArg);
+    return n;
+}
+
 // A node of a tree, found by following its parents in shared memory: its ancestors and itself, a bit each; fewer
 // than all of them where `most` (a window) ends before the tree does.
 enum NodeKind { kNode, kNoNode, kBadNode };

@@ -258,16 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) delta_chunks_kernel(const DeltaPa
     int64_t row0;
     delta_tokens(p, b, n, row0);
     const int32_t* path = p.path + (int64_t)b * p.P;
-    if constexpr (MODE == kDeltaCommit) {
-        uint64_t ends = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = i * 32 + lane, node = at < p.P ? path[at] : -1;
-            ends |= (uint64_t)__ballot_sync(0xffffffffu, node < 0 || node >= p.Lq) << (32 * i);
-            if (node >= p.Lq) record_error(p.err, kErrArg);
-        }
-        n = ends ? __ffsll((long long)ends) - 1 : p.P;
-    }
+    if constexpr (MODE == kDeltaCommit) n = path_length(p, b);
     const int slot = delta_slot<!TREE>(p, b);
     if (slot < 0) {
         if constexpr (HAS_Q)

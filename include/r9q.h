@@ -419,8 +419,8 @@ int r9q_gated_delta_step(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs
 /* Drafted tokens: the Lq (at most 64) tokens of each sequence are the nodes of a tree, with parents as for
  * r9q_kv4_tree_attention; a node's state comes from its parent's, or from the sequence's.  Only outputs are written;
  * r9q_gated_delta_commit takes the state on along an accepted path: path int32 [B][P] (P at most 64) on the
- * device, nodes from the tree's beginning on, until the first negative one.  A node of Lq or more is an error,
- * and ends the path too. */
+ * device, nodes from the tree's beginning on, until the first negative one.  A node of Lq or more before that is an
+ * error, and ends the path too.  What stands behind the end, or in a place without a sequence, is not looked at. */
 int r9q_gated_delta_tree(const void* q, int64_t q_bs, int64_t q_ts, int64_t q_hs, const void* k, int64_t k_bs,
                          int64_t k_ts, int64_t k_hs, const void* v, int64_t v_bs, int64_t v_ts, int64_t v_hs,
                          const float* g, const float* beta, const int32_t* parents, const int32_t* slots,

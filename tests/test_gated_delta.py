@@ -390,6 +390,41 @@ def test_bad_offsets_parents_and_paths(r9q):  # noqa: F811
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("P", [6, 32, 33, 64])
+@pytest.mark.parametrize("D", [64, 128])
+def test_what_stands_behind_a_path(r9q, P, D):  # noqa: F811
+    """Entries behind a path's end, and the path of a place without a sequence, are not looked at; a node out of range before
+    that is an error and ends the path."""
+    n, Hk, Hv = 40, 1, 2
+    _, k, v, g, beta = inputs((4, n), Hk, Hv, D, 541)
+    state = some_state(4, Hv, D, 543)
+    args, slots = (k, v, on(g), on(beta)), on(np.array([2, -1, 0, 1], np.int32))
+
+    def after(rest):
+        path = np.full((4, P), rest, np.int64)
+        path[0, :3] = 0, 3, -1
+        path[2, :5] = 1, 2, 4, 7, -9
+        path[3, 0] = -1
+        s = state.to(dev())
+        r9q.r9q_gated_delta_commit(*args, s, slots, on(path.astype(np.int32)))
+        return s
+    want = after(-1)
+    assert r9q.r9q_last_device_error() == 0
+    for rest in (n, 999, 2147483647, 5, -2147483648):
+        assert torch.equal(after(rest), want) and r9q.r9q_last_device_error() == 0, rest
+    for at in (0, 4, P - 1):
+        s, path = state.to(dev()), np.tile(np.arange(P) % n, (4, 1)).astype(np.int32)
+        path[3, at] = n
+        short = path.copy()
+        short[3, at] = -1
+        r9q.r9q_gated_delta_commit(*args, s, slots, on(path))
+        assert r9q.r9q_last_device_error() == -8
+        t = state.to(dev())
+        r9q.r9q_gated_delta_commit(*args, t, slots, on(short))
+        assert r9q.r9q_last_device_error() == 0 and torch.equal(s, t)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("n", [3, 100])
 def test_layouts_a_stream_and_a_graph(r9q, n):  # noqa: F811
     """Head-major and broadcast inputs, another stream, and a captured call replayed: the same values."""
