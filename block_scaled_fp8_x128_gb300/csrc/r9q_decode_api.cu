@@ -467,7 +467,7 @@ static int gated_delta(DeltaMode mode, const void* q, int64_t q_bs, int64_t q_ts
                        void* stream) {
     const int64_t tokens = cu ? T : Lq, batch = cu ? 1 : B;                    // of the strided dimensions
     if (!dims_ok(tokens, Hk, D) || !dims_ok(tokens, Hv, D) || Hv % Hk || B < 0 || P < 0) return R9Q_ERR_DIM;
-    if (B * Hv > INT_MAX / 4 || B * tokens > INT_MAX || n_states < 1 || n_states > INT_MAX) return R9Q_ERR_DIM;
+    if (B > INT_MAX / 4 / Hv || batch * tokens > INT_MAX || n_states < 1 || n_states > INT_MAX) return R9Q_ERR_DIM;
     if (mode != kDeltaChain && (Lq > kMostNodes || P > kMostNodes)) return R9Q_ERR_DIM;
     if (flags & ~R9Q_DELTA_FROM_ZERO) return R9Q_ERR_ARG;
     if (B == 0 || (!cu && Lq == 0) || (mode == kDeltaCommit && P == 0)) return R9Q_OK;

@@ -554,6 +554,40 @@ def test_refusals():
         lib.r9q_gated_delta(x, x, x, f, f, torch.zeros((1, 2, 128, 128)), i, torch.zeros(2, dtype=torch.int32))
 
 
+@pytest.mark.parametrize("T,B,taken", [(1 << 20, 2047, True), (1 << 20, 2048, True), (524288, 4096, True), (40, 1 << 28, True),
+                                       ((1 << 31) - 1, 1, True), (1 << 31, 1, False), (10, 1 << 29, False)])
+def test_how_many_packed_tokens_and_sequences(T, B, taken):
+    """T counts the tokens of all sequences: no product of the two is limited.  (A refusal that comes later, of eps, ends the
+    call on the host.)"""
+    import __graft_entry__
+    __graft_entry__._builder().build()
+    import block_scaled_fp8_x128_gb300 as lib
+    M = 1 << 30
+    r = lib._lib.r9q_gated_delta(M, 128, 128, 2 * M, 128, 128, 3 * M, 128, 128, 4 * M, 5 * M, 6 * M, 7 * M, 8 * M, 9 * M, T, B,
+                                 1, 1, 128, 3, 0.1, -1.0, 0, None)
+    assert r == (-8 if taken else -2)
+
+
+@pytest.mark.gpu
+def test_thousands_of_packed_sequences(r9q):  # noqa: F811
+    """4100 of up to 256 tokens, 524,800 in all."""
+    B, Hk, Hv, D = 4100, 1, 1, 64
+    lens = np.arange(B) * 101 % 256
+    lens[:524_800 - lens.sum()] += 1
+    assert lens.sum() == 524_800 and B * 524_800 > 1 << 31
+    cu = np.concatenate(([0], np.cumsum(lens))).astype(np.int32)
+    q, k, v, g, beta = inputs((cu[-1],), Hk, Hv, D, 551)
+    slots = np.random.default_rng(552).permutation(B).astype(np.int32)
+    s = torch.zeros((B, Hv, D, D), device=dev())
+    o = r9q.r9q_gated_delta(q, k, v, on(g), on(beta), s, on(slots), on(cu))
+    assert r9q.r9q_last_device_error() == 0 and bool(torch.isfinite(o).all())
+    for b in (0, 1, 255, 256, 2049, B - 1):
+        at = slice(cu[b], cu[b + 1])
+        S, E, e, w = ref.chain(np.zeros((Hv, D, D)), *(np64(x[at]) for x in (q, k, v)), g[at], beta[at], D ** -0.5)
+        check_state(s[int(slots[b])], S, E)
+        assert (np.abs(np64(o[at]) - e) <= w).all()
+
+
 @pytest.mark.gpu
 def test_tensors_of_other_types_and_shapes(r9q):  # noqa: F811
     q, k, v, g, beta = inputs((6,), 1, 2, 64, 511)
