@@ -10,16 +10,19 @@
 //                  subnormal c 2^-24, exactly (of two nibbles one weighs 16 times the other; so do Q's elements, inversely)
 //   score = fr (sk S + lk sum(q))
 //   O += P V'      P the weights in fp16, in S's place in tensor memory; V' = (c - 8) sv 2^(11 - E), fp16, E the exponent of
-//                  the largest step of the tile's keys
-// and what V' leaves out, lv + 8 sv, is summed with the weights in fp32 (of fp16 values).  Sums of (c - 8), which are near zero, do not
-// drift as those of codes would.  References move as there: a row's weights are taken against top - 8 + E of its own,
-// which moves only when a chunk of 32 weights passes 2^15, and takes what is summed and P with it.
+//                  the largest step (or 2^-10 of a lowest value) so far
+// and what V' leaves out, mid = lv + 8 sv, is summed in fp32 with the weights before their rounding, so that what fp16 loses counts
+// with the distance of codes from 8, however far from zero the values are.  (With mid and its weights in fp16 219 us instead of 233,
+// but an error of 2^-12 of a value's size; mid as bf16, with what that leaves in V': 238.)  Sums of (c - 8), which are near zero,
+// do not drift as those of codes would.  V' holds steps down to 2^-25 of the largest in full.  References move as there: a
+// row's weights are taken against top - 8 + E of its own, which moves only when a chunk of 32 weights passes 2^15, and takes
+// what is summed and P with it.
 // Tiles in which some row does not see some key (the tree's own, those at a window's edge or at the sequence's end) keep an
 // exponent for every key, so that no row's arithmetic depends on what it does not see; V' of a key without a finite pair
 // is zero there and everywhere, and rows that see it are NaN.
 //
 // What bounds it: the softmax's chain of loads, exponentials and stores, with two warps a scheduler (256 rows x 128 heads
-// of 8200 keys, D = 128: 220 us, 630 TFLOP/s; half of the issue slots, tensor cores busy for 30 %; with streams that take turns
+// of 8200 keys, D = 128: 233 us, 590 TFLOP/s; half of the issue slots, tensor cores busy for 30 %; with streams that take turns
 // at it 245, with two threads a row 308, for their registers spill), and 25 us of beginning and end.
 //
 // Warps 0-3 and 4-7: the streams; the first of each issues its products.  Warps 8-11 read the codes of a tile ahead into
@@ -51,7 +54,7 @@ constexpr float kMost = 32768.0f;            // a sum of 32 weights over this mo
 // Of a tile's keys.
 struct alignas(16) KeyScalars {
     uint32_t k[kTile];                       // the pair, as in the cache
-    uint16_t mid[kTile];                     // (lv + 8 sv) 2^-exponent as fp16: fewer bytes for every row's thread to read
+    float mid[kTile];                        // (lv + 8 sv) 2^-exponent
     float exponent[kTile];                   // biased; all the same where every row sees every key
     uint16_t v[kTile];                       // steps as fp16, 2^(11 - exponent) times
     uint32_t bad[4];                         // keys without a finite value pair
@@ -125,14 +128,6 @@ struct Waits {
         *failed = 1;                         // (recorded at the end)
     }
 };
-
-// Adds the products of two pairs of fp16 values, exactly, to a and b.
-__device__ __forceinline__ void add_products(float& a, float& b, uint32_t x, uint32_t y) {
-    asm("{\n\t.reg .b16 xl, xh, yl, yh;\n\tmov.b32 {xl, xh}, %2;\n\tmov.b32 {yl, yh}, %3;\n\tfma.rn.f32.f16 %0, xl, yl, %0;\n\t"
-        "fma.rn.f32.f16 %1, xh, yh, %1;\n\t}"
-        : "+f"(a), "+f"(b)
-        : "r"(x), "r"(y));
-}
 
 // Bits [lo, hi) of 32.
 __device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
@@ -430,10 +425,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                         const uint64_t top2 = pair_of(-top, -top), shift2 = pair_of((float)kHeadroom - ref, (float)kHeadroom - ref);
                         uint64_t total = 0;
                         float mid0 = 0.0f, mid1 = 0.0f;
-                        uint4 mid;
+                        float4 mid;
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
-                            if (x % 4 == 0) mid = *reinterpret_cast<const uint4*>(&ks.mid[c * 32 + 2 * x]);
+                            if (x % 2 == 0) mid = *reinterpret_cast<const float4*>(&ks.mid[c * 32 + 2 * x]);
                             uint64_t at = fma2(s[x], fr2, shift2);
                             if constexpr (!FAST)
                                 if (!near) at = fma2(add2(s[x], top2), fr2, pair_of((float)kHeadroom, (float)kHeadroom));
@@ -451,7 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                             }
                             total = add2(total, pair_of(p0, p1));
                             out[x] = pack_f16x2(w0, w1);
-                            add_products(mid0, mid1, out[x], x % 4 == 0 ? mid.x : x % 4 == 1 ? mid.y : x % 4 == 2 ? mid.z : mid.w);
+                            mid0 = fmaf(w0, x % 2 == 0 ? mid.x : mid.z, mid0);
+                            mid1 = fmaf(w1, x % 2 == 0 ? mid.y : mid.w, mid1);
                         }
                         const float2 both = parts_of(total);
                         chunk_sum = both.x + both.y;
@@ -732,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                 ks.k[t] = kpair;
                 const float sv = bad ? 0.0f : bf16_lo(vpair), lv = bad ? 0.0f : bf16_hi(vpair);
                 const float down = __uint_as_float((uint32_t)(254 - e) << 23);
-                ks.mid[t] = (uint16_t)pack_f16x2(fmaf(8.0f, sv * down, lv * down), 0.0f);
+                ks.mid[t] = fmaf(8.0f, sv * down, lv * down);
                 ks.exponent[t] = (float)e;
                 // 2^(11 + 127 - e) in two factors, so that neither is out of range
                 ks.v[t] = (uint16_t)pack_f16x2(sv * down * 2048.0f, 0.0f);

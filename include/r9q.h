@@ -336,9 +336,12 @@ int r9q_kv4_gather(const uint8_t* kc, const void* kp, const uint8_t* vc, const v
  * uses key-value head h / (Hq / Hk).  Keys that a token does not see do not reach
  * its result, whatever they hold (NaN and infinities too).  scale > 0.
  * Scores, sums and accumulators are fp32; weights (times the values' steps) are
- * rounded to fp16, which moves a result by about 2e-4 of its size before it is
- * rounded to bf16.  The result does not depend on timing; its last bits depend on the lengths of the
- * whole batch and on max_pages (they decide where the work is cut).
+ * rounded to fp16, which counts with the codes' distance from their middle and moves a
+ * result by about 2e-4 of the values' spread before it is rounded to bf16.  fp16's range ends
+ * where a key that is seen, with however little weight, has a step (or 2^-10 of a lowest value) more than
+ * 2^18 times those of the keys that count: results are then off by up to 2^-30 of that step,
+ * times the largest weight over the mean one.  The result does not depend on timing; its last
+ * bits depend on the lengths of the whole batch and on max_pages (they decide where the work is cut).
  * Built for few rows Lq * Hq / Hk of a key-value head: each 8 or 16 of them read
  * the codes again, of all keys that any new token of the sequence sees.
  * workspace: r9q_workspace_bytes(R9Q_OP_KV4_ATTENTION, Lq * Hq / Hk, D, ...), zeroed
