@@ -12,17 +12,17 @@
 //   O += P V'      P the weights in fp16, in S's place in tensor memory; V' = (c - 8) sv 2^(11 - E), fp16, E the exponent of
 //                  the largest step (or 2^-10 of a lowest value) so far
 // and what V' leaves out, mid = lv + 8 sv, is summed in fp32 with the weights before their rounding, so that what fp16 loses counts
-// with the distance of codes from 8, however far from zero the values are.  (With mid and its weights in fp16 219 us instead of 233,
-// but an error of 2^-12 of a value's size; mid as bf16, with what that leaves in V': 238.)  Sums of (c - 8), which are near zero,
+// with the distance of codes from 8, however far from zero the values are.  (With mid and its weights in fp16 6 % less time,
+// but an error of 2^-12 of a value's size; with mid as bf16, and what that leaves in V', 2 % more.)  Sums of (c - 8), which are near zero,
 // do not drift as those of codes would.  V' holds steps down to 2^-25 of the largest in full.  References move as there: a
 // row's weights are taken against top - 8 + E of its own, which moves only when a chunk of 32 weights passes 2^15, and takes
 // what is summed and P with it.
 // Tiles in which some row does not see some key (the tree's own, those at a window's edge or at the sequence's end) keep an
-// exponent for every key, so that no row's arithmetic depends on what it does not see; V' of a key without a finite pair
-// is zero there and everywhere, and rows that see it are NaN.
+// exponent for every key, and a row takes the same steps whatever the other rows of its warp need, so that its result depends on
+// nothing that it does not see; V' of a key without a finite pair is zero there and everywhere, and rows that see it are NaN.
 //
 // What bounds it: the softmax's chain of loads, exponentials and stores, with two warps a scheduler (256 rows x 128 heads
-// of 8200 keys, D = 128: 233 us, 590 TFLOP/s; half of the issue slots, tensor cores busy for 30 %; with streams that take turns
+// of 8200 keys, D = 128: 228 us, 603 TFLOP/s; half of the issue slots, tensor cores busy for 30 %; with streams that take turns
 // at it 245, with two threads a row 308, for their registers spill), and 25 us of beginning and end.
 //
 // Warps 0-3 and 4-7: the streams; the first of each issues its products.  Warps 8-11 read the codes of a tile ahead into
@@ -408,7 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                         const int e = (int)most;
                         // (a score that is not a number makes the row's sums that, whatever the reference)
                         const bool any = best > kNegInf || none;
-                        const bool up = any && (!seen_any || (best - top) * fr > (float)kSlack);
+                        // (a plain tile brings here rows that have seen something too, for others' sake)
+                        const bool up = any && (!seen_any || (!plain && (best - top) * fr > (float)kSlack));
                         const int to_e = any ? max(e_row, e) : e_row;
                         if (__any_sync(0xffffffffu, up || to_e > e_row)) move(up ? (none ? 0.0f : best) : top, to_e, 0);
                         seen_any = seen_any || any;
@@ -453,23 +454,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                         chunk_sum = both.x + both.y;
                         chunk_mid = mid0 + mid1;
                     };
-                    // Every row sees all, with the same exponent as its own: a fused multiply-add and nothing else stand
-                    // between a score and its weight.
-                    const bool fast = plain && __all_sync(0xffffffffu, e_row == (int)ks.one_exponent && fabsf(ref) < kNear);
+                    // A row that sees all, with the same exponent as its own: a fused multiply-add and nothing else stand between a
+                    // score and its weight, and the reference moves where 32 weights pass their bound.  A warp of such rows
+                    // takes the short way; in any other they come to the same, bit for bit (a row's result is its own).
+                    const bool short_row = plain && e_row == (int)ks.one_exponent && fabsf(ref) < kNear;
+                    const bool fast = __all_sync(0xffffffffu, short_row);
                     float a[32], z[32];
                     uint32_t y[16], u[16];
-                    tmem_ld(at_s, a);
-                    if (fast) {              // 64 keys at a time
+                    auto weigh_tile = [&](auto tag) {        // 64 keys at a time, from S's first columns in a
 #pragma unroll 1
                         for (int c = 0; c < 4; c += 2) {
                             float sum0, mid0, sum1, mid1;
                             tmem_ld(at_s + (c + 1) * 32, z);
                             tmem_wait_ld(a);
                             tmem_wait_ld(z);
-                            weigh(c, a, y, sum0, mid0, Yes());
-                            weigh(c + 1, z, u, sum1, mid1, Yes());
-                            const float over = fmaxf(sum0, sum1);
-                            if (__any_sync(0xffffffffu, over > kMost)) {     // (P of these is not written yet, and S is there)
+                            weigh(c, a, y, sum0, mid0, tag);
+                            weigh(c + 1, z, u, sum1, mid1, tag);
+                            const bool over = short_row && fmaxf(sum0, sum1) > kMost;
+                            if (__any_sync(0xffffffffu, over)) {             // (P of these is not written yet, and S is there)
                                 float best = kNegInf;
 #pragma unroll 1
                                 for (int k = c; k < c + 2; ++k) {
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                                         best = max3(best, f.x, f.y);
                                     }
                                 }
-                                move(over > kMost ? fmaxf(top, best) : top, e_row, c);
+                                move(over ? fmaxf(top, best) : top, e_row, c);
                                 tmem_ld(at_s + c * 32, a);
                                 tmem_wait_ld(a);
                                 weigh(c, a, y, sum0, mid0, No());
@@ -497,12 +499,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
                             tmem_store16(at_s + c * 16, y);
                             tmem_store16(at_s + c * 16 + 16, u);
                         }
+                    };
+                    tmem_ld(at_s, a);
+                    if (fast) {
+                        weigh_tile(Yes());
                     } else {
-                        // (the reference holds for all: what the row sees was looked through; or there are other exponents, or scores
+                        // (the reference holds for all: what the row sees was looked through; or it has another exponent, or scores
                         // too large for the short way, and it is looked through here)
                         if (plain) {
                             float best = kNegInf;
-                            bool none = false;
 #pragma unroll 1
                             for (int c = 0; c < 4; ++c) {
                                 uint64_t s[16];
@@ -512,24 +517,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attention_kernel(const Kv4At
 #pragma unroll
                                 for (int x = 0; x < 16; ++x) {
                                     const float2 f = parts_of(s[x]);
-                                    none = none || f.x != f.x || f.y != f.y;
                                     best = max3(best, f.x, f.y);
                                 }
                             }
-                            const bool up = (best - top) * fr > (float)kSlack;
+                            const bool up = !short_row && (best - top) * fr > (float)kSlack;
                             if (__any_sync(0xffffffffu, up)) move(up ? best : top, e_row, 0);
                             tmem_ld(at_s, a);
                         }
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            float sum0, mid0;
-                            tmem_wait_ld(a);
-                            weigh(c, a, y, sum0, mid0, No());
-                            if (c < 3) tmem_ld(at_s + (c + 1) * 32, a);
-                            sum += sum0;
-                            msum += mid0;
-                            tmem_store16(at_s + c * 16, y);
-                        }
+                        weigh_tile(No());
                     }
                     l += sum;
                     ml += msum;
