@@ -479,6 +479,46 @@ def test_states_beyond_32_bits(r9q):  # noqa: F811
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [3, 70])
+def test_inputs_beyond_32_bits(r9q, n):  # noqa: F811
+    """Heads, tokens and sequences of the inputs 2^32 elements and more apart: as of ordinary inputs, bit for bit."""
+    B, Hk, Hv, D = 2, 2, 4, 64
+    q, k, v, g, beta = inputs((B, n), Hk, Hv, D, 561)
+    g, beta, slots = on(g), on(beta), on(np.arange(B, dtype=np.int32))
+    start = some_state(B, Hv, D, 563).to(dev())
+    far = torch.empty((1 << 32) + (1 << 27), dtype=torch.bfloat16, device=dev())
+    m = min(n, 64)
+    parents = on(random_parents(B, m, 564))
+    path = on(np.tile(np.arange(m), (B, 1)).astype(np.int32))
+    cu = on(np.array([0, n], np.int32))
+
+    def run(q, k, v):
+        """All four calls, and one of the first sequence packed: outputs and states."""
+        s, t, u = start.clone(), start.clone(), start.clone()
+        few = [x[:, :m] for x in (q, k, v)] + [x[:, :m].contiguous() for x in (g, beta)]
+        return [r9q.r9q_gated_delta_step(q, k, v, g, beta, s, slots), s, r9q.r9q_gated_delta_tree(*few, start, slots, parents),
+                r9q.r9q_gated_delta_commit(*few[1:], t, slots, path), t,
+                r9q.r9q_gated_delta(q[0], k[0], v[0], g[0], beta[0], u, slots[:1], cu), u]
+    want = run(q, k, v)
+    # strides of sequences, tokens and heads; what is 2^32 apart comes last in memory
+    last = 1 << 32
+    for strides in ((1 << 18, 1 << 11, last // (Hk - 1)), (last, 1 << 11, 1 << 8), (1 << 25, -(-last // (n - 1)) + 7 & ~7, 1 << 8)):
+        def spread(x, offset):
+            hs = strides[2] // (3 if strides[2] > 1 << 20 and x.shape[2] > Hk else 1) // 8 * 8        # (four heads in the same room)
+            y = far.as_strided(x.shape, (strides[0], strides[1], hs, 1), offset)
+            y.copy_(x)
+            assert torch.equal(y, x)
+            return y
+        apart = [spread(x, 64 * (i if i < 2 else 8)) for i, x in enumerate((q, k, v))]
+        assert max(sum((d - 1) * st for d, st in zip(x.shape, x.stride())) for x in apart) >= 1 << 32
+        for x, y in zip((q, k, v), apart):                    # (one did not write over another)
+            assert torch.equal(x, y)
+        for a, b in zip(run(*apart), want):
+            assert (a is None and b is None) or torch.equal(a, b)
+    assert r9q.r9q_last_device_error() == 0
+
+
+@pytest.mark.gpu
 def test_a_long_sequence_in_parts(r9q):  # noqa: F811
     """Three thousand tokens at once, in parts of any size, and the last ones as steps: within the bounds of one another
     and of the definition."""
