@@ -307,6 +307,40 @@ def test_what_is_not_finite_shows_and_stays(r9q, bad, n, at, D):  # noqa: F811
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bad", [3.3e38, -1e30])
+@pytest.mark.parametrize("n,at,D", [(14, 2, 128), (40, 0, 64), (64, 29, 128), (64, 50, 64), (150, 64, 128), (150, 100, 64)])
+def test_a_large_value_stays_in_its_branch_row_and_head(r9q, bad, n, at, D):  # noqa: F811
+    """However large: earlier tokens, other branches and the state's other rows stay, bit for bit."""
+    Hk, Hv, m = 2, 4, min(n, 64)
+    q, k, v, g, beta = inputs((n,), Hk, Hv, D, 571)
+    g, beta = on(g), on(beta)
+    parents = random_parents(1, m, 572)
+    below = [at] if at < m else []
+    for i in range(at + 1, m):
+        if parents[0, i] in below:
+            below.append(i)
+    s, slots, cu = some_state(1, Hv, D, 573).to(dev()), on(np.zeros(1, np.int32)), on(np.array([0, n], np.int32))
+    got = []
+    for x in (v, v.clone()):
+        if got:
+            x[at, 1, 9] = bad
+        state = s.clone()
+        packed = r9q.r9q_gated_delta(q, k, x, g, beta, state, slots, cu)
+        nodes = r9q.r9q_gated_delta_tree(*(t[None, :m].contiguous() for t in (q, k, x, g, beta)), s, slots, on(parents))[0]
+        got.append((packed, nodes, state[0]))
+    for old, new, touched in ((got[0][0], got[1][0], range(at, n)), (got[0][1], got[1][1], below)):
+        same = torch.ones_like(old, dtype=torch.bool)
+        same[list(touched), 1, 9] = False
+        assert torch.equal(old[same], new[same])
+        assert at >= m or not torch.equal(old, new)
+    same = torch.ones((Hv, D), dtype=torch.bool)
+    same[1, 9] = False
+    same = same.to(dev())
+    assert torch.equal(got[0][2][same], got[1][2][same]) and not torch.equal(got[0][2][1, 9], got[1][2][1, 9])
+    assert r9q.r9q_last_device_error() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("n,D", [(17, 128), (40, 64), (64, 128)])
 def test_bad_parents_of_larger_trees(r9q, n, D):  # noqa: F811
     """A parent that is not one, in either half of a chunk: its node and what comes from it are NaN, the rest stays."""
