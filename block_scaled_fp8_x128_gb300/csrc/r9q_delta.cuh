@@ -52,14 +52,16 @@ __device__ __forceinline__ void delta_tokens(const DeltaParams& p, int b, int& n
 __device__ __forceinline__ int path_length(const DeltaParams& p, int b) {
     const int32_t* path = p.path + (int64_t)b * p.P;
     const int lane = threadIdx.x & 31;
-    uint64_t ends = 0;
+    uint64_t ends = 0, out = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int at = i * 32 + lane, node = at < p.P ? path[at] : -1;
         ends |= (uint64_t)__ballot_sync(0xffffffffu, node < 0 || node >= p.Lq) << (32 * i);
+        out |= (uint64_t)__ballot_sync(0xffffffffu, node >= p.Lq) << (32 * i);
     }
-    const int n = ends ? __ffsll((long long)ends) - 1 : p.P;
-    if (threadIdx.x == 0 && n < p.P && path[n] >= p.Lq && p.slots[b] >= 0) record_error(p.err, kErrArg);
+    if (ends == 0) return p.P;
+    const int n = __ffsll((long long)ends) - 1;
+    if (threadIdx.x == 0 && (out >> n & 1) && p.slots[b] >= 0) record_error(p.err, kErrArg);
     return n;
 }
 
