@@ -12,8 +12,8 @@
 // it goes.  In a tree S stays as it is.
 //
 // What bounds it: with one token HBM (128 sequences, 32 heads of 128: 79 us, 6.8 TB/s); with more about 1 us a token
-// for the sums over earlier tokens (16 trees of 16 nodes: 37 us, 64 paths of 5: 53 us, 5.1 TB/s).  A head's CTA of 8 warps
-// against one of 4 warps for half of it: the products among the tokens are formed once (53 -> 37 us).
+// for the sums over earlier tokens (16 trees of 16 nodes: 41 us, 64 paths of 5: 53 us, 5.1 TB/s).  A head's CTA of 8 warps
+// against one of 4 warps for half of it: the products among the tokens are formed once (53 -> 40 us).
 #include "r9q_delta.cuh"
 
 namespace r9q {
@@ -383,7 +383,8 @@ cudaError_t launch_delta(int D, DeltaMode mode, const DeltaParams& p, cudaStream
     // in chunks 10 to 16 us for up to 64 tokens, with one CTA an SM.  Measured, us here and in chunks, of the
     // steps of n tokens: one sequence of 32 heads of 128: n = 8 9.8 and 14.7, 12 14.5 and 14.8, 16 18.0 and 14.8; 16
     // sequences: 16 47 and 56, 24 66 and 56; 64: 16 184 and 200, 24 255 and 203; 12 heads of 64, 16 sequences: 16
-    // 19.7 and 20.8, 24 27 and 21.  Trees alike: one of 12 nodes 11.8 and 12.3, of 16 14.8 and 12.4, 16 of 16 37 and 46.
+    // 19.7 and 20.8, 24 27 and 21.  Trees alike: one of 12 nodes 11.8 and 12.3, of 16 14.8 and 12.4, 16 of 16 41 and 49 (with the
+    // states in L2 35 and 45).
     const bool waves = (int64_t)p.B * p.Hv > 152;
     bool few = p.Lq <= (waves ? kGroup : 12);
     // A path is as long as what was accepted, not as its width: of 64 sequences 32 wide 111 and 191 with a third

@@ -26,7 +26,7 @@
 // its parts 1450, W 1300, X 1000, U 1450, u 2000, the rest between them.  The parts run different code at once; at 185 KB
 // in all it was fetched anew every chunk over a path that the SMs of a group share, and SMs beside busy ones took 1.4 times as
 // long.  So loops are rolled where nothing waits for them, and a wait is a few instructions: 91 KB, 801 -> 641 us for
-// 8192 tokens and 32 heads of 128 (one sequence, 32 SMs), 425 -> 328 for 16 of 64 to 2000 (1.5 TB/s).
+// 8192 tokens and 32 heads of 128 (one sequence, 32 SMs; now 630), 425 -> 328 for 16 of 64 to 2000 (now 325, 1.5 TB/s).
 //
 // A value that is not finite would reach earlier tokens (or other branches) through the zeros of T and P.
 // So L's rows, X and u are zero in its place, and the outputs that it belongs to are NaN, as is the state's row.

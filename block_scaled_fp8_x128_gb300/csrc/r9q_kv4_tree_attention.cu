@@ -22,8 +22,8 @@
 // nothing that it does not see; V' of a key without a finite pair is zero there and everywhere, and rows that see it are NaN.
 //
 // What bounds it: the softmax's chain of loads, exponentials and stores, with two warps a scheduler (256 rows x 128 heads
-// of 8200 keys, D = 128: 228 us, 603 TFLOP/s; half of the issue slots, tensor cores busy for 30 %; with streams that take turns
-// at it 245, with two threads a row 308, for their registers spill), and 25 us of beginning and end.
+// of 8200 keys, D = 128: 228 us, 603 TFLOP/s; half of the issue slots, tensor cores busy for 29 %; streams that take turns
+// at it took 3 % more, two threads a row 30 %, for their registers spill), and 25 us of beginning and end.
 //
 // Warps 0-3 and 4-7: the streams; the first of each issues its products.  Warps 8-11 read the codes of a tile ahead into
 // registers, and write K and V' of the one at hand to shared memory.  Work is cut as in r9q_kv4_attention.cuh; an item that several
@@ -874,10 +874,10 @@ cudaError_t launch(Kv4AttnParams p, int2* items, int sms, cudaStream_t st) {
 
 // This kernel takes about 25 us for a part's beginning and end (the other about 9), and a quarter to a half of the other's
 // time for a row and key.  So: rows that fill at least half of a tile, and work, in 16 rows of 16 keys, worth the difference
-// (us, the other / this; rows, sequences x heads, tokens; D = 128 but where said): 64 x 128 of 8200 149/147; 80 x 128 of
-// 8200 180/151; 96 x 32 of 4100 45/38, x 128 124/92; 128 x 8 of 8200 34/36, x 64 of 2100 55/40, of 8200 146/90; 147 x 4 of 5000
-// (D = 64) 17/30, x 32 53/48; 256 x 8 of 4100 34/32, of 65600 301/111, x 128 of 8200 533/220; 512 x 128 of 350 120/61.  By
-// what the pages can hold, as the other's rules.
+// (us, the other / this; rows, sequences x heads, tokens; D = 128 but where said): 64 x 128 of 8200 150/152; 80 x 128 of
+// 8200 180/157; 96 x 32 of 4100 45/40, x 128 124/97; 128 x 8 of 8200 34/38, x 64 of 2100 55/42, of 8200 148/92; 147 x 4 of 5000
+// (D = 64) 17/34, x 32 55/49; 256 x 8 of 4100 34/36, of 65600 301/114, x 128 of 8200 533/229; 512 x 128 of 350 119/65.  By
+// what the pages can hold, as the other's rules: short sequences with a table for long ones pay for its beginning and end.
 bool kv4_tree_wide(const Kv4AttnParams& p) {
     const int64_t rows = (int64_t)p.Lq * p.G, groups = std::min(p.room, p.reach) / 16 + 1;
     return rows > kTreeFewRows && (int64_t)p.B * p.c.heads * groups * ((rows + 15) / 16) > 36000;
