@@ -190,7 +190,9 @@ __device__ __forceinline__ void move_reference(State<D, NT>& s, const float (&sc
                 s.acc[nt][t][c + 2] *= alpha;
             }
         }
-    s.sv_bound = __uint_as_float((uint32_t)(es_min + 1) << 23);          // the next power of two
+    // The next power of two; or the next step moves the references again, for a column that has seen nothing yet: a first
+    // score far under zero gives no weight that could pass a bound.
+    s.sv_bound = s.seen == (1u << (2 * NT)) - 1 ? __uint_as_float((uint32_t)(es_min + 1) << 23) : -1.0f;
 }
 
 // One step: 32 keys in the stage `st`, of which groups `bits` were loaded.

@@ -136,3 +136,27 @@ def test_windows_under_a_graph(r9q, case):  # noqa: F811
         check(r9q, cache, whole[some], now[some], tree[some], q[some], o[some], lse[some], window)
         want = r9q.r9q_kv4_tree_attention(q, cache, t, le, pa, window=window, return_lse=True)
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,G,D", [(40, 1, 128), (24, 2, 64), (64, 1, 128), (36, 8, 128)])
+@pytest.mark.parametrize("v_scale", [0.0, 1e-25])
+def test_low_scores_behind_a_window(r9q, n, G, D, v_scale):  # noqa: F811
+    """Tokens of which only the first see something of the first keys that a warp takes; then keys whose values are nearly nothing
+    and whose scores are far under zero (2^score is 0 in fp32).  All of them count, for newest tokens and for a chain of nodes."""
+    B, window, page = 160, 1500, 16
+    lens = np.array([n + window + i % 64 for i in range(B)], np.int32)        # (every place of the window's edge in a step)
+    cache, table, slots = make_cache(r9q, lens.tolist(), 1, D, page, 831)
+    k = torch.full((len(slots), 1, D), -5.0, dtype=torch.bfloat16)
+    r9q.r9q_kv4_append(k.to(dev()), rand((len(slots), 1, D), 832, v_scale).to(dev()), cache, on(slots))
+    q = torch.full((B, n, G, D), 0.5, dtype=torch.bfloat16, device=dev())
+    args = (q, cache, on(table), on(lens))
+    chain = np.tile(np.arange(n) - 1, (B, 1)).astype(np.int32)
+    # every key has the same score: lse is that and the logarithm of the window's tokens
+    want = -5.0 * 0.5 * D + np.log(window)
+    for o, lse in (r9q.r9q_kv4_attention(*args, scale=1.0, window=window, return_lse=True),
+                   r9q.r9q_kv4_tree_attention(*args, on(chain), scale=1.0, window=window, return_lse=True)):
+        off = np.abs(np64(lse) - want).max()
+        assert off <= 2.0 ** -17 * (5.0 * 0.5 * D), off
+        assert bool(torch.isfinite(o).all())
+    assert r9q.r9q_last_device_error() == 0
