@@ -140,10 +140,26 @@ struct State {
 };
 
 // Takes the columns' references to the largest score and the largest values they have
-// seen, this step's included, and what was summed against the old ones with them.
-template <int D, int NT, bool MASKED>
+// seen, this step's included, and what was summed against the old ones with them.  In a tree (OWN), whose
+// columns see different keys at a window's beginning too, a column moves for its own sake alone, so that its result does not
+// depend on what others see: of `sum`, the weights, and `sv_max`, the steps, that a lane looked at.
+template <int D, int NT, bool MASKED, bool OWN>
 __device__ __forceinline__ void move_reference(State<D, NT>& s, const float (&sc)[NT][2][4],
-                                               const uint32_t (&vq)[2][2]) {
+                                               const uint32_t (&vq)[2][2], const float (&sum)[NT][2], float sv_max) {
+    uint32_t moves = 0xFu;                   // columns
+    if constexpr (OWN && !MASKED) {
+        moves = 0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int e = kHeadroom + 127 - (int)s.shift[nt][c];
+                const uint32_t bit = 1u << (2 * nt + c);
+                if (!(s.seen & bit) || sum[nt][c] > s.bound[nt][c] || sv_max > __uint_as_float((uint32_t)(e + 1) << 23)) moves |= bit;
+            }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) moves |= __shfl_xor_sync(0xffffffffu, moves, o);
+    }
     int ek[2][2];                            // the exponent of a key's values; none for a pair that is not finite
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -170,6 +186,10 @@ __device__ __forceinline__ void move_reference(State<D, NT>& s, const float (&sc
             for (int o = 4; o < 32; o <<= 1) {
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
                 e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
+            }
+            if (OWN && !MASKED && !(moves & bit)) {
+                x = s.seen & bit ? s.top[nt][c] : kNegInf;
+                e = kHeadroom + 127 - (int)s.shift[nt][c];
             }
             float alpha = 0.0f;              // nothing seen before: the sums are zero
             s.bound[nt][c] = 0.0f;           // (nothing seen now either: no weight is over 0)
@@ -295,7 +315,7 @@ __device__ __forceinline__ void attend(State<D, NT>& s, const uint8_t* st, int k
     };
     weigh();
     if (__any_sync(0xffffffffu, move)) {
-        move_reference<D, NT, MASKED>(s, sc, vq);
+        move_reference<D, NT, MASKED, TREE>(s, sc, vq, sum, sv_max);
         weigh();
     }
     uint32_t pf[NT][2][2];

@@ -22,8 +22,11 @@ WINDOWS = [(32, 20, 16, 2, 64, 16, 1000, 2600), (32, 20, 16, 2, 128, 32, 1000, 2
            (60, 64, 32, 4, 64, 16, 1, 400), (60, 64, 32, 4, 128, 16, 7, 400), (7, 48, 8, 1, 128, 48, 4000, 5000),
            (34, 12, 16, 2, 128, 16, 1500, 2000), (34, 25, 10, 2, 64, 16, 1200, 3000)]
 
+# few rows, and many keys for each warp of the kernel that takes them
+FEW = [(96, 16, 8, 2, 128, 16, 1500, 2600), (96, 12, 8, 2, 64, 32, 900, 2600), (200, 7, 4, 4, 128, 16, 600, 2600)]
 
-def windowed(r9q, B, n, Hq, Hk, D, page, window, longest, kind, seed):  # noqa: F811
+
+def windowed(r9q, B, n, Hq, Hk, D, page, window, longest, kind, seed, q_scale=1.0):  # noqa: F811
     """Lengths about the window's edges and any; pages that no node sees any more are given back."""
     lens = [longest, 0, n - 1, n, n + window, n + window + 1, 1]
     lens += [1 + (i * 397) % longest for i in range(len(lens), B)]
@@ -34,8 +37,8 @@ def windowed(r9q, B, n, Hq, Hk, D, page, window, longest, kind, seed):  # noqa: 
         table[b, :max(0, length - n - window + 1) // page] = -1
     parents = {"random": random_parents(B, n, seed + 3), "chain": np.tile(np.arange(n) - 1, (B, 1))}[kind].astype(np.int32)
     parents[-1, n - 3:] = -2
-    q = rand((B, n, Hq, D), seed + 4).to(dev())
-    assert takes_many(B, Hk, n * Hq // Hk, table.shape[1] * page, window, n)
+    q = rand((B, n, Hq, D), seed + 4, q_scale).to(dev())
+    assert takes_many(B, Hk, n * Hq // Hk, table.shape[1] * page, window, n) == (n * Hq // Hk > 64)
     return cache, whole, table, lens.astype(np.int32), parents, q, slots
 
 
@@ -69,17 +72,13 @@ def test_windows_of_many_rows(r9q, case, kind):  # noqa: F811
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("case", [WINDOWS[1], WINDOWS[2], WINDOWS[4], WINDOWS[6], WINDOWS[7]])
-@pytest.mark.parametrize("many", [True, False])
-def test_what_is_before_a_window(r9q, case, many):  # noqa: F811
+@pytest.mark.parametrize("case", [WINDOWS[1], WINDOWS[2], WINDOWS[4], WINDOWS[6], WINDOWS[7], *FEW])
+@pytest.mark.parametrize("q_scale", [1.0, 12.0])
+def test_what_is_before_a_window(r9q, case, q_scale):  # noqa: F811
     """A key before the window reaches no node, and one at its edge only the nodes that are not deep: the others' results stay,
-    bit for bit, whatever it holds.  In both kernels (few sequences take the one for few rows)."""
+    bit for bit, whatever it holds.  Scores of about one, and large ones, against which references move."""
     B, n, Hq, Hk, D, page, window, _ = case
-    cache, whole, _, lens, parents, q, _ = windowed(r9q, *case, "random", 811)
-    if not many:
-        some = [4, 9, B - 1] if B > 9 else [0, 4]
-        B, whole, lens, parents, q = len(some), whole[some], lens[some], parents[some], q[some]
-        assert not takes_many(B, Hk, n * Hq // Hk, whole.shape[1] * page, window, n)
+    cache, whole, _, lens, parents, q, _ = windowed(r9q, *case, "random", 811, q_scale)
     args = (q, cache, on(whole), on(lens), on(parents))
     base = r9q.r9q_kv4_tree_attention(*args, window=window, return_lse=True)
     depth = np.array([[len(way_to(p, i) or []) - 1 for i in range(n)] for p in parents])
